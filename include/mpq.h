@@ -50,10 +50,12 @@ extern "C" {
 
 #define MPQ_OK               0
 #define MPQ_ENULL           -1   /* a required pointer is NULL */
-#define MPQ_ESHAPE          -2   /* m < 0, n < 1, n > 65536, r < 1, r > n, n % d != 0, K out of range */
+#define MPQ_ESHAPE          -2   /* m < 0, n < 1, n > 65536, r < 1, r > n, n % d != 0, K out of range;
+                                    a token count, vocabulary, list length or row stride out of range */
 #define MPQ_EPARAM          -3   /* T_vamp < 0, n_cd < 0, damping not in (0, 1], group < 0,
                                     safeguard_eps < 0, a non-finite codebook entry, or a
-                                    mpq_codebook that mpq_codebook_prepare did not fill */
+                                    mpq_codebook that mpq_codebook_prepare did not fill; an unknown
+                                    storage type or activation, a temperature out of range */
 #define MPQ_EUNSUPPORTED    -4   /* d not in {1, 8}, a d = 8 codebook not exact in bfloat16,
                                     column groups with d = 8 or the anchored prior, a log-prior
                                     with d = 8, or an option an entry point does not take */
@@ -462,6 +464,58 @@ size_t mpq_factor_workspace_bytes(int64_t n);
  * 1 <= r <= n <= 65536. */
 int mpq_factor(double* H, int64_t n, int64_t r, float* s, float* V, void* workspace, size_t ws_bytes,
                void* stream);
+
+/* ------------------------------------------------------------------ scoring and tuning a quantized model */
+
+/* Storage types of activations and logits. */
+#define MPQ_BF16 0
+#define MPQ_FP16 1
+#define MPQ_FP32 2
+
+/* Rows of logits, device, t x V of `dtype`, row stride ld >= V elements (any
+ * element alignment): per row
+ *   lse      log sum_j exp(z_j)
+ *   logprob  z[token] - lse
+ *   entropy  -sum_j q_j log q_j (nats), q = softmax(z)
+ *   top list the `top` largest logits (equal ones: lowest index first): their
+ *            indices and log probabilities
+ * Perplexity and likelihood scoring of a quantized model; the top list of the
+ * original model's logits is the teacher's list of mpq_distill.
+ *
+ * tokens: t int32 (may be NULL without logprob).  A negative token marks a
+ * position without one (padding): logprob 0.  A token >= V: logprob NaN.
+ * Logits of -inf have no mass and are no alternatives; where a row holds fewer
+ * alternatives than `top`, the rest of its list is -1 and -inf.  A row of -inf
+ * alone: lse and logprob -inf, entropy 0.  A row holding NaN or +inf: NaN, its
+ * list -1.  Outputs (device, float32 / int32; each may be NULL): logprob,
+ * entropy, lse: t; top_ids, top_logprobs: t x top.
+ * 1 <= V <= 2^20, 0 <= top <= 128, t times the segments of a row below 2^31.
+ * Sums are float64 over float32 exponentials. */
+size_t mpq_token_logprobs_workspace_bytes(int dtype, int64_t t, int64_t V, int top);
+int mpq_token_logprobs(const void* logits, int dtype, int64_t t, int64_t V, int64_t ld, const int32_t* tokens, int top,
+                       float* logprob, float* entropy, float* lse, int32_t* top_ids, float* top_logprobs,
+                       void* workspace, size_t ws_bytes, void* stream);
+
+/* Distillation from a teacher's top list, forward and backward: per row
+ *   loss = weight KL(p || q), q = softmax(z / temperature), with p
+ *   tail = 0: softmax(teacher / temperature) over the k listed tokens;
+ *   tail = 1: exp(teacher) -- log probabilities, temperature 1 -- and the
+ *             remainder 1 - sum p as one more outcome, against the student's
+ *             mass outside the list (a remainder below 2^-20, the resolution
+ *             of the log probabilities, counts as none).
+ * grad = d loss / d z (t x V of `dtype`, row stride ldg >= V; NULL: the loss
+ * alone), rounded once; it may be the logits themselves (same pointer and
+ * stride) and may not overlap them otherwise.
+ * ids, teacher: t x k int32 / float32 (mpq_token_logprobs' top_ids and
+ * top_logprobs); an id outside [0, V) is no entry, a token listed twice has
+ * both masses.  weights: t float32, NULL: 1.  Rows of weight 0 are not read:
+ * loss 0, gradient 0.  A row whose list is empty has loss 0 and gradient 0.
+ * 0 <= k <= 128; temperature > 0 (MPQ_EPARAM otherwise, and for tail with
+ * another temperature than 1). */
+size_t mpq_distill_workspace_bytes(int dtype, int64_t t, int64_t V, int k);
+int mpq_distill(const void* logits, int dtype, int64_t t, int64_t V, int64_t ld, const int32_t* ids,
+                const float* teacher, int k, float temperature, int tail, const float* weights, float* loss,
+                void* grad, int64_t ldg, void* workspace, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

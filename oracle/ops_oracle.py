@@ -1,0 +1,95 @@
+"""float64 CPU reference of the operators on logits and on a solved layer
+(test infrastructure only), row by row from their definitions."""
+from __future__ import annotations
+
+import math
+
+import numpy as np
+
+
+# ------------------------------------------------------------------ logits
+
+def token_logprobs(z, tokens, top):
+    """z: t x V float64.  dict(lse, logprob, entropy, top_ids, top_logprobs)."""
+    t, V = z.shape
+    out = dict(lse=np.empty(t), logprob=np.empty(t), entropy=np.empty(t), top_ids=np.full((t, top), -1, np.int64),
+               top_logprobs=np.full((t, top), -np.inf))
+    for i in range(t):
+        row = z[i]
+        if np.isnan(row).any() or np.isposinf(row).any():
+            for k in ("lse", "logprob", "entropy"):
+                out[k][i] = np.nan
+            if tokens[i] < 0:
+                out["logprob"][i] = 0.0
+            out["top_logprobs"][i] = np.nan
+            continue
+        alive = np.flatnonzero(row > -np.inf)
+        if alive.size == 0:
+            lse, H = -np.inf, 0.0
+        else:
+            x = row[alive]
+            m = x.max()
+            s = np.exp(x - m).sum()
+            lse = m + math.log(s)
+            q = np.exp(x - lse)
+            H = float(-(q * (x - lse)).sum())
+        out["lse"][i], out["entropy"][i] = lse, H
+        tok = int(tokens[i])
+        out["logprob"][i] = 0.0 if tok < 0 else np.nan if tok >= V else (
+            -np.inf if row[tok] == -np.inf else row[tok] - lse)
+        order = alive[np.lexsort((alive, -row[alive]))][:top]
+        out["top_ids"][i, :order.size] = order
+        out["top_logprobs"][i, :order.size] = row[order] - lse
+    return out
+
+
+def distill(z, ids, teacher, T=1.0, tail=False, weights=None):
+    """(loss, grad, scale): scale[i, j] = weight / T (q_j + the mass the teacher gives j), which
+    rounding errors of the gradient are measured against."""
+    t, V = z.shape
+    loss, grad, scale = np.zeros(t), np.zeros((t, V)), np.zeros((t, V))
+    for i in range(t):
+        w = 1.0 if weights is None else float(weights[i])
+        if w == 0.0:
+            continue
+        a = z[i] / T
+        a = a - a.max()
+        q = np.exp(a) / np.exp(a).sum()
+        lq = a - math.log(np.exp(a).sum())
+        keep = [(int(j), float(v) / T) for j, v in zip(ids[i], teacher[i]) if 0 <= j < V]
+        if not tail:
+            keep = [(j, v) for j, v in keep if v > -np.inf]
+        p = np.zeros(V)
+        if tail:
+            kl = 0.0
+            for j, v in keep:
+                p[j] += math.exp(v)
+                if v > -np.inf:
+                    kl += math.exp(v) * (v - lq[j])
+            rest = 1.0 - p.sum()
+            listed = np.zeros(V, bool)
+            listed[[j for j, _ in keep]] = True
+            if rest < 2.0 ** -20 or listed.all():
+                rest = 0.0
+            qr = q[~listed].sum()
+            g = np.where(listed, q - p, q)
+            share = 0.0
+            if rest > 0:
+                kl += rest * (math.log(rest) - (math.log(qr) if qr > 0 else -np.inf))
+                share = rest / qr if qr > 0 else np.inf
+                g = np.where(listed, g, q * (1 - share))
+        elif not keep:
+            continue
+        else:
+            m = max(v for _, v in keep)
+            tot = sum(math.exp(v - m) for _, v in keep)
+            kl = 0.0
+            for j, v in keep:
+                lp = v - m - math.log(tot)
+                p[j] += math.exp(lp)
+                kl += math.exp(lp) * (lp - lq[j])
+            g, share = q - p, 0.0
+        loss[i] = w * kl
+        grad[i] = w / T * g
+        scale[i] = w / T * (q * (1 + share) + p)
+    return loss, grad, scale

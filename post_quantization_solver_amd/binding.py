@@ -30,7 +30,8 @@ EXPORTS = ("mpq_workspace_bytes", "mpq_strerror", "mpq_codebook_bytes", "mpq_cod
            "mpq_vamp_step", "mpq_linear_step", "mpq_map", "mpq_cd", "mpq_objective", "mpq_greedy",
            "mpq_greedy_workspace_bytes", "mpq_gram_workspace_bytes", "mpq_gram", "mpq_rht",
            "mpq_factor_workspace_bytes", "mpq_factor", "mpq_codebook_kind", "mpq_hip_error_name",
-           "mpq_e8dp_transitions", "mpq_probe_rate")
+           "mpq_e8dp_transitions", "mpq_probe_rate",
+           "mpq_token_logprobs_workspace_bytes", "mpq_token_logprobs", "mpq_distill_workspace_bytes", "mpq_distill")
 
 
 class MPQError(RuntimeError):
@@ -201,6 +202,12 @@ def load_library(path: str = LIB_PATH):
     lib.mpq_hip_error_name.argtypes = []
     lib.mpq_hip_error_name.restype = ctypes.c_char_p
     lib.mpq_probe_rate.argtypes = [I, P, SZ, ctypes.POINTER(ctypes.c_double), P]
+    lib.mpq_token_logprobs_workspace_bytes.argtypes = [I, I64, I64, I]
+    lib.mpq_token_logprobs_workspace_bytes.restype = SZ
+    lib.mpq_token_logprobs.argtypes = [P, I, I64, I64, I64, P, I, P, P, P, P, P, P, SZ, P]
+    lib.mpq_distill_workspace_bytes.argtypes = [I, I64, I64, I]
+    lib.mpq_distill_workspace_bytes.restype = SZ
+    lib.mpq_distill.argtypes = [P, I, I64, I64, I64, P, P, I, F, I, P, P, P, I64, P, SZ, P]
     for name in EXPORTS[2:]:
         if name.endswith("_bytes") or name in ("mpq_hip_error_name", "mpq_e8dp_transitions", "mpq_profiler_destroy"):
             continue
@@ -688,3 +695,122 @@ def frontend(X, W, r=None, signs=None):
     H = gram(X)
     s, V = factor(H, n if r is None else r)
     return W, s, V
+
+
+# ---------------------------------------------------------------- scoring and tuning a quantized model
+
+def _dtype_code(t, name):
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) torch tensor")
+    code = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
+    return code
+
+
+def _rows(t, name, like=None, shape=None):
+    """A matrix whose rows are contiguous, with any row stride; returns the stride."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) torch tensor")
+    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+        raise TypeError(f"{name} must be {like.dtype} on {like.device}, got {t.dtype} on {t.device}")
+    if t.dim() != 2 or shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape) if shape is not None else '2 dimensions'}")
+    ld = t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+    if t.shape[1] > 1 and t.stride(1) != 1 or ld < t.shape[1]:
+        raise ValueError(f"{name} must have contiguous, non-overlapping rows")
+    return ld
+
+
+def _on(t, name, dev):
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+def _scratch(workspace, nb, dev, what):
+    import torch
+    if workspace is None:
+        return torch.empty(nb, dtype=torch.uint8, device=dev)
+    _dev(workspace, torch.uint8, "workspace")
+    _on(workspace, "workspace", dev)
+    return workspace
+
+
+def token_logprobs(logits, tokens=None, top=0, workspace=None):
+    """Log probabilities of given tokens, with entropy and top alternatives (mpq_token_logprobs).
+
+    `logits`: t x V, bfloat16, float16 or float32, contiguous rows; `tokens`:
+    t int32 (negative: no token, logprob 0) or None; `top` <= 128 alternatives
+    per row.  Returns dict(lse, entropy, logprob, top_ids, top_logprobs) of
+    float32 / int32 tensors (logprob without tokens and the lists without top
+    are None).
+    """
+    import torch
+    code = _dtype_code(logits, "logits")
+    ld = _rows(logits, "logits")
+    t, V = logits.shape
+    dev = logits.device
+    if tokens is not None:
+        _dev(tokens, torch.int32, "tokens", (t,))
+        _on(tokens, "tokens", dev)
+    lib = load_library()
+    with torch.cuda.device(dev):
+        stats = torch.empty((3, t), dtype=torch.float32, device=dev)
+        lse, entropy, logprob = stats.unbind(0)
+        ids = torch.empty((t, top), dtype=torch.int32, device=dev) if top > 0 else None
+        lps = torch.empty((t, top), dtype=torch.float32, device=dev) if top > 0 else None
+        ws = _scratch(workspace, lib.mpq_token_logprobs_workspace_bytes(code, t, V, top), dev, "mpq_token_logprobs")
+        rc = lib.mpq_token_logprobs(_ptr(logits), code, t, V, ld, _ptr(tokens), top,
+                                    _ptr(logprob) if tokens is not None else None, _ptr(entropy), _ptr(lse), _ptr(ids),
+                                    _ptr(lps), _ptr(ws), ws.numel(), _stream())
+    _check(rc, "mpq_token_logprobs")
+    return dict(lse=lse, entropy=entropy, logprob=logprob if tokens is not None else None, top_ids=ids,
+                top_logprobs=lps)
+
+
+def distill(logits, teacher_ids, teacher, temperature=1.0, tail=False, weights=None, grad=True, workspace=None):
+    """Distillation from a teacher's top list (mpq_distill): dict(loss, grad).
+
+    `logits`: t x V, bfloat16, float16 or float32, contiguous rows;
+    `teacher_ids` (t x k int32) and `teacher` (t x k float32): the teacher's
+    top tokens with their logits, or with their log probabilities
+    (token_logprobs' top_ids and top_logprobs), which `tail` needs: it matches
+    the mass outside the list too.  `weights` (t float32): per-row factors of
+    loss and gradient, 0 skips a row.  `grad`: True for a new tensor, False for
+    the loss alone, or a tensor to write (logits itself: in place).
+    loss: t float32, weight * KL(teacher || student) per row; grad: its
+    gradient with respect to the logits, in their type.
+    """
+    import torch
+    code = _dtype_code(logits, "logits")
+    ld = _rows(logits, "logits")
+    t, V = logits.shape
+    dev = logits.device
+    _dev(teacher_ids, torch.int32, "teacher_ids")
+    if teacher_ids.dim() != 2 or teacher_ids.shape[0] != t:
+        raise ValueError(f"teacher_ids has shape {tuple(teacher_ids.shape)}, expected ({t}, k)")
+    k = teacher_ids.shape[1]
+    _dev(teacher, torch.float32, "teacher", (t, k))
+    _on(teacher_ids, "teacher_ids", dev)
+    _on(teacher, "teacher", dev)
+    if weights is not None:
+        _dev(weights, torch.float32, "weights", (t,))
+        _on(weights, "weights", dev)
+    lib = load_library()
+    with torch.cuda.device(dev):
+        if grad is True:
+            grad = torch.empty((t, V), dtype=logits.dtype, device=dev)
+        ldg = V
+        if grad is not False and grad is not None:
+            ldg = _rows(grad, "grad", logits, (t, V))
+        else:
+            grad = None
+        loss = torch.empty(t, dtype=torch.float32, device=dev)
+        ws = _scratch(workspace, lib.mpq_distill_workspace_bytes(code, t, V, k), dev, "mpq_distill")
+        rc = lib.mpq_distill(_ptr(logits), code, t, V, ld, _ptr(teacher_ids), _ptr(teacher), k, float(temperature),
+                             1 if tail else 0, _ptr(weights), _ptr(loss), _ptr(grad), ldg, _ptr(ws), ws.numel(),
+                             _stream())
+    _check(rc, "mpq_distill")
+    return dict(loss=loss, grad=grad)

@@ -56,6 +56,15 @@ thread_local hipError_t g_last_hip_error = hipSuccess;
     }                                    \
   } while (0)
 
+}  // namespace
+namespace mpq {
+int hip_status(hipError_t e) {
+  g_last_hip_error = e;
+  return MPQ_EHIP;
+}
+}  // namespace mpq
+namespace {
+
 // Runs an entry point's body; a C++ exception (host allocation failure) becomes
 // MPQ_EHOST instead of crossing the C ABI.
 template <typename F>
@@ -1114,10 +1123,10 @@ const char* mpq_strerror(int status) {
   switch (status) {
     case MPQ_OK: return "ok";
     case MPQ_ENULL: return "a required pointer is NULL";
-    case MPQ_ESHAPE: return "invalid shape (m, n, r, K, d)";
+    case MPQ_ESHAPE: return "invalid shape (m, n, r, K, d; tokens, vocabulary, list length or a row stride)";
     case MPQ_EPARAM:
-      return "invalid parameter (T_vamp, n_cd, damping, safeguard_eps, a non-finite codebook entry or an unprepared "
-             "codebook)";
+      return "invalid parameter (T_vamp, n_cd, damping, safeguard_eps, a non-finite codebook entry, an unprepared "
+             "codebook, a storage type, an activation or a temperature)";
     case MPQ_EUNSUPPORTED:
       return "unsupported codebook (d must be 1 or 8; d = 8 entries must be exact in bfloat16; column groups need "
              "d = 1 and the uniform prior)";

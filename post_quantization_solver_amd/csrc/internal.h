@@ -262,4 +262,30 @@ hipError_t launch_copy_cols_f64(const double* src, int64_t lds, double* dst, int
                                 hipStream_t st);
 hipError_t launch_fill_i32(int32_t* dst, int64_t count, int32_t v, hipStream_t st);
 
+// ------------------------------------------------------------ logits ----
+// Storage types of activations and logits (MPQ_BF16, MPQ_FP16, MPQ_FP32).
+enum DType : int { DT_BF16 = 0, DT_F16 = 1, DT_F32 = 2 };
+
+struct LogitArgs {
+  const void* z; int64_t ldz;   // t x V logits, row stride in elements
+  int dtype;
+  int64_t t, V;
+  int64_t L; int S;             // elements per segment, segments per row (logit_split)
+  float c;                      // log2(e) / temperature
+  int top;                      // entries of the top list (0: none)
+  const int32_t* ids; int k;    // distillation: the teacher's list, t x k
+  const float* weights;         // distillation: per row, rows of weight 0 are skipped (nullptr: all 1)
+};
+constexpr int64_t LOGIT_MAX_V = (int64_t)1 << 20;
+constexpr int LOGIT_MAX_TOP = 128;
+void logit_split(LogitArgs& A);
+size_t logit_workspace(const LogitArgs& A);
+hipError_t launch_token_logprobs(const LogitArgs& A, const int32_t* tokens, float* logprob, float* entropy,
+                                 float* lse, int32_t* top_ids, float* top_lp, void* ws, hipStream_t st);
+hipError_t launch_distill(const LogitArgs& A, const float* teacher, double invT, bool tail, float* loss, void* grad,
+                          int64_t ldg, void* ws, hipStream_t st);
+
+// Notes a HIP error for mpq_hip_error_name and returns its status code.
+int hip_status(hipError_t e);
+
 }  // namespace mpq

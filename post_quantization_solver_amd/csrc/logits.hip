@@ -1,0 +1,651 @@
+// Rows of logits: token log probabilities, entropy and top alternatives, and
+// distillation from a teacher's top list.
+//
+// Mathematics.  With c = fl(log2(e) / T) and m = max_j z_j:
+//   y_j = c (z_j - m),  s = sum_j 2^y_j,  w = sum_j 2^y_j y_j,
+//   lse = m + log s,  H = ln 2 (log2 s - w / s),   q_j = 2^y_j / s.
+// The maximum is taken off before the scaling, so that logits masked by their
+// type's lowest value stay finite.  Each 2^y is one v_exp_f32 (1 ulp), eight
+// are summed as a tree and the trees in float64: a KL divergence is a small
+// difference of these sums.
+//
+// Split.  A workgroup holds one segment of a row (at most LG_SEG_BYTES) in
+// registers, so HBM is read once: the maximum, the sums and the top list come
+// from the registers.  Segments of a row are joined by a second kernel.
+//
+// Top list.  Each thread's maximum is sorted within its wave; wave w's r_w-th
+// largest (sum r_w >= k over the waves) bounds the k-th largest element from
+// below, so the elements at or above the smallest of those bounds hold the top
+// k and are few.  They go to LDS and are ranked by counting.  Should ties or
+// masked rows make them many, a bisection over the values, then over the
+// indices of equal values, finds the k exactly.
+#include <math.h>
+#include <algorithm>
+#include "mpq_device.h"
+#include "internal.h"
+
+namespace mpq {
+
+namespace {
+
+constexpr int LG_THREADS = 256;
+constexpr int LG_WAVES = LG_THREADS / 64;
+constexpr int LG_NV = 8;        // 16-byte vectors per thread
+constexpr int LG_CAP = 2048;    // candidates in LDS
+constexpr int LG_MERGE = 4096;  // keys of a row's segments merged in LDS
+constexpr double LOG2E = 1.4426950408889634074;
+constexpr double LN2 = 0.69314718055994530942;
+
+// The storage types of logits.
+struct Bf16 {
+  static constexpr int VEC = 8;
+  static constexpr uint32_t NEG_INF = 0xff80ff80u;
+  __device__ static float elem(const uint32_t* u, int e) {
+    return __uint_as_float(e & 1 ? u[e >> 1] & 0xffff0000u : u[e >> 1] << 16);
+  }
+  __device__ static float load(const void* p, int64_t i) {
+    return bf_bits2f(static_cast<const uint16_t*>(p)[i]);
+  }
+  __device__ static void store(void* p, int64_t i, float x) {
+    static_cast<uint16_t*>(p)[i] = (uint16_t)f2bf_bits(x);
+  }
+  __device__ static uint32_t pack(float x, float y) { return f2bf_pack(x, y); }
+};
+struct Fp16 {
+  static constexpr int VEC = 8;
+  static constexpr uint32_t NEG_INF = 0xfc00fc00u;
+  typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+  __device__ static float elem(const uint32_t* u, int e) { return (float)__builtin_bit_cast(h2, u[e >> 1])[e & 1]; }
+  __device__ static float load(const void* p, int64_t i) { return (float)static_cast<const _Float16*>(p)[i]; }
+  __device__ static void store(void* p, int64_t i, float x) { static_cast<_Float16*>(p)[i] = (_Float16)x; }
+  __device__ static uint32_t pack(float x, float y) {
+    h2 v = {(_Float16)x, (_Float16)y};
+    return __builtin_bit_cast(uint32_t, v);
+  }
+};
+struct Fp32 {
+  static constexpr int VEC = 4;
+  static constexpr uint32_t NEG_INF = 0xff800000u;
+  __device__ static float elem(const uint32_t* u, int e) { return __uint_as_float(u[e]); }
+  __device__ static float load(const void* p, int64_t i) { return static_cast<const float*>(p)[i]; }
+  __device__ static void store(void* p, int64_t i, float x) { static_cast<float*>(p)[i] = x; }
+  __device__ static uint32_t pack(float x, float) { return __float_as_uint(x); }
+};
+
+constexpr int es_of(int dtype) { return dtype == DT_F32 ? 4 : 2; }
+
+// 16 bytes from an element-aligned address.
+struct __attribute__((packed, aligned(2))) Raw16 {
+  uint32_t u[4];
+};
+template <typename T>
+__device__ __forceinline__ void load_vec(const void* row, int64_t i, int64_t end, uint32_t* u) {
+  constexpr int ES = 16 / T::VEC;
+  const char* p = static_cast<const char*>(row) + i * ES;
+  if (i + T::VEC <= end) {
+    const Raw16 r = *reinterpret_cast<const Raw16*>(p);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) u[q] = r.u[q];
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) u[q] = T::NEG_INF;
+#pragma unroll
+    for (int e = 0; e < T::VEC; ++e)
+      if (i + e < end) {
+        if (ES == 4) {
+          u[e] = *reinterpret_cast<const uint32_t*>(p + 4 * e);
+        } else {
+          const uint32_t h = *reinterpret_cast<const uint16_t*>(p + 2 * e);
+          u[e >> 1] = e & 1 ? (u[e >> 1] & 0xffffu) | h << 16 : (u[e >> 1] & 0xffff0000u) | h;
+        }
+      }
+  }
+}
+
+__device__ __forceinline__ float wave_max(float v) {
+  for (int o = 32; o; o >>= 1) v = fmaxf(v, shfl_xor_f(v, o));
+  return v;
+}
+__device__ __forceinline__ double wave_sum(double v) {
+  for (int o = 32; o; o >>= 1) v += shfl_d(v, (int)(threadIdx.x & 63) ^ o);
+  return v;
+}
+__device__ __forceinline__ int wave_sum_i(int v) {
+  for (int o = 32; o; o >>= 1) v += shfl_xor_i(v, o);
+  return v;
+}
+
+// Order of floats as unsigned integers; -0 equals +0 (the caller adds +0).
+__device__ __forceinline__ uint32_t ord(float x) {
+  const uint32_t u = __float_as_uint(x);
+  return u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float unord(uint32_t o) {
+  return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
+}
+// Larger key = larger value, then lower index.  0 is no entry.
+__device__ __forceinline__ uint64_t top_key(float x, int64_t idx) {
+  return (uint64_t)ord(x + 0.f) << 32 | (uint32_t)~(uint32_t)idx;
+}
+
+// Descending bitonic sort of one float per lane.
+__device__ __forceinline__ float wave_sort_desc(float v) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int k = 2; k <= 64; k <<= 1)
+#pragma unroll
+    for (int j = k >> 1; j; j >>= 1) {
+      const float o = shfl_xor_f(v, j);
+      const bool up = ((lane & k) != 0) != ((lane & j) != 0);   // this lane keeps the smaller
+      v = up ? fminf(v, o) : fmaxf(v, o);
+    }
+  return v;
+}
+
+// One segment's statistics.
+struct Part {
+  double s, w;      // sums of 2^y and 2^y y
+  double rest;      // s without the listed entries (tail form)
+  float m, pad;     // the maximum
+};
+
+struct Shared {
+  uint64_t key[LG_CAP];
+  double d[3][LG_WAVES];
+  float f[LG_WAVES];
+  int i[LG_WAVES];
+  int cnt;
+};
+
+__device__ __forceinline__ int block_count(int n, Shared& sh) {
+  n = wave_sum_i(n);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) sh.i[wave_id()] = n;
+  __syncthreads();
+  int a = 0;
+#pragma unroll
+  for (int w = 0; w < LG_WAVES; ++w) a += sh.i[w];
+  return a;
+}
+
+// The k largest (value, then lowest index) of this segment's registers, ranked,
+// into list[0..k); unused places hold 0.
+template <typename T>
+__device__ void segment_top(const uint32_t (&u)[LG_NV][4], float tmax, const char* z, int64_t base, int64_t end, int k,
+                            Shared& sh, uint64_t* __restrict__ list) {
+  const int t = threadIdx.x, wave = wave_id();
+  const float sorted = wave_sort_desc(tmax);
+  const int act = __popcll(__ballot(tmax > -INFINITY));
+  if ((t & 63) == 0) sh.i[wave] = act;
+  if (t == 0) sh.cnt = 0;
+  __syncthreads();
+  int A = 0;
+#pragma unroll
+  for (int w = 0; w < LG_WAVES; ++w) A += sh.i[w];
+  float bound = -INFINITY;
+  if (A >= k) {
+    const int r = (k * act + A - 1) / A;   // <= act
+    const float mine = r > 0 ? __shfl(sorted, r - 1, 64) : INFINITY;
+    if ((t & 63) == 0) sh.f[wave] = mine;
+    __syncthreads();
+    bound = sh.f[0];
+#pragma unroll
+    for (int w = 1; w < LG_WAVES; ++w) bound = fminf(bound, sh.f[w]);
+  }
+#pragma unroll
+  for (int j = 0; j < LG_NV; ++j) {
+    float m = T::elem(u[j], 0);
+#pragma unroll
+    for (int e = 1; e < T::VEC; ++e) m = fmaxf(m, T::elem(u[j], e));
+    if (m >= bound) {
+#pragma unroll
+      for (int e = 0; e < T::VEC; ++e) {
+        const float x = T::elem(u[j], e);
+        if (x >= bound && x > -INFINITY) {
+          const int at = atomicAdd(&sh.cnt, 1);
+          if (at < LG_CAP) sh.key[at] = top_key(x, base + (int64_t)(j * LG_THREADS + t) * T::VEC + e);
+        }
+      }
+    }
+  }
+  __syncthreads();
+  int N = sh.cnt;
+  if (N > LG_CAP) {
+    // bisection: the largest value with at least k elements at or above it,
+    // then the index below which enough of its equals lie (re-reads the
+    // segment: rare, and registers for it would halve the common case)
+    auto count = [&](uint32_t v, int64_t last) {
+      int n = 0;
+#pragma unroll 1
+      for (int64_t i = base + t; i < end; i += LG_THREADS) {
+        const float x = T::load(z, i);
+        const uint32_t o = ord(x + 0.f);
+        n += x > -INFINITY && (o > v || (o == v && i <= last)) ? 1 : 0;
+      }
+      return block_count(n, sh);
+    };
+    uint32_t lo = ord(-INFINITY), hi = ord(INFINITY);   // count(lo) >= k, as N > LG_CAP >= k
+    while (hi - lo > 1) {
+      const uint32_t mid = lo + (hi - lo) / 2;
+      if (count(mid, INT64_MAX) >= k) lo = mid; else hi = mid;
+    }
+    int64_t il = base - 1, ih = end - 1;
+    while (ih - il > 1) {
+      const int64_t mid = il + (ih - il) / 2;
+      if (count(lo, mid) >= k) ih = mid; else il = mid;
+    }
+    if (t == 0) sh.cnt = 0;
+    __syncthreads();
+#pragma unroll 1
+    for (int64_t i = base + t; i < end; i += LG_THREADS) {
+      const float x = T::load(z, i);
+      const uint32_t o = ord(x + 0.f);
+      if (x > -INFINITY && (o > lo || (o == lo && i <= ih))) {
+        const int at = atomicAdd(&sh.cnt, 1);
+        if (at < LG_CAP) sh.key[at] = top_key(x, i);
+      }
+    }
+    __syncthreads();
+    N = min(sh.cnt, LG_CAP);   // k, or more where the row holds +inf (its list is not reported)
+  }
+  for (int i = t; i < N; i += LG_THREADS) {
+    const uint64_t key = sh.key[i];
+    int rank = 0;
+    for (int j = 0; j < N; ++j) rank += sh.key[j] > key ? 1 : 0;
+    if (rank < k) list[rank] = key;
+  }
+  for (int i = N + t; i < k; i += LG_THREADS) list[i] = 0;
+}
+
+// One segment of one row: statistics, and the top list (k > 0) or the sum
+// without the listed entries (TAIL).
+template <typename T, bool TAIL>
+__global__ __launch_bounds__(LG_THREADS) void logit_part_kernel(LogitArgs A, Part* __restrict__ parts,
+                                                                uint64_t* __restrict__ lists,
+                                                                float* __restrict__ zl) {
+  __shared__ Shared sh;
+  const int t = threadIdx.x, wave = wave_id();
+  const int64_t row = blockIdx.x / A.S;
+  const int seg = (int)(blockIdx.x - row * A.S);
+  if (A.weights && A.weights[row] == 0.f) return;
+  const int64_t base = (int64_t)seg * A.L, end = min(A.V, base + A.L);
+  const char* z = static_cast<const char*>(A.z) + row * A.ldz * (16 / T::VEC);
+  uint32_t u[LG_NV][4];
+#pragma unroll
+  for (int j = 0; j < LG_NV; ++j) load_vec<T>(z, base + (int64_t)(j * LG_THREADS + t) * T::VEC, end, u[j]);
+  // distillation: the listed logits, kept for the second kernel (which may
+  // write the gradient over the logits)
+  for (int i = t; i < A.k; i += LG_THREADS) {
+    const int64_t id = A.ids[row * A.k + i];
+    if (id >= base && id < end) zl[row * A.k + i] = T::load(z, id);
+  }
+  uint8_t* listed = reinterpret_cast<uint8_t*>(sh.key);   // one byte per vector
+  if (TAIL) {
+    for (int i = t; i < LG_NV * LG_THREADS / 4; i += LG_THREADS) reinterpret_cast<uint32_t*>(listed)[i] = 0;
+    __syncthreads();
+    for (int i = t; i < A.k; i += LG_THREADS) {
+      const int64_t id = A.ids[row * A.k + i];
+      if (id >= base && id < end) {
+        const int v = (int)(id - base) / T::VEC, e = (int)(id - base) % T::VEC;
+        atomicOr(reinterpret_cast<uint32_t*>(listed) + (v >> 2), 1u << (8 * (v & 3) + e));
+      }
+    }
+  }
+  float tmax = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < LG_NV; ++j)
+#pragma unroll
+    for (int e = 0; e < T::VEC; ++e) tmax = fmaxf(tmax, T::elem(u[j], e));
+  float m = wave_max(tmax);
+  if ((t & 63) == 0) sh.f[wave] = m;
+  __syncthreads();
+  m = sh.f[0];
+#pragma unroll
+  for (int w = 1; w < LG_WAVES; ++w) m = fmaxf(m, sh.f[w]);
+  if (m == -INFINITY) m = 0.f;
+  double s = 0.0, w = 0.0, rest = 0.0;
+#pragma unroll
+  for (int j = 0; j < LG_NV; ++j) {
+    float es[T::VEC], ew[T::VEC];
+    float y[T::VEC];
+#pragma unroll
+    for (int e = 0; e < T::VEC; ++e) {
+      y[e] = (T::elem(u[j], e) - m) * A.c;
+      es[e] = __builtin_amdgcn_exp2f(y[e]);
+      ew[e] = es[e] * fmaxf(y[e], -1e30f);   // 0, not NaN, at -inf
+    }
+    if (TAIL) {
+      const uint32_t b = listed[j * LG_THREADS + t];
+#pragma unroll
+      for (int e = 0; e < T::VEC; ++e) ew[e] = b >> e & 1u ? 0.f : es[e];
+    }
+#pragma unroll
+    for (int o = T::VEC / 2; o; o >>= 1)
+#pragma unroll
+      for (int e = 0; e < o; ++e) {
+        es[e] += es[e + o];
+        ew[e] += ew[e + o];
+      }
+    s += (double)es[0];
+    if (TAIL) rest += (double)ew[0]; else w += (double)ew[0];
+  }
+  s = wave_sum(s);
+  w = wave_sum(TAIL ? rest : w);
+  if ((t & 63) == 0) {
+    sh.d[0][wave] = s;
+    sh.d[1][wave] = w;
+  }
+  __syncthreads();
+  if (t == 0) {
+    Part p;
+    p.s = p.w = 0.0;
+    for (int i = 0; i < LG_WAVES; ++i) {
+      p.s += sh.d[0][i];
+      p.w += sh.d[1][i];
+    }
+    p.rest = p.w;
+    p.m = m;
+    p.pad = 0.f;
+    parts[row * A.S + seg] = p;
+  }
+  if (!TAIL && A.top > 0) segment_top<T>(u, tmax, z, base, end, A.top, sh, lists + (row * A.S + seg) * A.top);
+}
+
+// Joins a row's segments: every lane returns the row's (s, w, rest) at the
+// common m.
+struct RowStat {
+  double s, w, rest;
+  float m;
+};
+__device__ RowStat join_parts(const Part* __restrict__ p, int S, float c) {
+  RowStat r;
+  float m = -INFINITY;
+  for (int i = 0; i < S; ++i)
+    if (!(p[i].s == 0.0)) m = fmaxf(m, p[i].m);   // NaN sums take part
+  r.m = m == -INFINITY ? 0.f : m;
+  r.s = r.w = r.rest = 0.0;
+  for (int i = 0; i < S; ++i) {
+    if (p[i].s == 0.0) continue;
+    const double d = ((double)p[i].m - (double)r.m) * (double)c, f = exp2(d);
+    r.s += f * p[i].s;
+    r.w += f * (p[i].w + d * p[i].s);
+    r.rest += f * p[i].rest;
+  }
+  return r;
+}
+
+// Entries of a descending list above key.
+__device__ __forceinline__ int count_above(const uint64_t* list, int k, uint64_t key) {
+  int lo = 0, hi = k;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (list[mid] > key) lo = mid + 1; else hi = mid;
+  }
+  return lo;
+}
+
+template <typename T>
+__global__ __launch_bounds__(LG_THREADS) void logprob_row_kernel(LogitArgs A, const Part* __restrict__ parts,
+                                                                 const uint64_t* __restrict__ lists,
+                                                                 const int32_t* __restrict__ tokens,
+                                                                 float* __restrict__ logprob,
+                                                                 float* __restrict__ entropy, float* __restrict__ lse_out,
+                                                                 int32_t* __restrict__ top_ids,
+                                                                 float* __restrict__ top_lp) {
+  __shared__ uint64_t keys[LG_MERGE];
+  const int64_t row = blockIdx.x;
+  const int t = threadIdx.x, k = A.top, S = A.S;
+  const RowStat r = join_parts(parts + row * S, S, A.c);
+  const bool bad = !(r.s >= 0.0);   // a NaN or +inf logit
+  // Log probabilities are taken of the logits as scaled by c; lse alone is
+  // corrected for c's rounding: d lse / d scale is the mean logit.
+  const double lg = log2(r.s);
+  const double lse = bad ? (double)NAN
+                     : r.s > 0.0 ? (double)r.m + lg * LN2 + (1.0 - (double)A.c * LN2) * (r.w / r.s / (double)A.c)
+                                 : -(double)INFINITY;
+  auto lp_of = [&](float x) {
+    return bad ? NAN : x == -INFINITY ? -INFINITY : (float)((((double)x - (double)r.m) * (double)A.c - lg) * LN2);
+  };
+  if (t == 0) {
+    if (lse_out) lse_out[row] = (float)lse;
+    if (entropy) entropy[row] = bad ? NAN : r.s > 0.0 ? (float)(LN2 * (lg - r.w / r.s)) : 0.f;
+    if (logprob) {
+      const int32_t tok = tokens[row];
+      float v = 0.f;
+      if (tok >= A.V)
+        v = NAN;
+      else if (tok >= 0)
+        v = lp_of(T::load(static_cast<const char*>(A.z) + row * A.ldz * (16 / T::VEC), tok));
+      logprob[row] = v;
+    }
+  }
+  if (k == 0) return;
+  const uint64_t* list = lists + row * S * k;
+  if (S * k <= LG_MERGE) {
+    for (int i = t; i < S * k; i += LG_THREADS) keys[i] = list[i];
+    __syncthreads();
+    list = keys;
+  }
+  auto put = [&](int rank, uint64_t key) {
+    const int64_t at = row * k + rank;
+    if (top_ids) top_ids[at] = bad || !key ? -1 : (int32_t)~(uint32_t)key;
+    if (top_lp) top_lp[at] = lp_of(key ? unord((uint32_t)(key >> 32)) : -INFINITY);
+  };
+  if (S == 1) {
+    for (int i = t; i < k; i += LG_THREADS) put(i, list[i]);
+    return;
+  }
+  int have = 0;
+  for (int g = 0; g < S; ++g) have += count_above(list + g * k, k, 0);
+  for (int i = t; i < S * k; i += LG_THREADS) {
+    const uint64_t key = list[i];
+    if (!key) continue;
+    const int g = i / k;
+    int rank = i - g * k;
+    for (int o = 0; o < S && rank < k; ++o)
+      if (o != g) rank += count_above(list + o * k, k, key);
+    if (rank < k) put(rank, key);
+  }
+  for (int i = have + t; i < k; i += LG_THREADS) put(i, 0);
+}
+
+// Distillation, one segment of one row: every workgroup joins the row's
+// statistics and the teacher's list itself (k <= 128 entries), segment 0 writes
+// the loss, each writes its share of the gradient: q_j times one factor per
+// row, then the listed entries, each by one thread, over it.
+template <typename T>
+__global__ __launch_bounds__(LG_THREADS) void distill_grad_kernel(LogitArgs A, const Part* __restrict__ parts,
+                                                                  const float* __restrict__ zl,
+                                                                  const float* __restrict__ teacher, double invT,
+                                                                  int tail, float* __restrict__ loss,
+                                                                  void* __restrict__ grad, int64_t ldg) {
+  __shared__ int32_t sid[LG_THREADS];
+  __shared__ float sp[LG_THREADS];
+  __shared__ double red[3][LG_WAVES];
+  __shared__ float redm[LG_WAVES];
+  const int t = threadIdx.x, wave = wave_id();
+  const int64_t row = blockIdx.x / A.S;
+  const int seg = (int)(blockIdx.x - row * A.S);
+  const float wt = A.weights ? A.weights[row] : 1.f;
+  const int64_t base = (int64_t)seg * A.L, end = min(A.V, base + A.L);
+  const char* z = static_cast<const char*>(A.z) + row * A.ldz * (16 / T::VEC);
+  char* gr = grad ? static_cast<char*>(grad) + row * ldg * (16 / T::VEC) : nullptr;
+  auto store_vec = [&](int64_t i, const float* g) {
+    if (i + T::VEC <= end) {
+      Raw16 r;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        r.u[q] = T::VEC == 8 ? T::pack(g[(2 * q) % T::VEC], g[(2 * q + 1) % T::VEC]) : T::pack(g[q % T::VEC], 0.f);
+      *reinterpret_cast<Raw16*>(gr + i * (16 / T::VEC)) = r;
+    } else {
+#pragma unroll
+      for (int e = 0; e < T::VEC; ++e)
+        if (i + e < end) T::store(gr, i + e, g[e]);
+    }
+  };
+  if (wt == 0.f) {
+    if (seg == 0 && t == 0) loss[row] = 0.f;
+    if (!gr) return;
+    const float zero[T::VEC] = {};
+    for (int64_t i = base + (int64_t)t * T::VEC; i < end; i += LG_THREADS * T::VEC) store_vec(i, zero);
+    return;
+  }
+  const RowStat r = join_parts(parts + row * A.S, A.S, A.c);
+  const double lg = log2(r.s);
+  // this thread's entry of the teacher's list
+  int32_t id = -1;
+  double lt = -INFINITY;
+  float zi = 0.f;
+  if (t < A.k) {
+    id = A.ids[row * A.k + t];
+    if (id < 0 || id >= A.V) id = -1;
+    if (id >= 0) {
+      lt = (double)teacher[row * A.k + t] * invT;
+      zi = zl[row * A.k + t];
+      if (!tail && lt == -INFINITY) id = -1;   // no mass: as if not listed
+    }
+  }
+  // p: softmax over the list, or the log probabilities themselves (tail)
+  double p, lp;
+  if (tail) {
+    lp = lt;
+    p = exp(lt);
+  } else {
+    float mx = wave_max((float)lt);
+    if ((t & 63) == 0) redm[wave] = mx;
+    __syncthreads();
+    mx = redm[0];
+    for (int i = 1; i < LG_WAVES; ++i) mx = fmaxf(mx, redm[i]);
+    const double e = id >= 0 ? exp(lt - (double)mx) : 0.0;
+    const double es = wave_sum(e);
+    if ((t & 63) == 0) red[0][wave] = es;
+    __syncthreads();
+    double tot = 0.0;
+    for (int i = 0; i < LG_WAVES; ++i) tot += red[0][i];
+    lp = lt - (double)mx - log(tot);
+    p = e / tot;
+    __syncthreads();
+  }
+  if (id < 0) p = 0.0;
+  const double lq = (((double)zi - (double)r.m) * (double)A.c - lg) * LN2;
+  const double term = p == 0.0 ? 0.0 : p * (lp - lq);
+  const double ps = wave_sum(p), ts = wave_sum(term);
+  if ((t & 63) == 0) {
+    red[1][wave] = ps;
+    red[2][wave] = ts;
+  }
+  sid[t] = id;
+  sp[t] = (float)p;
+  __syncthreads();
+  double psum = 0.0, kl = 0.0;
+  for (int i = 0; i < LG_WAVES; ++i) {
+    psum += red[1][i];
+    kl += red[2][i];
+  }
+  // how often the list names each token (a token named twice has the sum)
+  float pown = 0.f;
+  bool first = id >= 0;
+  int named = 0;
+  if (id >= 0)
+    for (int i = 0; i < A.k; ++i)
+      if (sid[i] == id) {
+        pown += sp[i];
+        if (i < t) first = false;
+      }
+  named = __syncthreads_count(first ? 1 : 0);
+  double coef = 1.0;   // of an unlisted q_j
+  if (tail) {
+    // below 2^-20 the remainder is the rounding of the k float32 log
+    // probabilities (k 2^-24 at most 2^-17 of them, of which most is shared);
+    // a list that names every token has none
+    double pt = 1.0 - psum;
+    if (pt < 0x1p-20 || named >= A.V) pt = 0.0;
+    if (pt > 0.0) {
+      const double qt = r.rest / r.s;
+      kl += pt * (log(pt) - log(qt));
+      coef = 1.0 - pt / qt;
+    }
+  } else {
+    coef = psum > 0.0 || psum != psum ? 1.0 : 0.0;   // an empty list teaches nothing
+  }
+  if (seg == 0 && t == 0) loss[row] = (float)((double)wt * kl);
+  if (!gr) return;
+  const double g0 = (double)wt * invT;
+  const float m = r.m, f = (float)(coef * g0 / r.s), inv = (float)(1.0 / r.s);
+  float glist = 0.f;
+  if (first) glist = (__builtin_amdgcn_exp2f((zi - m) * A.c) * inv - pown) * (float)g0;
+  for (int64_t i = base + (int64_t)t * T::VEC; i < end; i += LG_THREADS * T::VEC) {
+    uint32_t u[4];
+    load_vec<T>(z, i, end, u);
+    float g[T::VEC];
+#pragma unroll
+    for (int e = 0; e < T::VEC; ++e) g[e] = __builtin_amdgcn_exp2f((T::elem(u, e) - m) * A.c) * f;
+    store_vec(i, g);
+  }
+  __syncthreads();
+  if (first && id >= base && id < end) T::store(gr, id, glist);
+}
+
+}  // namespace
+
+// ------------------------------------------------------------------ launchers
+
+// Segments: at most the registers of a workgroup, and shorter where there are
+// few rows, so that at least 512 workgroups (two per CU) share the work, but
+// none under 4096 elements.
+void logit_split(LogitArgs& A) {
+  const int64_t vec = 16 / es_of(A.dtype);
+  const int64_t most = (int64_t)LG_NV * LG_THREADS * vec;
+  const int64_t need = (A.V + most - 1) / most;
+  const int64_t want = std::min((A.V + 4095) / 4096, (512 + A.t - 1) / std::max<int64_t>(A.t, 1));
+  int64_t S = std::max(need, want);
+  A.L = ((A.V + S - 1) / S + vec - 1) / vec * vec;
+  A.S = (int)((A.V + A.L - 1) / A.L);
+}
+
+size_t logit_workspace(const LogitArgs& A) {
+  const size_t rows = (size_t)A.t * A.S;
+  return rows * sizeof(Part) + rows * A.top * sizeof(uint64_t) + (size_t)A.t * A.k * sizeof(float);
+}
+
+#define LOGIT_TYPES(dtype, call)      \
+  switch (dtype) {                    \
+    case DT_BF16: { using T = Bf16; call; break; } \
+    case DT_F16: { using T = Fp16; call; break; }  \
+    default: { using T = Fp32; call; break; }      \
+  }
+
+hipError_t launch_token_logprobs(const LogitArgs& A, const int32_t* tokens, float* logprob, float* entropy,
+                                 float* lse, int32_t* top_ids, float* top_lp, void* ws, hipStream_t st) {
+  Part* parts = static_cast<Part*>(ws);
+  uint64_t* lists = reinterpret_cast<uint64_t*>(parts + A.t * A.S);
+  const dim3 grid((unsigned)(A.t * A.S)), block(LG_THREADS);
+  LOGIT_TYPES(A.dtype, hipLaunchKernelGGL((logit_part_kernel<T, false>), grid, block, 0, st, A, parts, lists,
+                                          static_cast<float*>(nullptr)));
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  LOGIT_TYPES(A.dtype, hipLaunchKernelGGL((logprob_row_kernel<T>), dim3((unsigned)A.t), block, 0, st, A, parts, lists,
+                                          tokens, logprob, entropy, lse, top_ids, top_lp));
+  return hipGetLastError();
+}
+
+hipError_t launch_distill(const LogitArgs& A, const float* teacher, double invT, bool tail, float* loss, void* grad,
+                          int64_t ldg, void* ws, hipStream_t st) {
+  Part* parts = static_cast<Part*>(ws);
+  float* zl = reinterpret_cast<float*>(parts + A.t * A.S);
+  const dim3 grid((unsigned)(A.t * A.S)), block(LG_THREADS);
+  if (tail) {
+    LOGIT_TYPES(A.dtype, hipLaunchKernelGGL((logit_part_kernel<T, true>), grid, block, 0, st, A, parts,
+                                            static_cast<uint64_t*>(nullptr), zl));
+  } else {
+    LOGIT_TYPES(A.dtype, hipLaunchKernelGGL((logit_part_kernel<T, false>), grid, block, 0, st, A, parts,
+                                            static_cast<uint64_t*>(nullptr), zl));
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  LOGIT_TYPES(A.dtype, hipLaunchKernelGGL((distill_grad_kernel<T>), grid, block, 0, st, A, parts, zl, teacher, invT,
+                                          tail ? 1 : 0, loss, grad, ldg));
+  return hipGetLastError();
+}
+
+}  // namespace mpq
