@@ -76,6 +76,8 @@ typedef struct {
   int32_t e8_last2[8];     /* E8 prefix: twice the last codeword's coordinates */
   const void* tables;      /* device, caller-owned: the codebook's tables */
   uint64_t magic;          /* set by mpq_codebook_prepare */
+  int32_t narrow;          /* 1: the entries (d = 1: their differences to level K / 2) are exact in
+                              bfloat16 and in float16, as mpq_pack needs them */
 } mpq_codebook;
 
 #define MPQ_CB_GENERIC   0
@@ -465,12 +467,74 @@ size_t mpq_factor_workspace_bytes(int64_t n);
 int mpq_factor(double* H, int64_t n, int64_t r, float* s, float* V, void* workspace, size_t ws_bytes,
                void* stream);
 
-/* ------------------------------------------------------------------ scoring and tuning a quantized model */
+/* ------------------------------------------------------------------ the quantized layer's product */
 
 /* Storage types of activations and logits. */
 #define MPQ_BF16 0
 #define MPQ_FP16 1
 #define MPQ_FP32 2
+
+/* A solved layer's codes, packed once for mpq_linear: 4 bits a weight (d = 1,
+ * K <= 16), 8 bits (d = 1, K <= 64) or 16 bits per 8 weights (d = 8), in the
+ * order the kernels read.  codes: m x n/d int32 (mpq_quantize_layer's; a code
+ * outside [0, K) is packed as code 0); packed: device, 256-byte aligned, at
+ * least mpq_pack_bytes(m, n, K, d) bytes (0 if the shapes are out of range:
+ * 0 <= m <= 2^24, 1 <= n <= 65536, n % d == 0, K as for a codebook).
+ * Errors: MPQ_EUNSUPPORTED also for a codebook without `narrow`. */
+size_t mpq_pack_bytes(int64_t m, int64_t n, int64_t K, int64_t d);
+int mpq_pack(const int32_t* codes, int64_t m, int64_t n, const mpq_codebook* cb, void* packed, size_t packed_bytes,
+             void* stream);
+
+/* Activations of mpq_linear's epilogue. */
+#define MPQ_ACT_NONE      0
+#define MPQ_ACT_RELU      1
+#define MPQ_ACT_GELU      2   /* u Phi(u), by erf */
+#define MPQ_ACT_GELU_TANH 3   /* its tanh form */
+#define MPQ_ACT_SILU      4   /* u / (1 + exp(-u)) */
+
+/* The quantized layer's product with its epilogue:
+ *   u = x W^T + bias,  y = act(u) + residual,
+ *   W[i][j] = scale[i][g] e + offset[i][g], e the entry of the weight's code,
+ *   g = j / group (group = 0 or >= n: one scale and offset per row).
+ * x: t x n of `dtype`, y, residual, pre: t x m of `dtype`, device, rows
+ * contiguous with strides ldx, ldy, ldr, ldp in elements (any element
+ * alignment; 16-byte aligned rows are fastest).  scale and offset: float32,
+ * m x ceil(n / group); offset NULL: zero.  bias: m float32, NULL: none.
+ * residual NULL: none.  pre NULL, or u, what mpq_linear_backward needs where
+ * there is an activation.  y may be the residual (same pointer and stride) and
+ * otherwise overlaps no input.
+ * Column groups need d = 1.  Sums are float32.  The entries enter as they are;
+ * where column groups and the token count make the weights themselves enter
+ * (more than 128 tokens, or groups that are no multiple of the packed chunk:
+ * 128 columns at 4 bits, 64 at 8), they enter as two 16-bit terms (float32 x:
+ * three).  A token whose x holds NaN or infinities has NaN or infinite outputs;
+ * no other token does.
+ * 0 <= t < 2^22.  Nothing is kept between calls; calls may overlap on separate
+ * workspaces. */
+size_t mpq_linear_workspace_bytes(int dtype, int64_t t, int64_t m, int64_t n, int64_t K, int64_t d, int64_t group);
+int mpq_linear(const void* x, int dtype, int64_t t, int64_t ldx, const void* packed, int64_t m, int64_t n,
+               const mpq_codebook* cb, const float* scale, const float* offset, int64_t group, const float* bias,
+               int act, const void* residual, int64_t ldr, void* y, int64_t ldy, void* pre, int64_t ldp,
+               void* workspace, size_t ws_bytes, void* stream);
+
+/* Its gradients, the codes fixed: with du = dy act'(pre),
+ *   dx = du W (t x n of `dtype`; NULL: not wanted),
+ *   dscale = sum over the tokens and a group's columns of du x e,
+ *   doffset = the same without e (both m x ceil(n / group) float32),
+ *   dbias = sum of du over the tokens (m float32);
+ * the last three together, or all NULL: not wanted.  The residual's gradient is
+ * dy.  pre: mpq_linear's (needed with an activation).  The sums are of du in 24
+ * bits; dx's du and scale are multiplied and rounded once to 8 bits (float16:
+ * 16, float32: 24).  t = 0: zeros. */
+size_t mpq_linear_backward_workspace_bytes(int dtype, int64_t t, int64_t m, int64_t n, int64_t K, int64_t d,
+                                           int64_t group);
+int mpq_linear_backward(const void* dy, int64_t lddy, const void* x, int dtype, int64_t t, int64_t ldx,
+                        const void* packed, int64_t m, int64_t n, const mpq_codebook* cb, const float* scale,
+                        const float* offset, int64_t group, int act, const void* pre, int64_t ldp, void* dx,
+                        int64_t lddx, float* dscale, float* doffset, float* dbias, void* workspace, size_t ws_bytes,
+                        void* stream);
+
+/* ------------------------------------------------------------------ scoring and tuning a quantized model */
 
 /* Rows of logits, device, t x V of `dtype`, row stride ld >= V elements (any
  * element alignment): per row

@@ -93,3 +93,73 @@ def distill(z, ids, teacher, T=1.0, tail=False, weights=None):
         grad[i] = w / T * g
         scale[i] = w / T * (q * (1 + share) + p)
     return loss, grad, scale
+
+
+# ------------------------------------------------------------------ a solved layer's product
+
+def layer_entries(codes, E, group):
+    """Entries (m x n) and each column's group."""
+    E = np.asarray(E, np.float64)
+    m = codes.shape[0]
+    e = E[codes].reshape(m, -1)
+    n = e.shape[1]
+    g = group if 0 < group < n else n
+    return e, np.arange(n) // g
+
+
+def layer_weights(codes, E, scale, offset, group=0):
+    e, col = layer_entries(codes, E, group)
+    a = np.asarray(scale, np.float64).reshape(e.shape[0], -1)[:, col]
+    w = a * e
+    if offset is not None:
+        w = w + np.asarray(offset, np.float64).reshape(e.shape[0], -1)[:, col]
+    return w
+
+
+def act(name, u):
+    if name is None:
+        return u
+    if name == "relu":
+        return np.where(u < 0, 0.0, u)
+    if name == "silu":
+        return u / (1 + np.exp(-u))
+    if name == "gelu":
+        return 0.5 * u * (1 + np.vectorize(math.erf)(u / math.sqrt(2)))
+    return 0.5 * u * (1 + np.tanh(math.sqrt(2 / math.pi) * (u + 0.044715 * u ** 3)))
+
+
+def act_slope(name, u):
+    if name is None:
+        return np.ones_like(u)
+    if name == "relu":
+        return (u > 0).astype(np.float64)
+    if name == "silu":
+        q = 1 / (1 + np.exp(-u))
+        return q * (1 + u * (1 - q))
+    if name == "gelu":
+        return 0.5 * (1 + np.vectorize(math.erf)(u / math.sqrt(2))) + u * np.exp(-0.5 * u * u) / math.sqrt(2 * math.pi)
+    c = math.sqrt(2 / math.pi)
+    th = np.tanh(c * (u + 0.044715 * u ** 3))
+    return 0.5 * (1 + th) + 0.5 * u * (1 - th * th) * c * (1 + 3 * 0.044715 * u * u)
+
+
+def linear(x, w, bias=None, name=None, residual=None):
+    """(y, pre)"""
+    u = x @ w.T
+    if bias is not None:
+        u = u + bias
+    y = act(name, u)
+    return (y if residual is None else y + residual), u
+
+
+def linear_backward(dy, x, codes, E, scale, offset, group=0, pre=None, name=None):
+    du = dy * (act_slope(name, pre) if name is not None else 1.0)
+    w = layer_weights(codes, E, scale, offset, group)
+    e, col = layer_entries(codes, E, group)
+    dW = du.T @ x
+    G = int(col[-1]) + 1
+    da, do = np.zeros((w.shape[0], G)), np.zeros((w.shape[0], G))
+    for g in range(G):
+        da[:, g] = (dW * e)[:, col == g].sum(1)
+        do[:, g] = dW[:, col == g].sum(1)
+    return dict(dx=du @ w, dscale=da.reshape(np.shape(scale)), doffset=do.reshape(np.shape(scale)), dbias=du.sum(0))

@@ -31,6 +31,8 @@ EXPORTS = ("mpq_workspace_bytes", "mpq_strerror", "mpq_codebook_bytes", "mpq_cod
            "mpq_greedy_workspace_bytes", "mpq_gram_workspace_bytes", "mpq_gram", "mpq_rht",
            "mpq_factor_workspace_bytes", "mpq_factor", "mpq_codebook_kind", "mpq_hip_error_name",
            "mpq_e8dp_transitions", "mpq_probe_rate",
+           "mpq_pack_bytes", "mpq_pack", "mpq_linear_workspace_bytes", "mpq_linear",
+           "mpq_linear_backward_workspace_bytes", "mpq_linear_backward",
            "mpq_token_logprobs_workspace_bytes", "mpq_token_logprobs", "mpq_distill_workspace_bytes", "mpq_distill")
 
 
@@ -62,7 +64,7 @@ PROF_COUNT = len(PROF_NAMES)
 class Codebook(ctypes.Structure):
     _fields_ = [("K", ctypes.c_int64), ("d", ctypes.c_int64), ("kind", ctypes.c_int32),
                 ("e8_qlast", ctypes.c_int32), ("e8_last2", ctypes.c_int32 * 8), ("tables", ctypes.c_void_p),
-                ("magic", ctypes.c_uint64)]
+                ("magic", ctypes.c_uint64), ("narrow", ctypes.c_int32)]
 
 
 class Options(ctypes.Structure):
@@ -202,6 +204,16 @@ def load_library(path: str = LIB_PATH):
     lib.mpq_hip_error_name.argtypes = []
     lib.mpq_hip_error_name.restype = ctypes.c_char_p
     lib.mpq_probe_rate.argtypes = [I, P, SZ, ctypes.POINTER(ctypes.c_double), P]
+    lib.mpq_pack_bytes.argtypes = [I64, I64, I64, I64]
+    lib.mpq_pack_bytes.restype = SZ
+    lib.mpq_pack.argtypes = [P, I64, I64, CB, P, SZ, P]
+    lib.mpq_linear_workspace_bytes.argtypes = [I, I64, I64, I64, I64, I64, I64]
+    lib.mpq_linear_workspace_bytes.restype = SZ
+    lib.mpq_linear.argtypes = [P, I, I64, I64, P, I64, I64, CB, P, P, I64, P, I, P, I64, P, I64, P, I64, P, SZ, P]
+    lib.mpq_linear_backward_workspace_bytes.argtypes = [I, I64, I64, I64, I64, I64, I64]
+    lib.mpq_linear_backward_workspace_bytes.restype = SZ
+    lib.mpq_linear_backward.argtypes = [P, I64, P, I, I64, I64, P, I64, I64, CB, P, P, I64, I, P, I64, P, I64, P, P, P,
+                                        P, SZ, P]
     lib.mpq_token_logprobs_workspace_bytes.argtypes = [I, I64, I64, I]
     lib.mpq_token_logprobs_workspace_bytes.restype = SZ
     lib.mpq_token_logprobs.argtypes = [P, I, I64, I64, I64, P, I, P, P, P, P, P, P, SZ, P]
@@ -697,7 +709,7 @@ def frontend(X, W, r=None, signs=None):
     return W, s, V
 
 
-# ---------------------------------------------------------------- scoring and tuning a quantized model
+# ---------------------------------------------------------------- the quantized layer's product, scoring and tuning
 
 def _dtype_code(t, name):
     import torch
@@ -729,13 +741,126 @@ def _on(t, name, dev):
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
 
 
-def _scratch(workspace, nb, dev, what):
+def _scratch(workspace, nb, dev):
     import torch
     if workspace is None:
         return torch.empty(nb, dtype=torch.uint8, device=dev)
     _dev(workspace, torch.uint8, "workspace")
     _on(workspace, "workspace", dev)
     return workspace
+
+
+ACTIVATIONS = {None: 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}   # MPQ_ACT_*
+
+
+class PackedLayer:
+    """A solved layer ready for `linear`: its packed codes, its codebook and its
+    affine (the given tensors themselves: tuned in place, they are used as tuned)."""
+
+    def __init__(self, codes, cb, row_scale, row_offset=None, group=None):
+        import torch
+        _dev(codes, torch.int32, "codes")
+        if codes.dim() != 2:
+            raise ValueError(f"codes has shape {tuple(codes.shape)}, expected 2 dimensions")
+        dev = codes.device
+        lib = load_library()
+        with torch.cuda.device(dev):
+            self.codebook = prepare_codebook(cb, dev)
+            _on(self.codebook.tables, "the codebook", dev)
+            self.m, self.n = codes.shape[0], codes.shape[1] * self.codebook.d
+            self.group = int(group) if group else 0
+            if self.group < 0 or self.group and self.codebook.d != 1:
+                raise MPQError(-3 if self.group < 0 else -4, "pack_layer")
+            self.scale, self.offset = row_scale, row_offset
+            _affine(row_scale, row_offset if row_offset is not None else row_scale, self.m, self.n, self.group)
+            _on(row_scale, "row_scale", dev)
+            if row_offset is not None:
+                _on(row_offset, "row_offset", dev)
+            self.packed = torch.empty(lib.mpq_pack_bytes(self.m, self.n, self.codebook.K, self.codebook.d),
+                                      dtype=torch.uint8, device=dev)
+            _check(lib.mpq_pack(_ptr(codes), self.m, self.n, self.codebook.ref(), _ptr(self.packed),
+                                self.packed.numel(), _stream()), "mpq_pack")
+
+
+def pack_layer(codes, cb, row_scale, row_offset=None, group=None) -> PackedLayer:
+    """Pack a solved layer's codes (quantize_layer's, m x n/d int32) once for
+    `linear` (mpq_pack).  `row_scale`, `row_offset` and `group` are the solve's;
+    row_offset None: zero."""
+    return PackedLayer(codes, cb, row_scale, row_offset, group)
+
+
+def _activation(name):
+    if name not in ACTIVATIONS:
+        raise ValueError(f"unknown activation {name!r}; one of {list(ACTIVATIONS)}")
+    return ACTIVATIONS[name]
+
+
+def linear(x, layer, bias=None, activation=None, residual=None, return_pre=False, out=None, workspace=None):
+    """act(x W^T + bias) + residual of a packed layer (mpq_linear).
+
+    `x`: t x n, bfloat16, float16 or float32, contiguous rows; `bias`: m
+    float32; `activation`: None, "relu", "gelu", "gelu_tanh" or "silu";
+    `residual`: t x m of x's type; `out`: t x m to write (it may be the
+    residual).  Returns y, or (y, pre) with the activation's argument, which
+    linear_backward takes.
+    """
+    import torch
+    code = _dtype_code(x, "x")
+    ldx = _rows(x, "x")
+    t, n = x.shape
+    m, cb, dev = layer.m, layer.codebook, x.device
+    if n != layer.n:
+        raise ValueError(f"x has {n} columns, the layer {layer.n}")
+    _on(layer.packed, "the layer", dev)
+    act = _activation(activation)
+    if bias is not None:
+        _dev(bias, torch.float32, "bias", (m,))
+        _on(bias, "bias", dev)
+    ldr = _rows(residual, "residual", x, (t, m)) if residual is not None else m
+    lib = load_library()
+    with torch.cuda.device(dev):
+        y = torch.empty((t, m), dtype=x.dtype, device=dev) if out is None else out
+        ldy = _rows(y, "out", x, (t, m)) if out is not None else max(m, 1)
+        pre = torch.empty((t, m), dtype=x.dtype, device=dev) if return_pre else None
+        ws = _scratch(workspace, lib.mpq_linear_workspace_bytes(code, t, m, n, cb.K, cb.d, layer.group), dev)
+        rc = lib.mpq_linear(_ptr(x), code, t, ldx, _ptr(layer.packed), m, n, cb.ref(), _ptr(layer.scale),
+                            _ptr(layer.offset), layer.group, _ptr(bias), act, _ptr(residual), ldr, _ptr(y), ldy,
+                            _ptr(pre), m, _ptr(ws), ws.numel(), _stream())
+    _check(rc, "mpq_linear")
+    return (y, pre) if return_pre else y
+
+
+def linear_backward(dy, x, layer, pre=None, activation=None, need_dx=True, need_dlayer=True, workspace=None):
+    """Gradients of `linear` with the codes fixed (mpq_linear_backward):
+    dict(dx, dscale, doffset, dbias), the last three float32 in the shapes of
+    the layer's affine and (m,).  `dy`: t x m of x's type; `pre`: linear's,
+    with an activation.  The residual's gradient is dy itself."""
+    import torch
+    code = _dtype_code(x, "x")
+    ldx = _rows(x, "x")
+    t, n = x.shape
+    m, cb, dev = layer.m, layer.codebook, x.device
+    if n != layer.n:
+        raise ValueError(f"x has {n} columns, the layer {layer.n}")
+    _on(layer.packed, "the layer", dev)
+    act = _activation(activation)
+    lddy = _rows(dy, "dy", x, (t, m))
+    if act and pre is None:
+        raise ValueError("pre (linear's second result) is needed with an activation")
+    ldp = _rows(pre, "pre", x, (t, m)) if act else m
+    lib = load_library()
+    with torch.cuda.device(dev):
+        dx = torch.empty((t, n), dtype=x.dtype, device=dev) if need_dx else None
+        dscale = torch.empty_like(layer.scale) if need_dlayer else None
+        doffset = torch.empty_like(layer.scale) if need_dlayer else None
+        dbias = torch.empty(m, dtype=torch.float32, device=dev) if need_dlayer else None
+        ws = _scratch(workspace, lib.mpq_linear_backward_workspace_bytes(code, t, m, n, cb.K, cb.d, layer.group), dev)
+        rc = lib.mpq_linear_backward(_ptr(dy), lddy, _ptr(x), code, t, ldx, _ptr(layer.packed), m, n, cb.ref(),
+                                     _ptr(layer.scale), _ptr(layer.offset), layer.group, act,
+                                     _ptr(pre) if act else None, ldp, _ptr(dx), n, _ptr(dscale), _ptr(doffset),
+                                     _ptr(dbias), _ptr(ws), ws.numel(), _stream())
+    _check(rc, "mpq_linear_backward")
+    return dict(dx=dx, dscale=dscale, doffset=doffset, dbias=dbias)
 
 
 def token_logprobs(logits, tokens=None, top=0, workspace=None):
@@ -761,7 +886,7 @@ def token_logprobs(logits, tokens=None, top=0, workspace=None):
         lse, entropy, logprob = stats.unbind(0)
         ids = torch.empty((t, top), dtype=torch.int32, device=dev) if top > 0 else None
         lps = torch.empty((t, top), dtype=torch.float32, device=dev) if top > 0 else None
-        ws = _scratch(workspace, lib.mpq_token_logprobs_workspace_bytes(code, t, V, top), dev, "mpq_token_logprobs")
+        ws = _scratch(workspace, lib.mpq_token_logprobs_workspace_bytes(code, t, V, top), dev)
         rc = lib.mpq_token_logprobs(_ptr(logits), code, t, V, ld, _ptr(tokens), top,
                                     _ptr(logprob) if tokens is not None else None, _ptr(entropy), _ptr(lse), _ptr(ids),
                                     _ptr(lps), _ptr(ws), ws.numel(), _stream())
@@ -808,7 +933,7 @@ def distill(logits, teacher_ids, teacher, temperature=1.0, tail=False, weights=N
         else:
             grad = None
         loss = torch.empty(t, dtype=torch.float32, device=dev)
-        ws = _scratch(workspace, lib.mpq_distill_workspace_bytes(code, t, V, k), dev, "mpq_distill")
+        ws = _scratch(workspace, lib.mpq_distill_workspace_bytes(code, t, V, k), dev)
         rc = lib.mpq_distill(_ptr(logits), code, t, V, ld, _ptr(teacher_ids), _ptr(teacher), k, float(temperature),
                              1 if tail else 0, _ptr(weights), _ptr(loss), _ptr(grad), ldg, _ptr(ws), ws.numel(),
                              _stream())

@@ -17,6 +17,7 @@
 #include "../../include/mpq.h"
 #include "internal.h"
 #include "e8dp.h"
+#include "qlayer.h"
 
 namespace mpq {
 // launchers and host helpers defined in the kernel files
@@ -236,7 +237,7 @@ Layout make_layout(int64_t m, int64_t n, int64_t r, int64_t K, int64_t d, bool g
 // the first is a bound on the codeword norms), float32
 // codewords (Kpad x 8), QK and PV operand fragments, sorted E8 keys + indices.
 struct TableLayout {
-  size_t levels, e32, qk, pv, e8k, total;
+  size_t levels, e32, qk, pv, e8k, pkl, pkm, total;
 };
 TableLayout table_layout(int64_t K, int64_t d) {
   TableLayout T;
@@ -252,6 +253,10 @@ TableLayout table_layout(int64_t K, int64_t d) {
   o += d == 8 ? round_up((size_t)Kp * 8 * sizeof(uint32_t)) : 0;
   T.e8k = o;
   o += d == 8 ? round_up((size_t)2 * K * sizeof(uint32_t)) : 0;
+  T.pkl = o;
+  o += d == 8 ? round_up((size_t)K * sizeof(uint32_t)) : 0;
+  T.pkm = o;
+  o += d == 8 ? round_up((size_t)K * sizeof(uint16_t)) : 0;
   T.total = o;
   return T;
 }
@@ -261,6 +266,9 @@ bool bf16_exact(float x) {
   memcpy(&u, &x, 4);
   return std::isfinite(x) && (u & 0xffffu) == 0;
 }
+
+// Exact in both 16-bit types.
+bool narrow_exact(float x) { return bf16_exact(x) && (float)(_Float16)x == x; }
 
 uint16_t bf16_bits(float x) {  // exact values only
   uint32_t u;
@@ -378,6 +386,31 @@ int check_prepared(const mpq_codebook* cb) {
   if (cb->d == 8 && (cb->K < 1 || cb->K > 65536)) return MPQ_ESHAPE;
   return MPQ_OK;
 }
+
+void fill_tables(const mpq_codebook* cb, CbTables& t) {
+  const TableLayout T = table_layout(cb->K, cb->d);
+  const char* tb = static_cast<const char*>(cb->tables);
+  t.K = (int)cb->K;
+  t.d = (int)cb->d;
+  t.Kpad = padded_k(cb->K, cb->d);
+  t.levels = reinterpret_cast<const float*>(tb + T.levels);
+  t.e32 = reinterpret_cast<const float*>(tb + T.e32);
+  t.qk_keys = reinterpret_cast<const uint32_t*>(tb + T.qk);
+  t.pv_ops = reinterpret_cast<const uint32_t*>(tb + T.pv);
+  t.e8keys = reinterpret_cast<const uint32_t*>(tb + T.e8k);
+  t.pk_lut = reinterpret_cast<const uint32_t*>(tb + T.pkl);
+  t.pk_map = reinterpret_cast<const uint16_t*>(tb + T.pkm);
+}
+
+}  // namespace
+namespace mpq {
+int prepared_tables(const mpq_codebook* cb, CbTables& T) {
+  const int rc = check_prepared(cb);
+  if (rc == MPQ_OK) fill_tables(cb, T);
+  return rc;
+}
+}  // namespace mpq
+namespace {
 
 // ------------------------------------------------------------ context
 
@@ -1033,17 +1066,7 @@ int begin(Ctx& c, int64_t m, int64_t n, int64_t r, const mpq_codebook* cb, void*
   c.e8_decode = !(opt && (opt->flags & MPQ_F_NO_E8_DECODE));
   c.digits = digits_fit(n, r) && !(opt && (opt->flags & MPQ_F_LINEAR_F64));
   if ((rc = digit_count(opt, c.dg_s))) return rc;
-  // codebook tables
-  const TableLayout T = table_layout(cb->K, cb->d);
-  const char* tb = static_cast<const char*>(cb->tables);
-  c.cb.K = (int)cb->K;
-  c.cb.d = (int)cb->d;
-  c.cb.Kpad = padded_k(cb->K, cb->d);
-  c.cb.levels = reinterpret_cast<const float*>(tb + T.levels);
-  c.cb.e32 = reinterpret_cast<const float*>(tb + T.e32);
-  c.cb.qk_keys = reinterpret_cast<const uint32_t*>(tb + T.qk);
-  c.cb.pv_ops = reinterpret_cast<const uint32_t*>(tb + T.pv);
-  c.cb.e8keys = reinterpret_cast<const uint32_t*>(tb + T.e8k);
+  fill_tables(cb, c.cb);
   c.e8dp = cb->d == 8 && cb->kind == MPQ_CB_E8_PREFIX && !(opt && (opt->flags & MPQ_F_NO_E8DP));
   c.e8p.qlast = cb->e8_qlast;
   for (int j = 0; j < 8; ++j) c.e8p.L2[j] = cb->e8_last2[j];
@@ -1163,7 +1186,11 @@ int mpq_codebook_prepare(const float* cb, int64_t K, int64_t d, void* tables, si
     std::vector<float> lv(64, 0.f);
     std::vector<float> e32;
     std::vector<uint16_t> qk, pv;
-    std::vector<uint32_t> e8k;
+    std::vector<uint32_t> e8k, pkl;
+    std::vector<uint16_t> pkm;
+    h.narrow = 1;
+    for (int64_t k = 0; k < K * d; ++k)
+      if (!narrow_exact(d == 1 ? cb[k] - cb[K / 2] : cb[k])) h.narrow = 0;
     if (d == 1) {
       for (int64_t k = 0; k < K; ++k) lv[k] = cb[k];
       MPQ_TRY(hipMemcpyAsync(tb + T.levels, lv.data(), 64 * sizeof(float), hipMemcpyHostToDevice, st));
@@ -1190,6 +1217,15 @@ int mpq_codebook_prepare(const float* cb, int64_t K, int64_t d, void* tables, si
         e8k.resize((size_t)2 * K);
         e8_key_table(cb, K, e8k.data(), reinterpret_cast<int32_t*>(e8k.data() + K));
         MPQ_TRY(hipMemcpyAsync(tb + T.e8k, e8k.data(), e8k.size() * sizeof(uint32_t), hipMemcpyHostToDevice, st));
+        pkl.assign((size_t)K, 0u);
+        pkm.assign((size_t)K, 0);
+        int entries = 0, pairs = 0;
+        if (q_e8_tables(cb, K, pkl.data(), pkm.data(), &entries, &pairs)) {
+          MPQ_TRY(hipMemcpyAsync(tb + T.pkl, pkl.data(), pkl.size() * sizeof(uint32_t), hipMemcpyHostToDevice, st));
+          MPQ_TRY(hipMemcpyAsync(tb + T.pkm, pkm.data(), pkm.size() * sizeof(uint16_t), hipMemcpyHostToDevice, st));
+        } else {
+          h.narrow = 0;
+        }
       }
     }
     // the host staging vectors end with this call

@@ -4,6 +4,8 @@
 #include <stdint.h>
 #include <stddef.h>
 
+#include "../../include/mpq.h"
+
 namespace mpq {
 
 // ---------------------------------------------------------------- GEMM ----
@@ -114,6 +116,8 @@ struct CbTables {
   const uint32_t* pv_ops;   // d = 8: PV operand fragments, Kpad/32 steps x 64 lanes x 4 words
   const float* e32;         // d = 8: base codewords as float32, Kpad x 8
   const uint32_t* e8keys;   // d = 8, E8-prefix codebooks: sorted lexicographic keys (K), then their indices (K)
+  const uint32_t* pk_lut;   // d = 8, E8-prefix codebooks: packed layers' decoder table (qlayer.h)
+  const uint16_t* pk_map;   // and the codes' places in it
   // Per-row affine layout: column j of row i uses a[i * G + j / gs],
   // o[i * G + j / gs] (one affine per row: gs = n, G = 1; column groups of
   // gs weights only with d = 1).
@@ -284,6 +288,9 @@ hipError_t launch_token_logprobs(const LogitArgs& A, const int32_t* tokens, floa
                                  float* lse, int32_t* top_ids, float* top_lp, void* ws, hipStream_t st);
 hipError_t launch_distill(const LogitArgs& A, const float* teacher, double invT, bool tail, float* loss, void* grad,
                           int64_t ldg, void* ws, hipStream_t st);
+
+// The device tables of a prepared codebook, checked (api.hip).
+int prepared_tables(const mpq_codebook* cb, CbTables& T);
 
 // Notes a HIP error for mpq_hip_error_name and returns its status code.
 int hip_status(hipError_t e);

@@ -1,0 +1,210 @@
+// 16-bit matrix products with a fused epilogue, for a solved layer's product
+// with many rows and for its gradients (qlayer.h, QGemm).
+//
+// Workgroup tile BM x BN of the output, K in steps of 64 through two LDS stages
+// filled by direct global -> LDS loads (16 bytes a lane) while the matrix cores
+// work on the other.  A row's eight 16-byte pieces of a step are stored
+// permuted by the row's low three bits, so that the sixteen rows of an operand
+// read spread over the banks.  Operands of more than 16 bits enter as planes
+// whose sum they are: the products of plane pairs add up in the same float32
+// accumulators.
+#include <algorithm>
+#include "qlayer.h"
+
+namespace mpq {
+
+namespace {
+
+constexpr int BK = 64;
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+
+// This wave's share of one step's rows, straight into an LDS stage.
+template <int BM, int LOADS>
+__device__ __forceinline__ void fetch_step(const QGemm& g, int64_t i0, int64_t j0, int kt, int kts, int wave,
+                                           const uint32_t* off, uint16_t* stage) {
+  const int pr = kt / kts, k = kt - pr * kts;
+  const char* a = reinterpret_cast<const char*>(g.A + g.pa[pr] * g.planeA + i0 * g.lda) + (size_t)k * (BK * 2);
+  const char* b = reinterpret_cast<const char*>(g.B + g.pb[pr] * g.planeB + j0 * g.ldb) + (size_t)k * (BK * 2);
+#pragma unroll
+  for (int l = 0; l < LOADS; ++l) {
+    const int r = (wave * LOADS + l) * 8;
+    __builtin_amdgcn_global_load_lds((r < BM ? a : b) + off[l], (lds_ptr_t)(stage + r * BK), 16, 0, 0);
+  }
+}
+
+template <typename T, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN) void q_gemm_kernel(QGemm g, float* __restrict__ part, int splits) {
+  constexpr int WAVES = WM * WN;
+  constexpr int SM = BM / WM / 16, SN = BN / WN / 16;   // 16 x 16 subtiles of a wave
+  constexpr int LOADS = (BM + BN) / 8 / WAVES;          // 1 KB loads per wave and step
+  __shared__ __attribute__((aligned(1024))) uint16_t lds[2][(BM + BN) * BK];
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  const int wm = wave / WN, wn = wave % WN;
+  // tiles: contiguous runs per XCD (workgroups go to the 8 XCDs in turn), and
+  // within a run groups of 8 tile rows column by column
+  const int tm = (int)((g.M + BM - 1) / BM), tn = (int)((g.N + BN - 1) / BN);
+  const int T_ = tm * tn;
+  const int split = (int)(blockIdx.x / T_);
+  int tile = (int)(blockIdx.x % T_);
+  {
+    const int per = T_ / 8, rem = T_ % 8, x = tile % 8, q = tile / 8;
+    tile = x * per + min(x, rem) + q;
+  }
+  const int grp = tile / (8 * tn), first = grp * 8, gm = min(tm - first, 8);
+  const int in = tile - grp * 8 * tn;
+  const int64_t i0 = (int64_t)(first + in % gm) * BM, j0 = (int64_t)(in / gm) * BN;
+
+  const int kts = (int)(g.K / BK), all = kts * g.npairs;
+  const int kt0 = (int)((int64_t)all * split / splits), kt1 = (int)((int64_t)all * (split + 1) / splits);
+
+  // this lane's byte offsets within the tile's rows
+  const int piece = (lane & 7) ^ (lane >> 3);
+  uint32_t off[LOADS];
+#pragma unroll
+  for (int l = 0; l < LOADS; ++l) {
+    const int r = (wave * LOADS + l) * 8 + (lane >> 3);
+    const bool a = r < BM;
+    const int64_t lim = a ? g.M - 1 - i0 : g.N - 1 - j0;
+    const int64_t row = min((int64_t)(a ? r : r - BM), lim);   // rows past the end repeat the last
+    off[l] = (uint32_t)(row * (a ? g.lda : g.ldb) * 2 + piece * 16);
+  }
+  v4f acc[SM][SN];
+#pragma unroll
+  for (int i = 0; i < SM; ++i)
+#pragma unroll
+    for (int j = 0; j < SN; ++j) acc[i][j] = (v4f){0.f, 0.f, 0.f, 0.f};
+
+  if (kt0 < kt1) fetch_step<BM, LOADS>(g, i0, j0, kt0, kts, wave, off, lds[0]);
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+  const int r = lane & 15, kb = lane >> 4;
+  for (int kt = kt0; kt < kt1; ++kt) {
+    const int cur = (kt - kt0) & 1;
+    if (kt + 1 < kt1) fetch_step<BM, LOADS>(g, i0, j0, kt + 1, kts, wave, off, lds[cur ^ 1]);
+    const uint16_t* As = lds[cur] + (wm * SM * 16 + r) * BK;
+    const uint16_t* Bs = lds[cur] + (BM + wn * SN * 16 + r) * BK;
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      const int pc = ((kk * 4 + kb) ^ (r & 7)) * 8;
+      v4u a[SM], b[SN];
+#pragma unroll
+      for (int i = 0; i < SM; ++i) a[i] = *reinterpret_cast<const v4u*>(As + i * 16 * BK + pc);
+#pragma unroll
+      for (int j = 0; j < SN; ++j) b[j] = *reinterpret_cast<const v4u*>(Bs + j * 16 * BK + pc);
+#pragma unroll
+      for (int i = 0; i < SM; ++i)
+#pragma unroll
+        for (int j = 0; j < SN; ++j) acc[i][j] = T::mfma(a[i], b[j], acc[i][j]);
+    }
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+  }
+  // Epilogue: sixteen rows of the output at a time through this wave's part of
+  // LDS (every read of the stages is done), so that a row leaves as runs of
+  // SM * 16 columns and the finishing code stands once, not per accumulator.
+  constexpr int PITCH = SM * 16 + 4, QUADS = SM * 4;
+  static_assert(WAVES * 16 * PITCH * 4 <= (int)sizeof(lds), "the epilogue's rows fit the stages");
+  float* reg = reinterpret_cast<float*>(lds[0]) + wave * 16 * PITCH;
+#pragma unroll
+  for (int j = 0; j < SN; ++j) {
+#pragma unroll
+    for (int i = 0; i < SM; ++i) *reinterpret_cast<v4f*>(reg + r * PITCH + i * 16 + 4 * kb) = acc[i][j];
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll 1
+    for (int q = lane; q < 16 * QUADS; q += 64) {
+      const int row = q / QUADS, c = (q - row * QUADS) * 4;
+      const int64_t jj = j0 + (wn * SN + j) * 16 + row, ii = i0 + wm * SM * 16 + c;
+      const float4 x = *reinterpret_cast<const float4*>(reg + row * PITCH + c);
+      float v[4] = {x.x, x.y, x.z, x.w};
+      if (part) {
+        if (jj < g.N && ii < g.M)   // rows of part are padded to four columns
+          *reinterpret_cast<float4*>(part + ((size_t)split * g.N + jj) * ((g.M + 3) / 4 * 4) + ii) = x;
+      } else {
+        q_finish4(g.O, jj, ii, v, false);
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  }
+}
+
+// Adds the splits in order and finishes.
+__global__ __launch_bounds__(256) void q_split_finish_kernel(const float* __restrict__ part, int splits, int64_t N,
+                                                             int64_t Mp, QOut O) {
+  const int64_t quads = Mp / 4;
+  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (at >= N * quads) return;
+  const int64_t j = at / quads, i = (at - j * quads) * 4;
+  float v[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < splits; ++s) {
+    const float4 q = *reinterpret_cast<const float4*>(part + ((size_t)s * N + j) * Mp + i);
+    v[0] += q.x;
+    v[1] += q.y;
+    v[2] += q.z;
+    v[3] += q.w;
+  }
+  q_finish4(O, j, i, v, false);
+}
+
+struct Plan {
+  bool big;
+  int64_t tiles;
+  int splits;
+};
+Plan plan(int64_t M, int64_t N, int64_t K, int npairs) {
+  Plan p;
+  const int64_t big = ((M + 255) / 256) * ((N + 255) / 256);
+  p.big = big >= 192;
+  p.tiles = p.big ? big : ((M + 127) / 128) * ((N + 127) / 128);
+  const int64_t kts = K / BK * npairs;
+  p.splits = 1;
+  // two workgroups of the small tile fit a CU; a split keeps at least 8 steps
+  if (!p.big && p.tiles < 256) p.splits = (int)std::max<int64_t>(1, std::min({512 / p.tiles, kts / 8, (int64_t)16}));
+  return p;
+}
+
+}  // namespace
+
+void q_pairs(QGemm& g, int PA, int PB) {
+  g.npairs = 0;
+  for (int s = 0; s <= 2; ++s)
+    for (int p = 0; p <= s; ++p)
+      if (p < PA && s - p < PB) {
+        g.pa[g.npairs] = (uint8_t)p;
+        g.pb[g.npairs++] = (uint8_t)(s - p);
+      }
+}
+
+size_t q_gemm_workspace(int64_t M, int64_t N, int64_t K, int npairs) {
+  if (M <= 0 || N <= 0) return 0;
+  const Plan p = plan(M, N, K, npairs);
+  return p.splits > 1 ? (size_t)p.splits * N * ((M + 3) / 4 * 4) * sizeof(float) : 0;
+}
+
+template <typename T>
+static hipError_t run(const QGemm& g, float* part, hipStream_t st) {
+  const Plan p = plan(g.M, g.N, g.K, g.npairs);
+  float* out = p.splits > 1 ? part : nullptr;
+  const dim3 grid((unsigned)(p.tiles * p.splits));
+  if (p.big)
+    hipLaunchKernelGGL((q_gemm_kernel<T, 256, 256, 2, 4>), grid, dim3(512), 0, st, g, out, p.splits);
+  else
+    hipLaunchKernelGGL((q_gemm_kernel<T, 128, 128, 2, 2>), grid, dim3(256), 0, st, g, out, p.splits);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.splits == 1) return e;
+  const int64_t Mp = (g.M + 3) / 4 * 4;
+  hipLaunchKernelGGL(q_split_finish_kernel, dim3((unsigned)((g.N * (Mp / 4) + 255) / 256)), dim3(256), 0, st, part,
+                     p.splits, g.N, Mp, g.O);
+  return hipGetLastError();
+}
+
+hipError_t launch_q_gemm(const QGemm& g, float* part, hipStream_t st) {
+  if (g.M <= 0 || g.N <= 0) return hipSuccess;
+  if (g.K % BK != 0 || g.K <= 0) return hipErrorInvalidValue;
+  return g.half ? run<OpF16>(g, part, st) : run<OpBf16>(g, part, st);
+}
+
+}  // namespace mpq

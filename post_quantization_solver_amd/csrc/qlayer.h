@@ -1,0 +1,342 @@
+// Packed codes of a solved layer and what the kernels that read them share.
+//
+// A layer's m x n weights are W[i][j] = a e + o with base entries e of a
+// codebook.  Codes are packed in tiles of 16 rows: chunk c of a tile holds
+// QFmt::STEPS * 32 columns as 64 lanes x 16 bytes, lane l holding row l % 16,
+// columns ((l / 16) * STEPS + s) * 8 .. + 7 of the chunk for s = 0 .. STEPS - 1.
+// One wave load is 1 KB of contiguous memory, and what lane l decodes for step
+// s is its A operand of v_mfma_f32_16x16x32 as it stands: row l % 16, eight
+// consecutive k (the order of the k among the lanes' quarters is free as long
+// as the B operand uses the same).
+//
+// d = 1: entries are taken about the middle level, e - levels[K / 2], so that
+// the sums over a grid 0 .. K - 1 do not carry a large common part that the
+// offset takes off again; o' = o + a levels[K / 2].
+#pragma once
+#include "mpq_device.h"
+#include "internal.h"
+
+namespace mpq {
+
+enum QFormat : int {
+  QF_NIB = 0,    // d = 1, K <= 16: 4 bits a weight
+  QF_BYTE = 1,   // d = 1, K <= 64: 8 bits a weight
+  QF_E8 = 2,     // the first K points of E8: 16 bits per 8 weights, re-indexed (see q_e8_tables)
+  QF_VEC = 3,    // other d = 8 codebooks: the codes, 16 bits per 8 weights
+};
+__host__ __device__ constexpr int q_steps(int f) { return f == QF_NIB ? 4 : f == QF_BYTE ? 2 : 8; }
+__host__ __device__ constexpr int q_chunk(int f) { return q_steps(f) * 32; }
+
+// Dwords of the decoder's LDS table.
+inline int q_lut_words(int f, int entries) { return f == QF_NIB ? 256 : f == QF_BYTE ? 4096 : f == QF_E8 ? entries : 0; }
+
+struct QLayer {
+  int fmt;
+  int64_t m, n;
+  int tiles, chunks;
+  const uint4* packed;
+  const float* scale;    // m x G
+  const float* offset;   // m x G, or nullptr: zero
+  int64_t group; int G;  // columns per affine group (n: one per row)
+  const float* levels;   // d = 1
+  int K;
+  const uint32_t* lut;   // QF_E8: sign-magnitude nibbles of 2 e, nibble {0,2,4,6,1,3,5,7}[q] = coordinate q
+  const uint16_t* map;   // QF_E8: code -> packed code
+  int lut_entries, pairs;
+  const float* e32;      // d = 8: K x 8
+  bool has_offset() const { return offset != nullptr || fmt == QF_NIB || fmt == QF_BYTE; }
+};
+
+#ifdef __HIPCC__
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+typedef _Float16 v2h __attribute__((ext_vector_type(2)));
+
+// The matrix cores' 16-bit operand types.
+struct OpBf16 {
+  static constexpr bool HALF = false;
+  __device__ static v4f mfma(v4u a, v4u b, v4f c) { return mfma_bf16_16x16x32(a, b, c); }
+  __device__ static uint32_t bits(float x) { return f2bf_bits(x); }
+  __device__ static float val(uint32_t b) { return bf_bits2f(b & 0xffffu); }
+  __device__ static uint32_t pack(float x, float y) { return f2bf_pack(x, y); }
+  static constexpr uint32_t ONES = 0x3f803f80u;
+};
+struct OpF16 {
+  static constexpr bool HALF = true;
+  __device__ static v4f mfma(v4u a, v4u b, v4f c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b), c, 0, 0, 0);
+  }
+  __device__ static uint32_t bits(float x) { return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)x); }
+  __device__ static float val(uint32_t b) { return (float)__builtin_bit_cast(_Float16, (uint16_t)b); }
+  __device__ static uint32_t pack(float x, float y) {
+    v2h v = {(_Float16)x, (_Float16)y};
+    return __builtin_bit_cast(uint32_t, v);
+  }
+  static constexpr uint32_t ONES = 0x3c003c00u;
+};
+
+__device__ __forceinline__ float q_centre(const QLayer& L) {
+  return L.fmt == QF_NIB || L.fmt == QF_BYTE ? L.levels[L.K / 2] : 0.f;
+}
+
+// Fills the decoder's LDS table (every thread of the workgroup; the caller synchronizes).
+template <int FMT, typename T>
+__device__ __forceinline__ void q_lut_fill(const QLayer& L, uint32_t* lut, int nthreads) {
+  const int t = threadIdx.x;
+  if constexpr (FMT == QF_E8) {
+    const int quads = (L.lut_entries + 3) / 4;   // the table is padded to 16 bytes
+    for (int i = t; i < quads; i += nthreads)
+      reinterpret_cast<uint4*>(lut)[i] = reinterpret_cast<const uint4*>(L.lut)[i];
+  } else if constexpr (FMT == QF_NIB || FMT == QF_BYTE) {
+    constexpr int BITS = FMT == QF_NIB ? 4 : 6;
+    const float mid = q_centre(L);
+    for (int i = t; i < 1 << (2 * BITS); i += nthreads) {
+      const int lo = i & ((1 << BITS) - 1), hi = i >> BITS;
+      lut[i] = T::pack(L.levels[lo < L.K ? lo : 0] - mid, L.levels[hi < L.K ? hi : 0] - mid);
+    }
+  }
+}
+
+// The eight entries of step s from a lane's 16 bytes of codes.
+template <int FMT, typename T>
+__device__ __forceinline__ v4u q_decode(const QLayer& L, const uint32_t* lut, const uint4& c, int s) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+  v4u r;
+  if constexpr (FMT == QF_NIB) {
+#pragma unroll
+    for (int b = 0; b < 4; ++b) r[b] = lut[(w[s] >> (8 * b)) & 255u];
+  } else if constexpr (FMT == QF_BYTE) {
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const uint32_t h = w[2 * s + (b >> 1)] >> (16 * (b & 1));
+      r[b] = lut[(h & 63u) | ((h >> 2) & 0xfc0u)];
+    }
+  } else if constexpr (FMT == QF_E8) {
+    // Packed code: 2 i + sign for the i-th of `pairs` points whose negative is
+    // in the codebook too, pairs + i for entry i beyond them; either way the
+    // entry is max(code / 2, code - pairs), and an odd code flips its signs
+    // (a lone entry with an odd code is stored flipped).
+    const uint32_t code = (w[s >> 1] >> (16 * (s & 1))) & 0xffffu;
+    const int e = max((int)(code >> 1), (int)code - L.pairs);
+    const uint32_t v = lut[e] ^ ((uint32_t)((int)(code << 31) >> 31) & 0x88888888u);
+    const uint32_t s0 = v & 0x07070707u, s1 = (v >> 4) & 0x07070707u;
+    const uint32_t g0 = (v << 4) & 0x80808080u, g1 = v & 0x80808080u;
+    // bytes of the 16-bit values of 0, 1/2, .., 7/2
+    uint32_t h0, h1, l0 = 0, l1 = 0;
+    if constexpr (T::HALF) {
+      h0 = __builtin_amdgcn_perm(0x43424140u, 0x3e3c3800u, s0);
+      h1 = __builtin_amdgcn_perm(0x43424140u, 0x3e3c3800u, s1);
+    } else {
+      h0 = __builtin_amdgcn_perm(0x40404040u, 0x3f3f3f00u, s0);
+      h1 = __builtin_amdgcn_perm(0x40404040u, 0x3f3f3f00u, s1);
+      l0 = __builtin_amdgcn_perm(0x60402000u, 0xc0800000u, s0);
+      l1 = __builtin_amdgcn_perm(0x60402000u, 0xc0800000u, s1);
+    }
+    h0 |= g0;
+    h1 |= g1;
+    r[0] = __builtin_amdgcn_perm(h0, l0, 0x05010400u);
+    r[1] = __builtin_amdgcn_perm(h0, l0, 0x07030602u);
+    r[2] = __builtin_amdgcn_perm(h1, l1, 0x05010400u);
+    r[3] = __builtin_amdgcn_perm(h1, l1, 0x07030602u);
+  } else {
+    const uint32_t code = (w[s >> 1] >> (16 * (s & 1))) & 0xffffu;
+    const float4* e = reinterpret_cast<const float4*>(L.e32 + (size_t)code * 8);
+    const float4 a = e[0], b = e[1];
+    r[0] = T::pack(a.x, a.y);
+    r[1] = T::pack(a.z, a.w);
+    r[2] = T::pack(b.x, b.y);
+    r[3] = T::pack(b.z, b.w);
+  }
+  return r;
+}
+
+// ------------------------------------------------------------------ epilogue
+
+enum QAct : int { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2, ACT_GELU_TANH = 3, ACT_SILU = 4 };
+
+__device__ __forceinline__ float act_fwd(int act, float u) {
+  switch (act) {
+    case ACT_RELU: return u < 0.f ? 0.f : u;   // keeps NaN
+    case ACT_GELU: return 0.5f * u * (1.f + erff(u * 0.70710678f));
+    case ACT_GELU_TANH: return 0.5f * u * (1.f + tanhf(0.79788456f * (u + 0.044715f * u * u * u)));
+    case ACT_SILU: return u / (1.f + expf(-u));
+  }
+  return u;
+}
+__device__ __forceinline__ float act_slope(int act, float u) {
+  switch (act) {
+    case ACT_RELU: return u > 0.f ? 1.f : u == u ? 0.f : u;
+    case ACT_GELU: return 0.5f * (1.f + erff(u * 0.70710678f)) + u * 0.39894228f * expf(-0.5f * u * u);
+    case ACT_GELU_TANH: {
+      const float th = tanhf(0.79788456f * (u + 0.044715f * u * u * u));
+      // 1 - th^2 is 0 where u^3 overflows; the product must not be inf * 0
+      const float q = 1.f - th * th;
+      return 0.5f * (1.f + th) + (q == 0.f ? 0.f : 0.5f * u * q * 0.79788456f * (1.f + 0.134145f * u * u));
+    }
+    case ACT_SILU: {
+      const float q = 1.f / (1.f + expf(-u));
+      return q == 0.f ? 0.f : q * (1.f + u * (1.f - q));
+    }
+  }
+  return 1.f;
+}
+
+__device__ __forceinline__ float load_as_f32(const void* p, int64_t i, int dtype) {
+  if (dtype == DT_F32) return static_cast<const float*>(p)[i];
+  const uint32_t b = static_cast<const uint16_t*>(p)[i];
+  return dtype == DT_BF16 ? OpBf16::val(b) : OpF16::val(b);
+}
+
+// Four consecutive elements at p[i], as many as `live`; vec: 4-element aligned.
+__device__ __forceinline__ void load4(const void* p, int64_t i, int dtype, bool vec, int live, float* v) {
+  if (vec && live >= 4) {
+    if (dtype == DT_F32) {
+      const float4 q = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+      v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+    } else {
+      const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
+      const uint32_t h[4] = {q.x & 0xffffu, q.x >> 16, q.y & 0xffffu, q.y >> 16};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = dtype == DT_BF16 ? OpBf16::val(h[k]) : OpF16::val(h[k]);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = k < live ? load_as_f32(p, i + k, dtype) : 0.f;
+  }
+}
+__device__ __forceinline__ void store4(void* p, int64_t i, int dtype, bool vec, int live, const float* v) {
+  if (vec && live >= 4) {
+    if (dtype == DT_F32) {
+      *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(v[0], v[1], v[2], v[3]);
+    } else if (dtype == DT_BF16) {
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) =
+          make_uint2(OpBf16::pack(v[0], v[1]), OpBf16::pack(v[2], v[3]));
+    } else {
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) =
+          make_uint2(OpF16::pack(v[0], v[1]), OpF16::pack(v[2], v[3]));
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k >= live) break;
+      if (dtype == DT_F32)
+        static_cast<float*>(p)[i + k] = v[k];
+      else
+        static_cast<uint16_t*>(p)[i + k] = (uint16_t)(dtype == DT_BF16 ? OpBf16::bits(v[k]) : OpF16::bits(v[k]));
+    }
+  }
+}
+#endif  // __HIPCC__
+
+// The outputs of a product, out[j][i] for row j and column i: four consecutive
+// columns at a time.
+struct QOut {
+  void* y; int64_t ldy;
+  void* pre; int64_t ldpre;         // the activation's argument (nullptr: not kept)
+  const void* res; int64_t ldres;   // added after the activation
+  const float* bias;                // per column
+  const float* colscale;            // per column: factor of the product (nullptr: 1)
+  const float* coloff;              // per column: factor of rowadd (nullptr: see mid)
+  const float* rowadd;              // per row
+  const float* levels; int mid;     // d = 1: levels[mid] is added to coloff as colscale times it (mid < 0: nothing)
+  int act, dtype;
+  int vec;                          // 4-element alignment of y, pre, res
+  int64_t rows, cols;
+};
+
+#ifdef __HIPCC__
+// u = colscale v + (coloff + colscale mid) rowadd + bias; y = act(u) + res.
+__device__ __forceinline__ void q_finish4(const QOut& O, int64_t j, int64_t i, float* v, bool scaled) {
+  const int live = (int)min((int64_t)4, O.cols - i);
+  if (j >= O.rows || live <= 0) return;
+  if (!scaled) {
+    const float add = O.rowadd ? O.rowadd[j] : 0.f;
+    const float mid = O.mid >= 0 ? O.levels[O.mid] : 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k >= live) break;
+      const float a = O.colscale ? O.colscale[i + k] : 1.f;
+      float o = O.coloff ? O.coloff[i + k] : 0.f;
+      if (O.mid >= 0) o = fmaf(a, mid, o);
+      if (!O.colscale && !O.coloff) o = 1.f;   // rowadd alone
+      v[k] = a * v[k];
+      if (O.rowadd) v[k] = fmaf(o, add, v[k]);
+    }
+  }
+  if (O.bias)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] += k < live ? O.bias[i + k] : 0.f;
+  if (O.pre) store4(O.pre, j * O.ldpre + i, O.dtype, O.vec, live, v);
+  if (O.act != ACT_NONE)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = act_fwd(O.act, v[k]);
+  if (O.res) {
+    float r[4];
+    load4(O.res, j * O.ldres + i, O.dtype, O.vec, live, r);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] += r[k];
+  }
+  store4(O.y, j * O.ldy + i, O.dtype, O.vec, live, v);
+}
+#endif
+
+// ------------------------------------------------------------------ launchers
+
+// D[j][i] = sum over the plane pairs (p, q) and k of A_p[i][k] B_q[j][k] (16-bit
+// planes, K a multiple of 64, rows of lda / ldb elements, 16-byte aligned), then
+// O.  part (split K): splits x rows x cols float32, or nullptr.
+struct QGemm {
+  const uint16_t* A; int64_t lda, planeA;
+  const uint16_t* B; int64_t ldb, planeB;
+  int64_t M, N, K;        // columns i, rows j, depth of one plane
+  int npairs;
+  uint8_t pa[6], pb[6];
+  bool half;              // fp16 operands (else bfloat16)
+  QOut O;
+};
+// Pairs of PA and PB planes whose orders add to at most two.
+void q_pairs(QGemm& g, int PA, int PB);
+size_t q_gemm_workspace(int64_t M, int64_t N, int64_t K, int npairs);
+hipError_t launch_q_gemm(const QGemm& g, float* part, hipStream_t st);
+
+// The product with few rows (qskinny.hip): x as planes of 16-bit rows, kblocks blocks of
+// eight columns each.  Column groups need chunks that lie in one group.
+bool q_skinny_ok(const QLayer& L);
+hipError_t launch_q_skinny(const QLayer& L, const uint16_t* x, int64_t ldx, int64_t planex, int kblocks, int64_t t,
+                           int planes, bool half, const QOut& O, hipStream_t st);
+
+struct QLinearArgs {
+  QLayer L;
+  const void* x; int64_t ldx;
+  int dtype;
+  int64_t t;
+  const float* bias;
+  int act;
+  const void* res; int64_t ldres;
+  void* y; int64_t ldy;
+  void* pre; int64_t ldpre;
+};
+struct QLinearGrad {
+  QLayer L;
+  const void* dy; int64_t lddy;
+  const void* x; int64_t ldx;
+  const void* pre; int64_t ldpre;
+  int dtype, act;
+  int64_t t;
+  bool need_dx, need_dlayer;
+  void* dx; int64_t lddx;
+  float *dscale, *doffset, *dbias;
+};
+size_t q_packed_bytes(const QLayer& L);
+hipError_t launch_q_pack(const int32_t* codes, const QLayer& L, void* packed, hipStream_t st);
+size_t q_linear_workspace(const QLinearArgs& A);
+hipError_t launch_q_linear(const QLinearArgs& A, void* ws, hipStream_t st);
+size_t q_grad_workspace(const QLinearGrad& A);
+hipError_t launch_q_grad(const QLinearGrad& A, void* ws, hipStream_t st);
+
+// Host images of an E8 prefix's decoder table and code map (K each at most);
+// false if the codebook does not have the shells' structure.
+bool q_e8_tables(const float* cb, int64_t K, uint32_t* lut, uint16_t* map, int* entries, int* pairs);
+int64_t q_e8_shell(int h);
+int q_e8_pairs(int64_t K);   // table entries that stand for a point and its negative
+
+}  // namespace mpq
