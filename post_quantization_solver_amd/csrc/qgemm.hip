@@ -1,11 +1,12 @@
 // 16-bit matrix products with a fused epilogue, for a solved layer's product
 // with many rows and for its gradients (qlayer.h, QGemm).
 //
-// Workgroup tile BM x BN of the output, K in steps of 64 through two LDS stages
-// filled by direct global -> LDS loads (16 bytes a lane) while the matrix cores
-// work on the other.  A row's eight 16-byte pieces of a step are stored
-// permuted by the row's low three bits, so that the sixteen rows of an operand
-// read spread over the banks.  Operands of more than 16 bits enter as planes
+// Workgroup tile BM x BN of the output, K in steps of 32 through four LDS
+// stages filled by direct global -> LDS loads (16 bytes a lane), so that three
+// steps are on their way while the matrix cores work on a fourth out of
+// registers.  A row's four 16-byte pieces of a step are stored permuted by the
+// row's bits 1 and 2, so that the sixteen rows of an operand read spread over
+// the banks.  Operands of more than 16 bits enter as planes
 // whose sum they are: the products of plane pairs add up in the same float32
 // accumulators.
 #include <algorithm>
@@ -15,29 +16,73 @@ namespace mpq {
 
 namespace {
 
-constexpr int BK = 64;
+constexpr int BK = 32, STAGES = 4;
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
-// This wave's share of one step's rows, straight into an LDS stage.
+// Waits until at most N of this wave's global -> LDS loads are on their way,
+// and for its LDS reads; then for the workgroup.
+template <int N>
+__device__ __forceinline__ void wait_stage() {
+  static_assert(N < 64, "the counter has six bits");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// Where the next step's rows are.
+struct Cursor {
+  const char *a, *b;
+  int pair, k;
+};
+__device__ __forceinline__ void seek(Cursor& c, const QGemm& g, int64_t i0, int64_t j0, int pair, int k) {
+  c.pair = pair;
+  c.k = k;
+  if (pair >= g.npairs) return;
+  c.a = reinterpret_cast<const char*>(g.A + g.pa[pair] * g.planeA + i0 * g.lda) + (size_t)k * (BK * 2);
+  c.b = reinterpret_cast<const char*>(g.B + g.pb[pair] * g.planeB + j0 * g.ldb) + (size_t)k * (BK * 2);
+}
+
+// This wave's share of the next step's rows, straight into an LDS stage.
 template <int BM, int LOADS>
-__device__ __forceinline__ void fetch_step(const QGemm& g, int64_t i0, int64_t j0, int kt, int kts, int wave,
+__device__ __forceinline__ void fetch_step(Cursor& c, const QGemm& g, int64_t i0, int64_t j0, int kts, int wave,
                                            const uint32_t* off, uint16_t* stage) {
-  const int pr = kt / kts, k = kt - pr * kts;
-  const char* a = reinterpret_cast<const char*>(g.A + g.pa[pr] * g.planeA + i0 * g.lda) + (size_t)k * (BK * 2);
-  const char* b = reinterpret_cast<const char*>(g.B + g.pb[pr] * g.planeB + j0 * g.ldb) + (size_t)k * (BK * 2);
 #pragma unroll
   for (int l = 0; l < LOADS; ++l) {
-    const int r = (wave * LOADS + l) * 8;
-    __builtin_amdgcn_global_load_lds((r < BM ? a : b) + off[l], (lds_ptr_t)(stage + r * BK), 16, 0, 0);
+    const int r = (wave * LOADS + l) * 16;
+    __builtin_amdgcn_global_load_lds((r < BM ? c.a : c.b) + off[l], (lds_ptr_t)(stage + r * BK), 16, 0, 0);
   }
+  c.a += BK * 2;
+  c.b += BK * 2;
+  if (++c.k == kts) seek(c, g, i0, j0, c.pair + 1, 0);
+}
+
+// One wave's operands of a step.
+template <int SM, int SN>
+struct Frags {
+  v4u a[SM], b[SN];
+};
+template <int BM, int SM, int SN>
+__device__ __forceinline__ void read_step(const uint16_t* stage, int wm, int wn, int r, int kb, Frags<SM, SN>& f) {
+  const int pc = (kb ^ ((r >> 1) & 3)) * 8;
+  const uint16_t* As = stage + (wm * SM * 16 + r) * BK + pc;
+  const uint16_t* Bs = stage + (BM + wn * SN * 16 + r) * BK + pc;
+#pragma unroll
+  for (int j = 0; j < SN; ++j) f.b[j] = *reinterpret_cast<const v4u*>(Bs + j * 16 * BK);
+#pragma unroll
+  for (int i = 0; i < SM; ++i) f.a[i] = *reinterpret_cast<const v4u*>(As + i * 16 * BK);
+}
+template <typename T, int SM, int SN>
+__device__ __forceinline__ void multiply(const Frags<SM, SN>& f, v4f (&acc)[SM][SN]) {
+#pragma unroll
+  for (int i = 0; i < SM; ++i)
+#pragma unroll
+    for (int j = 0; j < SN; ++j) acc[i][j] = T::mfma(f.a[i], f.b[j], acc[i][j]);
 }
 
 template <typename T, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN) void q_gemm_kernel(QGemm g, float* __restrict__ part, int splits) {
+__global__ __launch_bounds__(64 * WM * WN, 2) void q_gemm_kernel(QGemm g, float* __restrict__ part, int splits) {
   constexpr int WAVES = WM * WN;
   constexpr int SM = BM / WM / 16, SN = BN / WN / 16;   // 16 x 16 subtiles of a wave
-  constexpr int LOADS = (BM + BN) / 8 / WAVES;          // 1 KB loads per wave and step
-  __shared__ __attribute__((aligned(1024))) uint16_t lds[2][(BM + BN) * BK];
+  constexpr int LOADS = (BM + BN) / 16 / WAVES;         // 1 KB loads per wave and step
+  __shared__ __attribute__((aligned(1024))) uint16_t lds[STAGES][(BM + BN) * BK];
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int wm = wave / WN, wn = wave % WN;
   // tiles: contiguous runs per XCD (workgroups go to the 8 XCDs in turn), and
@@ -58,49 +103,50 @@ __global__ __launch_bounds__(64 * WM * WN) void q_gemm_kernel(QGemm g, float* __
   const int kt0 = (int)((int64_t)all * split / splits), kt1 = (int)((int64_t)all * (split + 1) / splits);
 
   // this lane's byte offsets within the tile's rows
-  const int piece = (lane & 7) ^ (lane >> 3);
+  const int piece = (lane & 3) ^ ((lane >> 3) & 3);
   uint32_t off[LOADS];
 #pragma unroll
   for (int l = 0; l < LOADS; ++l) {
-    const int r = (wave * LOADS + l) * 8 + (lane >> 3);
+    const int r = (wave * LOADS + l) * 16 + (lane >> 2);
     const bool a = r < BM;
     const int64_t lim = a ? g.M - 1 - i0 : g.N - 1 - j0;
     const int64_t row = min((int64_t)(a ? r : r - BM), lim);   // rows past the end repeat the last
     off[l] = (uint32_t)(row * (a ? g.lda : g.ldb) * 2 + piece * 16);
   }
+
   v4f acc[SM][SN];
 #pragma unroll
   for (int i = 0; i < SM; ++i)
 #pragma unroll
     for (int j = 0; j < SN; ++j) acc[i][j] = (v4f){0.f, 0.f, 0.f, 0.f};
 
-  if (kt0 < kt1) fetch_step<BM, LOADS>(g, i0, j0, kt0, kts, wave, off, lds[0]);
-  __builtin_amdgcn_s_waitcnt(0);
-  __syncthreads();
   const int r = lane & 15, kb = lane >> 4;
-  for (int kt = kt0; kt < kt1; ++kt) {
-    const int cur = (kt - kt0) & 1;
-    if (kt + 1 < kt1) fetch_step<BM, LOADS>(g, i0, j0, kt + 1, kts, wave, off, lds[cur ^ 1]);
-    const uint16_t* As = lds[cur] + (wm * SM * 16 + r) * BK;
-    const uint16_t* Bs = lds[cur] + (BM + wn * SN * 16 + r) * BK;
-#pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      const int pc = ((kk * 4 + kb) ^ (r & 7)) * 8;
-      v4u a[SM], b[SN];
-#pragma unroll
-      for (int i = 0; i < SM; ++i) a[i] = *reinterpret_cast<const v4u*>(As + i * 16 * BK + pc);
-#pragma unroll
-      for (int j = 0; j < SN; ++j) b[j] = *reinterpret_cast<const v4u*>(Bs + j * 16 * BK + pc);
-#pragma unroll
-      for (int i = 0; i < SM; ++i)
-#pragma unroll
-        for (int j = 0; j < SN; ++j) acc[i][j] = T::mfma(a[i], b[j], acc[i][j]);
-    }
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
+  Frags<SM, SN> f0, f1;
+  Cursor at;
+  seek(at, g, i0, j0, kt0 / kts, kt0 % kts);
+  // Step kt's operands are in registers when its turn begins; the barrier then
+  // says that stage kt + 1 is there and that every wave has read stage kt, whose
+  // place takes step kt + STAGES.
+  for (int s = 0; s < STAGES; ++s)
+    if (kt0 + s < kt1) fetch_step<BM, LOADS>(at, g, i0, j0, kts, wave, off, lds[s]);
+  if (kt0 + STAGES <= kt1) wait_stage<(STAGES - 1) * LOADS>(); else wait_stage<0>();
+  read_step<BM, SM, SN>(lds[0], wm, wn, r, kb, f0);
+#define Q_STEP(kt, cur, nxt)                                                                                 \
+  {                                                                                                          \
+    if ((kt) + STAGES <= kt1) wait_stage<(STAGES - 2) * LOADS>(); else wait_stage<0>();                      \
+    if ((kt) + STAGES < kt1)                                                                                 \
+      fetch_step<BM, LOADS>(at, g, i0, j0, kts, wave, off, lds[((kt) - kt0) % STAGES]);                      \
+    if ((kt) + 1 < kt1) read_step<BM, SM, SN>(lds[((kt) + 1 - kt0) % STAGES], wm, wn, r, kb, nxt);           \
+    multiply<T, SM, SN>(cur, acc);                                                                           \
   }
+  for (int kt = kt0; kt < kt1; kt += 2) {
+    Q_STEP(kt, f0, f1);
+    if (kt + 1 < kt1) Q_STEP(kt + 1, f1, f0);
+  }
+#undef Q_STEP
+  wait_stage<0>();   // every read of the stages is done
   // Epilogue: sixteen rows of the output at a time through this wave's part of
-  // LDS (every read of the stages is done), so that a row leaves as runs of
+  // LDS, so that a row leaves as runs of
   // SM * 16 columns and the finishing code stands once, not per accumulator.
   constexpr int PITCH = SM * 16 + 4, QUADS = SM * 4;
   static_assert(WAVES * 16 * PITCH * 4 <= (int)sizeof(lds), "the epilogue's rows fit the stages");
@@ -149,20 +195,25 @@ __global__ __launch_bounds__(256) void q_split_finish_kernel(const float* __rest
   q_finish4(O, j, i, v, false);
 }
 
+// Tile 256 x 256 moves the fewest bytes into LDS per product, 128 x 128 twice
+// as many, where the L2's 64 bytes a clock and CU are the limit: the largest
+// tile that still gives three CUs in four a workgroup is taken.  (2048 x 4096 x
+// 14336: 128 x 128 350 us, 256 x 128 265 us, 256 x 256 on half the CUs 370 us.)
+enum Tile : int { TILE_256 = 0, TILE_256_128 = 1, TILE_128 = 2 };
 struct Plan {
-  bool big;
+  int tile;
   int64_t tiles;
   int splits;
 };
 Plan plan(int64_t M, int64_t N, int64_t K, int npairs) {
   Plan p;
-  const int64_t big = ((M + 255) / 256) * ((N + 255) / 256);
-  p.big = big >= 192;
-  p.tiles = p.big ? big : ((M + 127) / 128) * ((N + 127) / 128);
+  auto count = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
+  p.tile = count(256, 256) >= 192 ? TILE_256 : count(256, 128) >= 192 ? TILE_256_128 : TILE_128;
+  p.tiles = p.tile == TILE_256 ? count(256, 256) : p.tile == TILE_256_128 ? count(256, 128) : count(128, 128);
   const int64_t kts = K / BK * npairs;
   p.splits = 1;
-  // two workgroups of the small tile fit a CU; a split keeps at least 8 steps
-  if (!p.big && p.tiles < 256) p.splits = (int)std::max<int64_t>(1, std::min({512 / p.tiles, kts / 8, (int64_t)16}));
+  // two workgroups of the small tile fit a CU; a split keeps at least 16 steps
+  if (p.tile == TILE_128 && p.tiles < 256) p.splits = (int)std::max<int64_t>(1, std::min({512 / p.tiles, kts / 16, (int64_t)16}));
   return p;
 }
 
@@ -189,8 +240,10 @@ static hipError_t run(const QGemm& g, float* part, hipStream_t st) {
   const Plan p = plan(g.M, g.N, g.K, g.npairs);
   float* out = p.splits > 1 ? part : nullptr;
   const dim3 grid((unsigned)(p.tiles * p.splits));
-  if (p.big)
+  if (p.tile == TILE_256)
     hipLaunchKernelGGL((q_gemm_kernel<T, 256, 256, 2, 4>), grid, dim3(512), 0, st, g, out, p.splits);
+  else if (p.tile == TILE_256_128)
+    hipLaunchKernelGGL((q_gemm_kernel<T, 256, 128, 4, 2>), grid, dim3(512), 0, st, g, out, p.splits);
   else
     hipLaunchKernelGGL((q_gemm_kernel<T, 128, 128, 2, 2>), grid, dim3(256), 0, st, g, out, p.splits);
   hipError_t e = hipGetLastError();

@@ -2,12 +2,11 @@
 //
 // A layer's m x n weights are W[i][j] = a e + o with base entries e of a
 // codebook.  Codes are packed in tiles of 16 rows: chunk c of a tile holds
-// QFmt::STEPS * 32 columns as 64 lanes x 16 bytes, lane l holding row l % 16,
-// columns ((l / 16) * STEPS + s) * 8 .. + 7 of the chunk for s = 0 .. STEPS - 1.
-// One wave load is 1 KB of contiguous memory, and what lane l decodes for step
-// s is its A operand of v_mfma_f32_16x16x32 as it stands: row l % 16, eight
-// consecutive k (the order of the k among the lanes' quarters is free as long
-// as the B operand uses the same).
+// q_steps(f) * 32 columns as 64 lanes x 16 bytes, lane l holding row l % 16 and,
+// for step s, columns s * 32 + (l / 16) * 8 .. + 7 of the chunk.  One wave load
+// is 1 KB of contiguous memory, and what lane l decodes for step s is its
+// operand of v_mfma_f32_16x16x32 as it stands; a row's four lanes of a step
+// cover 64 consecutive bytes of 16-bit activations or unpacked entries.
 //
 // d = 1: entries are taken about the middle level, e - levels[K / 2], so that
 // the sums over a grid 0 .. K - 1 do not carry a large common part that the

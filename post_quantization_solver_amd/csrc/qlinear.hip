@@ -43,13 +43,13 @@ __global__ __launch_bounds__(256) void q_pack_kernel(const int32_t* __restrict__
   const int64_t tc = at >> 6;
   const int64_t c = tc % L.chunks, i = tc / L.chunks * 16 + (lane & 15);
   const int steps = q_steps(L.fmt), kb = lane >> 4;
-  const int64_t blk0 = (c * 4 + kb) * steps;
+  const int64_t blk0 = c * steps * 4 + kb;   // step s: block blk0 + 4 s
   uint32_t w[4] = {0, 0, 0, 0};
   if (i < L.m) {
     if (L.fmt == QF_NIB || L.fmt == QF_BYTE) {
       const int bits = L.fmt == QF_NIB ? 4 : 8, count = steps * 8;
       for (int q = 0; q < count; ++q) {
-        const int64_t j = blk0 * 8 + q;
+        const int64_t j = (blk0 + q / 8 * 4) * 8 + q % 8;
         const int code = j < L.n ? safe_code(codes[i * L.n + j], L.K) : 0;
         const int bit = q * bits, hi = bit & 31;
         const uint32_t v = (uint32_t)code << hi;
@@ -61,7 +61,7 @@ __global__ __launch_bounds__(256) void q_pack_kernel(const int32_t* __restrict__
       const int64_t B = L.n / 8;
 #pragma unroll
       for (int s = 0; s < 8; ++s) {
-        uint32_t code = blk0 + s < B ? (uint32_t)safe_code(codes[i * B + blk0 + s], L.K) : 0u;
+        uint32_t code = blk0 + 4 * s < B ? (uint32_t)safe_code(codes[i * B + blk0 + 4 * s], L.K) : 0u;
         if (L.fmt == QF_E8) code = L.map[code];
         w[s >> 1] |= code << (16 * (s & 1));
       }
@@ -156,7 +156,7 @@ __global__ __launch_bounds__(64 * WAVES) void q_unpack_kernel(QLayer L, int tile
     const int64_t row = tl * 16 + (lane & 15), i = (int64_t)tile0 * 16 + row;
 #pragma unroll
     for (int s = 0; s < q_steps(FMT); ++s) {
-      const int64_t j0 = ((int64_t)(c * 4 + (lane >> 4)) * q_steps(FMT) + s) * 8;
+      const int64_t j0 = (((int64_t)c * q_steps(FMT) + s) * 4 + (lane >> 4)) * 8;
       v4u e = q_decode<FMT, T>(L, lds, code, s);
       if (i >= L.m || j0 >= Kp) continue;
       uint16_t* dst = out + row * Kp + j0;
@@ -220,7 +220,7 @@ __global__ __launch_bounds__(64 * WAVES) void q_unpack_t_kernel(QLayer L, int64_
         cs.x = s & 1 ? x >> 16 : x;
       }
       v4u e = q_decode<FMT, T>(L, lds, cs, 0);
-      const int64_t j0 = ((int64_t)(c * 4 + (lane >> 4)) * q_steps(FMT) + s) * 8;
+      const int64_t j0 = (((int64_t)c * q_steps(FMT) + s) * 4 + (lane >> 4)) * 8;
       v4u o[3];
       if (i >= L.m) e = (v4u){0u, 0u, 0u, 0u};
       o[0] = e;
@@ -242,7 +242,7 @@ __global__ __launch_bounds__(64 * WAVES) void q_unpack_t_kernel(QLayer L, int64_
         constexpr int PIECES = ROWS / 8;
         for (int k = threadIdx.x; k < 32 * PIECES; k += 64 * WAVES) {
           const int col = k / PIECES, piece = k - col * PIECES;
-          const int64_t j = ((int64_t)(c * 4 + (col >> 3)) * q_steps(FMT) + s) * 8 + (col & 7);
+          const int64_t j = ((int64_t)c * q_steps(FMT) + s) * 32 + col;
           const int64_t r = strip * ROWS + piece * 8;
           if (j < L.n && r < mp)
             *reinterpret_cast<v4u*>(out + p * plane + j * mp + r) =
@@ -360,7 +360,7 @@ __global__ __launch_bounds__(256) void q_affine_grad_kernel(QLayer L, const floa
     const float d = dW[row * ldw + j];
     // the weight's place in the packed tile
     const int64_t blk = j >> 3, c = blk / (4 * steps);
-    const int kb = (int)(blk - c * 4 * steps) / steps, s = (int)(blk - c * 4 * steps) % steps, q = (int)(j & 7);
+    const int kb = (int)(blk & 3), s = (int)(blk - c * 4 * steps) >> 2, q = (int)(j & 7);
     const size_t at = (((size_t)(i >> 4) * L.chunks + c) * 64 + kb * 16 + (i & 15)) * 8;   // 16-bit words
     float e;
     if (L.fmt == QF_NIB) {

@@ -77,19 +77,19 @@ __global__ __launch_bounds__(64 * SK_WAVES) void q_skinny_kernel(SkinnyArgs A) {
           for (int q = 0; q < R; ++q) z[q][n] = (v4f){0.f, 0.f, 0.f, 0.f};
         }
       }
-      const int blk0 = (c * 4 + kb) * STEPS;
+      const int blk0 = c * STEPS * 4 + kb;
 #pragma unroll
       for (int s = 0; s < STEPS; ++s) {
         v4u xf[NT][XP];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           const int64_t tok = tok0 + n * 16 + r;
-          const bool ok = tok < A.t && blk0 + s < A.kblocks;
+          const bool ok = tok < A.t && blk0 + s * 4 < A.kblocks;
 #pragma unroll
           for (int p = 0; p < XP; ++p) {
             xf[n][p] = (v4u){0u, 0u, 0u, 0u};
             if (ok)
-              xf[n][p] = *reinterpret_cast<const v4u*>(A.x + p * A.planex + tok * A.ldx + (int64_t)(blk0 + s) * 8);
+              xf[n][p] = *reinterpret_cast<const v4u*>(A.x + p * A.planex + tok * A.ldx + (int64_t)(blk0 + s * 4) * 8);
           }
         }
 #pragma unroll
