@@ -6,9 +6,8 @@
 // steps are on their way while the matrix cores work on a fourth out of
 // registers.  A row's four 16-byte pieces of a step are stored permuted by the
 // row's bits 1 and 2, so that the sixteen rows of an operand read spread over
-// the banks.  Operands of more than 16 bits enter as planes
-// whose sum they are: the products of plane pairs add up in the same float32
-// accumulators.
+// the banks.  Operands of more than 16 bits enter as planes whose sum they are:
+// the products of plane pairs add up in the same float32 accumulators.
 #include <algorithm>
 #include "qlayer.h"
 
@@ -146,29 +145,98 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void q_gemm_kernel(QGemm g, float*
 #undef Q_STEP
   wait_stage<0>();   // every read of the stages is done
   // Epilogue: sixteen rows of the output at a time through this wave's part of
-  // LDS, so that a row leaves as runs of
-  // SM * 16 columns and the finishing code stands once, not per accumulator.
-  constexpr int PITCH = SM * 16 + 4, QUADS = SM * 4;
+  // LDS, so that a row leaves as runs of SM * 16 columns.  A lane has the same
+  // four columns throughout; its rows' loads go out together.
+  constexpr int PITCH = SM * 16 + 4, QUADS = SM * 4, RPI = 64 / QUADS, IT = 16 / RPI;
   static_assert(WAVES * 16 * PITCH * 4 <= (int)sizeof(lds), "the epilogue's rows fit the stages");
   float* reg = reinterpret_cast<float*>(lds[0]) + wave * 16 * PITCH;
+  const int qrow = lane / QUADS, qcol = lane % QUADS * 4;
+  const int64_t ii = i0 + wm * SM * 16 + qcol;
+  float* own = reg + qrow * PITCH + qcol;   // and every RPI rows from there
+  const QCol C = q_col4(g.O, ii, true);
+  auto slot = [&](int it) { return reinterpret_cast<v4f*>(own + it * RPI * PITCH); };
+#pragma unroll 1
+  for (int j = 0; j < SN; ++j) {   // (one copy of the body; the accumulators by constant index)
 #pragma unroll
-  for (int j = 0; j < SN; ++j) {
+    for (int jc = 0; jc < SN; ++jc)
+      if (jc == j) {
 #pragma unroll
-    for (int i = 0; i < SM; ++i) *reinterpret_cast<v4f*>(reg + r * PITCH + i * 16 + 4 * kb) = acc[i][j];
+        for (int i = 0; i < SM; ++i) *reinterpret_cast<v4f*>(reg + r * PITCH + i * 16 + 4 * kb) = acc[i][jc];
+      }
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    const int64_t jj = j0 + (wn * SN + j) * 16 + qrow;   // and every RPI rows from there
+    if (g.cpart) {
+      uint32_t code[IT];
+      float f[IT];
+#pragma unroll
+      for (int it = 0; it < IT; ++it) {
+        const int64_t row = min(jj + it * RPI, g.N - 1);
+        code[it] = q_code4(g.L, g.row0 + row, min(ii, (g.M - 1) & ~(int64_t)3));
+        f[it] = pow2(-pow2_shift(g.O.rowmax[row]));
+      }
+#pragma unroll
+      for (int it = 0; it < IT; ++it) {
+        float e[4], se = 0.f, s1 = 0.f;
+        q_entries4(g.L, code[it], ii, e);
+        const v4f x = *slot(it);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (k < C.live) {
+            const float v = x[k] * C.a[k] * f[it];
+            se = fmaf(e[k], v, se);
+            s1 += v;
+          }
+        // sixteen lanes hold one row's 64 columns
+        se += dpp_f<DPP_XOR1>(se); s1 += dpp_f<DPP_XOR1>(s1);
+        se += dpp_f<DPP_XOR2>(se); s1 += dpp_f<DPP_XOR2>(s1);
+        se += dpp_f<DPP_HALF_MIRROR>(se); s1 += dpp_f<DPP_HALF_MIRROR>(s1);
+        se += dpp_f<DPP_MIRROR>(se); s1 += dpp_f<DPP_MIRROR>(s1);
+        if ((lane & 15) == 0 && jj + it * RPI < g.N && C.live > 0)
+          g.cpart[((size_t)split * g.N + jj + it * RPI) * g.cblocks + ii / Q_CONTRACT] = make_float2(se, s1);
+      }
+    } else if (part) {
+      // rows of part are padded to four columns
+#pragma unroll
+      for (int it = 0; it < IT; ++it)
+        if (jj + it * RPI < g.N && C.live > 0)
+          *reinterpret_cast<v4f*>(part + ((size_t)split * g.N + jj + it * RPI) * ((g.M + 3) / 4 * 4) + ii) = *slot(it);
+    } else if (C.live > 0) {
+      float res[IT][4];
+#pragma unroll
+      for (int it = 0; it < IT; ++it) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) res[it][k] = 0.f;
+        if (g.O.res && jj + it * RPI < g.N)
+          load4(g.O.res, (jj + it * RPI) * g.O.ldres + ii, g.O.dtype, g.O.vec, C.live, res[it]);
+      }
+#pragma unroll
+      for (int it = 0; it < IT; ++it) {
+        if (jj + it * RPI >= g.N) continue;
+        const v4f x = *slot(it);
+        float v[4] = {x[0], x[1], x[2], x[3]};
+        q_affine4(g.O, C, jj + it * RPI, v);
+        if (g.O.pre) store4(g.O.pre, (jj + it * RPI) * g.O.ldpre + ii, g.O.dtype, g.O.vec, C.live, v);
+        *slot(it) = (v4f){v[0], v[1], v[2], v[3]};
+      }
+      if (g.O.act != ACT_NONE) {   // (its code stands once)
 #pragma unroll 1
-    for (int q = lane; q < 16 * QUADS; q += 64) {
-      const int row = q / QUADS, c = (q - row * QUADS) * 4;
-      const int64_t jj = j0 + (wn * SN + j) * 16 + row, ii = i0 + wm * SM * 16 + c;
-      const float4 x = *reinterpret_cast<const float4*>(reg + row * PITCH + c);
-      float v[4] = {x.x, x.y, x.z, x.w};
-      if (part) {
-        if (jj < g.N && ii < g.M)   // rows of part are padded to four columns
-          *reinterpret_cast<float4*>(part + ((size_t)split * g.N + jj) * ((g.M + 3) / 4 * 4) + ii) = x;
-      } else {
-        q_finish4(g.O, jj, ii, v, false);
+        for (int it = 0; it < IT; ++it) {
+          v4f x = *slot(it);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x[k] = act_fwd(g.O.act, x[k]);
+          *slot(it) = x;
+        }
+      }
+#pragma unroll
+      for (int it = 0; it < IT; ++it) {
+        if (jj + it * RPI >= g.N) continue;
+        const v4f x = *slot(it);
+        float v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = x[k] + res[it][k];
+        store4(g.O.y, (jj + it * RPI) * g.O.ldy + ii, g.O.dtype, g.O.vec, C.live, v);
       }
     }
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -192,7 +260,7 @@ __global__ __launch_bounds__(256) void q_split_finish_kernel(const float* __rest
     v[2] += q.z;
     v[3] += q.w;
   }
-  q_finish4(O, j, i, v, false);
+  q_finish4(O, j, i, v, true);
 }
 
 // Tile 256 x 256 moves the fewest bytes into LDS per product, 128 x 128 twice
@@ -221,12 +289,16 @@ Plan plan(int64_t M, int64_t N, int64_t K, int npairs) {
 
 void q_pairs(QGemm& g, int PA, int PB) {
   g.npairs = 0;
-  for (int s = 0; s <= 2; ++s)
+  for (int s = 0; s <= 1; ++s)
     for (int p = 0; p <= s; ++p)
       if (p < PA && s - p < PB) {
         g.pa[g.npairs] = (uint8_t)p;
         g.pb[g.npairs++] = (uint8_t)(s - p);
       }
+}
+
+int q_gemm_splits(int64_t M, int64_t N, int64_t K, int npairs) {
+  return M <= 0 || N <= 0 ? 1 : plan(M, N, K, npairs).splits;
 }
 
 size_t q_gemm_workspace(int64_t M, int64_t N, int64_t K, int npairs) {
@@ -238,7 +310,7 @@ size_t q_gemm_workspace(int64_t M, int64_t N, int64_t K, int npairs) {
 template <typename T>
 static hipError_t run(const QGemm& g, float* part, hipStream_t st) {
   const Plan p = plan(g.M, g.N, g.K, g.npairs);
-  float* out = p.splits > 1 ? part : nullptr;
+  float* out = p.splits > 1 && !g.cpart ? part : nullptr;
   const dim3 grid((unsigned)(p.tiles * p.splits));
   if (p.tile == TILE_256)
     hipLaunchKernelGGL((q_gemm_kernel<T, 256, 256, 2, 4>), grid, dim3(512), 0, st, g, out, p.splits);
@@ -247,7 +319,7 @@ static hipError_t run(const QGemm& g, float* part, hipStream_t st) {
   else
     hipLaunchKernelGGL((q_gemm_kernel<T, 128, 128, 2, 2>), grid, dim3(256), 0, st, g, out, p.splits);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || p.splits == 1) return e;
+  if (e != hipSuccess || !out) return e;
   const int64_t Mp = (g.M + 3) / 4 * 4;
   hipLaunchKernelGGL(q_split_finish_kernel, dim3((unsigned)((g.N * (Mp / 4) + 255) / 256)), dim3(256), 0, st, part,
                      p.splits, g.N, Mp, g.O);
@@ -257,7 +329,7 @@ static hipError_t run(const QGemm& g, float* part, hipStream_t st) {
 hipError_t launch_q_gemm(const QGemm& g, float* part, hipStream_t st) {
   if (g.M <= 0 || g.N <= 0) return hipSuccess;
   if (g.K % BK != 0 || g.K <= 0) return hipErrorInvalidValue;
-  return g.half ? run<OpF16>(g, part, st) : run<OpBf16>(g, part, st);
+  return g.bf16 ? run<OpBf16>(g, part, st) : run<OpF16>(g, part, st);
 }
 
 }  // namespace mpq

@@ -226,6 +226,26 @@ __device__ __forceinline__ void store4(void* p, int64_t i, int dtype, bool vec, 
 }
 #endif  // __HIPCC__
 
+// Operands of the float16 products carry a power of two per row that takes the
+// row's largest magnitude to [2^14, 2^15): float16's eleven bits then hold
+// elements down to 2^-28 of it in full and smaller ones to 2^-39 of it, below
+// what float32 sums resolve.  The factor comes from the bits of that magnitude;
+// a row of zeros, or one that holds NaN or infinities, keeps factor 1.
+#ifdef __HIPCC__
+__device__ __forceinline__ int pow2_shift(uint32_t maxbits) {
+  const int e = (int)(maxbits >> 23) & 255;
+  return maxbits == 0 || e == 255 ? 0 : min(141 - max(e, 1), 126);
+}
+__device__ __forceinline__ float pow2(int k) { return __uint_as_float((uint32_t)(k + 127) << 23); }   // |k| <= 126
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+// x in two float16 terms.
+__device__ __forceinline__ void f16_terms(float x, uint32_t* b) {
+  b[0] = OpF16::bits(x);
+  const float lo = x - OpF16::val(b[0]);
+  b[1] = fabsf(x) <= 65504.f ? OpF16::bits(lo) : 0u;   // an infinite or NaN x stays what it is, alone
+}
+#endif
+
 // The outputs of a product, out[j][i] for row j and column i: four consecutive
 // columns at a time.
 struct QOut {
@@ -233,48 +253,106 @@ struct QOut {
   void* pre; int64_t ldpre;         // the activation's argument (nullptr: not kept)
   const void* res; int64_t ldres;   // added after the activation
   const float* bias;                // per column
+  const uint32_t* rowmax;           // per row: its operand's largest magnitude (pow2_shift; nullptr: no factor)
+  const uint32_t* colmax;           // per column, likewise
   const float* colscale;            // per column: factor of the product (nullptr: 1)
-  const float* coloff;              // per column: factor of rowadd (nullptr: see mid)
-  const float* rowadd;              // per row
-  const float* levels; int mid;     // d = 1: levels[mid] is added to coloff as colscale times it (mid < 0: nothing)
+  const float* coloff;              // per column: factor of rowadd
+  const float* rowadd;              // per row: added, times coloff + colscale mid if there is a colscale
+  const float* levels; int mid;     // d = 1: levels[mid] (mid < 0: zero)
   int act, dtype;
   int vec;                          // 4-element alignment of y, pre, res
   int64_t rows, cols;
 };
 
 #ifdef __HIPCC__
-// u = colscale v + (coloff + colscale mid) rowadd + bias; y = act(u) + res.
-__device__ __forceinline__ void q_finish4(const QOut& O, int64_t j, int64_t i, float* v, bool scaled) {
-  const int live = (int)min((int64_t)4, O.cols - i);
-  if (j >= O.rows || live <= 0) return;
-  if (!scaled) {
-    const float add = O.rowadd ? O.rowadd[j] : 0.f;
-    const float mid = O.mid >= 0 ? O.levels[O.mid] : 0.f;
+// What four columns multiply and add: u = a v + o rowadd + b.
+struct QCol {
+  float a[4], o[4], b[4];
+  int live;   // columns there are (<= 0: none)
+};
+__device__ __forceinline__ QCol q_col4(const QOut& O, int64_t i, bool affine) {
+  QCol C;
+  C.live = (int)min((int64_t)4, O.cols - i);
+  const float mid = affine && O.colscale && O.mid >= 0 ? O.levels[O.mid] : 0.f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (k >= live) break;
-      const float a = O.colscale ? O.colscale[i + k] : 1.f;
-      float o = O.coloff ? O.coloff[i + k] : 0.f;
-      if (O.mid >= 0) o = fmaf(a, mid, o);
-      if (!O.colscale && !O.coloff) o = 1.f;   // rowadd alone
-      v[k] = a * v[k];
-      if (O.rowadd) v[k] = fmaf(o, add, v[k]);
+  for (int k = 0; k < 4; ++k) {
+    C.a[k] = C.o[k] = 1.f;
+    C.b[k] = 0.f;
+    if (k >= C.live) continue;
+    if (O.bias) C.b[k] = O.bias[i + k];
+    if (!affine) continue;
+    if (O.colscale) {
+      C.a[k] = O.colscale[i + k];
+      C.o[k] = fmaf(C.a[k], mid, O.coloff ? O.coloff[i + k] : 0.f);
     }
+    if (O.colmax) C.a[k] *= pow2(-pow2_shift(O.colmax[i + k]));
   }
-  if (O.bias)
+  return C;
+}
+// Row j's part of it.
+__device__ __forceinline__ void q_affine4(const QOut& O, const QCol& C, int64_t j, float* v) {
+  const float f = O.rowmax ? pow2(-pow2_shift(O.rowmax[j])) : 1.f;
+  const float add = O.rowadd ? O.rowadd[j] : 0.f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] += k < live ? O.bias[i + k] : 0.f;
-  if (O.pre) store4(O.pre, j * O.ldpre + i, O.dtype, O.vec, live, v);
+  for (int k = 0; k < 4; ++k) v[k] = fmaf(C.a[k], v[k] * f, (O.rowadd ? C.o[k] * add : 0.f) + C.b[k]);
+}
+
+// Four columns of row j: y = act(v + bias) + res, v with the affine still to come or not.
+__device__ __forceinline__ void q_finish4(const QOut& O, int64_t j, int64_t i, float* v, bool affine) {
+  const QCol C = q_col4(O, i, affine);
+  if (j >= O.rows || C.live <= 0) return;
+  if (affine) {
+    q_affine4(O, C, j, v);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] += C.b[k];
+  }
+  if (O.pre) store4(O.pre, j * O.ldpre + i, O.dtype, O.vec, C.live, v);
   if (O.act != ACT_NONE)
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] = act_fwd(O.act, v[k]);
   if (O.res) {
     float r[4];
-    load4(O.res, j * O.ldres + i, O.dtype, O.vec, live, r);
+    load4(O.res, j * O.ldres + i, O.dtype, O.vec, C.live, r);
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] += r[k];
   }
-  store4(O.y, j * O.ldy + i, O.dtype, O.vec, live, v);
+  store4(O.y, j * O.ldy + i, O.dtype, O.vec, C.live, v);
+}
+
+// The entries of row i's columns j .. j + 3 (j a multiple of 4, inside the packed
+// chunks): the code's bits first, then the entries, so that loads of several
+// quads can be on their way together.
+__device__ __forceinline__ uint32_t q_code4(const QLayer& L, int64_t i, int64_t j) {
+  const int steps = q_steps(L.fmt);
+  const uint16_t* codes = reinterpret_cast<const uint16_t*>(L.packed);
+  const int64_t blk = j >> 3, c = blk / (4 * steps);
+  const int kb = (int)(blk & 3), s = (int)(blk - c * 4 * steps) >> 2, half = (int)(j >> 2) & 1;
+  const size_t at = (((size_t)(i >> 4) * L.chunks + c) * 64 + kb * 16 + (i & 15)) * 8;   // 16-bit words
+  if (L.fmt == QF_NIB) return codes[at + s * 2 + half];
+  if (L.fmt == QF_BYTE) return *reinterpret_cast<const uint32_t*>(codes + at + s * 4 + half * 2);
+  return codes[at + s];
+}
+__device__ __forceinline__ void q_entries4(const QLayer& L, uint32_t code, int64_t j, float* e) {
+  const int half = (int)(j >> 2) & 1;
+  if (L.fmt == QF_NIB) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) e[k] = L.levels[(code >> (4 * k)) & 15u];
+  } else if (L.fmt == QF_BYTE) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) e[k] = L.levels[(code >> (8 * k)) & 63u];
+  } else if (L.fmt == QF_E8) {
+    const int c = (int)code;
+    const uint32_t v = L.lut[max(c >> 1, c - L.pairs)] ^ (c & 1 ? 0x88888888u : 0u);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t nib = v >> (8 * k + 4 * half);
+      e[k] = 0.5f * (float)(nib & 7u) * (nib & 8u ? -1.f : 1.f);
+    }
+  } else {
+    const float4 q = *reinterpret_cast<const float4*>(L.e32 + (size_t)code * 8 + half * 4);
+    e[0] = q.x; e[1] = q.y; e[2] = q.z; e[3] = q.w;
+  }
 }
 #endif
 
@@ -282,26 +360,35 @@ __device__ __forceinline__ void q_finish4(const QOut& O, int64_t j, int64_t i, f
 
 // D[j][i] = sum over the plane pairs (p, q) and k of A_p[i][k] B_q[j][k] (16-bit
 // planes, K a multiple of 64, rows of lda / ldb elements, 16-byte aligned), then
-// O.  part (split K): splits x rows x cols float32, or nullptr.
+// O, or the contraction.  part (split K): splits x rows x cols float32.
 struct QGemm {
   const uint16_t* A; int64_t lda, planeA;
   const uint16_t* B; int64_t ldb, planeB;
   int64_t M, N, K;        // columns i, rows j, depth of one plane
   int npairs;
-  uint8_t pa[6], pb[6];
-  bool half;              // fp16 operands (else bfloat16)
+  uint8_t pa[4], pb[4];
+  bool bf16;              // bfloat16 operands (else float16)
   QOut O;
+  // Contraction (cpart != nullptr), D the gradient of layer rows row0 + j: per
+  // 64 columns the sums of e D and of D, cpart[split][j][block] (float2), in
+  // place of an output.
+  QLayer L;
+  int64_t row0;
+  float2* cpart; int64_t cblocks;
 };
-// Pairs of PA and PB planes whose orders add to at most two.
+constexpr int Q_CONTRACT = 64;
+// Pairs of PA and PB planes whose orders add to at most one.
 void q_pairs(QGemm& g, int PA, int PB);
+int q_gemm_splits(int64_t M, int64_t N, int64_t K, int npairs);
 size_t q_gemm_workspace(int64_t M, int64_t N, int64_t K, int npairs);
 hipError_t launch_q_gemm(const QGemm& g, float* part, hipStream_t st);
 
 // The product with few rows (qskinny.hip): x as planes of 16-bit rows, kblocks blocks of
-// eight columns each.  Column groups need chunks that lie in one group.
+// eight columns each (two planes: float16, with O.rowmax).  Column groups need
+// chunks that lie in one group.
 bool q_skinny_ok(const QLayer& L);
 hipError_t launch_q_skinny(const QLayer& L, const uint16_t* x, int64_t ldx, int64_t planex, int kblocks, int64_t t,
-                           int planes, bool half, const QOut& O, hipStream_t st);
+                           int planes, bool bf16, const QOut& O, hipStream_t st);
 
 struct QLinearArgs {
   QLayer L;

@@ -2,20 +2,23 @@
 // the order of the launches (qlayer.h; products in qskinny.hip and qgemm.hip).
 //
 // Many rows: the layer's entries e (one affine per row; exact in 16 bits) or
-// its weights a e + o' (column groups; two or three terms) become 16-bit planes
-// in the workspace, a block of rows at a time that stays in the last-level
-// cache, and the product runs on the matrix cores; the affine, bias,
-// activation and residual are its epilogue.
+// its weights a e + o (column groups) become 16-bit planes in the workspace, a
+// block of rows at a time that stays in the last-level cache, and the product
+// runs on the matrix cores; the affine, bias, activation and residual are its
+// epilogue.
 //
 // Gradients (codes fixed): du = dy act'(pre);
 //   dx = du W: one affine per row: (du a) e + du o', the second a number per
 //        row of dx; groups: du times the weights' planes;
-//   dW = du^T x, contracted: d scale = sum_j e_ij dW_ij, d offset = sum_j dW_ij
-//        over the columns of a group;
+//   dW = du^T x, contracted as it leaves the product: d scale = sum_j e_ij dW_ij,
+//        d offset = sum_j dW_ij over the columns of a group;
 //   d bias = sum_t du.
-// d scale and d offset are float32 sums: du enters dW as three bfloat16 terms
-// (one where it is dy itself), x as its exact terms.  dx is 16 bits wide (or
-// float32), so du a is rounded once to its type there (float32: three terms).
+//
+// Roundings.  What is not exact in 16 bits (float32 x, du under an activation
+// or times a scale, the weights of column groups) enters as float16 terms of
+// itself times a power of two per row of the operand (qlayer.h): one term, 11
+// bits, where a bfloat16 result is rounded to 8 anyway; two, 22 bits, for
+// float16 and float32 results and for the float32 sums of the layer's gradients.
 #include <string.h>
 #include <algorithm>
 #include "qlayer.h"
@@ -72,77 +75,115 @@ __global__ __launch_bounds__(256) void q_pack_kernel(const int32_t* __restrict__
 
 // ------------------------------------------------------------------ operands
 
-// Term p of x as bfloat16: x = sum of the terms, to 2^-8 per term.
-__device__ __forceinline__ void bf_terms(float x, uint32_t* b) {
-  split3_bf16(x, b[0], b[1], b[2]);
-  // an infinite or NaN x stays what it is, alone (inf - inf in a later term is NaN)
-  if (!(fabsf(x) <= 3.4028235e38f)) b[1] = b[2] = 0;
+// The largest magnitude among a row's weights, bounded: max |a| max |e'| + |o'|
+// over its groups; one wave per row.
+__device__ __forceinline__ float row_bound(const QLayer& L, int64_t i, int lane) {
+  float top = 0.f;
+  const float mid = q_centre(L);
+  for (int k = lane; k < L.K; k += 64) top = fmaxf(top, fabsf(L.levels[k] - mid));   // groups have d = 1
+  for (int o = 32; o; o >>= 1) top = fmaxf(top, shfl_xor_f(top, o));
+  float w = 0.f;
+  bool odd = false;
+  for (int64_t g = lane; g < L.G; g += 64) {
+    const float a = L.scale[i * L.G + g], o = fmaf(a, mid, L.offset ? L.offset[i * L.G + g] : 0.f);
+    const float b = fabsf(a) * top + fabsf(o);
+    odd |= !(b <= 3.4028235e38f);
+    w = fmaxf(w, b);
+  }
+  for (int o = 32; o; o >>= 1) w = fmaxf(w, shfl_xor_f(w, o));
+  return __ballot(odd) ? 0.f : w;   // a row that is not finite keeps factor 1
 }
-__device__ __forceinline__ uint32_t widened_or_half(float x, bool half) { return half ? OpF16::bits(x) : f2bf_bits(x); }
 
-// One row of x per workgroup: its 16-bit planes, padded with zeros to Kp
-// columns (planes = 0: none), and its sum (optional).
-__global__ __launch_bounds__(256) void q_prep_kernel(const void* __restrict__ x, int64_t ldx, int dtype, int64_t n,
-                                                     int64_t Kp, uint16_t* __restrict__ out, int64_t plane, int planes,
-                                                     bool half, float* __restrict__ sum) {
-  __shared__ float red[4];
-  const int64_t t = blockIdx.x;
+// Blocks 0 .. t - 1, one row of x each: its 16-bit planes, padded with zeros to
+// Kp columns -- planes = 0: none; raw: a copy of 16-bit x; else float16 terms of
+// x times 2^pow2_shift(rowmax), stored -- and its sum (optional).  The blocks
+// after them, a wave per row of the layer: refs = its weights' bound.
+__global__ __launch_bounds__(256) void q_prep_kernel(const void* __restrict__ x, int64_t ldx, int dtype, int64_t t,
+                                                     int64_t n, int64_t Kp, uint16_t* __restrict__ out, int64_t plane,
+                                                     int planes, bool raw, uint32_t* __restrict__ rowmax,
+                                                     float* __restrict__ sum, QLayer L, uint32_t* __restrict__ refs) {
+  __shared__ float red[2][4];
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  const int64_t row = blockIdx.x;
+  if (row >= t) {
+    const int64_t i = (row - t) * 4 + wave;
+    if (i >= L.m) return;
+    const float b = row_bound(L, i, lane);
+    if (lane == 0) refs[i] = __float_as_uint(b);
+    return;
+  }
   float s = 0.f;
-  for (int64_t j = threadIdx.x; j < Kp; j += 256) {
-    const float v = j < n ? load_as_f32(x, t * ldx + j, dtype) : 0.f;
-    s += v;
-    if (planes == 1) {
-      out[t * Kp + j] = (uint16_t)widened_or_half(v, half);
-    } else if (planes > 1) {
-      uint32_t b[3];
-      bf_terms(v, b);
-      for (int p = 0; p < planes; ++p) out[p * plane + t * Kp + j] = (uint16_t)(p == 0 ? b[0] : p == 1 ? b[1] : b[2]);
+  uint32_t top = 0;
+  if (sum || (planes && !raw)) {
+    for (int64_t j = threadIdx.x; j < n; j += 256) {
+      const float v = load_as_f32(x, row * ldx + j, dtype);
+      s += v;
+      top = max(top, abs_bits(v));
+    }
+    for (int o = 32; o; o >>= 1) {
+      s += shfl_xor_f(s, o);
+      top = max(top, (uint32_t)shfl_xor_i((int)top, o));
+    }
+    if (lane == 0) {
+      red[0][wave] = s;
+      red[1][wave] = __uint_as_float(top);
+    }
+    __syncthreads();
+    top = 0;
+    for (int w = 0; w < 4; ++w) top = max(top, __float_as_uint(red[1][w]));
+    if (threadIdx.x == 0) {
+      if (sum) sum[row] = (red[0][0] + red[0][1]) + (red[0][2] + red[0][3]);
+      if (planes && !raw) rowmax[row] = top;
     }
   }
-  if (!sum) return;
-  for (int o = 32; o; o >>= 1) s += shfl_xor_f(s, o);
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
-  __syncthreads();
-  if (threadIdx.x == 0) sum[t] = (red[0] + red[1]) + (red[2] + red[3]);
+  if (!planes) return;
+  const float f = pow2(pow2_shift(top));
+  for (int64_t j = threadIdx.x; j < Kp; j += 256) {
+    if (raw) {
+      out[row * Kp + j] = j < n ? static_cast<const uint16_t*>(x)[row * ldx + j] : (uint16_t)0;
+      continue;
+    }
+    uint32_t b[2];
+    f16_terms(j < n ? load_as_f32(x, row * ldx + j, dtype) * f : 0.f, b);
+    out[row * Kp + j] = (uint16_t)b[0];
+    if (planes > 1) out[plane + row * Kp + j] = (uint16_t)b[1];
+  }
 }
 
-// Planes of T terms of the eight values v at step columns.
-template <typename T>
-__device__ __forceinline__ void weight_terms(const float* v, int planes, v4u* out) {
+// Eight weights of row i from their entries, times f.
+__device__ __forceinline__ void weights8(const QLayer& L, int64_t i, int64_t j0, v4u e, float mid, float f, float* v) {
+  if (L.group % 8 == 0 || L.G == 1) {   // one group
+    const int64_t g = i * L.G + (L.G > 1 ? min(j0, L.n - 1) / L.group : 0);
+    const float a = L.scale[g], o = fmaf(a, mid, L.offset ? L.offset[g] : 0.f);
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      v[q] = j0 + q < L.n ? fmaf(a, OpF16::val(q & 1 ? e[q >> 1] >> 16 : e[q >> 1] & 0xffffu), o) * f : 0.f;
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int64_t g = i * L.G + min(j0 + q, L.n - 1) / L.group;
+      const float a = L.scale[g], o = fmaf(a, mid, L.offset ? L.offset[g] : 0.f);
+      v[q] = j0 + q < L.n ? fmaf(a, OpF16::val(q & 1 ? e[q >> 1] >> 16 : e[q >> 1] & 0xffffu), o) * f : 0.f;
+    }
+  }
+}
+__device__ __forceinline__ void weight_terms(const float* v, v4u* out) {
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    if (T::HALF) {
-      const uint32_t h = T::pack(v[2 * q], v[2 * q + 1]);
-      out[0][q] = h;
-      out[1][q] = T::pack(v[2 * q] - T::val(h & 0xffffu), v[2 * q + 1] - T::val(h >> 16));
-      out[2][q] = 0u;
-    } else {
-      uint32_t a[3], b[3];
-      bf_terms(v[2 * q], a);
-      bf_terms(v[2 * q + 1], b);
-#pragma unroll
-      for (int p = 0; p < 3; ++p) out[p][q] = pack2(a[p], b[p]);
-    }
-  }
-}
-
-// Eight weights of row i from their entries.
-template <typename T>
-__device__ __forceinline__ void weights8(const QLayer& L, int64_t i, int64_t j0, v4u e, float mid, float* v) {
-#pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    const float x = T::val(q & 1 ? e[q >> 1] >> 16 : e[q >> 1] & 0xffffu);
-    const int64_t j = min(j0 + q, L.n - 1);
-    const int64_t g = i * L.G + (L.G > 1 ? j / L.group : 0);
-    const float a = L.scale[g];
-    v[q] = j0 + q < L.n ? fmaf(a, x, fmaf(a, mid, L.offset ? L.offset[g] : 0.f)) : 0.f;
+    uint32_t a[2], b[2];
+    f16_terms(v[2 * q], a);
+    f16_terms(v[2 * q + 1], b);
+    out[0][q] = pack2(a[0], b[0]);
+    out[1][q] = pack2(a[1], b[1]);
   }
 }
 
 // Rows tile0 * 16 .. of the layer as planes of Kp columns: entries (planes = 0),
-// or weights in `planes` terms.  A wave per chunk of a tile.
+// or float16 terms of the weights times 2^pow2_shift(refs).  A wave per chunk of
+// a tile.
 template <int FMT, typename T, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void q_unpack_kernel(QLayer L, int tile0, int tiles, int64_t Kp, int planes,
+                                                              const uint32_t* __restrict__ refs,
                                                               uint16_t* __restrict__ out, int64_t plane) {
   extern __shared__ __attribute__((aligned(16))) uint32_t lds[];
   const int lane = threadIdx.x & 63, wave = wave_id();
@@ -154,6 +195,7 @@ __global__ __launch_bounds__(64 * WAVES) void q_unpack_kernel(QLayer L, int tile
     const int tl = (int)(w / L.chunks), c = (int)(w - (int64_t)tl * L.chunks);
     const uint4 code = L.packed[((size_t)(tile0 + tl) * L.chunks + c) * 64 + lane];
     const int64_t row = tl * 16 + (lane & 15), i = (int64_t)tile0 * 16 + row;
+    const float f = planes ? pow2(pow2_shift(refs[min(i, L.m - 1)])) : 1.f;
 #pragma unroll
     for (int s = 0; s < q_steps(FMT); ++s) {
       const int64_t j0 = (((int64_t)c * q_steps(FMT) + s) * 4 + (lane >> 4)) * 8;
@@ -168,30 +210,32 @@ __global__ __launch_bounds__(64 * WAVES) void q_unpack_kernel(QLayer L, int tile
             if (j0 + q >= L.n) e[q >> 1] &= q & 1 ? 0xffffu : 0xffff0000u;
         }
         *reinterpret_cast<v4u*>(dst) = e;
-      } else {
+      } else if constexpr (T::HALF) {
         float v[8];
-        v4u o[3];
-        weights8<T>(L, i, j0, e, mid, v);
-        weight_terms<T>(v, planes, o);
-#pragma unroll
-        for (int p = 0; p < 3; ++p)
-          if (p < planes) *reinterpret_cast<v4u*>(dst + p * plane) = o[p];
+        v4u o[2];
+        weights8(L, i, j0, e, mid, f, v);
+        weight_terms(v, o);
+        *reinterpret_cast<v4u*>(dst) = o[0];
+        if (planes > 1) *reinterpret_cast<v4u*>(dst + plane) = o[1];
       }
     }
   }
 }
 
-// The transpose: plane rows are the layer's columns, mp (m padded with zeros
-// to 64) entries or weights each.  A workgroup unpacks 16 WAVES rows of one
-// chunk, 32 columns at a time, through LDS.
+// The transpose, float16: plane rows are the layer's columns, mp (m padded
+// with zeros to 64) entries or weights each.  A workgroup unpacks 16 WAVES rows
+// of one chunk, 32 columns at a time, through LDS; a lane's eight columns are
+// spread over LDS rows padded by 16 bytes, so that the sixteen rows of a store
+// share no bank with the next column's.
 template <int FMT, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void q_unpack_t_kernel(QLayer L, int64_t mp, int planes,
+                                                                const uint32_t* __restrict__ refs,
                                                                 uint16_t* __restrict__ out, int64_t plane,
                                                                 int lut_words) {
-  using T = OpBf16;
+  using T = OpF16;
   extern __shared__ __attribute__((aligned(16))) uint32_t lds[];
-  constexpr int ROWS = 16 * WAVES;
-  uint16_t* tl = reinterpret_cast<uint16_t*>(lds + lut_words);   // 32 columns x ROWS
+  constexpr int ROWS = 16 * WAVES, PITCH = ROWS + 8;
+  uint16_t* tl = reinterpret_cast<uint16_t*>(lds + lut_words);   // 32 columns x PITCH
   const int lane = threadIdx.x & 63, wave = wave_id();
   q_lut_fill<FMT, T>(L, lds, 64 * WAVES);
   __syncthreads();
@@ -204,7 +248,8 @@ __global__ __launch_bounds__(64 * WAVES) void q_unpack_t_kernel(QLayer L, int64_
     const bool live = tile < L.tiles;
     uint4 code = make_uint4(0, 0, 0, 0);
     if (live) code = L.packed[((size_t)tile * L.chunks + c) * 64 + lane];
-    const int64_t i = tile * 16 + (lane & 15);
+    const int64_t i = tile * 16 + (lane & 15), is = min(i, L.m - 1);
+    const float f = planes ? pow2(pow2_shift(refs[is])) : 1.f;
 #pragma unroll 1
     for (int s = 0; s < q_steps(FMT); ++s) {
       // (the step is not unrolled: its word is picked, so that one copy of the decoder remains)
@@ -219,24 +264,20 @@ __global__ __launch_bounds__(64 * WAVES) void q_unpack_t_kernel(QLayer L, int64_
         const uint32_t x = s < 2 ? ws[0] : s < 4 ? ws[1] : s < 6 ? ws[2] : ws[3];
         cs.x = s & 1 ? x >> 16 : x;
       }
-      v4u e = q_decode<FMT, T>(L, lds, cs, 0);
-      const int64_t j0 = (((int64_t)c * q_steps(FMT) + s) * 4 + (lane >> 4)) * 8;
-      v4u o[3];
-      if (i >= L.m) e = (v4u){0u, 0u, 0u, 0u};
-      o[0] = e;
+      v4u o[2];
+      o[0] = q_decode<FMT, T>(L, lds, cs, 0);
       if (planes > 0) {
         float v[8];
-        weights8<T>(L, min(i, L.m - 1), j0, e, mid, v);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] = i < L.m ? v[q] : 0.f;
-        weight_terms<T>(v, planes, o);
+        weights8(L, is, (((int64_t)c * q_steps(FMT) + s) * 4 + (lane >> 4)) * 8, o[0], mid, f, v);
+        weight_terms(v, o);
       }
+      if (i >= L.m) o[0] = o[1] = (v4u){0u, 0u, 0u, 0u};
 #pragma unroll
-      for (int p = 0; p < 3; ++p) {
-        if (p >= (planes > 0 ? planes : 1)) break;
+      for (int p = 0; p < 2; ++p) {
+        if (p > 0 && p >= planes) break;
 #pragma unroll
         for (int q = 0; q < 8; ++q)
-          tl[((lane >> 4) * 8 + q) * ROWS + wave * 16 + (lane & 15)] =
+          tl[((lane >> 4) * 8 + q) * PITCH + wave * 16 + (lane & 15)] =
               (uint16_t)(q & 1 ? o[p][q >> 1] >> 16 : o[p][q >> 1] & 0xffffu);
         __syncthreads();
         constexpr int PIECES = ROWS / 8;
@@ -246,7 +287,7 @@ __global__ __launch_bounds__(64 * WAVES) void q_unpack_t_kernel(QLayer L, int64_
           const int64_t r = strip * ROWS + piece * 8;
           if (j < L.n && r < mp)
             *reinterpret_cast<v4u*>(out + p * plane + j * mp + r) =
-                *reinterpret_cast<const v4u*>(tl + col * ROWS + piece * 8);
+                *reinterpret_cast<const v4u*>(tl + col * PITCH + piece * 8);
         }
         __syncthreads();
       }
@@ -254,96 +295,238 @@ __global__ __launch_bounds__(64 * WAVES) void q_unpack_t_kernel(QLayer L, int64_
   }
 }
 
-// Bfloat16 planes of x^T: n rows of tp (t padded with zeros to 64).
-__global__ __launch_bounds__(256) void q_transpose_kernel(const void* __restrict__ x, int64_t ldx, int dtype, int64_t t,
-                                                          int64_t n, int64_t tp, int planes,
-                                                          uint16_t* __restrict__ out, int64_t plane) {
-  __shared__ float tl[64][65];
-  const int64_t j0 = (int64_t)blockIdx.x * 64, t0 = (int64_t)blockIdx.y * 64;
-  const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
-  for (int y = ty; y < 64; y += 4)
-    tl[y][tx] = t0 + y < t && j0 + tx < n ? load_as_f32(x, (t0 + y) * ldx + j0 + tx, dtype) : 0.f;
-  __syncthreads();
-  for (int y = ty; y < 64; y += 4) {
-    if (j0 + y >= n) break;
-    uint32_t b[3];
-    bf_terms(tl[tx][y], b);
-    for (int p = 0; p < planes; ++p)
-      out[p * plane + (j0 + y) * tp + t0 + tx] = (uint16_t)(p == 0 ? b[0] : p == 1 ? b[1] : b[2]);
-  }
-}
+// ------------------------------------------------------------------ gradients
 
+// Tiles of 64 x 64: thread (tid / 16, tid % 16) has rows tid / 16 + 16 k, four
+// consecutive columns.
 struct DuArgs {
   const void* dy; int64_t lddy;
   const void* pre; int64_t ldpre;
+  const void* x; int64_t ldx;
   int act, dtype;
-  int64_t t, m;
-  // (du a) or du, t rows of mp
+  bool vec_du, vec_x;                 // 4-element alignment of dy and pre, of x
+  int64_t t, m, n;
+  QLayer L;
+  bool want_d, want_t;
+  // largest magnitudes (bits): du times the layer row's factor per token, du
+  // per layer row, x per column; refs: the layer rows' bounds (groups)
+  uint32_t *dmax, *tmax, *xmax, *refs;
+  // du times the factor, float16 terms, t rows of mp
   uint16_t* d; int64_t plane_d, mp; int planes_d;
-  const float* scale;                 // per row of the layer, or nullptr
-  const float* offset;                // with scale
-  const float* levels; int mid;
   float* rowpart; int64_t rowtiles;   // t x rowtiles: sums of du o' over 64 columns (nullptr: none)
-  // du^T, m rows of tp
+  // du^T, float16 terms, m rows of tp
   uint16_t* dt; int64_t plane_t, tp; int planes_t;
   float* biaspart;                    // (tp / 64) x m: sums of du over 64 rows
+  // x^T, float16 terms, n rows of tp
+  uint16_t* xt; int64_t plane_x; int planes_x;
+  int64_t du_blocks, xtiles;          // 64 x 64 tiles of du, column tiles of x
 };
 
-// A 64 x 64 tile of du: its planes, its transpose's planes, its row and column sums.
-__global__ __launch_bounds__(256) void q_du_kernel(DuArgs A) {
-  __shared__ float tl[64][65];
-  const int64_t i0 = (int64_t)blockIdx.x * 64, t0 = (int64_t)blockIdx.y * 64;
-  const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
-  const int64_t i = i0 + tx;
-  float a = 1.f, o = 0.f;
-  if (A.scale && i < A.m) {
-    a = A.scale[i];
-    o = fmaf(a, A.mid >= 0 ? A.levels[A.mid] : 0.f, A.offset ? A.offset[i] : 0.f);
+// What the rows of du are multiplied by for dx: the scale itself (one affine
+// per row), or the inverse of what the weights' planes are scaled by.
+__device__ __forceinline__ float du_factor(const DuArgs& A, int64_t i) {
+  return A.L.G == 1 ? A.L.scale[i] : pow2(-pow2_shift(A.refs[i]));
+}
+
+// Four values of du at row t, columns i ..
+__device__ __forceinline__ void load_du(const DuArgs& A, int64_t t, int64_t i, float* v) {
+  const int live = t < A.t ? (int)max((int64_t)0, min((int64_t)4, A.m - i)) : 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = 0.f;
+  if (live == 0) return;
+  load4(A.dy, t * A.lddy + i, A.dtype, A.vec_du, live, v);
+  if (A.act != ACT_NONE) {
+    float u[4];
+    load4(A.pre, t * A.ldpre + i, A.dtype, A.vec_du, live, u);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (k < live) v[k] *= act_slope(A.act, u[k]);
   }
-  for (int y = ty; y < 64; y += 4) {
-    float v = 0.f;
-    if (t0 + y < A.t && i < A.m) {
-      v = load_as_f32(A.dy, (t0 + y) * A.lddy + i, A.dtype);
-      if (A.act != ACT_NONE) v *= act_slope(A.act, load_as_f32(A.pre, (t0 + y) * A.ldpre + i, A.dtype));
+}
+__device__ __forceinline__ void load_x(const DuArgs& A, int64_t t, int64_t j, float* v) {
+  const int live = t < A.t ? (int)max((int64_t)0, min((int64_t)4, A.n - j)) : 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = 0.f;
+  if (live) load4(A.x, t * A.ldx + j, A.dtype, A.vec_x, live, v);
+}
+
+// Clears the maxima and fills refs (groups; a wave per row).
+__global__ __launch_bounds__(256) void q_grad_init_kernel(DuArgs A) {
+  const int lane = threadIdx.x & 63;
+  for (int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x; k < max(max(A.t, A.m), A.n); k += (int64_t)gridDim.x * 256) {
+    if (k < A.t) A.dmax[k] = 0;
+    if (k < A.m) A.tmax[k] = 0;
+    if (k < A.n) A.xmax[k] = 0;
+  }
+  if (A.L.G > 1)
+    for (int64_t i = (int64_t)blockIdx.x * 4 + wave_id(); i < A.m; i += (int64_t)gridDim.x * 4) {
+      const float b = row_bound(A.L, i, lane);
+      if (lane == 0) A.refs[i] = __float_as_uint(b);
     }
-    tl[y][tx] = v;
-    if (A.d && t0 + y < A.t && i < A.mp) {
-      uint32_t b[3];
-      bf_terms(A.scale ? v * a : v, b);
-      for (int p = 0; p < A.planes_d; ++p)
-        A.d[p * A.plane_d + (t0 + y) * A.mp + i] = (uint16_t)(p == 0 ? b[0] : p == 1 ? b[1] : b[2]);
+}
+
+// The maxima (integer maxima of magnitudes' bits: in any order the same).
+__global__ __launch_bounds__(256) void q_grad_scan_kernel(DuArgs A) {
+  __shared__ uint32_t cm[4][64];
+  const int cx = threadIdx.x & 15, ry = threadIdx.x >> 4, wave = wave_id();
+  const bool is_x = blockIdx.x >= A.du_blocks;
+  const int64_t b = is_x ? blockIdx.x - A.du_blocks : blockIdx.x, ct = is_x ? A.xtiles : A.rowtiles;
+  const int64_t t0 = b / ct * 64, i = (b % ct) * 64 + cx * 4;
+  uint32_t col[4] = {0, 0, 0, 0};
+  float f[4] = {1.f, 1.f, 1.f, 1.f};
+  const bool rows = !is_x && A.want_d;
+  if (rows)
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (i + k < A.m) f[k] = du_factor(A, i + k);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int64_t t = t0 + ry + 16 * k;
+    float v[4];
+    if (is_x) load_x(A, t, i, v); else load_du(A, t, i, v);
+    uint32_t top = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      col[q] = max(col[q], abs_bits(v[q]));
+      top = max(top, abs_bits(v[q] * f[q]));
     }
-    if (A.rowpart) {
-      float s = v * o;
-      for (int k = 32; k; k >>= 1) s += shfl_xor_f(s, k);
-      if (tx == 0 && t0 + y < A.t) A.rowpart[(t0 + y) * A.rowtiles + blockIdx.x] = s;
+    if (rows) {
+      top = max(top, (uint32_t)dpp_i<DPP_XOR1>((int)top));
+      top = max(top, (uint32_t)dpp_i<DPP_XOR2>((int)top));
+      top = max(top, (uint32_t)dpp_i<DPP_HALF_MIRROR>((int)top));
+      top = max(top, (uint32_t)dpp_i<DPP_MIRROR>((int)top));
+      if (cx == 0 && t < A.t) atomicMax(A.dmax + t, top);
     }
+  }
+  if (!is_x && !A.want_t) return;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    col[q] = max(col[q], (uint32_t)shfl_xor_i((int)col[q], 16));
+    col[q] = max(col[q], (uint32_t)shfl_xor_i((int)col[q], 32));
+    if ((threadIdx.x & 63) < 16) cm[wave][cx * 4 + q] = col[q];
   }
   __syncthreads();
-  if (!A.dt) return;
-  for (int y = ty; y < 64; y += 4) {
-    if (i0 + y >= A.m) break;
-    const float v = tl[tx][y];
-    uint32_t b[3];
-    bf_terms(v, b);
-    for (int p = 0; p < A.planes_t; ++p)
-      A.dt[p * A.plane_t + (i0 + y) * A.tp + t0 + tx] = (uint16_t)(p == 0 ? b[0] : p == 1 ? b[1] : b[2]);
-    float s = v;
-    for (int k = 32; k; k >>= 1) s += shfl_xor_f(s, k);
-    if (tx == 0) A.biaspart[blockIdx.y * A.m + i0 + y] = s;
+  if (threadIdx.x < 64) {
+    const int64_t j = (b % ct) * 64 + threadIdx.x;
+    const uint32_t top = max(max(cm[0][threadIdx.x], cm[1][threadIdx.x]), max(cm[2][threadIdx.x], cm[3][threadIdx.x]));
+    if (j < (is_x ? A.n : A.m)) atomicMax((is_x ? A.xmax : A.tmax) + j, top);
   }
 }
 
-// out[r] = sum of part[r * ld + k * step], k < count, in order, in float64.
-__global__ __launch_bounds__(256) void q_sum_kernel(const float* __restrict__ part, int64_t rows, int64_t ld,
-                                                    int64_t step, int64_t count, float* __restrict__ out) {
-  const int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (r >= rows) return;
-  double s = 0.0;
-  for (int64_t k = 0; k < count; ++k) s += (double)part[r * ld + k * step];
-  out[r] = (float)s;
+// Four float16 terms of v at p[0 .. 3].
+__device__ __forceinline__ void put_terms(uint16_t* p, int64_t plane, int planes, const float* v) {
+  uint32_t b[4][2];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) f16_terms(v[k], b[k]);
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack2(b[0][0], b[1][0]), pack2(b[2][0], b[3][0]));
+  if (planes > 1)
+    *reinterpret_cast<uint2*>(p + plane) = make_uint2(pack2(b[0][1], b[1][1]), pack2(b[2][1], b[3][1]));
+}
+__device__ __forceinline__ float sum16(float s) {
+  s += dpp_f<DPP_XOR1>(s);
+  s += dpp_f<DPP_XOR2>(s);
+  s += dpp_f<DPP_HALF_MIRROR>(s);
+  s += dpp_f<DPP_MIRROR>(s);
+  return s;
 }
 
+// A 64 x 64 tile of du (its planes, its transpose's, its row and column sums)
+// or of x (its transpose's planes).
+__global__ __launch_bounds__(256) void q_grad_tile_kernel(DuArgs A) {
+  __shared__ float tl[64][65];
+  const int cx = threadIdx.x & 15, ry = threadIdx.x >> 4;
+  const bool is_x = blockIdx.x >= A.du_blocks;
+  const int64_t b = is_x ? blockIdx.x - A.du_blocks : blockIdx.x, ct = is_x ? A.xtiles : A.rowtiles;
+  const int64_t t0 = b / ct * 64, i0 = (b % ct) * 64, i = i0 + cx * 4;
+  float f[4] = {0.f, 0.f, 0.f, 0.f}, o[4] = {0.f, 0.f, 0.f, 0.f};
+  if (!is_x && A.want_d)
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (i + k < A.m) {
+        f[k] = du_factor(A, i + k);
+        if (A.rowpart) o[k] = fmaf(A.L.scale[i + k], q_centre(A.L), A.L.offset ? A.L.offset[i + k] : 0.f);
+      }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int64_t t = t0 + ry + 16 * k;
+    float v[4];
+    if (is_x) load_x(A, t, i, v); else load_du(A, t, i, v);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) tl[ry + 16 * k][cx * 4 + q] = v[q];
+    if (is_x || !A.want_d) continue;
+    if (A.rowpart) {
+      const float s = sum16(fmaf(v[0], o[0], v[1] * o[1]) + fmaf(v[2], o[2], v[3] * o[3]));
+      if (cx == 0 && t < A.t) A.rowpart[t * A.rowtiles + b % ct] = s;
+    }
+    if (t < A.t) {
+      const float g = pow2(pow2_shift(A.dmax[t]));
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] *= f[q] * g;
+      put_terms(A.d + t * A.mp + i, A.plane_d, A.planes_d, v);
+    }
+  }
+  if (!is_x && !A.want_t) return;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int64_t r = i0 + ry + 16 * k;   // row of the transpose: sixteen lanes have its 64 tokens
+    float v[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = tl[cx * 4 + q][ry + 16 * k];
+    const float s = sum16((v[0] + v[1]) + (v[2] + v[3]));
+    if (r >= (is_x ? A.n : A.m)) continue;
+    if (!is_x && cx == 0) A.biaspart[t0 / 64 * A.m + r] = s;
+    const float g = pow2(pow2_shift(is_x ? A.xmax[r] : A.tmax[r]));
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] *= g;
+    if (is_x) put_terms(A.xt + r * A.tp + t0 + cx * 4, A.plane_x, A.planes_x, v);
+    else put_terms(A.dt + r * A.tp + t0 + cx * 4, A.plane_t, A.planes_t, v);
+  }
+}
+
+// d bias (want_t) and du o' per token (rowpart), added up in order in float64.
+__global__ __launch_bounds__(256) void q_grad_sums_kernel(DuArgs A, float* __restrict__ dbias, float* __restrict__ rowadd) {
+  const int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  double s = 0.0;
+  if (A.want_t && r < A.m) {
+    for (int64_t k = 0; k < A.tp / 64; ++k) s += (double)A.biaspart[k * A.m + r];
+    dbias[r] = (float)s;
+  }
+  const int64_t t = r - (A.want_t ? (A.m + 255) / 256 * 256 : 0);
+  if (A.rowpart && t >= 0 && t < A.t) {
+    for (int64_t k = 0; k < A.rowtiles; ++k) s += (double)A.rowpart[t * A.rowtiles + k];
+    rowadd[t] = (float)s;
+  }
+}
+
+// The contraction's parts, added up in order in float64: sixteen lanes per (row, group).
+__global__ __launch_bounds__(256) void q_contract_finish_kernel(QLayer L, const float2* __restrict__ part, int splits,
+                                                                int64_t rows, int64_t blocks, int64_t row0,
+                                                                float* __restrict__ dscale,
+                                                                float* __restrict__ doffset) {
+  const int lane = threadIdx.x & 15;
+  const int64_t w = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+  if (w >= rows * L.G) return;
+  const int64_t row = w / L.G, g = w - row * L.G;
+  const int64_t b0 = g * (L.group / Q_CONTRACT), b1 = L.G == 1 ? blocks : min(blocks, b0 + L.group / Q_CONTRACT);
+  double se = 0.0, s1 = 0.0;
+  for (int s = 0; s < splits; ++s)
+    for (int64_t b = b0 + lane; b < b1; b += 16) {
+      const float2 p = part[((size_t)s * rows + row) * blocks + b];
+      se += (double)p.x;
+      s1 += (double)p.y;
+    }
+  for (int o = 8; o; o >>= 1) {
+    se += shfl_d(se, (int)(threadIdx.x & 63) ^ o);
+    s1 += shfl_d(s1, (int)(threadIdx.x & 63) ^ o);
+  }
+  if (lane == 0) {
+    dscale[(row0 + row) * L.G + g] = (float)se;
+    doffset[(row0 + row) * L.G + g] = (float)s1;
+  }
+}
+
+// Groups that are no multiple of 64 columns: the contraction of a dW in memory.
 // d scale and d offset of `rows` rows from row0 on: a wave per (row, group).
 __global__ __launch_bounds__(256) void q_affine_grad_kernel(QLayer L, const float* __restrict__ dW, int64_t ldw,
                                                             int64_t row0, int64_t rows, float* __restrict__ dscale,
@@ -353,30 +536,18 @@ __global__ __launch_bounds__(256) void q_affine_grad_kernel(QLayer L, const floa
   if (w >= rows * L.G) return;
   const int64_t row = w / L.G, g = w - row * L.G, i = row0 + row;
   const int64_t j0 = g * L.group, j1 = min(L.n, j0 + L.group);
-  const int steps = q_steps(L.fmt);
-  const uint16_t* codes = reinterpret_cast<const uint16_t*>(L.packed);
   double se = 0.0, s1 = 0.0;
-  for (int64_t j = j0 + lane; j < j1; j += 64) {
-    const float d = dW[row * ldw + j];
-    // the weight's place in the packed tile
-    const int64_t blk = j >> 3, c = blk / (4 * steps);
-    const int kb = (int)(blk & 3), s = (int)(blk - c * 4 * steps) >> 2, q = (int)(j & 7);
-    const size_t at = (((size_t)(i >> 4) * L.chunks + c) * 64 + kb * 16 + (i & 15)) * 8;   // 16-bit words
-    float e;
-    if (L.fmt == QF_NIB) {
-      e = L.levels[(codes[at + s * 2 + (q >> 2)] >> (4 * (q & 3))) & 15];
-    } else if (L.fmt == QF_BYTE) {
-      e = L.levels[(codes[at + s * 4 + (q >> 1)] >> (8 * (q & 1))) & 255];
-    } else if (L.fmt == QF_E8) {
-      const int code = codes[at + s];
-      const uint32_t v = L.lut[max(code >> 1, code - L.pairs)] ^ (code & 1 ? 0x88888888u : 0u);
-      const uint32_t nib = v >> (4 * (q < 4 ? 2 * q : 2 * q - 7));
-      e = 0.5f * (float)(nib & 7u) * (nib & 8u ? -1.f : 1.f);
-    } else {
-      e = L.e32[(size_t)codes[at + s] * 8 + q];
+  for (int64_t q = j0 / 4 + lane; q * 4 < j1; q += 64) {
+    float e[4];
+    q_entries4(L, q_code4(L, i, q * 4), q * 4, e);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t j = q * 4 + k;
+      if (j < j0 || j >= j1) continue;
+      const float d = dW[row * ldw + j];
+      se += (double)(e[k] * d);
+      s1 += (double)d;
     }
-    se += (double)(e * d);
-    s1 += (double)d;
   }
   for (int o = 32; o; o >>= 1) {
     se += shfl_d(se, lane ^ o);
@@ -391,37 +562,38 @@ __global__ __launch_bounds__(256) void q_affine_grad_kernel(QLayer L, const floa
 // ------------------------------------------------------------------ launches
 
 template <typename T>
-hipError_t unpack(const QLayer& L, int tile0, int tiles, int64_t Kp, int planes, uint16_t* out, int64_t plane,
-                  hipStream_t st) {
+hipError_t unpack(const QLayer& L, int tile0, int tiles, int64_t Kp, int planes, const uint32_t* refs, uint16_t* out,
+                  int64_t plane, hipStream_t st) {
   const size_t shared = (size_t)q_lut_words(L.fmt, (L.lut_entries + 3) / 4 * 4) * 4;
   const int64_t waves = (int64_t)tiles * L.chunks;
   auto grid = [&](int per, int most) { return dim3((unsigned)std::min<int64_t>((waves + per - 1) / per, most)); };
   switch (L.fmt) {
     case QF_NIB:
       hipLaunchKernelGGL((q_unpack_kernel<QF_NIB, T, 4>), grid(4, 2048), dim3(256), shared, st, L, tile0, tiles, Kp,
-                         planes, out, plane);
+                         planes, refs, out, plane);
       break;
     case QF_BYTE:
       hipLaunchKernelGGL((q_unpack_kernel<QF_BYTE, T, 4>), grid(4, 2048), dim3(256), shared, st, L, tile0, tiles, Kp,
-                         planes, out, plane);
+                         planes, refs, out, plane);
       break;
     case QF_E8:   // the table fills a CU's LDS: one workgroup of 16 waves each
       hipLaunchKernelGGL((q_unpack_kernel<QF_E8, T, 16>), grid(16, 256), dim3(1024), shared, st, L, tile0, tiles, Kp,
-                         planes, out, plane);
+                         planes, refs, out, plane);
       break;
     default:
       hipLaunchKernelGGL((q_unpack_kernel<QF_VEC, T, 4>), grid(4, 2048), dim3(256), shared, st, L, tile0, tiles, Kp,
-                         planes, out, plane);
+                         planes, refs, out, plane);
   }
   return hipGetLastError();
 }
 
-hipError_t unpack_t(const QLayer& L, int64_t mp, int planes, uint16_t* out, int64_t plane, hipStream_t st) {
+hipError_t unpack_t(const QLayer& L, int64_t mp, int planes, const uint32_t* refs, uint16_t* out, int64_t plane,
+                    hipStream_t st) {
   const int lut = q_lut_words(L.fmt, (L.lut_entries + 3) / 4 * 4);
   auto go = [&](auto kernel, int waves, int most) {
     const int64_t total = (mp + 16 * waves - 1) / (16 * waves) * L.chunks;
     hipLaunchKernelGGL(kernel, dim3((unsigned)std::min<int64_t>(total, most)), dim3(64 * waves),
-                       (size_t)lut * 4 + (size_t)32 * 16 * waves * 2, st, L, mp, planes, out, plane, lut);
+                       (size_t)lut * 4 + (size_t)32 * (16 * waves + 8) * 2, st, L, mp, planes, refs, out, plane, lut);
   };
   switch (L.fmt) {
     case QF_NIB: go(q_unpack_t_kernel<QF_NIB, 4>, 4, 2048); break;
@@ -432,28 +604,11 @@ hipError_t unpack_t(const QLayer& L, int64_t mp, int planes, uint16_t* out, int6
   return hipGetLastError();
 }
 
-// The operand planes of x for the forward product: x itself where its rows
-// are 16-bit, 16-byte aligned and whole steps, else padded copies.
-struct XPlan {
-  bool direct, half;
-  int planes;
-  int64_t Kp;
-};
-XPlan x_plan(const QLinearArgs& A, bool skinny) {
-  XPlan P;
-  P.half = A.dtype == DT_F16;
-  P.planes = A.dtype == DT_F32 ? 3 : 1;
-  P.Kp = up64(A.L.n);
-  const bool aligned = reinterpret_cast<uintptr_t>(A.x) % 16 == 0 && A.ldx % 8 == 0 && A.ldx <= (1 << 20);
-  P.direct = P.planes == 1 && aligned && A.L.n % (skinny ? 8 : 64) == 0;
-  return P;
-}
+// Token counts up to which the product reads the packed codes (one affine per
+// row, and groups of whole chunks; other groups always unpack).
+constexpr int64_t Q_SKINNY_TOKENS = 128;
 
-// Token counts from which the unpacked product is used.  (One affine per row and groups of whole chunks; other
-// groups always unpack.)
-int64_t skinny_tokens(const QLayer&) { return 128; }
-
-bool use_skinny(const QLinearArgs& A) { return q_skinny_ok(A.L) && A.t <= skinny_tokens(A.L); }
+bool use_skinny(const QLinearArgs& A) { return q_skinny_ok(A.L) && A.t <= Q_SKINNY_TOKENS; }
 
 struct Carve {
   char* base;
@@ -466,86 +621,101 @@ struct Carve {
   }
 };
 
-// Forward: lays out the workspace and, with a base, launches.
+bool whole_quads(const void* p, int64_t ld, int dtype) {
+  return !p || (reinterpret_cast<uintptr_t>(p) % (dtype == DT_F32 ? 16 : 8) == 0 && ld % 4 == 0);
+}
+
+// Forward: lays out the workspace (which depends on the shapes and types
+// alone) and, with a base, launches.
 hipError_t forward(const QLinearArgs& A, char* base, size_t* bytes, hipStream_t st) {
   const QLayer& L = A.L;
-  const bool skinny = use_skinny(A);
-  const XPlan P = x_plan(A, skinny);
+  const bool skinny = use_skinny(A), grouped = L.G > 1, weights = grouped && !skinny;
+  const int64_t Kp = up64(L.n);
+  // x: its own 16 bits, or float16 terms (float32; bfloat16 against weights)
+  const int XP = A.dtype == DT_F32 ? 2 : 1;
+  const bool raw = A.dtype == DT_F16 || (A.dtype == DT_BF16 && !weights);
+  const bool direct = raw && reinterpret_cast<uintptr_t>(A.x) % 16 == 0 && A.ldx % 8 == 0 && A.ldx <= (1 << 20) &&
+                      L.n % (skinny ? 8 : 64) == 0;
+  const bool bf16 = raw && A.dtype == DT_BF16;
+  const int WP = !weights ? 0 : A.dtype == DT_BF16 ? 1 : 2;   // terms of a weight (0: entries)
+  const bool sums = !skinny && !grouped && L.has_offset();
   Carve W{base};
-  // (the layout does not depend on x's alignment: the caller sizes it without x)
-  const int64_t plane = A.t * P.Kp;
-  uint16_t* xp = W.take<uint16_t>((size_t)P.planes * plane * 2);
+  const int64_t plane = A.t * Kp;
+  uint16_t* xp = W.take<uint16_t>((size_t)XP * plane * 2);
   float* xs = W.take<float>((size_t)A.t * 4);
-  const bool grouped = L.G > 1, sums = !skinny && !grouped && L.has_offset();
-  const int WP = !grouped ? 0 : A.dtype == DT_F32 ? 3 : 2;   // terms of a weight (0: entries)
+  uint32_t* rowmax = W.take<uint32_t>((size_t)A.t * 4);
+  uint32_t* refs = W.take<uint32_t>((size_t)L.m * 4);
   const int per = WP ? WP : 1;
-  int64_t rows = std::max<int64_t>(256, Q_BLOCK_BYTES / (per * P.Kp * 2) / 256 * 256);
+  int64_t rows = std::max<int64_t>(256, Q_BLOCK_BYTES / (per * Kp * 2) / 256 * 256);
   rows = std::min(rows, (int64_t)L.tiles * 16);
   QGemm g;
   memset(&g, 0, sizeof(g));
-  if (WP) q_pairs(g, WP, P.planes); else q_pairs(g, 1, P.planes);
+  q_pairs(g, per, XP);
   uint16_t* wp = nullptr;
   float* part = nullptr;
   if (!skinny) {
-    wp = W.take<uint16_t>((size_t)per * rows * P.Kp * 2);
+    wp = W.take<uint16_t>((size_t)per * rows * Kp * 2);
     size_t ps = 0;
     for (int64_t r0 = 0; r0 < L.m; r0 += rows)
-      ps = std::max(ps, q_gemm_workspace(std::min(rows, L.m - r0), A.t, P.Kp, g.npairs));
+      ps = std::max(ps, q_gemm_workspace(std::min(rows, L.m - r0), A.t, Kp, g.npairs));
     part = W.take<float>(ps);
   }
   if (bytes) *bytes = W.at;
   if (!base) return hipSuccess;
 
   hipError_t e;
-  if (!P.direct || sums) {
-    hipLaunchKernelGGL(q_prep_kernel, dim3((unsigned)A.t), dim3(256), 0, st, A.x, A.ldx, A.dtype, L.n, P.Kp, xp, plane,
-                       P.direct ? 0 : P.planes, P.half, sums ? xs : nullptr);
+  const bool copy = !direct;
+  if (copy || sums || weights) {
+    const int64_t blocks = A.t + (weights ? (L.m + 3) / 4 : 0);
+    hipLaunchKernelGGL(q_prep_kernel, dim3((unsigned)blocks), dim3(256), 0, st, A.x, A.ldx, A.dtype, A.t, L.n, Kp, xp,
+                       plane, copy ? XP : 0, raw, rowmax, sums ? xs : nullptr, L, refs);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  const uint16_t* x = P.direct ? static_cast<const uint16_t*>(A.x) : xp;
-  const int64_t ldx = P.direct ? A.ldx : P.Kp;
+  const uint16_t* x = direct ? static_cast<const uint16_t*>(A.x) : xp;
+  const int64_t ldx = direct ? A.ldx : Kp;
   QOut O;
   memset(&O, 0, sizeof(O));
   O.y = A.y; O.ldy = A.ldy;
   O.pre = A.pre; O.ldpre = A.ldpre;
   O.res = A.res; O.ldres = A.ldres;
   O.bias = A.bias;
+  O.rowmax = raw ? nullptr : rowmax;
   O.act = A.act;
   O.dtype = A.dtype;
   O.mid = -1;
   O.rows = A.t;
   O.cols = L.m;
-  const uintptr_t quad = A.dtype == DT_F32 ? 16 : 8;
-  auto whole = [&](const void* p, int64_t ld) {
-    return !p || (reinterpret_cast<uintptr_t>(p) % quad == 0 && ld % 4 == 0);
-  };
-  O.vec = whole(A.y, A.ldy) && whole(A.pre, A.ldpre) && whole(A.res, A.ldres);
+  O.vec = whole_quads(A.y, A.ldy, A.dtype) && whole_quads(A.pre, A.ldpre, A.dtype) &&
+          whole_quads(A.res, A.ldres, A.dtype);
   if (skinny)
-    return launch_q_skinny(L, x, ldx, plane, (int)(P.direct ? L.n / 8 : P.Kp / 8), A.t, P.planes, P.half, O, st);
+    return launch_q_skinny(L, x, ldx, plane, (int)(direct ? L.n / 8 : Kp / 8), A.t, XP, bf16, O, st);
   const int es = A.dtype == DT_F32 ? 4 : 2;
   for (int64_t r0 = 0; r0 < L.m; r0 += rows) {
     const int64_t nr = std::min(rows, L.m - r0);
     const int tiles = (int)((nr + 15) / 16);
-    e = P.half ? unpack<OpF16>(L, (int)(r0 / 16), tiles, P.Kp, WP, wp, rows * P.Kp, st)
-               : unpack<OpBf16>(L, (int)(r0 / 16), tiles, P.Kp, WP, wp, rows * P.Kp, st);
+    e = bf16 ? unpack<OpBf16>(L, (int)(r0 / 16), tiles, Kp, WP, refs, wp, rows * Kp, st)
+             : unpack<OpF16>(L, (int)(r0 / 16), tiles, Kp, WP, refs, wp, rows * Kp, st);
     if (e != hipSuccess) return e;
-    g.A = wp; g.lda = P.Kp; g.planeA = rows * P.Kp;
+    g.A = wp; g.lda = Kp; g.planeA = rows * Kp;
     g.B = x; g.ldb = ldx; g.planeB = plane;
-    g.M = nr; g.N = A.t; g.K = P.Kp;
-    g.half = P.half;
+    g.M = nr; g.N = A.t; g.K = Kp;
+    g.bf16 = bf16;
     g.O = O;
     g.O.cols = nr;
     g.O.y = static_cast<char*>(A.y) + r0 * es;
     if (A.pre) g.O.pre = static_cast<char*>(A.pre) + r0 * es;
     if (A.res) g.O.res = static_cast<const char*>(A.res) + r0 * es;
     if (A.bias) g.O.bias = A.bias + r0;
-    if (!grouped) {
+    if (weights) {
+      g.O.colmax = refs + r0;
+    } else {
       g.O.colscale = L.scale + r0;
       g.O.coloff = L.offset ? L.offset + r0 : nullptr;
       g.O.rowadd = sums ? xs : nullptr;
       g.O.levels = L.levels;
       g.O.mid = L.fmt == QF_NIB || L.fmt == QF_BYTE ? L.K / 2 : -1;
     }
+    // (the column blocks start at multiples of 256: their alignment is the whole's)
     if ((e = launch_q_gemm(g, part, st)) != hipSuccess) return e;
   }
   return hipSuccess;
@@ -553,107 +723,132 @@ hipError_t forward(const QLinearArgs& A, char* base, size_t* bytes, hipStream_t 
 
 hipError_t backward(const QLinearGrad& A, char* base, size_t* bytes, hipStream_t st) {
   const QLayer& L = A.L;
-  const bool grouped = L.G > 1;
+  const bool grouped = L.G > 1, contract = !grouped || L.group % Q_CONTRACT == 0;
   const int64_t mp = up64(L.m), tp = up64(A.t);
-  const int XP = A.dtype == DT_F32 ? 3 : A.dtype == DT_F16 ? 2 : 1;             // x, exactly
-  const int DP = A.act == ACT_NONE ? XP : 3;                                    // du for dW: exactly, or 24 bits
-  const int DX = A.dtype == DT_F32 ? 3 : A.dtype == DT_F16 ? 2 : 1;             // du (a) for dx
-  const int WP = !grouped ? 0 : A.dtype == DT_F32 ? 3 : 2, per = WP ? WP : 1;   // weights for dx
+  const int XP = A.dtype == DT_F32 ? 2 : 1;                             // x
+  const int DP = A.dtype == DT_F32 || A.act != ACT_NONE ? 2 : 1;        // du for the layer's gradients
+  const int DX = A.dtype == DT_BF16 ? 1 : 2;                            // du for dx
+  const int WP = !grouped ? 0 : A.dtype == DT_BF16 ? 1 : 2, per = WP ? WP : 1;
+  DuArgs D;
+  memset(&D, 0, sizeof(D));
   Carve W{base};
-  const int64_t plane_d = A.t * mp, plane_t = L.m * tp, plane_w = L.n * mp, plane_x = L.n * tp;
-  const int64_t rowtiles = mp / 64, ttiles = tp / 64;
-  uint16_t *d = nullptr, *dt = nullptr, *wt = nullptr, *xt = nullptr;
-  float *rowpart = nullptr, *rowadd = nullptr, *biaspart = nullptr, *dW = nullptr, *part = nullptr;
+  D.t = A.t; D.m = L.m; D.n = L.n;
+  D.mp = mp; D.tp = tp;
+  D.rowtiles = mp / 64; D.xtiles = up64(L.n) / 64;
+  D.plane_d = A.t * mp; D.plane_t = L.m * tp; D.plane_x = L.n * tp;
+  const int64_t plane_w = L.n * mp, ttiles = tp / 64;
   QGemm gx, gw;
   memset(&gx, 0, sizeof(gx));
   memset(&gw, 0, sizeof(gw));
   q_pairs(gx, per, DX);
   q_pairs(gw, XP, DP);
   const bool sums = A.need_dx && !grouped && L.has_offset();
-  // rows of the layer whose dW is formed at a time
-  int64_t rows = std::max<int64_t>(256, Q_BLOCK_BYTES / (L.n * 4) / 256 * 256);
-  rows = std::min(rows, L.m);
-  const int64_t ldw = (L.n + 3) / 4 * 4;
+  D.dmax = W.take<uint32_t>((size_t)A.t * 4);
+  D.tmax = W.take<uint32_t>((size_t)L.m * 4);
+  D.xmax = W.take<uint32_t>((size_t)L.n * 4);
+  D.refs = W.take<uint32_t>((size_t)L.m * 4);
+  uint16_t* wt = nullptr;
+  float *rowadd = nullptr, *dW = nullptr, *part = nullptr;
+  float2* cpart = nullptr;
   size_t ps = 0;
+  // rows of the layer whose dW is formed at a time, where it is formed
+  const int64_t ldw = (L.n + 3) / 4 * 4, cblocks = (L.n + Q_CONTRACT - 1) / Q_CONTRACT;
+  int64_t rows = contract ? L.m : std::max<int64_t>(256, Q_BLOCK_BYTES / (L.n * 4) / 256 * 256);
+  rows = std::min(rows, L.m);
+  int splits = 1;
   if (A.need_dx) {
-    d = W.take<uint16_t>((size_t)DX * plane_d * 2);
+    D.d = W.take<uint16_t>((size_t)DX * D.plane_d * 2);
     wt = W.take<uint16_t>((size_t)per * plane_w * 2);
     // (sized without the offset's pointer: room for its sums either way)
-    rowpart = W.take<float>((size_t)A.t * rowtiles * 4);
+    D.rowpart = W.take<float>((size_t)A.t * D.rowtiles * 4);
     rowadd = W.take<float>((size_t)A.t * 4);
-    if (!sums) rowpart = rowadd = nullptr;
+    if (!sums) D.rowpart = rowadd = nullptr;
     ps = q_gemm_workspace(L.n, A.t, mp, gx.npairs);
   }
   if (A.need_dlayer) {
-    dt = W.take<uint16_t>((size_t)DP * plane_t * 2);
-    xt = W.take<uint16_t>((size_t)XP * plane_x * 2);
-    biaspart = W.take<float>((size_t)ttiles * L.m * 4);
-    dW = W.take<float>((size_t)rows * ldw * 4);
-    for (int64_t r0 = 0; r0 < L.m; r0 += rows)
-      ps = std::max(ps, q_gemm_workspace(L.n, std::min(rows, L.m - r0), tp, gw.npairs));
+    D.dt = W.take<uint16_t>((size_t)DP * D.plane_t * 2);
+    D.xt = W.take<uint16_t>((size_t)XP * D.plane_x * 2);
+    D.biaspart = W.take<float>((size_t)ttiles * L.m * 4);
+    if (contract) {
+      splits = q_gemm_splits(L.n, L.m, tp, gw.npairs);
+      cpart = W.take<float2>((size_t)splits * L.m * cblocks * sizeof(float2));
+    } else {
+      dW = W.take<float>((size_t)rows * ldw * 4);
+      for (int64_t r0 = 0; r0 < L.m; r0 += rows)
+        ps = std::max(ps, q_gemm_workspace(L.n, std::min(rows, L.m - r0), tp, gw.npairs));
+    }
   }
   part = W.take<float>(ps);
   if (bytes) *bytes = W.at;
   if (!base) return hipSuccess;
 
   hipError_t e;
-  DuArgs D;
-  memset(&D, 0, sizeof(D));
   D.dy = A.dy; D.lddy = A.lddy;
   D.pre = A.pre; D.ldpre = A.ldpre;
+  D.x = A.x; D.ldx = A.ldx;
   D.act = A.act; D.dtype = A.dtype;
-  D.t = A.t; D.m = L.m;
-  D.d = d; D.plane_d = plane_d; D.mp = mp; D.planes_d = DX;
-  D.mid = L.fmt == QF_NIB || L.fmt == QF_BYTE ? L.K / 2 : -1;
-  D.levels = L.levels;
-  if (A.need_dx && !grouped) {
-    D.scale = L.scale;
-    D.offset = L.offset;
-  }
-  D.rowpart = rowpart; D.rowtiles = rowtiles;
-  D.dt = dt; D.plane_t = plane_t; D.tp = tp; D.planes_t = DP;
-  D.biaspart = biaspart;
-  hipLaunchKernelGGL(q_du_kernel, dim3((unsigned)rowtiles, (unsigned)ttiles), dim3(256), 0, st, D);
+  D.vec_du = whole_quads(A.dy, A.lddy, A.dtype) && (A.act == ACT_NONE || whole_quads(A.pre, A.ldpre, A.dtype));
+  D.vec_x = whole_quads(A.x, A.ldx, A.dtype);
+  D.L = L;
+  D.want_d = A.need_dx;
+  D.want_t = A.need_dlayer;
+  D.planes_d = DX; D.planes_t = DP; D.planes_x = XP;
+  D.du_blocks = D.rowtiles * ttiles;
+  const int64_t x_blocks = A.need_dlayer ? D.xtiles * ttiles : 0;
+  const int64_t longest = std::max(std::max(A.t, L.m), L.n);
+  hipLaunchKernelGGL(q_grad_init_kernel,
+                     dim3((unsigned)std::min<int64_t>(2048, std::max((longest + 255) / 256, grouped ? (L.m + 3) / 4 : 0))),
+                     dim3(256), 0, st, D);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  const uintptr_t quad = A.dtype == DT_F32 ? 16 : 8;
+  hipLaunchKernelGGL(q_grad_scan_kernel, dim3((unsigned)(D.du_blocks + x_blocks)), dim3(256), 0, st, D);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  hipLaunchKernelGGL(q_grad_tile_kernel, dim3((unsigned)(D.du_blocks + x_blocks)), dim3(256), 0, st, D);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  if (A.need_dlayer || sums) {
+    const int64_t n = (A.need_dlayer ? (L.m + 255) / 256 * 256 : 0) + (sums ? A.t : 0);
+    hipLaunchKernelGGL(q_grad_sums_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, D, A.dbias, rowadd);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
   if (A.need_dx) {
-    if (sums) {
-      hipLaunchKernelGGL(q_sum_kernel, dim3((unsigned)((A.t + 255) / 256)), dim3(256), 0, st, rowpart, A.t, rowtiles,
-                         (int64_t)1, rowtiles, rowadd);
-      if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
-    if ((e = unpack_t(L, mp, WP, wt, plane_w, st)) != hipSuccess) return e;
+    if ((e = unpack_t(L, mp, WP, D.refs, wt, plane_w, st)) != hipSuccess) return e;
     gx.A = wt; gx.lda = mp; gx.planeA = plane_w;
-    gx.B = d; gx.ldb = mp; gx.planeB = plane_d;
+    gx.B = D.d; gx.ldb = mp; gx.planeB = D.plane_d;
     gx.M = L.n; gx.N = A.t; gx.K = mp;
     gx.O.y = A.dx; gx.O.ldy = A.lddx;
+    gx.O.rowmax = D.dmax;
     gx.O.rowadd = rowadd;
     gx.O.mid = -1;
     gx.O.dtype = A.dtype;
-    gx.O.vec = reinterpret_cast<uintptr_t>(A.dx) % quad == 0 && A.lddx % 4 == 0;
+    gx.O.vec = whole_quads(A.dx, A.lddx, A.dtype);
     gx.O.rows = A.t; gx.O.cols = L.n;
     if ((e = launch_q_gemm(gx, part, st)) != hipSuccess) return e;
   }
   if (A.need_dlayer) {
-    hipLaunchKernelGGL(q_transpose_kernel, dim3((unsigned)((L.n + 63) / 64), (unsigned)ttiles), dim3(256), 0, st, A.x,
-                       A.ldx, A.dtype, A.t, L.n, tp, XP, xt, plane_x);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    hipLaunchKernelGGL(q_sum_kernel, dim3((unsigned)((L.m + 255) / 256)), dim3(256), 0, st, biaspart, L.m, (int64_t)1,
-                       L.m, ttiles, A.dbias);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+    gw.A = D.xt; gw.lda = tp; gw.planeA = D.plane_x;
+    gw.ldb = tp; gw.planeB = D.plane_t;
+    gw.M = L.n; gw.K = tp;
+    gw.O.colmax = D.xmax;
+    gw.O.mid = -1;
+    gw.O.dtype = DT_F32;
+    gw.O.vec = 1;
+    gw.O.cols = L.n;
+    gw.O.ldy = ldw;
+    gw.L = L;
+    gw.cpart = cpart; gw.cblocks = cblocks;
     for (int64_t r0 = 0; r0 < L.m; r0 += rows) {
       const int64_t nr = std::min(rows, L.m - r0);
-      gw.A = xt; gw.lda = tp; gw.planeA = plane_x;
-      gw.B = dt + r0 * tp; gw.ldb = tp; gw.planeB = plane_t;
-      gw.M = L.n; gw.N = nr; gw.K = tp;
-      gw.O.y = dW; gw.O.ldy = ldw;
-      gw.O.mid = -1;
-      gw.O.dtype = DT_F32;
-      gw.O.vec = 1;
-      gw.O.rows = nr; gw.O.cols = L.n;
+      gw.B = D.dt + r0 * tp;
+      gw.N = gw.O.rows = nr;
+      gw.O.y = dW;
+      gw.O.rowmax = D.tmax + r0;
+      gw.row0 = r0;
       if ((e = launch_q_gemm(gw, part, st)) != hipSuccess) return e;
-      hipLaunchKernelGGL(q_affine_grad_kernel, dim3((unsigned)((nr * L.G + 3) / 4)), dim3(256), 0, st, L, dW, ldw, r0,
-                         nr, A.dscale, A.doffset);
+      if (contract)
+        hipLaunchKernelGGL(q_contract_finish_kernel, dim3((unsigned)((nr * L.G + 15) / 16)), dim3(256), 0, st, L, cpart,
+                           splits, nr, cblocks, r0, A.dscale, A.doffset);
+      else
+        hipLaunchKernelGGL(q_affine_grad_kernel, dim3((unsigned)((nr * L.G + 3) / 4)), dim3(256), 0, st, L, dW, ldw,
+                           r0, nr, A.dscale, A.doffset);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
   }

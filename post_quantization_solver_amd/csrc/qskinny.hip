@@ -4,7 +4,7 @@
 // (exact in 16 bits) and float32 sums, then u = a z + o' sum_j x_j: no weight is
 // ever formed, so none is rounded.  The sum over x rides along as one more
 // matrix product, with a row of ones in the layer's place.  float32 x enters as
-// three bfloat16 terms whose sum it is.
+// two float16 terms (22 bits) of x times a power of two per token.
 //
 // Split.  HBM traffic is the packed codes (2 bits a weight for E8); a wave's
 // matrix operand is what its lanes decode, sixteen rows at a time, so the
@@ -141,6 +141,7 @@ __global__ __launch_bounds__(64 * SK_WAVES) void q_skinny_kernel(SkinnyArgs A) {
         }
     }
     // Subtile (q, n) is added up, in the order of the waves, by wave (q NT + n).
+    float mine[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int q = 0; q < R; ++q)
 #pragma unroll
@@ -148,19 +149,23 @@ __global__ __launch_bounds__(64 * SK_WAVES) void q_skinny_kernel(SkinnyArgs A) {
         const int dst = q * NT + n;
         if (wave != dst) red[(wave < dst ? wave : wave - 1) * 64 + lane] = acc[q][n];
         __syncthreads();
-        if (wave == dst) {
-          float v[4] = {0.f, 0.f, 0.f, 0.f};
+        if (wave == dst)
           for (int w = 0; w < SK_WAVES; ++w) {
             const v4f p = w == dst ? acc[q][n] : red[(w < dst ? w : w - 1) * 64 + lane];
-            v[0] += p[0];
-            v[1] += p[1];
-            v[2] += p[2];
-            v[3] += p[3];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mine[k] += p[k];
           }
-          q_finish4(A.O, tok0 + n * 16 + r, (int64_t)(tg * R + q) * 16 + 4 * kb, v, true);
-        }
         __syncthreads();
       }
+    if (wave < R * NT) {
+      const int64_t tok = tok0 + wave % NT * 16 + r;
+      if (XP > 1 && tok < A.t) {
+        const float f = pow2(-pow2_shift(A.O.rowmax[tok]));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mine[k] *= f;
+      }
+      q_finish4(A.O, tok, (int64_t)(tg * R + wave / NT) * 16 + 4 * kb, mine, false);
+    }
   }
 }
 
@@ -206,7 +211,7 @@ hipError_t pick_format(const SkinnyArgs& A, hipStream_t st) {
 bool q_skinny_ok(const QLayer& L) { return L.G == 1 || L.group % q_chunk(L.fmt) == 0; }
 
 hipError_t launch_q_skinny(const QLayer& L, const uint16_t* x, int64_t ldx, int64_t planex, int kblocks, int64_t t,
-                           int planes, bool half, const QOut& O, hipStream_t st) {
+                           int planes, bool bf16, const QOut& O, hipStream_t st) {
   SkinnyArgs A;
   A.L = L;
   A.x = x;
@@ -217,8 +222,8 @@ hipError_t launch_q_skinny(const QLayer& L, const uint16_t* x, int64_t ldx, int6
   A.has_offset = L.has_offset();
   A.lut_words = (q_lut_words(L.fmt, L.lut_entries) + 3) / 4 * 4;
   A.O = O;
-  if (half) return pick_format<OpF16, 1>(A, st);
-  return planes == 3 ? pick_format<OpBf16, 3>(A, st) : pick_format<OpBf16, 1>(A, st);
+  if (bf16) return pick_format<OpBf16, 1>(A, st);
+  return planes == 2 ? pick_format<OpF16, 2>(A, st) : pick_format<OpF16, 1>(A, st);
 }
 
 }  // namespace mpq
