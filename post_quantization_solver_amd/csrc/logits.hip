@@ -21,6 +21,7 @@
 // indices of equal values, finds the k exactly.
 #include <math.h>
 #include <algorithm>
+#include <type_traits>
 #include "mpq_device.h"
 #include "internal.h"
 
@@ -32,7 +33,6 @@ constexpr int LG_THREADS = 256;
 constexpr int LG_WAVES = LG_THREADS / 64;
 constexpr int LG_NV = 8;        // 16-byte vectors per thread
 constexpr int LG_CAP = 2048;    // candidates in LDS
-constexpr int LG_MERGE = 4096;  // keys of a row's segments merged in LDS
 constexpr double LOG2E = 1.4426950408889634074;
 constexpr double LN2 = 0.69314718055994530942;
 
@@ -55,7 +55,9 @@ struct Fp16 {
   static constexpr int VEC = 8;
   static constexpr uint32_t NEG_INF = 0xfc00fc00u;
   typedef _Float16 h2 __attribute__((ext_vector_type(2)));
-  __device__ static float elem(const uint32_t* u, int e) { return (float)__builtin_bit_cast(h2, u[e >> 1])[e & 1]; }
+  __device__ static float elem(const uint32_t* u, int e) {
+    return (float)__builtin_bit_cast(_Float16, (uint16_t)(e & 1 ? u[e >> 1] >> 16 : u[e >> 1]));
+  }
   __device__ static float load(const void* p, int64_t i) { return (float)static_cast<const _Float16*>(p)[i]; }
   __device__ static void store(void* p, int64_t i, float x) { static_cast<_Float16*>(p)[i] = (_Float16)x; }
   __device__ static uint32_t pack(float x, float y) {
@@ -102,6 +104,22 @@ __device__ __forceinline__ void load_vec(const void* row, int64_t i, int64_t end
   }
 }
 
+// Elements i .. of a row, as 16 bytes (or, at its end, one by one).
+template <typename T>
+__device__ __forceinline__ void store_vec(char* row, int64_t i, int64_t end, const float* g) {
+  if (i + T::VEC <= end) {
+    Raw16 r;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      r.u[q] = T::VEC == 8 ? T::pack(g[(2 * q) % T::VEC], g[(2 * q + 1) % T::VEC]) : T::pack(g[q % T::VEC], 0.f);
+    *reinterpret_cast<Raw16*>(row + i * (16 / T::VEC)) = r;
+  } else {
+#pragma unroll
+    for (int e = 0; e < T::VEC; ++e)
+      if (i + e < end) T::store(row, i + e, g[e]);
+  }
+}
+
 __device__ __forceinline__ float wave_max(float v) {
   for (int o = 32; o; o >>= 1) v = fmaxf(v, shfl_xor_f(v, o));
   return v;
@@ -113,6 +131,32 @@ __device__ __forceinline__ double wave_sum(double v) {
 __device__ __forceinline__ int wave_sum_i(int v) {
   for (int o = 32; o; o >>= 1) v += shfl_xor_i(v, o);
   return v;
+}
+
+// max(a, b, c) without the canonicalisation of fmaxf's operands (a NaN among
+// them may be dropped or win: the sums are NaN either way).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ float vec_max(const uint32_t* u) {
+  float m = max3(T::elem(u, 0), T::elem(u, 1), T::elem(u, 2));
+  if constexpr (T::VEC == 4) return max3(m, T::elem(u, 3), T::elem(u, 3));
+  m = max3(m, T::elem(u, 3), T::elem(u, 4));
+  m = max3(m, T::elem(u, 5), T::elem(u, 6));
+  return max3(m, T::elem(u, 7), T::elem(u, 7));
+}
+
+// Keeps the compiler from carrying unpacked elements from one pass over the
+// registers to the next (they would take twice the registers the raw words do).
+template <int NV>
+__device__ __forceinline__ void forget(uint32_t (&u)[NV][4]) {
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) asm volatile("" : "+v"(u[j][q]));
 }
 
 // Order of floats as unsigned integers; -0 equals +0 (the caller adds +0).
@@ -149,12 +193,66 @@ struct Part {
   float m, pad;     // the maximum
 };
 
+// A thread's sums over its vectors.  SAFE = false: y = c z - M by one fma, M =
+// fl(c m); the caller takes the common c m - M out again.  It needs |M| well
+// below 2^23; SAFE = true takes m off first, one more instruction an element.
+// (The 0 of a logit of -inf must not be multiplied by its y.)
+// MODE 0: s and w; 1: s and rest (bit e of listed(j): element e of vector j is
+// listed); 2: s alone.
+template <typename T, int NV, bool SAFE, int MODE, typename F>
+__device__ __forceinline__ void thread_sums(const uint32_t (&u)[NV][4], int nv, float c, float m, F&& listed,
+                                            double& s, double& w) {
+  const float M = m * c;
+  s = w = 0.0;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    if (j >= nv) continue;   // (the same for every thread)
+    float e[T::VEC], wv = 0.f;
+#pragma unroll
+    for (int q = 0; q < T::VEC; ++q) {
+      const float x = T::elem(u[j], q);
+      const float y = SAFE ? (x - m) * c : fmaf(x, c, -M);
+      e[q] = __builtin_amdgcn_exp2f(y);
+      if (MODE == 0) wv = fmaf(e[q], fmaxf(y, -1e30f), wv);
+    }
+    if (MODE == 1) {
+      const uint32_t b = listed(j);
+      if (b) {   // rare
+        float f[T::VEC];
+#pragma unroll
+        for (int q = 0; q < T::VEC; ++q) f[q] = b >> q & 1u ? 0.f : e[q];
+#pragma unroll
+        for (int o = T::VEC / 2; o; o >>= 1)
+#pragma unroll
+          for (int q = 0; q < o; ++q) f[q] += f[q + o];
+        wv = f[0];
+      }
+#pragma unroll
+      for (int o = T::VEC / 2; o; o >>= 1)
+#pragma unroll
+        for (int q = 0; q < o; ++q) e[q] += e[q + o];
+      if (!b) wv = e[0];
+    } else {
+#pragma unroll
+      for (int o = T::VEC / 2; o; o >>= 1)
+#pragma unroll
+        for (int q = 0; q < o; ++q) e[q] += e[q + o];
+    }
+    s += (double)e[0];
+    if (MODE != 2) w += (double)wv;
+    __builtin_amdgcn_sched_barrier(0);   // one vector's elements unpacked at a time
+  }
+}
+// Whether the fma form's M resolves y.
+__device__ __forceinline__ bool plain_scale(float m, float c) { return fabsf(m * c) < 0x1p20f; }
+
 struct Shared {
-  uint64_t key[LG_CAP];
-  double d[3][LG_WAVES];
+  alignas(16) uint64_t key[LG_CAP];   // LG_CAP is a multiple of 8
+  double d[2][LG_WAVES];
   float f[LG_WAVES];
   int i[LG_WAVES];
-  int cnt;
+  int cnt, nvec;
+  uint16_t vec[LG_NV * LG_THREADS];
 };
 
 __device__ __forceinline__ int block_count(int n, Shared& sh) {
@@ -168,16 +266,16 @@ __device__ __forceinline__ int block_count(int n, Shared& sh) {
   return a;
 }
 
-// The k largest (value, then lowest index) of this segment's registers, ranked,
-// into list[0..k); unused places hold 0.
+// The k largest (value, then lowest index) of this segment, ranked, into
+// list[0..k); unused places hold 0.  vm, tmax: the maxima of the thread's vectors.
 template <typename T>
-__device__ void segment_top(const uint32_t (&u)[LG_NV][4], float tmax, const char* z, int64_t base, int64_t end, int k,
-                            Shared& sh, uint64_t* __restrict__ list) {
+__device__ void segment_top(const float (&vm)[LG_NV], int nv, float tmax, const char* z, int64_t base, int64_t end,
+                            int k, Shared& sh, uint64_t* __restrict__ list) {
   const int t = threadIdx.x, wave = wave_id();
   const float sorted = wave_sort_desc(tmax);
   const int act = __popcll(__ballot(tmax > -INFINITY));
   if ((t & 63) == 0) sh.i[wave] = act;
-  if (t == 0) sh.cnt = 0;
+  if (t == 0) sh.cnt = sh.nvec = 0;
   __syncthreads();
   int A = 0;
 #pragma unroll
@@ -192,19 +290,25 @@ __device__ void segment_top(const uint32_t (&u)[LG_NV][4], float tmax, const cha
 #pragma unroll
     for (int w = 1; w < LG_WAVES; ++w) bound = fminf(bound, sh.f[w]);
   }
+  // the few vectors that hold such an element first, then their elements, a
+  // thread each (re-read: they are in the cache)
 #pragma unroll
   for (int j = 0; j < LG_NV; ++j) {
-    float m = T::elem(u[j], 0);
+    if (j >= nv) break;
+    if (vm[j] >= bound) sh.vec[atomicAdd(&sh.nvec, 1)] = (uint16_t)(j * LG_THREADS + t);
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int i = t; i < sh.nvec; i += LG_THREADS) {
+    const int64_t at0 = base + (int64_t)sh.vec[i] * T::VEC;
+    uint32_t w[4];
+    load_vec<T>(z, at0, end, w);
 #pragma unroll
-    for (int e = 1; e < T::VEC; ++e) m = fmaxf(m, T::elem(u[j], e));
-    if (m >= bound) {
-#pragma unroll
-      for (int e = 0; e < T::VEC; ++e) {
-        const float x = T::elem(u[j], e);
-        if (x >= bound && x > -INFINITY) {
-          const int at = atomicAdd(&sh.cnt, 1);
-          if (at < LG_CAP) sh.key[at] = top_key(x, base + (int64_t)(j * LG_THREADS + t) * T::VEC + e);
-        }
+    for (int e = 0; e < T::VEC; ++e) {
+      const float x = T::elem(w, e);
+      if (x >= bound && x > -INFINITY) {
+        const int at = atomicAdd(&sh.cnt, 1);
+        if (at < LG_CAP) sh.key[at] = top_key(x, at0 + e);
       }
     }
   }
@@ -248,10 +352,19 @@ __device__ void segment_top(const uint32_t (&u)[LG_NV][4], float tmax, const cha
     __syncthreads();
     N = min(sh.cnt, LG_CAP);   // k, or more where the row holds +inf (its list is not reported)
   }
+  // ranks by counting, eight keys to a round (zeros fill the last)
+  if (t < 8 && N + t < LG_CAP) sh.key[N + t] = 0;
+  __syncthreads();
   for (int i = t; i < N; i += LG_THREADS) {
     const uint64_t key = sh.key[i];
     int rank = 0;
-    for (int j = 0; j < N; ++j) rank += sh.key[j] > key ? 1 : 0;
+    for (int j = 0; j < N; j += 8) {
+      ulonglong2 q[4];
+#pragma unroll
+      for (int h = 0; h < 4; ++h) q[h] = reinterpret_cast<const ulonglong2*>(sh.key + j)[h];
+#pragma unroll
+      for (int h = 0; h < 4; ++h) rank += (q[h].x > key ? 1 : 0) + (q[h].y > key ? 1 : 0);
+    }
     if (rank < k) list[rank] = key;
   }
   for (int i = N + t; i < k; i += LG_THREADS) list[i] = 0;
@@ -271,8 +384,10 @@ __global__ __launch_bounds__(LG_THREADS) void logit_part_kernel(LogitArgs A, Par
   const int64_t base = (int64_t)seg * A.L, end = min(A.V, base + A.L);
   const char* z = static_cast<const char*>(A.z) + row * A.ldz * (16 / T::VEC);
   uint32_t u[LG_NV][4];
+  const int nv = (int)((end - base + LG_THREADS * T::VEC - 1) / (LG_THREADS * T::VEC));
 #pragma unroll
-  for (int j = 0; j < LG_NV; ++j) load_vec<T>(z, base + (int64_t)(j * LG_THREADS + t) * T::VEC, end, u[j]);
+  for (int j = 0; j < LG_NV; ++j)
+    if (j < nv) load_vec<T>(z, base + (int64_t)(j * LG_THREADS + t) * T::VEC, end, u[j]);
   // distillation: the listed logits, kept for the second kernel (which may
   // write the gradient over the logits)
   for (int i = t; i < A.k; i += LG_THREADS) {
@@ -291,11 +406,13 @@ __global__ __launch_bounds__(LG_THREADS) void logit_part_kernel(LogitArgs A, Par
       }
     }
   }
-  float tmax = -INFINITY;
+  float vm[LG_NV], tmax = -INFINITY;
 #pragma unroll
-  for (int j = 0; j < LG_NV; ++j)
-#pragma unroll
-    for (int e = 0; e < T::VEC; ++e) tmax = fmaxf(tmax, T::elem(u[j], e));
+  for (int j = 0; j < LG_NV; ++j) {
+    vm[j] = -INFINITY;
+    if (j < nv) vm[j] = vec_max<T>(u[j]);
+    tmax = max3(tmax, vm[j], vm[j]);
+  }
   float m = wave_max(tmax);
   if ((t & 63) == 0) sh.f[wave] = m;
   __syncthreads();
@@ -303,88 +420,113 @@ __global__ __launch_bounds__(LG_THREADS) void logit_part_kernel(LogitArgs A, Par
 #pragma unroll
   for (int w = 1; w < LG_WAVES; ++w) m = fmaxf(m, sh.f[w]);
   if (m == -INFINITY) m = 0.f;
-  double s = 0.0, w = 0.0, rest = 0.0;
-#pragma unroll
-  for (int j = 0; j < LG_NV; ++j) {
-    float es[T::VEC], ew[T::VEC];
-    float y[T::VEC];
-#pragma unroll
-    for (int e = 0; e < T::VEC; ++e) {
-      y[e] = (T::elem(u[j], e) - m) * A.c;
-      es[e] = __builtin_amdgcn_exp2f(y[e]);
-      ew[e] = es[e] * fmaxf(y[e], -1e30f);   // 0, not NaN, at -inf
+  constexpr int MODE = TAIL ? 1 : 0;
+  auto flags = [&](int j) -> uint32_t { return listed[j * LG_THREADS + t]; };
+  double s, w;
+  auto block_sums = [&]() {
+    s = wave_sum(s);
+    w = wave_sum(w);
+    __syncthreads();
+    if ((t & 63) == 0) {
+      sh.d[0][wave] = s;
+      sh.d[1][wave] = w;
     }
-    if (TAIL) {
-      const uint32_t b = listed[j * LG_THREADS + t];
-#pragma unroll
-      for (int e = 0; e < T::VEC; ++e) ew[e] = b >> e & 1u ? 0.f : es[e];
+    __syncthreads();
+    s = w = 0.0;
+    for (int i = 0; i < LG_WAVES; ++i) {
+      s += sh.d[0][i];
+      w += sh.d[1][i];
     }
-#pragma unroll
-    for (int o = T::VEC / 2; o; o >>= 1)
-#pragma unroll
-      for (int e = 0; e < o; ++e) {
-        es[e] += es[e + o];
-        ew[e] += ew[e + o];
-      }
-    s += (double)es[0];
-    if (TAIL) rest += (double)ew[0]; else w += (double)ew[0];
-  }
-  s = wave_sum(s);
-  w = wave_sum(TAIL ? rest : w);
-  if ((t & 63) == 0) {
-    sh.d[0][wave] = s;
-    sh.d[1][wave] = w;
-  }
-  __syncthreads();
+  };
+  const bool fast = plain_scale(m, A.c);
+  forget(u);
+  if (fast) thread_sums<T, LG_NV, false, MODE>(u, nv, A.c, m, flags, s, w);
+  else thread_sums<T, LG_NV, true, MODE>(u, nv, A.c, m, flags, s, w);
+  block_sums();
   if (t == 0) {
     Part p;
-    p.s = p.w = 0.0;
-    for (int i = 0; i < LG_WAVES; ++i) {
-      p.s += sh.d[0][i];
-      p.w += sh.d[1][i];
-    }
-    p.rest = p.w;
+    const double d = fast ? (double)(m * A.c) - (double)m * (double)A.c : 0.0, f = exp2(d);
+    p.s = s * f;
+    p.w = TAIL ? 0.0 : f * (w + d * s);
+    p.rest = w * f;
     p.m = m;
     p.pad = 0.f;
     parts[row * A.S + seg] = p;
   }
-  if (!TAIL && A.top > 0) segment_top<T>(u, tmax, z, base, end, A.top, sh, lists + (row * A.S + seg) * A.top);
+  if (!TAIL && A.top > 0) segment_top<T>(vm, nv, tmax, z, base, end, A.top, sh, lists + (row * A.S + seg) * A.top);
 }
 
-// Joins a row's segments: every lane returns the row's (s, w, rest) at the
-// common m.
+// Joins a row's segments, a lane each: every lane returns the row's (s, w,
+// rest) at the common m.
 struct RowStat {
   double s, w, rest;
   float m;
 };
 __device__ RowStat join_parts(const Part* __restrict__ p, int S, float c) {
   RowStat r;
+  const int lane = threadIdx.x & 63;
   float m = -INFINITY;
-  for (int i = 0; i < S; ++i)
+  for (int i = lane; i < S; i += 64)
     if (!(p[i].s == 0.0)) m = fmaxf(m, p[i].m);   // NaN sums take part
+  m = wave_max(m);
   r.m = m == -INFINITY ? 0.f : m;
   r.s = r.w = r.rest = 0.0;
-  for (int i = 0; i < S; ++i) {
-    if (p[i].s == 0.0) continue;
-    const double d = ((double)p[i].m - (double)r.m) * (double)c, f = exp2(d);
-    r.s += f * p[i].s;
-    r.w += f * (p[i].w + d * p[i].s);
-    r.rest += f * p[i].rest;
+  for (int i = lane; i < S; i += 64) {
+    const Part q = p[i];
+    if (q.s == 0.0) continue;
+    const double d = ((double)q.m - (double)r.m) * (double)c, f = exp2(d);
+    r.s += f * q.s;
+    r.w += f * (q.w + d * q.s);
+    r.rest += f * q.rest;
   }
+  r.s = wave_sum(r.s);
+  r.w = wave_sum(r.w);
+  r.rest = wave_sum(r.rest);
   return r;
 }
 
-// Entries of a descending list above key.
-__device__ __forceinline__ int count_above(const uint64_t* list, int k, uint64_t key) {
-  int lo = 0, hi = k;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (list[mid] > key) lo = mid + 1; else hi = mid;
-  }
-  return lo;
+__device__ __forceinline__ uint64_t shfl_key(uint64_t v, int src) {
+  return (uint64_t)shfl_i((uint32_t)(v >> 32), src) << 32 | shfl_i((uint32_t)v, src);
 }
 
-template <typename T>
+// A descending list of up to 64 R keys, entry 64 r + lane in register r.
+template <int R>
+struct TopList {
+  uint64_t v[R];
+  __device__ void load(const uint64_t* list, int k) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int i = 64 * r + (int)(threadIdx.x & 63);
+      v[r] = i < k ? list[i] : 0;
+    }
+  }
+  // The largest of this list and another: entry i against entry 64 R - 1 - i
+  // leaves them as a bitonic sequence, which log2(64 R) exchanges sort.
+  __device__ void merge(const TopList& o) {
+    const int lane = threadIdx.x & 63;
+    uint64_t b[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) b[r] = shfl_key(o.v[R - 1 - r], 63 - lane);
+#pragma unroll
+    for (int r = 0; r < R; ++r) v[r] = max(v[r], b[r]);
+    if constexpr (R == 2) {
+      const uint64_t hi = max(v[0], v[1]), lo = min(v[0], v[1]);
+      v[0] = hi;
+      v[1] = lo;
+    }
+#pragma unroll
+    for (int d = 32; d; d >>= 1)
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const uint64_t w = shfl_key(v[r], lane ^ d);
+        v[r] = lane & d ? min(v[r], w) : max(v[r], w);
+      }
+  }
+};
+
+// One row: its segments' statistics joined (wave 0) and their lists merged, the
+// waves each a share of them, then wave 0 the waves'.
+template <typename T, int R>
 __global__ __launch_bounds__(LG_THREADS) void logprob_row_kernel(LogitArgs A, const Part* __restrict__ parts,
                                                                  const uint64_t* __restrict__ lists,
                                                                  const int32_t* __restrict__ tokens,
@@ -392,22 +534,46 @@ __global__ __launch_bounds__(LG_THREADS) void logprob_row_kernel(LogitArgs A, co
                                                                  float* __restrict__ entropy, float* __restrict__ lse_out,
                                                                  int32_t* __restrict__ top_ids,
                                                                  float* __restrict__ top_lp) {
-  __shared__ uint64_t keys[LG_MERGE];
+  __shared__ uint64_t keys[LG_WAVES][64 * R];
   const int64_t row = blockIdx.x;
-  const int t = threadIdx.x, k = A.top, S = A.S;
+  const int lane = threadIdx.x & 63, wave = wave_id(), waves = blockDim.x / 64;
+  const int k = A.top, S = A.S;
+  TopList<R> top;
+  if (k > 0) {
+    const uint64_t* list = lists + row * S * k;
+    top.load(list + (int64_t)min(wave, S - 1) * k, wave < S ? k : 0);
+    for (int g = wave + waves; g < S; g += waves) {
+      TopList<R> o;
+      o.load(list + (int64_t)g * k, k);
+      top.merge(o);
+    }
+    if (waves > 1) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) keys[wave][64 * r + lane] = top.v[r];
+      __syncthreads();
+      if (wave == 0)
+        for (int w = 1; w < min(waves, S); ++w) {
+          TopList<R> o;
+          o.load(keys[w], 64 * R);
+          top.merge(o);
+        }
+    }
+  }
+  if (wave > 0) return;
   const RowStat r = join_parts(parts + row * S, S, A.c);
-  const bool bad = !(r.s >= 0.0);   // a NaN or +inf logit
+  const bool bad = !(r.s < INFINITY);   // a NaN or +inf logit
   // Log probabilities are taken of the logits as scaled by c; lse alone is
   // corrected for c's rounding: d lse / d scale is the mean logit.
   const double lg = log2(r.s);
-  const double lse = bad ? (double)NAN
-                     : r.s > 0.0 ? (double)r.m + lg * LN2 + (1.0 - (double)A.c * LN2) * (r.w / r.s / (double)A.c)
-                                 : -(double)INFINITY;
   auto lp_of = [&](float x) {
     return bad ? NAN : x == -INFINITY ? -INFINITY : (float)((((double)x - (double)r.m) * (double)A.c - lg) * LN2);
   };
-  if (t == 0) {
-    if (lse_out) lse_out[row] = (float)lse;
+  if (lane == 0) {
+    if (lse_out)
+      lse_out[row] = bad         ? NAN
+                     : r.s > 0.0 ? (float)((double)r.m + lg * LN2 +
+                                           (1.0 - (double)A.c * LN2) * (r.w / r.s / (double)A.c))
+                                 : -INFINITY;
     if (entropy) entropy[row] = bad ? NAN : r.s > 0.0 ? (float)(LN2 * (lg - r.w / r.s)) : 0.f;
     if (logprob) {
       const int32_t tok = tokens[row];
@@ -419,34 +585,14 @@ __global__ __launch_bounds__(LG_THREADS) void logprob_row_kernel(LogitArgs A, co
       logprob[row] = v;
     }
   }
-  if (k == 0) return;
-  const uint64_t* list = lists + row * S * k;
-  if (S * k <= LG_MERGE) {
-    for (int i = t; i < S * k; i += LG_THREADS) keys[i] = list[i];
-    __syncthreads();
-    list = keys;
+#pragma unroll
+  for (int q = 0; q < R; ++q) {
+    const int i = 64 * q + lane;
+    if (i >= k) continue;
+    const uint64_t key = top.v[q];
+    if (top_ids) top_ids[row * k + i] = bad || !key ? -1 : (int32_t)~(uint32_t)key;
+    if (top_lp) top_lp[row * k + i] = lp_of(key ? unord((uint32_t)(key >> 32)) : -INFINITY);
   }
-  auto put = [&](int rank, uint64_t key) {
-    const int64_t at = row * k + rank;
-    if (top_ids) top_ids[at] = bad || !key ? -1 : (int32_t)~(uint32_t)key;
-    if (top_lp) top_lp[at] = lp_of(key ? unord((uint32_t)(key >> 32)) : -INFINITY);
-  };
-  if (S == 1) {
-    for (int i = t; i < k; i += LG_THREADS) put(i, list[i]);
-    return;
-  }
-  int have = 0;
-  for (int g = 0; g < S; ++g) have += count_above(list + g * k, k, 0);
-  for (int i = t; i < S * k; i += LG_THREADS) {
-    const uint64_t key = list[i];
-    if (!key) continue;
-    const int g = i / k;
-    int rank = i - g * k;
-    for (int o = 0; o < S && rank < k; ++o)
-      if (o != g) rank += count_above(list + o * k, k, key);
-    if (rank < k) put(rank, key);
-  }
-  for (int i = have + t; i < k; i += LG_THREADS) put(i, 0);
 }
 
 // Distillation, one segment of one row: every workgroup joins the row's
@@ -470,24 +616,11 @@ __global__ __launch_bounds__(LG_THREADS) void distill_grad_kernel(LogitArgs A, c
   const int64_t base = (int64_t)seg * A.L, end = min(A.V, base + A.L);
   const char* z = static_cast<const char*>(A.z) + row * A.ldz * (16 / T::VEC);
   char* gr = grad ? static_cast<char*>(grad) + row * ldg * (16 / T::VEC) : nullptr;
-  auto store_vec = [&](int64_t i, const float* g) {
-    if (i + T::VEC <= end) {
-      Raw16 r;
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        r.u[q] = T::VEC == 8 ? T::pack(g[(2 * q) % T::VEC], g[(2 * q + 1) % T::VEC]) : T::pack(g[q % T::VEC], 0.f);
-      *reinterpret_cast<Raw16*>(gr + i * (16 / T::VEC)) = r;
-    } else {
-#pragma unroll
-      for (int e = 0; e < T::VEC; ++e)
-        if (i + e < end) T::store(gr, i + e, g[e]);
-    }
-  };
   if (wt == 0.f) {
     if (seg == 0 && t == 0) loss[row] = 0.f;
     if (!gr) return;
     const float zero[T::VEC] = {};
-    for (int64_t i = base + (int64_t)t * T::VEC; i < end; i += LG_THREADS * T::VEC) store_vec(i, zero);
+    for (int64_t i = base + (int64_t)t * T::VEC; i < end; i += LG_THREADS * T::VEC) store_vec<T>(gr, i, end, zero);
     return;
   }
   const RowStat r = join_parts(parts + row * A.S, A.S, A.c);
@@ -580,10 +713,214 @@ __global__ __launch_bounds__(LG_THREADS) void distill_grad_kernel(LogitArgs A, c
     float g[T::VEC];
 #pragma unroll
     for (int e = 0; e < T::VEC; ++e) g[e] = __builtin_amdgcn_exp2f((T::elem(u, e) - m) * A.c) * f;
-    store_vec(i, g);
+    store_vec<T>(gr, i, end, g);
   }
   __syncthreads();
   if (first && id >= base && id < end) T::store(gr, id, glist);
+}
+
+// Distillation, a whole row in one workgroup's registers: read once, written
+// once.  The row's last V % VEC elements, which fill no vector, are a thread's
+// each.  Wave 0 takes the teacher's list (two entries a lane).
+template <typename T, int THREADS, int NV, bool TAIL>
+__global__ __launch_bounds__(THREADS) void distill_row_kernel(LogitArgs A, const float* __restrict__ teacher,
+                                                              double invT, float* __restrict__ loss,
+                                                              void* __restrict__ grad, int64_t ldg) {
+  constexpr int WAVES = THREADS / 64;
+  __shared__ __attribute__((aligned(16))) uint8_t listed[NV * THREADS];   // bit e of byte v: element e of vector v
+  __shared__ double rs[WAVES], rw[WAVES];
+  __shared__ float rm[WAVES];
+  __shared__ int32_t sid[LOGIT_MAX_TOP];
+  __shared__ float sp[LOGIT_MAX_TOP];
+  __shared__ double s_pt;
+  __shared__ int s_twice;
+  const int t = threadIdx.x, lane = t & 63, wave = wave_id();
+  const int64_t row = blockIdx.x;
+  const float wt = A.weights ? A.weights[row] : 1.f;
+  const char* z = static_cast<const char*>(A.z) + row * A.ldz * (16 / T::VEC);
+  char* gr = grad ? static_cast<char*>(grad) + row * ldg * (16 / T::VEC) : nullptr;
+  const int full = (int)(A.V / T::VEC), odd = (int)(A.V % T::VEC), nv = (full + THREADS - 1) / THREADS;
+  if (wt == 0.f) {
+    if (t == 0) loss[row] = 0.f;
+    if (!gr) return;
+    const float zero[T::VEC] = {};
+    for (int64_t i = (int64_t)t * T::VEC; i < A.V; i += THREADS * T::VEC) store_vec<T>(gr, i, A.V, zero);
+    return;
+  }
+  uint32_t u[NV][4];
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+    if (j < nv) {
+      const int v = j * THREADS + t;
+      if (v < full) {
+        const Raw16 w = reinterpret_cast<const Raw16*>(z)[v];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) u[j][q] = w.u[q];
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) u[j][q] = T::NEG_INF;
+      }
+    }
+  const float last = t < odd ? T::load(z, (int64_t)full * T::VEC + t) : -INFINITY;
+  for (int i = t; i < NV * THREADS / 16; i += THREADS) reinterpret_cast<uint4*>(listed)[i] = make_uint4(0, 0, 0, 0);
+  if (t == 0) s_twice = 0;
+  __syncthreads();
+  // wave 0: entries lane and lane + 64 of the list (id -1: none)
+  int32_t id[2] = {-1, -1};
+  float zi[2] = {0.f, 0.f};
+  double p[2] = {0.0, 0.0}, lp[2] = {0.0, 0.0}, ps = 0.0;
+  int named = 0;
+  if (wave == 0) {
+    float mx = -INFINITY;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int i = 64 * q + lane;
+      if (i < A.k) {
+        id[q] = A.ids[row * A.k + i];
+        if (id[q] < 0 || id[q] >= A.V) id[q] = -1;
+        lp[q] = (double)teacher[row * A.k + i] * invT;
+        if (!TAIL && lp[q] == -INFINITY) id[q] = -1;   // no mass: as if not listed
+      }
+      if (id[q] >= 0) {
+        zi[q] = T::load(z, id[q]);
+        mx = fmaxf(mx, (float)lp[q]);
+        const int v = id[q] / T::VEC, e = id[q] % T::VEC;
+        const uint32_t bit = 1u << (8 * (v & 3) + e);
+        if (atomicOr(reinterpret_cast<uint32_t*>(listed) + (v >> 2), bit) & bit) s_twice = 1;
+        else ++named;
+      }
+    }
+    if (TAIL) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) p[q] = id[q] >= 0 ? exp(lp[q]) : 0.0;
+      ps = wave_sum(p[0] + p[1]);
+    } else {
+      mx = wave_max(mx);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) p[q] = id[q] >= 0 ? exp(lp[q] - (double)mx) : 0.0;
+      ps = wave_sum(p[0] + p[1]);
+      if (ps > 0.0 || ps != ps) {
+        const double l = log(ps), inv = 1.0 / ps;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          p[q] *= inv;
+          lp[q] -= (double)mx + l;
+        }
+        ps = 1.0;
+      }
+    }
+    named = wave_sum_i(named);
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      if (64 * q + lane < LOGIT_MAX_TOP) {
+        sid[64 * q + lane] = id[q];
+        sp[64 * q + lane] = (float)p[q];
+      }
+    if (lane == 0) {
+      // tail: the remainder (below 2^-20 it is the rounding of k float32 log
+      // probabilities; a list that names every token has none); else whether
+      // the list teaches anything
+      double pt = ps;
+      if (TAIL) {
+        pt = 1.0 - ps;
+        if (pt < 0x1p-20 || named >= A.V) pt = 0.0;
+      }
+      s_pt = pt;
+    }
+  }
+  float m = last;
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+    if (j < nv) {
+      const float v = vec_max<T>(u[j]);
+      m = max3(m, v, v);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  m = wave_max(m);
+  if (lane == 0) rm[wave] = m;
+  __syncthreads();
+  m = rm[0];
+#pragma unroll
+  for (int w = 1; w < WAVES; ++w) m = fmaxf(m, rm[w]);
+  if (m == -INFINITY) m = 0.f;
+  auto flags = [&](int j) -> uint32_t { return listed[j * THREADS + t]; };
+  constexpr int MODE = TAIL ? 1 : 2;
+  const bool fast = plain_scale(m, A.c);
+  double s, rest;
+  forget(u);
+  if (fast) thread_sums<T, NV, false, MODE>(u, nv, A.c, m, flags, s, rest);
+  else thread_sums<T, NV, true, MODE>(u, nv, A.c, m, flags, s, rest);
+  const float M = m * A.c;
+  auto two_to = [&](float x) { return __builtin_amdgcn_exp2f(fast ? fmaf(x, A.c, -M) : (x - m) * A.c); };
+  const float elast = two_to(last);
+  s += (double)elast;
+  if (TAIL && t < odd && !(listed[full] >> t & 1u)) rest += (double)elast;
+  s = wave_sum(s);
+  if (TAIL) rest = wave_sum(rest);
+  if (lane == 0) {
+    rs[wave] = s;
+    rw[wave] = rest;
+  }
+  __syncthreads();
+  s = rest = 0.0;
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) {
+    s += rs[w];
+    rest += rw[w];
+  }
+  // 2^y / s is q whatever M was rounded to: the sums carry the same factor
+  const double pt = s_pt, g0 = (double)wt * invT;
+  const double coef = TAIL ? (pt > 0.0 ? 1.0 - pt * s / rest : 1.0) : (pt != 0.0 ? 1.0 : 0.0);
+  const float f = (float)(coef * g0 / s);
+  if (gr) {
+    forget(u);
+    auto put = [&](auto safe) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (j < nv) {
+          float g[T::VEC];
+#pragma unroll
+          for (int e = 0; e < T::VEC; ++e) {
+            const float x = T::elem(u[j], e);
+            g[e] = __builtin_amdgcn_exp2f(safe.value ? (x - m) * A.c : fmaf(x, A.c, -M)) * f;
+          }
+          Raw16 w;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            w.u[q] = T::VEC == 8 ? T::pack(g[(2 * q) % T::VEC], g[(2 * q + 1) % T::VEC]) : T::pack(g[q % T::VEC], 0.f);
+          if (j * THREADS + t < full) reinterpret_cast<Raw16*>(gr)[j * THREADS + t] = w;
+          __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    if (fast) put(std::false_type{}); else put(std::true_type{});
+    if (t < odd) T::store(gr, (int64_t)full * T::VEC + t, elast * f);
+  }
+  __syncthreads();
+  if (wave != 0) return;
+  // the listed entries' gradients, over what was written there; the loss
+  const double lg = log2(s);
+  double kl = 0.0;
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    if (id[q] < 0) continue;
+    const double y = fast ? (double)zi[q] * (double)A.c - (double)M : ((double)zi[q] - (double)m) * (double)A.c;
+    if (p[q] != 0.0) kl += p[q] * (lp[q] - (y - lg) * LN2);
+    bool first = true;
+    float own = (float)p[q];
+    if (s_twice) {   // a token named twice has the sum, and one writer
+      own = 0.f;
+      for (int i = 0; i < A.k; ++i)
+        if (sid[i] == id[q]) {
+          own += sp[i];
+          if (i < 64 * q + lane) first = false;
+        }
+    }
+    const float e = two_to(zi[q]);
+    if (gr && first) T::store(gr, id[q], (e * (float)(1.0 / s) - own) * (float)g0);
+  }
+  kl = wave_sum(kl);
+  if (TAIL && pt > 0.0) kl += pt * (log(pt) - log(rest / s));
+  if (lane == 0) loss[row] = (float)((double)wt * kl);
 }
 
 }  // namespace
@@ -624,8 +961,15 @@ hipError_t launch_token_logprobs(const LogitArgs& A, const int32_t* tokens, floa
                                           static_cast<float*>(nullptr)));
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  LOGIT_TYPES(A.dtype, hipLaunchKernelGGL((logprob_row_kernel<T>), dim3((unsigned)A.t), block, 0, st, A, parts, lists,
-                                          tokens, logprob, entropy, lse, top_ids, top_lp));
+  // one wave per row where there is little to merge
+  const dim3 rows((unsigned)A.t), waves(A.S > 2 && A.top > 0 ? LG_THREADS : 64);
+  if (A.top <= 64) {
+    LOGIT_TYPES(A.dtype, hipLaunchKernelGGL((logprob_row_kernel<T, 1>), rows, waves, 0, st, A, parts, lists, tokens,
+                                            logprob, entropy, lse, top_ids, top_lp));
+  } else {
+    LOGIT_TYPES(A.dtype, hipLaunchKernelGGL((logprob_row_kernel<T, 2>), rows, waves, 0, st, A, parts, lists, tokens,
+                                            logprob, entropy, lse, top_ids, top_lp));
+  }
   return hipGetLastError();
 }
 
@@ -633,7 +977,30 @@ hipError_t launch_distill(const LogitArgs& A, const float* teacher, double invT,
                           int64_t ldg, void* ws, hipStream_t st) {
   Part* parts = static_cast<Part*>(ws);
   float* zl = reinterpret_cast<float*>(parts + A.t * A.S);
-  const dim3 grid((unsigned)(A.t * A.S)), block(LG_THREADS);
+  const dim3 grid((unsigned)(A.t * A.S)), block(LG_THREADS), rows((unsigned)A.t);
+  // rows that fit one workgroup's registers, where there are enough of them to
+  // keep half the CUs at work
+  const int64_t vec = 16 / es_of(A.dtype);
+  if (A.t >= 128 && A.V <= 1024 * 16 * vec) {
+    if (A.V <= 256 * 8 * vec) {
+      if (tail) {
+        LOGIT_TYPES(A.dtype, hipLaunchKernelGGL((distill_row_kernel<T, 256, 8, true>), rows, dim3(256), 0, st, A,
+                                                teacher, invT, loss, grad, ldg));
+      } else {
+        LOGIT_TYPES(A.dtype, hipLaunchKernelGGL((distill_row_kernel<T, 256, 8, false>), rows, dim3(256), 0, st, A,
+                                                teacher, invT, loss, grad, ldg));
+      }
+    } else {
+      if (tail) {
+        LOGIT_TYPES(A.dtype, hipLaunchKernelGGL((distill_row_kernel<T, 1024, 16, true>), rows, dim3(1024), 0, st, A,
+                                                teacher, invT, loss, grad, ldg));
+      } else {
+        LOGIT_TYPES(A.dtype, hipLaunchKernelGGL((distill_row_kernel<T, 1024, 16, false>), rows, dim3(1024), 0, st, A,
+                                                teacher, invT, loss, grad, ldg));
+      }
+    }
+    return hipGetLastError();
+  }
   if (tail) {
     LOGIT_TYPES(A.dtype, hipLaunchKernelGGL((logit_part_kernel<T, true>), grid, block, 0, st, A, parts,
                                             static_cast<uint64_t*>(nullptr), zl));

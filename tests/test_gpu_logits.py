@@ -272,3 +272,49 @@ def test_logits_refusals():
         mpq.distill(z, ids, lp, grad=torch.empty(4, 100, device="cuda").half())
     with pytest.raises(mpq.MPQError):
         mpq.token_logprobs(z, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"), top=3)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("V,k,T,tail", [(5, 3, 1.0, True), (4099, 128, 2.0, False), (16391, 64, 1.0, True),
+                                        (50257, 100, 4.0, False), (65537, 20, 1.0, True), (131072, 5, 1.0, True)])
+def test_distill_many_rows(dtype, V, k, T, tail):
+    """Enough rows for a workgroup each, around the widths that its registers hold."""
+    g = np.random.default_rng(V)
+    z = rows(g, 129, V, dtype, spread=2.5, pad=3, shift=1)
+    ids, lp = teacher_list(g, z, k)
+    check_distill(z, ids, lp, dtype, T, tail)
+
+
+@pytest.mark.parametrize("V", [9001, 40003])
+@pytest.mark.parametrize("tail", [False, True])
+def test_distill_many_rows_lists(V, tail):
+    """Lists with gaps, repeats and zero masses, weights of 0, masked and extreme logits, in rows of a workgroup each."""
+    import torch
+    g = np.random.default_rng(V)
+    z = rows(g, 140, V, "fp32", spread=2.0).clone()
+    z[7, V - 5:] = float("-inf")
+    z[8, ::2] = torch.finfo(torch.float32).min
+    z[9] = z[9] * 1e6               # beyond what one fused step scales exactly
+    z[10] = 0.5
+    ids, lp = teacher_list(g, z, 70, noise=0.2)
+    ids[0, 3:6] = [-1, V, 2 ** 31 - 1]
+    ids[1, 5] = ids[1, 2]
+    ids[1, 69] = ids[1, 2]
+    lp[2, 4] = -np.inf
+    ids[3] = -1
+    ids[11, 1] = V - 1
+    weights = (g.random(140) * 2).astype(np.float32).astype(np.float64)
+    weights[4:6] = 0.0
+    z[4] = float("nan")
+    lp[9] = -4.0
+    lp = np.maximum(lp, -60.0) + np.where(np.isinf(lp), -np.inf, 0.0).astype(np.float32)
+    check_distill(z[:9].contiguous(), ids[:9], lp[:9], "fp32", 1.0, tail, weights[:9])
+    keep = [i for i in range(140) if i != 9]
+    check_distill(z[keep].contiguous(), ids[keep], lp[keep], "fp32", 1.0, tail, weights[keep])
+    # row 9's masses: one token has all of the student's
+    import post_quantization_solver_amd as mpq
+    r = mpq.distill(z, dev(ids), dev(lp), tail=tail, weights=dev(weights.astype(np.float32)))
+    _, grad, scale = R.distill(z[9:10].double().cpu().numpy(), ids[9:10], lp[9:10].astype(np.float64), 1.0, tail,
+                               weights[9:10])
+    assert np.isfinite(grad).all()
+    assert (np.abs(host(r["grad"])[9] - grad[0]) <= 2.0 ** -16 * scale[0] + 1e-30).all()
