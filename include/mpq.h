@@ -76,8 +76,9 @@ typedef struct {
   int32_t e8_last2[8];     /* E8 prefix: twice the last codeword's coordinates */
   const void* tables;      /* device, caller-owned: the codebook's tables */
   uint64_t magic;          /* set by mpq_codebook_prepare */
-  int32_t narrow;          /* 1: the entries (d = 1: their differences to level K / 2) are exact in
-                              bfloat16 and in float16, as mpq_pack needs them */
+  int32_t narrow;          /* not 0: the entries (d = 1: their differences to level K / 2) are exact
+                              in bfloat16 and in float16, as mpq_pack needs them; 2: d = 1 and
+                              the levels are evenly spaced, too */
 } mpq_codebook;
 
 #define MPQ_CB_GENERIC   0

@@ -10,7 +10,9 @@ load, every call raises -- there is no CPU fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -741,10 +743,36 @@ def _on(t, name, dev):
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
 
 
-def _scratch(workspace, nb, dev):
+_same_device = contextlib.nullcontext()
+
+
+def _guard(dev):
+    """The device a call launches on, entered only where it is not the current one."""
+    import torch
+    return _same_device if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+def _raw_stream(dev):
+    """The current stream's handle.  (A call of a few microseconds should not spend them on Stream objects.)"""
+    import torch
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get(dev.index) if get is not None else torch.cuda.current_stream(dev).cuda_stream
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+@functools.lru_cache(maxsize=256)
+def _bytes_of(what, *args):
+    """A workspace size of the library (a function of its arguments alone)."""
+    return int(getattr(load_library(), what)(*args))
+
+
+def _scratch(workspace, dev, what, *args):
     import torch
     if workspace is None:
-        return torch.empty(nb, dtype=torch.uint8, device=dev)
+        return torch.empty(_bytes_of(what, *args), dtype=torch.uint8, device=dev)
     _dev(workspace, torch.uint8, "workspace")
     _on(workspace, "workspace", dev)
     return workspace
@@ -764,7 +792,7 @@ class PackedLayer:
             raise ValueError(f"codes has shape {tuple(codes.shape)}, expected 2 dimensions")
         dev = codes.device
         lib = load_library()
-        with torch.cuda.device(dev):
+        with _guard(dev):
             self.codebook = prepare_codebook(cb, dev)
             _on(self.codebook.tables, "the codebook", dev)
             self.m, self.n = codes.shape[0], codes.shape[1] * self.codebook.d
@@ -778,8 +806,8 @@ class PackedLayer:
                 _on(row_offset, "row_offset", dev)
             self.packed = torch.empty(lib.mpq_pack_bytes(self.m, self.n, self.codebook.K, self.codebook.d),
                                       dtype=torch.uint8, device=dev)
-            _check(lib.mpq_pack(_ptr(codes), self.m, self.n, self.codebook.ref(), _ptr(self.packed),
-                                self.packed.numel(), _stream()), "mpq_pack")
+            _check(lib.mpq_pack(_at(codes), self.m, self.n, self.codebook.ref(), _at(self.packed),
+                                self.packed.numel(), _raw_stream(dev)), "mpq_pack")
 
 
 def pack_layer(codes, cb, row_scale, row_offset=None, group=None) -> PackedLayer:
@@ -818,14 +846,14 @@ def linear(x, layer, bias=None, activation=None, residual=None, return_pre=False
         _on(bias, "bias", dev)
     ldr = _rows(residual, "residual", x, (t, m)) if residual is not None else m
     lib = load_library()
-    with torch.cuda.device(dev):
+    with _guard(dev):
         y = torch.empty((t, m), dtype=x.dtype, device=dev) if out is None else out
         ldy = _rows(y, "out", x, (t, m)) if out is not None else max(m, 1)
         pre = torch.empty((t, m), dtype=x.dtype, device=dev) if return_pre else None
-        ws = _scratch(workspace, lib.mpq_linear_workspace_bytes(code, t, m, n, cb.K, cb.d, layer.group), dev)
-        rc = lib.mpq_linear(_ptr(x), code, t, ldx, _ptr(layer.packed), m, n, cb.ref(), _ptr(layer.scale),
-                            _ptr(layer.offset), layer.group, _ptr(bias), act, _ptr(residual), ldr, _ptr(y), ldy,
-                            _ptr(pre), m, _ptr(ws), ws.numel(), _stream())
+        ws = _scratch(workspace, dev, "mpq_linear_workspace_bytes", code, t, m, n, cb.K, cb.d, layer.group)
+        rc = lib.mpq_linear(_at(x), code, t, ldx, _at(layer.packed), m, n, cb.ref(), _at(layer.scale),
+                            _at(layer.offset), layer.group, _at(bias), act, _at(residual), ldr, _at(y), ldy,
+                            _at(pre), m, _at(ws), ws.numel(), _raw_stream(dev))
     _check(rc, "mpq_linear")
     return (y, pre) if return_pre else y
 
@@ -849,16 +877,16 @@ def linear_backward(dy, x, layer, pre=None, activation=None, need_dx=True, need_
         raise ValueError("pre (linear's second result) is needed with an activation")
     ldp = _rows(pre, "pre", x, (t, m)) if act else m
     lib = load_library()
-    with torch.cuda.device(dev):
+    with _guard(dev):
         dx = torch.empty((t, n), dtype=x.dtype, device=dev) if need_dx else None
         dscale = torch.empty_like(layer.scale) if need_dlayer else None
         doffset = torch.empty_like(layer.scale) if need_dlayer else None
         dbias = torch.empty(m, dtype=torch.float32, device=dev) if need_dlayer else None
-        ws = _scratch(workspace, lib.mpq_linear_backward_workspace_bytes(code, t, m, n, cb.K, cb.d, layer.group), dev)
-        rc = lib.mpq_linear_backward(_ptr(dy), lddy, _ptr(x), code, t, ldx, _ptr(layer.packed), m, n, cb.ref(),
-                                     _ptr(layer.scale), _ptr(layer.offset), layer.group, act,
-                                     _ptr(pre) if act else None, ldp, _ptr(dx), n, _ptr(dscale), _ptr(doffset),
-                                     _ptr(dbias), _ptr(ws), ws.numel(), _stream())
+        ws = _scratch(workspace, dev, "mpq_linear_backward_workspace_bytes", code, t, m, n, cb.K, cb.d, layer.group)
+        rc = lib.mpq_linear_backward(_at(dy), lddy, _at(x), code, t, ldx, _at(layer.packed), m, n, cb.ref(),
+                                     _at(layer.scale), _at(layer.offset), layer.group, act,
+                                     _at(pre) if act else None, ldp, _at(dx), n, _at(dscale), _at(doffset),
+                                     _at(dbias), _at(ws), ws.numel(), _raw_stream(dev))
     _check(rc, "mpq_linear_backward")
     return dict(dx=dx, dscale=dscale, doffset=doffset, dbias=dbias)
 
@@ -881,15 +909,15 @@ def token_logprobs(logits, tokens=None, top=0, workspace=None):
         _dev(tokens, torch.int32, "tokens", (t,))
         _on(tokens, "tokens", dev)
     lib = load_library()
-    with torch.cuda.device(dev):
+    with _guard(dev):
         stats = torch.empty((3, t), dtype=torch.float32, device=dev)
         lse, entropy, logprob = stats.unbind(0)
         ids = torch.empty((t, top), dtype=torch.int32, device=dev) if top > 0 else None
         lps = torch.empty((t, top), dtype=torch.float32, device=dev) if top > 0 else None
-        ws = _scratch(workspace, lib.mpq_token_logprobs_workspace_bytes(code, t, V, top), dev)
-        rc = lib.mpq_token_logprobs(_ptr(logits), code, t, V, ld, _ptr(tokens), top,
-                                    _ptr(logprob) if tokens is not None else None, _ptr(entropy), _ptr(lse), _ptr(ids),
-                                    _ptr(lps), _ptr(ws), ws.numel(), _stream())
+        ws = _scratch(workspace, dev, "mpq_token_logprobs_workspace_bytes", code, t, V, top)
+        rc = lib.mpq_token_logprobs(_at(logits), code, t, V, ld, _at(tokens), top,
+                                    _at(logprob) if tokens is not None else None, _at(entropy), _at(lse), _at(ids),
+                                    _at(lps), _at(ws), ws.numel(), _raw_stream(dev))
     _check(rc, "mpq_token_logprobs")
     return dict(lse=lse, entropy=entropy, logprob=logprob if tokens is not None else None, top_ids=ids,
                 top_logprobs=lps)
@@ -924,7 +952,7 @@ def distill(logits, teacher_ids, teacher, temperature=1.0, tail=False, weights=N
         _dev(weights, torch.float32, "weights", (t,))
         _on(weights, "weights", dev)
     lib = load_library()
-    with torch.cuda.device(dev):
+    with _guard(dev):
         if grad is True:
             grad = torch.empty((t, V), dtype=logits.dtype, device=dev)
         ldg = V
@@ -933,9 +961,9 @@ def distill(logits, teacher_ids, teacher, temperature=1.0, tail=False, weights=N
         else:
             grad = None
         loss = torch.empty(t, dtype=torch.float32, device=dev)
-        ws = _scratch(workspace, lib.mpq_distill_workspace_bytes(code, t, V, k), dev)
-        rc = lib.mpq_distill(_ptr(logits), code, t, V, ld, _ptr(teacher_ids), _ptr(teacher), k, float(temperature),
-                             1 if tail else 0, _ptr(weights), _ptr(loss), _ptr(grad), ldg, _ptr(ws), ws.numel(),
-                             _stream())
+        ws = _scratch(workspace, dev, "mpq_distill_workspace_bytes", code, t, V, k)
+        rc = lib.mpq_distill(_at(logits), code, t, V, ld, _at(teacher_ids), _at(teacher), k, float(temperature),
+                             1 if tail else 0, _at(weights), _at(loss), _at(grad), ldg, _at(ws), ws.numel(),
+                             _raw_stream(dev))
     _check(rc, "mpq_distill")
     return dict(loss=loss, grad=grad)

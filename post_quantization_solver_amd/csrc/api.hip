@@ -1191,6 +1191,13 @@ int mpq_codebook_prepare(const float* cb, int64_t K, int64_t d, void* tables, si
     h.narrow = 1;
     for (int64_t k = 0; k < K * d; ++k)
       if (!narrow_exact(d == 1 ? cb[k] - cb[K / 2] : cb[k])) h.narrow = 0;
+    // evenly spaced levels (in float64, where they and their multiples are exact)
+    if (d == 1 && h.narrow) {
+      const double step = (double)cb[1] - (double)cb[0];
+      bool even = (double)(cb[1] - cb[0]) == step;
+      for (int64_t k = 0; k < K; ++k) even = even && (double)cb[k] == (double)cb[0] + (double)k * step;
+      if (even) h.narrow = 2;
+    }
     if (d == 1) {
       for (int64_t k = 0; k < K; ++k) lv[k] = cb[k];
       MPQ_TRY(hipMemcpyAsync(tb + T.levels, lv.data(), 64 * sizeof(float), hipMemcpyHostToDevice, st));

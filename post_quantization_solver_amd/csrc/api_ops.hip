@@ -73,6 +73,7 @@ int layer_of(QLayer& L, const void* packed, int64_t m, int64_t n, const mpq_code
   L.scale = scale;
   L.offset = offset;
   L.levels = T.levels;
+  L.uniform = cb->narrow == 2;
   L.lut = T.pk_lut;
   L.map = T.pk_map;
   L.e32 = T.e32;

@@ -10,7 +10,10 @@
 //
 // d = 1: entries are taken about the middle level, e - levels[K / 2], so that
 // the sums over a grid 0 .. K - 1 do not carry a large common part that the
-// offset takes off again; o' = o + a levels[K / 2].
+// offset takes off again; o' = o + a levels[K / 2].  A step's eight 4-bit codes
+// are stored with code 2 p in nibble p and code 2 p + 1 in nibble p + 4, its
+// 8-bit codes with code 2 p in byte p and code 2 p + 1 in byte p + 2 (of a word
+// of four): a pair is 16 bits apart, where a pair of 16-bit values wants it.
 #pragma once
 #include "mpq_device.h"
 #include "internal.h"
@@ -38,6 +41,7 @@ struct QLayer {
   const float* offset;   // m x G, or nullptr: zero
   int64_t group; int G;  // columns per affine group (n: one per row)
   const float* levels;   // d = 1
+  bool uniform;          // d = 1: levels[q] = levels[0] + q (levels[1] - levels[0]), exactly
   int K;
   const uint32_t* lut;   // QF_E8: sign-magnitude nibbles of 2 e, nibble {0,2,4,6,1,3,5,7}[q] = coordinate q
   const uint16_t* map;   // QF_E8: code -> packed code
@@ -102,12 +106,12 @@ __device__ __forceinline__ v4u q_decode(const QLayer& L, const uint32_t* lut, co
   v4u r;
   if constexpr (FMT == QF_NIB) {
 #pragma unroll
-    for (int b = 0; b < 4; ++b) r[b] = lut[(w[s] >> (8 * b)) & 255u];
+    for (int b = 0; b < 4; ++b) r[b] = lut[((w[s] >> (4 * b)) & 15u) | ((w[s] >> (4 * b + 12)) & 240u)];
   } else if constexpr (FMT == QF_BYTE) {
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
-      const uint32_t h = w[2 * s + (b >> 1)] >> (16 * (b & 1));
-      r[b] = lut[(h & 63u) | ((h >> 2) & 0xfc0u)];
+      const uint32_t h = w[2 * s + (b >> 1)] >> (8 * (b & 1));
+      r[b] = lut[(h & 63u) | ((h >> 10) & 0xfc0u)];
     }
   } else if constexpr (FMT == QF_E8) {
     // Packed code: 2 i + sign for the i-th of `pairs` points whose negative is
@@ -144,6 +148,29 @@ __device__ __forceinline__ v4u q_decode(const QLayer& L, const uint32_t* lut, co
     r[1] = T::pack(a.z, a.w);
     r[2] = T::pack(b.x, b.y);
     r[3] = T::pack(b.z, b.w);
+  }
+  return r;
+}
+
+// The same for uniform levels, by arithmetic: q_base + code (bfloat16: 128 + q is
+// 0x4300 | q; the caller takes q_base off, see qskinny.hip) or, in float16, whose
+// 1024 + q is 0x6400 | q and which adds in pairs, code - K / 2 itself.
+constexpr float Q_BASE = 128.f;
+template <int FMT, typename T>
+__device__ __forceinline__ v4u q_decode_uniform(const QLayer& L, const uint4& c, int s) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+  v4u r;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    uint32_t q;
+    if constexpr (FMT == QF_NIB) q = (w[s] >> (4 * b)) & 0x000f000fu;
+    else q = (w[2 * s + (b >> 1)] >> (8 * (b & 1))) & 0x00ff00ffu;
+    if constexpr (T::HALF) {
+      const v2h mid = {(_Float16)(float)(-1024 - L.K / 2), (_Float16)(float)(-1024 - L.K / 2)};
+      r[b] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(v2h, q | 0x64006400u) + mid);
+    } else {
+      r[b] = q | 0x43004300u;
+    }
   }
   return r;
 }
@@ -329,7 +356,7 @@ __device__ __forceinline__ uint32_t q_code4(const QLayer& L, int64_t i, int64_t 
   const int64_t blk = j >> 3, c = blk / (4 * steps);
   const int kb = (int)(blk & 3), s = (int)(blk - c * 4 * steps) >> 2, half = (int)(j >> 2) & 1;
   const size_t at = (((size_t)(i >> 4) * L.chunks + c) * 64 + kb * 16 + (i & 15)) * 8;   // 16-bit words
-  if (L.fmt == QF_NIB) return codes[at + s * 2 + half];
+  if (L.fmt == QF_NIB) return *reinterpret_cast<const uint32_t*>(codes + at + s * 2);
   if (L.fmt == QF_BYTE) return *reinterpret_cast<const uint32_t*>(codes + at + s * 4 + half * 2);
   return codes[at + s];
 }
@@ -337,10 +364,10 @@ __device__ __forceinline__ void q_entries4(const QLayer& L, uint32_t code, int64
   const int half = (int)(j >> 2) & 1;
   if (L.fmt == QF_NIB) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) e[k] = L.levels[(code >> (4 * k)) & 15u];
+    for (int k = 0; k < 4; ++k) e[k] = L.levels[(code >> (8 * half + 4 * (k >> 1) + 16 * (k & 1))) & 15u];
   } else if (L.fmt == QF_BYTE) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) e[k] = L.levels[(code >> (8 * k)) & 63u];
+    for (int k = 0; k < 4; ++k) e[k] = L.levels[(code >> (8 * (k >> 1) + 16 * (k & 1))) & 63u];
   } else if (L.fmt == QF_E8) {
     const int c = (int)code;
     const uint32_t v = L.lut[max(c >> 1, c - L.pairs)] ^ (c & 1 ? 0x88888888u : 0u);
@@ -383,12 +410,14 @@ int q_gemm_splits(int64_t M, int64_t N, int64_t K, int npairs);
 size_t q_gemm_workspace(int64_t M, int64_t N, int64_t K, int npairs);
 hipError_t launch_q_gemm(const QGemm& g, float* part, hipStream_t st);
 
-// The product with few rows (qskinny.hip): x as planes of 16-bit rows, kblocks blocks of
-// eight columns each (two planes: float16, with O.rowmax).  Column groups need
-// chunks that lie in one group.
+// The product with few rows (qskinny.hip): x in place (16-bit rows of ldx > 0
+// elements, 16-byte aligned, n a multiple of 8), or in operand order (ldx = 0):
+// planes of whole chunks, 16 rows by 16 rows, each step's 64 lanes x 16 bytes
+// together.  Two planes: float16, with O.rowmax.  Column groups need chunks that
+// lie in one group.
 bool q_skinny_ok(const QLayer& L);
-hipError_t launch_q_skinny(const QLayer& L, const uint16_t* x, int64_t ldx, int64_t planex, int kblocks, int64_t t,
-                           int planes, bool bf16, const QOut& O, hipStream_t st);
+hipError_t launch_q_skinny(const QLayer& L, const uint16_t* x, int64_t ldx, int64_t planex, int64_t t, int planes,
+                           bool bf16, const QOut& O, hipStream_t st);
 
 struct QLinearArgs {
   QLayer L;

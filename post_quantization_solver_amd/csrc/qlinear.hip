@@ -54,11 +54,12 @@ __global__ __launch_bounds__(256) void q_pack_kernel(const int32_t* __restrict__
       for (int q = 0; q < count; ++q) {
         const int64_t j = (blk0 + q / 8 * 4) * 8 + q % 8;
         const int code = j < L.n ? safe_code(codes[i * L.n + j], L.K) : 0;
-        const int bit = q * bits, hi = bit & 31;
-        const uint32_t v = (uint32_t)code << hi;
+        // place of the q-th code (see qlayer.h)
+        const int at = bits == 4 ? q / 8 * 8 + (q % 8 >> 1) + 4 * (q & 1) : q / 4 * 4 + (q % 4 >> 1) + 2 * (q & 1);
+        const uint32_t v = (uint32_t)code << (at * bits & 31);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          if (bit >> 5 == k) w[k] |= v;
+          if (at * bits >> 5 == k) w[k] |= v;
       }
     } else {
       const int64_t B = L.n / 8;
@@ -94,31 +95,65 @@ __device__ __forceinline__ float row_bound(const QLayer& L, int64_t i, int lane)
   return __ballot(odd) ? 0.f : w;   // a row that is not finite keeps factor 1
 }
 
-// Blocks 0 .. t - 1, one row of x each: its 16-bit planes, padded with zeros to
-// Kp columns -- planes = 0: none; raw: a copy of 16-bit x; else float16 terms of
-// x times 2^pow2_shift(rowmax), stored -- and its sum (optional).  The blocks
-// after them, a wave per row of the layer: refs = its weights' bound.
-__global__ __launch_bounds__(256) void q_prep_kernel(const void* __restrict__ x, int64_t ldx, int dtype, int64_t t,
-                                                     int64_t n, int64_t Kp, uint16_t* __restrict__ out, int64_t plane,
-                                                     int planes, bool raw, uint32_t* __restrict__ rowmax,
-                                                     float* __restrict__ sum, QLayer L, uint32_t* __restrict__ refs) {
+__device__ __forceinline__ void weight_terms(const float* v, v4u* out) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t a[2], b[2];
+    f16_terms(v[2 * q], a);
+    f16_terms(v[2 * q + 1], b);
+    out[0][q] = pack2(a[0], b[0]);
+    out[1][q] = pack2(a[1], b[1]);
+  }
+}
+
+struct PrepArgs {
+  const void* x; int64_t ldx;
+  int dtype;
+  int64_t t, rows;      // rows t .. rows - 1 of the planes are zeros
+  int64_t n, Kp;        // columns n .. Kp - 1 too
+  uint16_t* out; int64_t plane;
+  int planes;           // 0: none
+  bool raw;             // 16-bit x as it is; else float16 terms of x times 2^pow2_shift(rowmax)
+  bool frags;           // planes in the order of qskinny.hip's operands, else rows of Kp
+  bool vec;             // rows of x can be read 8 elements at a time
+  int segs;             // workgroups per row (1 where a row's sum or maximum is wanted)
+  uint32_t* rowmax;
+  float* sum;
+  QLayer L; uint32_t* refs;
+};
+
+// Workgroups 0 .. rows segs - 1: a row (or a part) of x, its planes, and
+// optionally its sum.  The ones after them, a wave per row of the layer: refs =
+// its weights' bound.
+__global__ __launch_bounds__(256) void q_prep_kernel(PrepArgs A) {
   __shared__ float red[2][4];
   const int lane = threadIdx.x & 63, wave = wave_id();
-  const int64_t row = blockIdx.x;
-  if (row >= t) {
-    const int64_t i = (row - t) * 4 + wave;
-    if (i >= L.m) return;
-    const float b = row_bound(L, i, lane);
-    if (lane == 0) refs[i] = __float_as_uint(b);
+  const int64_t row = blockIdx.x / A.segs;
+  if (row >= A.rows) {
+    const int64_t i = (blockIdx.x - A.rows * A.segs) * 4 + wave;
+    if (i >= A.L.m) return;
+    const float b = row_bound(A.L, i, lane);
+    if (lane == 0) A.refs[i] = __float_as_uint(b);
     return;
   }
-  float s = 0.f;
+  const int seg = (int)(blockIdx.x - row * A.segs);
+  const bool live = row < A.t;
+  auto load8 = [&](int64_t j, float* v) {
+    const int have = live ? (int)max((int64_t)0, min((int64_t)8, A.n - j)) : 0;
+    load4(A.x, row * A.ldx + j, A.dtype, A.vec, min(have, 4), v);
+    load4(A.x, row * A.ldx + j + 4, A.dtype, A.vec, max(have - 4, 0), v + 4);
+  };
   uint32_t top = 0;
-  if (sum || (planes && !raw)) {
-    for (int64_t j = threadIdx.x; j < n; j += 256) {
-      const float v = load_as_f32(x, row * ldx + j, dtype);
-      s += v;
-      top = max(top, abs_bits(v));
+  if (A.sum || (A.planes && !A.raw)) {
+    float s = 0.f;
+    for (int64_t j = threadIdx.x * 8; j < A.n; j += 256 * 8) {
+      float v[8];
+      load8(j, v);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        s += v[k];
+        top = max(top, abs_bits(v[k]));
+      }
     }
     for (int o = 32; o; o >>= 1) {
       s += shfl_xor_f(s, o);
@@ -131,22 +166,31 @@ __global__ __launch_bounds__(256) void q_prep_kernel(const void* __restrict__ x,
     __syncthreads();
     top = 0;
     for (int w = 0; w < 4; ++w) top = max(top, __float_as_uint(red[1][w]));
-    if (threadIdx.x == 0) {
-      if (sum) sum[row] = (red[0][0] + red[0][1]) + (red[0][2] + red[0][3]);
-      if (planes && !raw) rowmax[row] = top;
+    if (threadIdx.x == 0 && live) {
+      if (A.sum) A.sum[row] = (red[0][0] + red[0][1]) + (red[0][2] + red[0][3]);
+      if (A.planes && !A.raw) A.rowmax[row] = top;
     }
   }
-  if (!planes) return;
+  if (!A.planes) return;
   const float f = pow2(pow2_shift(top));
-  for (int64_t j = threadIdx.x; j < Kp; j += 256) {
-    if (raw) {
-      out[row * Kp + j] = j < n ? static_cast<const uint16_t*>(x)[row * ldx + j] : (uint16_t)0;
-      continue;
+  for (int64_t j = ((int64_t)seg * 256 + threadIdx.x) * 8; j < A.Kp; j += (int64_t)A.segs * 256 * 8) {
+    float v[8];
+    load8(j, v);
+    v4u o[2];
+    if (A.raw) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        o[0][q] = A.dtype == DT_BF16 ? OpBf16::pack(v[2 * q], v[2 * q + 1]) : OpF16::pack(v[2 * q], v[2 * q + 1]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] *= f;
+      weight_terms(v, o);
     }
-    uint32_t b[2];
-    f16_terms(j < n ? load_as_f32(x, row * ldx + j, dtype) * f : 0.f, b);
-    out[row * Kp + j] = (uint16_t)b[0];
-    if (planes > 1) out[plane + row * Kp + j] = (uint16_t)b[1];
+    // operand order: step of 32 columns by step, lane (j / 8 % 4) 16 + row % 16
+    uint16_t* dst = A.out + (A.frags ? ((row >> 4) * (A.Kp >> 5) + (j >> 5)) * 512 + ((j >> 3 & 3) * 16 + (row & 15)) * 8
+                                     : row * A.Kp + j);
+    *reinterpret_cast<v4u*>(dst) = o[0];
+    if (A.planes > 1) *reinterpret_cast<v4u*>(dst + A.plane) = o[1];
   }
 }
 
@@ -167,17 +211,6 @@ __device__ __forceinline__ void weights8(const QLayer& L, int64_t i, int64_t j0,
     }
   }
 }
-__device__ __forceinline__ void weight_terms(const float* v, v4u* out) {
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    uint32_t a[2], b[2];
-    f16_terms(v[2 * q], a);
-    f16_terms(v[2 * q + 1], b);
-    out[0][q] = pack2(a[0], b[0]);
-    out[1][q] = pack2(a[1], b[1]);
-  }
-}
-
 // Rows tile0 * 16 .. of the layer as planes of Kp columns: entries (planes = 0),
 // or float16 terms of the weights times 2^pow2_shift(refs).  A wave per chunk of
 // a tile.
@@ -608,6 +641,9 @@ hipError_t unpack_t(const QLayer& L, int64_t mp, int planes, const uint32_t* ref
 // row, and groups of whole chunks; other groups always unpack).
 constexpr int64_t Q_SKINNY_TOKENS = 128;
 
+// Elements of x up to which the few-row product reads it in place.
+constexpr int64_t Q_DIRECT = 65536;
+
 bool use_skinny(const QLinearArgs& A) { return q_skinny_ok(A.L) && A.t <= Q_SKINNY_TOKENS; }
 
 struct Carve {
@@ -630,17 +666,22 @@ bool whole_quads(const void* p, int64_t ld, int dtype) {
 hipError_t forward(const QLinearArgs& A, char* base, size_t* bytes, hipStream_t st) {
   const QLayer& L = A.L;
   const bool skinny = use_skinny(A), grouped = L.G > 1, weights = grouped && !skinny;
-  const int64_t Kp = up64(L.n);
+  // the few-row product reads whole chunks
+  const int64_t Kp = skinny ? (int64_t)L.chunks * q_chunk(L.fmt) : up64(L.n);
   // x: its own 16 bits, or float16 terms (float32; bfloat16 against weights)
   const int XP = A.dtype == DT_F32 ? 2 : 1;
   const bool raw = A.dtype == DT_F16 || (A.dtype == DT_BF16 && !weights);
-  const bool direct = raw && reinterpret_cast<uintptr_t>(A.x) % 16 == 0 && A.ldx % 8 == 0 && A.ldx <= (1 << 20) &&
-                      L.n % (skinny ? 8 : 64) == 0;
+  const bool aligned = reinterpret_cast<uintptr_t>(A.x) % 16 == 0 && A.ldx % 8 == 0 && A.ldx <= (1 << 20);
+  // Few rows: one token's operand is read in place.  More tokens' rows lie 16 at
+  // a stride that sends them to the same few cache channels (64 clocks a load of
+  // 1 KB, against 16 in operand order), so they are laid out first -- unless
+  // that launch costs more than it saves.
+  const bool direct = raw && aligned && (skinny ? L.n % 8 == 0 && (A.t == 1 || A.t * L.n <= Q_DIRECT) : L.n % 64 == 0);
   const bool bf16 = raw && A.dtype == DT_BF16;
   const int WP = !weights ? 0 : A.dtype == DT_BF16 ? 1 : 2;   // terms of a weight (0: entries)
   const bool sums = !skinny && !grouped && L.has_offset();
   Carve W{base};
-  const int64_t plane = A.t * Kp;
+  const int64_t xrows = skinny ? (A.t + 15) / 16 * 16 : A.t, plane = xrows * Kp;
   uint16_t* xp = W.take<uint16_t>((size_t)XP * plane * 2);
   float* xs = W.take<float>((size_t)A.t * 4);
   uint32_t* rowmax = W.take<uint32_t>((size_t)A.t * 4);
@@ -664,11 +705,24 @@ hipError_t forward(const QLinearArgs& A, char* base, size_t* bytes, hipStream_t 
   if (!base) return hipSuccess;
 
   hipError_t e;
-  const bool copy = !direct;
-  if (copy || sums || weights) {
-    const int64_t blocks = A.t + (weights ? (L.m + 3) / 4 : 0);
-    hipLaunchKernelGGL(q_prep_kernel, dim3((unsigned)blocks), dim3(256), 0, st, A.x, A.ldx, A.dtype, A.t, L.n, Kp, xp,
-                       plane, copy ? XP : 0, raw, rowmax, sums ? xs : nullptr, L, refs);
+  if (!direct || sums || weights) {
+    PrepArgs P;
+    memset(&P, 0, sizeof(P));
+    P.x = A.x; P.ldx = A.ldx;
+    P.dtype = A.dtype;
+    P.t = A.t; P.rows = direct ? A.t : xrows;
+    P.n = L.n; P.Kp = Kp;
+    P.out = xp; P.plane = plane;
+    P.planes = direct ? 0 : XP;
+    P.raw = raw;
+    P.frags = skinny;
+    P.vec = reinterpret_cast<uintptr_t>(A.x) % 16 == 0 && A.ldx % 4 == 0;
+    P.rowmax = rowmax;
+    P.sum = sums ? xs : nullptr;
+    P.L = L; P.refs = refs;
+    P.segs = !raw || sums ? 1 : (int)std::max<int64_t>(1, std::min((Kp + 2047) / 2048, 512 / P.rows));
+    const int64_t blocks = P.rows * P.segs + (weights ? (L.m + 3) / 4 : 0);
+    hipLaunchKernelGGL(q_prep_kernel, dim3((unsigned)blocks), dim3(256), 0, st, P);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   const uint16_t* x = direct ? static_cast<const uint16_t*>(A.x) : xp;
@@ -688,7 +742,7 @@ hipError_t forward(const QLinearArgs& A, char* base, size_t* bytes, hipStream_t 
   O.vec = whole_quads(A.y, A.ldy, A.dtype) && whole_quads(A.pre, A.ldpre, A.dtype) &&
           whole_quads(A.res, A.ldres, A.dtype);
   if (skinny)
-    return launch_q_skinny(L, x, ldx, plane, (int)(direct ? L.n / 8 : Kp / 8), A.t, XP, bf16, O, st);
+    return launch_q_skinny(L, x, direct ? A.ldx : 0, plane, A.t, XP, bf16, O, st);
   const int es = A.dtype == DT_F32 ? 4 : 2;
   for (int64_t r0 = 0; r0 < L.m; r0 += rows) {
     const int64_t nr = std::min(rows, L.m - r0);
