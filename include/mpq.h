@@ -504,12 +504,13 @@ int mpq_pack(const int32_t* codes, int64_t m, int64_t n, const mpq_codebook* cb,
  * residual NULL: none.  pre NULL, or u, what mpq_linear_backward needs where
  * there is an activation.  y may be the residual (same pointer and stride) and
  * otherwise overlaps no input.
- * Column groups need d = 1.  Sums are float32.  The entries enter as they are;
- * where column groups and the token count make the weights themselves enter
- * (more than 128 tokens, or groups that are no multiple of the packed chunk:
- * 128 columns at 4 bits, 64 at 8), they enter as two 16-bit terms (float32 x:
- * three).  A token whose x holds NaN or infinities has NaN or infinite outputs;
- * no other token does.
+ * Column groups need d = 1.  Sums are float32.  The entries enter as they are,
+ * float32 x as two float16 terms (22 bits, under a power of two per token).
+ * Where column groups make the weights themselves enter (more than 192 tokens on
+ * large layers, or groups that are no multiple of the packed chunk: 128 columns
+ * at 4 bits, 64 at 8), they and x are float16 terms under a power of two per
+ * row: one (11 bits) for bfloat16 x, else two for the weights.  A token whose x
+ * holds NaN or infinities has NaN or infinite outputs; no other token does.
  * 0 <= t < 2^22.  Nothing is kept between calls; calls may overlap on separate
  * workspaces. */
 size_t mpq_linear_workspace_bytes(int dtype, int64_t t, int64_t m, int64_t n, int64_t K, int64_t d, int64_t group);
@@ -524,9 +525,9 @@ int mpq_linear(const void* x, int dtype, int64_t t, int64_t ldx, const void* pac
  *   doffset = the same without e (both m x ceil(n / group) float32),
  *   dbias = sum of du over the tokens (m float32);
  * the last three together, or all NULL: not wanted.  The residual's gradient is
- * dy.  pre: mpq_linear's (needed with an activation).  The sums are of du in 24
- * bits; dx's du and scale are multiplied and rounded once to 8 bits (float16:
- * 16, float32: 24).  t = 0: zeros. */
+ * dy.  pre: mpq_linear's (needed with an activation).  du and x enter the sums
+ * as two float16 terms (22 bits) under a power of two per row; dx's du times scale
+ * as one (11 bits; float16 and float32: two).  t = 0: zeros. */
 size_t mpq_linear_backward_workspace_bytes(int dtype, int64_t t, int64_t m, int64_t n, int64_t K, int64_t d,
                                            int64_t group);
 int mpq_linear_backward(const void* dy, int64_t lddy, const void* x, int dtype, int64_t t, int64_t ldx,

@@ -638,13 +638,29 @@ hipError_t unpack_t(const QLayer& L, int64_t mp, int planes, const uint32_t* ref
 }
 
 // Token counts up to which the product reads the packed codes (one affine per
-// row, and groups of whole chunks; other groups always unpack).
-constexpr int64_t Q_SKINNY_TOKENS = 128;
+// row, or groups of whole chunks; other groups always unpack).  Beyond, every 64
+// tokens decode the layer once more, and laying the planes out once is cheaper.
+// Measured, few-row product against planes and tiles, 4096 x 14336: E8 bfloat16
+// 63 | 67 us at 128 tokens, 90 | 86 at 192, float32 93 | 92 at 96, 120 | 98 at
+// 128; groups of 128, whose planes hold weights (two terms but for bfloat16):
+// bfloat16 95 | 114 at 192, 123 | 115 at 256, float16 183 | 230 at 384, 240 |
+// 271 at 512, float32 188 | 251 at 192.  The planes take 20 us and more however
+// small the layer: 1024 x 1024 at 384 tokens 19 | 24 (E8), 14 | 23 (4 bits), 19
+// | 27 (float32), at 777 33 | 27, 23 | 27, 35 | 32.
+constexpr int64_t Q_SMALL_TOKENS = 1024, Q_SMALL_WORK = 3ll << 27;
+
+bool use_skinny(const QLinearArgs& A) {
+  if (!q_skinny_ok(A.L)) return false;
+  if (A.t <= Q_SMALL_TOKENS && A.t * A.L.m * A.L.n <= Q_SMALL_WORK) return true;
+  if (A.L.G > 1) return A.t <= (A.dtype == DT_F16 ? 384 : 192);
+  return A.t <= (A.dtype == DT_F32 ? 96 : 128);
+}
 
 // Elements of x up to which the few-row product reads it in place.
-constexpr int64_t Q_DIRECT = 65536;
-
-bool use_skinny(const QLinearArgs& A) { return q_skinny_ok(A.L) && A.t <= Q_SKINNY_TOKENS; }
+// Measured, in place | laid out first: 4096 columns, 2 tokens 8.7 | 11.3 us, 32
+// tokens 14.4 | 14.2; 8192 columns, 16 tokens 13.3 | 13.8, 32 tokens 21 | 19;
+// 14336 columns, 8 tokens 16.4 | 18.6, 16 tokens 20.8 | 19.3.
+constexpr int64_t Q_DIRECT = 131072;
 
 struct Carve {
   char* base;

@@ -8,14 +8,26 @@
 // Evenly spaced levels need no table: 128 + code is the code's bits under a
 // constant exponent in bfloat16.  The 128 and the middle level come off again
 // unit by unit (128 columns), with the sum over x, before their part could
-// outgrow float32's bits.
+// outgrow float32's bits (a unit's sum is rounded at 2^-24 of some 140 sum |x|:
+// far under half a bfloat16 step of the result).
 //
-// Split.  HBM traffic is the packed codes (2 bits a weight for E8); a wave's
-// matrix operand is what its lanes decode, sixteen rows at a time, so the
-// sixteen columns of the other operand are tokens: one token costs what
-// sixteen do.  A workgroup takes R tiles of 16 rows, its waves the chunks of the
-// tiles in turn, and joins their sums in a fixed order through LDS.  E8's table (148 KB for 65536 points) fills a CU's LDS, so those
-// workgroups stay, one per CU, and take tile after tile.
+// Bound.  HBM traffic is the packed codes (2 bits a weight for E8); what the
+// waves wait on is their own decoding (some 30 instructions a step of 64 blocks)
+// and, from two token tiles on, the operand loads.  A wave's matrix operand is
+// what its lanes decode, sixteen rows at a time, so the sixteen columns of the
+// other operand are tokens: one token costs what sixteen do but for x's loads.
+//
+// Split.  A workgroup takes R tiles of 16 rows, its waves the chunks of the tiles
+// in turn, and joins their sums in a fixed order through LDS.  E8's table (148 KB
+// for 65536 points) fills a CU's LDS, so those workgroups stay, one per CU, and
+// take tile after tile.  x lies in operand order (1 KB a load, whole lines): in
+// place its sixteen rows often start a multiple of 4 KB apart, on the same few
+// cache channels, 64 clocks a load instead of 16.
+//
+// Measured (microseconds at 1, 16, 32, 64, 128 tokens, bfloat16): E8 4096 x
+// 14336 14.3, 18.6, 26.5, 33, 59; 4096 x 4096 8.1, 9.4, 13.6, 15.8, 27; 32768 x
+// 4096 30, 33, 44, 73, 138; four bits 4096 x 14336 10.6, 15.1, 22.5, 31, 54.  An
+// empty call (64 columns) is 5.7 with E8's table and 3.9 without.
 #include <algorithm>
 #include <type_traits>
 #include "qlayer.h"

@@ -141,6 +141,30 @@ def test_linear_groups(dtype, name, n, group, t):
     run_case(name, 50, n, t, dtype, group=group, act="gelu_tanh", seed=n + group + t)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("name,m,n,group", [
+    ("s16", 1, 1, 0), ("s8", 17, 65, 0), ("s64", 33, 127, 0), ("e865536", 16, 8, 0), ("e830000", 70, 136, 0),
+    ("vec", 70, 136, 0), ("levels", 130, 200, 0), ("s16", 50, 512, 128), ("s16", 50, 500, 128), ("s64", 50, 320, 64)])
+def test_linear_many_tokens(dtype, name, m, n, group):
+    """More tokens than the packed codes are ever read for."""
+    run_case(name, m, n, 1030, dtype, group=group, act="silu", bias=True, residual=True, seed=m + n)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("pad,shift", [(0, 1), (3, 0), (8, 8)])
+def test_linear_many_tokens_strides(dtype, pad, shift):
+    run_case("e865536", 131, 128, 1025, dtype, residual=True, pad=pad, shift=shift)
+    run_case("s16", 64, 129, 1025, dtype, residual=True, pad=pad, shift=shift)
+
+
+@pytest.mark.parametrize("dtype,t,group", [("bf16", 128, 0), ("bf16", 129, 0), ("fp32", 96, 0), ("fp32", 97, 0),
+                                           ("bf16", 192, 128), ("bf16", 193, 128), ("fp16", 384, 128),
+                                           ("fp16", 385, 128)])
+def test_linear_either_side_of_the_packed_codes(dtype, t, group):
+    """A layer large enough that the token count decides, at the counts where it does."""
+    run_case("s16", 2050, 2176, t, dtype, group=group, bias=True)
+
+
 @pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu"])
 def test_linear_activations(act):
     run_case("s16", 64, 256, 9, "fp32", act=act, bias=True, residual=True)
@@ -180,6 +204,22 @@ def test_linear_in_place_residual_and_rows_left_alone():
         got = mpq.linear(x, layer, residual=buf[:t, :48], out=buf[:t, :48])
         assert got.data_ptr() == buf.data_ptr() and torch.equal(buf[:t, :48], want)
         assert torch.equal(buf[t:], before[t:]) and torch.equal(buf[:, 48:], before[:, 48:])
+
+
+def test_linear_nonfinite_among_many_tokens():
+    import torch
+    import post_quantization_solver_amd as mpq
+    for name, group in (("e865536", 0), ("s16", 128)):
+        codes, E, scale, off = make_layer(name, 48, 256, group, 4)
+        layer = mpq.pack_layer(dev(codes), E, dev(scale), dev(off), group=group or None)
+        for dtype in ("bf16", "fp16", "fp32"):
+            x = torch.randn(1030, 256, device="cuda").to(dtype_of(dtype))
+            clean = mpq.linear(x, layer)
+            x[3, 7], x[1029, 100] = float("nan"), float("inf")
+            y = mpq.linear(x, layer)
+            keep = [i for i in range(1030) if i not in (3, 1029)]
+            assert torch.equal(y[keep], clean[keep])
+            assert torch.isnan(y[3]).all() and not torch.isfinite(y[1029]).any()
 
 
 def test_linear_nonfinite_tokens_stay_apart():
