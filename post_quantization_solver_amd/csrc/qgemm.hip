@@ -15,42 +15,58 @@ namespace mpq {
 
 namespace {
 
-constexpr int BK = 32, STAGES = 4;
+constexpr int BK = 32;
+constexpr int gemm_stages(int BM, int BN) { return BM + BN <= 256 ? 4 : BM + BN <= 384 ? 6 : 5; }
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
 // Waits until at most N of this wave's global -> LDS loads are on their way,
-// and for its LDS reads; then for the workgroup.
+// and for its LDS reads; then for the workgroup.  (The builtin, so that the
+// compiler knows that the reads are there and puts no wait of its own before the
+// products.)
 template <int N>
 __device__ __forceinline__ void wait_stage() {
   static_assert(N < 64, "the counter has six bits");
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+  constexpr int EXP_ANY = 7 << 4, LGKM_0 = 0 << 8;
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);   // the products before stay before
+  __builtin_amdgcn_s_waitcnt((N & 15) | EXP_ANY | LGKM_0 | (N >> 4) << 14);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
 }
 
-// Where the next step's rows are.
-struct Cursor {
-  const char *a, *b;
-  int pair, k;
-};
-__device__ __forceinline__ void seek(Cursor& c, const QGemm& g, int64_t i0, int64_t j0, int pair, int k) {
-  c.pair = pair;
-  c.k = k;
-  if (pair >= g.npairs) return;
-  c.a = reinterpret_cast<const char*>(g.A + g.pa[pair] * g.planeA + i0 * g.lda) + (size_t)k * (BK * 2);
-  c.b = reinterpret_cast<const char*>(g.B + g.pb[pair] * g.planeB + j0 * g.ldb) + (size_t)k * (BK * 2);
-}
-
-// This wave's share of the next step's rows, straight into an LDS stage.
+// This wave's share of the next step's rows: sixteen rows of either operand per
+// load.
 template <int BM, int LOADS>
-__device__ __forceinline__ void fetch_step(Cursor& c, const QGemm& g, int64_t i0, int64_t j0, int kts, int wave,
+struct Cursor {
+  const char* p[LOADS];
+  int pair, k, kts;
+  __device__ __forceinline__ void seek(const QGemm& g, int64_t i0, int64_t j0, int wave, const uint32_t* off, int pair_,
+                                       int k_) {
+    pair = pair_;
+    k = k_;
+    if (pair >= g.npairs) return;
+    const char* a = reinterpret_cast<const char*>(g.A + g.pa[pair] * g.planeA + i0 * g.K) + (size_t)k * 1024;
+    const char* b = reinterpret_cast<const char*>(g.B + g.pb[pair] * g.planeB + j0 * (g.ldb ? g.ldb : g.K)) +
+                    (size_t)k * (g.ldb ? BK * 2 : 1024);
+#pragma unroll
+    for (int l = 0; l < LOADS; ++l) p[l] = ((wave * LOADS + l) * 16 < BM ? a : b) + off[l];
+  }
+};
+
+// Straight into an LDS stage: a KB per wave.
+__device__ __forceinline__ void load_lds(const char* src, uint16_t* dst) {
+  __builtin_amdgcn_global_load_lds(src, (lds_ptr_t)dst, 16, 0, 0);
+}
+template <int BM, int LOADS>
+__device__ __forceinline__ void fetch_step(Cursor<BM, LOADS>& c, const QGemm& g, int64_t i0, int64_t j0, int wave,
                                            const uint32_t* off, uint16_t* stage) {
 #pragma unroll
   for (int l = 0; l < LOADS; ++l) {
     const int r = (wave * LOADS + l) * 16;
-    __builtin_amdgcn_global_load_lds((r < BM ? c.a : c.b) + off[l], (lds_ptr_t)(stage + r * BK), 16, 0, 0);
+    load_lds(c.p[l], stage + r * BK);
+    c.p[l] += r < BM || !g.ldb ? 1024 : BK * 2;
   }
-  c.a += BK * 2;
-  c.b += BK * 2;
-  if (++c.k == kts) seek(c, g, i0, j0, c.pair + 1, 0);
+  if (++c.k == c.kts) c.seek(g, i0, j0, wave, off, c.pair + 1, 0);
 }
 
 // One wave's operands of a step.
@@ -67,6 +83,7 @@ __device__ __forceinline__ void read_step(const uint16_t* stage, int wm, int wn,
   for (int j = 0; j < SN; ++j) f.b[j] = *reinterpret_cast<const v4u*>(Bs + j * 16 * BK);
 #pragma unroll
   for (int i = 0; i < SM; ++i) f.a[i] = *reinterpret_cast<const v4u*>(As + i * 16 * BK);
+  __builtin_amdgcn_sched_barrier(0);   // before the products
 }
 template <typename T, int SM, int SN>
 __device__ __forceinline__ void multiply(const Frags<SM, SN>& f, v4f (&acc)[SM][SN]) {
@@ -81,6 +98,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void q_gemm_kernel(QGemm g, float*
   constexpr int WAVES = WM * WN;
   constexpr int SM = BM / WM / 16, SN = BN / WN / 16;   // 16 x 16 subtiles of a wave
   constexpr int LOADS = (BM + BN) / 16 / WAVES;         // 1 KB loads per wave and step
+  constexpr int STAGES = gemm_stages(BM, BN);
   __shared__ __attribute__((aligned(1024))) uint16_t lds[STAGES][(BM + BN) * BK];
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int wm = wave / WN, wn = wave % WN;
@@ -106,11 +124,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void q_gemm_kernel(QGemm g, float*
   uint32_t off[LOADS];
 #pragma unroll
   for (int l = 0; l < LOADS; ++l) {
-    const int r = (wave * LOADS + l) * 16 + (lane >> 2);
+    const int r = (wave * LOADS + l) * 16;
     const bool a = r < BM;
-    const int64_t lim = a ? g.M - 1 - i0 : g.N - 1 - j0;
-    const int64_t row = min((int64_t)(a ? r : r - BM), lim);   // rows past the end repeat the last
-    off[l] = (uint32_t)(row * (a ? g.lda : g.ldb) * 2 + piece * 16);
+    const int64_t lim = (a ? g.M - 1 - i0 : g.N - 1 - j0), row = a ? r : r - BM;
+    // rows past the end repeat the last sixteen, or the last
+    if (a || !g.ldb) off[l] = (uint32_t)(min(row / 16, lim / 16) * (g.K * 32) + (lane >> 2) * (BK * 2) + piece * 16);
+    else off[l] = (uint32_t)(min(row + (lane >> 2), lim) * g.ldb * 2 + piece * 16);
   }
 
   v4f acc[SM][SN];
@@ -121,24 +140,41 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void q_gemm_kernel(QGemm g, float*
 
   const int r = lane & 15, kb = lane >> 4;
   Frags<SM, SN> f0, f1;
-  Cursor at;
-  seek(at, g, i0, j0, kt0 / kts, kt0 % kts);
+  Cursor<BM, LOADS> at;
+  at.kts = kts;
+  at.seek(g, i0, j0, wave, off, kt0 / kts, kt0 % kts);
   // Step kt's operands are in registers when its turn begins; the barrier then
   // says that stage kt + 1 is there and that every wave has read stage kt, whose
-  // place takes step kt + STAGES.
+  // place takes step kt + STAGES.  A step in the run's middle has no branch
+  // between its reads and its products, so that these wait for the reads of the
+  // step before alone.
   for (int s = 0; s < STAGES; ++s)
-    if (kt0 + s < kt1) fetch_step<BM, LOADS>(at, g, i0, j0, kts, wave, off, lds[s]);
+    if (kt0 + s < kt1) fetch_step(at, g, i0, j0, wave, off, lds[s]);
   if (kt0 + STAGES <= kt1) wait_stage<(STAGES - 1) * LOADS>(); else wait_stage<0>();
   read_step<BM, SM, SN>(lds[0], wm, wn, r, kb, f0);
+  int here = 0, kt = kt0;   // kt's stage
+#define Q_STEP(cur, nxt)                                                                                     \
+  {                                                                                                          \
+    wait_stage<(STAGES - 2) * LOADS>();                                                                      \
+    fetch_step(at, g, i0, j0, wave, off, lds[here]);                                                               \
+    here = here + 1 == STAGES ? 0 : here + 1;                                                                \
+    read_step<BM, SM, SN>(lds[here], wm, wn, r, kb, nxt);                                                    \
+    multiply<T, SM, SN>(cur, acc);                                                                           \
+  }
+  for (; kt + STAGES + 1 < kt1; kt += 2) {
+    Q_STEP(f0, f1);
+    Q_STEP(f1, f0);
+  }
+#undef Q_STEP
 #define Q_STEP(kt, cur, nxt)                                                                                 \
   {                                                                                                          \
     if ((kt) + STAGES <= kt1) wait_stage<(STAGES - 2) * LOADS>(); else wait_stage<0>();                      \
-    if ((kt) + STAGES < kt1)                                                                                 \
-      fetch_step<BM, LOADS>(at, g, i0, j0, kts, wave, off, lds[((kt) - kt0) % STAGES]);                      \
-    if ((kt) + 1 < kt1) read_step<BM, SM, SN>(lds[((kt) + 1 - kt0) % STAGES], wm, wn, r, kb, nxt);           \
+    if ((kt) + STAGES < kt1) fetch_step(at, g, i0, j0, wave, off, lds[here]);                                      \
+    here = here + 1 == STAGES ? 0 : here + 1;                                                                \
+    if ((kt) + 1 < kt1) read_step<BM, SM, SN>(lds[here], wm, wn, r, kb, nxt);                                \
     multiply<T, SM, SN>(cur, acc);                                                                           \
   }
-  for (int kt = kt0; kt < kt1; kt += 2) {
+  for (; kt < kt1; kt += 2) {
     Q_STEP(kt, f0, f1);
     if (kt + 1 < kt1) Q_STEP(kt + 1, f1, f0);
   }

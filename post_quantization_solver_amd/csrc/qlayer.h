@@ -388,9 +388,15 @@ __device__ __forceinline__ void q_entries4(const QLayer& L, uint32_t code, int64
 // D[j][i] = sum over the plane pairs (p, q) and k of A_p[i][k] B_q[j][k] (16-bit
 // planes, K a multiple of 64, rows of lda / ldb elements, 16-byte aligned), then
 // O, or the contraction.  part (split K): splits x rows x cols float32.
+// Operand order of a plane: sixteen rows by 32 columns after another, along the
+// row first, each a contiguous KB of its rows (64 bytes each).  K: the plane's
+// columns, a multiple of 32; its rows are padded to a multiple of 16.
+__device__ __forceinline__ int64_t q_at(int64_t row, int64_t k, int64_t K) {
+  return ((row >> 4) * (K >> 5) + (k >> 5)) * 512 + (row & 15) * 32 + (k & 31);
+}
 struct QGemm {
-  const uint16_t* A; int64_t lda, planeA;
-  const uint16_t* B; int64_t ldb, planeB;
+  const uint16_t* A; int64_t planeA;        // operand order
+  const uint16_t* B; int64_t ldb, planeB;   // operand order (ldb = 0), or rows
   int64_t M, N, K;        // columns i, rows j, depth of one plane
   int npairs;
   uint8_t pa[4], pb[4];

@@ -114,7 +114,7 @@ struct PrepArgs {
   uint16_t* out; int64_t plane;
   int planes;           // 0: none
   bool raw;             // 16-bit x as it is; else float16 terms of x times 2^pow2_shift(rowmax)
-  bool frags;           // planes in the order of qskinny.hip's operands, else rows of Kp
+  bool frags;           // planes in the order of qskinny.hip's operands, else of qgemm.hip's
   bool vec;             // rows of x can be read 8 elements at a time
   int segs;             // workgroups per row (1 where a row's sum or maximum is wanted)
   uint32_t* rowmax;
@@ -188,7 +188,7 @@ __global__ __launch_bounds__(256) void q_prep_kernel(PrepArgs A) {
     }
     // operand order: step of 32 columns by step, lane (j / 8 % 4) 16 + row % 16
     uint16_t* dst = A.out + (A.frags ? ((row >> 4) * (A.Kp >> 5) + (j >> 5)) * 512 + ((j >> 3 & 3) * 16 + (row & 15)) * 8
-                                     : row * A.Kp + j);
+                                     : q_at(row, j, A.Kp));
     *reinterpret_cast<v4u*>(dst) = o[0];
     if (A.planes > 1) *reinterpret_cast<v4u*>(dst + A.plane) = o[1];
   }
@@ -233,8 +233,8 @@ __global__ __launch_bounds__(64 * WAVES) void q_unpack_kernel(QLayer L, int tile
     for (int s = 0; s < q_steps(FMT); ++s) {
       const int64_t j0 = (((int64_t)c * q_steps(FMT) + s) * 4 + (lane >> 4)) * 8;
       v4u e = q_decode<FMT, T>(L, lds, code, s);
-      if (i >= L.m || j0 >= Kp) continue;
-      uint16_t* dst = out + row * Kp + j0;
+      if (j0 >= Kp) continue;
+      uint16_t* dst = out + q_at(row, j0, Kp);
       if (planes == 0) {
         // columns past the last hold zero, whatever their codes
         if (j0 + 8 > L.n) {
@@ -246,7 +246,7 @@ __global__ __launch_bounds__(64 * WAVES) void q_unpack_kernel(QLayer L, int tile
       } else if constexpr (T::HALF) {
         float v[8];
         v4u o[2];
-        weights8(L, i, j0, e, mid, f, v);
+        weights8(L, min(i, L.m - 1), j0, e, mid, f, v);
         weight_terms(v, o);
         *reinterpret_cast<v4u*>(dst) = o[0];
         if (planes > 1) *reinterpret_cast<v4u*>(dst + plane) = o[1];
@@ -319,7 +319,7 @@ __global__ __launch_bounds__(64 * WAVES) void q_unpack_t_kernel(QLayer L, int64_
           const int64_t j = ((int64_t)c * q_steps(FMT) + s) * 32 + col;
           const int64_t r = strip * ROWS + piece * 8;
           if (j < L.n && r < mp)
-            *reinterpret_cast<v4u*>(out + p * plane + j * mp + r) =
+            *reinterpret_cast<v4u*>(out + p * plane + q_at(j, r, mp)) =
                 *reinterpret_cast<const v4u*>(tl + col * PITCH + piece * 8);
         }
         __syncthreads();
@@ -495,7 +495,7 @@ __global__ __launch_bounds__(256) void q_grad_tile_kernel(DuArgs A) {
       const float g = pow2(pow2_shift(A.dmax[t]));
 #pragma unroll
       for (int q = 0; q < 4; ++q) v[q] *= f[q] * g;
-      put_terms(A.d + t * A.mp + i, A.plane_d, A.planes_d, v);
+      put_terms(A.d + q_at(t, i, A.mp), A.plane_d, A.planes_d, v);
     }
   }
   if (!is_x && !A.want_t) return;
@@ -512,8 +512,8 @@ __global__ __launch_bounds__(256) void q_grad_tile_kernel(DuArgs A) {
     const float g = pow2(pow2_shift(is_x ? A.xmax[r] : A.tmax[r]));
 #pragma unroll
     for (int q = 0; q < 4; ++q) v[q] *= g;
-    if (is_x) put_terms(A.xt + r * A.tp + t0 + cx * 4, A.plane_x, A.planes_x, v);
-    else put_terms(A.dt + r * A.tp + t0 + cx * 4, A.plane_t, A.planes_t, v);
+    if (is_x) put_terms(A.xt + q_at(r, t0 + cx * 4, A.tp), A.plane_x, A.planes_x, v);
+    else put_terms(A.dt + q_at(r, t0 + cx * 4, A.tp), A.plane_t, A.planes_t, v);
   }
 }
 
@@ -662,6 +662,8 @@ bool use_skinny(const QLinearArgs& A) {
 // 14336 columns, 8 tokens 16.4 | 18.6, 16 tokens 20.8 | 19.3.
 constexpr int64_t Q_DIRECT = 131072;
 
+int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }
+
 struct Carve {
   char* base;
   size_t at = 0;
@@ -697,7 +699,7 @@ hipError_t forward(const QLinearArgs& A, char* base, size_t* bytes, hipStream_t 
   const int WP = !weights ? 0 : A.dtype == DT_BF16 ? 1 : 2;   // terms of a weight (0: entries)
   const bool sums = !skinny && !grouped && L.has_offset();
   Carve W{base};
-  const int64_t xrows = skinny ? (A.t + 15) / 16 * 16 : A.t, plane = xrows * Kp;
+  const int64_t xrows = up16(A.t), plane = xrows * Kp;
   uint16_t* xp = W.take<uint16_t>((size_t)XP * plane * 2);
   float* xs = W.take<float>((size_t)A.t * 4);
   uint32_t* rowmax = W.take<uint32_t>((size_t)A.t * 4);
@@ -742,7 +744,6 @@ hipError_t forward(const QLinearArgs& A, char* base, size_t* bytes, hipStream_t 
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   const uint16_t* x = direct ? static_cast<const uint16_t*>(A.x) : xp;
-  const int64_t ldx = direct ? A.ldx : Kp;
   QOut O;
   memset(&O, 0, sizeof(O));
   O.y = A.y; O.ldy = A.ldy;
@@ -766,8 +767,8 @@ hipError_t forward(const QLinearArgs& A, char* base, size_t* bytes, hipStream_t 
     e = bf16 ? unpack<OpBf16>(L, (int)(r0 / 16), tiles, Kp, WP, refs, wp, rows * Kp, st)
              : unpack<OpF16>(L, (int)(r0 / 16), tiles, Kp, WP, refs, wp, rows * Kp, st);
     if (e != hipSuccess) return e;
-    g.A = wp; g.lda = Kp; g.planeA = rows * Kp;
-    g.B = x; g.ldb = ldx; g.planeB = plane;
+    g.A = wp; g.planeA = rows * Kp;
+    g.B = x; g.ldb = direct ? A.ldx : 0; g.planeB = plane;
     g.M = nr; g.N = A.t; g.K = Kp;
     g.bf16 = bf16;
     g.O = O;
@@ -805,8 +806,8 @@ hipError_t backward(const QLinearGrad& A, char* base, size_t* bytes, hipStream_t
   D.t = A.t; D.m = L.m; D.n = L.n;
   D.mp = mp; D.tp = tp;
   D.rowtiles = mp / 64; D.xtiles = up64(L.n) / 64;
-  D.plane_d = A.t * mp; D.plane_t = L.m * tp; D.plane_x = L.n * tp;
-  const int64_t plane_w = L.n * mp, ttiles = tp / 64;
+  D.plane_d = up16(A.t) * mp; D.plane_t = up16(L.m) * tp; D.plane_x = up16(L.n) * tp;
+  const int64_t plane_w = up16(L.n) * mp, ttiles = tp / 64;
   QGemm gx, gw;
   memset(&gx, 0, sizeof(gx));
   memset(&gw, 0, sizeof(gw));
@@ -881,8 +882,8 @@ hipError_t backward(const QLinearGrad& A, char* base, size_t* bytes, hipStream_t
   }
   if (A.need_dx) {
     if ((e = unpack_t(L, mp, WP, D.refs, wt, plane_w, st)) != hipSuccess) return e;
-    gx.A = wt; gx.lda = mp; gx.planeA = plane_w;
-    gx.B = D.d; gx.ldb = mp; gx.planeB = D.plane_d;
+    gx.A = wt; gx.planeA = plane_w;
+    gx.B = D.d; gx.planeB = D.plane_d;
     gx.M = L.n; gx.N = A.t; gx.K = mp;
     gx.O.y = A.dx; gx.O.ldy = A.lddx;
     gx.O.rowmax = D.dmax;
@@ -894,8 +895,8 @@ hipError_t backward(const QLinearGrad& A, char* base, size_t* bytes, hipStream_t
     if ((e = launch_q_gemm(gx, part, st)) != hipSuccess) return e;
   }
   if (A.need_dlayer) {
-    gw.A = D.xt; gw.lda = tp; gw.planeA = D.plane_x;
-    gw.ldb = tp; gw.planeB = D.plane_t;
+    gw.A = D.xt; gw.planeA = D.plane_x;
+    gw.planeB = D.plane_t;
     gw.M = L.n; gw.K = tp;
     gw.O.colmax = D.xmax;
     gw.O.mid = -1;
