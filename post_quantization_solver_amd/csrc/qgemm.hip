@@ -66,7 +66,7 @@ __device__ __forceinline__ void fetch_step(Cursor<BM, LOADS>& c, const QGemm& g,
     load_lds(c.p[l], stage + r * BK);
     c.p[l] += r < BM || !g.ldb ? 1024 : BK * 2;
   }
-  if (++c.k == c.kts) c.seek(g, i0, j0, wave, off, c.pair + 1, 0);
+  ++c.k;
 }
 
 // One wave's operands of a step.
@@ -83,7 +83,6 @@ __device__ __forceinline__ void read_step(const uint16_t* stage, int wm, int wn,
   for (int j = 0; j < SN; ++j) f.b[j] = *reinterpret_cast<const v4u*>(Bs + j * 16 * BK);
 #pragma unroll
   for (int i = 0; i < SM; ++i) f.a[i] = *reinterpret_cast<const v4u*>(As + i * 16 * BK);
-  __builtin_amdgcn_sched_barrier(0);   // before the products
 }
 template <typename T, int SM, int SN>
 __device__ __forceinline__ void multiply(const Frags<SM, SN>& f, v4f (&acc)[SM][SN]) {
@@ -91,6 +90,24 @@ __device__ __forceinline__ void multiply(const Frags<SM, SN>& f, v4f (&acc)[SM][
   for (int i = 0; i < SM; ++i)
 #pragma unroll
     for (int j = 0; j < SN; ++j) acc[i][j] = T::mfma(f.a[i], f.b[j], acc[i][j]);
+}
+
+// A step's instructions in turn: loads and reads go out between the products.
+template <int MFMAS, int READS, int LOADS>
+__device__ __forceinline__ void interleave() {
+  constexpr int MFMA = 0x8, VMEM = 0x10, DS_READ = 0x100;
+  static_assert(READS + LOADS <= MFMAS, "a product before each");
+#pragma unroll
+  for (int k = 0; k < LOADS; ++k) {
+    __builtin_amdgcn_sched_group_barrier(MFMA, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(VMEM, 1, 0);
+  }
+#pragma unroll
+  for (int k = 0; k < READS; ++k) {
+    __builtin_amdgcn_sched_group_barrier(MFMA, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(DS_READ, 1, 0);
+  }
+  __builtin_amdgcn_sched_group_barrier(MFMA, MFMAS - READS - LOADS, 0);
 }
 
 template <typename T, int BM, int BN, int WM, int WN>
@@ -149,17 +166,22 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void q_gemm_kernel(QGemm g, float*
   // between its reads and its products, so that these wait for the reads of the
   // step before alone.
   for (int s = 0; s < STAGES; ++s)
-    if (kt0 + s < kt1) fetch_step(at, g, i0, j0, wave, off, lds[s]);
+    if (kt0 + s < kt1) {
+      fetch_step(at, g, i0, j0, wave, off, lds[s]);
+      if (at.k == kts) at.seek(g, i0, j0, wave, off, at.pair + 1, 0);
+    }
   if (kt0 + STAGES <= kt1) wait_stage<(STAGES - 1) * LOADS>(); else wait_stage<0>();
   read_step<BM, SM, SN>(lds[0], wm, wn, r, kb, f0);
   int here = 0, kt = kt0;   // kt's stage
 #define Q_STEP(cur, nxt)                                                                                     \
   {                                                                                                          \
     wait_stage<(STAGES - 2) * LOADS>();                                                                      \
-    fetch_step(at, g, i0, j0, wave, off, lds[here]);                                                               \
+    fetch_step(at, g, i0, j0, wave, off, lds[here]);                                                         \
     here = here + 1 == STAGES ? 0 : here + 1;                                                                \
     read_step<BM, SM, SN>(lds[here], wm, wn, r, kb, nxt);                                                    \
     multiply<T, SM, SN>(cur, acc);                                                                           \
+    interleave<SM * SN, SM + SN, LOADS>();                                                                   \
+    if (at.k == kts) at.seek(g, i0, j0, wave, off, at.pair + 1, 0);                                          \
   }
   for (; kt + STAGES + 1 < kt1; kt += 2) {
     Q_STEP(f0, f1);
@@ -169,7 +191,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void q_gemm_kernel(QGemm g, float*
 #define Q_STEP(kt, cur, nxt)                                                                                 \
   {                                                                                                          \
     if ((kt) + STAGES <= kt1) wait_stage<(STAGES - 2) * LOADS>(); else wait_stage<0>();                      \
-    if ((kt) + STAGES < kt1) fetch_step(at, g, i0, j0, wave, off, lds[here]);                                      \
+    if ((kt) + STAGES < kt1) {                                                                               \
+      fetch_step(at, g, i0, j0, wave, off, lds[here]);                                                       \
+      if (at.k == kts) at.seek(g, i0, j0, wave, off, at.pair + 1, 0);                                        \
+    }                                                                                                        \
     here = here + 1 == STAGES ? 0 : here + 1;                                                                \
     if ((kt) + 1 < kt1) read_step<BM, SM, SN>(lds[here], wm, wn, r, kb, nxt);                                \
     multiply<T, SM, SN>(cur, acc);                                                                           \
