@@ -17,7 +17,6 @@ namespace {
 
 constexpr int BK = 32;
 constexpr int gemm_stages(int BM, int BN) { return BM + BN <= 256 ? 4 : BM + BN <= 384 ? 6 : 5; }
-typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
 // Waits until at most N of this wave's global -> LDS loads are on their way,
 // and for its LDS reads; then for the workgroup.  (The builtin, so that the
@@ -25,11 +24,9 @@ typedef __attribute__((address_space(3))) void* lds_ptr_t;
 // products.)
 template <int N>
 __device__ __forceinline__ void wait_stage() {
-  static_assert(N < 64, "the counter has six bits");
-  constexpr int EXP_ANY = 7 << 4, LGKM_0 = 0 << 8;
   asm volatile("" ::: "memory");
   __builtin_amdgcn_sched_barrier(0);   // the products before stay before
-  __builtin_amdgcn_s_waitcnt((N & 15) | EXP_ANY | LGKM_0 | (N >> 4) << 14);
+  __builtin_amdgcn_s_waitcnt(q_waitcnt(N));
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
@@ -53,17 +50,14 @@ struct Cursor {
   }
 };
 
-// Straight into an LDS stage: a KB per wave.
-__device__ __forceinline__ void load_lds(const char* src, uint16_t* dst) {
-  __builtin_amdgcn_global_load_lds(src, (lds_ptr_t)dst, 16, 0, 0);
-}
+// Straight into an LDS stage.
 template <int BM, int LOADS>
 __device__ __forceinline__ void fetch_step(Cursor<BM, LOADS>& c, const QGemm& g, int64_t i0, int64_t j0, int wave,
                                            const uint32_t* off, uint16_t* stage) {
 #pragma unroll
   for (int l = 0; l < LOADS; ++l) {
     const int r = (wave * LOADS + l) * 16;
-    load_lds(c.p[l], stage + r * BK);
+    q_load_lds(c.p[l], stage + r * BK);
     c.p[l] += r < BM || !g.ldb ? 1024 : BK * 2;
   }
   ++c.k;

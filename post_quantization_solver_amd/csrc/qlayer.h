@@ -43,7 +43,7 @@ struct QLayer {
   const float* levels;   // d = 1
   bool uniform;          // d = 1: levels[q] = levels[0] + q (levels[1] - levels[0]), exactly
   int K;
-  const uint32_t* lut;   // QF_E8: sign-magnitude nibbles of 2 e, nibble {0,2,4,6,1,3,5,7}[q] = coordinate q
+  const uint32_t* lut;   // QF_E8: nibbles 8 + 2 e, coordinate 2 p in nibble p, 2 p + 1 in nibble p + 4
   const uint16_t* map;   // QF_E8: code -> packed code
   int lut_entries, pairs;
   const float* e32;      // d = 8: K x 8
@@ -81,14 +81,23 @@ __device__ __forceinline__ float q_centre(const QLayer& L) {
   return L.fmt == QF_NIB || L.fmt == QF_BYTE ? L.levels[L.K / 2] : 0.f;
 }
 
-// Fills the decoder's LDS table (every thread of the workgroup; the caller synchronizes).
+// 16 bytes a lane from src (this lane's) to dst (the wave's, 1 KB), past the registers.
+typedef __attribute__((address_space(3))) void* q_lds_ptr;
+__device__ __forceinline__ void q_load_lds(const void* src, void* dst) {
+  __builtin_amdgcn_global_load_lds(src, (q_lds_ptr)dst, 16, 0, 0);
+}
+// The operand of s_waitcnt: at most n loads on their way, and no LDS operation.
+constexpr int q_waitcnt(int n) { return (n & 15) | 7 << 4 | (n >> 4) << 14; }
+
+// Fills the decoder's LDS table (every thread of the workgroup; the caller
+// synchronizes, for E8 after a wait for the loads: q_lut_wait).
 template <int FMT, typename T>
 __device__ __forceinline__ void q_lut_fill(const QLayer& L, uint32_t* lut, int nthreads) {
   const int t = threadIdx.x;
   if constexpr (FMT == QF_E8) {
     const int quads = (L.lut_entries + 3) / 4;   // the table is padded to 16 bytes
     for (int i = t; i < quads; i += nthreads)
-      reinterpret_cast<uint4*>(lut)[i] = reinterpret_cast<const uint4*>(L.lut)[i];
+      q_load_lds(reinterpret_cast<const uint4*>(L.lut) + i, reinterpret_cast<uint4*>(lut) + (i & ~63));
   } else if constexpr (FMT == QF_NIB || FMT == QF_BYTE) {
     constexpr int BITS = FMT == QF_NIB ? 4 : 6;
     const float mid = q_centre(L);
@@ -97,6 +106,52 @@ __device__ __forceinline__ void q_lut_fill(const QLayer& L, uint32_t* lut, int n
       lut[i] = T::pack(L.levels[lo < L.K ? lo : 0] - mid, L.levels[hi < L.K ? hi : 0] - mid);
     }
   }
+}
+
+// Waits for the table's loads; `after` loads went out behind them.
+template <int AFTER>
+__device__ __forceinline__ void q_lut_wait() {
+  static_assert(AFTER < 64, "the counter has six bits");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(q_waitcnt(AFTER));
+  asm volatile("" ::: "memory");
+}
+
+// The table's nibbles of a packed E8 code (its low 16 bits): 2 i + sign for the
+// i-th of `pairs` points whose negative is in the codebook too, pairs + i for
+// entry i beyond them; either way the entry is max(code / 2, code - pairs), and
+// an odd code negates it (a lone entry with an odd code is stored negated).
+// Nibbles are 1 to 15, so that 16 - v goes through all eight without a carry.
+__device__ __forceinline__ uint32_t q_e8_nibbles(const QLayer& L, const uint32_t* lut, uint32_t word) {
+  const uint32_t code = word & 0xffffu;
+  const uint32_t v = lut[max((int)(code >> 1), (int)code - L.pairs)];
+  const uint32_t odd = (uint32_t)((int)(word << 31) >> 31);
+  return (v ^ odd) + (odd & 0x11111111u);
+}
+
+// The nibbles as entries, or, in bfloat16, lifted: 64 + q / 2 (the entry and 68).
+template <typename T>
+__device__ __forceinline__ v4u q_e8_entries(uint32_t v) {
+  v4u r;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const uint32_t q = (v >> (4 * b)) & 0x000f000fu;
+    if constexpr (T::HALF) {   // 512 + q / 2 is 0x6000 | q
+      r[b] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(v2h, q | 0x60006000u) +
+                                              (v2h){(_Float16)-516.f, (_Float16)-516.f});
+    } else {                   // 64 + q / 2 is 0x4280 | q
+      const uint32_t u = q | 0x42804280u;
+      r[b] = __builtin_amdgcn_perm(__float_as_uint(__uint_as_float(u & 0xffff0000u) - 68.f),
+                                   __float_as_uint(__uint_as_float(u << 16) - 68.f), 0x07060302u);
+    }
+  }
+  return r;
+}
+__device__ __forceinline__ v4u q_e8_lifted(uint32_t v) {
+  v4u r;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) r[b] = ((v >> (4 * b)) & 0x000f000fu) | 0x42804280u;
+  return r;
 }
 
 // The eight entries of step s from a lane's 16 bytes of codes.
@@ -114,32 +169,7 @@ __device__ __forceinline__ v4u q_decode(const QLayer& L, const uint32_t* lut, co
       r[b] = lut[(h & 63u) | ((h >> 10) & 0xfc0u)];
     }
   } else if constexpr (FMT == QF_E8) {
-    // Packed code: 2 i + sign for the i-th of `pairs` points whose negative is
-    // in the codebook too, pairs + i for entry i beyond them; either way the
-    // entry is max(code / 2, code - pairs), and an odd code flips its signs
-    // (a lone entry with an odd code is stored flipped).
-    const uint32_t code = (w[s >> 1] >> (16 * (s & 1))) & 0xffffu;
-    const int e = max((int)(code >> 1), (int)code - L.pairs);
-    const uint32_t v = lut[e] ^ ((uint32_t)((int)(code << 31) >> 31) & 0x88888888u);
-    const uint32_t s0 = v & 0x07070707u, s1 = (v >> 4) & 0x07070707u;
-    const uint32_t g0 = (v << 4) & 0x80808080u, g1 = v & 0x80808080u;
-    // bytes of the 16-bit values of 0, 1/2, .., 7/2
-    uint32_t h0, h1, l0 = 0, l1 = 0;
-    if constexpr (T::HALF) {
-      h0 = __builtin_amdgcn_perm(0x43424140u, 0x3e3c3800u, s0);
-      h1 = __builtin_amdgcn_perm(0x43424140u, 0x3e3c3800u, s1);
-    } else {
-      h0 = __builtin_amdgcn_perm(0x40404040u, 0x3f3f3f00u, s0);
-      h1 = __builtin_amdgcn_perm(0x40404040u, 0x3f3f3f00u, s1);
-      l0 = __builtin_amdgcn_perm(0x60402000u, 0xc0800000u, s0);
-      l1 = __builtin_amdgcn_perm(0x60402000u, 0xc0800000u, s1);
-    }
-    h0 |= g0;
-    h1 |= g1;
-    r[0] = __builtin_amdgcn_perm(h0, l0, 0x05010400u);
-    r[1] = __builtin_amdgcn_perm(h0, l0, 0x07030602u);
-    r[2] = __builtin_amdgcn_perm(h1, l1, 0x05010400u);
-    r[3] = __builtin_amdgcn_perm(h1, l1, 0x07030602u);
+    r = q_e8_entries<T>(q_e8_nibbles(L, lut, w[s >> 1] >> (16 * (s & 1))));
   } else {
     const uint32_t code = (w[s >> 1] >> (16 * (s & 1))) & 0xffffu;
     const float4* e = reinterpret_cast<const float4*>(L.e32 + (size_t)code * 8);
@@ -152,12 +182,16 @@ __device__ __forceinline__ v4u q_decode(const QLayer& L, const uint32_t* lut, co
   return r;
 }
 
-// The same for uniform levels, by arithmetic: q_base + code (bfloat16: 128 + q is
-// 0x4300 | q; the caller takes q_base off, see qskinny.hip) or, in float16, whose
-// 1024 + q is 0x6400 | q and which adds in pairs, code - K / 2 itself.
-constexpr float Q_BASE = 128.f;
+// What lifted entries carry (see qskinny.hip).
+template <int FMT>
+__device__ __forceinline__ float q_lift(const QLayer& L) {
+  return FMT == QF_E8 ? 68.f : 128.f + (float)(L.K / 2);
+}
+// Uniform levels by arithmetic alone, in units of their step: in bfloat16 lifted,
+// 128 + q is 0x4300 | q; in float16, whose 1024 + q is 0x6400 | q and which adds
+// in pairs, the entry itself, code - K / 2.
 template <int FMT, typename T>
-__device__ __forceinline__ v4u q_decode_uniform(const QLayer& L, const uint4& c, int s) {
+__device__ __forceinline__ v4u q_decode_lifted(const QLayer& L, const uint4& c, int s) {
   const uint32_t w[4] = {c.x, c.y, c.z, c.w};
   v4u r;
 #pragma unroll
@@ -369,13 +403,10 @@ __device__ __forceinline__ void q_entries4(const QLayer& L, uint32_t code, int64
 #pragma unroll
     for (int k = 0; k < 4; ++k) e[k] = L.levels[(code >> (8 * (k >> 1) + 16 * (k & 1))) & 63u];
   } else if (L.fmt == QF_E8) {
-    const int c = (int)code;
-    const uint32_t v = L.lut[max(c >> 1, c - L.pairs)] ^ (c & 1 ? 0x88888888u : 0u);
+    const uint32_t v = q_e8_nibbles(L, L.lut, code);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t nib = v >> (8 * k + 4 * half);
-      e[k] = 0.5f * (float)(nib & 7u) * (nib & 8u ? -1.f : 1.f);
-    }
+    for (int k = 0; k < 4; ++k)
+      e[k] = 0.5f * (float)((int)((v >> (8 * half + 4 * (k >> 1) + 16 * (k & 1))) & 15u) - 8);
   } else {
     const float4 q = *reinterpret_cast<const float4*>(L.e32 + (size_t)code * 8 + half * 4);
     e[0] = q.x; e[1] = q.y; e[2] = q.z; e[3] = q.w;

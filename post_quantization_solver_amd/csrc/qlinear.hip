@@ -221,6 +221,7 @@ __global__ __launch_bounds__(64 * WAVES) void q_unpack_kernel(QLayer L, int tile
   extern __shared__ __attribute__((aligned(16))) uint32_t lds[];
   const int lane = threadIdx.x & 63, wave = wave_id();
   q_lut_fill<FMT, T>(L, lds, 64 * WAVES);
+  if (FMT == QF_E8) q_lut_wait<0>();
   __syncthreads();
   const float mid = q_centre(L);
   const int64_t total = (int64_t)tiles * L.chunks;
@@ -271,6 +272,7 @@ __global__ __launch_bounds__(64 * WAVES) void q_unpack_t_kernel(QLayer L, int64_
   uint16_t* tl = reinterpret_cast<uint16_t*>(lds + lut_words);   // 32 columns x PITCH
   const int lane = threadIdx.x & 63, wave = wave_id();
   q_lut_fill<FMT, T>(L, lds, 64 * WAVES);
+  if (FMT == QF_E8) q_lut_wait<0>();
   __syncthreads();
   const float mid = q_centre(L);
   const int64_t strips = (mp + ROWS - 1) / ROWS, total = strips * L.chunks;
@@ -955,7 +957,7 @@ hipError_t launch_q_grad(const QLinearGrad& A, void* ws, hipStream_t st) {
   return backward(A, static_cast<char*>(ws), nullptr, st);
 }
 
-// E8 prefixes: the sign-magnitude table and the codes' places in it.
+// E8 prefixes: the table of nibbles and the codes' places in it.
 //
 // Within a shell (points of one norm, in lexicographic order) the negative of
 // point k of N is point N - 1 - k, so a point whose negative is among the first
@@ -967,7 +969,7 @@ bool q_e8_tables(const float* cb, int64_t K, uint32_t* lut, uint16_t* map, int* 
       const float x = cb[c * 8 + q];
       const int h = (int)(2.f * (x < 0 ? -x : x));
       if (h > 7 || 0.5f * h != (x < 0 ? -x : x)) return false;
-      *v |= (uint32_t)(h | (x < 0 ? 8 : 0)) << (4 * (q < 4 ? 2 * q : 2 * q - 7));
+      *v |= (uint32_t)(x < 0 ? 8 - h : 8 + h) << (4 * (q / 2 + 4 * (q % 2)));
     }
     return true;
   };
@@ -996,7 +998,7 @@ bool q_e8_tables(const float* cb, int64_t K, uint32_t* lut, uint16_t* map, int* 
         ++pair;
       } else {
         const int64_t code = 2 * (int64_t)*pairs + lone;
-        lut[*pairs + lone] = code & 1 ? v ^ 0x88888888u : v;
+        lut[*pairs + lone] = code & 1 ? 0x11111110u - v : v;
         map[s0 + k] = (uint16_t)code;
         ++lone;
       }

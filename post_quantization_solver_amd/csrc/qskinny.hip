@@ -5,11 +5,12 @@
 // ever formed, so none is rounded.  The sum over x rides along as one more
 // matrix product, with a row of ones in the layer's place.  float32 x enters as
 // two float16 terms (22 bits) of x times a power of two per token.
-// Evenly spaced levels need no table: 128 + code is the code's bits under a
-// constant exponent in bfloat16.  The 128 and the middle level come off again
-// unit by unit (128 columns), with the sum over x, before their part could
-// outgrow float32's bits (a unit's sum is rounded at 2^-24 of some 140 sum |x|:
-// far under half a bfloat16 step of the result).
+// With bfloat16 x, E8's entries and evenly spaced levels enter lifted: 64 + q / 2
+// and 128 + q are the code's bits under a constant exponent, two instructions a
+// pair where the entry itself takes six.  The lift comes off again unit by unit
+// (128 columns), with the sum over x, before its part could outgrow float32's
+// bits (a unit's sum is rounded at 2^-24 of some 140 sum |x|: far under half a
+// bfloat16 step of the result).
 //
 // Bound.  HBM traffic is the packed codes (2 bits a weight for E8); what the
 // waves wait on is their own decoding (some 30 instructions a step of 64 blocks)
@@ -37,15 +38,21 @@ namespace mpq {
 namespace {
 
 // Sixteen waves where a wave's operands fit 128 registers, else eight.
-constexpr int sk_waves(int XP, int NT, int R) { return XP * NT * R == 1 ? 16 : 8; }
+constexpr int sk_waves(int XP, int NT, int R, bool grouped) { return XP * NT * R == 1 && !grouped ? 16 : 8; }
+
+// Whether entries are looked up: all but evenly spaced levels and those of the
+// generic codebook, which come straight from memory.
+constexpr bool sk_table(int f, bool uni) { return f == QF_E8 || (f != QF_VEC && !uni); }
 
 struct SkinnyArgs {
   QLayer L;
   const uint16_t* x; int64_t ldx, planex;   // ldx = 0: operand order
   int kblocks;          // blocks of eight columns that x holds
+  uint32_t xbytes;      // of one plane
   int64_t t;
   bool has_offset;
   int lut_words;
+  uint32_t ginv;        // 2^32 over a group's units, rounded up; 0: one unit
   QOut O;
 };
 
@@ -53,101 +60,122 @@ struct SkinnyArgs {
 // whole chunk of two.
 constexpr int unit_steps(int f) { return q_steps(f) < 4 ? q_steps(f) : 4; }
 
+// 16 or 8 bytes at p[at], zeros from `bytes` on.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00027000);
+}
+__device__ __forceinline__ v4u load_words(const void* p, uint32_t bytes, uint32_t at) {
+  return __builtin_amdgcn_raw_buffer_load_b128(buffer_of(p, bytes), at, 0, 0);
+}
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ v2u load_half(const void* p, uint32_t bytes, uint32_t at) {
+  return __builtin_amdgcn_raw_buffer_load_b64(buffer_of(p, bytes), at, 0, 0);
+}
+template <int N>
+__device__ __forceinline__ uint4 load_buffer(const void* p, uint32_t bytes, uint32_t at) {
+  if constexpr (N == 16) {
+    const v4u w = load_words(p, bytes, at);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+    const v2u w = load_half(p, bytes, at);
+    return make_uint4(w[0], w[1], 0, 0);
+  }
+}
+__device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0); }
+
 template <int FMT, typename T, int XP, int NT, int R, bool GROUPED, bool UNI>
-__global__ __launch_bounds__(64 * sk_waves(XP, NT, R)) void q_skinny_kernel(SkinnyArgs A) {
+__global__ __launch_bounds__(64 * sk_waves(XP, NT, R, GROUPED)) void q_skinny_kernel(SkinnyArgs A) {
   extern __shared__ __attribute__((aligned(16))) uint32_t lds[];
   constexpr int US = unit_steps(FMT), UPC = q_steps(FMT) / US;
-  constexpr int SUBS = R * NT, SK_WAVES = sk_waves(XP, NT, R);
+  constexpr int SUBS = R * NT, SK_WAVES = sk_waves(XP, NT, R, GROUPED);
+  constexpr bool TABLE = sk_table(FMT, UNI);
   static_assert(SUBS <= SK_WAVES, "a wave adds up one subtile");
   // one subtile's worth of sums beside the table, or all of them over it once
   // no more tile needs it (E8), or beside it (the others' tables are small)
   constexpr bool OVER = FMT == QF_E8;
   uint32_t* lut = lds;
-  v4f* red = reinterpret_cast<v4f*>(lds + (UNI ? 0 : A.lut_words));
+  v4f* red = reinterpret_cast<v4f*>(lds + (TABLE ? A.lut_words : 0));
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int r = lane & 15, kb = lane >> 4;
   const int64_t tok0 = (int64_t)blockIdx.y * (16 * NT);
   const int tgs = (A.L.tiles + R - 1) / R, units = A.L.chunks * UPC;
   // tokens past the last repeat it: a token's sums are its own column's
-  const uint16_t* xrow[NT];
-  const int xstep = A.ldx ? 32 : 512;   // elements from step to step
+  uint32_t xrow[NT];   // in bytes
+  const int xstep = A.ldx ? 64 : 1024;
 #pragma unroll
   for (int n = 0; n < NT; ++n)
-    xrow[n] = A.ldx ? A.x + min(tok0 + n * 16 + r, A.t - 1) * A.ldx + kb * 8
-                    : A.x + min(tok0 / 16 + n, (A.t - 1) / 16) * ((int64_t)units * US * 512) + lane * 8;
+    xrow[n] = A.ldx ? (uint32_t)(min(tok0 + n * 16 + r, A.t - 1) * A.ldx * 2) + kb * 16
+                    : (uint32_t)(min(tok0 / 16 + n, (A.t - 1) / 16) * (units * US)) * 1024u + lane * 16;
 
   struct Codes {
     uint4 v[R];
+    float scale[R][4], offset[R][4];   // GROUPED: of the unit's group
   };
   struct Xs {
     v4u v[US][NT][XP];
   };
+  // No load stands under a branch (past the last unit and past x's columns the
+  // buffers' bounds give zeros): what a use waits for is then a constant number of
+  // loads back, and the ones after it stay on their way.
   auto load_codes = [&](Codes& c, int tg, int u) {
 #pragma unroll
     for (int q = 0; q < R; ++q) {   // a tile past the last repeats it; its sums are not stored
-      const char* p = reinterpret_cast<const char*>(
-          A.L.packed + ((size_t)min(tg * R + q, A.L.tiles - 1) * A.L.chunks + u / UPC) * 64 + lane);
-      if constexpr (UPC == 1) {
-        c.v[q] = *reinterpret_cast<const uint4*>(p);
-      } else {
-        const uint2 h = *reinterpret_cast<const uint2*>(p + (u % UPC) * 8);
-        c.v[q] = make_uint4(h.x, h.y, 0, 0);
+      const int tile = min(tg * R + q, A.L.tiles - 1);
+      const uint4* p = A.L.packed + (size_t)tile * A.L.chunks * 64;
+      const uint32_t bytes = (uint32_t)A.L.chunks * 1024, at = (uint32_t)(u / UPC * 64 + lane) * 16 + u % UPC * 8;
+      c.v[q] = load_buffer<UPC == 1 ? 16 : 8>(p, bytes, at);
+      if constexpr (GROUPED) {
+        // the unit (a chunk) lies in one group
+        const uint32_t in = (uint32_t)min(u, units - 1);
+        const int64_t g = A.ginv ? __umulhi(in, A.ginv) : in;
+        const float* off = A.L.offset ? A.L.offset : A.L.scale;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const int64_t i = min((int64_t)tile * 16 + 4 * kb + v, A.L.m - 1) * A.L.G + g;
+          c.scale[q][v] = A.L.scale[i];
+          c.offset[q][v] = off[i];
+        }
       }
     }
   };
-  // (the lanes of tokens there are not load nothing and keep their zeros, or,
-  // where x is not loaded ahead, what the operand order holds for them)
-  bool there[NT];
+  auto load_x = [&](Xs& x, int u) {
 #pragma unroll
-  for (int n = 0; n < NT; ++n) there[n] = tok0 + n * 16 + r < A.t;
-  auto load_x = [&](Xs& x, int u, auto masked) {
-    const int64_t at = (int64_t)u * US * xstep;
-    const bool whole = (u + 1) * (US * 4) <= A.kblocks;
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-      if (!masked.value || there[n])
-#pragma unroll
-        for (int s = 0; s < US; ++s)
-#pragma unroll
-          for (int p = 0; p < XP; ++p) {
-            const v4u* src = reinterpret_cast<const v4u*>(xrow[n] + p * A.planex + at + s * xstep);
-            if (whole) {
-              x.v[s][n][p] = *src;
-            } else {
-              x.v[s][n][p] = (v4u){0u, 0u, 0u, 0u};
-              if ((u * US + s) * 4 + kb < A.kblocks) x.v[s][n][p] = *src;
-            }
-          }
-  };
-  // Codes come from HBM, a microsecond away: DEPTH units ahead.  x comes from the
-  // cache, one unit ahead where the registers allow it.
-  constexpr bool AHEAD = NT * XP <= 2;
-  constexpr int DEPTH = SK_WAVES == 16 ? 2 : 4;
-  Codes next[DEPTH];
-  Xs xnext;
-  if (AHEAD)
-#pragma unroll
-    for (int s = 0; s < US; ++s)
+    for (int s = 0; s < US; ++s) {
+      const bool in = (u * US + s) * 4 + kb < A.kblocks;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int p = 0; p < XP; ++p) xnext.v[s][n][p] = (v4u){0u, 0u, 0u, 0u};
-  auto load_first = [&](int tg) {
-#pragma unroll
-    for (int h = 0; h < DEPTH; ++h)
-      if (wave + h * SK_WAVES < units) load_codes(next[h], tg, wave + h * SK_WAVES);
-    if (AHEAD && wave < units) load_x(xnext, wave, std::true_type{});
+        for (int p = 0; p < XP; ++p)
+          x.v[s][n][p] = load_words(A.x + p * A.planex, A.xbytes, in ? xrow[n] + (uint32_t)((u * US + s) * xstep) : A.xbytes);
+    }
   };
-  load_first(blockIdx.x);
-  if (!UNI) {
+  // A unit's codes are loaded two units ahead, its x two or, where the registers
+  // are wanted, one.
+  constexpr int XD = NT * XP <= 2 ? 2 : 1;
+  Codes next[2];
+  Xs xs_[XD];
+  auto load_first = [&](int tg, int first) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {   // (in the order of their uses)
+      load_codes(next[h], tg, first + h * SK_WAVES);
+      if (h < XD) load_x(xs_[h], first + h * SK_WAVES);
+      keep_order();
+    }
+  };
+  if (TABLE) {
     q_lut_fill<FMT, T>(A.L, lut, 64 * SK_WAVES);
+    keep_order();
+  }
+  load_first(blockIdx.x, wave);
+  if (TABLE) {
+    if (FMT == QF_E8) q_lut_wait<2 * R + XD * US * NT * XP>();
     __syncthreads();
   }
-  const float mid = q_centre(A.L), step = UNI ? A.L.levels[1] - A.L.levels[0] : 1.f;
-  constexpr bool LIFTED = UNI && !T::HALF;   // decoded entries carry Q_BASE
-  const float lift = LIFTED ? Q_BASE + (float)(A.L.K / 2) : 0.f;
+  const float mid = q_centre(A.L), step = UNI && FMT != QF_E8 ? A.L.levels[1] - A.L.levels[0] : 1.f;
+  constexpr bool LIFTED = UNI && !T::HALF;   // decoded entries carry q_lift
+  const float lift = LIFTED ? q_lift<FMT>(A.L) : 0.f;
   for (int tg = blockIdx.x; tg < tgs; tg += gridDim.x) {
-    const bool more = tg + (int)gridDim.x < tgs;
+    const bool more = FMT == QF_E8 && tg + (int)gridDim.x < tgs;   // (the others' grids have a workgroup per tile)
     // this wave's part of the epilogue's operands, and the affine, early
     const int64_t tok = tok0 + wave % NT * 16 + r, i0 = (int64_t)(tg * R + wave / NT) * 16 + 4 * kb;
     float res[4] = {0.f, 0.f, 0.f, 0.f}, bias[4] = {0.f, 0.f, 0.f, 0.f};
@@ -175,46 +203,42 @@ __global__ __launch_bounds__(64 * sk_waves(XP, NT, R)) void q_skinny_kernel(Skin
 #pragma unroll
       for (int q = 0; q < R; ++q) acc[q][n] = (v4f){0.f, 0.f, 0.f, 0.f};
     }
-    for (int ub = wave; ub < units; ub += DEPTH * SK_WAVES)
+    auto unit = [&](Codes& code, Xs& x, int u, auto reload) {
+      // the table's words of the whole unit first: one wait for LDS, not one a step
+      uint32_t nib[R][US];
+      if constexpr (FMT == QF_E8)
 #pragma unroll
-    for (int h = 0; h < DEPTH; ++h) {
-      const int u = ub + h * SK_WAVES;
-      if (u >= units) break;
-      const Codes code = next[h];
-      if (u + DEPTH * SK_WAVES < units) load_codes(next[h], tg, u + DEPTH * SK_WAVES);
-      Xs x;
-      if (AHEAD) {
-        x = xnext;
-        if (u + SK_WAVES < units) load_x(xnext, u + SK_WAVES, std::true_type{});
-      } else {
-        load_x(x, u, std::false_type{});
-      }
-      constexpr bool FRESH = GROUPED || LIFTED;   // this unit's sums apart
+        for (int q = 0; q < R; ++q)
+#pragma unroll
+          for (int s = 0; s < US; ++s)
+            nib[q][s] = q_e8_nibbles(A.L, lut, (s < 2 ? code.v[q].x : code.v[q].y) >> (16 * (s & 1)));
+      keep_order();
+      constexpr bool FRESH = GROUPED || LIFTED;   // this unit's sum over x apart
       v4f z[R][NT], zx[NT];
-      if (FRESH) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          zx[n] = (v4f){0.f, 0.f, 0.f, 0.f};
+      for (int n = 0; n < NT; ++n) {
+        if (FRESH) zx[n] = (v4f){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int q = 0; q < R; ++q) z[q][n] = (v4f){0.f, 0.f, 0.f, 0.f};
-        }
+        for (int q = 0; q < R; ++q)
+          if (GROUPED) z[q][n] = (v4f){0.f, 0.f, 0.f, 0.f};
       }
 #pragma unroll
       for (int s = 0; s < US; ++s) {
 #pragma unroll
         for (int q = 0; q < R; ++q) {
           v4u w;
-          if constexpr (UNI) w = q_decode_uniform<FMT, T>(A.L, code.v[q], s);
+          if constexpr (FMT == QF_E8) w = UNI ? q_e8_lifted(nib[q][s]) : q_e8_entries<T>(nib[q][s]);
+          else if constexpr (UNI) w = q_decode_lifted<FMT, T>(A.L, code.v[q], s);
           else w = q_decode<FMT, T>(A.L, lut, code.v[q], s);
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int p = 0; p < XP; ++p) {
-              if (FRESH) z[q][n] = T::mfma(w, x.v[s][n][p], z[q][n]);
+              if (GROUPED) z[q][n] = T::mfma(w, x.v[s][n][p], z[q][n]);
               else acc[q][n] = T::mfma(w, x.v[s][n][p], acc[q][n]);
             }
         }
-        if (A.has_offset) {
+        if (LIFTED || A.has_offset) {
           const v4u one = {T::ONES, T::ONES, T::ONES, T::ONES};
 #pragma unroll
           for (int n = 0; n < NT; ++n)
@@ -229,31 +253,39 @@ __global__ __launch_bounds__(64 * sk_waves(XP, NT, R)) void q_skinny_kernel(Skin
 #pragma unroll
         for (int q = 0; q < R; ++q)
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+          for (int n = 0; n < NT; ++n) {
+            v4f& c = GROUPED ? z[q][n] : acc[q][n];
 #pragma unroll
-            for (int v = 0; v < 4; ++v) z[q][n][v] = fmaf(-lift, zx[n][v], z[q][n][v]);
+            for (int v = 0; v < 4; ++v) c[v] = fmaf(-lift, zx[n][v], c[v]);
+          }
       if (GROUPED) {
-        const int64_t g = (int64_t)u * (US * 32) / A.L.group;   // the unit (a chunk) lies in one group
 #pragma unroll
         for (int q = 0; q < R; ++q)
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
-            const int64_t i = min((int64_t)(tg * R + q) * 16 + 4 * kb + v, A.L.m - 1);
-            const float a = A.L.scale[i * A.L.G + g];
-            const float o = fmaf(a, mid, A.L.offset ? A.L.offset[i * A.L.G + g] : 0.f);
+            const float a = code.scale[q][v], o = fmaf(a, mid, A.L.offset ? code.offset[q][v] : 0.f);
 #pragma unroll
             for (int n = 0; n < NT; ++n) acc[q][n][v] = fmaf(a * step, z[q][n][v], fmaf(o, zx[n][v], acc[q][n][v]));
           }
-      } else if (LIFTED) {
+      } else if (LIFTED && A.has_offset) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          xs[n] += zx[n];
-#pragma unroll
-          for (int q = 0; q < R; ++q) acc[q][n] += z[q][n];
-        }
+        for (int n = 0; n < NT; ++n) xs[n] += zx[n];
       }
+      if (reload.value) {
+        load_codes(code, tg, u + 2 * SK_WAVES);
+        load_x(x, u + XD * SK_WAVES);
+        keep_order();
+      }
+    };
+    // (one way round the loop, so that every turn finds the same loads behind it)
+    int u = wave;
+    for (; u + SK_WAVES < units; u += 2 * SK_WAVES) {
+      unit(next[0], xs_[0], u, std::true_type{});
+      unit(next[1], xs_[XD - 1], u + SK_WAVES, std::true_type{});
     }
-    if (more) load_first(tg + gridDim.x);
+    if (u < units) unit(next[0], xs_[0], u, std::false_type{});
+    // (not under a branch either; after the last tile nothing)
+    if constexpr (FMT == QF_E8) load_first(more ? tg + gridDim.x : tg, more ? wave : units);
     if (!GROUPED) {
 #pragma unroll
       for (int q = 0; q < R; ++q)
@@ -315,15 +347,16 @@ __global__ __launch_bounds__(64 * sk_waves(XP, NT, R)) void q_skinny_kernel(Skin
       for (int k = 0; k < 4; ++k) mine[k] += res[k];
       store4(A.O.y, tok * A.O.ldy + i0, A.O.dtype, A.O.vec, live, mine);
     }
+    if (FMT != QF_E8) break;
   }
 }
 
 template <int FMT, typename T, int XP, int NT, int R, bool GROUPED, bool UNI>
 hipError_t launch(const SkinnyArgs& A, hipStream_t st) {
-  constexpr int SK_WAVES = sk_waves(XP, NT, R);
+  constexpr int SK_WAVES = sk_waves(XP, NT, R, GROUPED);
   const int tgs = (A.L.tiles + R - 1) / R;
   const int wgs = FMT == QF_E8 ? std::min(tgs, 256) : tgs;
-  const size_t table = UNI ? 0 : (size_t)A.lut_words * 4, tile = 64 * sizeof(v4f);
+  const size_t table = sk_table(FMT, UNI) ? (size_t)A.lut_words * 4 : 0, tile = 64 * sizeof(v4f);
   const size_t shared = FMT == QF_E8 ? std::max(table + (SK_WAVES - 1) * tile, R * NT * SK_WAVES * tile)
                                      : table + R * NT * SK_WAVES * tile;
   hipLaunchKernelGGL((q_skinny_kernel<FMT, T, XP, NT, R, GROUPED, UNI>),
@@ -334,7 +367,7 @@ hipError_t launch(const SkinnyArgs& A, hipStream_t st) {
 template <int FMT, typename T, int XP, int NT, bool GROUPED, bool UNI>
 hipError_t pick_rows(const SkinnyArgs& A, hipStream_t st) {
   // two tiles per workgroup share x's loads, once that still leaves every CU one
-  if constexpr (XP == 1 && NT <= 2 && (FMT == QF_E8 || FMT == QF_NIB))
+  if constexpr (XP == 1 && NT * (GROUPED ? 2 : 1) <= 2 && (FMT == QF_E8 || FMT == QF_NIB))
     if (A.L.tiles >= 512) return launch<FMT, T, XP, NT, 2, GROUPED, UNI>(A, st);
   return launch<FMT, T, XP, NT, 1, GROUPED, UNI>(A, st);
 }
@@ -361,7 +394,7 @@ hipError_t pick_format(const SkinnyArgs& A, hipStream_t st) {
   switch (A.L.fmt) {
     case QF_NIB: return grouped ? pick_levels<QF_NIB, T, XP, true>(A, st) : pick_levels<QF_NIB, T, XP, false>(A, st);
     case QF_BYTE: return grouped ? pick_levels<QF_BYTE, T, XP, true>(A, st) : pick_levels<QF_BYTE, T, XP, false>(A, st);
-    case QF_E8: return pick_tokens<QF_E8, T, XP, false, false>(A, st);
+    case QF_E8: return pick_tokens<QF_E8, T, XP, false, !T::HALF>(A, st);
     default: return pick_tokens<QF_VEC, T, XP, false, false>(A, st);
   }
 }
@@ -378,10 +411,13 @@ hipError_t launch_q_skinny(const QLayer& L, const uint16_t* x, int64_t ldx, int6
   A.ldx = ldx;
   A.planex = planex;
   A.kblocks = (int)(ldx ? L.n / 8 : (int64_t)L.chunks * q_chunk(L.fmt) / 8);
+  A.xbytes = (uint32_t)(ldx ? ((t - 1) * ldx + L.n) * 2 : (t + 15) / 16 * 16 * A.kblocks * 16);
   A.t = t;
   A.has_offset = L.has_offset();
   A.lut_words = (q_lut_words(L.fmt, L.lut_entries) + 3) / 4 * 4;
   A.O = O;
+  const uint64_t per = L.G > 1 ? (uint64_t)(L.group / q_chunk(L.fmt)) : 1;
+  A.ginv = per > 1 ? (uint32_t)(((1ull << 32) + per - 1) / per) : 0;   // (units and per are below 2^16: exact)
   if (bf16) return pick_format<OpBf16, 1>(A, st);
   return planes == 2 ? pick_format<OpF16, 2>(A, st) : pick_format<OpF16, 1>(A, st);
 }
