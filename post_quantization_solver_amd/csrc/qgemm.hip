@@ -1,13 +1,22 @@
 // 16-bit matrix products with a fused epilogue, for a solved layer's product
 // with many rows and for its gradients (qlayer.h, QGemm).
 //
-// Workgroup tile BM x BN of the output, K in steps of 32 through four LDS
-// stages filled by direct global -> LDS loads (16 bytes a lane), so that three
-// steps are on their way while the matrix cores work on a fourth out of
-// registers.  A row's four 16-byte pieces of a step are stored permuted by the
-// row's bits 1 and 2, so that the sixteen rows of an operand read spread over
-// the banks.  Operands of more than 16 bits enter as planes whose sum they are:
-// the products of plane pairs add up in the same float32 accumulators.
+// Workgroup tile BM x BN of the output, K in steps of 32 through four to six LDS
+// stages filled by direct global -> LDS loads (16 bytes a lane), so that three to
+// five steps are on their way while the matrix cores work on another out of
+// registers.  A step's products stand between its loads and the LDS reads of the
+// next step's operands, one each, and one barrier ends it.  A row's four 16-byte
+// pieces of a step are stored permuted by the row's bits 1 and 2, so that the
+// sixteen rows of an operand read spread over the banks.  Operands of more than
+// 16 bits enter as planes whose sum they are: the products of plane pairs add up
+// in the same float32 accumulators.
+//
+// Bound.  The matrix cores are busy some 60 % of the time in the large tiles (2048
+// x 4096 x 14336: 184 us, 1.3 PFLOP/s of the 2.07 that they reach alone), the rest
+// is the step's barrier; the small tile waits for the L2's 64 bytes a clock and
+// CU.  Planes are in blocks of 16 rows by 32 columns: rows of a matrix a multiple
+// of 4 KB apart lie on the same few cache channels (the same product with planes
+// in rows 262 us).
 #include <algorithm>
 #include "qlayer.h"
 
@@ -320,8 +329,9 @@ __global__ __launch_bounds__(256) void q_split_finish_kernel(const float* __rest
 
 // Tile 256 x 256 moves the fewest bytes into LDS per product, 128 x 128 twice
 // as many, where the L2's 64 bytes a clock and CU are the limit: the largest
-// tile that still gives three CUs in four a workgroup is taken.  (2048 x 4096 x
-// 14336: 128 x 128 350 us, 256 x 128 265 us, 256 x 256 on half the CUs 370 us.)
+// tile that still gives three CUs in four a workgroup is taken.  (4096 x 14336,
+// whole calls: 2048 tokens 128 x 128 273 us, 256 x 128 222 us, 256 x 256 in two
+// splits 238 us; 4096 tokens 553, 415, 377.)
 enum Tile : int { TILE_256 = 0, TILE_256_128 = 1, TILE_128 = 2 };
 struct Plan {
   int tile;

@@ -642,27 +642,29 @@ hipError_t unpack_t(const QLayer& L, int64_t mp, int planes, const uint32_t* ref
 // Token counts up to which the product reads the packed codes (one affine per
 // row, or groups of whole chunks; other groups always unpack).  Beyond, every 64
 // tokens decode the layer once more, and laying the planes out once is cheaper.
-// Measured, few-row product against planes and tiles, 4096 x 14336: E8 bfloat16
-// 63 | 67 us at 128 tokens, 90 | 86 at 192, float32 93 | 92 at 96, 120 | 98 at
-// 128; groups of 128, whose planes hold weights (two terms but for bfloat16):
-// bfloat16 95 | 114 at 192, 123 | 115 at 256, float16 183 | 230 at 384, 240 |
-// 271 at 512, float32 188 | 251 at 192.  The planes take 20 us and more however
-// small the layer: 1024 x 1024 at 384 tokens 19 | 24 (E8), 14 | 23 (4 bits), 19
-// | 27 (float32), at 777 33 | 27, 23 | 27, 35 | 32.
+// Measured, few-row product | planes and tiles, 4096 x 14336: E8 bfloat16 58 | 61
+// us at 128 tokens, 84 | 77 at 192, float32 85 | 87 at 96, 109 | 90 at 128; four
+// bits bfloat16 71 | 83 at 192, 93 | 85 at 256; groups of 128, whose planes hold
+// weights (two terms but for bfloat16): float16 156 | 213 at 384 (14336 x 4096
+// 235 | 211 at 512), float32 188 | 251 at 192.  The planes take 18 us and more
+// however small the layer: 1024 x 1024 at 384 tokens 17 | 20 (E8), 12 | 21 (four
+// bits), 24 | 28 (float32), at 768 25 | 23, 17 | 24, 44 | 32.
 constexpr int64_t Q_SMALL_TOKENS = 1024, Q_SMALL_WORK = 3ll << 27;
 
 bool use_skinny(const QLinearArgs& A) {
   if (!q_skinny_ok(A.L)) return false;
   if (A.t <= Q_SMALL_TOKENS && A.t * A.L.m * A.L.n <= Q_SMALL_WORK) return true;
-  if (A.L.G > 1) return A.t <= (A.dtype == DT_F16 ? 384 : 192);
-  return A.t <= (A.dtype == DT_F32 ? 96 : 128);
+  const bool scalar = A.L.fmt == QF_NIB || A.L.fmt == QF_BYTE, grouped = A.L.G > 1;
+  if (A.dtype == DT_F32) return A.t <= (grouped ? 192 : 96);
+  return A.t <= (grouped && A.dtype == DT_F16 ? 384 : scalar ? 192 : 128);
 }
 
 // Elements of x up to which the few-row product reads it in place.
-// Measured, in place | laid out first: 4096 columns, 2 tokens 8.7 | 11.3 us, 32
-// tokens 14.4 | 14.2; 8192 columns, 16 tokens 13.3 | 13.8, 32 tokens 21 | 19;
-// 14336 columns, 8 tokens 16.4 | 18.6, 16 tokens 20.8 | 19.3.
-constexpr int64_t Q_DIRECT = 131072;
+// Measured, in place | laid out first (E8): 4096 columns, 2 tokens 8.7 | 11.5 us,
+// 16 tokens 10.7 | 11.8, 32 tokens 13.6 | 12.5; 8192 columns, 8 tokens 11.5 |
+// 12.9, 13 tokens 12.6 | 13.0, 16 tokens 13.8 | 12.9; 14336 columns, 8 tokens 16.0
+// | 16.3, 13 tokens 18.3 | 16.7.
+constexpr int64_t Q_DIRECT = 7 << 14;
 
 int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }
 
@@ -692,11 +694,9 @@ hipError_t forward(const QLinearArgs& A, char* base, size_t* bytes, hipStream_t 
   const int XP = A.dtype == DT_F32 ? 2 : 1;
   const bool raw = A.dtype == DT_F16 || (A.dtype == DT_BF16 && !weights);
   const bool aligned = reinterpret_cast<uintptr_t>(A.x) % 16 == 0 && A.ldx % 8 == 0 && A.ldx <= (1 << 20);
-  // Few rows: one token's operand is read in place.  More tokens' rows lie 16 at
-  // a stride that sends them to the same few cache channels (64 clocks a load of
-  // 1 KB, against 16 in operand order), so they are laid out first -- unless
-  // that launch costs more than it saves.
-  const bool direct = raw && aligned && (skinny ? L.n % 8 == 0 && (A.t == 1 || A.t * L.n <= Q_DIRECT) : L.n % 64 == 0);
+  // Few rows: see Q_DIRECT.  Many: the product's tiles read x in place as they do
+  // operand order (2048 tokens of 14336 columns 258 us, laid out first 292).
+  const bool direct = raw && aligned && (skinny ? L.n % 8 == 0 && A.t * L.n <= Q_DIRECT : L.n % 64 == 0);
   const bool bf16 = raw && A.dtype == DT_BF16;
   const int WP = !weights ? 0 : A.dtype == DT_BF16 ? 1 : 2;   // terms of a weight (0: entries)
   const bool sums = !skinny && !grouped && L.has_offset();

@@ -13,10 +13,11 @@
 // bfloat16 step of the result).
 //
 // Bound.  HBM traffic is the packed codes (2 bits a weight for E8); what the
-// waves wait on is their own decoding (some 30 instructions a step of 64 blocks)
-// and, from two token tiles on, the operand loads.  A wave's matrix operand is
-// what its lanes decode, sixteen rows at a time, so the sixteen columns of the
-// other operand are tokens: one token costs what sixteen do but for x's loads.
+// waves wait on is their own decoding (some 20 instructions a step of 64 blocks
+// for E8 and its table's look-ups) and, from two token tiles on, the operand
+// loads.  A wave's matrix operand is what its lanes decode, sixteen rows at a
+// time, so the sixteen columns of the other operand are tokens: one token costs
+// what sixteen do but for x's loads.
 //
 // Split.  A workgroup takes R tiles of 16 rows, its waves the chunks of the tiles
 // in turn, and joins their sums in a fixed order through LDS.  E8's table (148 KB
@@ -26,9 +27,10 @@
 // cache channels, 64 clocks a load instead of 16.
 //
 // Measured (microseconds at 1, 16, 32, 64, 128 tokens, bfloat16): E8 4096 x
-// 14336 14.3, 18.6, 26.5, 33, 59; 4096 x 4096 8.1, 9.4, 13.6, 15.8, 27; 32768 x
-// 4096 30, 33, 44, 73, 138; four bits 4096 x 14336 10.6, 15.1, 22.5, 31, 54.  An
-// empty call (64 columns) is 5.7 with E8's table and 3.9 without.
+// 14336 12.1, 16.0, 21.0, 31.5, 56; 4096 x 4096 8.0, 10.1, 12.9, 15.5, 26; 32768 x
+// 4096 23, 28, 46, 67, 124; four bits 4096 x 14336 7.9, 12.4, 18.1, 28, 48; 32768
+// x 4096 15.6 (4.3 TB/s of codes), 23, 41, 61, 113.  An empty call (64 columns) is
+// 6.3 with E8's table and 3.9 without.
 #include <algorithm>
 #include <type_traits>
 #include "qlayer.h"
@@ -37,7 +39,9 @@ namespace mpq {
 
 namespace {
 
-// Sixteen waves where a wave's operands fit 128 registers, else eight.
+// Sixteen waves where a wave's operands fit 128 registers, else eight (one token,
+// 4096 x 14336: eight waves 16 us for E8 and 11 for four bits, sixteen 14 and 10,
+// before the loads were counted).
 constexpr int sk_waves(int XP, int NT, int R, bool grouped) { return XP * NT * R == 1 && !grouped ? 16 : 8; }
 
 // Whether entries are looked up: all but evenly spaced levels and those of the

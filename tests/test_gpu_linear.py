@@ -157,7 +157,8 @@ def test_linear_many_tokens_strides(dtype, pad, shift):
     run_case("s16", 64, 129, 1025, dtype, residual=True, pad=pad, shift=shift)
 
 
-@pytest.mark.parametrize("dtype,t,group", [("bf16", 128, 0), ("bf16", 129, 0), ("fp32", 96, 0), ("fp32", 97, 0),
+@pytest.mark.parametrize("dtype,t,group", [("bf16", 128, 0), ("bf16", 129, 0), ("bf16", 192, 0),
+                                           ("bf16", 193, 0), ("fp32", 96, 0), ("fp32", 97, 0),
                                            ("bf16", 192, 128), ("bf16", 193, 128), ("fp16", 384, 128),
                                            ("fp16", 385, 128)])
 def test_linear_either_side_of_the_packed_codes(dtype, t, group):
