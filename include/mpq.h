@@ -505,7 +505,11 @@ int mpq_pack(const int32_t* codes, int64_t m, int64_t n, const mpq_codebook* cb,
  * there is an activation.  y may be the residual (same pointer and stride) and
  * otherwise overlaps no input.
  * Column groups need d = 1.  Sums are float32.  The entries enter as they are,
- * float32 x as two float16 terms (22 bits, under a power of two per token).
+ * float32 x as two float16 terms (22 bits, under a power of two per token).  With
+ * bfloat16 x and few tokens, E8's entries and evenly spaced levels enter with a
+ * constant (at most 160) added that comes off every 128 columns: errors of some
+ * 2^-17, at most 2^-13, of the scale times (E8: half) the sum of |x|, and |x| below
+ * 2^112.
  * Where column groups make the weights themselves enter (more than 192 tokens on
  * large layers, or groups that are no multiple of the packed chunk: 128 columns
  * at 4 bits, 64 at 8), they and x are float16 terms under a power of two per

@@ -55,7 +55,7 @@ struct Cursor {
     const char* b = reinterpret_cast<const char*>(g.B + g.pb[pair] * g.planeB + j0 * (g.ldb ? g.ldb : g.K)) +
                     (size_t)k * (g.ldb ? BK * 2 : 1024);
 #pragma unroll
-    for (int l = 0; l < LOADS; ++l) p[l] = ((wave * LOADS + l) * 16 < BM ? a : b) + off[l];
+    for (int l = 0; l < LOADS; ++l) p[l] = ((wave * LOADS + l) * 16 < BM ? a : b) + (size_t)off[l] * 16;
   }
 };
 
@@ -139,7 +139,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void q_gemm_kernel(QGemm g, float*
   const int kts = (int)(g.K / BK), all = kts * g.npairs;
   const int kt0 = (int)((int64_t)all * split / splits), kt1 = (int)((int64_t)all * (split + 1) / splits);
 
-  // this lane's byte offsets within the tile's rows
+  // this lane's offsets within the tile's rows, in 16 bytes (a tile's 256 rows of
+  // 2^24 columns are 8 GB)
   const int piece = (lane & 3) ^ ((lane >> 3) & 3);
   uint32_t off[LOADS];
 #pragma unroll
@@ -148,8 +149,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void q_gemm_kernel(QGemm g, float*
     const bool a = r < BM;
     const int64_t lim = (a ? g.M - 1 - i0 : g.N - 1 - j0), row = a ? r : r - BM;
     // rows past the end repeat the last sixteen, or the last
-    if (a || !g.ldb) off[l] = (uint32_t)(min(row / 16, lim / 16) * (g.K * 32) + (lane >> 2) * (BK * 2) + piece * 16);
-    else off[l] = (uint32_t)(min(row + (lane >> 2), lim) * g.ldb * 2 + piece * 16);
+    if (a || !g.ldb) off[l] = (uint32_t)(min(row / 16, lim / 16) * (g.K * 2) + (lane >> 2) * (BK / 8) + piece);
+    else off[l] = (uint32_t)(min(row + (lane >> 2), lim) * g.ldb / 8 + piece);
   }
 
   v4f acc[SM][SN];

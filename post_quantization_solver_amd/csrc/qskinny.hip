@@ -157,12 +157,12 @@ __global__ __launch_bounds__(64 * sk_waves(XP, NT, R, GROUPED)) void q_skinny_ke
   // are wanted, one.
   constexpr int XD = NT * XP <= 2 ? 2 : 1;
   Codes next[2];
-  Xs xs_[XD];
+  Xs xnext[XD];
   auto load_first = [&](int tg, int first) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {   // (in the order of their uses)
       load_codes(next[h], tg, first + h * SK_WAVES);
-      if (h < XD) load_x(xs_[h], first + h * SK_WAVES);
+      if (h < XD) load_x(xnext[h], first + h * SK_WAVES);
       keep_order();
     }
   };
@@ -197,7 +197,7 @@ __global__ __launch_bounds__(64 * sk_waves(XP, NT, R, GROUPED)) void q_skinny_ke
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           const int64_t i = min((int64_t)(tg * R + q) * 16 + 4 * kb + v, A.L.m - 1);
-          sa[q][v] = A.L.scale[i];   // (times step: see below)
+          sa[q][v] = A.L.scale[i];
           so[q][v] = A.has_offset && A.L.offset ? A.L.offset[i] : 0.f;
         }
     v4f acc[R][NT], xs[NT];
@@ -284,10 +284,10 @@ __global__ __launch_bounds__(64 * sk_waves(XP, NT, R, GROUPED)) void q_skinny_ke
     // (one way round the loop, so that every turn finds the same loads behind it)
     int u = wave;
     for (; u + SK_WAVES < units; u += 2 * SK_WAVES) {
-      unit(next[0], xs_[0], u, std::true_type{});
-      unit(next[1], xs_[XD - 1], u + SK_WAVES, std::true_type{});
+      unit(next[0], xnext[0], u, std::true_type{});
+      unit(next[1], xnext[XD - 1], u + SK_WAVES, std::true_type{});
     }
-    if (u < units) unit(next[0], xs_[0], u, std::false_type{});
+    if (u < units) unit(next[0], xnext[0], u, std::false_type{});
     // (not under a branch either; after the last tile nothing)
     if constexpr (FMT == QF_E8) load_first(more ? tg + gridDim.x : tg, more ? wave : units);
     if (!GROUPED) {

@@ -394,6 +394,77 @@ def test_linear_graph_replays(t):
                 assert torch.equal(a, b), k
 
 
+@pytest.mark.parametrize("name,t", [("e865536", 1), ("e865536", 40), ("e865536", 1030), ("s16", 1), ("s16", 1030)])
+def test_linear_graph_replays_on_every_path(name, t):
+    """A chain of calls captured, replayed on new inputs and a tuned scale, with eager work between."""
+    import torch
+    import post_quantization_solver_amd as mpq
+    codes, E, scale, off = make_layer(name, 256, 256, 0, 6)
+    layer = mpq.pack_layer(dev(codes), E, dev(scale), dev(off))
+    x = torch.randn(t, 256, device="cuda").bfloat16()
+
+    def chain():
+        h = mpq.linear(x, layer, activation="silu")
+        y = mpq.linear(h, layer, residual=x)
+        r = mpq.linear_backward(y, x, layer)
+        return [h, y, r["dx"], r["dscale"], r["doffset"], r["dbias"]]
+    chain()
+    torch.cuda.synchronize()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        out = chain()
+    for k in range(3):
+        x.copy_(torch.randn(t, 256, device="cuda"))
+        layer.scale.mul_(1.25)
+        torch.cuda.synchronize()
+        gr.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, chain()):
+            assert torch.equal(a, b), k
+
+
+@pytest.mark.parametrize("t", [1, 20, 1100])
+def test_linear_two_streams_at_once(t):
+    """Calls on two streams that overlap: each has its own workspace, and the results are the serial ones."""
+    import torch
+    import post_quantization_solver_amd as mpq
+    layers = []
+    for seed, name in ((1, "e865536"), (2, "s16")):
+        codes, E, scale, off = make_layer(name, 1024, 1024, 0, seed)
+        layers.append(mpq.pack_layer(dev(codes), E, dev(scale), dev(off)))
+    xs = [torch.randn(t, 1024, device="cuda").bfloat16() for _ in layers]
+    want = [mpq.linear(x, layer, activation="gelu") for x, layer in zip(xs, layers)]
+    streams = [torch.cuda.Stream() for _ in layers]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(8):
+        for k, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[k].append(mpq.linear(xs[k], layers[k], activation="gelu"))
+    torch.cuda.synchronize()
+    for k in range(2):
+        assert all(torch.equal(g, want[k]) for g in got[k])
+
+
+@pytest.mark.parametrize("name,half", [("e865536", 0.5), ("s16", 1.0), ("s64", 1.0)])
+@pytest.mark.parametrize("t", [1, 17, 70])
+def test_linear_outliers_in_x(name, half, t):
+    """One element of a token 2^14 times the others.  Lifted entries: a unit's sum of up to 191 (E8: 143 half units)
+    |x| and its lift come off each other, some six roundings of 2^-24 of 351 (E8: 140) |x| at most: 2^-13 a sum |x|."""
+    import torch
+    import post_quantization_solver_amd as mpq
+    codes, E, scale, _ = make_layer(name, 96, 1024, 0, 7, False)
+    layer = mpq.pack_layer(dev(codes), E, dev(scale))
+    x = torch.randn(t, 1024, device="cuda").bfloat16()
+    x[:, 300] = 16384.0
+    got = f64(mpq.linear(x, layer))
+    xr = f64(x)
+    want = xr @ R.layer_weights(codes, E, scale, None, 0).T
+    step = half * 2 if name.startswith("e8") else float(E[1, 0] - E[0, 0])
+    tol = 2.0 ** -13 * np.abs(xr).sum(1)[:, None] * np.abs(scale)[None, :] * step
+    assert (np.abs(got - want) <= tol + STEP["bf16"] * (np.abs(want) + tol)).all()
+
+
 def test_solve_run_score_tune():
     """The operators together: a solved layer as an output head, its logits scored and tuned to the original's."""
     import torch
@@ -464,3 +535,23 @@ def test_linear_refusals():
         mpq.pack_layer(dev(codes), E, dev(scale), dev(off), group=16)
     with pytest.raises(TypeError):
         mpq.pack_layer(dev(codes).long(), E, dev(scale), dev(off))
+
+
+def test_backward_of_the_longest_layer():
+    """2^24 rows: a tile's planes span more than 4 GB.  du is not zero in ten rows alone, so the sums are theirs."""
+    import torch
+    import post_quantization_solver_amd as mpq
+    m, n = 1 << 24, 144
+    E = (np.arange(16, dtype=np.float32) - 8).reshape(16, 1)
+    codes = torch.randint(0, 16, (m, n), dtype=torch.int32, device="cuda")
+    scale = torch.ones(m, device="cuda")
+    layer = mpq.pack_layer(codes, E, scale)
+    at = torch.linspace(0, m - 1, 10, device="cuda").long()
+    dy = torch.zeros((1, m), dtype=torch.bfloat16, device="cuda")
+    dy[0, at] = torch.arange(1, 11, device="cuda").bfloat16()
+    entries = codes[at].double().cpu().numpy() - 8
+    del codes
+    x = torch.zeros((1, n), dtype=torch.bfloat16, device="cuda")
+    dx = f64(mpq.linear_backward(dy, x, layer, need_dlayer=False)["dx"])
+    want = np.arange(1, 11) @ entries   # integers below 2^24: exact but for dx's own rounding
+    assert (np.abs(dx[0] - want) <= STEP["bf16"] * np.abs(want)).all()
