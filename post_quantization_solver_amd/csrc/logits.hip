@@ -124,6 +124,26 @@ __device__ __forceinline__ float wave_max(float v) {
   for (int o = 32; o; o >>= 1) v = fmaxf(v, shfl_xor_f(v, o));
   return v;
 }
+// 2^y in float64 to 2^-36, by 2^n and the exponential series of f ln 2, |f| <= 1/2
+// (its tenth term is below 2^-36).
+__device__ __forceinline__ double exp2_series(double y) {
+  y = fmax(y, -1100.0);
+  const double n = rint(y), x = (y - n) * LN2;
+  double p = 1.0;
+#pragma unroll
+  for (int k = 9; k >= 1; --k) p = fma(p * x, 1.0 / k, 1.0);
+  return ldexp(p, (int)n);
+}
+
+// The tail form's s: its unlisted part as it was summed, its listed part in
+// float64.  A divergence near zero is a difference that errors of the listed
+// elements enter in full (of a list of one at a loss of 1e-4, 2^-13 of it), while
+// an error e of the unlisted sum enters as e times the difference of the
+// remainders.  Sums that are not finite stay.
+__device__ __forceinline__ double tail_sum(double s, double rest, double list) {
+  return s > 0.0 && s < INFINITY ? rest + list : s;
+}
+
 __device__ __forceinline__ double wave_sum(double v) {
   for (int o = 32; o; o >>= 1) v += shfl_d(v, (int)(threadIdx.x & 63) ^ o);
   return v;
@@ -624,7 +644,6 @@ __global__ __launch_bounds__(LG_THREADS) void distill_grad_kernel(LogitArgs A, c
     return;
   }
   const RowStat r = join_parts(parts + row * A.S, A.S, A.c);
-  const double lg = log2(r.s);
   // this thread's entry of the teacher's list
   int32_t id = -1;
   double lt = -INFINITY;
@@ -660,32 +679,41 @@ __global__ __launch_bounds__(LG_THREADS) void distill_grad_kernel(LogitArgs A, c
     __syncthreads();
   }
   if (id < 0) p = 0.0;
-  const double lq = (((double)zi - (double)r.m) * (double)A.c - lg) * LN2;
-  const double term = p == 0.0 ? 0.0 : p * (lp - lq);
-  const double ps = wave_sum(p), ts = wave_sum(term);
-  if ((t & 63) == 0) {
-    red[1][wave] = ps;
-    red[2][wave] = ts;
-  }
   sid[t] = id;
   sp[t] = (float)p;
   __syncthreads();
-  double psum = 0.0, kl = 0.0;
-  for (int i = 0; i < LG_WAVES; ++i) {
-    psum += red[1][i];
-    kl += red[2][i];
-  }
   // how often the list names each token (a token named twice has the sum)
   float pown = 0.f;
   bool first = id >= 0;
-  int named = 0;
   if (id >= 0)
     for (int i = 0; i < A.k; ++i)
       if (sid[i] == id) {
         pown += sp[i];
         if (i < t) first = false;
       }
-  named = __syncthreads_count(first ? 1 : 0);
+  const int named = __syncthreads_count(first ? 1 : 0);
+  const double y = ((double)zi - (double)r.m) * (double)A.c;
+  double s = r.s;
+  if (tail) {
+    const double ls = wave_sum(first ? exp2_series(y) : 0.0);
+    if ((t & 63) == 0) red[0][wave] = ls;
+    __syncthreads();
+    double list = 0.0;
+    for (int i = 0; i < LG_WAVES; ++i) list += red[0][i];
+    s = tail_sum(r.s, r.rest, list);
+  }
+  const double term = p == 0.0 ? 0.0 : p * (lp - (y - log2(s)) * LN2);
+  const double ps = wave_sum(p), ts = wave_sum(term);
+  if ((t & 63) == 0) {
+    red[1][wave] = ps;
+    red[2][wave] = ts;
+  }
+  __syncthreads();
+  double psum = 0.0, kl = 0.0;
+  for (int i = 0; i < LG_WAVES; ++i) {
+    psum += red[1][i];
+    kl += red[2][i];
+  }
   double coef = 1.0;   // of an unlisted q_j
   if (tail) {
     // below 2^-20 the remainder is the rounding of the k float32 log
@@ -694,7 +722,7 @@ __global__ __launch_bounds__(LG_THREADS) void distill_grad_kernel(LogitArgs A, c
     double pt = 1.0 - psum;
     if (pt < 0x1p-20 || named >= A.V) pt = 0.0;
     if (pt > 0.0) {
-      const double qt = r.rest / r.s;
+      const double qt = r.rest / s;
       kl += pt * (log(pt) - log(qt));
       coef = 1.0 - pt / qt;
     }
@@ -704,7 +732,7 @@ __global__ __launch_bounds__(LG_THREADS) void distill_grad_kernel(LogitArgs A, c
   if (seg == 0 && t == 0) loss[row] = (float)((double)wt * kl);
   if (!gr) return;
   const double g0 = (double)wt * invT;
-  const float m = r.m, f = (float)(coef * g0 / r.s), inv = (float)(1.0 / r.s);
+  const float m = r.m, f = (float)(coef * g0 / s), inv = (float)(1.0 / s);
   float glist = 0.f;
   if (first) glist = (__builtin_amdgcn_exp2f((zi - m) * A.c) * inv - pown) * (float)g0;
   for (int64_t i = base + (int64_t)t * T::VEC; i < end; i += LG_THREADS * T::VEC) {
@@ -898,25 +926,30 @@ __global__ __launch_bounds__(THREADS) void distill_row_kernel(LogitArgs A, const
   __syncthreads();
   if (wave != 0) return;
   // the listed entries' gradients, over what was written there; the loss
-  const double lg = log2(s);
-  double kl = 0.0;
+  double y[2], list = 0.0, kl = 0.0;
+  bool first[2];
+  float own[2];
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    if (id[q] < 0) continue;
-    const double y = fast ? (double)zi[q] * (double)A.c - (double)M : ((double)zi[q] - (double)m) * (double)A.c;
-    if (p[q] != 0.0) kl += p[q] * (lp[q] - (y - lg) * LN2);
-    bool first = true;
-    float own = (float)p[q];
-    if (s_twice) {   // a token named twice has the sum, and one writer
-      own = 0.f;
+    y[q] = fast ? (double)zi[q] * (double)A.c - (double)M : ((double)zi[q] - (double)m) * (double)A.c;
+    first[q] = id[q] >= 0;
+    own[q] = (float)p[q];
+    if (s_twice && first[q]) {   // a token named twice has the sum, and one writer
+      own[q] = 0.f;
       for (int i = 0; i < A.k; ++i)
         if (sid[i] == id[q]) {
-          own += sp[i];
-          if (i < 64 * q + lane) first = false;
+          own[q] += sp[i];
+          if (i < 64 * q + lane) first[q] = false;
         }
     }
-    const float e = two_to(zi[q]);
-    if (gr && first) T::store(gr, id[q], (e * (float)(1.0 / s) - own) * (float)g0);
+    if (TAIL && first[q]) list += exp2_series(y[q]);
+  }
+  if (TAIL) s = tail_sum(s, rest, wave_sum(list));
+  const double lg = log2(s);
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    if (p[q] != 0.0) kl += p[q] * (lp[q] - (y[q] - lg) * LN2);
+    if (gr && first[q]) T::store(gr, id[q], (two_to(zi[q]) * (float)(1.0 / s) - own[q]) * (float)g0);
   }
   kl = wave_sum(kl);
   if (TAIL && pt > 0.0) kl += pt * (log(pt) - log(rest / s));

@@ -217,6 +217,38 @@ def test_teacher_list_to_distill():
     assert np.abs(host(same["loss"])).max() < 2.0 ** -17   # a teacher has nothing to learn from itself
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("t,k", [(16, 1), (16, 64), (130, 1), (130, 64)])
+def test_divergences_near_zero(dtype, t, k):
+    """A student that is nearly the teacher.  The listed elements enter in float64 and the unlisted sum with a relative
+    error of at most 2^-20 (float32's rounding of an exponent of up to 2^5 and of its power), which the loss has times
+    the difference of the two remainders; 2^-23 of the loss is its own rounding, and 2^-36 the series'.  log2(e) is
+    used as a float32, half a step of 2^-23 off at most: logits times 1 + 2^-24 / 1.44, which the loss, whose slope in
+    that factor is sum_j (q_j - p_j) z_j (unlisted p_j = q_j pt / qt), has 2^-24 times."""
+    import torch
+    import post_quantization_solver_amd as mpq
+    g = np.random.default_rng(31 + t + k)
+    teacher = rows(g, t, 20011, "fp32").double().cpu().numpy() * 2
+    lp = teacher - np.log(np.exp(teacher - teacher.max(1, keepdims=True)).sum(1, keepdims=True)) - teacher.max(1, keepdims=True)
+    ids = np.argsort(-lp, axis=1)[:, :k].astype(np.int32)
+    lists = np.take_along_axis(lp, ids.astype(np.int64), 1).astype(np.float32)
+    student = torch.from_numpy(teacher + 0.01 * g.standard_normal(teacher.shape)).to("cuda", dtype_of(dtype))
+    got = mpq.distill(student, dev(ids), dev(lists), tail=True)["loss"].double().cpu().numpy()
+    z = student.double().cpu().numpy()
+    z = z - z.max(1, keepdims=True)
+    lq = z - np.log(np.exp(z).sum(1, keepdims=True))
+    p = np.exp(lists.astype(np.float64))
+    hidden = np.ones(z.shape, bool)
+    np.put_along_axis(hidden, ids.astype(np.int64), False, 1)
+    pt, qt = 1 - p.sum(1), np.where(hidden, np.exp(lq), 0).sum(1)
+    want = (p * (lists - np.take_along_axis(lq, ids.astype(np.int64), 1))).sum(1) + pt * (np.log(pt) - np.log(qt))
+    full = np.exp(lq) * (pt / qt)[:, None]
+    np.put_along_axis(full, ids.astype(np.int64), p, 1)
+    slope = (np.abs(np.exp(lq) - full) * np.abs(z)).sum(1)
+    tol = 2.0 ** -20 * np.abs(pt - qt) + 2.0 ** -24 * slope + 2.0 ** -23 * np.abs(want) + 2.0 ** -36
+    assert (np.abs(got - want) <= tol).all()
+
+
 def test_logits_graph_replays():
     """Captured and replayed on new inputs, with eager work between: every replay equals the eager call."""
     import torch
