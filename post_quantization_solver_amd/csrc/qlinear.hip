@@ -519,26 +519,32 @@ __global__ __launch_bounds__(256) void q_grad_tile_kernel(DuArgs A) {
   }
 }
 
-// d bias (want_t) and du o' per token (rowpart), added up in order in float64.
-__global__ __launch_bounds__(256) void q_grad_sums_kernel(DuArgs A, float* __restrict__ dbias, float* __restrict__ rowadd) {
-  const int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x;
+// d bias of row r, and du o' per token: added up in order in float64.
+__device__ __forceinline__ void add_bias(const DuArgs& A, int64_t r, float* __restrict__ dbias) {
+  if (r >= A.m) return;
   double s = 0.0;
-  if (A.want_t && r < A.m) {
-    for (int64_t k = 0; k < A.tp / 64; ++k) s += (double)A.biaspart[k * A.m + r];
-    dbias[r] = (float)s;
-  }
-  const int64_t t = r - (A.want_t ? (A.m + 255) / 256 * 256 : 0);
-  if (A.rowpart && t >= 0 && t < A.t) {
-    for (int64_t k = 0; k < A.rowtiles; ++k) s += (double)A.rowpart[t * A.rowtiles + k];
-    rowadd[t] = (float)s;
-  }
+  for (int64_t k = 0; k < A.tp / 64; ++k) s += (double)A.biaspart[k * A.m + r];
+  dbias[r] = (float)s;
+}
+__global__ __launch_bounds__(256) void q_grad_rowsum_kernel(DuArgs A, float* __restrict__ rowadd) {
+  const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (t >= A.t) return;
+  double s = 0.0;
+  for (int64_t k = 0; k < A.rowtiles; ++k) s += (double)A.rowpart[t * A.rowtiles + k];
+  rowadd[t] = (float)s;
 }
 
 // The contraction's parts, added up in order in float64: sixteen lanes per (row, group).
 __global__ __launch_bounds__(256) void q_contract_finish_kernel(QLayer L, const float2* __restrict__ part, int splits,
                                                                 int64_t rows, int64_t blocks, int64_t row0,
                                                                 float* __restrict__ dscale,
-                                                                float* __restrict__ doffset) {
+                                                                float* __restrict__ doffset, DuArgs A,
+                                                                float* __restrict__ dbias) {
+  const int64_t own = (rows * L.G + 15) / 16;
+  if (blockIdx.x >= own) {   // d bias
+    add_bias(A, (blockIdx.x - own) * 256 + threadIdx.x, dbias);
+    return;
+  }
   const int lane = threadIdx.x & 15;
   const int64_t w = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
   if (w >= rows * L.G) return;
@@ -565,7 +571,13 @@ __global__ __launch_bounds__(256) void q_contract_finish_kernel(QLayer L, const 
 // d scale and d offset of `rows` rows from row0 on: a wave per (row, group).
 __global__ __launch_bounds__(256) void q_affine_grad_kernel(QLayer L, const float* __restrict__ dW, int64_t ldw,
                                                             int64_t row0, int64_t rows, float* __restrict__ dscale,
-                                                            float* __restrict__ doffset) {
+                                                            float* __restrict__ doffset, DuArgs A,
+                                                            float* __restrict__ dbias) {
+  const int64_t own = (rows * L.G + 3) / 4;
+  if (blockIdx.x >= own) {   // d bias
+    add_bias(A, (blockIdx.x - own) * 256 + threadIdx.x, dbias);
+    return;
+  }
   const int lane = threadIdx.x & 63;
   const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (w >= rows * L.G) return;
@@ -877,9 +889,8 @@ hipError_t backward(const QLinearGrad& A, char* base, size_t* bytes, hipStream_t
   if ((e = hipGetLastError()) != hipSuccess) return e;
   hipLaunchKernelGGL(q_grad_tile_kernel, dim3((unsigned)(D.du_blocks + x_blocks)), dim3(256), 0, st, D);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  if (A.need_dlayer || sums) {
-    const int64_t n = (A.need_dlayer ? (L.m + 255) / 256 * 256 : 0) + (sums ? A.t : 0);
-    hipLaunchKernelGGL(q_grad_sums_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, D, A.dbias, rowadd);
+  if (sums) {
+    hipLaunchKernelGGL(q_grad_rowsum_kernel, dim3((unsigned)((A.t + 255) / 256)), dim3(256), 0, st, D, rowadd);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   if (A.need_dx) {
@@ -916,12 +927,14 @@ hipError_t backward(const QLinearGrad& A, char* base, size_t* bytes, hipStream_t
       gw.O.rowmax = D.tmax + r0;
       gw.row0 = r0;
       if ((e = launch_q_gemm(gw, part, st)) != hipSuccess) return e;
+      // d bias rides behind the first block of rows
+      const unsigned bias = r0 == 0 ? (unsigned)((L.m + 255) / 256) : 0;
       if (contract)
-        hipLaunchKernelGGL(q_contract_finish_kernel, dim3((unsigned)((nr * L.G + 15) / 16)), dim3(256), 0, st, L, cpart,
-                           splits, nr, cblocks, r0, A.dscale, A.doffset);
+        hipLaunchKernelGGL(q_contract_finish_kernel, dim3((unsigned)((nr * L.G + 15) / 16) + bias), dim3(256), 0, st, L,
+                           cpart, splits, nr, cblocks, r0, A.dscale, A.doffset, D, A.dbias);
       else
-        hipLaunchKernelGGL(q_affine_grad_kernel, dim3((unsigned)((nr * L.G + 3) / 4)), dim3(256), 0, st, L, dW, ldw,
-                           r0, nr, A.dscale, A.doffset);
+        hipLaunchKernelGGL(q_affine_grad_kernel, dim3((unsigned)((nr * L.G + 3) / 4) + bias), dim3(256), 0, st, L, dW,
+                           ldw, r0, nr, A.dscale, A.doffset, D, A.dbias);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
   }
