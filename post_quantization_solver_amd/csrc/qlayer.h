@@ -417,7 +417,8 @@ __device__ __forceinline__ void q_entries4(const QLayer& L, uint32_t code, int64
 // ------------------------------------------------------------------ launchers
 
 // D[j][i] = sum over the plane pairs (p, q) and k of A_p[i][k] B_q[j][k] (16-bit
-// planes, K a multiple of 64, rows of lda / ldb elements, 16-byte aligned), then
+// planes, K a multiple of 32; B may stay in rows of ldb elements, a multiple of 8,
+// 16-byte aligned), then
 // O, or the contraction.  part (split K): splits x rows x cols float32.
 // Operand order of a plane: sixteen rows by 32 columns after another, along the
 // row first, each a contiguous KB of its rows (64 bytes each).  K: the plane's
