@@ -496,7 +496,7 @@ __global__ __launch_bounds__(256) void q_grad_tile_kernel(DuArgs A) {
     if (t < A.t) {
       const float g = pow2(pow2_shift(A.dmax[t]));
 #pragma unroll
-      for (int q = 0; q < 4; ++q) v[q] *= f[q] * g;
+      for (int q = 0; q < 4; ++q) v[q] = v[q] * f[q] * g;   // (as the scan took it: f g alone may overflow)
       put_terms(A.d + q_at(t, i, A.mp), A.plane_d, A.planes_d, v);
     }
   }
