@@ -225,7 +225,11 @@ __device__ __forceinline__ float act_fwd(int act, float u) {
 __device__ __forceinline__ float act_slope(int act, float u) {
   switch (act) {
     case ACT_RELU: return u > 0.f ? 1.f : u == u ? 0.f : u;
-    case ACT_GELU: return 0.5f * (1.f + erff(u * 0.70710678f)) + u * 0.39894228f * expf(-0.5f * u * u);
+    case ACT_GELU: {
+      // (a u beyond float16 is kept as an infinity: u times the density is 0 there, not inf * 0)
+      const float d = expf(-0.5f * u * u);
+      return 0.5f * (1.f + erff(u * 0.70710678f)) + (d == 0.f ? 0.f : u * 0.39894228f * d);
+    }
     case ACT_GELU_TANH: {
       const float th = tanhf(0.79788456f * (u + 0.044715f * u * u * u));
       // 1 - th^2 is 0 where u^3 overflows; the product must not be inf * 0
@@ -234,7 +238,7 @@ __device__ __forceinline__ float act_slope(int act, float u) {
     }
     case ACT_SILU: {
       const float q = 1.f / (1.f + expf(-u));
-      return q == 0.f ? 0.f : q * (1.f + u * (1.f - q));
+      return q == 0.f || q == 1.f ? q : q * (1.f + u * (1.f - q));   // (its ends: not inf * 0)
     }
   }
   return 1.f;

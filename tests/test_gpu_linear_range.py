@@ -39,3 +39,29 @@ def test_backward_of_vanishing_gradients(dtype, name, group):
     lim = ((m / 16 + 32) * 2.0 ** -22 + 2 * one) * (np.abs(f64(dy)) @ parts)
     err = np.abs(f64(r["dx"]) - want["dx"])
     assert (err <= lim + STEP[dtype] * (np.abs(want["dx"]) + lim) + 1e-40).all(), err.max()
+
+
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+def test_slopes_far_out(act, dtype):
+    """Arguments beyond float16 are kept as infinities: their slopes are 0 and 1, as the activation's finite values
+    there say, and a NaN stays one.  d bias of one token is du itself: the slope, exact at both ends (2^-20 where it
+    is not: the activation's own error)."""
+    import torch
+    import post_quantization_solver_amd as mpq
+    far = 65504.0 if dtype == "fp16" else 3e38
+    pre = torch.tensor([[-np.inf, np.inf, -far, far, -300.0, 300.0, -40.0, 40.0, 0.0, np.nan]], device="cuda")
+    m = pre.shape[1]
+    codes, E, scale, off = make_layer("s16", m, 32, 0, 1)
+    layer = mpq.pack_layer(dev(codes), E, dev(scale), dev(off))
+    one = torch.ones(1, m, device="cuda").to(dtype_of(dtype))
+    x = torch.ones(1, 32, device="cuda").to(dtype_of(dtype))
+    r = mpq.linear_backward(one, x, layer, pre=pre.to(dtype_of(dtype)), activation=act)
+    got = f64(r["dbias"])
+    assert np.isnan(got[-1]) and np.isfinite(got[:-1]).all(), got
+    assert np.array_equal(got[:6], [0, 1, 0, 1, 0, 1])
+    half = 0.0 if act == "relu" else 0.5
+    assert np.abs(got[6:9] - [0, 1, half]).max() <= 2.0 ** -20
+    y = f64(mpq.linear_backward(one[:, :-1].contiguous(), x, mpq.pack_layer(dev(codes[:-1]), E, dev(scale[:-1]),
+            dev(off[:-1])), pre=pre[:, :-1].contiguous().to(dtype_of(dtype)), activation=act)["dx"])
+    assert np.isfinite(y).all()
