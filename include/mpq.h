@@ -572,7 +572,9 @@ int mpq_token_logprobs(const void* logits, int dtype, int64_t t, int64_t V, int6
  *   tail = 1: exp(teacher) -- log probabilities, temperature 1 -- and the
  *             remainder 1 - sum p as one more outcome, against the student's
  *             mass outside the list (a remainder below 2^-20, the resolution
- *             of the log probabilities, counts as none).
+ *             of the log probabilities, counts as none).  The mass outside the
+ *             list may be as small as the logits make it; where it is nothing
+ *             (-inf alone) the loss is +inf, the gradient there 0.
  * grad = d loss / d z (t x V of `dtype`, row stride ldg >= V; NULL: the loss
  * alone), rounded once; it may be the logits themselves (same pointer and
  * stride) and may not overlap them otherwise.

@@ -71,13 +71,18 @@ def distill(z, ids, teacher, T=1.0, tail=False, weights=None):
             listed[[j for j, _ in keep]] = True
             if rest < 2.0 ** -20 or listed.all():
                 rest = 0.0
-            qr = q[~listed].sum()
             g = np.where(listed, q - p, q)
             share = 0.0
             if rest > 0:
-                kl += rest * (math.log(rest) - (math.log(qr) if qr > 0 else -np.inf))
-                share = rest / qr if qr > 0 else np.inf
-                g = np.where(listed, g, q * (1 - share))
+                # the unlisted mass by its own maximum: it may be far below what float64 holds about the row's
+                top = lq[~listed].max()
+                if top == -np.inf:
+                    kl, share = np.inf, 0.0   # nothing to move: no gradient but the listed tokens'
+                else:
+                    e = np.exp(np.where(listed, -np.inf, lq - top))
+                    kl += rest * (math.log(rest) - top - math.log(e.sum()))
+                    share = rest * (e / e.sum())
+                g = np.where(listed, g, q - share)
         elif not keep:
             continue
         else:
@@ -91,7 +96,7 @@ def distill(z, ids, teacher, T=1.0, tail=False, weights=None):
             g, share = q - p, 0.0
         loss[i] = w * kl
         grad[i] = w / T * g
-        scale[i] = w / T * (q * (1 + share) + p)
+        scale[i] = w / T * (q + share + p)
     return loss, grad, scale
 
 

@@ -209,9 +209,15 @@ __device__ __forceinline__ float wave_sort_desc(float v) {
 // One segment's statistics.
 struct Part {
   double s, w;      // sums of 2^y and 2^y y
-  double rest;      // s without the listed entries (tail form)
-  float m, pad;     // the maximum
+  double rest;      // s without the listed entries (tail form), about mr
+  float m, mr;      // the maximum; m, or the unlisted elements' own (FAR_TAIL)
 };
+
+// A sum of the unlisted elements below this share of the maximum's is taken again
+// about their own maximum: float32's exponentials end at 2^-126, and 2^20 of them
+// that were lost there are 2^-42 of this.  (The loss and the gradient depend on the
+// unlisted elements among themselves however far they lie below the listed ones.)
+constexpr double FAR_TAIL = 0x1p-64;
 
 // A thread's sums over its vectors.  SAFE = false: y = c z - M by one fma, M =
 // fl(c m); the caller takes the common c m - M out again.  It needs |M| well
@@ -265,6 +271,35 @@ __device__ __forceinline__ void thread_sums(const uint32_t (&u)[NV][4], int nv, 
 }
 // Whether the fma form's M resolves y.
 __device__ __forceinline__ bool plain_scale(float m, float c) { return fabsf(m * c) < 0x1p20f; }
+
+// Elements base .. end of a row that `listed` (bit e of byte v: element e of vector
+// v from base on) does not name: their maximum and the sum of 2^(c (z - maximum)),
+// the same in every thread.  Re-reads the row: rare.  red_m, red_s: a place per wave.
+template <typename T, int THREADS>
+__device__ __forceinline__ void unlisted_apart(const char* z, int64_t base, int64_t end, const uint8_t* listed,
+                                               float c, float* red_m, double* red_s, float& mu, double& sum) {
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  auto each = [&](auto&& f) {
+#pragma unroll 1
+    for (int at = threadIdx.x; at < (int)(end - base); at += THREADS)
+      if (!(listed[at / T::VEC] >> (at % T::VEC) & 1u)) f(T::load(z, base + at));
+  };
+  mu = -INFINITY;
+  each([&](float x) { mu = fmaxf(mu, x); });
+  mu = wave_max(mu);
+  __syncthreads();
+  if (lane == 0) red_m[wave] = mu;
+  __syncthreads();
+  mu = red_m[0];
+  for (int w = 1; w < THREADS / 64; ++w) mu = fmaxf(mu, red_m[w]);
+  sum = 0.0;
+  if (mu > -INFINITY) each([&](float x) { sum += (double)__builtin_amdgcn_exp2f((x - mu) * c); });
+  sum = wave_sum(sum);
+  if (lane == 0) red_s[wave] = sum;
+  __syncthreads();
+  sum = 0.0;
+  for (int w = 0; w < THREADS / 64; ++w) sum += red_s[w];
+}
 
 struct Shared {
   alignas(16) uint64_t key[LG_CAP];   // LG_CAP is a multiple of 8
@@ -463,25 +498,30 @@ __global__ __launch_bounds__(LG_THREADS) void logit_part_kernel(LogitArgs A, Par
   if (fast) thread_sums<T, LG_NV, false, MODE>(u, nv, A.c, m, flags, s, w);
   else thread_sums<T, LG_NV, true, MODE>(u, nv, A.c, m, flags, s, w);
   block_sums();
+  float mu = m;
+  double own = 0.0;
+  const bool apart = TAIL && w < FAR_TAIL && s > 0.0;   // (the same in every thread; NaN is not)
+  if (apart) unlisted_apart<T, LG_THREADS>(z, base, end, listed, A.c, sh.f, sh.d[0], mu, own);
   if (t == 0) {
     Part p;
     const double d = fast ? (double)(m * A.c) - (double)m * (double)A.c : 0.0, f = exp2(d);
     p.s = s * f;
     p.w = TAIL ? 0.0 : f * (w + d * s);
-    p.rest = w * f;
+    p.rest = apart ? own : w * f;
     p.m = m;
-    p.pad = 0.f;
+    p.mr = mu;
     parts[row * A.S + seg] = p;
   }
   if (!TAIL && A.top > 0) segment_top<T>(vm, nv, tmax, z, base, end, A.top, sh, lists + (row * A.S + seg) * A.top);
 }
 
-// Joins a row's segments, a lane each: every lane returns the row's (s, w,
-// rest) at the common m.
+// Joins a row's segments, a lane each: every lane returns the row's (s, w) at the
+// common m and, with TAIL, rest at mr (-inf: no unlisted element has mass).
 struct RowStat {
   double s, w, rest;
-  float m;
+  float m, mr;
 };
+template <bool TAIL>
 __device__ RowStat join_parts(const Part* __restrict__ p, int S, float c) {
   RowStat r;
   const int lane = threadIdx.x & 63;
@@ -491,17 +531,23 @@ __device__ RowStat join_parts(const Part* __restrict__ p, int S, float c) {
   m = wave_max(m);
   r.m = m == -INFINITY ? 0.f : m;
   r.s = r.w = r.rest = 0.0;
+  r.mr = -INFINITY;
+  if (TAIL) {
+    for (int i = lane; i < S; i += 64)
+      if (!(p[i].rest == 0.0)) r.mr = fmaxf(r.mr, p[i].mr);
+    r.mr = wave_max(r.mr);
+  }
   for (int i = lane; i < S; i += 64) {
     const Part q = p[i];
     if (q.s == 0.0) continue;
     const double d = ((double)q.m - (double)r.m) * (double)c, f = exp2(d);
     r.s += f * q.s;
     r.w += f * (q.w + d * q.s);
-    r.rest += f * q.rest;
+    if (TAIL && !(q.rest == 0.0)) r.rest += exp2(((double)q.mr - (double)r.mr) * (double)c) * q.rest;
   }
   r.s = wave_sum(r.s);
   r.w = wave_sum(r.w);
-  r.rest = wave_sum(r.rest);
+  if (TAIL) r.rest = wave_sum(r.rest);
   return r;
 }
 
@@ -580,7 +626,7 @@ __global__ __launch_bounds__(LG_THREADS) void logprob_row_kernel(LogitArgs A, co
     }
   }
   if (wave > 0) return;
-  const RowStat r = join_parts(parts + row * S, S, A.c);
+  const RowStat r = join_parts<false>(parts + row * S, S, A.c);
   const bool bad = !(r.s < INFINITY);   // a NaN or +inf logit
   // Log probabilities are taken of the logits as scaled by c; lse alone is
   // corrected for c's rounding: d lse / d scale is the mean logit.
@@ -619,11 +665,11 @@ __global__ __launch_bounds__(LG_THREADS) void logprob_row_kernel(LogitArgs A, co
 // statistics and the teacher's list itself (k <= 128 entries), segment 0 writes
 // the loss, each writes its share of the gradient: q_j times one factor per
 // row, then the listed entries, each by one thread, over it.
-template <typename T>
+template <typename T, bool TAIL>
 __global__ __launch_bounds__(LG_THREADS) void distill_grad_kernel(LogitArgs A, const Part* __restrict__ parts,
                                                                   const float* __restrict__ zl,
                                                                   const float* __restrict__ teacher, double invT,
-                                                                  int tail, float* __restrict__ loss,
+                                                                  float* __restrict__ loss,
                                                                   void* __restrict__ grad, int64_t ldg) {
   __shared__ int32_t sid[LG_THREADS];
   __shared__ float sp[LG_THREADS];
@@ -643,7 +689,7 @@ __global__ __launch_bounds__(LG_THREADS) void distill_grad_kernel(LogitArgs A, c
     for (int64_t i = base + (int64_t)t * T::VEC; i < end; i += LG_THREADS * T::VEC) store_vec<T>(gr, i, end, zero);
     return;
   }
-  const RowStat r = join_parts(parts + row * A.S, A.S, A.c);
+  const RowStat r = join_parts<TAIL>(parts + row * A.S, A.S, A.c);
   // this thread's entry of the teacher's list
   int32_t id = -1;
   double lt = -INFINITY;
@@ -654,12 +700,12 @@ __global__ __launch_bounds__(LG_THREADS) void distill_grad_kernel(LogitArgs A, c
     if (id >= 0) {
       lt = (double)teacher[row * A.k + t] * invT;
       zi = zl[row * A.k + t];
-      if (!tail && lt == -INFINITY) id = -1;   // no mass: as if not listed
+      if (!TAIL && lt == -INFINITY) id = -1;   // no mass: as if not listed
     }
   }
   // p: softmax over the list, or the log probabilities themselves (tail)
   double p, lp;
-  if (tail) {
+  if (TAIL) {
     lp = lt;
     p = exp(lt);
   } else {
@@ -693,14 +739,15 @@ __global__ __launch_bounds__(LG_THREADS) void distill_grad_kernel(LogitArgs A, c
       }
   const int named = __syncthreads_count(first ? 1 : 0);
   const double y = ((double)zi - (double)r.m) * (double)A.c;
-  double s = r.s;
-  if (tail) {
+  double s = r.s, rest = 0.0;   // rest: of s, without the listed entries
+  if (TAIL) {
+    if (r.mr > -INFINITY) rest = r.rest * exp2(((double)r.mr - (double)r.m) * (double)A.c);
     const double ls = wave_sum(first ? exp2_series(y) : 0.0);
     if ((t & 63) == 0) red[0][wave] = ls;
     __syncthreads();
     double list = 0.0;
     for (int i = 0; i < LG_WAVES; ++i) list += red[0][i];
-    s = tail_sum(r.s, r.rest, list);
+    s = tail_sum(r.s, rest, list);
   }
   const double term = p == 0.0 ? 0.0 : p * (lp - (y - log2(s)) * LN2);
   const double ps = wave_sum(p), ts = wave_sum(term);
@@ -714,25 +761,37 @@ __global__ __launch_bounds__(LG_THREADS) void distill_grad_kernel(LogitArgs A, c
     psum += red[1][i];
     kl += red[2][i];
   }
+  const double g0 = (double)wt * invT;
   double coef = 1.0;   // of an unlisted q_j
-  if (tail) {
+  float mg = r.m;      // what the unlisted elements' gradients are taken about,
+  double fg = 0.0;     // and their factor, where it is not coef's
+  bool apart = false;
+  if (TAIL) {
     // below 2^-20 the remainder is the rounding of the k float32 log
     // probabilities (k 2^-24 at most 2^-17 of them, of which most is shared);
     // a list that names every token has none
     double pt = 1.0 - psum;
     if (pt < 0x1p-20 || named >= A.V) pt = 0.0;
     if (pt > 0.0) {
-      const double qt = r.rest / s;
-      kl += pt * (log(pt) - log(qt));
-      coef = 1.0 - pt / qt;
+      apart = rest < FAR_TAIL && s > 0.0;
+      if (apart) {
+        // among themselves: their gradient is q_j (1 - pt / qt), where q_j is nothing beside its share of pt
+        const bool any = r.mr > -INFINITY;
+        kl += pt * (log(pt) - (any ? ((double)r.mr - (double)r.m) * (double)A.c + log2(r.rest) - log2(s) : -INFINITY) * LN2);
+        mg = any ? r.mr : 0.f;
+        fg = any ? -g0 * pt / r.rest : 0.0;
+      } else {
+        const double qt = rest / s;
+        kl += pt * (log(pt) - log(qt));
+        coef = 1.0 - pt / qt;
+      }
     }
   } else {
     coef = psum > 0.0 || psum != psum ? 1.0 : 0.0;   // an empty list teaches nothing
   }
   if (seg == 0 && t == 0) loss[row] = (float)((double)wt * kl);
   if (!gr) return;
-  const double g0 = (double)wt * invT;
-  const float m = r.m, f = (float)(coef * g0 / s), inv = (float)(1.0 / s);
+  const float m = r.m, f = (float)(apart ? fg : coef * g0 / s), inv = (float)(1.0 / s);
   float glist = 0.f;
   if (first) glist = (__builtin_amdgcn_exp2f((zi - m) * A.c) * inv - pown) * (float)g0;
   for (int64_t i = base + (int64_t)t * T::VEC; i < end; i += LG_THREADS * T::VEC) {
@@ -740,7 +799,7 @@ __global__ __launch_bounds__(LG_THREADS) void distill_grad_kernel(LogitArgs A, c
     load_vec<T>(z, i, end, u);
     float g[T::VEC];
 #pragma unroll
-    for (int e = 0; e < T::VEC; ++e) g[e] = __builtin_amdgcn_exp2f((T::elem(u, e) - m) * A.c) * f;
+    for (int e = 0; e < T::VEC; ++e) g[e] = __builtin_amdgcn_exp2f((T::elem(u, e) - mg) * A.c) * f;
     store_vec<T>(gr, i, end, g);
   }
   __syncthreads();
@@ -760,7 +819,7 @@ __global__ __launch_bounds__(THREADS) void distill_row_kernel(LogitArgs A, const
   __shared__ float rm[WAVES];
   __shared__ int32_t sid[LOGIT_MAX_TOP];
   __shared__ float sp[LOGIT_MAX_TOP];
-  __shared__ double s_pt;
+  __shared__ double s_pt, s_rest;
   __shared__ int s_twice;
   const int t = threadIdx.x, lane = t & 63, wave = wave_id();
   const int64_t row = blockIdx.x;
@@ -899,7 +958,17 @@ __global__ __launch_bounds__(THREADS) void distill_row_kernel(LogitArgs A, const
   // 2^y / s is q whatever M was rounded to: the sums carry the same factor
   const double pt = s_pt, g0 = (double)wt * invT;
   const double coef = TAIL ? (pt > 0.0 ? 1.0 - pt * s / rest : 1.0) : (pt != 0.0 ? 1.0 : 0.0);
-  const float f = (float)(coef * g0 / s);
+  float f = (float)(coef * g0 / s), mg = m;
+  const bool apart = TAIL && pt > 0.0 && rest < FAR_TAIL && s > 0.0;   // (the same in every thread; NaN is not)
+  if (apart) {   // the unlisted elements' gradients among themselves, as in distill_grad_kernel
+    float mu;
+    double own;
+    unlisted_apart<T, THREADS>(z, 0, A.V, listed, A.c, rm, rs, mu, own);
+    const bool any = mu > -INFINITY;
+    if (t == 0) s_rest = own;   // (for the loss, when the row's registers are free)
+    mg = any ? mu : 0.f;
+    f = any ? -(float)(g0 * pt) / (float)own : 0.f;   // (1 <= own <= 2^20)
+  }
   if (gr) {
     forget(u);
     auto put = [&](auto safe) {
@@ -910,7 +979,7 @@ __global__ __launch_bounds__(THREADS) void distill_row_kernel(LogitArgs A, const
 #pragma unroll
           for (int e = 0; e < T::VEC; ++e) {
             const float x = T::elem(u[j], e);
-            g[e] = __builtin_amdgcn_exp2f(safe.value ? (x - m) * A.c : fmaf(x, A.c, -M)) * f;
+            g[e] = __builtin_amdgcn_exp2f(safe.value ? (x - mg) * A.c : fmaf(x, A.c, -M)) * f;
           }
           Raw16 w;
 #pragma unroll
@@ -920,8 +989,9 @@ __global__ __launch_bounds__(THREADS) void distill_row_kernel(LogitArgs A, const
           __builtin_amdgcn_sched_barrier(0);
         }
     };
-    if (fast) put(std::false_type{}); else put(std::true_type{});
-    if (t < odd) T::store(gr, (int64_t)full * T::VEC + t, elast * f);
+    if (fast && !apart) put(std::false_type{}); else put(std::true_type{});
+    if (t < odd)
+      T::store(gr, (int64_t)full * T::VEC + t, (apart ? __builtin_amdgcn_exp2f((last - mg) * A.c) : elast) * f);
   }
   __syncthreads();
   if (wave != 0) return;
@@ -952,7 +1022,14 @@ __global__ __launch_bounds__(THREADS) void distill_row_kernel(LogitArgs A, const
     if (gr && first[q]) T::store(gr, id[q], (two_to(zi[q]) * (float)(1.0 / s) - own[q]) * (float)g0);
   }
   kl = wave_sum(kl);
-  if (TAIL && pt > 0.0) kl += pt * (log(pt) - log(rest / s));
+  if (TAIL && pt > 0.0) {
+    if (apart) {   // (mg is the unlisted maximum; 0, with no sum, where there is none)
+      const double far = fast ? (double)mg * (double)A.c - (double)M : ((double)mg - (double)m) * (double)A.c;
+      kl += pt * (log(pt) - (far + log2(s_rest) - lg) * LN2);
+    } else {
+      kl += pt * (log(pt) - log(rest / s));
+    }
+  }
   if (lane == 0) loss[row] = (float)((double)wt * kl);
 }
 
@@ -1043,8 +1120,13 @@ hipError_t launch_distill(const LogitArgs& A, const float* teacher, double invT,
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  LOGIT_TYPES(A.dtype, hipLaunchKernelGGL((distill_grad_kernel<T>), grid, block, 0, st, A, parts, zl, teacher, invT,
-                                          tail ? 1 : 0, loss, grad, ldg));
+  if (tail) {
+    LOGIT_TYPES(A.dtype, hipLaunchKernelGGL((distill_grad_kernel<T, true>), grid, block, 0, st, A, parts, zl, teacher,
+                                            invT, loss, grad, ldg));
+  } else {
+    LOGIT_TYPES(A.dtype, hipLaunchKernelGGL((distill_grad_kernel<T, false>), grid, block, 0, st, A, parts, zl, teacher,
+                                            invT, loss, grad, ldg));
+  }
   return hipGetLastError();
 }
 
