@@ -267,8 +267,28 @@ bool bf16_exact(float x) {
   return std::isfinite(x) && (u & 0xffffu) == 0;
 }
 
-// Exact in both 16-bit types.
-bool narrow_exact(float x) { return bf16_exact(x) && (float)(_Float16)x == x; }
+// Exact in both 16-bit types: bfloat16's eight bits fit float16's eleven in its
+// normal range; below it float16 has the multiples of 2^-24.  (A conversion to
+// float16 is a library call on the host.)
+bool narrow_exact(float x) {
+  const float a = std::fabs(x);
+  return bf16_exact(x) && a <= 65504.f && (a >= 0x1p-14f || (float)(int)(a * 0x1p24f) == a * 0x1p24f);
+}
+bool all_narrow(const float* x, int64_t count) {
+  // most often zeros and values of both normal ranges: no branch an element
+  uint32_t odd = 0;
+  for (int64_t k = 0; k < count; ++k) {
+    uint32_t u;
+    memcpy(&u, x + k, 4);
+    u &= 0x7fffffffu;
+    const uint32_t in = u - 0x38800000u <= 0x477f0000u - 0x38800000u ? 0u : u;   // 2^-14 .. 65280
+    odd |= (u & 0xffffu) | in;
+  }
+  if (odd == 0) return true;
+  for (int64_t k = 0; k < count; ++k)
+    if (!narrow_exact(x[k])) return false;
+  return true;
+}
 
 uint16_t bf16_bits(float x) {  // exact values only
   uint32_t u;
@@ -1188,9 +1208,12 @@ int mpq_codebook_prepare(const float* cb, int64_t K, int64_t d, void* tables, si
     std::vector<uint16_t> qk, pv;
     std::vector<uint32_t> e8k, pkl;
     std::vector<uint16_t> pkm;
-    h.narrow = 1;
-    for (int64_t k = 0; k < K * d; ++k)
-      if (!narrow_exact(d == 1 ? cb[k] - cb[K / 2] : cb[k])) h.narrow = 0;
+    if (d == 1) {
+      for (int64_t k = 0; k < K; ++k) lv[k] = cb[k] - cb[K / 2];
+      h.narrow = all_narrow(lv.data(), K);
+    } else {
+      h.narrow = all_narrow(cb, K * d);
+    }
     // evenly spaced levels (in float64, where they and their multiples are exact)
     if (d == 1 && h.narrow) {
       const double step = (double)cb[1] - (double)cb[0];

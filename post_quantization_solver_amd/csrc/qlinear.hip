@@ -21,6 +21,7 @@
 // float16 and float32 results and for the float32 sums of the layer's gradients.
 #include <string.h>
 #include <algorithm>
+#include <vector>
 #include "qlayer.h"
 
 namespace mpq {
@@ -976,35 +977,31 @@ hipError_t launch_q_grad(const QLinearGrad& A, void* ws, hipStream_t st) {
 // point k of N is point N - 1 - k, so a point whose negative is among the first
 // K codewords too shares one table entry with it.
 bool q_e8_tables(const float* cb, int64_t K, uint32_t* lut, uint16_t* map, int* entries, int* pairs) {
-  auto nibbles = [&](int64_t c, uint32_t* v) {
-    *v = 0;
-    for (int q = 0; q < 8; ++q) {
-      const float x = cb[c * 8 + q];
-      const int h = (int)(2.f * (x < 0 ? -x : x));
-      if (h > 7 || 0.5f * h != (x < 0 ? -x : x)) return false;
-      *v |= (uint32_t)(x < 0 ? 8 - h : 8 + h) << (4 * (q / 2 + 4 * (q % 2)));
+  // every codeword's nibbles, 8 + 2 e
+  std::vector<uint32_t> nib((size_t)K);
+  int32_t odd = 0;
+  for (int64_t c = 0; c < K; ++c) {
+    int32_t h[8];
+    for (int q = 0; q < 8; ++q) {   // (without branches: the host's vectors take it)
+      const float x = 2.f * cb[c * 8 + q];
+      h[q] = (int32_t)x + 8;
+      odd |= ((float)(h[q] - 8) != x) | ((h[q] - 1) & ~15) | (h[q] == 16);
     }
-    return true;
-  };
-  auto norm = [&](int64_t c) {
-    float s = 0.f;
-    for (int q = 0; q < 8; ++q) s += cb[c * 8 + q] * cb[c * 8 + q];
-    return s;
-  };
+    nib[(size_t)c] = (uint32_t)(h[0] | h[1] << 16 | h[2] << 4 | h[3] << 20 | h[4] << 8 | h[5] << 24 | h[6] << 12) |
+                     (uint32_t)h[7] << 28;
+  }
+  if (odd) return false;
+  bool ok = true;
   *pairs = q_e8_pairs(K);
-  int64_t pair = 0, lone = 0;
-  for (int64_t s0 = 0; s0 < K;) {
-    int64_t s1 = s0 + 1;
-    while (s1 < K && norm(s1) == norm(s0)) ++s1;
-    const int64_t N = q_e8_shell((int)(norm(s0) / 2.f)), have = s1 - s0;
+  int64_t pair = 0, lone = 0, s0 = 0;
+  for (int h = 0; s0 < K; ++h) {
+    const int64_t N = q_e8_shell(h), have = std::min(N, K - s0);
     for (int64_t k = 0; k < have; ++k) {
       const int64_t o = N - 1 - k;
-      uint32_t v;
-      if (!nibbles(s0 + k, &v)) return false;
+      const uint32_t v = nib[(size_t)(s0 + k)];
       if (o < have && o != k) {
         if (o < k) continue;   // its partner made the entry
-        for (int q = 0; q < 8; ++q)
-          if (cb[(s0 + k) * 8 + q] != -cb[(s0 + o) * 8 + q]) return false;
+        ok &= nib[(size_t)(s0 + o)] == 0x11111110u - v;
         lut[pair] = v;
         map[s0 + k] = (uint16_t)(2 * pair);
         map[s0 + o] = (uint16_t)(2 * pair + 1);
@@ -1016,10 +1013,10 @@ bool q_e8_tables(const float* cb, int64_t K, uint32_t* lut, uint16_t* map, int* 
         ++lone;
       }
     }
-    s0 = s1;
+    s0 += N;
   }
   *entries = (int)(*pairs + lone);
-  return pair == *pairs && 2 * pair + lone == K;
+  return ok && pair == *pairs && 2 * pair + lone == K;
 }
 
 // Points of E8 of squared norm 2 h: 240 times the sum of the cubes of h's divisors.

@@ -65,3 +65,22 @@ def test_slopes_far_out(act, dtype):
     y = f64(mpq.linear_backward(one[:, :-1].contiguous(), x, mpq.pack_layer(dev(codes[:-1]), E, dev(scale[:-1]),
             dev(off[:-1])), pre=pre[:, :-1].contiguous().to(dtype_of(dtype)), activation=act)["dx"])
     assert np.isfinite(y).all()
+
+
+def test_levels_that_both_16_bit_types_hold():
+    """pack_layer takes differences to the middle level that bfloat16 and float16 hold, subnormal ones too, and no
+    others."""
+    import torch
+    import post_quantization_solver_amd as mpq
+    codes = torch.zeros(2, 8, dtype=torch.int32, device="cuda")
+    scale = torch.ones(2, device="cuda")
+    for low, taken in ((2.0 ** -24, True), (2.0 ** -25, False), (1.5 * 2.0 ** -24, False), (3 * 2.0 ** -24, True),
+                       (2.0 ** -14, True), (65280.0, True), (65536.0, False), (1 + 2.0 ** -7, True),
+                       (1 + 2.0 ** -8, False), (float(np.float32(0.1)), False)):
+        for x in (low, -low):
+            E = np.array([[x], [0.0]] if x < 0 else [[0.0], [0.0], [x]], np.float32)
+            if taken:
+                mpq.pack_layer(codes, E, scale)
+            else:
+                with pytest.raises(mpq.MPQError):
+                    mpq.pack_layer(codes, E, scale)
