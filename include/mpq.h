@@ -76,9 +76,6 @@ typedef struct {
   int32_t e8_last2[8];     /* E8 prefix: twice the last codeword's coordinates */
   const void* tables;      /* device, caller-owned: the codebook's tables */
   uint64_t magic;          /* set by mpq_codebook_prepare */
-  int32_t narrow;          /* not 0: the entries (d = 1: their differences to level K / 2) are exact
-                              in bfloat16 and in float16, as mpq_pack needs them; 2: d = 1 and
-                              the levels are evenly spaced, too */
 } mpq_codebook;
 
 #define MPQ_CB_GENERIC   0
@@ -481,7 +478,8 @@ int mpq_factor(double* H, int64_t n, int64_t r, float* s, float* V, void* worksp
  * outside [0, K) is packed as code 0); packed: device, 256-byte aligned, at
  * least mpq_pack_bytes(m, n, K, d) bytes (0 if the shapes are out of range:
  * 0 <= m <= 2^24, 1 <= n <= 65536, n % d == 0, K as for a codebook).
- * Errors: MPQ_EUNSUPPORTED also for a codebook without `narrow`. */
+ * Errors: MPQ_EUNSUPPORTED also for a codebook whose entries (d = 1: their
+ * differences to level K / 2, in float32) are not exact in bfloat16 and in float16. */
 size_t mpq_pack_bytes(int64_t m, int64_t n, int64_t K, int64_t d);
 int mpq_pack(const int32_t* codes, int64_t m, int64_t n, const mpq_codebook* cb, void* packed, size_t packed_bytes,
              void* stream);

@@ -66,7 +66,16 @@ PROF_COUNT = len(PROF_NAMES)
 class Codebook(ctypes.Structure):
     _fields_ = [("K", ctypes.c_int64), ("d", ctypes.c_int64), ("kind", ctypes.c_int32),
                 ("e8_qlast", ctypes.c_int32), ("e8_last2", ctypes.c_int32 * 8), ("tables", ctypes.c_void_p),
-                ("magic", ctypes.c_uint64), ("narrow", ctypes.c_int32)]
+                ("magic", ctypes.c_uint64)]
+
+    @property
+    def narrow(self):
+        """Whether layers of it can be packed: 0, 1, or 2 (1, and evenly spaced levels)."""
+        return (0, 1, 0, 2)[self.magic & 3]
+
+    @narrow.setter
+    def narrow(self, value):
+        self.magic = self.magic & ~3 | (0, 1, 3)[value]
 
 
 class Options(ctypes.Structure):

@@ -400,7 +400,7 @@ void build_lattice_tables(const float* cb, int64_t K, int Kp, std::vector<float>
 // A prepared codebook, checked.
 int check_prepared(const mpq_codebook* cb) {
   if (!cb || !cb->tables) return MPQ_ENULL;
-  if (cb->magic != CB_MAGIC) return MPQ_EPARAM;
+  if ((cb->magic & ~CB_NOTES) != CB_MAGIC) return MPQ_EPARAM;
   if (cb->d != 1 && cb->d != 8) return MPQ_EUNSUPPORTED;
   if (cb->d == 1 && (cb->K < 2 || cb->K > 64)) return MPQ_ESHAPE;
   if (cb->d == 8 && (cb->K < 1 || cb->K > 65536)) return MPQ_ESHAPE;
@@ -1208,18 +1208,18 @@ int mpq_codebook_prepare(const float* cb, int64_t K, int64_t d, void* tables, si
     std::vector<uint16_t> qk, pv;
     std::vector<uint32_t> e8k, pkl;
     std::vector<uint16_t> pkm;
+    bool narrow, even = false;
     if (d == 1) {
       for (int64_t k = 0; k < K; ++k) lv[k] = cb[k] - cb[K / 2];
-      h.narrow = all_narrow(lv.data(), K);
+      narrow = all_narrow(lv.data(), K);
     } else {
-      h.narrow = all_narrow(cb, K * d);
+      narrow = all_narrow(cb, K * d);
     }
     // evenly spaced levels (in float64, where they and their multiples are exact)
-    if (d == 1 && h.narrow) {
+    if (d == 1) {
       const double step = (double)cb[1] - (double)cb[0];
-      bool even = (double)(cb[1] - cb[0]) == step;
+      even = (double)(cb[1] - cb[0]) == step;
       for (int64_t k = 0; k < K; ++k) even = even && (double)cb[k] == (double)cb[0] + (double)k * step;
-      if (even) h.narrow = 2;
     }
     if (d == 1) {
       for (int64_t k = 0; k < K; ++k) lv[k] = cb[k];
@@ -1254,13 +1254,13 @@ int mpq_codebook_prepare(const float* cb, int64_t K, int64_t d, void* tables, si
           MPQ_TRY(hipMemcpyAsync(tb + T.pkl, pkl.data(), pkl.size() * sizeof(uint32_t), hipMemcpyHostToDevice, st));
           MPQ_TRY(hipMemcpyAsync(tb + T.pkm, pkm.data(), pkm.size() * sizeof(uint16_t), hipMemcpyHostToDevice, st));
         } else {
-          h.narrow = 0;
+          narrow = false;
         }
       }
     }
     // the host staging vectors end with this call
     MPQ_TRY(hipStreamSynchronize(st));
-    h.magic = CB_MAGIC;
+    h.magic = CB_MAGIC | (narrow ? CB_NARROW : 0) | (narrow && even ? CB_EVEN : 0);
     *out = h;
     return MPQ_OK;
   });

@@ -68,12 +68,12 @@ int layer_of(QLayer& L, const void* packed, int64_t m, int64_t n, const mpq_code
   int rc = prepared_tables(cb, T);
   if (rc) return rc;
   if ((rc = layer_shape(L, m, n, cb->K, cb->d, group, cb->kind))) return rc;
-  if (!cb->narrow) return MPQ_EUNSUPPORTED;
+  if (!(cb->magic & CB_NARROW)) return MPQ_EUNSUPPORTED;
   L.packed = static_cast<const uint4*>(packed);
   L.scale = scale;
   L.offset = offset;
   L.levels = T.levels;
-  L.uniform = cb->narrow == 2;
+  L.uniform = (cb->magic & CB_EVEN) != 0;
   L.lut = T.pk_lut;
   L.map = T.pk_map;
   L.e32 = T.e32;
