@@ -529,7 +529,7 @@ int mpq_linear(const void* x, int dtype, int64_t t, int64_t ldx, const void* pac
  * the last three together, or all NULL: not wanted.  The residual's gradient is
  * dy.  pre: mpq_linear's (needed with an activation).  du and x enter the sums
  * as two float16 terms (22 bits) under a power of two per row; dx's du times scale
- * as one (11 bits; float16 and float32: two).  t = 0: zeros. */
+ * as one (11 bits; float16 and float32: two).  t = 0 or m = 0: zeros. */
 size_t mpq_linear_backward_workspace_bytes(int dtype, int64_t t, int64_t m, int64_t n, int64_t K, int64_t d,
                                            int64_t group);
 int mpq_linear_backward(const void* dy, int64_t lddy, const void* x, int dtype, int64_t t, int64_t ldx,

@@ -180,7 +180,7 @@ int mpq_linear_backward(const void* dy, int64_t lddy, const void* x, int dtype, 
       if (e == hipSuccess) e = launch_fill_i32(reinterpret_cast<int32_t*>(doffset), m * A.L.G, 0, st);
       if (e == hipSuccess) e = launch_fill_i32(reinterpret_cast<int32_t*>(dbias), m, 0, st);
     }
-    if (t > 0 && dx) return MPQ_ESHAPE;   // a layer without rows has no gradient to give
+    if (e == hipSuccess && t > 0 && dx) e = launch_q_zero_rows(dx, t, n, lddx, dtype, st);   // a layer without rows
     return status_of(e);
   }
   if (!dy || !x || !packed || !scale || (act != MPQ_ACT_NONE && !pre)) return MPQ_ENULL;

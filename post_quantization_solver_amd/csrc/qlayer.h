@@ -489,6 +489,7 @@ size_t q_linear_workspace(const QLinearArgs& A);
 hipError_t launch_q_linear(const QLinearArgs& A, void* ws, hipStream_t st);
 size_t q_grad_workspace(const QLinearGrad& A);
 hipError_t launch_q_grad(const QLinearGrad& A, void* ws, hipStream_t st);
+hipError_t launch_q_zero_rows(void* p, int64_t rows, int64_t cols, int64_t ld, int dtype, hipStream_t st);
 
 // Host images of an E8 prefix's decoder table and code map (K each at most);
 // false if the codebook does not have the shells' structure.

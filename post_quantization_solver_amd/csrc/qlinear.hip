@@ -967,6 +967,24 @@ size_t q_grad_workspace(const QLinearGrad& A) {
   (void)backward(A, nullptr, &b, nullptr);
   return b;
 }
+// Zeros for dx, whose rows may stand apart.
+__global__ __launch_bounds__(256) void q_zero_rows_kernel(char* __restrict__ p, int64_t rows, int64_t cols, int64_t ld,
+                                                          int es) {
+  const int64_t total = rows * cols, step = (int64_t)gridDim.x * 256;
+  for (int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x; k < total; k += step) {
+    char* at = p + (k / cols * ld + k % cols) * es;
+    if (es == 4) *reinterpret_cast<uint32_t*>(at) = 0;
+    else *reinterpret_cast<uint16_t*>(at) = 0;
+  }
+}
+hipError_t launch_q_zero_rows(void* p, int64_t rows, int64_t cols, int64_t ld, int dtype, hipStream_t st) {
+  const int64_t blocks = std::min<int64_t>((rows * cols + 255) / 256, 4096);
+  if (blocks == 0) return hipSuccess;
+  hipLaunchKernelGGL(q_zero_rows_kernel, dim3((unsigned)blocks), dim3(256), 0, st, static_cast<char*>(p), rows, cols, ld,
+                     dtype == DT_F32 ? 4 : 2);
+  return hipGetLastError();
+}
+
 hipError_t launch_q_grad(const QLinearGrad& A, void* ws, hipStream_t st) {
   return backward(A, static_cast<char*>(ws), nullptr, st);
 }

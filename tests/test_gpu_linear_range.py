@@ -84,3 +84,22 @@ def test_levels_that_both_16_bit_types_hold():
             else:
                 with pytest.raises(mpq.MPQError):
                     mpq.pack_layer(codes, E, scale)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_backward_of_a_layer_without_rows(dtype):
+    """dx is zeros, in its own elements alone; nothing else has an element."""
+    import torch
+    import post_quantization_solver_amd as mpq
+    codes, E, scale, off = make_layer("s16", 4, 33, 0, 1)
+    none = mpq.pack_layer(dev(codes[:0]), E, dev(scale[:0]), dev(off[:0]))
+    x = torch.ones(70, 33, device="cuda").to(dtype_of(dtype))
+    r = mpq.linear_backward(x[:, :0], x, none)
+    assert r["dx"].shape == (70, 33) and not r["dx"].any() and r["dscale"].shape == (0,) == r["dbias"].shape
+    buf = torch.ones(70, 40, device="cuda").to(dtype_of(dtype))
+    lib = mpq.load_library()
+    code = {"bf16": 0, "fp32": 2}[dtype]
+    assert lib.mpq_linear_backward(None, 0, x.data_ptr(), code, 70, 33, None, 0, 33, none.codebook.ref(), None, None, 0,
+                                   0, None, 0, buf.data_ptr(), 40, None, None, None, None, 0,
+                                   torch.cuda.current_stream().cuda_stream) == 0
+    assert not buf[:, :33].any() and (buf[:, 33:] == 1).all()
