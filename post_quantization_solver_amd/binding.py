@@ -792,7 +792,8 @@ ACTIVATIONS = {None: 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}   # MPQ
 
 class PackedLayer:
     """A solved layer ready for `linear`: its packed codes, its codebook and its
-    affine (the given tensors themselves: tuned in place, they are used as tuned)."""
+    affine (the given tensors themselves: tuned in place, they are used as tuned;
+    `scale` and `offset` may also be set to others of their shape and type)."""
 
     def __init__(self, codes, cb, row_scale, row_offset=None, group=None):
         import torch
@@ -809,14 +810,31 @@ class PackedLayer:
             if self.group < 0 or self.group and self.codebook.d != 1:
                 raise MPQError(-3 if self.group < 0 else -4, "pack_layer")
             self.scale, self.offset = row_scale, row_offset
-            _affine(row_scale, row_offset if row_offset is not None else row_scale, self.m, self.n, self.group)
-            _on(row_scale, "row_scale", dev)
-            if row_offset is not None:
-                _on(row_offset, "row_offset", dev)
+            G = -(-self.n // self.group) if 0 < self.group < self.n else 1
+            self._shapes = ((self.m,), (self.m, 1)) if G == 1 else ((self.m, G),)
+            self._kind = (torch.float32, dev)
+            self.check_affine(dev)
             self.packed = torch.empty(lib.mpq_pack_bytes(self.m, self.n, self.codebook.K, self.codebook.d),
                                       dtype=torch.uint8, device=dev)
             _check(lib.mpq_pack(_at(codes), self.m, self.n, self.codebook.ref(), _at(self.packed),
                                 self.packed.numel(), _raw_stream(dev)), "mpq_pack")
+
+    def check_affine(self, dev):
+        """Raises unless scale and offset, which tuning may have replaced, are what the kernels read."""
+        kind, shapes, a, o = self._kind, self._shapes, self.scale, self.offset
+        try:   # (a call of a few microseconds should not spend them here)
+            if (a.shape in shapes and (a.dtype, a.device) == kind and a.is_contiguous()
+                    and (o is None or o.shape in shapes and (o.dtype, o.device) == kind and o.is_contiguous())):
+                return
+        except AttributeError:
+            pass
+        for t, name in ((a, "row_scale"), (o, "row_offset")):
+            if t is None and name == "row_offset":
+                continue
+            _dev(t, kind[0], name)
+            _on(t, name, dev)
+            if t.shape not in shapes:
+                raise ValueError(f"{name} has shape {tuple(t.shape)}, expected " + " or ".join(map(str, shapes)))
 
 
 def pack_layer(codes, cb, row_scale, row_offset=None, group=None) -> PackedLayer:
@@ -849,6 +867,7 @@ def linear(x, layer, bias=None, activation=None, residual=None, return_pre=False
     if n != layer.n:
         raise ValueError(f"x has {n} columns, the layer {layer.n}")
     _on(layer.packed, "the layer", dev)
+    layer.check_affine(dev)
     act = _activation(activation)
     if bias is not None:
         _dev(bias, torch.float32, "bias", (m,))
@@ -880,6 +899,7 @@ def linear_backward(dy, x, layer, pre=None, activation=None, need_dx=True, need_
     if n != layer.n:
         raise ValueError(f"x has {n} columns, the layer {layer.n}")
     _on(layer.packed, "the layer", dev)
+    layer.check_affine(dev)
     act = _activation(activation)
     lddy = _rows(dy, "dy", x, (t, m))
     if act and pre is None:

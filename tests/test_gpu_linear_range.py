@@ -103,3 +103,32 @@ def test_backward_of_a_layer_without_rows(dtype):
                                    0, None, 0, buf.data_ptr(), 40, None, None, None, None, 0,
                                    torch.cuda.current_stream().cuda_stream) == 0
     assert not buf[:, :33].any() and (buf[:, 33:] == 1).all()
+
+
+@pytest.mark.parametrize("group", [0, 16])
+def test_a_replaced_affine_is_checked(group):
+    """scale and offset of a packed layer are public: others of their kind are used, anything else is refused."""
+    import torch
+    import post_quantization_solver_amd as mpq
+    codes, E, scale, off = make_layer("s16", 20, 64, group, 1)
+    layer = mpq.pack_layer(dev(codes), E, dev(scale), dev(off), group=group or None)
+    x, dy = torch.randn(3, 64, device="cuda"), torch.randn(3, 20, device="cuda")
+    y = mpq.linear(x, layer)
+    good = {"scale": dev(scale), "offset": dev(off)}
+    for name, t in good.items():
+        for bad in (t.half(), t.double(), t.cpu(), None if name == "scale" else 0.5, t[:19].contiguous(),
+                    t.view(-1)[:1], torch.zeros(20, 3, device="cuda"), torch.zeros(40, 4, device="cuda")[::2],
+                    torch.zeros(4, 20, device="cuda").t()):
+            setattr(layer, name, bad)
+            with pytest.raises((TypeError, ValueError)):
+                mpq.linear(x, layer)
+            with pytest.raises((TypeError, ValueError)):
+                mpq.linear_backward(dy, x, layer)
+        setattr(layer, name, t.clone())
+        assert torch.equal(mpq.linear(x, layer), y)
+    layer.offset = None
+    assert torch.equal(mpq.linear(x, layer), mpq.linear(x, mpq.pack_layer(dev(codes), E, dev(scale), group=group or None)))
+    if not group:
+        layer.scale = dev(scale)[:, None]
+        r = mpq.linear_backward(dy, x, layer)
+        assert r["dscale"].shape == (20, 1)
