@@ -850,6 +850,14 @@ def _activation(name):
     return ACTIVATIONS[name]
 
 
+def _no_graph(t, name):
+    """Refuses a tensor whose autograd graph would end here unnoticed."""
+    import torch
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name} requires a gradient, which linear does not record: detach it, or call under "
+                         "torch.no_grad(), and take the gradients from linear_backward")
+
+
 def linear(x, layer, bias=None, activation=None, residual=None, return_pre=False, out=None, workspace=None):
     """act(x W^T + bias) + residual of a packed layer (mpq_linear).
 
@@ -857,10 +865,12 @@ def linear(x, layer, bias=None, activation=None, residual=None, return_pre=False
     float32; `activation`: None, "relu", "gelu", "gelu_tanh" or "silu";
     `residual`: t x m of x's type; `out`: t x m to write (it may be the
     residual).  Returns y, or (y, pre) with the activation's argument, which
-    linear_backward takes.
+    linear_backward takes.  No autograd graph is recorded: an x or residual that
+    requires a gradient is refused where gradients are enabled.
     """
     import torch
     code = _dtype_code(x, "x")
+    _no_graph(x, "x")
     ldx = _rows(x, "x")
     t, n = x.shape
     m, cb, dev = layer.m, layer.codebook, x.device
@@ -872,7 +882,10 @@ def linear(x, layer, bias=None, activation=None, residual=None, return_pre=False
     if bias is not None:
         _dev(bias, torch.float32, "bias", (m,))
         _on(bias, "bias", dev)
-    ldr = _rows(residual, "residual", x, (t, m)) if residual is not None else m
+    ldr = m
+    if residual is not None:
+        ldr = _rows(residual, "residual", x, (t, m))
+        _no_graph(residual, "residual")
     lib = load_library()
     with _guard(dev):
         y = torch.empty((t, m), dtype=x.dtype, device=dev) if out is None else out
@@ -963,7 +976,8 @@ def distill(logits, teacher_ids, teacher, temperature=1.0, tail=False, weights=N
     loss and gradient, 0 skips a row.  `grad`: True for a new tensor, False for
     the loss alone, or a tensor to write (logits itself: in place).
     loss: t float32, weight * KL(teacher || student) per row; grad: its
-    gradient with respect to the logits, in their type.
+    gradient with respect to the logits, in their type (no autograd graph is
+    recorded: logits.backward(grad) takes it on).
     """
     import torch
     code = _dtype_code(logits, "logits")

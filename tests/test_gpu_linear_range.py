@@ -132,3 +132,26 @@ def test_a_replaced_affine_is_checked(group):
         layer.scale = dev(scale)[:, None]
         r = mpq.linear_backward(dy, x, layer)
         assert r["dscale"].shape == (20, 1)
+
+
+def test_an_autograd_graph_does_not_end_unnoticed():
+    """linear records no graph: an input that has one is refused, except where gradients are off.  The graph goes on by
+    hand, through linear_backward."""
+    import torch
+    import post_quantization_solver_amd as mpq
+    codes, E, scale, off = make_layer("s16", 20, 64, 0, 1)
+    layer = mpq.pack_layer(dev(codes), E, dev(scale), dev(off))
+    leaf = torch.randn(3, 64, device="cuda", requires_grad=True)
+    x, res = leaf * 2, torch.zeros(3, 20, device="cuda", requires_grad=True)
+    with pytest.raises(ValueError):
+        mpq.linear(x, layer)
+    with pytest.raises(ValueError):
+        mpq.linear(leaf, layer)
+    with pytest.raises(ValueError):
+        mpq.linear(x.detach(), layer, residual=res)
+    y = mpq.linear(x.detach(), layer, residual=res.detach())
+    with torch.no_grad():
+        assert torch.equal(mpq.linear(x, layer, residual=res), y)
+    dx = mpq.linear_backward(y, x, layer)["dx"]
+    x.backward(dx)
+    assert torch.equal(leaf.grad, 2 * dx)
