@@ -477,7 +477,8 @@ int mpq_factor(double* H, int64_t n, int64_t r, float* s, float* V, void* worksp
  * order the kernels read.  codes: m x n/d int32 (mpq_quantize_layer's; a code
  * outside [0, K) is packed as code 0); packed: device, 256-byte aligned, at
  * least mpq_pack_bytes(m, n, K, d) bytes (0 if the shapes are out of range:
- * 0 <= m <= 2^24, 1 <= n <= 65536, n % d == 0, K as for a codebook).
+ * 0 <= m <= 2^24, 1 <= n <= 65536, n % d == 0, K as for a codebook, packed
+ * codes of less than 64 GiB).
  * Errors: MPQ_EUNSUPPORTED also for a codebook whose entries (d = 1: their
  * differences to level K / 2, in float32) are not exact in bfloat16 and in float16. */
 size_t mpq_pack_bytes(int64_t m, int64_t n, int64_t K, int64_t d);
@@ -529,7 +530,9 @@ int mpq_linear(const void* x, int dtype, int64_t t, int64_t ldx, const void* pac
  * the last three together, or all NULL: not wanted.  The residual's gradient is
  * dy.  pre: mpq_linear's (needed with an activation).  du and x enter the sums
  * as two float16 terms (22 bits) under a power of two per row; dx's du times scale
- * as one (11 bits; float16 and float32: two).  t = 0 or m = 0: zeros. */
+ * as one (11 bits; float16 and float32: two).  t = 0 or m = 0: zeros.
+ * ceil(t / 64) (ceil(m / 64) + ceil(n / 64)) < 2^24; groups of multiples of 64
+ * columns: ceil(m ceil(n / group) / 16) + ceil(m / 256) < 2^24. */
 size_t mpq_linear_backward_workspace_bytes(int dtype, int64_t t, int64_t m, int64_t n, int64_t K, int64_t d,
                                            int64_t group);
 int mpq_linear_backward(const void* dy, int64_t lddy, const void* x, int dtype, int64_t t, int64_t ldx,

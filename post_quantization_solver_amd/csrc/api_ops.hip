@@ -57,6 +57,8 @@ int layer_shape(QLayer& L, int64_t m, int64_t n, int64_t K, int64_t d, int64_t g
   L.K = (int)K;
   L.tiles = (int)((m + 15) / 16);
   L.chunks = (int)((n + q_chunk(L.fmt) - 1) / q_chunk(L.fmt));
+  // (a thread per 16 bytes lays them out, and a grid has fewer than 2^32)
+  if ((int64_t)L.tiles * L.chunks >= (int64_t)1 << 26) return MPQ_ESHAPE;
   L.group = group > 0 && group < n ? group : n;
   L.G = (int)((n + L.group - 1) / L.group);
   return MPQ_OK;
@@ -82,6 +84,15 @@ int layer_of(QLayer& L, const void* packed, int64_t m, int64_t n, const mpq_code
     L.lut_entries = (int)cb->K - L.pairs;
   }
   return MPQ_OK;
+}
+
+// What the gradients' grids of 256 threads a workgroup take (fewer than 2^32 in
+// all): tiles of 64 x 64 of du and x; 16 entries of the affine a workgroup beside
+// d bias, where the contraction takes the layer in one piece.
+bool grad_fits(const QLayer& L, int64_t t) {
+  const int64_t most = (int64_t)1 << 24;
+  return ((L.m + 63) / 64 + (L.n + 63) / 64) * ((t + 63) / 64) < most &&
+         (L.group % Q_CONTRACT != 0 || (L.m * L.G + 15) / 16 + (L.m + 255) / 256 < most);
 }
 
 // Enough for every combination of outputs and activation.
@@ -151,7 +162,8 @@ int mpq_linear(const void* x, int dtype, int64_t t, int64_t ldx, const void* pac
 size_t mpq_linear_backward_workspace_bytes(int dtype, int64_t t, int64_t m, int64_t n, int64_t K, int64_t d,
                                            int64_t group) {
   QLinearGrad A = {};
-  if (!dtype_ok(dtype) || t < 0 || t >= Q_MAX_T || layer_shape(A.L, m, n, K, d, group, MPQ_CB_GENERIC) != MPQ_OK)
+  if (!dtype_ok(dtype) || t < 0 || t >= Q_MAX_T || layer_shape(A.L, m, n, K, d, group, MPQ_CB_GENERIC) != MPQ_OK ||
+      !grad_fits(A.L, t))
     return 0;
   A.dtype = dtype;
   A.t = t;
@@ -168,7 +180,8 @@ int mpq_linear_backward(const void* dy, int64_t lddy, const void* x, int dtype, 
   if (rc) return rc;
   const bool need_dlayer = dscale || doffset || dbias;
   if (!dtype_ok(dtype) || act < MPQ_ACT_NONE || act > MPQ_ACT_SILU) return MPQ_EPARAM;
-  if (t < 0 || t >= Q_MAX_T || lddy < m || ldx < n || (act != MPQ_ACT_NONE && ldp < m) || (dx && lddx < n))
+  if (t < 0 || t >= Q_MAX_T || lddy < m || ldx < n || (act != MPQ_ACT_NONE && ldp < m) || (dx && lddx < n) ||
+      !grad_fits(A.L, t))
     return MPQ_ESHAPE;
   if (need_dlayer && m > 0 && (!dscale || !doffset || !dbias)) return MPQ_ENULL;
   hipStream_t st = static_cast<hipStream_t>(stream);

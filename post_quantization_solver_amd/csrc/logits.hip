@@ -1062,72 +1062,103 @@ size_t logit_workspace(const LogitArgs& A) {
     default: { using T = Fp32; call; break; }      \
   }
 
-hipError_t launch_token_logprobs(const LogitArgs& A, const int32_t* tokens, float* logprob, float* entropy,
-                                 float* lse, int32_t* top_ids, float* top_lp, void* ws, hipStream_t st) {
-  Part* parts = static_cast<Part*>(ws);
-  uint64_t* lists = reinterpret_cast<uint64_t*>(parts + A.t * A.S);
-  const dim3 grid((unsigned)(A.t * A.S)), block(LG_THREADS);
-  LOGIT_TYPES(A.dtype, hipLaunchKernelGGL((logit_part_kernel<T, false>), grid, block, 0, st, A, parts, lists,
-                                          static_cast<float*>(nullptr)));
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  // one wave per row where there is little to merge
-  const dim3 rows((unsigned)A.t), waves(A.S > 2 && A.top > 0 ? LG_THREADS : 64);
-  if (A.top <= 64) {
-    LOGIT_TYPES(A.dtype, hipLaunchKernelGGL((logprob_row_kernel<T, 1>), rows, waves, 0, st, A, parts, lists, tokens,
-                                            logprob, entropy, lse, top_ids, top_lp));
-  } else {
-    LOGIT_TYPES(A.dtype, hipLaunchKernelGGL((logprob_row_kernel<T, 2>), rows, waves, 0, st, A, parts, lists, tokens,
-                                            logprob, entropy, lse, top_ids, top_lp));
-  }
-  return hipGetLastError();
-}
+// Launches for as many rows at a time as a grid takes (fewer than 2^32 threads in
+// all, of up to 1024 a workgroup): launch(those rows' arguments, the first row).
+constexpr int64_t LG_LAUNCH = 1 << 21;   // workgroups
 
-hipError_t launch_distill(const LogitArgs& A, const float* teacher, double invT, bool tail, float* loss, void* grad,
-                          int64_t ldg, void* ws, hipStream_t st) {
-  Part* parts = static_cast<Part*>(ws);
-  float* zl = reinterpret_cast<float*>(parts + A.t * A.S);
-  const dim3 grid((unsigned)(A.t * A.S)), block(LG_THREADS), rows((unsigned)A.t);
-  // rows that fit one workgroup's registers, where there are enough of them to
-  // keep half the CUs at work
-  const int64_t vec = 16 / es_of(A.dtype);
-  if (A.t >= 128 && A.V <= 1024 * 16 * vec) {
-    if (A.V <= 256 * 8 * vec) {
-      if (tail) {
-        LOGIT_TYPES(A.dtype, hipLaunchKernelGGL((distill_row_kernel<T, 256, 8, true>), rows, dim3(256), 0, st, A,
-                                                teacher, invT, loss, grad, ldg));
-      } else {
-        LOGIT_TYPES(A.dtype, hipLaunchKernelGGL((distill_row_kernel<T, 256, 8, false>), rows, dim3(256), 0, st, A,
-                                                teacher, invT, loss, grad, ldg));
-      }
+template <typename F>
+static hipError_t in_slices(const LogitArgs& A, F&& launch) {
+  const int64_t most = std::max<int64_t>(1, LG_LAUNCH / A.S);
+  for (int64_t r0 = 0; r0 < A.t; r0 += most) {
+    LogitArgs B = A;
+    B.t = std::min(most, A.t - r0);
+    B.z = static_cast<const char*>(A.z) + r0 * A.ldz * es_of(A.dtype);
+    if (A.ids) B.ids += r0 * A.k;
+    if (A.weights) B.weights += r0;
+    const hipError_t e = launch(B, r0);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+template <typename P>
+static P* from_row(P* p, int64_t elements) { return p ? p + elements : nullptr; }
+
+hipError_t launch_token_logprobs(const LogitArgs& all, const int32_t* tokens, float* logprob, float* entropy,
+                                 float* lse, int32_t* top_ids, float* top_lp, void* ws, hipStream_t st) {
+  Part* const all_parts = static_cast<Part*>(ws);
+  uint64_t* const all_lists = reinterpret_cast<uint64_t*>(all_parts + all.t * all.S);
+  return in_slices(all, [&](const LogitArgs& A, int64_t r0) {
+    Part* parts = all_parts + r0 * A.S;
+    uint64_t* lists = all_lists + r0 * A.S * A.top;
+    LOGIT_TYPES(A.dtype, hipLaunchKernelGGL((logit_part_kernel<T, false>), dim3((unsigned)(A.t * A.S)),
+                                            dim3(LG_THREADS), 0, st, A, parts, lists, static_cast<float*>(nullptr)));
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    // one wave per row where there is little to merge
+    auto rows = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, dim3((unsigned)A.t), dim3(A.S > 2 && A.top > 0 ? LG_THREADS : 64), 0, st, A, parts,
+                         lists, from_row(tokens, r0), from_row(logprob, r0), from_row(entropy, r0), from_row(lse, r0),
+                         from_row(top_ids, r0 * A.top), from_row(top_lp, r0 * A.top));
+    };
+    if (A.top <= 64) {
+      LOGIT_TYPES(A.dtype, (rows(logprob_row_kernel<T, 1>)));
     } else {
-      if (tail) {
-        LOGIT_TYPES(A.dtype, hipLaunchKernelGGL((distill_row_kernel<T, 1024, 16, true>), rows, dim3(1024), 0, st, A,
-                                                teacher, invT, loss, grad, ldg));
-      } else {
-        LOGIT_TYPES(A.dtype, hipLaunchKernelGGL((distill_row_kernel<T, 1024, 16, false>), rows, dim3(1024), 0, st, A,
-                                                teacher, invT, loss, grad, ldg));
-      }
+      LOGIT_TYPES(A.dtype, (rows(logprob_row_kernel<T, 2>)));
     }
     return hipGetLastError();
-  }
-  if (tail) {
-    LOGIT_TYPES(A.dtype, hipLaunchKernelGGL((logit_part_kernel<T, true>), grid, block, 0, st, A, parts,
-                                            static_cast<uint64_t*>(nullptr), zl));
-  } else {
-    LOGIT_TYPES(A.dtype, hipLaunchKernelGGL((logit_part_kernel<T, false>), grid, block, 0, st, A, parts,
-                                            static_cast<uint64_t*>(nullptr), zl));
-  }
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  if (tail) {
-    LOGIT_TYPES(A.dtype, hipLaunchKernelGGL((distill_grad_kernel<T, true>), grid, block, 0, st, A, parts, zl, teacher,
-                                            invT, loss, grad, ldg));
-  } else {
-    LOGIT_TYPES(A.dtype, hipLaunchKernelGGL((distill_grad_kernel<T, false>), grid, block, 0, st, A, parts, zl, teacher,
-                                            invT, loss, grad, ldg));
-  }
-  return hipGetLastError();
+  });
+}
+
+hipError_t launch_distill(const LogitArgs& all, const float* teacher, double invT, bool tail, float* loss, void* grad,
+                          int64_t ldg, void* ws, hipStream_t st) {
+  Part* const all_parts = static_cast<Part*>(ws);
+  float* const all_zl = reinterpret_cast<float*>(all_parts + all.t * all.S);
+  // rows that fit one workgroup's registers, where there are enough of them to
+  // keep half the CUs at work
+  const int64_t vec = 16 / es_of(all.dtype);
+  const bool whole = all.t >= 128 && all.V <= 1024 * 16 * vec, narrow = all.V <= 256 * 8 * vec;
+  return in_slices(all, [&](const LogitArgs& A, int64_t r0) {
+    const float* list = from_row(teacher, r0 * A.k);
+    float* l = loss + r0;
+    void* g = from_row(static_cast<char*>(grad), r0 * ldg * es_of(A.dtype));
+    if (whole) {
+      auto row = [&](auto kernel, int threads) {
+        hipLaunchKernelGGL(kernel, dim3((unsigned)A.t), dim3(threads), 0, st, A, list, invT, l, g, ldg);
+      };
+      if (narrow && tail) {
+        LOGIT_TYPES(A.dtype, (row(distill_row_kernel<T, 256, 8, true>, 256)));
+      } else if (narrow) {
+        LOGIT_TYPES(A.dtype, (row(distill_row_kernel<T, 256, 8, false>, 256)));
+      } else if (tail) {
+        LOGIT_TYPES(A.dtype, (row(distill_row_kernel<T, 1024, 16, true>, 1024)));
+      } else {
+        LOGIT_TYPES(A.dtype, (row(distill_row_kernel<T, 1024, 16, false>, 1024)));
+      }
+      return hipGetLastError();
+    }
+    Part* parts = all_parts + r0 * A.S;
+    float* zl = all_zl + r0 * A.k;
+    const dim3 grid((unsigned)(A.t * A.S)), block(LG_THREADS);
+    auto part = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, grid, block, 0, st, A, parts, static_cast<uint64_t*>(nullptr), zl);
+    };
+    auto finish = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, grid, block, 0, st, A, parts, zl, list, invT, l, g, ldg);
+    };
+    if (tail) {
+      LOGIT_TYPES(A.dtype, (part(logit_part_kernel<T, true>)));
+    } else {
+      LOGIT_TYPES(A.dtype, (part(logit_part_kernel<T, false>)));
+    }
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (tail) {
+      LOGIT_TYPES(A.dtype, (finish(distill_grad_kernel<T, true>)));
+    } else {
+      LOGIT_TYPES(A.dtype, (finish(distill_grad_kernel<T, false>)));
+    }
+    return hipGetLastError();
+  });
 }
 
 }  // namespace mpq
