@@ -45,7 +45,7 @@ __device__ __forceinline__ void wait_stage() {
 template <int BM, int LOADS>
 struct Cursor {
   const char* p[LOADS];
-  int pair, k, kts;
+  int pair, k;
   __device__ __forceinline__ void seek(const QGemm& g, int64_t i0, int64_t j0, int wave, const uint32_t* off, int pair_,
                                        int k_) {
     pair = pair_;
@@ -162,7 +162,6 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void q_gemm_kernel(QGemm g, float*
   const int r = lane & 15, kb = lane >> 4;
   Frags<SM, SN> f0, f1;
   Cursor<BM, LOADS> at;
-  at.kts = kts;
   at.seek(g, i0, j0, wave, off, kt0 / kts, kt0 % kts);
   // Step kt's operands are in registers when its turn begins; the barrier then
   // says that stage kt + 1 is there and that every wave has read stage kt, whose
@@ -218,7 +217,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void q_gemm_kernel(QGemm g, float*
   const int qrow = lane / QUADS, qcol = lane % QUADS * 4;
   const int64_t ii = i0 + wm * SM * 16 + qcol;
   float* own = reg + qrow * PITCH + qcol;   // and every RPI rows from there
-  const QCol C = q_col4(g.O, ii, true);
+  const QCol C = q_col4(g.O, ii);
   auto slot = [&](int it) { return reinterpret_cast<v4f*>(own + it * RPI * PITCH); };
 #pragma unroll 1
   for (int j = 0; j < SN; ++j) {   // (one copy of the body; the accumulators by constant index)
@@ -325,7 +324,7 @@ __global__ __launch_bounds__(256) void q_split_finish_kernel(const float* __rest
     v[2] += q.z;
     v[3] += q.w;
   }
-  q_finish4(O, j, i, v, true);
+  q_finish4(O, j, i, v);
 }
 
 // Tile 256 x 256 moves the fewest bytes into LDS per product, 128 x 128 twice

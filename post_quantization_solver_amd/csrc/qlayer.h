@@ -335,17 +335,16 @@ struct QCol {
   float a[4], o[4], b[4];
   int live;   // columns there are (<= 0: none)
 };
-__device__ __forceinline__ QCol q_col4(const QOut& O, int64_t i, bool affine) {
+__device__ __forceinline__ QCol q_col4(const QOut& O, int64_t i) {
   QCol C;
   C.live = (int)min((int64_t)4, O.cols - i);
-  const float mid = affine && O.colscale && O.mid >= 0 ? O.levels[O.mid] : 0.f;
+  const float mid = O.colscale && O.mid >= 0 ? O.levels[O.mid] : 0.f;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     C.a[k] = C.o[k] = 1.f;
     C.b[k] = 0.f;
     if (k >= C.live) continue;
     if (O.bias) C.b[k] = O.bias[i + k];
-    if (!affine) continue;
     if (O.colscale) {
       C.a[k] = O.colscale[i + k];
       C.o[k] = fmaf(C.a[k], mid, O.coloff ? O.coloff[i + k] : 0.f);
@@ -362,16 +361,11 @@ __device__ __forceinline__ void q_affine4(const QOut& O, const QCol& C, int64_t 
   for (int k = 0; k < 4; ++k) v[k] = fmaf(C.a[k], v[k] * f, (O.rowadd ? C.o[k] * add : 0.f) + C.b[k]);
 }
 
-// Four columns of row j: y = act(v + bias) + res, v with the affine still to come or not.
-__device__ __forceinline__ void q_finish4(const QOut& O, int64_t j, int64_t i, float* v, bool affine) {
-  const QCol C = q_col4(O, i, affine);
+// Four columns of row j: y = act(affine of v + bias) + res.
+__device__ __forceinline__ void q_finish4(const QOut& O, int64_t j, int64_t i, float* v) {
+  const QCol C = q_col4(O, i);
   if (j >= O.rows || C.live <= 0) return;
-  if (affine) {
-    q_affine4(O, C, j, v);
-  } else {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] += C.b[k];
-  }
+  q_affine4(O, C, j, v);
   if (O.pre) store4(O.pre, j * O.ldpre + i, O.dtype, O.vec, C.live, v);
   if (O.act != ACT_NONE)
 #pragma unroll
