@@ -739,6 +739,8 @@ def _rows(t, name, like=None, shape=None):
         raise TypeError(f"{name} must be a CUDA (HIP) torch tensor")
     if like is not None and (t.dtype != like.dtype or t.device != like.device):
         raise TypeError(f"{name} must be {like.dtype} on {like.device}, got {t.dtype} on {t.device}")
+    if t.dim() == 2 and t.is_contiguous() and (shape is None or t.shape == shape):
+        return t.shape[1] or 1   # (most often, and a call of a few microseconds should not spend them on the rest)
     if t.dim() != 2 or shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape) if shape is not None else '2 dimensions'}")
     ld = t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
@@ -851,9 +853,9 @@ def _activation(name):
 
 
 def _no_graph(t, name):
-    """Refuses a tensor whose autograd graph would end here unnoticed."""
+    """Refuses a tensor that requires a gradient, where its graph would end here unnoticed."""
     import torch
-    if t.requires_grad and torch.is_grad_enabled():
+    if torch.is_grad_enabled():
         raise ValueError(f"{name} requires a gradient, which linear does not record: detach it, or call under "
                          "torch.no_grad(), and take the gradients from linear_backward")
 
@@ -870,7 +872,8 @@ def linear(x, layer, bias=None, activation=None, residual=None, return_pre=False
     """
     import torch
     code = _dtype_code(x, "x")
-    _no_graph(x, "x")
+    if x.requires_grad:
+        _no_graph(x, "x")
     ldx = _rows(x, "x")
     t, n = x.shape
     m, cb, dev = layer.m, layer.codebook, x.device
@@ -885,7 +888,8 @@ def linear(x, layer, bias=None, activation=None, residual=None, return_pre=False
     ldr = m
     if residual is not None:
         ldr = _rows(residual, "residual", x, (t, m))
-        _no_graph(residual, "residual")
+        if residual.requires_grad:
+            _no_graph(residual, "residual")
     lib = load_library()
     with _guard(dev):
         y = torch.empty((t, m), dtype=x.dtype, device=dev) if out is None else out
