@@ -379,10 +379,17 @@ hipError_t pick_rows(const SkinnyArgs& A, hipStream_t st) {
 template <int FMT, typename T, int XP, bool GROUPED, bool UNI>
 hipError_t pick_tokens(const SkinnyArgs& A, hipStream_t st) {
   if (A.t <= 16) return pick_rows<FMT, T, XP, 1, GROUPED, UNI>(A, st);
-  // four tiles of 16 tokens share a decoding, or five where that saves one (65
-  // tokens of 4096 x 4096, E8: 25.4 us in two passes, 18 in one)
+  // Four tiles of 16 tokens share a decoding, or five where that saves a round of
+  // workgroups, one on each of the 256 CUs.
+  // Measured, five | four, bfloat16: 80 tokens of 2304 x 8192 E8 24.8 | 33.3 us,
+  // four bits 21.3 | 28.1, 8 bits 21.7 | 27.8, generic 31 | 47; of 2048 x 8192 (256
+  // workgroups of four) 24.7 | 21.6, 21.3 | 19.0, 21.7 | 19.2, 31 | 31; 160 tokens of
+  // four bits 4096 x 4096 24.9 | 28.0; 1024 x 1024 E8, 160 tokens 11.3 | 10.5, 320
+  // 12.4 | 16.4, 384 (two rounds either way) 18.2 | 16.5; float16 alike.
   if constexpr (XP == 1) {
-    if ((A.t + 79) / 80 < (A.t + 63) / 64) return pick_rows<FMT, T, XP, 5, GROUPED, UNI>(A, st);
+    const int64_t tgs = A.L.tiles;
+    if ((tgs * ((A.t + 79) / 80) + 255) / 256 < (tgs * ((A.t + 63) / 64) + 255) / 256)
+      return pick_rows<FMT, T, XP, 5, GROUPED, UNI>(A, st);
     if (A.t > 32) return pick_rows<FMT, T, XP, 4, GROUPED, UNI>(A, st);
   }
   return pick_rows<FMT, T, XP, 2, GROUPED, UNI>(A, st);

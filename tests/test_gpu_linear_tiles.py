@@ -80,3 +80,13 @@ def test_gradients_blocks_of_rows():
     lim = ((m / 16 + 32) * 2.0 ** -22 + 2.0 ** -20) * (np.abs(du) @ parts) + 2.0 ** -20 * (np.abs(dyr) @ parts + mag)
     err = np.abs(f64(r["dx"]) - want)
     assert (err <= lim + STEP["fp16"] * (np.abs(want) + lim) + 2.0 ** -25).all(), (err / lim).max()
+
+
+# 4100 rows are 257 tiles of sixteen: five tiles of tokens a workgroup take two rounds of the card where four take three
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("name,n,group", [("e865536", 264, 0), ("e8241", 40, 0), ("s16", 130, 0), ("s64", 257, 0),
+                                          ("levels", 200, 0), ("vec", 136, 0), ("s16", 500, 128), ("s64", 320, 64),
+                                          ("levels", 256, 128)])
+@pytest.mark.parametrize("t", [65, 80, 145])
+def test_five_tiles_of_tokens(dtype, name, n, group, t):
+    run_case(name, 4100, n, t, dtype, group=group, act="silu", bias=True, residual=True, seed=n + t)
