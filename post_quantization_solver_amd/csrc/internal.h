@@ -289,12 +289,6 @@ hipError_t launch_token_logprobs(const LogitArgs& A, const int32_t* tokens, floa
 hipError_t launch_distill(const LogitArgs& A, const float* teacher, double invT, bool tail, float* loss, void* grad,
                           int64_t ldg, void* ws, hipStream_t st);
 
-// What mpq_codebook_prepare notes in the low bits of mpq_codebook.magic (the struct
-// keeps the size that callers were built with): whether packed layers can hold the
-// entries (d = 1: their differences to level K / 2), exact in bfloat16 and in
-// float16, and whether (d = 1) the levels are evenly spaced, too.
-constexpr uint64_t CB_NARROW = 1, CB_EVEN = 2, CB_NOTES = CB_NARROW | CB_EVEN;
-
 // The device tables of a prepared codebook, checked (api.hip).
 int prepared_tables(const mpq_codebook* cb, CbTables& T);
 

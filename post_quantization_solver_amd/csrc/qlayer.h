@@ -485,6 +485,12 @@ size_t q_grad_workspace(const QLinearGrad& A);
 hipError_t launch_q_grad(const QLinearGrad& A, void* ws, hipStream_t st);
 hipError_t launch_q_zero_rows(void* p, int64_t rows, int64_t cols, int64_t ld, int dtype, hipStream_t st);
 
+// What mpq_codebook_prepare notes in the low bits of mpq_codebook.magic (the struct
+// keeps the size that callers were built with): whether packed layers can hold the
+// entries (d = 1: their differences to level K / 2), exact in bfloat16 and in
+// float16, and whether (d = 1) the levels are evenly spaced, too.
+constexpr uint64_t CB_NARROW = 1, CB_EVEN = 2, CB_NOTES = CB_NARROW | CB_EVEN;
+
 // Host images of an E8 prefix's decoder table and code map (K each at most);
 // false if the codebook does not have the shells' structure.
 bool q_e8_tables(const float* cb, int64_t K, uint32_t* lut, uint16_t* map, int* entries, int* pairs);
