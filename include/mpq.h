@@ -509,12 +509,13 @@ int mpq_pack(const int32_t* codes, int64_t m, int64_t n, const mpq_codebook* cb,
  * constant (at most 160) added that comes off every 128 columns: errors of some
  * 2^-17, at most 2^-13, of the scale times (E8: half) the sum of |x|, and |x| below
  * 2^112.
- * Where column groups make the weights themselves enter (more than 192 tokens on
- * large layers, or groups that are no multiple of the packed chunk: 128 columns
- * at 4 bits, 64 at 8), they and x are float16 terms under a power of two per
- * row: one (11 bits) for bfloat16 x, else two for the weights.  A token whose x
- * holds NaN or infinities has NaN or infinite outputs; no other token does.
- * 0 <= t < 2^22.  Nothing is kept between calls; calls may overlap on separate
+ * Where column groups make the weights themselves enter (more than 192 tokens,
+ * float16 384, unless t <= 1024 and t m n <= 3 2^27; or groups that are no multiple
+ * of the packed chunk: 128 columns at 4 bits, 64 at 8), they and x are float16
+ * terms under a power of two per row: one (11 bits) for bfloat16 x, else two for
+ * the weights.  (Elements below 2^-28 of their row's largest lose bits of their
+ * terms, those below 2^-39 are gone.)  A token whose x holds NaN or infinities
+ * has NaN or infinite outputs; no other token does.  0 <= t < 2^22.  Nothing is kept between calls; calls may overlap on separate
  * workspaces. */
 size_t mpq_linear_workspace_bytes(int dtype, int64_t t, int64_t m, int64_t n, int64_t K, int64_t d, int64_t group);
 int mpq_linear(const void* x, int dtype, int64_t t, int64_t ldx, const void* packed, int64_t m, int64_t n,

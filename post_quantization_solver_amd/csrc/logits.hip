@@ -9,14 +9,16 @@
 // are summed as a tree and the trees in float64: a KL divergence is a small
 // difference of these sums.
 //
-// Split.  A workgroup holds one segment of a row (at most LG_SEG_BYTES) in
-// registers, so HBM is read once: the maximum, the sums and the top list come
-// from the registers.  Segments of a row are joined by a second kernel.
+// Split.  A workgroup holds one segment of a row (at most LG_NV 16-byte vectors a
+// thread) in registers: the maximum and the sums come from them.  Segments of a row
+// are joined by a second kernel.
 //
 // Top list.  Each thread's maximum is sorted within its wave; wave w's r_w-th
 // largest (sum r_w >= k over the waves) bounds the k-th largest element from
 // below, so the elements at or above the smallest of those bounds hold the top
-// k and are few.  They go to LDS and are ranked by counting.  Should ties or
+// k and are few.  The vectors that hold them are read again (of 2048 x 128256
+// bfloat16, top 64, 109 MB beside the logits' 525, from beyond the L2), they go to
+// LDS and are ranked by counting.  Should ties or
 // masked rows make them many, a bisection over the values, then over the
 // indices of equal values, finds the k exactly.
 #include <math.h>
@@ -346,7 +348,7 @@ __device__ void segment_top(const float (&vm)[LG_NV], int nv, float tmax, const 
     for (int w = 1; w < LG_WAVES; ++w) bound = fminf(bound, sh.f[w]);
   }
   // the few vectors that hold such an element first, then their elements, a
-  // thread each (re-read: they are in the cache)
+  // thread each (re-read: by now many have left the L2)
 #pragma unroll
   for (int j = 0; j < LG_NV; ++j) {
     if (j >= nv) break;
@@ -1038,8 +1040,8 @@ __global__ __launch_bounds__(THREADS) void distill_row_kernel(LogitArgs A, const
 // ------------------------------------------------------------------ launchers
 
 // Segments: at most the registers of a workgroup, and shorter where there are
-// few rows, so that at least 512 workgroups (two per CU) share the work, but
-// none under 4096 elements.
+// few rows, so that at least 512 workgroups (two per CU) share the work, but no
+// more of them than a row has 4096 elements or a part of them.
 void logit_split(LogitArgs& A) {
   const int64_t vec = 16 / es_of(A.dtype);
   const int64_t most = (int64_t)LG_NV * LG_THREADS * vec;

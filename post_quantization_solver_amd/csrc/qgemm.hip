@@ -11,12 +11,13 @@
 // 16 bits enter as planes whose sum they are: the products of plane pairs add up
 // in the same float32 accumulators.
 //
-// Bound.  The matrix cores are busy some 60 % of the time in the large tiles (2048
-// x 4096 x 14336, one call after the other on the same operands: 184 us, 1.3
-// PFLOP/s of the 2.07 that they reach alone), the rest is the step's barrier; the small tile waits for the L2's 64 bytes a clock and
-// CU.  Planes are in blocks of 16 rows by 32 columns: rows of a matrix a multiple
-// of 4 KB apart lie on the same few cache channels (the same product with planes
-// in rows 262 us).
+// Bound.  The matrix cores are busy 62 % of the time in the large tiles (2048 x
+// 4096 x 14336: 198 us of the 224 of a whole call in a graph, 1.2 PFLOP/s of the
+// 2.07 that they reach alone; 222 under a tracer), the rest is the step's barrier;
+// the small tile waits for the L2's 64 bytes a clock and CU.  Planes are in blocks
+// of 16 rows by 32 columns: rows of a matrix a multiple of 4 KB apart lie on the
+// same few cache channels (before the loads stood between the products, the call
+// took 293 us with planes in rows and 262 in blocks).
 #include <algorithm>
 #include "qlayer.h"
 

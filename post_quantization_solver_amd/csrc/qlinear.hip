@@ -657,11 +657,16 @@ hipError_t unpack_t(const QLayer& L, int64_t mp, int planes, const uint32_t* ref
 // tokens decode the layer once more, and laying the planes out once is cheaper.
 // Measured, few-row product | planes and tiles, 4096 x 14336: E8 bfloat16 58 | 61
 // us at 128 tokens, 84 | 77 at 192, float32 85 | 87 at 96, 109 | 90 at 128; four
-// bits bfloat16 71 | 83 at 192, 93 | 85 at 256; groups of 128, whose planes hold
+// bits bfloat16 71 | 83 at 192, 93 | 85 at 256; 8 bits 81 | 97 at 192, 104 | 100 at
+// 256, float32 79 | 105 at 96, 103 | 108 at 128; groups of 128, whose planes hold
 // weights (two terms but for bfloat16): float16 156 | 213 at 384 (14336 x 4096
 // 235 | 211 at 512), float32 188 | 251 at 192.  The planes take 18 us and more
 // however small the layer: 1024 x 1024 at 384 tokens 17 | 20 (E8), 12 | 21 (four
-// bits), 24 | 28 (float32), at 768 25 | 23, 17 | 24, 44 | 32.
+// bits), 24 | 28 (float32), at 768 25 | 23, 17 | 24, 44 | 32; 8 bits at 768 20 | 26.
+// A generic codebook's entries come from memory, and from 81 tokens on (float32:
+// 65) a large layer of it would be better off with planes: 87 | 70 at 96, 93 | 71 at
+// 128 (4096 x 4096 31 | 34, 33 | 34).  It takes E8's counts all the same: a
+// workspace's size knows the codes, not the codebook, and planes take 128 MB.
 constexpr int64_t Q_SMALL_TOKENS = 1024, Q_SMALL_WORK = 3ll << 27;
 
 bool use_skinny(const QLinearArgs& A) {
@@ -676,7 +681,9 @@ bool use_skinny(const QLinearArgs& A) {
 // Measured, in place | laid out first (E8): 4096 columns, 2 tokens 8.7 | 11.5 us,
 // 16 tokens 10.7 | 11.8, 32 tokens 13.6 | 12.5; 8192 columns, 8 tokens 11.5 |
 // 12.9, 13 tokens 12.6 | 13.0, 16 tokens 13.8 | 12.9; 14336 columns, 8 tokens 16.0
-// | 16.3, 13 tokens 18.3 | 16.7.
+// | 16.3, 13 tokens 18.3 | 16.7.  8 bits: 4096 columns, 16 tokens 8.1 | 9.3, 32
+// tokens 11.6 | 10.5; 8192 columns, 13 tokens 10.7 | 11.6, 16 tokens 11.9 | 11.7; 14336
+// columns, 8 tokens 13.6 | 15.3, 13 tokens 15.7 | 15.4; four bits and generic alike.
 constexpr int64_t Q_DIRECT = 7 << 14;
 
 int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }
@@ -708,7 +715,8 @@ hipError_t forward(const QLinearArgs& A, char* base, size_t* bytes, hipStream_t 
   const bool raw = A.dtype == DT_F16 || (A.dtype == DT_BF16 && !weights);
   const bool aligned = reinterpret_cast<uintptr_t>(A.x) % 16 == 0 && A.ldx % 8 == 0 && A.ldx <= (1 << 20);
   // Few rows: see Q_DIRECT.  Many: the product's tiles read x in place as they do
-  // operand order (2048 tokens of 14336 columns 258 us, laid out first 292).
+  // operand order (2048 tokens, 4096 x 14336 E8 224 us, laid out first 235; 4096 x
+  // 4096 four bits 79, 83).
   const bool direct = raw && aligned && (skinny ? L.n % 8 == 0 && A.t * L.n <= Q_DIRECT : L.n % 64 == 0);
   const bool bf16 = raw && A.dtype == DT_BF16;
   const int WP = !weights ? 0 : A.dtype == DT_BF16 ? 1 : 2;   // terms of a weight (0: entries)

@@ -26,11 +26,14 @@
 // place its sixteen rows often start a multiple of 4 KB apart, on the same few
 // cache channels, 64 clocks a load instead of 16.
 //
-// Measured (microseconds at 1, 16, 32, 64, 128 tokens, bfloat16): E8 4096 x
-// 14336 12.1, 16.0, 21.0, 31.5, 56; 4096 x 4096 8.0, 10.1, 12.9, 15.5, 26; 32768 x
-// 4096 23, 28, 46, 67, 124; four bits 4096 x 14336 7.9, 12.4, 18.1, 28, 48; 32768
-// x 4096 15.6 (4.3 TB/s of codes), 23, 41, 61, 113.  An empty call (64 columns) is
-// 6.3 with E8's table and 3.9 without.
+// Measured (microseconds at 1, 16, 32, 64, 128 tokens, bfloat16, one layer again
+// and again, so that its codes come from the last-level cache): E8 4096 x 14336
+// 12.1, 16.0, 21.0, 31.5, 56; 4096 x 4096 8.0, 10.1, 12.9, 15.5, 26; 32768 x 4096
+// 23, 28, 46, 67, 124; four bits 4096 x 14336 7.9, 12.4, 18.1, 28, 48; 32768 x 4096
+// 15.6, 23, 41, 61, 113.  An empty call (64 columns) is 6.3 with E8's table and 3.9
+// without.  One token through layers in turn, whose codes come from HBM (more than
+// 256 MB of them), against one layer again: E8 4096 x 14336 13.4 | 12.6, 32768 x
+// 4096 24.2 | 24.1; four bits 12.2 | 8.5, 19.3 (3.5 TB/s of codes) | 17.3.
 #include <algorithm>
 #include <type_traits>
 #include "qlayer.h"
