@@ -335,14 +335,17 @@ def _words(s, t, count):
 
 
 def _stochastic(v, fraction, u):
-    """8-bit codes of values (float64) and their blocks' scales, rounded up with the probability u says."""
+    """8-bit codes of values (float64) and their blocks' scales, rounded up with the probability u says: of where the
+    value (of a root: its square) lies between two codes'."""
     levels = _levels(fraction)
     b = v.view(-1, BLOCK)
     scale = (b.abs().amax(1) / levels[-1]).float()
     d = scale.double()[:, None]
     x = torch.where(d > 0, b.abs() / torch.where(d > 0, d, 1.0), 0.0).clamp_max(levels[-1].item())
     low = (torch.bucketize(x, levels, right=True) - 1).clamp_max(len(levels) - 2)
-    code = low + (x - levels[low] >= (1.0 - u.view(-1, BLOCK)) * (levels[low + 1] - levels[low]))
+    power = 1 if fraction == 3 else 2
+    below, above = levels[low] ** power, levels[low + 1] ** power
+    code = low + (x ** power - below >= (1.0 - u.view(-1, BLOCK)) * (above - below))
     if fraction == 3:
         code = code + 128 * ((b < 0) & (code > 0))
     else:
@@ -504,14 +507,16 @@ def _exact_step(s):
             index = torch.arange(at, at + len(p), device="cuda")
             word = _mix((index % 2 ** 32) ^ _mix((index // 2 ** 32 + key) % 2 ** 32))
             def encode(v, bits, u):
-                """Values rounded down, or up with the probability of where they lie between two codes."""
+                """Values rounded down, or up with the probability of where they (roots: their squares) lie between."""
                 v = torch.nn.functional.pad(v, (0, size - len(p))).view(-1, BLOCK)
                 u = torch.nn.functional.pad(u, (0, size - len(p))).view(-1, BLOCK)
                 top = (2 ** (bits + 1) - 1) * 2.0 ** 14
                 scale = (v.abs().amax(1, keepdim=True) / top).float().double()
                 x = (v.abs() / torch.where(scale > 0, scale, 1.0)).clamp(0, top)
                 gap = torch.exp2(torch.floor(torch.log2(x.clamp_min(2.0 ** bits))) - bits)
-                x = torch.floor(x / gap + (u + 0.5) / 65536) * gap
+                low = torch.floor(x / gap) * gap
+                share = (x - low) / gap * (1.0 if bits == 3 else (x + low) / (2 * low + gap))
+                x = low + gap * torch.floor(share + (u + 0.5) / 65536)
                 if bits == 4:
                     x = torch.where(v > 0, x.clamp_min(1), x)
                 return (torch.sign(v) * x.clamp_max(top) * scale).view(-1)[:len(p)]
