@@ -591,6 +591,85 @@ int mpq_distill(const void* logits, int dtype, int64_t t, int64_t V, int64_t ld,
                 const float* teacher, int k, float temperature, int tail, const float* weights, float* loss,
                 void* grad, int64_t ldg, void* workspace, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------ the optimizer's step */
+
+/* One AdamW step over many tensors at once (scales, offsets and biases of a
+ * model's layers, an unquantized head).  With g = grad * grad_scale, times
+ * max_norm / norm where the norm of all gradients is beyond max_norm, and the
+ * step's number t from 1 on:
+ *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2,
+ *   p = p - lr weight_decay p - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps).
+ *
+ * Tensors: param (device, `count` elements of `dtype`, any alignment, contiguous),
+ * where its moments begin (`at`, a multiple of 256: tensors in ascending order,
+ * each with all the 256s that it begins to itself), its learning rate and decay.
+ * mpq_adamw_plan checks them (MPQ_ENULL, MPQ_ESHAPE: counts and places;
+ * MPQ_EPARAM: a type, a rate that is negative or not finite, parameters that
+ * overlap), writes the plan into `plan` (device, caller-owned, 256-byte aligned,
+ * at least mpq_adamw_plan_bytes(tensors, count) bytes; 0: counts and places
+ * out of range), waits for that, and fills *out.  A plan holds addresses:
+ * it is to be made again when a parameter moves.  One call at a time may use it.
+ * At most 2^16 tensors, 2^40 elements.
+ *
+ * Moments: state.elements of each (at least the end of the last tensor's last
+ * 256), zero at first.  state.bits 32: m and v, float32.  8: one byte each, and
+ * m_scale and v_scale, float32, one per 256 elements (else NULL): a code's low
+ * 7 bits (m; the eighth is its sign) or 8 bits (sqrt(v)) are 4 exponent bits and
+ * F = 3 or 4 fraction bits and stand for scale times 0 .. 2^F - 1, then
+ * (2^F + f) 2^(E - 1); the largest of 256 has the largest code.  Codes are rounded
+ * up or down at random with the probability of where the value (of a root: its
+ * square, so that m and v are what they would be on average) lies between them (a root
+ * that is not zero, never to zero), and so are 16-bit parameters: the random bits are a hash of (seed, t, place in the moments), and the same call
+ * gives the same bits.  State of 8 bits is computed in float64.  step: device
+ * int32, the number of steps taken, counted by the call (0 at first).
+ *
+ * grads: HOST array of `count` device pointers, gradients in their parameters'
+ * types.  grad_scale: finite.  max_norm: 0 for none; else > 0, +inf for the norm
+ * alone: a step whose norm is not finite is not taken (nothing changes but
+ * *norm), and `norm` (device float, may be NULL) receives the norm of the gradients
+ * times grad_scale, before clipping.  Without max_norm a gradient that is not finite
+ * makes its element's moments (8 bits: the 256's) NaN.  Every learning rate is
+ * multiplied by lr_scale (finite, >= 0) and, unless NULL, by lr_factor (a device
+ * float that the call reads once it runs).  A call reads
+ * and writes device memory alone once it is enqueued, so that it may be captured and
+ * replayed with gradients at the same addresses.
+ * Errors: MPQ_ENULL, MPQ_ESHAPE (state.elements), MPQ_EPARAM (betas outside [0, 1),
+ * eps <= 0, grad_scale, max_norm or lr_scale out of range, state.bits, a plan that mpq_adamw_plan did not fill). */
+typedef struct {
+  void* param;
+  int64_t count, at;
+  float lr, weight_decay;
+  int32_t dtype;            /* MPQ_BF16, MPQ_FP16 or MPQ_FP32 */
+  int32_t reserved;         /* 0 */
+} mpq_adamw_tensor;
+typedef struct {
+  int64_t count, units, elements;
+  void* table;              /* device, caller-owned */
+  uint64_t magic;           /* set by mpq_adamw_plan */
+} mpq_adamw_plan_t;
+typedef struct {
+  int32_t* step;
+  void *m, *v;
+  float *m_scale, *v_scale;
+  int64_t elements;
+  int32_t bits;             /* 8 or 32 */
+  uint32_t seed;
+} mpq_adamw_state;
+typedef struct {
+  double beta1, beta2, eps, grad_scale, max_norm, lr_scale;
+  const float* lr_factor;
+  float* norm;
+} mpq_adamw_options;
+size_t mpq_adamw_plan_bytes(const mpq_adamw_tensor* tensors, int64_t count);
+int mpq_adamw_plan(const mpq_adamw_tensor* tensors, int64_t count, void* plan, size_t plan_bytes, void* stream,
+                   mpq_adamw_plan_t* out);
+int mpq_adamw(const mpq_adamw_plan_t* plan, const void* const* grads, const mpq_adamw_options* options,
+              const mpq_adamw_state* state, void* stream);
+
+/* What the 8-bit moments of a state stand for: m and v (sqrt(v)'s square), float32,
+ * state.elements each (16-byte aligned).  MPQ_EPARAM with another state. */
+int mpq_adamw_moments(const mpq_adamw_state* state, float* m, float* v, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

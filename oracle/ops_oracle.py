@@ -168,3 +168,69 @@ def linear_backward(dy, x, codes, E, scale, offset, group=0, pre=None, name=None
         da[:, g] = (dW * e)[:, col == g].sum(1)
         do[:, g] = dW[:, col == g].sum(1)
     return dict(dx=du @ w, dscale=da.reshape(np.shape(scale)), doffset=do.reshape(np.shape(scale)), dbias=du.sum(0))
+
+
+# ------------------------------------------------------------------ the optimizer's step
+
+def mix(x):
+    """The step's hash of 32-bit words (uint64 arrays or ints)."""
+    x = np.asarray(x, np.uint64)
+    m = np.uint64(0xffffffff)
+    x = x ^ (x >> np.uint64(16))
+    x = (x * np.uint64(0x6A09E667)) & m
+    x = x ^ (x >> np.uint64(15))
+    x = (x * np.uint64(0xBB67AE85)) & m
+    return x ^ (x >> np.uint64(16))
+
+
+def adamw_words(seed, t, at, n):
+    """Random words of `n` elements from place `at` on, in step t."""
+    i = np.arange(n, dtype=np.uint64) + np.uint64(at)
+    m = np.uint64(0xffffffff)
+    key = mix(mix(np.uint64(seed)) ^ np.uint64(t))
+    return mix((i & m) ^ mix((key + (i >> np.uint64(32))) & m))
+
+
+def code_levels(F):
+    """What the codes 0 .. 2^(4 + F) - 1 stand for, in units of the scale, by the definition."""
+    c = np.arange(16 << F)
+    E, f = c >> F, c & ((1 << F) - 1)
+    return np.where(E == 0, f, ((1 << F) + f) * 2.0 ** (E - 1))
+
+
+def decode8(code, scale, F):
+    code = code.astype(np.int64)
+    v = code_levels(F)[code & 127 if F == 3 else code]
+    if F == 3:
+        v = np.where(code & 128, -v, v)
+    return v * np.repeat(scale.astype(np.float64), 256)
+
+
+def encode8(v, F, h):
+    """(codes, scales): v's elements (whole blocks), rounded up where h says (16 random bits); F = 4: roots, by
+    their squares."""
+    L = code_levels(F)
+    b = v.reshape(-1, 256)
+    scale = (np.abs(b).max(1) / L[-1]).astype(np.float32)
+    s = scale.astype(np.float64)[:, None]
+    x = np.minimum(np.abs(b) / np.where(s > 0, s, 1.0), L[-1])
+    lo = np.minimum(np.searchsorted(L, x, side="right") - 1, len(L) - 2)
+    k = 1 if F == 3 else 2
+    share = (x ** k - L[lo] ** k) / (L[lo + 1] ** k - L[lo] ** k)
+    code = lo + (share + (h.reshape(-1, 256).astype(np.float64) + 0.5) / 65536 >= 1.0)
+    if F == 3:
+        code = np.where((b < 0) & (code > 0), code | 128, code)
+    else:
+        code = np.where((b > 0) & (code == 0), 1, code)
+    return code.reshape(-1).astype(np.uint8), scale
+
+
+def adamw(p, g, m, v, t, lr, betas, eps, decay, factor):
+    """Step t of one tensor in float64: (p', m', v', size), size the magnitudes that p' is the sum of."""
+    g = g.astype(np.float64) * factor
+    m2 = betas[0] * m + (1 - betas[0]) * g
+    v2 = betas[1] * v + (1 - betas[1]) * g * g
+    den = np.sqrt(v2 / (1 - betas[1] ** t)) + eps
+    c1 = 1 / (1 - betas[0] ** t)
+    size = lr * c1 * (betas[0] * np.abs(m) + (1 - betas[0]) * np.abs(g)) / den
+    return p - lr * decay * p - lr * c1 * m2 / den, m2, v2, size

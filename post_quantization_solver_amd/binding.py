@@ -35,7 +35,8 @@ EXPORTS = ("mpq_workspace_bytes", "mpq_strerror", "mpq_codebook_bytes", "mpq_cod
            "mpq_e8dp_transitions", "mpq_probe_rate",
            "mpq_pack_bytes", "mpq_pack", "mpq_linear_workspace_bytes", "mpq_linear",
            "mpq_linear_backward_workspace_bytes", "mpq_linear_backward",
-           "mpq_token_logprobs_workspace_bytes", "mpq_token_logprobs", "mpq_distill_workspace_bytes", "mpq_distill")
+           "mpq_token_logprobs_workspace_bytes", "mpq_token_logprobs", "mpq_distill_workspace_bytes", "mpq_distill",
+           "mpq_adamw_plan_bytes", "mpq_adamw_plan", "mpq_adamw", "mpq_adamw_moments")
 
 
 class MPQError(RuntimeError):
@@ -86,6 +87,28 @@ class Options(ctypes.Structure):
                 ("prof_ms", ctypes.POINTER(ctypes.c_double)), ("prof_launches", ctypes.POINTER(ctypes.c_int64)),
                 ("map_codes", ctypes.c_void_p), ("objective", ctypes.c_void_p), ("fallbacks", ctypes.c_void_p),
                 ("sweeps", ctypes.c_void_p), ("digits", ctypes.c_int32)]
+
+
+class AdamWTensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("count", ctypes.c_int64), ("at", ctypes.c_int64), ("lr", ctypes.c_float),
+                ("weight_decay", ctypes.c_float), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class AdamWPlan(ctypes.Structure):
+    _fields_ = [("count", ctypes.c_int64), ("units", ctypes.c_int64), ("elements", ctypes.c_int64),
+                ("table", ctypes.c_void_p), ("magic", ctypes.c_uint64)]
+
+
+class AdamWState(ctypes.Structure):
+    _fields_ = [("step", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("elements", ctypes.c_int64),
+                ("bits", ctypes.c_int32), ("seed", ctypes.c_uint32)]
+
+
+class AdamWOptions(ctypes.Structure):
+    _fields_ = [("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
+                ("grad_scale", ctypes.c_double), ("max_norm", ctypes.c_double), ("lr_scale", ctypes.c_double),
+                ("lr_factor", ctypes.c_void_p), ("norm", ctypes.c_void_p)]
 
 
 class PreparedCodebook:
@@ -231,6 +254,11 @@ def load_library(path: str = LIB_PATH):
     lib.mpq_distill_workspace_bytes.argtypes = [I, I64, I64, I]
     lib.mpq_distill_workspace_bytes.restype = SZ
     lib.mpq_distill.argtypes = [P, I, I64, I64, I64, P, P, I, F, I, P, P, P, I64, P, SZ, P]
+    lib.mpq_adamw_plan_bytes.argtypes = [ctypes.POINTER(AdamWTensor), I64]
+    lib.mpq_adamw_plan_bytes.restype = SZ
+    lib.mpq_adamw_plan.argtypes = [ctypes.POINTER(AdamWTensor), I64, P, SZ, P, ctypes.POINTER(AdamWPlan)]
+    lib.mpq_adamw.argtypes = [ctypes.POINTER(AdamWPlan), P, ctypes.POINTER(AdamWOptions), ctypes.POINTER(AdamWState), P]
+    lib.mpq_adamw_moments.argtypes = [ctypes.POINTER(AdamWState), P, P, P]
     for name in EXPORTS[2:]:
         if name.endswith("_bytes") or name in ("mpq_hip_error_name", "mpq_e8dp_transitions", "mpq_profiler_destroy"):
             continue
@@ -1014,3 +1042,164 @@ def distill(logits, teacher_ids, teacher, temperature=1.0, tail=False, weights=N
                              _raw_stream(dev))
     _check(rc, "mpq_distill")
     return dict(loss=loss, grad=grad)
+
+
+class AdamW:
+    """AdamW over many tensors at once (mpq_adamw), one step a call and a launch or two whatever their number.
+
+    `params`: float32, bfloat16 or float16 tensors of one device, contiguous,
+    written in place (past autograd's notice, as under torch.no_grad()): a packed
+    layer's scale and offset, biases, an unquantized head.  `lr` and `weight_decay`: a
+    number, or one per tensor.  `state_bits`: 32, or 8 for moments of a byte each
+    and a scale per 256 elements.  8-bit moments and 16-bit parameters are rounded
+    stochastically, by random bits made of `seed`, the step and the element's place.
+
+    The moments lie one tensor after another, each from a multiple of 256 on:
+    `m`, `v` (32 bits), or the codes `m`, `r` (of sqrt(v)) with `m_scale`, `r_scale`;
+    `steps` counts the steps taken, on the device.
+    """
+
+    def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0, state_bits=32, seed=0):
+        import torch
+        self.params = list(params)
+        if not self.params:
+            raise ValueError("no parameters")
+        if state_bits not in (8, 32):
+            raise ValueError(f"state_bits must be 8 or 32, got {state_bits}")
+        for k, p in enumerate(self.params):
+            _dtype_code(p, f"params[{k}]")
+            _on(p, f"params[{k}]", self.params[0].device)
+            if not p.is_contiguous():
+                raise ValueError(f"params[{k}] must be contiguous")
+        self.device = dev = self.params[0].device
+        count = len(self.params)
+        self._rates = []
+        for values, name in ((lr, "lr"), (weight_decay, "weight_decay")):
+            values = [float(v) for v in values] if hasattr(values, "__len__") else [float(values)] * count
+            if len(values) != count:
+                raise ValueError(f"{len(values)} values of {name} for {count} parameters")
+            self._rates.append(values)
+        self.betas, self.eps, self.state_bits, self.seed = tuple(map(float, betas)), float(eps), state_bits, int(seed)
+        if not (all(0.0 <= b < 1.0 for b in self.betas) and len(self.betas) == 2) or not self.eps > 0.0:
+            raise ValueError(f"betas must lie in [0, 1) and eps be positive, got {betas} and {eps}")
+        self._counts = [p.numel() for p in self.params]
+        self._dtypes = [p.dtype for p in self.params]
+        self.offsets, total = [], 0
+        for n in self._counts:
+            self.offsets.append(total)
+            total += -(-n // 256) * 256
+        self.elements = total
+        with _guard(dev):
+            self.steps = torch.zeros(1, dtype=torch.int32, device=dev)
+            kind = torch.uint8 if state_bits == 8 else torch.float32
+            # (an empty state keeps an address)
+            m, v = (torch.zeros(max(total, 256), dtype=kind, device=dev)[:total] for _ in range(2))
+            scales = [torch.zeros(max(total // 256, 1), device=dev)[:total // 256] for _ in range(2)] if state_bits == 8 else ()
+            self._plan(torch)
+        self.m = m
+        if state_bits == 8:
+            self.r, (self.m_scale, self.r_scale) = v, scales
+        else:
+            self.v = v
+        self._state = AdamWState(_at(self.steps), _at(m), _at(v), *(map(_at, scales) if scales else (None, None)), total,
+                                 state_bits, self.seed & 0xffffffff)
+
+    def _plan(self, torch):
+        """The parameters' places for the kernels (again where one has moved)."""
+        lib, count = load_library(), len(self.params)
+        self._where = [p.data_ptr() for p in self.params]
+        tensors = (AdamWTensor * count)(*(
+            AdamWTensor(p, n, at, lr, wd, _dtype_code(t, "params"), 0) for p, n, at, lr, wd, t in
+            zip(self._where, self._counts, self.offsets, *self._rates, self.params)))
+        nb = int(lib.mpq_adamw_plan_bytes(tensors, count))
+        if nb == 0:
+            raise MPQError(-2, "mpq_adamw_plan_bytes")
+        self._table = torch.empty(nb, dtype=torch.uint8, device=self.device)
+        self._struct = AdamWPlan()
+        _check(lib.mpq_adamw_plan(tensors, count, _at(self._table), nb, _raw_stream(self.device),
+                                  ctypes.byref(self._struct)), "mpq_adamw_plan")
+
+    def _same(self, tensors, name):
+        """Raises unless the tensors are laid out as the parameters were; their addresses."""
+        import torch
+        T = torch.Tensor
+        # (whole lists at a time: hundreds of small tensors are stepped in some ten microseconds)
+        try:
+            if (list(map(T.numel, tensors)) == self._counts and [t.dtype for t in tensors] == self._dtypes
+                    and all(map(T.is_contiguous, tensors)) and set(map(T.get_device, tensors)) <= {self.device.index}):
+                return list(map(T.data_ptr, tensors))
+        except TypeError:
+            pass
+        if len(tensors) != len(self.params):
+            raise ValueError(f"{len(tensors)} {name} for {len(self.params)} parameters")
+        for k, (t, p) in enumerate(zip(tensors, self.params)):
+            _dtype_code(t, f"{name}[{k}]")
+            _on(t, f"{name}[{k}]", self.device)
+            if t.dtype != self._dtypes[k] or t.numel() != self._counts[k] or not t.is_contiguous():
+                raise ValueError(f"{name}[{k}] must be contiguous, {self._counts[k]} elements of {self._dtypes[k]}")
+        raise ValueError(f"{name} do not match the parameters")
+
+    def step(self, grads, grad_scale=1.0, max_norm=None, lr_factor=None):
+        """One step with the parameters' gradients (in their types and order).
+
+        `grad_scale` multiplies the gradients (the inverse of a loss scale);
+        `max_norm` clips their common norm, which is then returned (a float32 scalar
+        on the device, before clipping); a step whose norm is not finite is not
+        taken, float("inf") asks for the norm and that alone.  `lr_factor`: a number
+        or a float32 scalar on the device (read by the step, so that a captured one
+        follows a schedule) that multiplies the learning rates.
+        """
+        import torch
+        where = self._same(grads, "grads")
+        dev = self.device
+        if max_norm is not None and not max_norm > 0.0:
+            raise ValueError(f"max_norm must be positive, got {max_norm}")
+        with _guard(dev):
+            if list(map(torch.Tensor.data_ptr, self.params)) != self._where:
+                self._same(self.params, "params")
+                self._plan(torch)
+            lr_scale = 1.0
+            if lr_factor is not None and not isinstance(lr_factor, torch.Tensor):
+                lr_scale, lr_factor = float(lr_factor), None
+            if lr_factor is not None:
+                _dev(lr_factor, torch.float32, "lr_factor")
+                _on(lr_factor, "lr_factor", dev)
+                if lr_factor.numel() != 1:
+                    raise ValueError(f"lr_factor has {lr_factor.numel()} elements, expected 1")
+            norm = torch.empty((), dtype=torch.float32, device=dev) if max_norm is not None else None
+            options = AdamWOptions(*self.betas, self.eps, grad_scale, max_norm or 0.0, lr_scale, _at(lr_factor),
+                                   _at(norm))
+            _check(load_library().mpq_adamw(ctypes.byref(self._struct), (ctypes.c_void_p * len(where))(*where),
+                                            ctypes.byref(options), ctypes.byref(self._state), _raw_stream(dev)), "mpq_adamw")
+        return norm
+
+    def moments(self):
+        """(m, v), float32: the moments, or what their 8-bit codes stand for."""
+        import torch
+        if self.state_bits == 32:
+            return self.m, self.v
+        with _guard(self.device):
+            m, v = (torch.empty(self.elements, dtype=torch.float32, device=self.device) for _ in range(2))
+            _check(load_library().mpq_adamw_moments(ctypes.byref(self._state), _at(m), _at(v), _raw_stream(self.device)),
+                   "mpq_adamw_moments")
+        return m, v
+
+    def _saved(self):
+        names = ("m", "r", "m_scale", "r_scale") if self.state_bits == 8 else ("m", "v")
+        return {"step": self.steps, **{k: getattr(self, k) for k in names}}
+
+    def state_dict(self):
+        """The step count and the moments (the live tensors)."""
+        return self._saved()
+
+    def load_state_dict(self, state):
+        """Copies a state_dict of an AdamW of the same sizes and state_bits."""
+        own = self._saved()
+        if set(state) != set(own):
+            raise ValueError(f"the state has {sorted(state)}, expected {sorted(own)}")
+        for k, t in own.items():
+            if state[k].shape != t.shape or state[k].dtype != t.dtype:
+                raise ValueError(f"{k} has shape {tuple(state[k].shape)} and type {state[k].dtype}, expected "
+                                 f"{tuple(t.shape)} and {t.dtype}")
+        for k, t in own.items():
+            t.copy_(state[k])
