@@ -10,6 +10,7 @@ load, every call raises -- there is no CPU fallback.
 """
 from __future__ import annotations
 
+import array
 import contextlib
 import ctypes
 import functools
@@ -1107,7 +1108,7 @@ class AdamW:
     def _plan(self, torch):
         """The parameters' places for the kernels (again where one has moved)."""
         lib, count = load_library(), len(self.params)
-        self._where = [p.data_ptr() for p in self.params]
+        self._where = array.array("Q", (p.data_ptr() for p in self.params))
         tensors = (AdamWTensor * count)(*(
             AdamWTensor(p, n, at, lr, wd, _dtype_code(t, "params"), 0) for p, n, at, lr, wd, t in
             zip(self._where, self._counts, self.offsets, *self._rates, self.params)))
@@ -1127,7 +1128,7 @@ class AdamW:
         try:
             if (list(map(T.numel, tensors)) == self._counts and [t.dtype for t in tensors] == self._dtypes
                     and all(map(T.is_contiguous, tensors)) and set(map(T.get_device, tensors)) <= {self.device.index}):
-                return list(map(T.data_ptr, tensors))
+                return array.array("Q", map(T.data_ptr, tensors))
         except TypeError:
             pass
         if len(tensors) != len(self.params):
@@ -1155,7 +1156,7 @@ class AdamW:
         if max_norm is not None and not max_norm > 0.0:
             raise ValueError(f"max_norm must be positive, got {max_norm}")
         with _guard(dev):
-            if list(map(torch.Tensor.data_ptr, self.params)) != self._where:
+            if array.array("Q", map(torch.Tensor.data_ptr, self.params)) != self._where:
                 self._same(self.params, "params")
                 self._plan(torch)
             lr_scale = 1.0
@@ -1169,8 +1170,8 @@ class AdamW:
             norm = torch.empty((), dtype=torch.float32, device=dev) if max_norm is not None else None
             options = AdamWOptions(*self.betas, self.eps, grad_scale, max_norm or 0.0, lr_scale, _at(lr_factor),
                                    _at(norm))
-            _check(load_library().mpq_adamw(ctypes.byref(self._struct), (ctypes.c_void_p * len(where))(*where),
-                                            ctypes.byref(options), ctypes.byref(self._state), _raw_stream(dev)), "mpq_adamw")
+            _check(load_library().mpq_adamw(ctypes.byref(self._struct), where.buffer_info()[0], ctypes.byref(options),
+                                            ctypes.byref(self._state), _raw_stream(dev)), "mpq_adamw")
         return norm
 
     def moments(self):

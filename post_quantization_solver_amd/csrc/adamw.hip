@@ -166,12 +166,12 @@ struct StepArgs {
 __device__ __forceinline__ bool whole(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 // Whether this is the last workgroup of the launch to come here (asked once, by
-// one thread, after the workgroup's work); the counter is ready for the next.
+// one thread); the counter is ready for the next.  No fence: what the others leave
+// for the last goes through atomics that have been performed by then.  (A fence of
+// device scope writes a whole L2 back, in every workgroup.)
 __device__ __forceinline__ bool came_last(uint32_t* counter) {
-  __threadfence();
-  const bool last = atomicAdd(counter, 1u) == gridDim.x - 1;
+  const bool last = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
   if (last) *counter = 0;
-  __threadfence();
   return last;
 }
 
@@ -202,8 +202,11 @@ __global__ __launch_bounds__(THREADS) void adamw_norm_kernel(AdamwTable T, int64
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
   __syncthreads();
   if (threadIdx.x == 0) {
-    __hip_atomic_store(T.partial + (int64_t)launch * ADAMW_NORM_GROUPS + blockIdx.x, (part[0] + part[1]) + (part[2] + part[3]),
-                       __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    // (an exchange: its answer says that it has been performed)
+    const uint64_t was = __hip_atomic_exchange(
+        reinterpret_cast<uint64_t*>(T.partial) + (int64_t)launch * ADAMW_NORM_GROUPS + blockIdx.x,
+        __builtin_bit_cast(uint64_t, (part[0] + part[1]) + (part[2] + part[3])), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    asm volatile("" ::"v"((uint32_t)was), "v"((uint32_t)(was >> 32)) : "memory");
     mine = came_last(T.control + CTL_NORM_COUNT) && last;
   }
   __syncthreads();
