@@ -591,6 +591,49 @@ int mpq_distill(const void* logits, int dtype, int64_t t, int64_t V, int64_t ld,
                 const float* teacher, int k, float temperature, int tail, const float* weights, float* loss,
                 void* grad, int64_t ldg, void* workspace, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------ a head's cross entropy */
+
+/* Softmax cross entropy of an output head, in pieces of its vocabulary (m rows)
+ * and without keeping the logits: per token with target r = targets[t]
+ *   z_v = sum_j x_j W[v][j] + bias_v,   loss = weight (log sum_v exp z_v - z_r),
+ * the head as in mpq_linear, and, where asked for, the gradients of the sum of the
+ * losses, the codes fixed:
+ *   dz_v = weight (exp(z_v - lse) - [v = r]),   dx = dz W (t x n of `dtype`; NULL: not
+ *   wanted),   dscale, doffset, dbias as in mpq_linear_backward (together, or all NULL).
+ * x: t x n of `dtype`, rows contiguous, strides ldx and lddx.  targets: t int32; a
+ * negative one marks a position without (padding).  weights: t float32, NULL: 1.
+ * Rows of weight 0 or without a target are not read: loss 0, gradient 0.  A target
+ * >= m: the row's loss and gradient NaN (and so the head's gradients).  loss: t
+ * float32; small losses keep their relative accuracy.  A bias of -inf takes its token
+ * out of the vocabulary: a target among those has loss +inf, and where no other token
+ * is left either, gradient 0.
+ * Sums are float32, joined in float64 beyond a workgroup.  Entries enter as they are;
+ * x as float16 terms under a power of two per token: one, exact, for 16-bit types
+ * (elements below 2^-28 of their row's largest lose bits, those below 2^-39 are gone),
+ * two (22 bits) for float32; the weights of column groups as two terms.  For dx, dz
+ * enters as one term (11 bits; float32: two) under a power of two per token; for
+ * the gradients of column groups as two.
+ * 1 <= m, 0 <= t < 2^22, ceil(t / 64) ceil(n / 64) < 2^24.  The workspace holds some
+ * 128 MB of operands and of logits each, or 1024 rows of the head's; t = 0: gradients
+ * of zero. */
+size_t mpq_linear_cross_entropy_workspace_bytes(int dtype, int64_t t, int64_t m, int64_t n, int64_t K, int64_t d,
+                                                int64_t group);
+int mpq_linear_cross_entropy(const void* x, int dtype, int64_t t, int64_t ldx, const void* packed, int64_t m, int64_t n,
+                             const mpq_codebook* cb, const float* scale, const float* offset, int64_t group,
+                             const float* bias, const int32_t* targets, const float* weights, float* loss, void* dx,
+                             int64_t lddx, float* dscale, float* doffset, float* dbias, void* workspace, size_t ws_bytes,
+                             void* stream);
+
+/* The same of a head that is not quantized: W, m x n of x's `dtype`, row stride
+ * ldw; its gradient dW (m x n of `dtype`, row stride lddw, rounded once) and dbias
+ * together, or both NULL.  W's rows enter as x does; for dW, dz enters as one term
+ * (float32: two). */
+size_t mpq_matrix_cross_entropy_workspace_bytes(int dtype, int64_t t, int64_t m, int64_t n);
+int mpq_matrix_cross_entropy(const void* x, int dtype, int64_t t, int64_t ldx, const void* W, int64_t ldw, int64_t m,
+                             int64_t n, const float* bias, const int32_t* targets, const float* weights, float* loss,
+                             void* dx, int64_t lddx, void* dW, int64_t lddw, float* dbias, void* workspace,
+                             size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------------------------ the optimizer's step */
 
 /* One AdamW step over many tensors at once (scales, offsets and biases of a

@@ -37,6 +37,8 @@ EXPORTS = ("mpq_workspace_bytes", "mpq_strerror", "mpq_codebook_bytes", "mpq_cod
            "mpq_pack_bytes", "mpq_pack", "mpq_linear_workspace_bytes", "mpq_linear",
            "mpq_linear_backward_workspace_bytes", "mpq_linear_backward",
            "mpq_token_logprobs_workspace_bytes", "mpq_token_logprobs", "mpq_distill_workspace_bytes", "mpq_distill",
+           "mpq_linear_cross_entropy_workspace_bytes", "mpq_linear_cross_entropy",
+           "mpq_matrix_cross_entropy_workspace_bytes", "mpq_matrix_cross_entropy",
            "mpq_adamw_plan_bytes", "mpq_adamw_plan", "mpq_adamw", "mpq_adamw_moments")
 
 
@@ -255,6 +257,12 @@ def load_library(path: str = LIB_PATH):
     lib.mpq_distill_workspace_bytes.argtypes = [I, I64, I64, I]
     lib.mpq_distill_workspace_bytes.restype = SZ
     lib.mpq_distill.argtypes = [P, I, I64, I64, I64, P, P, I, F, I, P, P, P, I64, P, SZ, P]
+    lib.mpq_linear_cross_entropy_workspace_bytes.argtypes = [I, I64, I64, I64, I64, I64, I64]
+    lib.mpq_linear_cross_entropy_workspace_bytes.restype = SZ
+    lib.mpq_linear_cross_entropy.argtypes = [P, I, I64, I64, P, I64, I64, CB, P, P, I64, P, P, P, P, P, I64, P, P, P, P, SZ, P]
+    lib.mpq_matrix_cross_entropy_workspace_bytes.argtypes = [I, I64, I64, I64]
+    lib.mpq_matrix_cross_entropy_workspace_bytes.restype = SZ
+    lib.mpq_matrix_cross_entropy.argtypes = [P, I, I64, I64, P, I64, I64, I64, P, P, P, P, P, I64, P, I64, P, P, SZ, P]
     lib.mpq_adamw_plan_bytes.argtypes = [ctypes.POINTER(AdamWTensor), I64]
     lib.mpq_adamw_plan_bytes.restype = SZ
     lib.mpq_adamw_plan.argtypes = [ctypes.POINTER(AdamWTensor), I64, P, SZ, P, ctypes.POINTER(AdamWPlan)]
@@ -1043,6 +1051,66 @@ def distill(logits, teacher_ids, teacher, temperature=1.0, tail=False, weights=N
                              _raw_stream(dev))
     _check(rc, "mpq_distill")
     return dict(loss=loss, grad=grad)
+
+
+def linear_cross_entropy(x, head, targets, bias=None, weights=None, need_dx=True, need_dhead=True, workspace=None):
+    """Softmax cross entropy of an output head without keeping its logits, and its
+    gradients (mpq_linear_cross_entropy, mpq_matrix_cross_entropy).
+
+    `x`: t x n hidden states, bfloat16, float16 or float32, contiguous rows;
+    `head`: a PackedLayer, or a matrix (vocabulary x n) of x's type with contiguous rows;
+    `targets`: t int32 (negative: no target, loss and gradient 0); `bias`: one float32 per
+    row of the head; `weights` (t float32): per-token factors of loss and
+    gradient, 0 skips a row.  Returns dict(loss, dx) with loss t float32 and dx of x's
+    type, and of the head, float32 unless it is a matrix of 16 bits: dscale, doffset
+    and dbias (in the shapes of the layer's affine and (m,)), or dweight and
+    dbias.  What is not wanted is None.  The gradients are those of the losses' sum; no
+    autograd graph is recorded (x.backward(dx) takes it on).
+    """
+    import torch
+    code = _dtype_code(x, "x")
+    ldx = _rows(x, "x")
+    t, n = x.shape
+    dev = x.device
+    packed = isinstance(head, PackedLayer)
+    if packed:
+        m, hn, cb = head.m, head.n, head.codebook
+        _on(head.packed, "the layer", dev)
+        head.check_affine(dev)
+    else:
+        ldw = _rows(head, "head", x)
+        m, hn = head.shape
+    if n != hn:
+        raise ValueError(f"x has {n} columns, the head {hn}")
+    if m < 1:
+        raise ValueError("the head has no rows")
+    _dev(targets, torch.int32, "targets", (t,))
+    _on(targets, "targets", dev)
+    for v, name, size in ((bias, "bias", m), (weights, "weights", t)):
+        if v is not None:
+            _dev(v, torch.float32, name, (size,))
+            _on(v, name, dev)
+    lib = load_library()
+    with _guard(dev):
+        loss = torch.empty(t, dtype=torch.float32, device=dev)
+        dx = torch.empty((t, n), dtype=x.dtype, device=dev) if need_dx else None
+        dbias = torch.empty(m, dtype=torch.float32, device=dev) if need_dhead else None
+        stream = _raw_stream(dev)
+        if packed:
+            dscale = torch.empty_like(head.scale) if need_dhead else None
+            doffset = torch.empty_like(head.scale) if need_dhead else None
+            ws = _scratch(workspace, dev, "mpq_linear_cross_entropy_workspace_bytes", code, t, m, n, cb.K, cb.d, head.group)
+            rc = lib.mpq_linear_cross_entropy(_at(x), code, t, ldx, _at(head.packed), m, n, cb.ref(), _at(head.scale),
+                                              _at(head.offset), head.group, _at(bias), _at(targets), _at(weights), _at(loss),
+                                              _at(dx), n, _at(dscale), _at(doffset), _at(dbias), _at(ws), ws.numel(), stream)
+            _check(rc, "mpq_linear_cross_entropy")
+            return dict(loss=loss, dx=dx, dscale=dscale, doffset=doffset, dbias=dbias)
+        dweight = torch.empty((m, n), dtype=x.dtype, device=dev) if need_dhead else None
+        ws = _scratch(workspace, dev, "mpq_matrix_cross_entropy_workspace_bytes", code, t, m, n)
+        rc = lib.mpq_matrix_cross_entropy(_at(x), code, t, ldx, _at(head), ldw, m, n, _at(bias), _at(targets), _at(weights),
+                                          _at(loss), _at(dx), n, _at(dweight), n, _at(dbias), _at(ws), ws.numel(), stream)
+    _check(rc, "mpq_matrix_cross_entropy")
+    return dict(loss=loss, dx=dx, dweight=dweight, dbias=dbias)
 
 
 class AdamW:

@@ -104,6 +104,16 @@ size_t grad_workspace(QLinearGrad A) {
 
 }  // namespace
 
+namespace mpq {
+int q_layer_shape(QLayer& L, int64_t m, int64_t n, int64_t K, int64_t d, int64_t group, int kind) {
+  return layer_shape(L, m, n, K, d, group, kind);
+}
+int q_layer_of(QLayer& L, const void* packed, int64_t m, int64_t n, const mpq_codebook* cb, const float* scale,
+               const float* offset, int64_t group) {
+  return layer_of(L, packed, m, n, cb, scale, offset, group);
+}
+}  // namespace mpq
+
 extern "C" {
 
 size_t mpq_pack_bytes(int64_t m, int64_t n, int64_t K, int64_t d) {

@@ -9,6 +9,7 @@
 
 #include "../../include/mpq.h"
 #include "adamw.h"
+#include "head.h"
 
 using namespace mpq;
 
@@ -119,9 +120,125 @@ int state_ok(const mpq_adamw_state& s, int64_t elements) {
   return MPQ_OK;
 }
 
+constexpr int64_t HEAD_MAX_T = (int64_t)1 << 22, HEAD_MAX_M = (int64_t)1 << 24, HEAD_MAX_N = 65536;
+
+// A matrix's shapes.
+int matrix_shape(QLayer& L, int64_t m, int64_t n) {
+  if (m < 0 || m > HEAD_MAX_M || n < 1 || n > HEAD_MAX_N) return MPQ_ESHAPE;
+  L = QLayer{};
+  L.fmt = QF_VEC;
+  L.m = m;
+  L.n = n;
+  L.tiles = (int)((m + 15) / 16);
+  L.group = n;
+  L.G = 1;
+  return MPQ_OK;
+}
+
+// Grids of 256 threads a workgroup (fewer than 2^32 in all): the transpose of x in
+// tiles of 64 x 64, 16 entries of a piece's affine a workgroup.
+bool head_fits(const HeadArgs& A) {
+  return A.t >= 0 && A.t < HEAD_MAX_T && A.L.m >= 1 && (A.t + 63) / 64 * ((A.L.n + 63) / 64) < (int64_t)1 << 24;
+}
+
+// Enough for every combination of outputs.
+size_t head_bytes(HeadArgs A) {
+  A.need_dx = A.need_dhead = true;
+  const size_t b = head_workspace(A);
+  return b > ALIGN ? b : ALIGN;
+}
+
+// The arguments that both kinds of head have.
+int head_call(HeadArgs& A, int dtype, const void* x, int64_t t, int64_t ldx, const float* bias, const int32_t* targets,
+              const float* weights, float* loss, void* dx, int64_t lddx, void* workspace, size_t ws_bytes, hipStream_t st,
+              float* dscale, float* doffset, float* dbias, void* dW, int64_t lddw) {
+  if (!plain_dtype(dtype)) return MPQ_EPARAM;
+  A.t = t;
+  if (!head_fits(A) || ldx < A.L.n || (dx && lddx < A.L.n) || (dW && lddw < A.L.n)) return MPQ_ESHAPE;
+  if (A.need_dhead && (!dbias || (A.dense ? !dW : !dscale || !doffset))) return MPQ_ENULL;
+  if (t == 0) {   // nothing to sum
+    hipError_t e = hipSuccess;
+    if (A.need_dhead) {
+      if (dscale) e = launch_fill_i32(reinterpret_cast<int32_t*>(dscale), A.L.m * A.L.G, 0, st);
+      if (e == hipSuccess && doffset) e = launch_fill_i32(reinterpret_cast<int32_t*>(doffset), A.L.m * A.L.G, 0, st);
+      if (e == hipSuccess) e = launch_fill_i32(reinterpret_cast<int32_t*>(dbias), A.L.m, 0, st);
+      if (e == hipSuccess && dW) e = launch_q_zero_rows(dW, A.L.m, A.L.n, lddw, dtype, st);
+    }
+    return status_of(e);
+  }
+  if (!x || !targets || !loss) return MPQ_ENULL;
+  A.dtype = dtype;
+  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % ALIGN != 0 || ws_bytes < head_bytes(A)) return MPQ_EWORKSPACE;
+  A.x = x;
+  A.ldx = ldx;
+  A.bias = bias;
+  A.targets = targets;
+  A.weights = weights;
+  A.loss = loss;
+  A.need_dx = dx != nullptr;
+  A.dx = dx;
+  A.lddx = lddx;
+  A.dscale = dscale;
+  A.doffset = doffset;
+  A.dbias = dbias;
+  A.dW = dW;
+  A.lddw = lddw;
+  return status_of(launch_head(A, workspace, st));
+}
+
 }  // namespace
 
 extern "C" {
+
+size_t mpq_linear_cross_entropy_workspace_bytes(int dtype, int64_t t, int64_t m, int64_t n, int64_t K, int64_t d,
+                                                int64_t group) {
+  HeadArgs A = {};
+  if (!plain_dtype(dtype) || q_layer_shape(A.L, m, n, K, d, group, MPQ_CB_GENERIC) != MPQ_OK) return 0;
+  A.dtype = dtype;
+  A.t = t;
+  return head_fits(A) ? head_bytes(A) : 0;
+}
+
+int mpq_linear_cross_entropy(const void* x, int dtype, int64_t t, int64_t ldx, const void* packed, int64_t m, int64_t n,
+                             const mpq_codebook* cb, const float* scale, const float* offset, int64_t group,
+                             const float* bias, const int32_t* targets, const float* weights, float* loss, void* dx,
+                             int64_t lddx, float* dscale, float* doffset, float* dbias, void* workspace, size_t ws_bytes,
+                             void* stream) {
+  HeadArgs A = {};
+  const int rc = q_layer_of(A.L, packed, m, n, cb, scale, offset, group);
+  if (rc) return rc;
+  if (t != 0 && (!packed || !scale)) return MPQ_ENULL;
+  if (reinterpret_cast<uintptr_t>(packed) % ALIGN != 0) return MPQ_EWORKSPACE;
+  A.need_dhead = dscale || doffset || dbias;
+  return head_call(A, dtype, x, t, ldx, bias, targets, weights, loss, dx, lddx, workspace, ws_bytes,
+                   static_cast<hipStream_t>(stream), dscale, doffset, dbias, nullptr, n);
+}
+
+size_t mpq_matrix_cross_entropy_workspace_bytes(int dtype, int64_t t, int64_t m, int64_t n) {
+  HeadArgs A = {};
+  if (!plain_dtype(dtype) || matrix_shape(A.L, m, n) != MPQ_OK) return 0;
+  A.dense = true;
+  A.dtype = dtype;
+  A.t = t;
+  return head_fits(A) ? head_bytes(A) : 0;
+}
+
+int mpq_matrix_cross_entropy(const void* x, int dtype, int64_t t, int64_t ldx, const void* W, int64_t ldw, int64_t m,
+                             int64_t n, const float* bias, const int32_t* targets, const float* weights, float* loss,
+                             void* dx, int64_t lddx, void* dW, int64_t lddw, float* dbias, void* workspace,
+                             size_t ws_bytes, void* stream) {
+  HeadArgs A = {};
+  const int rc = matrix_shape(A.L, m, n);
+  if (rc) return rc;
+  if (ldw < n) return MPQ_ESHAPE;
+  if (t != 0 && !W) return MPQ_ENULL;
+  A.dense = true;
+  A.W = W;
+  A.ldw = ldw;
+  A.need_dhead = dW || dbias;
+  return head_call(A, dtype, x, t, ldx, bias, targets, weights, loss, dx, lddx, workspace, ws_bytes,
+                   static_cast<hipStream_t>(stream), nullptr, nullptr, dbias, dW, lddw);
+}
 
 size_t mpq_adamw_plan_bytes(const mpq_adamw_tensor* tensors, int64_t count) {
   int64_t units, elements;

@@ -1,0 +1,830 @@
+// Softmax cross entropy of an output head in pieces of the vocabulary, and its
+// gradients; the logits are never kept.
+//
+// Mathematics.  z_tv = a_v s_tv + o_v X_t + b_v with s = x e^T over the head's
+// entries and X_t = sum_j x_tj (a matrix or column groups: s = x W^T alone); r the
+// target, w the token's weight:
+//   R_t = log sum_{v != r} exp z_tv,     loss = w log(1 + exp(R_t - z_tr)),
+//   dz_tv = w exp(z_tv - lse_t), v != r,  dz_tr = -w / (1 + exp(z_tr - R_t)),
+//   dx = dz W,  db_v = sum_t dz_tv,  da_v = sum_t dz_tv s_tv,  do_v = sum_t dz_tv X_t;
+//   a matrix: dW = dz^T x; column groups: dW's sums with the entries and without.
+// With the target's term apart a small loss, and the gradient of a token that is
+// all but certain, keep their relative accuracy.  With one affine per row the
+// layer's gradients are sums over what the logits are made of: no product of
+// their own.
+//
+// Order.  The vocabulary goes in pieces of some thousand rows: the piece's
+// operand planes, its logits, and of each token the largest and the sum of the
+// exponentials.  Once all pieces have gone by (R is known) they come again for the
+// gradients: logits once more, dz, its products.  A vocabulary that is one
+// piece is multiplied once.
+#include <string.h>
+#include <math.h>
+#include <algorithm>
+#include "head.h"
+
+namespace mpq {
+
+namespace {
+
+constexpr size_t HALIGN = 256;
+inline size_t up(size_t x) { return (x + HALIGN - 1) / HALIGN * HALIGN; }
+inline int64_t up64(int64_t x) { return (x + 63) / 64 * 64; }
+inline int64_t up16(int64_t x) { return (x + 15) / 16 * 16; }
+struct Carve {
+  char* base;
+  size_t at = 0;
+  template <typename P>
+  P* take(size_t bytes) {
+    P* p = base ? reinterpret_cast<P*>(base + at) : nullptr;
+    at += up(bytes);
+    return p;
+  }
+};
+
+// What a piece's planes, and its logits, should take: half of the last-level cache.
+constexpr int64_t H_BYTES = (int64_t)128 << 20, H_ROWS = 1024;
+constexpr int H_SEG = 4096;   // columns of a token's logits that a workgroup reduces
+constexpr float H_LOG2E = 1.44269504f;
+
+// ------------------------------------------------------------------ tokens
+
+struct TokenArgs {
+  const void* x; int64_t ldx;
+  int dtype;
+  int64_t t, n, V;
+  const int32_t* targets;
+  const float* weights;
+  bool vec;                           // rows of x four elements at a time
+  float *weight, *sum, *target_z;     // the weight (0: the row is not read), X, the target's logit
+  uint32_t* rowmax;
+  uint32_t* gmax;                     // cleared
+  uint16_t* planes; int64_t plane;    // float16 terms, operand order of Kp columns
+  int terms; int64_t Kp;
+  // the transpose: columns' maxima, and terms
+  uint32_t* colmax;
+  uint16_t* xt; int64_t plane_t, tp;
+};
+
+__device__ __forceinline__ float token_weight(const TokenArgs& A, int64_t t) {
+  return t < A.t && A.targets[t] >= 0 ? (A.weights ? A.weights[t] : 1.f) : 0.f;
+}
+
+// A workgroup per row of the planes: the tokens' rows, zeros for those that are
+// not read and behind the last.
+__global__ __launch_bounds__(256) void head_token_kernel(TokenArgs A) {
+  __shared__ float red[2][4];
+  const int64_t row = blockIdx.x;
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  const float w = token_weight(A, row);
+  const bool live = w != 0.f;   // (a NaN weight is one)
+  auto load8 = [&](int64_t j, float* v) {
+    const int have = live ? (int)max((int64_t)0, min((int64_t)8, A.n - j)) : 0;
+    load4(A.x, row * A.ldx + j, A.dtype, A.vec, min(have, 4), v);
+    load4(A.x, row * A.ldx + j + 4, A.dtype, A.vec, max(have - 4, 0), v + 4);
+  };
+  uint32_t top = 0;
+  float s = 0.f;
+  for (int64_t j = threadIdx.x * 8; j < A.n; j += 256 * 8) {
+    float v[8];
+    load8(j, v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      s += v[k];
+      top = max(top, abs_bits(v[k]));
+    }
+  }
+  for (int o = 32; o; o >>= 1) {
+    s += shfl_xor_f(s, o);
+    top = max(top, (uint32_t)shfl_xor_i((int)top, o));
+  }
+  if (lane == 0) {
+    red[0][wave] = s;
+    red[1][wave] = __uint_as_float(top);
+  }
+  __syncthreads();
+  top = 0;
+  for (int k = 0; k < 4; ++k) top = max(top, __float_as_uint(red[1][k]));
+  if (threadIdx.x == 0 && row < A.t) {
+    A.weight[row] = w;
+    A.sum[row] = (red[0][0] + red[0][1]) + (red[0][2] + red[0][3]);
+    A.rowmax[row] = top;
+    A.target_z[row] = __uint_as_float(0x7fc00000u);   // a target past the vocabulary stays NaN
+  }
+  if (row == 0 && threadIdx.x == 0) *A.gmax = 0;
+  if (row == 0 && A.colmax)
+    for (int64_t j = threadIdx.x; j < A.n; j += 256) A.colmax[j] = 0;
+  const float f = pow2(pow2_shift(top));
+  for (int64_t j = threadIdx.x * 8; j < A.Kp; j += 256 * 8) {
+    float v[8];
+    load8(j, v);
+    v4u o[2];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t a[2], b[2];
+      f16_terms(v[2 * q] * f, a);
+      f16_terms(v[2 * q + 1] * f, b);
+      o[0][q] = pack2(a[0], b[0]);
+      o[1][q] = pack2(a[1], b[1]);
+    }
+    uint16_t* dst = A.planes + q_at(row, j, A.Kp);
+    *reinterpret_cast<v4u*>(dst) = o[0];
+    if (A.terms > 1) *reinterpret_cast<v4u*>(dst + A.plane) = o[1];
+  }
+}
+
+__device__ __forceinline__ void load_token4(const TokenArgs& A, int64_t t, int64_t j, float* v) {
+  const int live = token_weight(A, t) != 0.f ? (int)max((int64_t)0, min((int64_t)4, A.n - j)) : 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = 0.f;
+  if (live) load4(A.x, t * A.ldx + j, A.dtype, A.vec, live, v);
+}
+
+// Columns' largest magnitudes, tiles of 64 x 64 (integer maxima of bits: in any order the same).
+__global__ __launch_bounds__(256) void head_colmax_kernel(TokenArgs A) {
+  __shared__ uint32_t cm[4][64];
+  const int cx = threadIdx.x & 15, ry = threadIdx.x >> 4, wave = wave_id();
+  const int64_t tiles = (A.n + 63) / 64, t0 = blockIdx.x / tiles * 64, j = blockIdx.x % tiles * 64 + cx * 4;
+  uint32_t col[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    float v[4];
+    load_token4(A, t0 + ry + 16 * k, j, v);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) col[q] = max(col[q], abs_bits(v[q]));
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    col[q] = max(col[q], (uint32_t)shfl_xor_i((int)col[q], 16));
+    col[q] = max(col[q], (uint32_t)shfl_xor_i((int)col[q], 32));
+    if ((threadIdx.x & 63) < 16) cm[wave][cx * 4 + q] = col[q];
+  }
+  __syncthreads();
+  if (threadIdx.x < 64) {
+    const int64_t c = blockIdx.x % tiles * 64 + threadIdx.x;
+    const uint32_t top = max(max(cm[0][threadIdx.x], cm[1][threadIdx.x]), max(cm[2][threadIdx.x], cm[3][threadIdx.x]));
+    if (c < A.n) atomicMax(A.colmax + c, top);
+  }
+}
+
+__device__ __forceinline__ void put_terms(uint16_t* p, int64_t plane, int planes, const float* v) {
+  uint32_t b[4][2];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) f16_terms(v[k], b[k]);
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack2(b[0][0], b[1][0]), pack2(b[2][0], b[3][0]));
+  if (planes > 1)
+    *reinterpret_cast<uint2*>(p + plane) = make_uint2(pack2(b[0][1], b[1][1]), pack2(b[2][1], b[3][1]));
+}
+
+// x^T's planes: n rows of tp tokens.
+__global__ __launch_bounds__(256) void head_token_t_kernel(TokenArgs A) {
+  __shared__ float tl[64][65];
+  const int cx = threadIdx.x & 15, ry = threadIdx.x >> 4;
+  const int64_t tiles = (A.n + 63) / 64, t0 = blockIdx.x / tiles * 64, j0 = blockIdx.x % tiles * 64;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    float v[4];
+    load_token4(A, t0 + ry + 16 * k, j0 + cx * 4, v);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) tl[ry + 16 * k][cx * 4 + q] = v[q];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int64_t r = j0 + ry + 16 * k;
+    if (r >= A.n) continue;
+    const float f = pow2(pow2_shift(A.colmax[r]));
+    float v[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = tl[cx * 4 + q][ry + 16 * k] * f;
+    put_terms(A.xt + q_at(r, t0 + cx * 4, A.tp), A.plane_t, A.terms, v);
+  }
+}
+
+// ------------------------------------------------------------------ a matrix's planes
+
+struct DenseArgs {
+  const void* W; int64_t ldw;
+  int dtype;
+  bool vec;
+  int64_t m, n, Kp, mp;
+  int terms;
+  uint32_t* refs;                 // rows' largest magnitudes
+  uint16_t* out; int64_t plane;   // m rows of Kp
+  uint16_t* t; int64_t plane_t;   // the transpose, n rows of mp (nullptr: none)
+};
+
+// Rows' largest magnitudes and planes: a workgroup per row of the planes.
+__global__ __launch_bounds__(256) void head_dense_kernel(DenseArgs A) {
+  __shared__ uint32_t red[4];
+  const int64_t row = blockIdx.x;
+  const bool live = row < A.m;
+  auto load8 = [&](int64_t j, float* v) {
+    const int have = live ? (int)max((int64_t)0, min((int64_t)8, A.n - j)) : 0;
+    load4(A.W, row * A.ldw + j, A.dtype, A.vec, min(have, 4), v);
+    load4(A.W, row * A.ldw + j + 4, A.dtype, A.vec, max(have - 4, 0), v + 4);
+  };
+  uint32_t top = 0;
+  for (int64_t j = threadIdx.x * 8; j < A.n; j += 256 * 8) {
+    float v[8];
+    load8(j, v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top = max(top, abs_bits(v[k]));
+  }
+  for (int o = 32; o; o >>= 1) top = max(top, (uint32_t)shfl_xor_i((int)top, o));
+  if ((threadIdx.x & 63) == 0) red[wave_id()] = top;
+  __syncthreads();
+  top = max(max(red[0], red[1]), max(red[2], red[3]));
+  if (threadIdx.x == 0 && live) A.refs[row] = top;
+  const float f = pow2(pow2_shift(top));
+  for (int64_t j = threadIdx.x * 8; j < A.Kp; j += 256 * 8) {
+    float v[8];
+    load8(j, v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] *= f;
+    put_terms(A.out + q_at(row, j, A.Kp), A.plane, A.terms, v);
+    put_terms(A.out + q_at(row, j + 4, A.Kp), A.plane, A.terms, v + 4);
+  }
+}
+// The transpose, tiles of 64 x 64.
+__global__ __launch_bounds__(256) void head_dense_t_kernel(DenseArgs A) {
+  __shared__ float tl[64][65];
+  const int cx = threadIdx.x & 15, ry = threadIdx.x >> 4;
+  const int64_t tiles = (A.n + 63) / 64, r0 = blockIdx.x / tiles * 64, j0 = blockIdx.x % tiles * 64, j = j0 + cx * 4;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int64_t r = r0 + ry + 16 * k;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    const int live = r < A.m ? (int)max((int64_t)0, min((int64_t)4, A.n - j)) : 0;
+    const float f = r < A.m ? pow2(pow2_shift(A.refs[r])) : 1.f;
+    if (live) load4(A.W, r * A.ldw + j, A.dtype, A.vec, live, v);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) tl[ry + 16 * k][cx * 4 + q] = v[q] * f;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int64_t c = j0 + ry + 16 * k;
+    if (c >= A.n) continue;
+    float v[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = tl[cx * 4 + q][ry + 16 * k];
+    put_terms(A.t + q_at(c, r0 + cx * 4, A.mp), A.plane_t, A.terms, v);
+  }
+}
+
+// ------------------------------------------------------------------ a piece's logits
+
+struct PieceArgs {
+  const float* S; int64_t lds;     // t x m: s
+  int64_t t, m, row0;              // the piece's tokens and rows, the first of them
+  const float *a, *o, *b;          // of the piece's rows (nullptr: 1, 0, 0)
+  const float* levels; int mid;    // s is of entries less levels[mid] (mid < 0: as they are)
+  const float *weight, *sum;
+  const int32_t* targets;
+  float* target_z;
+  float2* part;                    // per segment and token: the largest, the sum
+  // gradients
+  const float *row_top, *row_scale, *row_target;   // the largest, w / sum of exponentials, dz of the target
+  const uint32_t* gmax;
+  const float* fmax;               // the largest factor of dz
+  const uint32_t* refs;            // the weights' planes' factors (nullptr: a is dz's factor)
+  uint32_t* dmax;
+  uint16_t* d; int64_t plane_d, mp; int terms_d;    // dz times its factors: t rows of mp (nullptr: none)
+  float* rowpart;                  // t x (mp / 64): sums of dz o' (nullptr: none)
+  uint16_t* dt; int64_t plane_t, tp; int terms_t;   // dz^T: m rows of tp (nullptr: none)
+  float* colpart;                  // (tp / 64) x 3 x m: sums of dz, dz s, dz X (nullptr: none)
+};
+
+struct Col4 {
+  float a[4], o[4], b[4];
+};
+__device__ __forceinline__ Col4 col4(const PieceArgs& A, int64_t i) {
+  Col4 C;
+  const float mid = A.mid >= 0 ? A.levels[A.mid] : 0.f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    C.a[k] = 1.f;
+    C.o[k] = C.b[k] = 0.f;
+    if (i + k >= A.m) continue;
+    if (A.a) {
+      C.a[k] = A.a[i + k];
+      C.o[k] = fmaf(C.a[k], mid, A.o ? A.o[i + k] : 0.f);
+    }
+    if (A.b) C.b[k] = A.b[i + k];
+  }
+  return C;
+}
+
+// A token's segment: its largest logit and the sum of the exponentials, without the target.
+__global__ __launch_bounds__(256) void head_stats_kernel(PieceArgs A) {
+  __shared__ float red[4];
+  const int64_t t = blockIdx.x, i0 = (int64_t)blockIdx.y * H_SEG;
+  const int wave = wave_id();
+  const int64_t target = (int64_t)A.targets[t] - A.row0;
+  const float X = A.sum[t];
+  float z[H_SEG / 256], top = -INFINITY;
+#pragma unroll
+  for (int q = 0; q < H_SEG / 1024; ++q) {
+    const int64_t i = i0 + q * 1024 + threadIdx.x * 4;
+    const Col4 C = col4(A, i);
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (i < A.m) s = *reinterpret_cast<const float4*>(A.S + t * A.lds + i);
+    const float v[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float y = i + k < A.m ? fmaf(C.a[k], v[k], fmaf(C.o[k], X, C.b[k])) : -INFINITY;
+      if (i + k == target && i + k < A.m) {
+        A.target_z[t] = y;
+        y = -INFINITY;
+      }
+      z[q * 4 + k] = y;
+      top = fmaxf(top, y);
+    }
+  }
+  for (int o = 32; o; o >>= 1) top = fmaxf(top, shfl_xor_f(top, o));
+  if ((threadIdx.x & 63) == 0) red[wave] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  const float from = top == -INFINITY ? 0.f : top;
+  float sum = 0.f;
+#pragma unroll
+  for (int k = 0; k < H_SEG / 256; ++k) sum += __builtin_amdgcn_exp2f((z[k] - from) * H_LOG2E);
+  for (int o = 32; o; o >>= 1) sum += shfl_xor_f(sum, o);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) red[wave] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) A.part[(int64_t)blockIdx.y * A.t + t] = make_float2(top, (red[0] + red[1]) + (red[2] + red[3]));
+}
+
+// The segments joined, the loss, and what the gradients take of a token: a wave each.
+__global__ __launch_bounds__(256) void head_join_kernel(const float2* __restrict__ part, int64_t segs, int64_t T,
+                                                        const float* __restrict__ weight, const float* __restrict__ target_z,
+                                                        float* __restrict__ loss, float* __restrict__ row_top,
+                                                        float* __restrict__ row_scale, float* __restrict__ row_target,
+                                                        uint32_t* __restrict__ gmax) {
+  const int64_t t = (int64_t)blockIdx.x * 4 + wave_id();
+  const int lane = threadIdx.x & 63;
+  if (t >= T) return;
+  float top = -INFINITY;
+  for (int64_t k = lane; k < segs; k += 64) top = fmaxf(top, part[k * T + t].x);
+  for (int o = 32; o; o >>= 1) top = fmaxf(top, shfl_xor_f(top, o));
+  double s = 0.0;
+  for (int64_t k = lane; k < segs; k += 64) {
+    const float2 p = part[k * T + t];
+    // (a segment of -inf alone has sum 0, or NaN)
+    s += p.x == -INFINITY ? (double)p.y : (double)p.y * exp((double)p.x - (double)top);
+  }
+  for (int o = 32; o; o >>= 1) s += shfl_d(s, lane ^ o);
+  if (lane != 0) return;
+  const float w = weight[t], zt = target_z[t];
+  if (w == 0.f) {   // not read
+    loss[t] = row_top[t] = row_scale[t] = row_target[t] = 0.f;
+    return;
+  }
+  if (!(s == s) || !(zt == zt)) {
+    row_top[t] = 0.f;
+    loss[t] = row_scale[t] = row_target[t] = __uint_as_float(0x7fc00000u);
+    if (gmax) atomicMax(gmax, 0x7fc00000u);
+    return;
+  }
+  // R - z of the target: log of the others' mass over its own
+  const double d = (double)top + log(s) - (double)zt;
+  const bool none = zt == -INFINITY;   // (all of them: nothing to move)
+  const double rest = none ? 1.0 : d > 0.0 ? 1.0 / (1.0 + exp(-d)) : exp(d) / (1.0 + exp(d));
+  const double l = none ? INFINITY : d > 0.0 ? d + log1p(exp(-d)) : log1p(exp(d));
+  const float all = fmaxf(top, zt);
+  const double total = s * exp((double)top - (double)all) + exp((double)zt - (double)all);
+  loss[t] = (float)((double)w * l);
+  row_top[t] = all;
+  row_scale[t] = all == -INFINITY ? 0.f : (float)((double)w / total);
+  row_target[t] = all == -INFINITY ? 0.f : (float)(-(double)w * rest);
+  if (gmax) atomicMax(gmax, abs_bits(row_target[t]));
+}
+
+__device__ __forceinline__ float dz_factor(const PieceArgs& A, int64_t i) {
+  return A.refs ? pow2(-pow2_shift(A.refs[i])) : A.a ? A.a[i] : 1.f;
+}
+
+// The largest factor of dz in the piece (one workgroup).
+__global__ __launch_bounds__(1024) void head_factor_kernel(PieceArgs A, float* __restrict__ out) {
+  __shared__ float red[16];
+  float top = 0.f;
+  for (int64_t i = threadIdx.x; i < A.m; i += 1024) top = fmaxf(top, fabsf(dz_factor(A, i)));
+  for (int o = 32; o; o >>= 1) top = fmaxf(top, shfl_xor_f(top, o));
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = top;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int k = 1; k < 16; ++k) top = fmaxf(top, red[k]);
+    *out = top;
+  }
+}
+
+__device__ __forceinline__ float sum16(float s) {
+  s += dpp_f<DPP_XOR1>(s);
+  s += dpp_f<DPP_XOR2>(s);
+  s += dpp_f<DPP_HALF_MIRROR>(s);
+  s += dpp_f<DPP_MIRROR>(s);
+  return s;
+}
+
+// A 64 x 64 tile of dz: its planes, its transpose's, its rows' and columns' sums.
+__global__ __launch_bounds__(256) void head_grad_kernel(PieceArgs A) {
+  __shared__ float tl[64][65];
+  __shared__ float cs[3][4][64];
+  const int cx = threadIdx.x & 15, ry = threadIdx.x >> 4, wave = wave_id();
+  const int64_t tiles = A.mp / 64, t0 = blockIdx.x / tiles * 64, i0 = blockIdx.x % tiles * 64, i = i0 + cx * 4;
+  const Col4 C = col4(A, i);
+  const float mid = A.mid >= 0 ? A.levels[A.mid] : 0.f, fm = A.d ? *A.fmax : 0.f;
+  float f[4] = {0.f, 0.f, 0.f, 0.f}, sums[3][4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if (A.d && i + q < A.m) f[q] = dz_factor(A, i + q);
+    sums[0][q] = sums[1][q] = sums[2][q] = 0.f;
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int64_t t = t0 + ry + 16 * k;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    if (t < A.t && A.weight[t] != 0.f) {
+      const float X = A.sum[t], top = A.row_top[t], scale = A.row_scale[t];
+      const int64_t target = (int64_t)A.targets[t] - A.row0;
+      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < A.m) s = *reinterpret_cast<const float4*>(A.S + t * A.lds + i);
+      const float sv[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (i + q >= A.m) continue;
+        const float z = fmaf(C.a[q], sv[q], fmaf(C.o[q], X, C.b[q]));
+        v[q] = i + q == target ? A.row_target[t] : scale == 0.f ? 0.f : __builtin_amdgcn_exp2f((z - top) * H_LOG2E) * scale;
+        sums[0][q] += v[q];
+        sums[1][q] = fmaf(v[q], fmaf(mid, X, sv[q]), sums[1][q]);
+        sums[2][q] = fmaf(v[q], X, sums[2][q]);
+      }
+      if (A.d) {
+        const uint32_t bound = abs_bits(A.row_target[t] * fm);
+        if (blockIdx.x % tiles == 0 && cx == 0) A.dmax[t] = bound;
+        const float g = pow2(pow2_shift(bound));
+        float u[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) u[q] = v[q] * f[q] * g;
+        put_terms(A.d + q_at(t, i, A.mp), A.plane_d, A.terms_d, u);
+      }
+    } else if (A.d && t < A.t) {
+      if (blockIdx.x % tiles == 0 && cx == 0) A.dmax[t] = 0;
+      put_terms(A.d + q_at(t, i, A.mp), A.plane_d, A.terms_d, v);
+    }
+    if (A.rowpart) {
+      const float s = sum16(fmaf(v[0], C.o[0], v[1] * C.o[1]) + fmaf(v[2], C.o[2], v[3] * C.o[3]));
+      if (cx == 0 && t < A.t) A.rowpart[t * tiles + blockIdx.x % tiles] = s;
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) tl[ry + 16 * k][cx * 4 + q] = v[q];
+  }
+  if (A.colpart) {
+#pragma unroll
+    for (int c = 0; c < 3; ++c)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float s = sums[c][q];
+        s += shfl_xor_f(s, 16);
+        s += shfl_xor_f(s, 32);
+        if ((threadIdx.x & 63) < 16) cs[c][wave][cx * 4 + q] = s;
+      }
+  }
+  __syncthreads();
+  if (A.colpart && threadIdx.x < 192) {
+    const int c = threadIdx.x >> 6, q = threadIdx.x & 63;
+    if (i0 + q < A.m)
+      A.colpart[(t0 / 64 * 3 + c) * A.m + i0 + q] = (cs[c][0][q] + cs[c][1][q]) + (cs[c][2][q] + cs[c][3][q]);
+  }
+  if (!A.dt) return;
+  const float g = pow2(pow2_shift(*A.gmax));
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int64_t r = i0 + ry + 16 * k;
+    if (r >= A.m) continue;
+    float v[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = tl[cx * 4 + q][ry + 16 * k] * g;
+    put_terms(A.dt + q_at(r, t0 + cx * 4, A.tp), A.plane_t, A.terms_t, v);
+  }
+}
+
+// Columns' sums, added up in order in float64.
+__global__ __launch_bounds__(256) void head_colsum_kernel(const float* __restrict__ part, int64_t ttiles, int64_t m,
+                                                          float* __restrict__ dbias, float* __restrict__ dscale,
+                                                          float* __restrict__ doffset) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= m) return;
+  float* out[3] = {dbias, dscale, doffset};
+#pragma unroll
+  for (int c = 0; c < 3; ++c) {
+    if (!out[c]) continue;
+    double s = 0.0;
+    for (int64_t k = 0; k < ttiles; ++k) s += (double)part[(k * 3 + c) * m + i];
+    out[c][i] = (float)s;
+  }
+}
+// Rows' sums over the pieces so far; and the row of the largest magnitudes that dz^T's planes share.
+__global__ __launch_bounds__(256) void head_rowsum_kernel(const float* __restrict__ part, int64_t tiles, int64_t T, bool first,
+                                                          float* __restrict__ rowadd) {
+  const int64_t t = (int64_t)blockIdx.x * 4 + wave_id();
+  const int lane = threadIdx.x & 63;
+  if (t >= T) return;
+  double s = 0.0;
+  for (int64_t k = lane; k < tiles; k += 64) s += (double)part[t * tiles + k];
+  for (int o = 32; o; o >>= 1) s += shfl_d(s, lane ^ o);
+  if (lane == 0) rowadd[t] = (float)((first ? 0.0 : (double)rowadd[t]) + s);
+}
+__global__ __launch_bounds__(256) void head_fill_kernel(uint32_t* __restrict__ out, int64_t n, const uint32_t* __restrict__ v) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i < n) out[i] = *v;
+}
+
+// dx from its sum over the pieces.
+__global__ __launch_bounds__(256) void head_dx_kernel(const float* __restrict__ acc, int64_t lda, int64_t T, int64_t n,
+                                                      const float* __restrict__ rowadd, void* __restrict__ dx, int64_t ld,
+                                                      int dtype, bool vec) {
+  const int64_t quads = (n + 3) / 4, step = (int64_t)gridDim.x * 256;
+  for (int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x; k < T * quads; k += step) {
+    const int64_t t = k / quads, j = (k - t * quads) * 4;
+    const float4 s = *reinterpret_cast<const float4*>(acc + t * lda + j);
+    const float add = rowadd ? rowadd[t] : 0.f;
+    const float v[4] = {s.x + add, s.y + add, s.z + add, s.w + add};
+    store4(dx, t * ld + j, dtype, vec, (int)min((int64_t)4, n - j), v);
+  }
+}
+
+bool whole_quads(const void* p, int64_t ld, int dtype) {
+  return !p || (reinterpret_cast<uintptr_t>(p) % (dtype == DT_F32 ? 16 : 8) == 0 && ld % 4 == 0);
+}
+
+// Rows row0 .. row0 + rows - 1 of a packed layer (row0 a multiple of 16).
+QLayer layer_rows(const QLayer& L, int64_t row0, int64_t rows) {
+  QLayer P = L;
+  P.m = rows;
+  P.tiles = (int)((rows + 15) / 16);
+  if (L.packed) P.packed = L.packed + (size_t)(row0 / 16) * L.chunks * 64;
+  if (L.scale) P.scale = L.scale + row0 * L.G;
+  if (L.offset) P.offset = L.offset + row0 * L.G;
+  return P;
+}
+
+#define H_TRY(x)                            \
+  do {                                      \
+    const hipError_t e_ = (x);              \
+    if (e_ != hipSuccess) return e_;        \
+  } while (0)
+#define H_LAUNCH(kernel, grid, block, ...)                                            \
+  do {                                                                                \
+    hipLaunchKernelGGL(kernel, dim3 grid, dim3(block), 0, st, __VA_ARGS__);           \
+    H_TRY(hipGetLastError());                                                         \
+  } while (0)
+
+hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
+  const QLayer& L = A.L;
+  const int64_t T = A.t, V = L.m, n = L.n, Kp = up64(n), tp = up64(T), ttiles = tp / 64;
+  const bool f32 = A.dtype == DT_F32, weights = A.dense || L.G > 1;   // the planes hold weights, not entries
+  const int XP = f32 ? 2 : 1;
+  // A matrix in 16 bits is one term, exact; a group's a e + o takes two, as float32 does.
+  const int WP = A.dense && !f32 ? 1 : weights ? 2 : 1;
+  const bool grads = A.need_dx || A.need_dhead, product = A.need_dhead && weights;
+  const int DX = f32 ? 2 : 1;                   // dz for dx
+  const int DT = A.dense && !f32 ? 1 : 2;       // dz^T for dW
+  const bool contract = !A.dense && L.group % Q_CONTRACT == 0;
+  // rows of a piece
+  int64_t rows = std::min(H_BYTES / (WP * Kp * 2), H_BYTES / (std::max<int64_t>(T, 1) * 4));
+  rows = std::min(std::max(rows / 256 * 256, H_ROWS), (V + 255) / 256 * 256);
+  const int64_t pieces = (V + rows - 1) / rows, segs = (rows + H_SEG - 1) / H_SEG;
+  const int64_t lds = rows;
+  Carve W{base};
+  TokenArgs K;
+  memset(&K, 0, sizeof(K));
+  K.weight = W.take<float>((size_t)T * 4);
+  K.sum = W.take<float>((size_t)T * 4);
+  K.target_z = W.take<float>((size_t)T * 4);
+  K.rowmax = W.take<uint32_t>((size_t)T * 4);
+  K.gmax = W.take<uint32_t>(8);
+  float* fmax = K.gmax ? reinterpret_cast<float*>(K.gmax + 1) : nullptr;
+  float* row_top = W.take<float>((size_t)T * 4);
+  float* row_scale = W.take<float>((size_t)T * 4);
+  float* row_target = W.take<float>((size_t)T * 4);
+  K.plane = up16(T) * Kp;
+  K.planes = W.take<uint16_t>((size_t)XP * K.plane * 2);
+  uint32_t* refs = W.take<uint32_t>(weights ? (size_t)rows * 4 : 0);
+  uint16_t* wp = W.take<uint16_t>((size_t)WP * up16(rows) * Kp * 2);
+  float* S = W.take<float>((size_t)T * lds * 4);
+  float2* part = W.take<float2>((size_t)pieces * segs * T * sizeof(float2));
+  QGemm gz, gx, gw;
+  memset(&gz, 0, sizeof(gz));
+  memset(&gx, 0, sizeof(gx));
+  memset(&gw, 0, sizeof(gw));
+  q_pairs(gz, WP, XP);
+  q_pairs(gx, WP, DX);
+  q_pairs(gw, XP, DT);
+  size_t ps = 0;
+  auto both_sizes = [&](auto f) {   // a whole piece's, and the last's
+    f(std::min(rows, V));
+    f(V - (pieces - 1) * rows);
+  };
+  both_sizes([&](int64_t nr) { ps = std::max(ps, q_gemm_workspace(nr, T, Kp, gz.npairs)); });
+  uint16_t *wt = nullptr, *d = nullptr, *dt = nullptr;
+  uint32_t *dmax = nullptr, *tmax = nullptr;
+  float *rowpart = nullptr, *rowadd = nullptr, *acc = nullptr, *colpart = nullptr, *dW = nullptr;
+  float2* cpart = nullptr;
+  const int64_t lda = (n + 3) / 4 * 4, cblocks = (n + Q_CONTRACT - 1) / Q_CONTRACT;
+  int splits = 1;
+  // (workspaces are sized without the offset's pointer: room for its sums either way)
+  const bool sums = A.need_dx && !weights && L.has_offset();
+  if (A.need_dx) {
+    wt = W.take<uint16_t>((size_t)WP * up16(n) * rows * 2);
+    d = W.take<uint16_t>((size_t)DX * up16(T) * rows * 2);
+    dmax = W.take<uint32_t>((size_t)T * 4);
+    rowpart = W.take<float>((size_t)T * (rows / 64) * 4);
+    rowadd = W.take<float>((size_t)T * 4);
+    if (pieces > 1) acc = W.take<float>((size_t)T * lda * 4);
+    both_sizes([&](int64_t nr) { ps = std::max(ps, q_gemm_workspace(n, T, up64(nr), gx.npairs)); });
+  }
+  if (A.need_dhead) colpart = W.take<float>((size_t)ttiles * 3 * rows * 4);
+  if (product) {
+    K.colmax = W.take<uint32_t>((size_t)n * 4);
+    K.plane_t = up16(n) * tp;
+    K.xt = W.take<uint16_t>((size_t)XP * K.plane_t * 2);
+    tmax = W.take<uint32_t>((size_t)rows * 4);
+    dt = W.take<uint16_t>((size_t)DT * up16(rows) * tp * 2);
+    if (contract) {
+      both_sizes([&](int64_t nr) { splits = std::max(splits, q_gemm_splits(n, nr, tp, gw.npairs)); });
+      cpart = W.take<float2>((size_t)splits * rows * cblocks * sizeof(float2));
+    } else {
+      if (!A.dense) dW = W.take<float>((size_t)rows * lda * 4);
+      both_sizes([&](int64_t nr) { ps = std::max(ps, q_gemm_workspace(n, nr, tp, gw.npairs)); });
+    }
+  }
+  float* gpart = W.take<float>(ps);
+  if (bytes) *bytes = W.at;
+  if (!base) return hipSuccess;
+
+  // the tokens
+  K.x = A.x; K.ldx = A.ldx;
+  K.dtype = A.dtype;
+  K.t = T; K.n = n; K.V = V;
+  K.targets = A.targets;
+  K.weights = A.weights;
+  K.vec = whole_quads(A.x, A.ldx, A.dtype);
+  K.terms = XP;
+  K.Kp = Kp;
+  K.tp = tp;
+  H_LAUNCH(head_token_kernel, ((unsigned)up16(T)), 256, K);
+  if (product) {
+    H_LAUNCH(head_colmax_kernel, ((unsigned)(ttiles * ((n + 63) / 64))), 256, K);
+    H_LAUNCH(head_token_t_kernel, ((unsigned)(ttiles * ((n + 63) / 64))), 256, K);
+  }
+  PieceArgs P;
+  memset(&P, 0, sizeof(P));
+  P.S = S; P.lds = lds;
+  P.t = T;
+  P.mid = -1;
+  P.weight = K.weight; P.sum = K.sum;
+  P.targets = A.targets;
+  P.target_z = K.target_z;
+  P.row_top = row_top; P.row_scale = row_scale; P.row_target = row_target;
+  P.gmax = K.gmax; P.fmax = fmax;
+  P.dmax = dmax;
+  P.terms_d = DX; P.terms_t = DT;
+  P.tp = tp;
+  // a piece's planes, and (logits) its s
+  auto piece = [&](int64_t k, bool logits, bool transposed) -> hipError_t {
+    const int64_t r0 = k * rows, nr = std::min(rows, V - r0), plane = up16(nr) * Kp, mp = up64(nr);
+    const QLayer Q = layer_rows(L, r0, nr);
+    if (A.dense) {
+      DenseArgs D;
+      memset(&D, 0, sizeof(D));
+      D.W = static_cast<const char*>(A.W) + r0 * A.ldw * (f32 ? 4 : 2);
+      D.ldw = A.ldw;
+      D.dtype = A.dtype;
+      D.vec = whole_quads(D.W, D.ldw, A.dtype);
+      D.m = nr; D.n = n; D.Kp = Kp; D.mp = mp;
+      D.terms = WP;
+      D.refs = refs;
+      D.out = wp; D.plane = plane;
+      D.t = wt; D.plane_t = up16(n) * mp;
+      H_LAUNCH(head_dense_kernel, ((unsigned)up16(nr)), 256, D);
+      if (transposed) H_LAUNCH(head_dense_t_kernel, ((unsigned)(mp / 64 * ((n + 63) / 64))), 256, D);
+    } else {
+      if (weights) H_TRY(launch_q_bounds(Q, refs, st));
+      if (logits) H_TRY(launch_q_unpack(Q, Kp, weights ? WP : 0, refs, wp, plane, st));
+      if (transposed) H_TRY(launch_q_unpack_t(Q, mp, weights ? WP : 0, refs, wt, up16(n) * mp, st));
+    }
+    P.m = nr;
+    P.row0 = r0;
+    P.mp = mp;
+    P.plane_d = up16(T) * mp;
+    P.plane_t = up16(nr) * tp;
+    P.a = weights ? nullptr : Q.scale;
+    P.o = weights ? nullptr : Q.offset;
+    P.b = A.bias ? A.bias + r0 : nullptr;
+    P.refs = weights ? refs : nullptr;
+    P.levels = L.levels;
+    P.mid = !weights && (L.fmt == QF_NIB || L.fmt == QF_BYTE) ? L.K / 2 : -1;
+    P.part = part + k * segs * T;
+    if (!logits) return hipSuccess;
+    gz.A = wp; gz.planeA = plane;
+    gz.B = K.planes; gz.planeB = K.plane;
+    gz.M = nr; gz.N = T; gz.K = Kp;
+    gz.O.y = S; gz.O.ldy = lds;
+    gz.O.rowmax = K.rowmax;
+    gz.O.colmax = weights ? refs : nullptr;
+    gz.O.mid = -1;
+    gz.O.dtype = DT_F32;
+    gz.O.vec = 1;
+    gz.O.rows = T; gz.O.cols = nr;
+    return launch_q_gemm(gz, gpart, st);
+  };
+  for (int64_t k = 0; k < pieces; ++k) {
+    H_TRY(piece(k, true, A.need_dx && pieces == 1));
+    H_LAUNCH(head_stats_kernel, ((unsigned)T, (unsigned)((P.m + H_SEG - 1) / H_SEG)), 256, P);
+  }
+  // (a piece's segments past its end are not written: the last piece has fewer)
+  const int64_t last = V - (pieces - 1) * rows, all_segs = (pieces - 1) * segs + (last + H_SEG - 1) / H_SEG;
+  H_LAUNCH(head_join_kernel, ((unsigned)((T + 3) / 4)), 256, part, all_segs, T, K.weight, K.target_z, A.loss, row_top, row_scale,
+           row_target, K.gmax);
+  if (!grads) return hipSuccess;
+  for (int64_t k = 0; k < pieces; ++k) {
+    if (pieces > 1) H_TRY(piece(k, true, A.need_dx));
+    const int64_t r0 = P.row0, nr = P.m, mp = P.mp;
+    P.d = A.need_dx ? d : nullptr;
+    P.rowpart = sums ? rowpart : nullptr;
+    P.dt = product ? dt : nullptr;
+    P.colpart = A.need_dhead ? colpart : nullptr;
+    if (A.need_dx) H_LAUNCH(head_factor_kernel, (1), 1024, P, fmax);
+    H_LAUNCH(head_grad_kernel, ((unsigned)(mp / 64 * ttiles)), 256, P);
+    if (A.need_dhead)
+      H_LAUNCH(head_colsum_kernel, ((unsigned)((nr + 255) / 256)), 256, colpart, ttiles, nr, A.dbias + r0,
+               weights ? nullptr : A.dscale + r0, weights ? nullptr : A.doffset + r0);
+    if (sums) H_LAUNCH(head_rowsum_kernel, ((unsigned)((T + 3) / 4)), 256, rowpart, mp / 64, T, k == 0, rowadd);
+    if (A.need_dx) {
+      gx.A = wt; gx.planeA = up16(n) * mp;
+      gx.B = d; gx.planeB = P.plane_d;
+      gx.M = n; gx.N = T; gx.K = mp;
+      gx.O.y = acc; gx.O.ldy = lda;
+      gx.O.res = k > 0 ? acc : nullptr; gx.O.ldres = lda;
+      gx.O.rowmax = dmax;
+      gx.O.mid = -1;
+      gx.O.dtype = DT_F32;
+      gx.O.vec = 1;
+      gx.O.rows = T; gx.O.cols = n;
+      if (pieces == 1) {
+        gx.O.y = A.dx; gx.O.ldy = A.lddx;
+        gx.O.rowadd = sums ? rowadd : nullptr;
+        gx.O.dtype = A.dtype;
+        gx.O.vec = whole_quads(A.dx, A.lddx, A.dtype);
+      }
+      H_TRY(launch_q_gemm(gx, gpart, st));
+    }
+    if (product) {
+      H_LAUNCH(head_fill_kernel, ((unsigned)((nr + 255) / 256)), 256, tmax, nr, K.gmax);
+      gw.A = K.xt; gw.planeA = K.plane_t;
+      gw.B = dt; gw.planeB = P.plane_t;
+      gw.M = n; gw.N = nr; gw.K = tp;
+      gw.O.rowmax = tmax;
+      gw.O.colmax = K.colmax;
+      gw.O.mid = -1;
+      gw.O.rows = nr; gw.O.cols = n;
+      if (A.dense) {
+        gw.O.y = static_cast<char*>(A.dW) + r0 * A.lddw * (f32 ? 4 : 2); gw.O.ldy = A.lddw;
+        gw.O.dtype = A.dtype;
+        gw.O.vec = whole_quads(gw.O.y, A.lddw, A.dtype);
+        H_TRY(launch_q_gemm(gw, gpart, st));
+      } else {
+        const QLayer Q = layer_rows(L, r0, nr);
+        gw.O.y = dW; gw.O.ldy = lda;
+        gw.O.dtype = DT_F32;
+        gw.O.vec = 1;
+        gw.L = Q;
+        gw.cpart = contract ? cpart : nullptr;
+        gw.cblocks = cblocks;
+        H_TRY(launch_q_gemm(gw, gpart, st));
+        H_TRY(launch_q_affine_sums(Q, contract ? cpart : nullptr, q_gemm_splits(n, nr, tp, gw.npairs), cblocks, dW, lda,
+                                   A.dscale + r0 * L.G, A.doffset + r0 * L.G, st));
+      }
+    }
+  }
+  if (A.need_dx && pieces > 1)
+    H_LAUNCH(head_dx_kernel, ((unsigned)std::min<int64_t>((T * (lda / 4) + 255) / 256, 4096)), 256, acc, lda, T, n,
+             sums ? rowadd : nullptr, A.dx, A.lddx, A.dtype, whole_quads(A.dx, A.lddx, A.dtype));
+  return hipSuccess;
+}
+
+}  // namespace
+
+size_t head_workspace(const HeadArgs& A) {
+  size_t b = 0;
+  (void)head(A, nullptr, &b, nullptr);
+  return b;
+}
+hipError_t launch_head(const HeadArgs& A, void* ws, hipStream_t st) {
+  return head(A, static_cast<char*>(ws), nullptr, st);
+}
+
+}  // namespace mpq

@@ -477,12 +477,28 @@ struct QLinearGrad {
   void* dx; int64_t lddx;
   float *dscale, *doffset, *dbias;
 };
+// A layer from a C entry's arguments, checked (api_ops.hip): its shapes and format, and
+// with its pointers.
+int q_layer_shape(QLayer& L, int64_t m, int64_t n, int64_t K, int64_t d, int64_t group, int kind);
+int q_layer_of(QLayer& L, const void* packed, int64_t m, int64_t n, const mpq_codebook* cb, const float* scale,
+               const float* offset, int64_t group);
+
 size_t q_packed_bytes(const QLayer& L);
 hipError_t launch_q_pack(const int32_t* codes, const QLayer& L, void* packed, hipStream_t st);
 size_t q_linear_workspace(const QLinearArgs& A);
 hipError_t launch_q_linear(const QLinearArgs& A, void* ws, hipStream_t st);
 size_t q_grad_workspace(const QLinearGrad& A);
 hipError_t launch_q_grad(const QLinearGrad& A, void* ws, hipStream_t st);
+// Parts of them, float16: a layer's planes in operand order (planes = 0: entries; else
+// terms of its weights times 2^pow2_shift(refs)), their transposes (rows of mp), the
+// bounds refs, and the affine's sums of a dW that is contracted (cpart) or in memory.
+hipError_t launch_q_unpack(const QLayer& L, int64_t Kp, int planes, const uint32_t* refs, uint16_t* out, int64_t plane,
+                           hipStream_t st);
+hipError_t launch_q_unpack_t(const QLayer& L, int64_t mp, int planes, const uint32_t* refs, uint16_t* out, int64_t plane,
+                             hipStream_t st);
+hipError_t launch_q_bounds(const QLayer& L, uint32_t* refs, hipStream_t st);
+hipError_t launch_q_affine_sums(const QLayer& L, const float2* cpart, int splits, int64_t cblocks, const float* dW, int64_t ldw,
+                                float* dscale, float* doffset, hipStream_t st);
 hipError_t launch_q_zero_rows(void* p, int64_t rows, int64_t cols, int64_t ld, int dtype, hipStream_t st);
 
 // What mpq_codebook_prepare notes in the low bits of mpq_codebook.magic (the struct

@@ -993,6 +993,36 @@ hipError_t launch_q_zero_rows(void* p, int64_t rows, int64_t cols, int64_t ld, i
   return hipGetLastError();
 }
 
+hipError_t launch_q_unpack(const QLayer& L, int64_t Kp, int planes, const uint32_t* refs, uint16_t* out, int64_t plane,
+                           hipStream_t st) {
+  return unpack<OpF16>(L, 0, L.tiles, Kp, planes, refs, out, plane, st);
+}
+hipError_t launch_q_unpack_t(const QLayer& L, int64_t mp, int planes, const uint32_t* refs, uint16_t* out, int64_t plane,
+                             hipStream_t st) {
+  return unpack_t(L, mp, planes, refs, out, plane, st);
+}
+hipError_t launch_q_bounds(const QLayer& L, uint32_t* refs, hipStream_t st) {
+  PrepArgs P;
+  memset(&P, 0, sizeof(P));
+  P.segs = 1;
+  P.L = L;
+  P.refs = refs;
+  hipLaunchKernelGGL(q_prep_kernel, dim3((unsigned)((L.m + 3) / 4)), dim3(256), 0, st, P);
+  return hipGetLastError();
+}
+hipError_t launch_q_affine_sums(const QLayer& L, const float2* cpart, int splits, int64_t cblocks, const float* dW, int64_t ldw,
+                                float* dscale, float* doffset, hipStream_t st) {
+  DuArgs D;   // (no d bias beside them)
+  memset(&D, 0, sizeof(D));
+  if (cpart)
+    hipLaunchKernelGGL(q_contract_finish_kernel, dim3((unsigned)((L.m * L.G + 15) / 16)), dim3(256), 0, st, L, cpart, splits,
+                       L.m, cblocks, 0, dscale, doffset, D, nullptr);
+  else
+    hipLaunchKernelGGL(q_affine_grad_kernel, dim3((unsigned)((L.m * L.G + 3) / 4)), dim3(256), 0, st, L, dW, ldw, 0, L.m,
+                       dscale, doffset, D, nullptr);
+  return hipGetLastError();
+}
+
 hipError_t launch_q_grad(const QLinearGrad& A, void* ws, hipStream_t st) {
   return backward(A, static_cast<char*>(ws), nullptr, st);
 }

@@ -117,3 +117,46 @@ def test_codes_are_the_formats():
         v[0] = L[-1]
         code, scale = R.encode8(v, F, np.full(len(v), 65535))
         assert scale[0] == 1.0 and np.array_equal(R.decode8(code, scale, F), v)
+
+
+def head(lib, dtype=0, t=4, ldx=32, packed=FAKE, m=16, n=32, cb=None, scale=FAKE, group=0, targets=FAKE, loss=FAKE, x=FAKE,
+         dx=FAKE, lddx=32, ds=FAKE, do=FAKE, db=FAKE, ws=FAKE, nb=1 << 40):
+    from test_abi_ops import book
+    cb = book() if cb is None else cb
+    return lib.mpq_linear_cross_entropy(x, dtype, t, ldx, packed, m, n, ctypes.byref(cb), scale, None, group, None, targets,
+                                        None, loss, dx, lddx, ds, do, db, ws, nb, None)
+
+
+def matrix(lib, dtype=0, t=4, ldx=32, W=FAKE, ldw=32, m=16, n=32, targets=FAKE, loss=FAKE, x=FAKE, dx=FAKE, lddx=32, dW=FAKE,
+           lddw=32, db=FAKE, ws=FAKE, nb=1 << 40):
+    return lib.mpq_matrix_cross_entropy(x, dtype, t, ldx, W, ldw, m, n, None, targets, None, loss, dx, lddx, dW, lddw, db, ws,
+                                        nb, None)
+
+
+def test_head_refusals(lib):  # noqa: F811
+    from test_abi_ops import book
+    off = ctypes.c_void_p((1 << 20) + 8)
+    for call in (head, matrix):
+        assert call(lib, dtype=3) == -3 and call(lib, t=-1) == -2 and call(lib, t=1 << 22) == -2 and call(lib, m=0) == -2
+        assert call(lib, n=0) == -2 and call(lib, ldx=31) == -2 and call(lib, lddx=31) == -2
+        assert call(lib, x=None) == -1 and call(lib, targets=None) == -1 and call(lib, loss=None) == -1
+        assert call(lib, db=None) == -1 and call(lib, ws=None) == -5 and call(lib, ws=off) == -5 and call(lib, nb=64) == -5
+    assert head(lib, packed=None) == -1 and head(lib, packed=off) == -5 and head(lib, scale=None) == -1
+    assert head(lib, do=None) == -1 and head(lib, ds=None) == -1
+    assert head(lib, group=-1) == -3 and head(lib, group=8, cb=book(K=256, d=8)) == -4
+    assert head(lib, cb=book(narrow=0)) == -4 and head(lib, cb=book(magic=1)) == -3
+    assert matrix(lib, W=None) == -1 and matrix(lib, dW=None) == -1 and matrix(lib, ldw=31) == -2
+    assert matrix(lib, lddw=31) == -2 and matrix(lib, m=(1 << 24) + 1) == -2 and matrix(lib, n=65537, ldx=1 << 17) == -2
+    assert head(lib, t=0, dx=None, ds=None, do=None, db=None) == 0 and matrix(lib, t=0, dx=None, dW=None, db=None) == 0
+
+
+def test_head_sizes(lib):  # noqa: F811
+    f, g = lib.mpq_linear_cross_entropy_workspace_bytes, lib.mpq_matrix_cross_entropy_workspace_bytes
+    for dtype in (0, 1, 2):
+        for t in (0, 1, 17, 2048):
+            assert f(dtype, t, 1000, 256, 16, 1, 0) > 0 and f(dtype, t, 1000, 256, 16, 1, 64) > 0
+            assert f(dtype, t, 1000, 256, 65536, 8, 0) > 0 and g(dtype, t, 1000, 256) > 0
+    assert f(3, 1, 10, 64, 16, 1, 0) == 0 and g(3, 1, 10, 64) == 0 and g(0, -1, 10, 64) == 0 and g(0, 1, 0, 64) == 0
+    assert f(0, 1 << 22, 10, 64, 16, 1, 0) == 0 and f(0, 1, 10, 64, 16, 3, 0) == 0 and g(0, (1 << 22) - 1, 10, 65536) == 0
+    # far from what the logits would take
+    assert f(0, 1 << 16, 1 << 20, 4096, 65536, 8, 0) < 4 << 30
