@@ -20,7 +20,7 @@ LIB = os.path.join(HERE, "libmpq.so")
 OBJDIR = os.path.join(HERE, "_build")
 SOURCES = ["api.hip", "gemm64.hip", "rowops.hip", "scalar.hip", "lattice.hip", "cd.hip", "cd_lattice.hip",
            "chol.hip", "greedy.hip", "frontend.hip", "e8dp.hip", "probe.hip", "digitgemm.hip",
-           "logits.hip", "qlinear.hip", "qskinny.hip", "qgemm.hip", "api_ops.hip", "adamw.hip", "head.hip", "api_tune.hip"]
+           "logits.hip", "qlinear.hip", "qskinny.hip", "qgemm.hip", "api_ops.hip", "adamw.hip", "head.hip", "headgemm.hip", "api_tune.hip"]
 ARCH = os.environ.get("MPQ_OFFLOAD_ARCH", "gfx950")
 
 FLAGS = [

@@ -45,7 +45,6 @@ struct Carve {
 // What a piece's planes, and its logits, should take: half of the last-level cache.
 constexpr int64_t H_BYTES = (int64_t)128 << 20, H_ROWS = 1024;
 constexpr int H_SEG = 4096;   // columns of a token's logits that a workgroup reduces
-constexpr float H_LOG2E = 1.44269504f;
 
 // ------------------------------------------------------------------ tokens
 
@@ -167,15 +166,6 @@ __global__ __launch_bounds__(256) void head_colmax_kernel(TokenArgs A) {
   }
 }
 
-__device__ __forceinline__ void put_terms(uint16_t* p, int64_t plane, int planes, const float* v) {
-  uint32_t b[4][2];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) f16_terms(v[k], b[k]);
-  *reinterpret_cast<uint2*>(p) = make_uint2(pack2(b[0][0], b[1][0]), pack2(b[2][0], b[3][0]));
-  if (planes > 1)
-    *reinterpret_cast<uint2*>(p + plane) = make_uint2(pack2(b[0][1], b[1][1]), pack2(b[2][1], b[3][1]));
-}
-
 // x^T's planes: n rows of tp tokens.
 __global__ __launch_bounds__(256) void head_token_t_kernel(TokenArgs A) {
   __shared__ float tl[64][65];
@@ -275,27 +265,6 @@ __global__ __launch_bounds__(256) void head_dense_t_kernel(DenseArgs A) {
 
 // ------------------------------------------------------------------ a piece's logits
 
-struct PieceArgs {
-  const float* S; int64_t lds;     // t x m: s
-  int64_t t, m, row0;              // the piece's tokens and rows, the first of them
-  const float *a, *o, *b;          // of the piece's rows (nullptr: 1, 0, 0)
-  const float* levels; int mid;    // s is of entries less levels[mid] (mid < 0: as they are)
-  const float *weight, *sum;
-  const int32_t* targets;
-  float* target_z;
-  float2* part;                    // per segment and token: the largest, the sum
-  // gradients
-  const float *row_top, *row_scale, *row_target;   // the largest, w / sum of exponentials, dz of the target
-  const uint32_t* gmax;
-  const float* fmax;               // the largest factor of dz
-  const uint32_t* refs;            // the weights' planes' factors (nullptr: a is dz's factor)
-  uint32_t* dmax;
-  uint16_t* d; int64_t plane_d, mp; int terms_d;    // dz times its factors: t rows of mp (nullptr: none)
-  float* rowpart;                  // t x (mp / 64): sums of dz o' (nullptr: none)
-  uint16_t* dt; int64_t plane_t, tp; int terms_t;   // dz^T: m rows of tp (nullptr: none)
-  float* colpart;                  // (tp / 64) x 3 x m: sums of dz, dz s, dz X (nullptr: none)
-};
-
 struct Col4 {
   float a[4], o[4], b[4];
 };
@@ -357,26 +326,36 @@ __global__ __launch_bounds__(256) void head_stats_kernel(PieceArgs A) {
   if (threadIdx.x == 0) A.part[(int64_t)blockIdx.y * A.t + t] = make_float2(top, (red[0] + red[1]) + (red[2] + red[3]));
 }
 
-// The segments joined, the loss, and what the gradients take of a token: a wave each.
+// The segments joined, the loss, and what the gradients take of a token: sixteen
+// tokens a workgroup, sixteen threads each.
 __global__ __launch_bounds__(256) void head_join_kernel(const float2* __restrict__ part, int64_t segs, int64_t T,
                                                         const float* __restrict__ weight, const float* __restrict__ target_z,
                                                         float* __restrict__ loss, float* __restrict__ row_top,
                                                         float* __restrict__ row_scale, float* __restrict__ row_target,
                                                         uint32_t* __restrict__ gmax) {
-  const int64_t t = (int64_t)blockIdx.x * 4 + wave_id();
-  const int lane = threadIdx.x & 63;
-  if (t >= T) return;
+  __shared__ float tops[16][16];
+  __shared__ double sums[16][16];
+  const int own = threadIdx.x & 15, lane = threadIdx.x >> 4;
+  const int64_t t = (int64_t)blockIdx.x * 16 + own, at = min(t, T - 1);
   float top = -INFINITY;
-  for (int64_t k = lane; k < segs; k += 64) top = fmaxf(top, part[k * T + t].x);
-  for (int o = 32; o; o >>= 1) top = fmaxf(top, shfl_xor_f(top, o));
+#pragma unroll 4
+  for (int64_t k = lane; k < segs; k += 16) top = fmaxf(top, part[k * T + at].x);
+  tops[lane][own] = top;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 16; ++k) top = fmaxf(top, tops[k][own]);
   double s = 0.0;
-  for (int64_t k = lane; k < segs; k += 64) {
-    const float2 p = part[k * T + t];
+#pragma unroll 4
+  for (int64_t k = lane; k < segs; k += 16) {
+    const float2 p = part[k * T + at];
     // (a segment of -inf alone has sum 0, or NaN)
     s += p.x == -INFINITY ? (double)p.y : (double)p.y * exp((double)p.x - (double)top);
   }
-  for (int o = 32; o; o >>= 1) s += shfl_d(s, lane ^ o);
-  if (lane != 0) return;
+  sums[lane][own] = s;
+  __syncthreads();
+  if (lane != 0 || t >= T) return;
+  s = 0.0;
+  for (int k = 0; k < 16; ++k) s += sums[k][own];
   const float w = weight[t], zt = target_z[t];
   if (w == 0.f) {   // not read
     loss[t] = row_top[t] = row_scale[t] = row_target[t] = 0.f;
@@ -418,14 +397,6 @@ __global__ __launch_bounds__(1024) void head_factor_kernel(PieceArgs A, float* _
     for (int k = 1; k < 16; ++k) top = fmaxf(top, red[k]);
     *out = top;
   }
-}
-
-__device__ __forceinline__ float sum16(float s) {
-  s += dpp_f<DPP_XOR1>(s);
-  s += dpp_f<DPP_XOR2>(s);
-  s += dpp_f<DPP_HALF_MIRROR>(s);
-  s += dpp_f<DPP_MIRROR>(s);
-  return s;
 }
 
 // A 64 x 64 tile of dz: its planes, its transpose's, its rows' and columns' sums.
@@ -593,11 +564,19 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
   const int DX = f32 ? 2 : 1;                   // dz for dx
   const int DT = A.dense && !f32 ? 1 : 2;       // dz^T for dW
   const bool contract = !A.dense && L.group % Q_CONTRACT == 0;
+  // Logits that fit half of the last-level cache are kept for the gradients: written and
+  // read there, they cost less than their product.  Others leave the product as
+  // statistics, and as dz.
+  const int64_t lds = (V + 255) / 256 * 256;
+  const bool kept = T * lds * 4 <= H_BYTES;
   // rows of a piece
-  int64_t rows = std::min(H_BYTES / (WP * Kp * 2), H_BYTES / (std::max<int64_t>(T, 1) * 4));
-  rows = std::min(std::max(rows / 256 * 256, H_ROWS), (V + 255) / 256 * 256);
-  const int64_t pieces = (V + rows - 1) / rows, segs = (rows + H_SEG - 1) / H_SEG;
-  const int64_t lds = rows;
+  int64_t rows = H_BYTES / (WP * Kp * 2);
+  if (!kept) rows = std::min(rows, H_BYTES / (T * 4));
+  rows = std::min(std::max(rows / 256 * 256, H_ROWS), lds);
+  const int64_t pieces = (V + rows - 1) / rows, last = V - (pieces - 1) * rows;
+  const HeadTile tile = head_tile(rows, T);
+  const int64_t seg = kept ? H_SEG : tile.rows, segs = (rows + seg - 1) / seg;
+  const int64_t row_tiles = kept ? rows / 64 : rows / tile.rows, token_tiles = kept ? ttiles : (T + 127) / 128;
   Carve W{base};
   TokenArgs K;
   memset(&K, 0, sizeof(K));
@@ -612,9 +591,9 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
   float* row_target = W.take<float>((size_t)T * 4);
   K.plane = up16(T) * Kp;
   K.planes = W.take<uint16_t>((size_t)XP * K.plane * 2);
-  uint32_t* refs = W.take<uint32_t>(weights ? (size_t)rows * 4 : 0);
+  uint32_t* refs = W.take<uint32_t>(weights ? (size_t)V * 4 : 0);
   uint16_t* wp = W.take<uint16_t>((size_t)WP * up16(rows) * Kp * 2);
-  float* S = W.take<float>((size_t)T * lds * 4);
+  float* S = W.take<float>(kept ? (size_t)T * lds * 4 : 0);
   float2* part = W.take<float2>((size_t)pieces * segs * T * sizeof(float2));
   QGemm gz, gx, gw;
   memset(&gz, 0, sizeof(gz));
@@ -628,7 +607,7 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
     f(std::min(rows, V));
     f(V - (pieces - 1) * rows);
   };
-  both_sizes([&](int64_t nr) { ps = std::max(ps, q_gemm_workspace(nr, T, Kp, gz.npairs)); });
+  if (kept) both_sizes([&](int64_t nr) { ps = std::max(ps, q_gemm_workspace(nr, T, Kp, gz.npairs)); });
   uint16_t *wt = nullptr, *d = nullptr, *dt = nullptr;
   uint32_t *dmax = nullptr, *tmax = nullptr;
   float *rowpart = nullptr, *rowadd = nullptr, *acc = nullptr, *colpart = nullptr, *dW = nullptr;
@@ -641,12 +620,12 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
     wt = W.take<uint16_t>((size_t)WP * up16(n) * rows * 2);
     d = W.take<uint16_t>((size_t)DX * up16(T) * rows * 2);
     dmax = W.take<uint32_t>((size_t)T * 4);
-    rowpart = W.take<float>((size_t)T * (rows / 64) * 4);
+    rowpart = W.take<float>((size_t)T * row_tiles * 4);
     rowadd = W.take<float>((size_t)T * 4);
     if (pieces > 1) acc = W.take<float>((size_t)T * lda * 4);
     both_sizes([&](int64_t nr) { ps = std::max(ps, q_gemm_workspace(n, T, up64(nr), gx.npairs)); });
   }
-  if (A.need_dhead) colpart = W.take<float>((size_t)ttiles * 3 * rows * 4);
+  if (A.need_dhead) colpart = W.take<float>((size_t)token_tiles * 3 * rows * 4);
   if (product) {
     K.colmax = W.take<uint32_t>((size_t)n * 4);
     K.plane_t = up16(n) * tp;
@@ -682,9 +661,8 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
   }
   PieceArgs P;
   memset(&P, 0, sizeof(P));
-  P.S = S; P.lds = lds;
+  P.lds = lds;
   P.t = T;
-  P.mid = -1;
   P.weight = K.weight; P.sum = K.sum;
   P.targets = A.targets;
   P.target_z = K.target_z;
@@ -693,10 +671,24 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
   P.dmax = dmax;
   P.terms_d = DX; P.terms_t = DT;
   P.tp = tp;
-  // a piece's planes, and (logits) its s
+  P.levels = L.levels;
+  P.mid = !weights && (L.fmt == QF_NIB || L.fmt == QF_BYTE) ? L.K / 2 : -1;
+  QLayer Q;
+  // The piece's rows, and its planes: for the logits, or the transpose.
   auto piece = [&](int64_t k, bool logits, bool transposed) -> hipError_t {
     const int64_t r0 = k * rows, nr = std::min(rows, V - r0), plane = up16(nr) * Kp, mp = up64(nr);
-    const QLayer Q = layer_rows(L, r0, nr);
+    Q = layer_rows(L, r0, nr);
+    P.m = nr;
+    P.row0 = r0;
+    P.mp = mp;
+    P.plane_d = up16(T) * mp;
+    P.plane_t = up16(nr) * tp;
+    P.S = S + r0;
+    P.a = weights ? nullptr : Q.scale;
+    P.o = weights ? nullptr : Q.offset;
+    P.b = A.bias ? A.bias + r0 : nullptr;
+    P.refs = weights ? refs + r0 : nullptr;
+    P.part = part + k * segs * T;
     if (A.dense) {
       DenseArgs D;
       memset(&D, 0, sizeof(D));
@@ -706,63 +698,61 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
       D.vec = whole_quads(D.W, D.ldw, A.dtype);
       D.m = nr; D.n = n; D.Kp = Kp; D.mp = mp;
       D.terms = WP;
-      D.refs = refs;
+      D.refs = refs + r0;
       D.out = wp; D.plane = plane;
       D.t = wt; D.plane_t = up16(n) * mp;
-      H_LAUNCH(head_dense_kernel, ((unsigned)up16(nr)), 256, D);
+      if (logits) H_LAUNCH(head_dense_kernel, ((unsigned)up16(nr)), 256, D);
       if (transposed) H_LAUNCH(head_dense_t_kernel, ((unsigned)(mp / 64 * ((n + 63) / 64))), 256, D);
     } else {
-      if (weights) H_TRY(launch_q_bounds(Q, refs, st));
-      if (logits) H_TRY(launch_q_unpack(Q, Kp, weights ? WP : 0, refs, wp, plane, st));
-      if (transposed) H_TRY(launch_q_unpack_t(Q, mp, weights ? WP : 0, refs, wt, up16(n) * mp, st));
+      if (weights && logits) H_TRY(launch_q_bounds(Q, refs + r0, st));
+      if (logits) H_TRY(launch_q_unpack(Q, Kp, weights ? WP : 0, refs + r0, wp, plane, st));
+      if (transposed) H_TRY(launch_q_unpack_t(Q, mp, weights ? WP : 0, refs + r0, wt, up16(n) * mp, st));
     }
-    P.m = nr;
-    P.row0 = r0;
-    P.mp = mp;
-    P.plane_d = up16(T) * mp;
-    P.plane_t = up16(nr) * tp;
-    P.a = weights ? nullptr : Q.scale;
-    P.o = weights ? nullptr : Q.offset;
-    P.b = A.bias ? A.bias + r0 : nullptr;
-    P.refs = weights ? refs : nullptr;
-    P.levels = L.levels;
-    P.mid = !weights && (L.fmt == QF_NIB || L.fmt == QF_BYTE) ? L.K / 2 : -1;
-    P.part = part + k * segs * T;
-    if (!logits) return hipSuccess;
     gz.A = wp; gz.planeA = plane;
     gz.B = K.planes; gz.planeB = K.plane;
     gz.M = nr; gz.N = T; gz.K = Kp;
-    gz.O.y = S; gz.O.ldy = lds;
-    gz.O.rowmax = K.rowmax;
-    gz.O.colmax = weights ? refs : nullptr;
-    gz.O.mid = -1;
-    gz.O.dtype = DT_F32;
-    gz.O.vec = 1;
-    gz.O.rows = T; gz.O.cols = nr;
-    return launch_q_gemm(gz, gpart, st);
+    return hipSuccess;
   };
   for (int64_t k = 0; k < pieces; ++k) {
-    H_TRY(piece(k, true, A.need_dx && pieces == 1));
-    H_LAUNCH(head_stats_kernel, ((unsigned)T, (unsigned)((P.m + H_SEG - 1) / H_SEG)), 256, P);
+    H_TRY(piece(k, true, false));
+    if (kept) {
+      gz.O.y = S + P.row0; gz.O.ldy = lds;
+      gz.O.rowmax = K.rowmax;
+      gz.O.colmax = P.refs;
+      gz.O.mid = -1;
+      gz.O.dtype = DT_F32;
+      gz.O.vec = 1;
+      gz.O.rows = T; gz.O.cols = P.m;
+      H_TRY(launch_q_gemm(gz, gpart, st));
+      H_LAUNCH(head_stats_kernel, ((unsigned)T, (unsigned)((P.m + H_SEG - 1) / H_SEG)), 256, P);
+    } else {
+      H_TRY(launch_head_gemm(gz, P, K.rowmax, false, st));
+    }
   }
-  // (a piece's segments past its end are not written: the last piece has fewer)
-  const int64_t last = V - (pieces - 1) * rows, all_segs = (pieces - 1) * segs + (last + H_SEG - 1) / H_SEG;
-  H_LAUNCH(head_join_kernel, ((unsigned)((T + 3) / 4)), 256, part, all_segs, T, K.weight, K.target_z, A.loss, row_top, row_scale,
+  // (the last piece may have fewer segments)
+  const int64_t all_segs = (pieces - 1) * segs + (last + seg - 1) / seg;
+  H_LAUNCH(head_join_kernel, ((unsigned)((T + 15) / 16)), 256, part, all_segs, T, K.weight, K.target_z, A.loss, row_top, row_scale,
            row_target, K.gmax);
   if (!grads) return hipSuccess;
   for (int64_t k = 0; k < pieces; ++k) {
-    if (pieces > 1) H_TRY(piece(k, true, A.need_dx));
+    H_TRY(piece(k, !kept, A.need_dx));
     const int64_t r0 = P.row0, nr = P.m, mp = P.mp;
     P.d = A.need_dx ? d : nullptr;
     P.rowpart = sums ? rowpart : nullptr;
     P.dt = product ? dt : nullptr;
     P.colpart = A.need_dhead ? colpart : nullptr;
     if (A.need_dx) H_LAUNCH(head_factor_kernel, (1), 1024, P, fmax);
-    H_LAUNCH(head_grad_kernel, ((unsigned)(mp / 64 * ttiles)), 256, P);
+    if (kept)
+      H_LAUNCH(head_grad_kernel, ((unsigned)(mp / 64 * ttiles)), 256, P);
+    else
+      H_TRY(launch_head_gemm(gz, P, K.rowmax, true, st));
+    const HeadTile own = head_tile(nr, T);   // (of the last piece, smaller)
     if (A.need_dhead)
-      H_LAUNCH(head_colsum_kernel, ((unsigned)((nr + 255) / 256)), 256, colpart, ttiles, nr, A.dbias + r0,
+      H_LAUNCH(head_colsum_kernel, ((unsigned)((nr + 255) / 256)), 256, colpart,
+               kept ? ttiles : (T + own.tokens - 1) / own.tokens, nr, A.dbias + r0,
                weights ? nullptr : A.dscale + r0, weights ? nullptr : A.doffset + r0);
-    if (sums) H_LAUNCH(head_rowsum_kernel, ((unsigned)((T + 3) / 4)), 256, rowpart, mp / 64, T, k == 0, rowadd);
+    if (sums) H_LAUNCH(head_rowsum_kernel, ((unsigned)((T + 3) / 4)), 256, rowpart,
+                       kept ? mp / 64 : (nr + own.rows - 1) / own.rows, T, k == 0, rowadd);
     if (A.need_dx) {
       gx.A = wt; gx.planeA = up16(n) * mp;
       gx.B = d; gx.planeB = P.plane_d;
@@ -797,7 +787,6 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
         gw.O.vec = whole_quads(gw.O.y, A.lddw, A.dtype);
         H_TRY(launch_q_gemm(gw, gpart, st));
       } else {
-        const QLayer Q = layer_rows(L, r0, nr);
         gw.O.y = dW; gw.O.ldy = lda;
         gw.O.dtype = DT_F32;
         gw.O.vec = 1;

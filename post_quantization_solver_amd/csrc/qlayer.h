@@ -425,7 +425,8 @@ __device__ __forceinline__ int64_t q_at(int64_t row, int64_t k, int64_t K) {
   return ((row >> 4) * (K >> 5) + (k >> 5)) * 512 + (row & 15) * 32 + (k & 31);
 }
 struct QGemm {
-  const uint16_t* A; int64_t planeA;        // operand order
+  const uint16_t* A; int64_t planeA;        // operand order (lda: of the tile loop that reads it in rows)
+  int64_t lda;
   const uint16_t* B; int64_t ldb, planeB;   // operand order (ldb = 0), or rows
   int64_t M, N, K;        // columns i, rows j, depth of one plane
   int npairs;

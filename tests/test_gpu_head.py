@@ -242,6 +242,8 @@ def test_pieces(dtype):
     """Vocabularies of several pieces: many tokens, and long rows."""
     matrix_case(2600, 40, 33000, dtype, padded=True, seed=1)
     packed_case("s16", 2600, 40, 33000, dtype, padded=True, seed=2)
+    packed_case("s64", 2060, 72, 33001, dtype, padded=True, seed=2)
+    packed_case("s16", 2100, 192, 33000, dtype, group=64, seed=3)
     packed_case("s16", 2100, 96, 33000, dtype, group=32, seed=3)
     packed_case("e8240", 1500, 40, 33000, dtype, seed=4, offset=False)
     packed_case("s16", 2500, 40960, 5, dtype, seed=5)
