@@ -611,8 +611,8 @@ int mpq_distill(const void* logits, int dtype, int64_t t, int64_t V, int64_t ld,
  * x as float16 terms under a power of two per token: one, exact, for 16-bit types
  * (elements below 2^-28 of their row's largest lose bits, those below 2^-39 are gone),
  * two (22 bits) for float32; the weights of column groups as two terms.  For dx, dz
- * enters as one term (11 bits; float32: two) under a power of two per token; for
- * the gradients of column groups as two.
+ * (under a power of two per token) and the weights of column groups enter as one term
+ * (11 bits; float32: two); for the gradients of column groups dz as two.
  * 1 <= m, 0 <= t < 2^22, ceil(t / 64) ceil(n / 64) < 2^24.  The workspace holds some
  * 128 MB of operands and of logits each, or 1024 rows of the head's; t = 0: gradients
  * of zero. */

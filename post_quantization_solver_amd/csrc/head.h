@@ -27,6 +27,7 @@ struct PieceArgs {
   int64_t t, m, row0;              // the piece's tokens and rows, the first of them
   const float *a, *o, *b;          // of the piece's rows (nullptr: 1, 0, 0)
   const float* levels; int mid;    // s is of entries less levels[mid] (mid < 0: as they are)
+  int centre;                      // as mid, of the entries that dz meets
   const float *weight, *sum;
   const int32_t* targets;
   float* target_z;

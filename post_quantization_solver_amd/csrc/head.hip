@@ -44,7 +44,6 @@ struct Carve {
 
 // What a piece's planes, and its logits, should take: half of the last-level cache.
 constexpr int64_t H_BYTES = (int64_t)128 << 20, H_ROWS = 1024;
-constexpr int H_SEG = 4096;   // columns of a token's logits that a workgroup reduces
 
 // ------------------------------------------------------------------ tokens
 
@@ -57,9 +56,12 @@ struct TokenArgs {
   bool vec;                           // rows of x four elements at a time
   float *weight, *sum, *target_z;     // the weight (0: the row is not read), X, the target's logit
   uint32_t* rowmax;
-  uint32_t* gmax;                     // cleared
+  uint32_t* gmax;                     // two words, cleared
   uint16_t* planes; int64_t plane;    // float16 terms, operand order of Kp columns
   int terms; int64_t Kp;
+  bool raw;                           // bfloat16 as it is, in place of terms
+  bool frags;                         // in the few-row product's order
+  float* ones;                        // V ones, or nullptr
   // the transpose: columns' maxima, and terms
   uint32_t* colmax;
   uint16_t* xt; int64_t plane_t, tp;
@@ -73,8 +75,13 @@ __device__ __forceinline__ float token_weight(const TokenArgs& A, int64_t t) {
 // not read and behind the last.
 __global__ __launch_bounds__(256) void head_token_kernel(TokenArgs A) {
   __shared__ float red[2][4];
-  const int64_t row = blockIdx.x;
+  const int64_t row = blockIdx.x, rows = (A.t + 15) / 16 * 16;
   const int lane = threadIdx.x & 63, wave = wave_id();
+  if (row >= rows) {   // the workgroups behind them
+    const int64_t i = (row - rows) * 256 + threadIdx.x;
+    if (i < A.V) A.ones[i] = 1.f;
+    return;
+  }
   const float w = token_weight(A, row);
   const bool live = w != 0.f;   // (a NaN weight is one)
   auto load8 = [&](int64_t j, float* v) {
@@ -110,7 +117,7 @@ __global__ __launch_bounds__(256) void head_token_kernel(TokenArgs A) {
     A.rowmax[row] = top;
     A.target_z[row] = __uint_as_float(0x7fc00000u);   // a target past the vocabulary stays NaN
   }
-  if (row == 0 && threadIdx.x == 0) *A.gmax = 0;
+  if (row == 0 && threadIdx.x < 2) A.gmax[threadIdx.x] = 0;
   if (row == 0 && A.colmax)
     for (int64_t j = threadIdx.x; j < A.n; j += 256) A.colmax[j] = 0;
   const float f = pow2(pow2_shift(top));
@@ -126,7 +133,11 @@ __global__ __launch_bounds__(256) void head_token_kernel(TokenArgs A) {
       o[0][q] = pack2(a[0], b[0]);
       o[1][q] = pack2(a[1], b[1]);
     }
-    uint16_t* dst = A.planes + q_at(row, j, A.Kp);
+    if (A.raw)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) o[0][q] = OpBf16::pack(v[2 * q], v[2 * q + 1]);
+    uint16_t* dst = A.planes + (A.frags ? ((row >> 4) * (A.Kp >> 5) + (j >> 5)) * 512 + ((j >> 3 & 3) * 16 + (row & 15)) * 8
+                                        : q_at(row, j, A.Kp));
     *reinterpret_cast<v4u*>(dst) = o[0];
     if (A.terms > 1) *reinterpret_cast<v4u*>(dst + A.plane) = o[1];
   }
@@ -236,6 +247,24 @@ __global__ __launch_bounds__(256) void head_dense_kernel(DenseArgs A) {
     put_terms(A.out + q_at(row, j + 4, A.Kp), A.plane, A.terms, v + 4);
   }
 }
+// Rows' largest magnitudes alone, a wave each.
+__global__ __launch_bounds__(256) void head_rowmax_kernel(DenseArgs A) {
+  const int lane = threadIdx.x & 63;
+  const int64_t row = (int64_t)blockIdx.x * 4 + wave_id();
+  if (row >= A.m) return;
+  uint32_t top = 0;
+#pragma unroll 4
+  for (int64_t j = lane * 8; j < A.n; j += 64 * 8) {
+    const int have = (int)min((int64_t)8, A.n - j);
+    float v[8];
+    load4(A.W, row * A.ldw + j, A.dtype, A.vec, min(have, 4), v);
+    load4(A.W, row * A.ldw + j + 4, A.dtype, A.vec, max(have - 4, 0), v + 4);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top = max(top, abs_bits(v[k]));
+  }
+  for (int o = 32; o; o >>= 1) top = max(top, (uint32_t)shfl_xor_i((int)top, o));
+  if (lane == 0) A.refs[row] = top;
+}
 // The transpose, tiles of 64 x 64.
 __global__ __launch_bounds__(256) void head_dense_t_kernel(DenseArgs A) {
   __shared__ float tl[64][65];
@@ -285,16 +314,18 @@ __device__ __forceinline__ Col4 col4(const PieceArgs& A, int64_t i) {
   return C;
 }
 
-// A token's segment: its largest logit and the sum of the exponentials, without the target.
+// A token's segment of 1024 NQ rows: its largest logit and the sum of the exponentials,
+// without the target.
+template <int NQ>
 __global__ __launch_bounds__(256) void head_stats_kernel(PieceArgs A) {
   __shared__ float red[4];
-  const int64_t t = blockIdx.x, i0 = (int64_t)blockIdx.y * H_SEG;
+  const int64_t t = blockIdx.x, i0 = (int64_t)blockIdx.y * (NQ * 1024);
   const int wave = wave_id();
   const int64_t target = (int64_t)A.targets[t] - A.row0;
   const float X = A.sum[t];
-  float z[H_SEG / 256], top = -INFINITY;
+  float z[NQ * 4], top = -INFINITY;
 #pragma unroll
-  for (int q = 0; q < H_SEG / 1024; ++q) {
+  for (int q = 0; q < NQ; ++q) {
     const int64_t i = i0 + q * 1024 + threadIdx.x * 4;
     const Col4 C = col4(A, i);
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -318,7 +349,7 @@ __global__ __launch_bounds__(256) void head_stats_kernel(PieceArgs A) {
   const float from = top == -INFINITY ? 0.f : top;
   float sum = 0.f;
 #pragma unroll
-  for (int k = 0; k < H_SEG / 256; ++k) sum += __builtin_amdgcn_exp2f((z[k] - from) * H_LOG2E);
+  for (int k = 0; k < NQ * 4; ++k) sum += __builtin_amdgcn_exp2f((z[k] - from) * H_LOG2E);
   for (int o = 32; o; o >>= 1) sum += shfl_xor_f(sum, o);
   __syncthreads();
   if ((threadIdx.x & 63) == 0) red[wave] = sum;
@@ -385,18 +416,13 @@ __device__ __forceinline__ float dz_factor(const PieceArgs& A, int64_t i) {
   return A.refs ? pow2(-pow2_shift(A.refs[i])) : A.a ? A.a[i] : 1.f;
 }
 
-// The largest factor of dz in the piece (one workgroup).
-__global__ __launch_bounds__(1024) void head_factor_kernel(PieceArgs A, float* __restrict__ out) {
-  __shared__ float red[16];
-  float top = 0.f;
-  for (int64_t i = threadIdx.x; i < A.m; i += 1024) top = fmaxf(top, fabsf(dz_factor(A, i)));
-  for (int o = 32; o; o >>= 1) top = fmaxf(top, shfl_xor_f(top, o));
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = top;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int k = 1; k < 16; ++k) top = fmaxf(top, red[k]);
-    *out = top;
-  }
+// The largest factor of dz over all rows (by its bits: in any order the same).
+__global__ __launch_bounds__(256) void head_factor_kernel(PieceArgs A, uint32_t* __restrict__ out) {
+  uint32_t top = 0;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < A.m; i += (int64_t)gridDim.x * 256)
+    top = max(top, abs_bits(dz_factor(A, i)));
+  for (int o = 32; o; o >>= 1) top = max(top, (uint32_t)shfl_xor_i((int)top, o));
+  if ((threadIdx.x & 63) == 0) atomicMax(out, top);
 }
 
 // A 64 x 64 tile of dz: its planes, its transpose's, its rows' and columns' sums.
@@ -407,10 +433,12 @@ __global__ __launch_bounds__(256) void head_grad_kernel(PieceArgs A) {
   const int64_t tiles = A.mp / 64, t0 = blockIdx.x / tiles * 64, i0 = blockIdx.x % tiles * 64, i = i0 + cx * 4;
   const Col4 C = col4(A, i);
   const float mid = A.mid >= 0 ? A.levels[A.mid] : 0.f, fm = A.d ? *A.fmax : 0.f;
-  float f[4] = {0.f, 0.f, 0.f, 0.f}, sums[3][4];
+  const float off = A.mid == A.centre ? 0.f : A.levels[A.centre];
+  float f[4] = {0.f, 0.f, 0.f, 0.f}, od[4], sums[3][4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     if (A.d && i + q < A.m) f[q] = dz_factor(A, i + q);
+    od[q] = fmaf(C.a[q], off, C.o[q]);
     sums[0][q] = sums[1][q] = sums[2][q] = 0.f;
   }
 #pragma unroll
@@ -446,7 +474,7 @@ __global__ __launch_bounds__(256) void head_grad_kernel(PieceArgs A) {
       put_terms(A.d + q_at(t, i, A.mp), A.plane_d, A.terms_d, v);
     }
     if (A.rowpart) {
-      const float s = sum16(fmaf(v[0], C.o[0], v[1] * C.o[1]) + fmaf(v[2], C.o[2], v[3] * C.o[3]));
+      const float s = sum16(fmaf(v[0], od[0], v[1] * od[1]) + fmaf(v[2], od[2], v[3] * od[3]));
       if (cx == 0 && t < A.t) A.rowpart[t * tiles + blockIdx.x % tiles] = s;
     }
 #pragma unroll
@@ -561,7 +589,11 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
   // A matrix in 16 bits is one term, exact; a group's a e + o takes two, as float32 does.
   const int WP = A.dense && !f32 ? 1 : weights ? 2 : 1;
   const bool grads = A.need_dx || A.need_dhead, product = A.need_dhead && weights;
+  // A 16-bit matrix whose rows the product's tiles can read in place goes without planes.
+  const bool in_place = A.dense && !f32 && n % 64 == 0 && A.ldw % 8 == 0 && A.ldw <= (1 << 20) &&
+                        reinterpret_cast<uintptr_t>(A.W) % 16 == 0;
   const int DX = f32 ? 2 : 1;                   // dz for dx
+  const int WX = f32 ? WP : 1;                  // the weights for dx: as many terms as dz
   const int DT = A.dense && !f32 ? 1 : 2;       // dz^T for dW
   const bool contract = !A.dense && L.group % Q_CONTRACT == 0;
   // Logits that fit half of the last-level cache are kept for the gradients: written and
@@ -575,7 +607,11 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
   rows = std::min(std::max(rows / 256 * 256, H_ROWS), lds);
   const int64_t pieces = (V + rows - 1) / rows, last = V - (pieces - 1) * rows;
   const HeadTile tile = head_tile(rows, T);
-  const int64_t seg = kept ? H_SEG : tile.rows, segs = (rows + seg - 1) / seg;
+  // Few tokens: straight from the packed codes.
+  const bool few = kept && !A.dense && q_few_rows(L, A.dtype, T);
+  const int64_t seg_rows = T <= 64 ? 1024 : 4096;   // (short segments: as many workgroups as there are CUs)
+  // (pieces begin at multiples of the tile's rows)
+  const int64_t seg = kept ? seg_rows : tile.rows, all_segs = (V + seg - 1) / seg;
   const int64_t row_tiles = kept ? rows / 64 : rows / tile.rows, token_tiles = kept ? ttiles : (T + 127) / 128;
   Carve W{base};
   TokenArgs K;
@@ -585,22 +621,24 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
   K.target_z = W.take<float>((size_t)T * 4);
   K.rowmax = W.take<uint32_t>((size_t)T * 4);
   K.gmax = W.take<uint32_t>(8);
-  float* fmax = K.gmax ? reinterpret_cast<float*>(K.gmax + 1) : nullptr;
+  uint32_t* fmax = K.gmax ? K.gmax + 1 : nullptr;
+  float* ones = W.take<float>(!A.dense && !weights ? (size_t)V * 4 : 0);
   float* row_top = W.take<float>((size_t)T * 4);
   float* row_scale = W.take<float>((size_t)T * 4);
   float* row_target = W.take<float>((size_t)T * 4);
-  K.plane = up16(T) * Kp;
+  const int64_t Kx = few ? (int64_t)L.chunks * q_chunk(L.fmt) : Kp;
+  K.plane = up16(T) * Kx;
   K.planes = W.take<uint16_t>((size_t)XP * K.plane * 2);
   uint32_t* refs = W.take<uint32_t>(weights ? (size_t)V * 4 : 0);
   uint16_t* wp = W.take<uint16_t>((size_t)WP * up16(rows) * Kp * 2);
   float* S = W.take<float>(kept ? (size_t)T * lds * 4 : 0);
-  float2* part = W.take<float2>((size_t)pieces * segs * T * sizeof(float2));
+  float2* part = W.take<float2>((size_t)all_segs * T * sizeof(float2));
   QGemm gz, gx, gw;
   memset(&gz, 0, sizeof(gz));
   memset(&gx, 0, sizeof(gx));
   memset(&gw, 0, sizeof(gw));
   q_pairs(gz, WP, XP);
-  q_pairs(gx, WP, DX);
+  q_pairs(gx, WX, DX);
   q_pairs(gw, XP, DT);
   size_t ps = 0;
   auto both_sizes = [&](auto f) {   // a whole piece's, and the last's
@@ -617,7 +655,7 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
   // (workspaces are sized without the offset's pointer: room for its sums either way)
   const bool sums = A.need_dx && !weights && L.has_offset();
   if (A.need_dx) {
-    wt = W.take<uint16_t>((size_t)WP * up16(n) * rows * 2);
+    wt = W.take<uint16_t>((size_t)WX * up16(n) * rows * 2);
     d = W.take<uint16_t>((size_t)DX * up16(T) * rows * 2);
     dmax = W.take<uint32_t>((size_t)T * 4);
     rowpart = W.take<float>((size_t)T * row_tiles * 4);
@@ -652,9 +690,13 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
   K.weights = A.weights;
   K.vec = whole_quads(A.x, A.ldx, A.dtype);
   K.terms = XP;
-  K.Kp = Kp;
+  K.Kp = Kx;
   K.tp = tp;
-  H_LAUNCH(head_token_kernel, ((unsigned)up16(T)), 256, K);
+  K.frags = few;
+  K.raw = in_place && A.dtype == DT_BF16;
+  K.ones = few && !weights ? ones : nullptr;
+  const uint32_t* rowmax = K.raw ? nullptr : K.rowmax;
+  H_LAUNCH(head_token_kernel, ((unsigned)(up16(T) + (K.ones ? (V + 255) / 256 : 0))), 256, K);
   if (product) {
     H_LAUNCH(head_colmax_kernel, ((unsigned)(ttiles * ((n + 63) / 64))), 256, K);
     H_LAUNCH(head_token_t_kernel, ((unsigned)(ttiles * ((n + 63) / 64))), 256, K);
@@ -667,12 +709,13 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
   P.targets = A.targets;
   P.target_z = K.target_z;
   P.row_top = row_top; P.row_scale = row_scale; P.row_target = row_target;
-  P.gmax = K.gmax; P.fmax = fmax;
+  P.gmax = K.gmax; P.fmax = reinterpret_cast<const float*>(fmax);
   P.dmax = dmax;
   P.terms_d = DX; P.terms_t = DT;
   P.tp = tp;
   P.levels = L.levels;
-  P.mid = !weights && (L.fmt == QF_NIB || L.fmt == QF_BYTE) ? L.K / 2 : -1;
+  P.centre = !weights && (L.fmt == QF_NIB || L.fmt == QF_BYTE) ? L.K / 2 : -1;
+  P.mid = few ? -1 : P.centre;
   QLayer Q;
   // The piece's rows, and its planes: for the logits, or the transpose.
   auto piece = [&](int64_t k, bool logits, bool transposed) -> hipError_t {
@@ -687,8 +730,8 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
     P.a = weights ? nullptr : Q.scale;
     P.o = weights ? nullptr : Q.offset;
     P.b = A.bias ? A.bias + r0 : nullptr;
-    P.refs = weights ? refs + r0 : nullptr;
-    P.part = part + k * segs * T;
+    P.refs = weights ? refs + r0 : nullptr;      // (of the planes that dz meets; in_place: not of the logits')
+    P.part = part + r0 / tile.rows * T;
     if (A.dense) {
       DenseArgs D;
       memset(&D, 0, sizeof(D));
@@ -701,39 +744,80 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
       D.refs = refs + r0;
       D.out = wp; D.plane = plane;
       D.t = wt; D.plane_t = up16(n) * mp;
-      if (logits) H_LAUNCH(head_dense_kernel, ((unsigned)up16(nr)), 256, D);
+      if (logits && !in_place) H_LAUNCH(head_dense_kernel, ((unsigned)up16(nr)), 256, D);
+      if (transposed && in_place) H_LAUNCH(head_rowmax_kernel, ((unsigned)((nr + 3) / 4)), 256, D);
       if (transposed) H_LAUNCH(head_dense_t_kernel, ((unsigned)(mp / 64 * ((n + 63) / 64))), 256, D);
     } else {
       if (weights && logits) H_TRY(launch_q_bounds(Q, refs + r0, st));
       if (logits) H_TRY(launch_q_unpack(Q, Kp, weights ? WP : 0, refs + r0, wp, plane, st));
-      if (transposed) H_TRY(launch_q_unpack_t(Q, mp, weights ? WP : 0, refs + r0, wt, up16(n) * mp, st));
+      if (transposed) H_TRY(launch_q_unpack_t(Q, mp, weights ? WX : 0, refs + r0, wt, up16(n) * mp, st));
     }
     gz.A = wp; gz.planeA = plane;
+    if (in_place) {
+      gz.A = reinterpret_cast<const uint16_t*>(static_cast<const char*>(A.W) + r0 * A.ldw * 2);
+      gz.lda = A.ldw;
+      gz.bf16 = A.dtype == DT_BF16;
+    }
     gz.B = K.planes; gz.planeB = K.plane;
     gz.M = nr; gz.N = T; gz.K = Kp;
     return hipSuccess;
   };
-  for (int64_t k = 0; k < pieces; ++k) {
+  if (few) {
+    QLayer F = L;
+    if (!weights) {
+      F.scale = ones;
+      F.offset = nullptr;
+    }
+    QOut O;
+    memset(&O, 0, sizeof(O));
+    O.y = S; O.ldy = lds;
+    O.rowmax = rowmax;
+    O.mid = -1;
+    O.dtype = DT_F32;
+    O.vec = 1;
+    O.rows = T; O.cols = V;
+    H_TRY(launch_q_skinny(F, K.planes, 0, K.plane, T, XP, false, O, st));
+  }
+  for (int64_t k = 0; k < pieces && !few; ++k) {
     H_TRY(piece(k, true, false));
+    P.refs = in_place ? nullptr : P.refs;
     if (kept) {
       gz.O.y = S + P.row0; gz.O.ldy = lds;
-      gz.O.rowmax = K.rowmax;
+      gz.O.rowmax = rowmax;
       gz.O.colmax = P.refs;
       gz.O.mid = -1;
       gz.O.dtype = DT_F32;
       gz.O.vec = 1;
       gz.O.rows = T; gz.O.cols = P.m;
       H_TRY(launch_q_gemm(gz, gpart, st));
-      H_LAUNCH(head_stats_kernel, ((unsigned)T, (unsigned)((P.m + H_SEG - 1) / H_SEG)), 256, P);
     } else {
-      H_TRY(launch_head_gemm(gz, P, K.rowmax, false, st));
+      H_TRY(launch_head_gemm(gz, P, rowmax, false, st));
     }
   }
-  // (the last piece may have fewer segments)
-  const int64_t all_segs = (pieces - 1) * segs + (last + seg - 1) / seg;
+  if (kept) {
+    PieceArgs F = P;   // all of it
+    F.m = V;
+    F.row0 = 0;
+    F.S = S;
+    F.a = weights ? nullptr : L.scale;
+    F.o = weights ? nullptr : L.offset;
+    F.b = A.bias;
+    F.part = part;
+    if (seg == 1024) H_LAUNCH(head_stats_kernel<1>, ((unsigned)T, (unsigned)all_segs), 256, F);
+    else H_LAUNCH(head_stats_kernel<4>, ((unsigned)T, (unsigned)all_segs), 256, F);
+  }
   H_LAUNCH(head_join_kernel, ((unsigned)((T + 15) / 16)), 256, part, all_segs, T, K.weight, K.target_z, A.loss, row_top, row_scale,
            row_target, K.gmax);
   if (!grads) return hipSuccess;
+  // (a matrix in place has its rows' maxima with the transposes)
+  if (A.need_dx && !in_place) {
+    PieceArgs F = P;
+    F.m = V;
+    F.refs = weights ? refs : nullptr;
+    F.a = weights ? nullptr : L.scale;
+    if (few && weights) H_TRY(launch_q_bounds(L, refs, st));
+    H_LAUNCH(head_factor_kernel, ((unsigned)std::min<int64_t>((V + 255) / 256, 64)), 256, F, fmax);
+  }
   for (int64_t k = 0; k < pieces; ++k) {
     H_TRY(piece(k, !kept, A.need_dx));
     const int64_t r0 = P.row0, nr = P.m, mp = P.mp;
@@ -741,11 +825,12 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
     P.rowpart = sums ? rowpart : nullptr;
     P.dt = product ? dt : nullptr;
     P.colpart = A.need_dhead ? colpart : nullptr;
-    if (A.need_dx) H_LAUNCH(head_factor_kernel, (1), 1024, P, fmax);
+    if (A.need_dx && in_place)
+      H_LAUNCH(head_factor_kernel, ((unsigned)std::min<int64_t>((nr + 255) / 256, 64)), 256, P, fmax);
     if (kept)
       H_LAUNCH(head_grad_kernel, ((unsigned)(mp / 64 * ttiles)), 256, P);
     else
-      H_TRY(launch_head_gemm(gz, P, K.rowmax, true, st));
+      H_TRY(launch_head_gemm(gz, P, rowmax, true, st));
     const HeadTile own = head_tile(nr, T);   // (of the last piece, smaller)
     if (A.need_dhead)
       H_LAUNCH(head_colsum_kernel, ((unsigned)((nr + 255) / 256)), 256, colpart,

@@ -58,7 +58,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void head_gemm_kernel(QGemm g, Pie
       o = A.a ? fmaf(a, mid, A.o ? A.o[i] : 0.f) : 0.f;
       b = A.b ? A.b[i] : 0.f;
       f = a;
-      if (A.refs) a = f = pow2(-pow2_shift(A.refs[i]));
+      if (A.refs) {
+        f = pow2(-pow2_shift(A.refs[i]));
+        if (!AROWS) a = f;   // (rows read in place are what they are)
+      }
     }
     ca[k] = a;
     co[k] = o;
@@ -214,7 +217,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void head_gemm_kernel(QGemm g, Pie
   }
 }
 
-template <typename T, bool GRADS, bool AROWS>
+template <typename T, bool AROWS, bool GRADS>
 hipError_t launch(const QGemm& g, const PieceArgs& A, const uint32_t* rowmax, hipStream_t st) {
   const HeadTile tile = head_tile(g.M, g.N);
   const unsigned tiles = (unsigned)(((g.M + tile.rows - 1) / tile.rows) * ((g.N + tile.tokens - 1) / tile.tokens));
@@ -224,6 +227,10 @@ hipError_t launch(const QGemm& g, const PieceArgs& A, const uint32_t* rowmax, hi
     hipLaunchKernelGGL((head_gemm_kernel<T, 256, 128, 4, 2, GRADS, AROWS>), dim3(tiles), dim3(512), 0, st, g, A, rowmax);
   return hipGetLastError();
 }
+template <typename T, bool AROWS>
+hipError_t pick(const QGemm& g, const PieceArgs& A, const uint32_t* rowmax, bool grads, hipStream_t st) {
+  return grads ? launch<T, AROWS, true>(g, A, rowmax, st) : launch<T, AROWS, false>(g, A, rowmax, st);
+}
 
 }  // namespace
 
@@ -232,7 +239,8 @@ HeadTile head_tile(int64_t m, int64_t t) { return {256, (m + 255) / 256 * ((t + 
 
 hipError_t launch_head_gemm(const QGemm& g, const PieceArgs& A, const uint32_t* rowmax, bool grads, hipStream_t st) {
   if (g.K % BK != 0 || g.K <= 0) return hipErrorInvalidValue;
-  return grads ? launch<OpF16, true, false>(g, A, rowmax, st) : launch<OpF16, false, false>(g, A, rowmax, st);
+  if (!g.lda) return pick<OpF16, false>(g, A, rowmax, grads, st);
+  return g.bf16 ? pick<OpBf16, true>(g, A, rowmax, grads, st) : pick<OpF16, true>(g, A, rowmax, grads, st);
 }
 
 }  // namespace mpq

@@ -425,8 +425,7 @@ __device__ __forceinline__ int64_t q_at(int64_t row, int64_t k, int64_t K) {
   return ((row >> 4) * (K >> 5) + (k >> 5)) * 512 + (row & 15) * 32 + (k & 31);
 }
 struct QGemm {
-  const uint16_t* A; int64_t planeA;        // operand order (lda: of the tile loop that reads it in rows)
-  int64_t lda;
+  const uint16_t* A; int64_t lda, planeA;   // operand order (lda = 0), or rows, as B's
   const uint16_t* B; int64_t ldb, planeB;   // operand order (ldb = 0), or rows
   int64_t M, N, K;        // columns i, rows j, depth of one plane
   int npairs;
@@ -450,9 +449,10 @@ hipError_t launch_q_gemm(const QGemm& g, float* part, hipStream_t st);
 // The product with few rows (qskinny.hip): x in place (16-bit rows of ldx > 0
 // elements, 16-byte aligned, n a multiple of 8), or in operand order (ldx = 0):
 // planes of whole chunks, 16 rows by 16 rows, each step's 64 lanes x 16 bytes
-// together.  Two planes: float16, with O.rowmax.  Column groups need chunks that
+// together.  Two planes: float16, with O.rowmax (one float16 plane: with or without).  Column groups need chunks that
 // lie in one group.
 bool q_skinny_ok(const QLayer& L);
+bool q_few_rows(const QLayer& L, int dtype, int64_t t);   // whether a product of t rows should take it (qlinear.hip)
 hipError_t launch_q_skinny(const QLayer& L, const uint16_t* x, int64_t ldx, int64_t planex, int64_t t, int planes,
                            bool bf16, const QOut& O, hipStream_t st);
 

@@ -669,13 +669,14 @@ hipError_t unpack_t(const QLayer& L, int64_t mp, int planes, const uint32_t* ref
 // workspace's size knows the codes, not the codebook, and planes take 128 MB.
 constexpr int64_t Q_SMALL_TOKENS = 1024, Q_SMALL_WORK = 3ll << 27;
 
-bool use_skinny(const QLinearArgs& A) {
-  if (!q_skinny_ok(A.L)) return false;
-  if (A.t <= Q_SMALL_TOKENS && A.t * A.L.m * A.L.n <= Q_SMALL_WORK) return true;
-  const bool scalar = A.L.fmt == QF_NIB || A.L.fmt == QF_BYTE, grouped = A.L.G > 1;
-  if (A.dtype == DT_F32) return A.t <= (grouped ? 192 : 96);
-  return A.t <= (grouped && A.dtype == DT_F16 ? 384 : scalar ? 192 : 128);
+bool few_rows(const QLayer& L, int dtype, int64_t t) {
+  if (!q_skinny_ok(L)) return false;
+  if (t <= Q_SMALL_TOKENS && t * L.m * L.n <= Q_SMALL_WORK) return true;
+  const bool scalar = L.fmt == QF_NIB || L.fmt == QF_BYTE, grouped = L.G > 1;
+  if (dtype == DT_F32) return t <= (grouped ? 192 : 96);
+  return t <= (grouped && dtype == DT_F16 ? 384 : scalar ? 192 : 128);
 }
+bool use_skinny(const QLinearArgs& A) { return few_rows(A.L, A.dtype, A.t); }
 
 // Elements of x up to which the few-row product reads it in place.
 // Measured, in place | laid out first (E8): 4096 columns, 2 tokens 8.7 | 11.5 us,
@@ -993,6 +994,7 @@ hipError_t launch_q_zero_rows(void* p, int64_t rows, int64_t cols, int64_t ld, i
   return hipGetLastError();
 }
 
+bool q_few_rows(const QLayer& L, int dtype, int64_t t) { return few_rows(L, dtype, t); }
 hipError_t launch_q_unpack(const QLayer& L, int64_t Kp, int planes, const uint32_t* refs, uint16_t* out, int64_t plane,
                            hipStream_t st) {
   return unpack<OpF16>(L, 0, L.tiles, Kp, planes, refs, out, plane, st);

@@ -339,7 +339,7 @@ __global__ __launch_bounds__(64 * sk_waves(XP, NT, R, GROUPED)) void q_skinny_ke
       if (more) __syncthreads();
     }
     if (live > 0) {
-      if (XP > 1) {
+      if (A.O.rowmax) {
         const float f = pow2(-pow2_shift(A.O.rowmax[tok]));
 #pragma unroll
         for (int k = 0; k < 4; ++k) mine[k] *= f;

@@ -11,7 +11,7 @@ is the sum of (e' the entry less the middle level, o' the offset with it):
     slope `rest` (1 less the target's probability): w rest (2 d_t + 2^-18), and one
     rounding; twice that covers the second order;
   - dz: relative 2 d_t + 2^-16 (|z - max| below 100);
-  - dx: dz's, its terms (2^-11 for one, 2^-20 for two and for two of the weights),
+  - dx: dz's, its terms and those of the weights of groups (2^-11 for one, 2^-20 for two),
     elements below 2^-28 of the row's bound 2^-39 of it, float32 sums over the
     vocabulary (V / 16 + 32) 2^-22, one rounding of the result;
   - the head's gradients: dz's, s's own d_t, sums of 64 tokens (2^-19); of a matrix and
@@ -85,7 +85,7 @@ def check(got, ref, dtype, n, exact_terms, kind, head=None, need_dx=True, need_d
     bound = adz.amax(1)
     if need_dx:
         M, E = adz @ ref["A"], ddz @ ref["A"]
-        terms = (2.0 ** -11 if half else 2.0 ** -20) + (2.0 ** -20 if kind == "groups" or not half else 0.0)
+        terms = 2.0 ** -11 * (2 if kind == "groups" else 1) if half else 2.0 ** -19
         low = 2.0 ** -38 * (bound[:, None] * ref["A"].sum(0)[None] * (head["spread"] if head and "spread" in head else 1.0))
         tol = E + terms * M + low + (V / 16 + 32) * 2.0 ** -22 * M
         within("dx", got["dx"], ref["dz"] @ ref["W"], tol + step * ((ref["dz"] @ ref["W"]).abs() + tol) + tiny)
@@ -247,6 +247,10 @@ def test_pieces(dtype):
     packed_case("s16", 2100, 96, 33000, dtype, group=32, seed=3)
     packed_case("e8240", 1500, 40, 33000, dtype, seed=4, offset=False)
     packed_case("s16", 2500, 40960, 5, dtype, seed=5)
+    packed_case("s16", 2500, 40960, 300, dtype, seed=6)
+    matrix_case(2600, 128, 33000, dtype, padded=True, seed=7)
+    matrix_case(2500, 40960, 300, dtype, seed=8)
+    matrix_case(2570, 64, 33000, dtype, pad=1, seed=9)
 
 
 def test_rows_of_very_different_scales():
