@@ -144,6 +144,7 @@ bool head_fits(const HeadArgs& A) {
 // Enough for every combination of outputs.
 size_t head_bytes(HeadArgs A) {
   A.need_dx = A.need_dhead = true;
+  A.t = std::max<int64_t>(A.t, 1);
   const size_t b = head_workspace(A);
   return b > ALIGN ? b : ALIGN;
 }

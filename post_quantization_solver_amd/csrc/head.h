@@ -39,6 +39,7 @@ struct PieceArgs {
   const uint32_t* refs;            // the weights' planes' factors (nullptr: a is dz's factor)
   uint32_t* dmax;                  // the bound that a token's d is scaled by
   uint16_t* d; int64_t plane_d, mp; int terms_d;    // dz times its factors: t rows of mp (nullptr: none)
+  bool raw_d;                      // dz itself in bfloat16, the target's left out
   float* rowpart;                  // t x (mp / 64): sums of dz o' (nullptr: none)
   uint16_t* dt; int64_t plane_t, tp; int terms_t;   // dz^T: m rows of tp (nullptr: none)
   float* colpart;                  // (tp / 64) x 3 x m: sums of dz, dz s, dz X (nullptr: none)
@@ -53,6 +54,13 @@ __device__ __forceinline__ void put_terms(uint16_t* p, int64_t plane, int planes
   *reinterpret_cast<uint2*>(p) = make_uint2(pack2(b[0][0], b[1][0]), pack2(b[2][0], b[3][0]));
   if (planes > 1)
     *reinterpret_cast<uint2*>(p + plane) = make_uint2(pack2(b[0][1], b[1][1]), pack2(b[2][1], b[3][1]));
+}
+// Four values of dz times their factors as d's operand.
+__device__ __forceinline__ void put_dz(const PieceArgs& A, int64_t t, int64_t i, const float* u) {
+  if (A.raw_d)
+    *reinterpret_cast<uint2*>(A.d + q_at(t, i, A.mp)) = make_uint2(OpBf16::pack(u[0], u[1]), OpBf16::pack(u[2], u[3]));
+  else
+    put_terms(A.d + q_at(t, i, A.mp), A.plane_d, A.terms_d, u);
 }
 // Over the sixteen lanes of a row.
 __device__ __forceinline__ float sum16(float s) {
@@ -72,6 +80,13 @@ struct HeadTile {
 };
 HeadTile head_tile(int64_t m, int64_t t);
 hipError_t launch_head_gemm(const QGemm& g, const PieceArgs& A, const uint32_t* rowmax, bool grads, hipStream_t st);
+
+// dx's sums over the pieces, `splits` of t x ldo (a piece has `rows` rows, the last may
+// have fewer): added to, but for the first piece.  g: the planes of the head with their
+// rows as depth (g.arows of them), dz.
+int head_dx_splits(int64_t n, int64_t t, int64_t rows, int npairs);
+hipError_t launch_head_dx(const QGemm& g, const uint32_t* rowmax, float* out, int64_t ldo, int64_t rows, bool first,
+                          hipStream_t st);
 
 size_t head_workspace(const HeadArgs& A);
 hipError_t launch_head(const HeadArgs& A, void* ws, hipStream_t st);

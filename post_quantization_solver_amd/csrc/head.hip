@@ -208,11 +208,10 @@ struct DenseArgs {
   const void* W; int64_t ldw;
   int dtype;
   bool vec;
-  int64_t m, n, Kp, mp;
+  int64_t m, n, Kp;
   int terms;
   uint32_t* refs;                 // rows' largest magnitudes
   uint16_t* out; int64_t plane;   // m rows of Kp
-  uint16_t* t; int64_t plane_t;   // the transpose, n rows of mp (nullptr: none)
 };
 
 // Rows' largest magnitudes and planes: a workgroup per row of the planes.
@@ -247,51 +246,6 @@ __global__ __launch_bounds__(256) void head_dense_kernel(DenseArgs A) {
     put_terms(A.out + q_at(row, j + 4, A.Kp), A.plane, A.terms, v + 4);
   }
 }
-// Rows' largest magnitudes alone, a wave each.
-__global__ __launch_bounds__(256) void head_rowmax_kernel(DenseArgs A) {
-  const int lane = threadIdx.x & 63;
-  const int64_t row = (int64_t)blockIdx.x * 4 + wave_id();
-  if (row >= A.m) return;
-  uint32_t top = 0;
-#pragma unroll 4
-  for (int64_t j = lane * 8; j < A.n; j += 64 * 8) {
-    const int have = (int)min((int64_t)8, A.n - j);
-    float v[8];
-    load4(A.W, row * A.ldw + j, A.dtype, A.vec, min(have, 4), v);
-    load4(A.W, row * A.ldw + j + 4, A.dtype, A.vec, max(have - 4, 0), v + 4);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) top = max(top, abs_bits(v[k]));
-  }
-  for (int o = 32; o; o >>= 1) top = max(top, (uint32_t)shfl_xor_i((int)top, o));
-  if (lane == 0) A.refs[row] = top;
-}
-// The transpose, tiles of 64 x 64.
-__global__ __launch_bounds__(256) void head_dense_t_kernel(DenseArgs A) {
-  __shared__ float tl[64][65];
-  const int cx = threadIdx.x & 15, ry = threadIdx.x >> 4;
-  const int64_t tiles = (A.n + 63) / 64, r0 = blockIdx.x / tiles * 64, j0 = blockIdx.x % tiles * 64, j = j0 + cx * 4;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int64_t r = r0 + ry + 16 * k;
-    float v[4] = {0.f, 0.f, 0.f, 0.f};
-    const int live = r < A.m ? (int)max((int64_t)0, min((int64_t)4, A.n - j)) : 0;
-    const float f = r < A.m ? pow2(pow2_shift(A.refs[r])) : 1.f;
-    if (live) load4(A.W, r * A.ldw + j, A.dtype, A.vec, live, v);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) tl[ry + 16 * k][cx * 4 + q] = v[q] * f;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int64_t c = j0 + ry + 16 * k;
-    if (c >= A.n) continue;
-    float v[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) v[q] = tl[cx * 4 + q][ry + 16 * k];
-    put_terms(A.t + q_at(c, r0 + cx * 4, A.mp), A.plane_t, A.terms, v);
-  }
-}
-
 // ------------------------------------------------------------------ a piece's logits
 
 struct Col4 {
@@ -466,12 +420,12 @@ __global__ __launch_bounds__(256) void head_grad_kernel(PieceArgs A) {
         const float g = pow2(pow2_shift(bound));
         float u[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) u[q] = v[q] * f[q] * g;
-        put_terms(A.d + q_at(t, i, A.mp), A.plane_d, A.terms_d, u);
+        for (int q = 0; q < 4; ++q) u[q] = !A.raw_d ? v[q] * f[q] * g : i + q == target ? 0.f : v[q];
+        put_dz(A, t, i, u);
       }
     } else if (A.d && t < A.t) {
       if (blockIdx.x % tiles == 0 && cx == 0) A.dmax[t] = 0;
-      put_terms(A.d + q_at(t, i, A.mp), A.plane_d, A.terms_d, v);
+      put_dz(A, t, i, v);
     }
     if (A.rowpart) {
       const float s = sum16(fmaf(v[0], od[0], v[1] * od[1]) + fmaf(v[2], od[2], v[3] * od[3]));
@@ -541,16 +495,34 @@ __global__ __launch_bounds__(256) void head_fill_kernel(uint32_t* __restrict__ o
   if (i < n) out[i] = *v;
 }
 
-// dx from its sum over the pieces.
-__global__ __launch_bounds__(256) void head_dx_kernel(const float* __restrict__ acc, int64_t lda, int64_t T, int64_t n,
-                                                      const float* __restrict__ rowadd, void* __restrict__ dx, int64_t ld,
-                                                      int dtype, bool vec) {
+// dx from its sums over the pieces, and the targets' terms where W is given: -w rest W[r],
+// the largest of a token's, would carry bfloat16's rounding of dz into all of its row.
+struct TargetTerms {
+  const uint16_t* W; int64_t ldw, V;
+  const int32_t* targets;
+  const float *weight, *row_target;
+};
+__global__ __launch_bounds__(256) void head_dx_kernel(const float* __restrict__ acc, int splits, int64_t lda, int64_t T, int64_t n,
+                                                      const float* __restrict__ rowadd, TargetTerms R, void* __restrict__ dx,
+                                                      int64_t ld, int dtype, bool vec) {
   const int64_t quads = (n + 3) / 4, step = (int64_t)gridDim.x * 256;
   for (int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x; k < T * quads; k += step) {
     const int64_t t = k / quads, j = (k - t * quads) * 4;
-    const float4 s = *reinterpret_cast<const float4*>(acc + t * lda + j);
     const float add = rowadd ? rowadd[t] : 0.f;
-    const float v[4] = {s.x + add, s.y + add, s.z + add, s.w + add};
+    float v[4] = {add, add, add, add};
+    for (int s = 0; s < splits; ++s) {
+      const float4 q = *reinterpret_cast<const float4*>(acc + ((int64_t)s * T + t) * lda + j);
+      v[0] += q.x;
+      v[1] += q.y;
+      v[2] += q.z;
+      v[3] += q.w;
+    }
+    if (R.W && R.weight[t] != 0.f && R.targets[t] < R.V) {   // (n is a multiple of 64)
+      float w[4];
+      load4(R.W, R.targets[t] * R.ldw + j, DT_BF16, true, 4, w);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] = fmaf(R.row_target[t], w[q], v[q]);
+    }
     store4(dx, t * ld + j, dtype, vec, (int)min((int64_t)4, n - j), v);
   }
 }
@@ -646,22 +618,21 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
     f(V - (pieces - 1) * rows);
   };
   if (kept) both_sizes([&](int64_t nr) { ps = std::max(ps, q_gemm_workspace(nr, T, Kp, gz.npairs)); });
-  uint16_t *wt = nullptr, *d = nullptr, *dt = nullptr;
+  uint16_t *d = nullptr, *dt = nullptr;
   uint32_t *dmax = nullptr, *tmax = nullptr;
   float *rowpart = nullptr, *rowadd = nullptr, *acc = nullptr, *colpart = nullptr, *dW = nullptr;
   float2* cpart = nullptr;
   const int64_t lda = (n + 3) / 4 * 4, cblocks = (n + Q_CONTRACT - 1) / Q_CONTRACT;
-  int splits = 1;
+  int splits = 1, dx_splits = 1;
   // (workspaces are sized without the offset's pointer: room for its sums either way)
   const bool sums = A.need_dx && !weights && L.has_offset();
   if (A.need_dx) {
-    wt = W.take<uint16_t>((size_t)WX * up16(n) * rows * 2);
     d = W.take<uint16_t>((size_t)DX * up16(T) * rows * 2);
     dmax = W.take<uint32_t>((size_t)T * 4);
     rowpart = W.take<float>((size_t)T * row_tiles * 4);
     rowadd = W.take<float>((size_t)T * 4);
-    if (pieces > 1) acc = W.take<float>((size_t)T * lda * 4);
-    both_sizes([&](int64_t nr) { ps = std::max(ps, q_gemm_workspace(n, T, up64(nr), gx.npairs)); });
+    dx_splits = head_dx_splits(n, T, rows, gx.npairs);
+    acc = W.take<float>((size_t)dx_splits * T * lda * 4);
   }
   if (A.need_dhead) colpart = W.take<float>((size_t)token_tiles * 3 * rows * 4);
   if (product) {
@@ -717,40 +688,36 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
   P.centre = !weights && (L.fmt == QF_NIB || L.fmt == QF_BYTE) ? L.K / 2 : -1;
   P.mid = few ? -1 : P.centre;
   QLayer Q;
-  // The piece's rows, and its planes: for the logits, or the transpose.
-  auto piece = [&](int64_t k, bool logits, bool transposed) -> hipError_t {
-    const int64_t r0 = k * rows, nr = std::min(rows, V - r0), plane = up16(nr) * Kp, mp = up64(nr);
+  // The piece's rows, and its planes.
+  auto piece = [&](int64_t k, bool planes) -> hipError_t {
+    const int64_t r0 = k * rows, nr = std::min(rows, V - r0), plane = up16(nr) * Kp;
     Q = layer_rows(L, r0, nr);
     P.m = nr;
     P.row0 = r0;
-    P.mp = mp;
-    P.plane_d = up16(T) * mp;
+    P.mp = up64(nr);
+    P.plane_d = up16(T) * P.mp;
     P.plane_t = up16(nr) * tp;
     P.S = S + r0;
     P.a = weights ? nullptr : Q.scale;
     P.o = weights ? nullptr : Q.offset;
     P.b = A.bias ? A.bias + r0 : nullptr;
-    P.refs = weights ? refs + r0 : nullptr;      // (of the planes that dz meets; in_place: not of the logits')
+    P.refs = weights && !in_place ? refs + r0 : nullptr;
     P.part = part + r0 / tile.rows * T;
-    if (A.dense) {
+    if (planes && A.dense && !in_place) {
       DenseArgs D;
       memset(&D, 0, sizeof(D));
       D.W = static_cast<const char*>(A.W) + r0 * A.ldw * (f32 ? 4 : 2);
       D.ldw = A.ldw;
       D.dtype = A.dtype;
       D.vec = whole_quads(D.W, D.ldw, A.dtype);
-      D.m = nr; D.n = n; D.Kp = Kp; D.mp = mp;
+      D.m = nr; D.n = n; D.Kp = Kp;
       D.terms = WP;
       D.refs = refs + r0;
       D.out = wp; D.plane = plane;
-      D.t = wt; D.plane_t = up16(n) * mp;
-      if (logits && !in_place) H_LAUNCH(head_dense_kernel, ((unsigned)up16(nr)), 256, D);
-      if (transposed && in_place) H_LAUNCH(head_rowmax_kernel, ((unsigned)((nr + 3) / 4)), 256, D);
-      if (transposed) H_LAUNCH(head_dense_t_kernel, ((unsigned)(mp / 64 * ((n + 63) / 64))), 256, D);
-    } else {
-      if (weights && logits) H_TRY(launch_q_bounds(Q, refs + r0, st));
-      if (logits) H_TRY(launch_q_unpack(Q, Kp, weights ? WP : 0, refs + r0, wp, plane, st));
-      if (transposed) H_TRY(launch_q_unpack_t(Q, mp, weights ? WX : 0, refs + r0, wt, up16(n) * mp, st));
+      H_LAUNCH(head_dense_kernel, ((unsigned)up16(nr)), 256, D);
+    } else if (planes && !A.dense) {
+      if (weights) H_TRY(launch_q_bounds(Q, refs + r0, st));
+      H_TRY(launch_q_unpack(Q, Kp, weights ? WP : 0, refs + r0, wp, plane, st));
     }
     gz.A = wp; gz.planeA = plane;
     if (in_place) {
@@ -779,8 +746,7 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
     H_TRY(launch_q_skinny(F, K.planes, 0, K.plane, T, XP, false, O, st));
   }
   for (int64_t k = 0; k < pieces && !few; ++k) {
-    H_TRY(piece(k, true, false));
-    P.refs = in_place ? nullptr : P.refs;
+    H_TRY(piece(k, true));
     if (kept) {
       gz.O.y = S + P.row0; gz.O.ldy = lds;
       gz.O.rowmax = rowmax;
@@ -809,24 +775,24 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
   H_LAUNCH(head_join_kernel, ((unsigned)((T + 15) / 16)), 256, part, all_segs, T, K.weight, K.target_z, A.loss, row_top, row_scale,
            row_target, K.gmax);
   if (!grads) return hipSuccess;
-  // (a matrix in place has its rows' maxima with the transposes)
-  if (A.need_dx && !in_place) {
+  P.raw_d = K.raw;
+  if (A.need_dx && !P.raw_d) {
     PieceArgs F = P;
-    F.m = V;
-    F.refs = weights ? refs : nullptr;
+    F.m = in_place ? 1 : V;   // (1 for every row)
+    F.refs = weights && !in_place ? refs : nullptr;
     F.a = weights ? nullptr : L.scale;
     if (few && weights) H_TRY(launch_q_bounds(L, refs, st));
-    H_LAUNCH(head_factor_kernel, ((unsigned)std::min<int64_t>((V + 255) / 256, 64)), 256, F, fmax);
+    H_LAUNCH(head_factor_kernel, ((unsigned)std::min<int64_t>((F.m + 255) / 256, 64)), 256, F, fmax);
   }
+  // (a single piece's planes are still there)
+  const bool again = pieces > 1 || few;
   for (int64_t k = 0; k < pieces; ++k) {
-    H_TRY(piece(k, !kept, A.need_dx));
+    H_TRY(piece(k, again && (!kept || A.need_dx)));
     const int64_t r0 = P.row0, nr = P.m, mp = P.mp;
     P.d = A.need_dx ? d : nullptr;
     P.rowpart = sums ? rowpart : nullptr;
     P.dt = product ? dt : nullptr;
     P.colpart = A.need_dhead ? colpart : nullptr;
-    if (A.need_dx && in_place)
-      H_LAUNCH(head_factor_kernel, ((unsigned)std::min<int64_t>((nr + 255) / 256, 64)), 256, P, fmax);
     if (kept)
       H_LAUNCH(head_grad_kernel, ((unsigned)(mp / 64 * ttiles)), 256, P);
     else
@@ -839,23 +805,12 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
     if (sums) H_LAUNCH(head_rowsum_kernel, ((unsigned)((T + 3) / 4)), 256, rowpart,
                        kept ? mp / 64 : (nr + own.rows - 1) / own.rows, T, k == 0, rowadd);
     if (A.need_dx) {
-      gx.A = wt; gx.planeA = up16(n) * mp;
+      gx.A = gz.A; gx.lda = gz.lda; gx.planeA = gz.planeA;
+      gx.bf16 = gz.bf16;
+      gx.acols = Kp; gx.arows = nr;
       gx.B = d; gx.planeB = P.plane_d;
       gx.M = n; gx.N = T; gx.K = mp;
-      gx.O.y = acc; gx.O.ldy = lda;
-      gx.O.res = k > 0 ? acc : nullptr; gx.O.ldres = lda;
-      gx.O.rowmax = dmax;
-      gx.O.mid = -1;
-      gx.O.dtype = DT_F32;
-      gx.O.vec = 1;
-      gx.O.rows = T; gx.O.cols = n;
-      if (pieces == 1) {
-        gx.O.y = A.dx; gx.O.ldy = A.lddx;
-        gx.O.rowadd = sums ? rowadd : nullptr;
-        gx.O.dtype = A.dtype;
-        gx.O.vec = whole_quads(A.dx, A.lddx, A.dtype);
-      }
-      H_TRY(launch_q_gemm(gx, gpart, st));
+      H_TRY(launch_head_dx(gx, P.raw_d ? nullptr : dmax, acc, lda, rows, k == 0, st));
     }
     if (product) {
       H_LAUNCH(head_fill_kernel, ((unsigned)((nr + 255) / 256)), 256, tmax, nr, K.gmax);
@@ -884,9 +839,10 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
       }
     }
   }
-  if (A.need_dx && pieces > 1)
-    H_LAUNCH(head_dx_kernel, ((unsigned)std::min<int64_t>((T * (lda / 4) + 255) / 256, 4096)), 256, acc, lda, T, n,
-             sums ? rowadd : nullptr, A.dx, A.lddx, A.dtype, whole_quads(A.dx, A.lddx, A.dtype));
+  const TargetTerms R = {P.raw_d ? static_cast<const uint16_t*>(A.W) : nullptr, A.ldw, V, A.targets, K.weight, row_target};
+  if (A.need_dx)
+    H_LAUNCH(head_dx_kernel, ((unsigned)std::min<int64_t>((T * (lda / 4) + 255) / 256, 4096)), 256, acc, dx_splits, lda, T, n,
+             sums ? rowadd : nullptr, R, A.dx, A.lddx, A.dtype, whole_quads(A.dx, A.lddx, A.dtype));
   return hipSuccess;
 }
 

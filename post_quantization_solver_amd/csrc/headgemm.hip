@@ -36,7 +36,7 @@ __device__ __forceinline__ void transpose_quads(float* v, int lane) {
   }
 }
 
-template <typename T, int BM, int BN, int WM, int WN, bool GRADS, bool AROWS>
+template <typename T, int BM, int BN, int WM, int WN, bool GRADS, int AMODE>
 __global__ __launch_bounds__(64 * WM * WN, 2) void head_gemm_kernel(QGemm g, PieceArgs A, const uint32_t* __restrict__ rowmax) {
   constexpr int SM = BM / WM / 16, SN = BN / WN / 16;
   __shared__ __attribute__((aligned(1024))) uint16_t lds[gemm_stages(BM, BN)][(BM + BN) * BK];
@@ -45,7 +45,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void head_gemm_kernel(QGemm g, Pie
   int split;
   int64_t i0, j0;
   v4f acc[SM][SN];
-  q_gemm_tile<T, BM, BN, WM, WN, AROWS>(g, 1, lds, acc, split, i0, j0);
+  q_gemm_tile<T, BM, BN, WM, WN, AMODE>(g, 1, lds, acc, split, i0, j0);
   // The rows of the head: factor of s, of X, what is added; dz's factor.
   float* const cols = reinterpret_cast<float*>(lds);
   float *ca = cols, *co = cols + BM, *cb = cols + 2 * BM, *cf = cols + 3 * BM, *work = cols + 4 * BM;
@@ -60,7 +60,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void head_gemm_kernel(QGemm g, Pie
       f = a;
       if (A.refs) {
         f = pow2(-pow2_shift(A.refs[i]));
-        if (!AROWS) a = f;   // (rows read in place are what they are)
+        if (AMODE == A_BLOCKS) a = f;   // (rows read in place are what they are)
       }
     }
     ca[k] = a;
@@ -166,10 +166,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void head_gemm_kernel(QGemm g, Pie
           sums[0][k] += v[k];
           sums[1][k] = fmaf(v[k], fmaf(mid, X[jj], sv), sums[1][k]);
           sums[2][k] = fmaf(v[k], X[jj], sums[2][k]);
-          u[k] = v[k] * cd[k] * gd[jj];
+          u[k] = !A.raw_d ? v[k] * cd[k] * gd[jj] : target[jj] == s * 16 + k ? 0.f : v[k];
         }
         if (A.rowpart) rows[jj] += fmaf(v[0], o[0], v[1] * o[1]) + fmaf(v[2], o[2], v[3] * o[3]);
-        if (A.d && t < A.t && i < A.mp) put_terms(A.d + q_at(t, i, A.mp), A.plane_d, A.terms_d, u);
+        if (A.d && t < A.t && i < A.mp) put_dz(A, t, i, u);
         if (A.dt) {
           transpose_quads(v, lane);
 #pragma unroll
@@ -217,19 +217,85 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void head_gemm_kernel(QGemm g, Pie
   }
 }
 
-template <typename T, bool AROWS, bool GRADS>
+// dx's sum over the pieces: out[split][t][j] (+)= D[t][j] 2^-shift(rowmax[t]), the head's
+// planes with their rows as depth.  A split has a sum of its own, so that the largest
+// tile fills the CUs and nothing is joined before the end.
+template <typename T, int BM, int BN, int WM, int WN, int AMODE>
+__global__ __launch_bounds__(64 * WM * WN, 2) void head_dx_gemm_kernel(QGemm g, const uint32_t* __restrict__ rowmax,
+                                                                       float* __restrict__ out, int64_t ldo, int splits,
+                                                                       bool first) {
+  constexpr int SM = BM / WM / 16, SN = BN / WN / 16;
+  __shared__ __attribute__((aligned(1024))) uint16_t lds[gemm_stages(BM, BN)][(BM + BN) * BK];
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  const int wm = wave / WN, wn = wave % WN, r = lane & 15, kb = lane >> 4;
+  int split;
+  int64_t i0, j0;
+  v4f acc[SM][SN];
+  q_gemm_tile<T, BM, BN, WM, WN, AMODE>(g, splits, lds, acc, split, i0, j0);
+#pragma unroll
+  for (int jj = 0; jj < SN; ++jj) {
+    const int64_t t = j0 + (wn * SN + jj) * 16 + r;
+    if (t >= g.N) continue;
+    const float f = rowmax ? pow2(-pow2_shift(rowmax[t])) : 1.f;
+    float* row = out + ((int64_t)split * g.N + t) * ldo;
+    v4f old[SM];
+#pragma unroll
+    for (int s = 0; s < SM; ++s) {
+      const int64_t i = i0 + (wm * SM + s) * 16 + 4 * kb;
+      old[s] = (v4f){0.f, 0.f, 0.f, 0.f};
+      if (!first && i < ldo) old[s] = *reinterpret_cast<const v4f*>(row + i);
+    }
+#pragma unroll
+    for (int s = 0; s < SM; ++s) {
+      const int64_t i = i0 + (wm * SM + s) * 16 + 4 * kb;
+      if (i < ldo) *reinterpret_cast<v4f*>(row + i) = old[s] + acc[s][jj] * f;
+    }
+  }
+}
+
+struct DxPlan {
+  int tile;   // 0: 256 x 256, 1: 256 x 128, 2: 128 x 128
+  int64_t tiles;
+  int splits;
+};
+// The largest tile that fills three CUs in four with at most eight splits of sixteen steps
+// and more; each split writes and reads its sum once a piece.
+DxPlan dx_plan(int64_t n, int64_t T, int64_t steps) {
+  const int64_t bm[3] = {256, 256, 128}, bn[3] = {256, 128, 128};
+  DxPlan p;
+  for (p.tile = 0;; ++p.tile) {
+    p.tiles = (n + bm[p.tile] - 1) / bm[p.tile] * ((T + bn[p.tile] - 1) / bn[p.tile]);
+    const int64_t fill = p.tile == 2 ? 512 : 256;
+    p.splits = (int)std::max<int64_t>(1, std::min({(int64_t)8, fill / p.tiles, steps / 16}));
+    if (p.tile == 2 || p.tiles * p.splits >= 192) return p;
+  }
+}
+
+template <typename T, int AMODE>
+hipError_t launch_dx(const QGemm& g, const uint32_t* rowmax, float* out, int64_t ldo, const DxPlan& p, bool first, hipStream_t st) {
+  const dim3 grid((unsigned)(p.tiles * p.splits));
+  if (p.tile == 0)
+    hipLaunchKernelGGL((head_dx_gemm_kernel<T, 256, 256, 2, 4, AMODE>), grid, dim3(512), 0, st, g, rowmax, out, ldo, p.splits, first);
+  else if (p.tile == 1)
+    hipLaunchKernelGGL((head_dx_gemm_kernel<T, 256, 128, 4, 2, AMODE>), grid, dim3(512), 0, st, g, rowmax, out, ldo, p.splits, first);
+  else
+    hipLaunchKernelGGL((head_dx_gemm_kernel<T, 128, 128, 2, 2, AMODE>), grid, dim3(256), 0, st, g, rowmax, out, ldo, p.splits, first);
+  return hipGetLastError();
+}
+
+template <typename T, int AMODE, bool GRADS>
 hipError_t launch(const QGemm& g, const PieceArgs& A, const uint32_t* rowmax, hipStream_t st) {
   const HeadTile tile = head_tile(g.M, g.N);
   const unsigned tiles = (unsigned)(((g.M + tile.rows - 1) / tile.rows) * ((g.N + tile.tokens - 1) / tile.tokens));
   if (tile.tokens == 256)
-    hipLaunchKernelGGL((head_gemm_kernel<T, 256, 256, 2, 4, GRADS, AROWS>), dim3(tiles), dim3(512), 0, st, g, A, rowmax);
+    hipLaunchKernelGGL((head_gemm_kernel<T, 256, 256, 2, 4, GRADS, AMODE>), dim3(tiles), dim3(512), 0, st, g, A, rowmax);
   else
-    hipLaunchKernelGGL((head_gemm_kernel<T, 256, 128, 4, 2, GRADS, AROWS>), dim3(tiles), dim3(512), 0, st, g, A, rowmax);
+    hipLaunchKernelGGL((head_gemm_kernel<T, 256, 128, 4, 2, GRADS, AMODE>), dim3(tiles), dim3(512), 0, st, g, A, rowmax);
   return hipGetLastError();
 }
-template <typename T, bool AROWS>
+template <typename T, int AMODE>
 hipError_t pick(const QGemm& g, const PieceArgs& A, const uint32_t* rowmax, bool grads, hipStream_t st) {
-  return grads ? launch<T, AROWS, true>(g, A, rowmax, st) : launch<T, AROWS, false>(g, A, rowmax, st);
+  return grads ? launch<T, AMODE, true>(g, A, rowmax, st) : launch<T, AMODE, false>(g, A, rowmax, st);
 }
 
 }  // namespace
@@ -237,10 +303,20 @@ hipError_t pick(const QGemm& g, const PieceArgs& A, const uint32_t* rowmax, bool
 // As the product's own rule: 256 x 256 where that gives three CUs in four a workgroup.
 HeadTile head_tile(int64_t m, int64_t t) { return {256, (m + 255) / 256 * ((t + 255) / 256) >= 192 ? 256 : 128}; }
 
+int head_dx_splits(int64_t n, int64_t t, int64_t rows, int npairs) { return dx_plan(n, t, rows / BK * npairs).splits; }
+hipError_t launch_head_dx(const QGemm& g, const uint32_t* rowmax, float* out, int64_t ldo, int64_t rows, bool first,
+                          hipStream_t st) {
+  if (g.K % BK != 0 || g.K <= 0 || g.arows <= 0) return hipErrorInvalidValue;
+  const DxPlan p = dx_plan(g.M, g.N, rows / BK * g.npairs);
+  if (!g.lda) return launch_dx<OpF16, A_T_BLOCKS>(g, rowmax, out, ldo, p, first, st);
+  return g.bf16 ? launch_dx<OpBf16, A_T_ROWS>(g, rowmax, out, ldo, p, first, st)
+                : launch_dx<OpF16, A_T_ROWS>(g, rowmax, out, ldo, p, first, st);
+}
+
 hipError_t launch_head_gemm(const QGemm& g, const PieceArgs& A, const uint32_t* rowmax, bool grads, hipStream_t st) {
   if (g.K % BK != 0 || g.K <= 0) return hipErrorInvalidValue;
-  if (!g.lda) return pick<OpF16, false>(g, A, rowmax, grads, st);
-  return g.bf16 ? pick<OpBf16, true>(g, A, rowmax, grads, st) : pick<OpF16, true>(g, A, rowmax, grads, st);
+  if (!g.lda) return pick<OpF16, A_BLOCKS>(g, A, rowmax, grads, st);
+  return g.bf16 ? pick<OpBf16, A_ROWS>(g, A, rowmax, grads, st) : pick<OpF16, A_ROWS>(g, A, rowmax, grads, st);
 }
 
 }  // namespace mpq

@@ -25,7 +25,7 @@ namespace mpq {
 
 namespace {
 
-template <typename T, int BM, int BN, int WM, int WN, bool AROWS>
+template <typename T, int BM, int BN, int WM, int WN, int AMODE>
 __global__ __launch_bounds__(64 * WM * WN, 2) void q_gemm_kernel(QGemm g, float* __restrict__ part, int splits) {
   constexpr int WAVES = WM * WN;
   constexpr int SM = BM / WM / 16, SN = BN / WN / 16;   // 16 x 16 subtiles of a wave
@@ -36,7 +36,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void q_gemm_kernel(QGemm g, float*
   int split;
   int64_t i0, j0;
   v4f acc[SM][SN];
-  q_gemm_tile<T, BM, BN, WM, WN, AROWS>(g, splits, lds, acc, split, i0, j0);
+  q_gemm_tile<T, BM, BN, WM, WN, AMODE>(g, splits, lds, acc, split, i0, j0);
   // Epilogue: sixteen rows of the output at a time through this wave's part of
   // LDS, so that a row leaves as runs of SM * 16 columns.  A lane has the same
   // four columns throughout; its rows' loads go out together.
@@ -201,17 +201,17 @@ size_t q_gemm_workspace(int64_t M, int64_t N, int64_t K, int npairs) {
   return p.splits > 1 ? (size_t)p.splits * N * ((M + 3) / 4 * 4) * sizeof(float) : 0;
 }
 
-template <typename T, bool AROWS>
+template <typename T, int AMODE>
 static hipError_t run(const QGemm& g, float* part, hipStream_t st) {
   const Plan p = plan(g.M, g.N, g.K, g.npairs);
   float* out = p.splits > 1 && !g.cpart ? part : nullptr;
   const dim3 grid((unsigned)(p.tiles * p.splits));
   if (p.tile == TILE_256)
-    hipLaunchKernelGGL((q_gemm_kernel<T, 256, 256, 2, 4, AROWS>), grid, dim3(512), 0, st, g, out, p.splits);
+    hipLaunchKernelGGL((q_gemm_kernel<T, 256, 256, 2, 4, AMODE>), grid, dim3(512), 0, st, g, out, p.splits);
   else if (p.tile == TILE_256_128)
-    hipLaunchKernelGGL((q_gemm_kernel<T, 256, 128, 4, 2, AROWS>), grid, dim3(512), 0, st, g, out, p.splits);
+    hipLaunchKernelGGL((q_gemm_kernel<T, 256, 128, 4, 2, AMODE>), grid, dim3(512), 0, st, g, out, p.splits);
   else
-    hipLaunchKernelGGL((q_gemm_kernel<T, 128, 128, 2, 2, AROWS>), grid, dim3(256), 0, st, g, out, p.splits);
+    hipLaunchKernelGGL((q_gemm_kernel<T, 128, 128, 2, 2, AMODE>), grid, dim3(256), 0, st, g, out, p.splits);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !out) return e;
   const int64_t Mp = (g.M + 3) / 4 * 4;
@@ -223,8 +223,8 @@ static hipError_t run(const QGemm& g, float* part, hipStream_t st) {
 hipError_t launch_q_gemm(const QGemm& g, float* part, hipStream_t st) {
   if (g.M <= 0 || g.N <= 0) return hipSuccess;
   if (g.K % BK != 0 || g.K <= 0) return hipErrorInvalidValue;
-  if (g.lda) return g.bf16 ? run<OpBf16, true>(g, part, st) : run<OpF16, true>(g, part, st);
-  return g.bf16 ? run<OpBf16, false>(g, part, st) : run<OpF16, false>(g, part, st);
+  if (g.lda) return g.bf16 ? run<OpBf16, A_ROWS>(g, part, st) : run<OpF16, A_ROWS>(g, part, st);
+  return g.bf16 ? run<OpBf16, A_BLOCKS>(g, part, st) : run<OpF16, A_BLOCKS>(g, part, st);
 }
 
 }  // namespace mpq

@@ -426,6 +426,7 @@ __device__ __forceinline__ int64_t q_at(int64_t row, int64_t k, int64_t K) {
 }
 struct QGemm {
   const uint16_t* A; int64_t lda, planeA;   // operand order (lda = 0), or rows, as B's
+  int64_t acols, arows;                     // of an A that lies transposed (qgemm_tile.h)
   const uint16_t* B; int64_t ldb, planeB;   // operand order (ldb = 0), or rows
   int64_t M, N, K;        // columns i, rows j, depth of one plane
   int npairs;

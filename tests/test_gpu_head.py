@@ -11,7 +11,8 @@ is the sum of (e' the entry less the middle level, o' the offset with it):
     slope `rest` (1 less the target's probability): w rest (2 d_t + 2^-18), and one
     rounding; twice that covers the second order;
   - dz: relative 2 d_t + 2^-16 (|z - max| below 100);
-  - dx: dz's, its terms and those of the weights of groups (2^-11 for one, 2^-20 for two),
+  - dx: dz's, its terms and those of the weights of groups (2^-11 for one, 2^-20 for two;
+    a bfloat16 matrix: dz in bfloat16, 2^-8, but for the target's, whose term is float32),
     elements below 2^-28 of the row's bound 2^-39 of it, float32 sums over the
     vocabulary (V / 16 + 32) 2^-22, one rounding of the result;
   - the head's gradients: dz's, s's own d_t, sums of 64 tokens (2^-19); of a matrix and
@@ -61,7 +62,9 @@ def reference(x, head, targets, bias, weights):
     dz = w[:, None] * torch.exp(z - lse[:, None])
     dz[row, r] = -w * rest
     dz[skip] = 0.0
-    return dict(x=x, ax=ax, W=W, A=A, z=z, S=S, loss=loss, rest=rest, w=w, dz=dz, skip=skip, top=top, W_abs=W.abs())
+    adz_others = dz.abs()
+    adz_others[row, r] = 0.0
+    return dict(x=x, ax=ax, W=W, A=A, z=z, S=S, loss=loss, rest=rest, w=w, dz=dz, skip=skip, top=top, adz_others=adz_others)
 
 
 def check(got, ref, dtype, n, exact_terms, kind, head=None, need_dx=True, need_dhead=True):
@@ -87,6 +90,9 @@ def check(got, ref, dtype, n, exact_terms, kind, head=None, need_dx=True, need_d
         M, E = adz @ ref["A"], ddz @ ref["A"]
         terms = 2.0 ** -11 * (2 if kind == "groups" else 1) if half else 2.0 ** -19
         low = 2.0 ** -38 * (bound[:, None] * ref["A"].sum(0)[None] * (head["spread"] if head and "spread" in head else 1.0))
+        if kind == "matrix" and dtype == "bf16":
+            terms = 2.0 ** -20
+            E = E + 2.0 ** -8 * ref["adz_others"] @ ref["A"]
         tol = E + terms * M + low + (V / 16 + 32) * 2.0 ** -22 * M
         within("dx", got["dx"], ref["dz"] @ ref["W"], tol + step * ((ref["dz"] @ ref["W"]).abs() + tol) + tiny)
     else:
