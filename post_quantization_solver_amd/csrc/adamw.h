@@ -9,8 +9,16 @@ constexpr int ADAMW_BLOCK = 256;         // 8-bit moments: elements that share a
 constexpr int ADAMW_LAUNCH = 440;        // tensors a launch takes (their gradients' addresses are its arguments: 4 KB)
 constexpr int ADAMW_NORM_GROUPS = 1024;  // workgroups of the norm's kernel
 
-// Words of the plan's control block.
-enum AdamwControl : int { CTL_NORM_COUNT = 0, CTL_STEP_COUNT = 1, CTL_FACTOR = 2, CTL_SKIP = 3, CTL_WORDS = 64 };
+// Words of the plan's control block.  A counter has 32 parts and their sum, a cache line
+// each: a thousand workgroups that count in one word wait for each other, 10 ns a turn.
+constexpr int ADAMW_PARTS = 32, ADAMW_LINE = 32, ADAMW_COUNTER = (ADAMW_PARTS + 1) * ADAMW_LINE;
+enum AdamwControl : int {
+  CTL_NORM_COUNT = 0,
+  CTL_STEP_COUNT = ADAMW_COUNTER,
+  CTL_FACTOR = 2 * ADAMW_COUNTER,
+  CTL_SKIP,
+  CTL_WORDS = 2 * ADAMW_COUNTER + ADAMW_LINE
+};
 
 struct AdamwTensor {
   void* param;

@@ -27,6 +27,7 @@
 // last workgroup to end counts the step, and in the norm's kernel adds up the
 // others' sums, in a fixed order: no further launch.
 #include <math.h>
+#include <type_traits>
 #include "internal.h"
 #include "adamw.h"
 #include "qlayer.h"
@@ -56,40 +57,56 @@ __host__ __device__ constexpr uint32_t mix(uint32_t x) {
 template <int F>
 constexpr double top_value() { return (double)((2 << F) - 1) * 16384.0; }
 
-// What a code stands for, in units of its scale.  A code's bits are a double's
+// What a code stands for, in units of its scale.  A code's bits are a float's
 // exponent and leading fraction bits; the codes below 2^F, evenly spaced like the
 // 2^F after them, come as those less 2^F.
 template <int F>
 __device__ __forceinline__ double code_value(uint32_t c) {
   const bool low = c < 1u << F;
-  const uint32_t hi = ((low ? c + (1u << F) : c) + ((1022u + F) << F)) << (20 - F);
-  return __hiloint2double((int)hi, 0) - (low ? (double)(1 << F) : 0.0);
+  const float x = __uint_as_float(((low ? c + (1u << F) : c) + ((126u + F) << F)) << (23 - F));
+  return (double)(low ? x - (float)(1 << F) : x);
 }
-// x (not negative, in units of the scale) as the code at or below it, after
-// `more` (in units of 2^-17 of the codes' distance) has been added.
-template <int F>
-__device__ __forceinline__ uint32_t code_below(double x, uint32_t more) {
-  const bool low = x < (double)(1 << F);
-  const double y = low ? x + (double)(1 << F) : x;
-  const uint64_t b = __builtin_bit_cast(uint64_t, y) + ((uint64_t)more << (35 - F));
-  return (uint32_t)(b >> (52 - F)) - ((1022u + F) << F) - (low ? 1u << F : 0u);
+// |m| in units of the scale as a code: up where its rest and u = (h + 1/2) / 2^16 are 1
+// and more together (a code is the double's leading bits; u is added below them).
+__device__ __forceinline__ uint32_t code_of_mean(double x, uint32_t h) {
+  const bool low = x < 8.0;
+  const uint32_t hi = (uint32_t)__double2hiint(low ? x + 8.0 : x) + 2 * h + 1;
+  return min((hi >> 17) - (1025u << 3) - (low ? 8u : 0u), 127u);
 }
-// A code's value: up where the rest of x and u = (h + 1/2) / 2^16 are 1 and more together.
-__device__ __forceinline__ uint32_t code_of_mean(double x, uint32_t h) { return min(code_below<3>(x, 2 * h + 1), 127u); }
-// A root's, by where its square y lies between the codes' squares: those are what has
-// to be kept on average (by the roots, each rounding would add its variance to v).
-__device__ __forceinline__ uint32_t code_of_root(double x, double y, uint32_t h) {
-  const uint32_t c = min(code_below<4>(x, 0), 254u);
-  const double lo = code_value<4>(c), hi = code_value<4>(c + 1);
-  const double rest = (1.0 - ((double)h + 0.5) * (1.0 / 65536.0)) * ((hi - lo) * (hi + lo));
-  return fma(-lo, lo, y) >= rest ? c + 1 : c;
+// A root's code, by where its square y (in units of the scale's) lies between the codes'
+// squares: those are what has to be kept on average (by the roots, each rounding would add
+// its variance to v).  The code 16 e + M stands for M 2^e (M from 16 on where e > 0), and in
+// units of 2^(2 e - 17) its square, and the square where rounding up begins, are whole
+// numbers.  M and e come from float32's root: next to a code that may be one off, and the
+// comparison then goes the same way (u is no nearer to 0 or 1 than 2^-17).
+__device__ __forceinline__ uint32_t code_of_root(double y, uint32_t h) {
+  const float x = __builtin_amdgcn_sqrtf((float)y);
+  const int e = max(__builtin_amdgcn_frexp_expf(x) - 5, 0);
+  const uint32_t M = (uint32_t)ldexpf(x, -e);
+  const uint32_t up = (M * M << 17) + __umul24(131071u - 2u * h, 2u * M + 1u);
+  const uint32_t c = (uint32_t)(e << 4) + M;
+  return min(__builtin_amdgcn_ldexp(y, 17 - 2 * e) >= (double)up ? c + 1 : c, 255u);
+}
+
+// What the codes of m (with their sign) and of the root stand for, for decoding: in LDS.
+struct CodeTables {
+  double m[256], r[256];
+};
+__device__ __forceinline__ void fill_tables(CodeTables& T) {
+  static_assert(THREADS == 256, "a code a thread");
+  const uint32_t c = threadIdx.x;
+  const double v = code_value<3>(c & 127u);
+  T.m[c] = c & 128u ? -v : v;
+  T.r[c] = code_value<4>(c);
 }
 
 // ------------------------------------------------------------------ memory
 
-// Eight consecutive elements from p[i] on, as many as live.
-__device__ __forceinline__ void load8(const void* p, int64_t i, int dtype, bool vec, int live, float* v) {
-  if (vec && live >= 8) {
+// Eight consecutive elements from p[i] on, as many as live (FULL: all, from aligned
+// addresses: no load under a branch, so that they are on their way together).
+template <bool FULL>
+__device__ __forceinline__ void load8(const void* p, int64_t i, int dtype, int live, float* v) {
+  if constexpr (FULL) {
     if (dtype == DT_F32) {
       const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
       const float4 a = q[0], b = q[1];
@@ -118,11 +135,11 @@ __device__ __forceinline__ uint32_t round16(float x, int dtype, uint32_t h) {
   if (dtype == DT_BF16) return (b + (h & 0xffffu)) >> 16;
   return OpF16::bits(__uint_as_float((b + (h & 0x1fffu)) & ~0x1fffu));
 }
-__device__ __forceinline__ void store8(void* p, int64_t i, int dtype, bool vec, int live, const float* v,
-                                       const uint32_t* h) {
+template <bool FULL>
+__device__ __forceinline__ void store8(void* p, int64_t i, int dtype, int live, const float* v, const uint32_t* h) {
   if (dtype == DT_F32) {
     float* q = static_cast<float*>(p) + i;
-    if (vec && live >= 8) {
+    if constexpr (FULL) {
       reinterpret_cast<float4*>(q)[0] = make_float4(v[0], v[1], v[2], v[3]);
       reinterpret_cast<float4*>(q)[1] = make_float4(v[4], v[5], v[6], v[7]);
     } else {
@@ -136,7 +153,7 @@ __device__ __forceinline__ void store8(void* p, int64_t i, int dtype, bool vec, 
   uint32_t b[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) b[k] = round16(v[k], dtype, h[k]);
-  if (vec && live >= 8) {
+  if constexpr (FULL) {
     *reinterpret_cast<uint4*>(q) = make_uint4(pack2(b[0], b[1]), pack2(b[2], b[3]), pack2(b[4], b[5]), pack2(b[6], b[7]));
   } else {
 #pragma unroll
@@ -170,9 +187,13 @@ __device__ __forceinline__ bool whole(const void* p) { return reinterpret_cast<u
 // for the last goes through atomics that have been performed by then.  (A fence of
 // device scope writes a whole L2 back, in every workgroup.)
 __device__ __forceinline__ bool came_last(uint32_t* counter) {
-  const bool last = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
-  if (last) *counter = 0;
-  return last;
+  auto last_of = [](uint32_t* word, uint32_t all) {
+    const bool last = __hip_atomic_fetch_add(word, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == all - 1;
+    if (last) __hip_atomic_store(word, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return last;
+  };
+  const uint32_t parts = min(gridDim.x, (uint32_t)ADAMW_PARTS), part = blockIdx.x % parts;
+  return last_of(counter + (part + 1) * ADAMW_LINE, (gridDim.x - part + parts - 1) / parts) && last_of(counter, parts);
 }
 
 __device__ __forceinline__ double wave_sum(double s) {
@@ -186,17 +207,42 @@ __global__ __launch_bounds__(THREADS) void adamw_norm_kernel(AdamwTable T, int64
                                                              GradList G) {
   __shared__ double part[THREADS / 64];
   __shared__ bool mine;
-  const int64_t u1 = T.first[hi];
+  // a run of units each, tensor by tensor, four units' loads together
+  const int64_t u0 = T.first[lo], all = T.first[hi] - u0, run = (all + gridDim.x - 1) / gridDim.x;
+  int64_t u = u0 + run * blockIdx.x;
+  const int64_t u1 = min(u + run, u0 + all);
   double s = 0.0;
-  for (int64_t u = T.first[lo] + blockIdx.x; u < u1; u += gridDim.x) {
+  while (u < u1) {
     const int k = __builtin_amdgcn_readfirstlane(T.owner[u]);
     const AdamwTensor A = T.tensors[k];
     const void* g = G.p[k - lo];
-    const int64_t at = (u - T.first[k]) * UNIT + threadIdx.x * PER;
-    float v[PER];
-    load8(g, at, A.dtype, whole(g), (int)max((int64_t)0, min((int64_t)PER, A.count - at)), v);
+    const int64_t f = T.first[k], end = min(u1, T.first[k + 1]);
+    auto square = [&](const float* v) {
 #pragma unroll
-    for (int q = 0; q < PER; ++q) s = fma((double)v[q], (double)v[q], s);
+      for (int q = 0; q < PER; ++q) s = fma((double)v[q], (double)v[q], s);
+    };
+    auto four = [&](int dtype) {
+      float v[4][PER];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) load8<true>(g, (u + j - f) * UNIT + threadIdx.x * PER, dtype, PER, v[j]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) square(v[j]);
+    };
+    if (whole(g))
+      for (; u + 4 <= end && (u + 4 - f) * UNIT <= A.count; u += 4) {
+        if (A.dtype == DT_F32) four(DT_F32);
+        else if (A.dtype == DT_BF16) four(DT_BF16);
+        else four(DT_F16);
+      }
+    for (; u < end; ++u) {
+      const int64_t at = (u - f) * UNIT + threadIdx.x * PER;
+      const int live = (int)max((int64_t)0, min((int64_t)PER, A.count - at));
+      float v[PER];
+      if (live == PER && whole(g)) load8<true>(g, at, A.dtype, live, v);
+      else load8<false>(g, at, A.dtype, live, v);
+      square(v);
+    }
+    u = end;
   }
   s = wave_sum(s);
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
@@ -245,13 +291,110 @@ __device__ __forceinline__ Common common(const StepArgs& A) {
   C.key = mix(mix(A.seed) ^ (uint32_t)t);
   return C;
 }
-__device__ __forceinline__ float stepped(float p, float m, float r, float lr, float decay, float eps, const Common& C) {
-  return fmaf(-decay, p, p) - lr * (m * C.c1) / fmaf(r, C.c2, eps);
+// rate: -lr c1.  (v_rcp_f32 is within a step of float32.)
+__device__ __forceinline__ float stepped(float p, float m, float r, float rate, float decay, float eps, float c2) {
+  return fmaf(rate * m, __builtin_amdgcn_rcpf(fmaf(r, c2, eps)), fmaf(-decay, p, p));
+}
+
+// A unit of a tensor: elements `at` on of this thread, `place` in the moments.  FULL: there
+// are eight of them, and addresses are aligned.
+template <bool SMALL, int DTYPE, bool FULL>
+__device__ __forceinline__ void step_unit(const StepArgs& A, const Common& C, const CodeTables* T, const AdamwTensor& P,
+                                          const void* grad, int64_t at, int64_t place, int live) {
+  const float lr = P.lr * C.lrf, decay = lr * P.weight_decay, rate = -lr * C.c1;
+  float g[PER], p[PER];
+  uint32_t h[PER];
+  load8<FULL>(grad, at, DTYPE, live, g);
+  load8<FULL>(P.param, at, DTYPE, live, p);
+  const uint32_t key = mix(C.key + (uint32_t)(place >> 32));
+#pragma unroll
+  for (int q = 0; q < PER; ++q) h[q] = SMALL || DTYPE != DT_F32 ? mix((uint32_t)(place + q) ^ key) : 0u;
+  if constexpr (SMALL) {
+    // 32 lanes have a block; the ones behind the tensor's last block read the first
+    const bool in = FULL || at < (P.count + ADAMW_BLOCK - 1) / ADAMW_BLOCK * ADAMW_BLOCK;
+    const int64_t here = in ? place : P.at;
+    uint8_t* mc = static_cast<uint8_t*>(A.m) + here;
+    uint8_t* rc = static_cast<uint8_t*>(A.v) + here;
+    const uint2 mw = *reinterpret_cast<const uint2*>(mc), rw = *reinterpret_cast<const uint2*>(rc);
+    const double ms = (double)A.m_scale[here / ADAMW_BLOCK], rs = (double)A.v_scale[here / ADAMW_BLOCK];
+    double m[PER], v[PER], mt = 0.0, vt = 0.0;
+    bool odd = false;
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+#pragma clang fp contract(off)
+      const uint32_t cm = (q < 4 ? mw.x : mw.y) >> (8 * (q & 3)) & 255u, cr = (q < 4 ? rw.x : rw.y) >> (8 * (q & 3)) & 255u;
+      const double gd = FULL || q < live ? (double)g[q] * (double)C.factor : 0.0;
+      const double old = T->m[cm] * ms, root = T->r[cr] * rs;
+      m[q] = A.beta1 * old + (1.0 - A.beta1) * gd;
+      v[q] = A.beta2 * (root * root) + (1.0 - A.beta2) * gd * gd;
+      mt = fmax(mt, fabs(m[q]));
+      vt = fmax(vt, v[q]);
+      odd |= !(v[q] <= 1.7976931348623157e308);   // (m is finite where v is)
+      p[q] = stepped(p[q], (float)m[q], __builtin_amdgcn_sqrtf((float)v[q]), rate, decay, A.eps, C.c2);
+    }
+    // a block's scales, by their bits: NaN over everything
+    uint32_t mb = __float_as_uint((float)(mt / top_value<3>())), rb = __float_as_uint((float)(sqrt(vt) / top_value<4>()));
+    if (odd) mb = rb = 0x7fc00000u;
+    auto join = [&](uint32_t b) {
+      b = max(b, (uint32_t)dpp_i<DPP_XOR1>((int)b));
+      b = max(b, (uint32_t)dpp_i<DPP_XOR2>((int)b));
+      b = max(b, (uint32_t)dpp_i<DPP_HALF_MIRROR>((int)b));
+      b = max(b, (uint32_t)dpp_i<DPP_MIRROR>((int)b));
+      return max(b, (uint32_t)shfl_xor_i((int)b, 16));
+    };
+    mb = join(mb);
+    rb = join(rb);
+    const double rd = (double)__uint_as_float(rb);
+    const double mi = mb ? 1.0 / (double)__uint_as_float(mb) : 0.0, ri = rb ? 1.0 / (rd * rd) : 0.0;
+    uint32_t mo[2] = {0, 0}, ro[2] = {0, 0};
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+      uint32_t cm = code_of_mean(fabs(m[q]) * mi, h[q] & 0xffffu);
+      if (cm && m[q] < 0.0) cm |= 128u;
+      uint32_t cr = code_of_root(v[q] * ri, h[q] >> 16);
+      if (v[q] > 0.0) cr = max(cr, 1u);
+      mo[q >> 2] |= cm << (8 * (q & 3));
+      ro[q >> 2] |= cr << (8 * (q & 3));
+    }
+    if (in) {
+      *reinterpret_cast<uint2*>(mc) = make_uint2(mo[0], mo[1]);
+      *reinterpret_cast<uint2*>(rc) = make_uint2(ro[0], ro[1]);
+      if ((threadIdx.x & 31) == 0) {
+        A.m_scale[here / ADAMW_BLOCK] = __uint_as_float(mb);
+        A.v_scale[here / ADAMW_BLOCK] = __uint_as_float(rb);
+      }
+    }
+  } else {
+    float* mp = static_cast<float*>(A.m);
+    float* vp = static_cast<float*>(A.v);
+    const float b1 = (float)A.beta1, b2 = (float)A.beta2, d1 = (float)(1.0 - A.beta1), d2 = (float)(1.0 - A.beta2);
+    float m[PER], v[PER];
+    load8<FULL>(mp, place, DT_F32, live, m);
+    load8<FULL>(vp, place, DT_F32, live, v);
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+      const float gs = g[q] * C.factor;
+      m[q] = fmaf(b1, m[q], d1 * gs);
+      v[q] = fmaf(b2, v[q], d2 * gs * gs);
+      p[q] = stepped(p[q], m[q], __builtin_amdgcn_sqrtf(v[q]), rate, decay, A.eps, C.c2);
+    }
+    store8<FULL>(mp, place, DT_F32, live, m, nullptr);
+    store8<FULL>(vp, place, DT_F32, live, v, nullptr);
+  }
+#pragma unroll
+  for (int q = 0; q < PER; ++q) h[q] = DTYPE != DT_F32 ? mix(h[q] ^ 0x9e3779b9u) : 0u;
+  store8<FULL>(P.param, at, DTYPE, live, p, h);
 }
 
 template <bool SMALL>
 __global__ __launch_bounds__(THREADS) void adamw_step_kernel(StepArgs A, GradList G) {
   __shared__ Common shared;
+  __shared__ std::conditional_t<SMALL, CodeTables, int> tables;
+  const CodeTables* T = nullptr;
+  if constexpr (SMALL) {
+    fill_tables(tables);
+    T = &tables;
+  }
   if (threadIdx.x == 0) shared = common(A);
   __syncthreads();
   const Common C = shared;
@@ -260,92 +403,17 @@ __global__ __launch_bounds__(THREADS) void adamw_step_kernel(StepArgs A, GradLis
     const int k = __builtin_amdgcn_readfirstlane(A.T.owner[u]);
     const AdamwTensor P = A.T.tensors[k];
     const void* grad = G.p[k - A.lo];
-    const int64_t at = (u - A.T.first[k]) * UNIT + threadIdx.x * PER;
+    const int64_t start = (u - A.T.first[k]) * UNIT, at = start + threadIdx.x * PER;
     const int live = (int)max((int64_t)0, min((int64_t)PER, P.count - at));
     const int64_t place = P.at + at;   // in the moments, whose last block is whole
-    const float lr = P.lr * C.lrf, decay = lr * P.weight_decay;
-    float g[PER], p[PER];
-    uint32_t h[PER];
-    load8(grad, at, P.dtype, whole(grad), live, g);
-    load8(P.param, at, P.dtype, whole(P.param), live, p);
-    const uint32_t key = mix(C.key + (uint32_t)(place >> 32));
-#pragma unroll
-    for (int q = 0; q < PER; ++q) h[q] = SMALL || P.dtype != DT_F32 ? mix((uint32_t)(place + q) ^ key) : 0u;
-    if constexpr (SMALL) {
-      // 32 lanes have a block; the ones behind the tensor's last block read the first
-      const bool in = at < (P.count + ADAMW_BLOCK - 1) / ADAMW_BLOCK * ADAMW_BLOCK;
-      const int64_t here = in ? place : P.at;
-      uint8_t* mc = static_cast<uint8_t*>(A.m) + here;
-      uint8_t* rc = static_cast<uint8_t*>(A.v) + here;
-      const uint2 mw = *reinterpret_cast<const uint2*>(mc), rw = *reinterpret_cast<const uint2*>(rc);
-      const double ms = (double)A.m_scale[here / ADAMW_BLOCK], rs = (double)A.v_scale[here / ADAMW_BLOCK];
-      double m[PER], r[PER], mt = 0.0, rt = 0.0, odd = 0.0;
-#pragma unroll
-      for (int q = 0; q < PER; ++q) {
-#pragma clang fp contract(off)
-        const uint32_t cm = (q < 4 ? mw.x : mw.y) >> (8 * (q & 3)) & 255u, cr = (q < 4 ? rw.x : rw.y) >> (8 * (q & 3)) & 255u;
-        const double gd = q < live ? (double)g[q] * (double)C.factor : 0.0;
-        const double old = code_value<3>(cm & 127u) * ms, root = code_value<4>(cr) * rs;
-        m[q] = A.beta1 * (cm & 128u ? -old : old) + (1.0 - A.beta1) * gd;
-        const double v = A.beta2 * (root * root) + (1.0 - A.beta2) * gd * gd;
-        r[q] = sqrt(v);
-        mt = fmax(mt, fabs(m[q]));
-        rt = fmax(rt, r[q]);
-        odd += (m[q] - m[q]) + (v - v);   // NaN where one is not finite
-        p[q] = stepped(p[q], (float)m[q], (float)r[q], lr, decay, A.eps, C);
-      }
-      // a block's scales, by their bits: NaN over everything
-      uint32_t mb = __float_as_uint((float)(mt / top_value<3>())), rb = __float_as_uint((float)(rt / top_value<4>()));
-      if (!(odd == 0.0)) mb = rb = 0x7fc00000u;
-      auto join = [&](uint32_t b) {
-        b = max(b, (uint32_t)dpp_i<DPP_XOR1>((int)b));
-        b = max(b, (uint32_t)dpp_i<DPP_XOR2>((int)b));
-        b = max(b, (uint32_t)dpp_i<DPP_HALF_MIRROR>((int)b));
-        b = max(b, (uint32_t)dpp_i<DPP_MIRROR>((int)b));
-        return max(b, (uint32_t)shfl_xor_i((int)b, 16));
-      };
-      mb = join(mb);
-      rb = join(rb);
-      const double mi = mb ? 1.0 / (double)__uint_as_float(mb) : 0.0, ri = rb ? 1.0 / (double)__uint_as_float(rb) : 0.0;
-      uint32_t mo[2] = {0, 0}, ro[2] = {0, 0};
-#pragma unroll
-      for (int q = 0; q < PER; ++q) {
-        uint32_t cm = code_of_mean(fabs(m[q]) * mi, h[q] & 0xffffu);
-        if (cm && m[q] < 0.0) cm |= 128u;
-        const double x = fmin(r[q] * ri, top_value<4>());
-        uint32_t cr = code_of_root(x, x * x, h[q] >> 16);
-        if (r[q] > 0.0) cr = max(cr, 1u);
-        mo[q >> 2] |= cm << (8 * (q & 3));
-        ro[q >> 2] |= cr << (8 * (q & 3));
-      }
-      if (in) {
-        *reinterpret_cast<uint2*>(mc) = make_uint2(mo[0], mo[1]);
-        *reinterpret_cast<uint2*>(rc) = make_uint2(ro[0], ro[1]);
-        if ((threadIdx.x & 31) == 0) {
-          A.m_scale[here / ADAMW_BLOCK] = __uint_as_float(mb);
-          A.v_scale[here / ADAMW_BLOCK] = __uint_as_float(rb);
-        }
-      }
-    } else {
-      float* mp = static_cast<float*>(A.m);
-      float* vp = static_cast<float*>(A.v);
-      const float b1 = (float)A.beta1, b2 = (float)A.beta2, d1 = (float)(1.0 - A.beta1), d2 = (float)(1.0 - A.beta2);
-      float m[PER], v[PER];
-      load8(mp, place, DT_F32, true, live, m);
-      load8(vp, place, DT_F32, true, live, v);
-#pragma unroll
-      for (int q = 0; q < PER; ++q) {
-        const float gs = g[q] * C.factor;
-        m[q] = fmaf(b1, m[q], d1 * gs);
-        v[q] = fmaf(b2, v[q], d2 * gs * gs);
-        p[q] = stepped(p[q], m[q], sqrtf(v[q]), lr, decay, A.eps, C);
-      }
-      store8(mp, place, DT_F32, true, live, m, nullptr);
-      store8(vp, place, DT_F32, true, live, v, nullptr);
-    }
-#pragma unroll
-    for (int q = 0; q < PER; ++q) h[q] = P.dtype != DT_F32 ? mix(h[q] ^ 0x9e3779b9u) : 0u;
-    store8(P.param, at, P.dtype, whole(P.param), live, p, h);
+    const bool full = start + UNIT <= P.count && whole(grad) && whole(P.param);
+    auto go = [&](auto dtype) {
+      if (full) step_unit<SMALL, dtype.value, true>(A, C, T, P, grad, at, place, PER);
+      else step_unit<SMALL, dtype.value, false>(A, C, T, P, grad, at, place, live);
+    };
+    if (P.dtype == DT_F32) go(std::integral_constant<int, DT_F32>{});
+    else if (P.dtype == DT_BF16) go(std::integral_constant<int, DT_BF16>{});
+    else go(std::integral_constant<int, DT_F16>{});
   }
   __syncthreads();
   if (threadIdx.x == 0 && came_last(A.T.control + CTL_STEP_COUNT) && A.last && !C.skip) *A.step += 1;

@@ -35,14 +35,17 @@ struct PieceArgs {
   // gradients
   const float *row_top, *row_scale, *row_target;   // the largest, w / sum of exponentials, dz of the target
   const uint32_t* gmax;
-  const float* fmax;               // the largest factor of dz
+  const float* fmax;               // the largest factor of dz, in 64 parts (nullptr: 1)
+  const uint32_t* xmax;            // the tokens' factors in x's operand: dz^T carries the inverse
   const uint32_t* refs;            // the weights' planes' factors (nullptr: a is dz's factor)
   uint32_t* dmax;                  // the bound that a token's d is scaled by
   uint16_t* d; int64_t plane_d, mp; int terms_d;    // dz times its factors: t rows of mp (nullptr: none)
-  bool raw_d;                      // dz itself in bfloat16, the target's left out
+  bool raw_d;                      // dz itself, in bfloat16
+  bool own_target;                 // the targets' left out
   float* rowpart;                  // t x (mp / 64): sums of dz o' (nullptr: none)
   uint16_t* dt; int64_t plane_t, tp; int terms_t;   // dz^T: m rows of tp (nullptr: none)
   float* colpart;                  // (tp / 64) x 3 x m: sums of dz, dz s, dz X (nullptr: none)
+  float *dbias, *dscale, *doffset; // or those themselves, where there is one tile of tokens
 };
 
 #ifdef __HIPCC__
@@ -61,6 +64,12 @@ __device__ __forceinline__ void put_dz(const PieceArgs& A, int64_t t, int64_t i,
     *reinterpret_cast<uint2*>(A.d + q_at(t, i, A.mp)) = make_uint2(OpBf16::pack(u[0], u[1]), OpBf16::pack(u[2], u[3]));
   else
     put_terms(A.d + q_at(t, i, A.mp), A.plane_d, A.terms_d, u);
+}
+__device__ __forceinline__ float largest_factor(const PieceArgs& A) {
+  if (!A.fmax) return 1.f;
+  uint32_t top = abs_bits(A.fmax[threadIdx.x & 63]);
+  for (int o = 32; o; o >>= 1) top = max(top, (uint32_t)shfl_xor_i((int)top, o));
+  return __uint_as_float(top);
 }
 // Over the sixteen lanes of a row.
 __device__ __forceinline__ float sum16(float s) {

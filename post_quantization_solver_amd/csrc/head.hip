@@ -56,20 +56,22 @@ struct TokenArgs {
   bool vec;                           // rows of x four elements at a time
   float *weight, *sum, *target_z;     // the weight (0: the row is not read), X, the target's logit
   uint32_t* rowmax;
-  uint32_t* gmax;                     // two words, cleared
+  uint32_t* gmax;                     // cleared
   uint16_t* planes; int64_t plane;    // float16 terms, operand order of Kp columns
   int terms; int64_t Kp;
   bool raw;                           // bfloat16 as it is, in place of terms
   bool frags;                         // in the few-row product's order
+  uint16_t* again; int64_t plane_again, Kp_again;   // terms in operand order beside them (nullptr: none)
   float* ones;                        // V ones, or nullptr
-  // the transpose: columns' maxima, and terms
-  uint32_t* colmax;
-  uint16_t* xt; int64_t plane_t, tp;
+  const float* scale; float* fpart;   // the largest of V scales, in 64 parts (nullptr: not wanted)
 };
 
 __device__ __forceinline__ float token_weight(const TokenArgs& A, int64_t t) {
   return t < A.t && A.targets[t] >= 0 ? (A.weights ? A.weights[t] : 1.f) : 0.f;
 }
+
+// The larger magnitude, by its bits (NaN over everything).
+__device__ __forceinline__ float bits_max(float a, float b) { return __uint_as_float(max(abs_bits(a), abs_bits(b))); }
 
 // A workgroup per row of the planes: the tokens' rows, zeros for those that are
 // not read and behind the last.
@@ -78,7 +80,17 @@ __global__ __launch_bounds__(256) void head_token_kernel(TokenArgs A) {
   const int64_t row = blockIdx.x, rows = (A.t + 15) / 16 * 16;
   const int lane = threadIdx.x & 63, wave = wave_id();
   if (row >= rows) {   // the workgroups behind them
-    const int64_t i = (row - rows) * 256 + threadIdx.x;
+    const int64_t k = row - rows;
+    if (A.fpart && k < 64) {
+      float top = 0.f;
+      for (int64_t i = k * 256 + threadIdx.x; i < A.V; i += 64 * 256) top = bits_max(top, A.scale[i]);
+      for (int o = 32; o; o >>= 1) top = bits_max(top, shfl_xor_f(top, o));
+      if (lane == 0) red[0][wave] = top;
+      __syncthreads();
+      if (threadIdx.x == 0) A.fpart[k] = bits_max(bits_max(red[0][0], red[0][1]), bits_max(red[0][2], red[0][3]));
+      return;
+    }
+    const int64_t i = (k - (A.fpart ? 64 : 0)) * 256 + threadIdx.x;
     if (i < A.V) A.ones[i] = 1.f;
     return;
   }
@@ -117,9 +129,7 @@ __global__ __launch_bounds__(256) void head_token_kernel(TokenArgs A) {
     A.rowmax[row] = top;
     A.target_z[row] = __uint_as_float(0x7fc00000u);   // a target past the vocabulary stays NaN
   }
-  if (row == 0 && threadIdx.x < 2) A.gmax[threadIdx.x] = 0;
-  if (row == 0 && A.colmax)
-    for (int64_t j = threadIdx.x; j < A.n; j += 256) A.colmax[j] = 0;
+  if (row == 0 && threadIdx.x == 0) *A.gmax = 0;
   const float f = pow2(pow2_shift(top));
   for (int64_t j = threadIdx.x * 8; j < A.Kp; j += 256 * 8) {
     float v[8];
@@ -133,6 +143,11 @@ __global__ __launch_bounds__(256) void head_token_kernel(TokenArgs A) {
       o[0][q] = pack2(a[0], b[0]);
       o[1][q] = pack2(a[1], b[1]);
     }
+    if (A.again && j < A.Kp_again) {
+      uint16_t* dst = A.again + q_at(row, j, A.Kp_again);
+      *reinterpret_cast<v4u*>(dst) = o[0];
+      if (A.terms > 1) *reinterpret_cast<v4u*>(dst + A.plane_again) = o[1];
+    }
     if (A.raw)
 #pragma unroll
       for (int q = 0; q < 4; ++q) o[0][q] = OpBf16::pack(v[2 * q], v[2 * q + 1]);
@@ -140,65 +155,6 @@ __global__ __launch_bounds__(256) void head_token_kernel(TokenArgs A) {
                                         : q_at(row, j, A.Kp));
     *reinterpret_cast<v4u*>(dst) = o[0];
     if (A.terms > 1) *reinterpret_cast<v4u*>(dst + A.plane) = o[1];
-  }
-}
-
-__device__ __forceinline__ void load_token4(const TokenArgs& A, int64_t t, int64_t j, float* v) {
-  const int live = token_weight(A, t) != 0.f ? (int)max((int64_t)0, min((int64_t)4, A.n - j)) : 0;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) v[k] = 0.f;
-  if (live) load4(A.x, t * A.ldx + j, A.dtype, A.vec, live, v);
-}
-
-// Columns' largest magnitudes, tiles of 64 x 64 (integer maxima of bits: in any order the same).
-__global__ __launch_bounds__(256) void head_colmax_kernel(TokenArgs A) {
-  __shared__ uint32_t cm[4][64];
-  const int cx = threadIdx.x & 15, ry = threadIdx.x >> 4, wave = wave_id();
-  const int64_t tiles = (A.n + 63) / 64, t0 = blockIdx.x / tiles * 64, j = blockIdx.x % tiles * 64 + cx * 4;
-  uint32_t col[4] = {0, 0, 0, 0};
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    float v[4];
-    load_token4(A, t0 + ry + 16 * k, j, v);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) col[q] = max(col[q], abs_bits(v[q]));
-  }
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    col[q] = max(col[q], (uint32_t)shfl_xor_i((int)col[q], 16));
-    col[q] = max(col[q], (uint32_t)shfl_xor_i((int)col[q], 32));
-    if ((threadIdx.x & 63) < 16) cm[wave][cx * 4 + q] = col[q];
-  }
-  __syncthreads();
-  if (threadIdx.x < 64) {
-    const int64_t c = blockIdx.x % tiles * 64 + threadIdx.x;
-    const uint32_t top = max(max(cm[0][threadIdx.x], cm[1][threadIdx.x]), max(cm[2][threadIdx.x], cm[3][threadIdx.x]));
-    if (c < A.n) atomicMax(A.colmax + c, top);
-  }
-}
-
-// x^T's planes: n rows of tp tokens.
-__global__ __launch_bounds__(256) void head_token_t_kernel(TokenArgs A) {
-  __shared__ float tl[64][65];
-  const int cx = threadIdx.x & 15, ry = threadIdx.x >> 4;
-  const int64_t tiles = (A.n + 63) / 64, t0 = blockIdx.x / tiles * 64, j0 = blockIdx.x % tiles * 64;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    float v[4];
-    load_token4(A, t0 + ry + 16 * k, j0 + cx * 4, v);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) tl[ry + 16 * k][cx * 4 + q] = v[q];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int64_t r = j0 + ry + 16 * k;
-    if (r >= A.n) continue;
-    const float f = pow2(pow2_shift(A.colmax[r]));
-    float v[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) v[q] = tl[cx * 4 + q][ry + 16 * k] * f;
-    put_terms(A.xt + q_at(r, t0 + cx * 4, A.tp), A.plane_t, A.terms, v);
   }
 }
 
@@ -311,13 +267,44 @@ __global__ __launch_bounds__(256) void head_stats_kernel(PieceArgs A) {
   if (threadIdx.x == 0) A.part[(int64_t)blockIdx.y * A.t + t] = make_float2(top, (red[0] + red[1]) + (red[2] + red[3]));
 }
 
-// The segments joined, the loss, and what the gradients take of a token: sixteen
-// tokens a workgroup, sixteen threads each.
+// A token's loss, and what its gradients take, from the largest of the others' logits, the
+// sum of their exponentials about it, and the target's.
+struct TokenOut {
+  const float* weight;
+  float *loss, *row_top, *row_scale, *row_target;
+  const uint32_t* xmax;   // dz^T's operand carries the inverse of the token's factor
+  uint32_t* gmax;
+};
+__device__ __forceinline__ void finish_token(const TokenOut& A, int64_t t, float top, double s, float zt) {
+  const float w = A.weight[t];
+  if (w == 0.f) {   // not read
+    A.loss[t] = A.row_top[t] = A.row_scale[t] = A.row_target[t] = 0.f;
+    return;
+  }
+  if (!(s == s) || !(zt == zt)) {
+    A.row_top[t] = 0.f;
+    A.loss[t] = A.row_scale[t] = A.row_target[t] = __uint_as_float(0x7fc00000u);
+    atomicMax(A.gmax, 0x7fc00000u);
+    return;
+  }
+  // R - z of the target: log of the others' mass over its own
+  const double d = (double)top + log(s) - (double)zt;
+  const bool none = zt == -INFINITY;   // (all of them: nothing to move)
+  const double rest = none ? 1.0 : d > 0.0 ? 1.0 / (1.0 + exp(-d)) : exp(d) / (1.0 + exp(d));
+  const double l = none ? INFINITY : d > 0.0 ? d + log1p(exp(-d)) : log1p(exp(d));
+  const float all = fmaxf(top, zt);
+  const double total = s * exp((double)top - (double)all) + exp((double)zt - (double)all);
+  const float target = all == -INFINITY ? 0.f : (float)(-(double)w * rest);
+  A.loss[t] = (float)((double)w * l);
+  A.row_top[t] = all;
+  A.row_scale[t] = all == -INFINITY ? 0.f : (float)((double)w / total);
+  A.row_target[t] = target;
+  atomicMax(A.gmax, abs_bits(target * pow2(-pow2_shift(A.xmax[t]))));
+}
+
+// The segments joined: sixteen tokens a workgroup, sixteen threads each.
 __global__ __launch_bounds__(256) void head_join_kernel(const float2* __restrict__ part, int64_t segs, int64_t T,
-                                                        const float* __restrict__ weight, const float* __restrict__ target_z,
-                                                        float* __restrict__ loss, float* __restrict__ row_top,
-                                                        float* __restrict__ row_scale, float* __restrict__ row_target,
-                                                        uint32_t* __restrict__ gmax) {
+                                                        const float* __restrict__ target_z, TokenOut O) {
   __shared__ float tops[16][16];
   __shared__ double sums[16][16];
   const int own = threadIdx.x & 15, lane = threadIdx.x >> 4;
@@ -341,42 +328,67 @@ __global__ __launch_bounds__(256) void head_join_kernel(const float2* __restrict
   if (lane != 0 || t >= T) return;
   s = 0.0;
   for (int k = 0; k < 16; ++k) s += sums[k][own];
-  const float w = weight[t], zt = target_z[t];
-  if (w == 0.f) {   // not read
-    loss[t] = row_top[t] = row_scale[t] = row_target[t] = 0.f;
-    return;
+  finish_token(O, t, top, s, target_z[t]);
+}
+
+// A short vocabulary's logits of a token in one workgroup, start to end.
+__global__ __launch_bounds__(256) void head_row_kernel(PieceArgs A, TokenOut O) {
+  __shared__ float red[4], own;
+  __shared__ double sums[4];
+  const int64_t t = blockIdx.x, target = A.targets[t];
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  const float X = A.sum[t];
+  auto logits = [&](int64_t i, float* z) {
+    const Col4 C = col4(A, i);
+    const float4 s = *reinterpret_cast<const float4*>(A.S + t * A.lds + i);
+    const float v[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) z[k] = i + k < A.m ? fmaf(C.a[k], v[k], fmaf(C.o[k], X, C.b[k])) : -INFINITY;
+  };
+  if (threadIdx.x == 0) own = __uint_as_float(0x7fc00000u);
+  __syncthreads();
+  float top = -INFINITY;
+  for (int64_t i = threadIdx.x * 4; i < A.m; i += 1024) {
+    float z[4];
+    logits(i, z);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (i + k == target && i + k < A.m) own = z[k];
+      else top = fmaxf(top, z[k]);
+    }
   }
-  if (!(s == s) || !(zt == zt)) {
-    row_top[t] = 0.f;
-    loss[t] = row_scale[t] = row_target[t] = __uint_as_float(0x7fc00000u);
-    if (gmax) atomicMax(gmax, 0x7fc00000u);
-    return;
+  for (int o = 32; o; o >>= 1) top = fmaxf(top, shfl_xor_f(top, o));
+  if (lane == 0) red[wave] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  const float from = top == -INFINITY ? 0.f : top;
+  double sum = 0.0;
+  for (int64_t i = threadIdx.x * 4; i < A.m; i += 1024) {
+    float z[4];
+    logits(i, z);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) z[k] = i + k == target ? 0.f : __builtin_amdgcn_exp2f((z[k] - from) * H_LOG2E);
+    sum += (double)((z[0] + z[1]) + (z[2] + z[3]));
   }
-  // R - z of the target: log of the others' mass over its own
-  const double d = (double)top + log(s) - (double)zt;
-  const bool none = zt == -INFINITY;   // (all of them: nothing to move)
-  const double rest = none ? 1.0 : d > 0.0 ? 1.0 / (1.0 + exp(-d)) : exp(d) / (1.0 + exp(d));
-  const double l = none ? INFINITY : d > 0.0 ? d + log1p(exp(-d)) : log1p(exp(d));
-  const float all = fmaxf(top, zt);
-  const double total = s * exp((double)top - (double)all) + exp((double)zt - (double)all);
-  loss[t] = (float)((double)w * l);
-  row_top[t] = all;
-  row_scale[t] = all == -INFINITY ? 0.f : (float)((double)w / total);
-  row_target[t] = all == -INFINITY ? 0.f : (float)(-(double)w * rest);
-  if (gmax) atomicMax(gmax, abs_bits(row_target[t]));
+  for (int o = 32; o; o >>= 1) sum += shfl_d(sum, lane ^ o);
+  if (lane == 0) sums[wave] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) finish_token(O, t, top, (sums[0] + sums[1]) + (sums[2] + sums[3]), own);
 }
 
 __device__ __forceinline__ float dz_factor(const PieceArgs& A, int64_t i) {
   return A.refs ? pow2(-pow2_shift(A.refs[i])) : A.a ? A.a[i] : 1.f;
 }
 
-// The largest factor of dz over all rows (by its bits: in any order the same).
-__global__ __launch_bounds__(256) void head_factor_kernel(PieceArgs A, uint32_t* __restrict__ out) {
-  uint32_t top = 0;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < A.m; i += (int64_t)gridDim.x * 256)
-    top = max(top, abs_bits(dz_factor(A, i)));
-  for (int o = 32; o; o >>= 1) top = max(top, (uint32_t)shfl_xor_i((int)top, o));
-  if ((threadIdx.x & 63) == 0) atomicMax(out, top);
+// The largest factor of dz over all rows, in 64 parts.
+__global__ __launch_bounds__(256) void head_factor_kernel(PieceArgs A, float* __restrict__ out) {
+  __shared__ float red[4];
+  float top = 0.f;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < A.m; i += 64 * 256) top = bits_max(top, dz_factor(A, i));
+  for (int o = 32; o; o >>= 1) top = bits_max(top, shfl_xor_f(top, o));
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = top;
+  __syncthreads();
+  if (threadIdx.x == 0) out[blockIdx.x] = bits_max(bits_max(red[0], red[1]), bits_max(red[2], red[3]));
 }
 
 // A 64 x 64 tile of dz: its planes, its transpose's, its rows' and columns' sums.
@@ -386,7 +398,7 @@ __global__ __launch_bounds__(256) void head_grad_kernel(PieceArgs A) {
   const int cx = threadIdx.x & 15, ry = threadIdx.x >> 4, wave = wave_id();
   const int64_t tiles = A.mp / 64, t0 = blockIdx.x / tiles * 64, i0 = blockIdx.x % tiles * 64, i = i0 + cx * 4;
   const Col4 C = col4(A, i);
-  const float mid = A.mid >= 0 ? A.levels[A.mid] : 0.f, fm = A.d ? *A.fmax : 0.f;
+  const float mid = A.mid >= 0 ? A.levels[A.mid] : 0.f, fm = A.d ? largest_factor(A) : 0.f;
   const float off = A.mid == A.centre ? 0.f : A.levels[A.centre];
   float f[4] = {0.f, 0.f, 0.f, 0.f}, od[4], sums[3][4];
 #pragma unroll
@@ -420,7 +432,7 @@ __global__ __launch_bounds__(256) void head_grad_kernel(PieceArgs A) {
         const float g = pow2(pow2_shift(bound));
         float u[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) u[q] = !A.raw_d ? v[q] * f[q] * g : i + q == target ? 0.f : v[q];
+        for (int q = 0; q < 4; ++q) u[q] = i + q == target && A.own_target ? 0.f : A.raw_d ? v[q] : v[q] * f[q] * g;
         put_dz(A, t, i, u);
       }
     } else if (A.d && t < A.t) {
@@ -431,10 +443,11 @@ __global__ __launch_bounds__(256) void head_grad_kernel(PieceArgs A) {
       const float s = sum16(fmaf(v[0], od[0], v[1] * od[1]) + fmaf(v[2], od[2], v[3] * od[3]));
       if (cx == 0 && t < A.t) A.rowpart[t * tiles + blockIdx.x % tiles] = s;
     }
+    const float ft = A.dt && t < A.t ? pow2(-pow2_shift(A.xmax[t])) : 1.f;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) tl[ry + 16 * k][cx * 4 + q] = v[q];
+    for (int q = 0; q < 4; ++q) tl[ry + 16 * k][cx * 4 + q] = v[q] * ft;
   }
-  if (A.colpart) {
+  if (A.colpart || A.dbias) {
 #pragma unroll
     for (int c = 0; c < 3; ++c)
 #pragma unroll
@@ -446,10 +459,14 @@ __global__ __launch_bounds__(256) void head_grad_kernel(PieceArgs A) {
       }
   }
   __syncthreads();
-  if (A.colpart && threadIdx.x < 192) {
+  if ((A.colpart || A.dbias) && threadIdx.x < 192) {
     const int c = threadIdx.x >> 6, q = threadIdx.x & 63;
-    if (i0 + q < A.m)
-      A.colpart[(t0 / 64 * 3 + c) * A.m + i0 + q] = (cs[c][0][q] + cs[c][1][q]) + (cs[c][2][q] + cs[c][3][q]);
+    const float sum = (cs[c][0][q] + cs[c][1][q]) + (cs[c][2][q] + cs[c][3][q]);
+    float* out = c == 0 ? A.dbias : c == 1 ? A.dscale : A.doffset;
+    if (i0 + q < A.m) {
+      if (A.colpart) A.colpart[(t0 / 64 * 3 + c) * A.m + i0 + q] = sum;
+      else if (out) out[i0 + q] = sum;   // (the only tile of tokens)
+    }
   }
   if (!A.dt) return;
   const float g = pow2(pow2_shift(*A.gmax));
@@ -490,18 +507,31 @@ __global__ __launch_bounds__(256) void head_rowsum_kernel(const float* __restric
   for (int o = 32; o; o >>= 1) s += shfl_d(s, lane ^ o);
   if (lane == 0) rowadd[t] = (float)((first ? 0.0 : (double)rowadd[t]) + s);
 }
-__global__ __launch_bounds__(256) void head_fill_kernel(uint32_t* __restrict__ out, int64_t n, const uint32_t* __restrict__ v) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i < n) out[i] = *v;
-}
 
-// dx from its sums over the pieces, and the targets' terms where W is given: -w rest W[r],
-// the largest of a token's, would carry bfloat16's rounding of dz into all of its row.
+// dx from its sums over the pieces, and the targets' terms -w rest W[r] where dz's operand
+// leaves them out: the largest of a token's, they would carry their 16-bit rounding into
+// all of its row.
 struct TargetTerms {
-  const uint16_t* W; int64_t ldw, V;
+  bool wanted, packed, rows, vec;   // rows: entries times the scale, less the middle level's (the rows' sums have the rest)
+  const void* W; int64_t ldw, V;
+  int dtype;
+  QLayer L;
   const int32_t* targets;
   const float *weight, *row_target;
 };
+__device__ __forceinline__ void target_row4(const TargetTerms& R, int64_t r, int64_t j, float* w) {
+  if (!R.packed) {
+    load4(R.W, r * R.ldw + j, R.dtype, R.vec, (int)min((int64_t)4, R.L.n - j), w);
+    return;
+  }
+  q_entries4(R.L, q_code4(R.L, r, j), j, w);
+  const float mid = q_centre(R.L);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int64_t g = r * R.L.G + (R.L.G > 1 ? min(j + q, R.L.n - 1) / R.L.group : 0);
+    w[q] = R.rows ? R.L.scale[g] * (w[q] - mid) : fmaf(R.L.scale[g], w[q], R.L.offset ? R.L.offset[g] : 0.f);
+  }
+}
 __global__ __launch_bounds__(256) void head_dx_kernel(const float* __restrict__ acc, int splits, int64_t lda, int64_t T, int64_t n,
                                                       const float* __restrict__ rowadd, TargetTerms R, void* __restrict__ dx,
                                                       int64_t ld, int dtype, bool vec) {
@@ -517,9 +547,9 @@ __global__ __launch_bounds__(256) void head_dx_kernel(const float* __restrict__ 
       v[2] += q.z;
       v[3] += q.w;
     }
-    if (R.W && R.weight[t] != 0.f && R.targets[t] < R.V) {   // (n is a multiple of 64)
+    if (R.wanted && R.weight[t] != 0.f && R.targets[t] < R.V) {
       float w[4];
-      load4(R.W, R.targets[t] * R.ldw + j, DT_BF16, true, 4, w);
+      target_row4(R, R.targets[t], j, w);
 #pragma unroll
       for (int q = 0; q < 4; ++q) v[q] = fmaf(R.row_target[t], w[q], v[q]);
     }
@@ -583,6 +613,7 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
   const bool few = kept && !A.dense && q_few_rows(L, A.dtype, T);
   const int64_t seg_rows = T <= 64 ? 1024 : 4096;   // (short segments: as many workgroups as there are CUs)
   // (pieces begin at multiples of the tile's rows)
+  const bool short_rows = kept && V <= 16384;   // (one workgroup a token, start to end)
   const int64_t seg = kept ? seg_rows : tile.rows, all_segs = (V + seg - 1) / seg;
   const int64_t row_tiles = kept ? rows / 64 : rows / tile.rows, token_tiles = kept ? ttiles : (T + 127) / 128;
   Carve W{base};
@@ -593,7 +624,7 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
   K.target_z = W.take<float>((size_t)T * 4);
   K.rowmax = W.take<uint32_t>((size_t)T * 4);
   K.gmax = W.take<uint32_t>(8);
-  uint32_t* fmax = K.gmax ? K.gmax + 1 : nullptr;
+  float* fpart = W.take<float>(64 * 4);
   float* ones = W.take<float>(!A.dense && !weights ? (size_t)V * 4 : 0);
   float* row_top = W.take<float>((size_t)T * 4);
   float* row_scale = W.take<float>((size_t)T * 4);
@@ -619,7 +650,7 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
   };
   if (kept) both_sizes([&](int64_t nr) { ps = std::max(ps, q_gemm_workspace(nr, T, Kp, gz.npairs)); });
   uint16_t *d = nullptr, *dt = nullptr;
-  uint32_t *dmax = nullptr, *tmax = nullptr;
+  uint32_t* dmax = nullptr;
   float *rowpart = nullptr, *rowadd = nullptr, *acc = nullptr, *colpart = nullptr, *dW = nullptr;
   float2* cpart = nullptr;
   const int64_t lda = (n + 3) / 4 * 4, cblocks = (n + Q_CONTRACT - 1) / Q_CONTRACT;
@@ -636,10 +667,9 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
   }
   if (A.need_dhead) colpart = W.take<float>((size_t)token_tiles * 3 * rows * 4);
   if (product) {
-    K.colmax = W.take<uint32_t>((size_t)n * 4);
-    K.plane_t = up16(n) * tp;
-    K.xt = W.take<uint16_t>((size_t)XP * K.plane_t * 2);
-    tmax = W.take<uint32_t>((size_t)rows * 4);
+    K.plane_again = up16(T) * Kp;
+    K.Kp_again = Kp;
+    K.again = W.take<uint16_t>((size_t)XP * K.plane_again * 2);
     dt = W.take<uint16_t>((size_t)DT * up16(rows) * tp * 2);
     if (contract) {
       both_sizes([&](int64_t nr) { splits = std::max(splits, q_gemm_splits(n, nr, tp, gw.npairs)); });
@@ -662,16 +692,19 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
   K.vec = whole_quads(A.x, A.ldx, A.dtype);
   K.terms = XP;
   K.Kp = Kx;
-  K.tp = tp;
   K.frags = few;
   K.raw = in_place && A.dtype == DT_BF16;
+  const bool twice = product && (K.raw || few);   // the logits' operand is no float16 one in operand order
+  const uint16_t* xplanes = twice ? K.again : K.planes;
+  const int64_t xplane = twice ? K.plane_again : K.plane;
+  if (!twice) K.again = nullptr;
   K.ones = few && !weights ? ones : nullptr;
-  const uint32_t* rowmax = K.raw ? nullptr : K.rowmax;
-  H_LAUNCH(head_token_kernel, ((unsigned)(up16(T) + (K.ones ? (V + 255) / 256 : 0))), 256, K);
-  if (product) {
-    H_LAUNCH(head_colmax_kernel, ((unsigned)(ttiles * ((n + 63) / 64))), 256, K);
-    H_LAUNCH(head_token_t_kernel, ((unsigned)(ttiles * ((n + 63) / 64))), 256, K);
+  if (A.need_dx && !weights) {
+    K.scale = L.scale;
+    K.fpart = fpart;
   }
+  const uint32_t* rowmax = K.raw ? nullptr : K.rowmax;
+  H_LAUNCH(head_token_kernel, ((unsigned)(up16(T) + (K.fpart ? 64 : 0) + (K.ones ? (V + 255) / 256 : 0))), 256, K);
   PieceArgs P;
   memset(&P, 0, sizeof(P));
   P.lds = lds;
@@ -680,7 +713,8 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
   P.targets = A.targets;
   P.target_z = K.target_z;
   P.row_top = row_top; P.row_scale = row_scale; P.row_target = row_target;
-  P.gmax = K.gmax; P.fmax = reinterpret_cast<const float*>(fmax);
+  P.gmax = K.gmax; P.xmax = K.rowmax;
+  P.fmax = in_place ? nullptr : fpart;
   P.dmax = dmax;
   P.terms_d = DX; P.terms_t = DT;
   P.tp = tp;
@@ -760,6 +794,7 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
       H_TRY(launch_head_gemm(gz, P, rowmax, false, st));
     }
   }
+  const TokenOut O = {K.weight, A.loss, row_top, row_scale, row_target, K.rowmax, K.gmax};
   if (kept) {
     PieceArgs F = P;   // all of it
     F.m = V;
@@ -769,20 +804,20 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
     F.o = weights ? nullptr : L.offset;
     F.b = A.bias;
     F.part = part;
-    if (seg == 1024) H_LAUNCH(head_stats_kernel<1>, ((unsigned)T, (unsigned)all_segs), 256, F);
+    if (short_rows) H_LAUNCH(head_row_kernel, ((unsigned)T), 256, F, O);
+    else if (seg == 1024) H_LAUNCH(head_stats_kernel<1>, ((unsigned)T, (unsigned)all_segs), 256, F);
     else H_LAUNCH(head_stats_kernel<4>, ((unsigned)T, (unsigned)all_segs), 256, F);
   }
-  H_LAUNCH(head_join_kernel, ((unsigned)((T + 15) / 16)), 256, part, all_segs, T, K.weight, K.target_z, A.loss, row_top, row_scale,
-           row_target, K.gmax);
+  if (!short_rows) H_LAUNCH(head_join_kernel, ((unsigned)((T + 15) / 16)), 256, part, all_segs, T, K.target_z, O);
   if (!grads) return hipSuccess;
   P.raw_d = K.raw;
-  if (A.need_dx && !P.raw_d) {
+  P.own_target = !f32 && (P.raw_d || A.dtype == DT_F16);
+  if (A.need_dx && weights && !in_place) {
     PieceArgs F = P;
-    F.m = in_place ? 1 : V;   // (1 for every row)
-    F.refs = weights && !in_place ? refs : nullptr;
-    F.a = weights ? nullptr : L.scale;
-    if (few && weights) H_TRY(launch_q_bounds(L, refs, st));
-    H_LAUNCH(head_factor_kernel, ((unsigned)std::min<int64_t>((F.m + 255) / 256, 64)), 256, F, fmax);
+    F.m = V;
+    F.refs = refs;
+    if (few) H_TRY(launch_q_bounds(L, refs, st));
+    H_LAUNCH(head_factor_kernel, (64), 256, F, fpart);
   }
   // (a single piece's planes are still there)
   const bool again = pieces > 1 || few;
@@ -792,13 +827,19 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
     P.d = A.need_dx ? d : nullptr;
     P.rowpart = sums ? rowpart : nullptr;
     P.dt = product ? dt : nullptr;
-    P.colpart = A.need_dhead ? colpart : nullptr;
+    const bool straight = kept && ttiles == 1;   // no tiles of tokens to add up
+    P.colpart = A.need_dhead && !straight ? colpart : nullptr;
+    if (A.need_dhead && straight) {
+      P.dbias = A.dbias + r0;
+      P.dscale = weights ? nullptr : A.dscale + r0;
+      P.doffset = weights ? nullptr : A.doffset + r0;
+    }
     if (kept)
       H_LAUNCH(head_grad_kernel, ((unsigned)(mp / 64 * ttiles)), 256, P);
     else
       H_TRY(launch_head_gemm(gz, P, rowmax, true, st));
     const HeadTile own = head_tile(nr, T);   // (of the last piece, smaller)
-    if (A.need_dhead)
+    if (P.colpart)
       H_LAUNCH(head_colsum_kernel, ((unsigned)((nr + 255) / 256)), 256, colpart,
                kept ? ttiles : (T + own.tokens - 1) / own.tokens, nr, A.dbias + r0,
                weights ? nullptr : A.dscale + r0, weights ? nullptr : A.doffset + r0);
@@ -813,12 +854,12 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
       H_TRY(launch_head_dx(gx, P.raw_d ? nullptr : dmax, acc, lda, rows, k == 0, st));
     }
     if (product) {
-      H_LAUNCH(head_fill_kernel, ((unsigned)((nr + 255) / 256)), 256, tmax, nr, K.gmax);
-      gw.A = K.xt; gw.planeA = K.plane_t;
+      gw.A = xplanes; gw.planeA = xplane;
+      gw.acols = Kp; gw.arows = T;
       gw.B = dt; gw.planeB = P.plane_t;
       gw.M = n; gw.N = nr; gw.K = tp;
-      gw.O.rowmax = tmax;
-      gw.O.colmax = K.colmax;
+      gw.O.rowmax = K.gmax;
+      gw.O.one_rowmax = true;
       gw.O.mid = -1;
       gw.O.rows = nr; gw.O.cols = n;
       if (A.dense) {
@@ -839,7 +880,15 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
       }
     }
   }
-  const TargetTerms R = {P.raw_d ? static_cast<const uint16_t*>(A.W) : nullptr, A.ldw, V, A.targets, K.weight, row_target};
+  TargetTerms R;
+  memset(&R, 0, sizeof(R));
+  R.wanted = P.own_target;
+  R.packed = !A.dense; R.rows = !weights;
+  R.vec = whole_quads(A.W, A.ldw, A.dtype);
+  R.W = A.W; R.ldw = A.ldw; R.V = V;
+  R.dtype = A.dtype;
+  R.L = L;
+  R.targets = A.targets; R.weight = K.weight; R.row_target = row_target;
   if (A.need_dx)
     H_LAUNCH(head_dx_kernel, ((unsigned)std::min<int64_t>((T * (lda / 4) + 255) / 256, 4096)), 256, acc, dx_splits, lda, T, n,
              sums ? rowadd : nullptr, R, A.dx, A.lddx, A.dtype, whole_quads(A.dx, A.lddx, A.dtype));

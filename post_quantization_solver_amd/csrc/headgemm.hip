@@ -126,9 +126,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void head_gemm_kernel(QGemm g, Pie
       A.part[i0 / BM * A.t + j0 + k] = make_float2(top, sum);
     }
   } else {
-    float f[SN], X[SN], top[SN], scale[SN], own[SN], gd[SN], rows[SN];
+    float f[SN], X[SN], top[SN], scale[SN], own[SN], gd[SN], ft[SN], rows[SN];
     int target[SN];
-    const float fm = A.d ? *A.fmax : 0.f, gt = A.dt ? pow2(pow2_shift(*A.gmax)) : 1.f;
+    const float fm = A.d ? largest_factor(A) : 0.f, gt = A.dt ? pow2(pow2_shift(*A.gmax)) : 1.f;
 #pragma unroll
     for (int jj = 0; jj < SN; ++jj) {
       const int64_t t = j0 + (wn * SN + jj) * 16 + r, th = min(t, A.t - 1);
@@ -143,6 +143,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void head_gemm_kernel(QGemm g, Pie
       const uint32_t bound = abs_bits(own[jj] * fm);
       if (A.d && i0 == 0 && wm == 0 && kb == 0 && live) A.dmax[t] = bound;
       gd[jj] = pow2(pow2_shift(bound));
+      ft[jj] = A.dt ? pow2(-pow2_shift(A.xmax[th])) * gt : 0.f;
       rows[jj] = 0.f;
     }
     float* red = work;   // [WN][3][BM], and [WM][BN] after it
@@ -166,14 +167,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void head_gemm_kernel(QGemm g, Pie
           sums[0][k] += v[k];
           sums[1][k] = fmaf(v[k], fmaf(mid, X[jj], sv), sums[1][k]);
           sums[2][k] = fmaf(v[k], X[jj], sums[2][k]);
-          u[k] = !A.raw_d ? v[k] * cd[k] * gd[jj] : target[jj] == s * 16 + k ? 0.f : v[k];
+          u[k] = target[jj] == s * 16 + k && A.own_target ? 0.f : A.raw_d ? v[k] : v[k] * cd[k] * gd[jj];
         }
         if (A.rowpart) rows[jj] += fmaf(v[0], o[0], v[1] * o[1]) + fmaf(v[2], o[2], v[3] * o[3]);
         if (A.d && t < A.t && i < A.mp) put_dz(A, t, i, u);
         if (A.dt) {
-          transpose_quads(v, lane);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) v[k] *= gt;
+          for (int k = 0; k < 4; ++k) v[k] *= ft[jj];
+          transpose_quads(v, lane);
           const int64_t row = i + (r & 3), tok = t & ~(int64_t)3;
           if (row < A.m && tok < A.tp) put_terms(A.dt + q_at(row, tok, A.tp), A.plane_t, A.terms_t, v);
         }

@@ -67,7 +67,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void q_gemm_kernel(QGemm g, float*
       for (int it = 0; it < IT; ++it) {
         const int64_t row = min(jj + it * RPI, g.N - 1);
         code[it] = q_code4(g.L, g.row0 + row, min(ii, (g.M - 1) & ~(int64_t)3));
-        f[it] = pow2(-pow2_shift(g.O.rowmax[row]));
+        f[it] = pow2(-pow2_shift(g.O.rowmax[g.O.one_rowmax ? 0 : row]));
       }
 #pragma unroll
       for (int it = 0; it < IT; ++it) {
@@ -223,6 +223,7 @@ static hipError_t run(const QGemm& g, float* part, hipStream_t st) {
 hipError_t launch_q_gemm(const QGemm& g, float* part, hipStream_t st) {
   if (g.M <= 0 || g.N <= 0) return hipSuccess;
   if (g.K % BK != 0 || g.K <= 0) return hipErrorInvalidValue;
+  if (g.acols) return run<OpF16, A_T_BLOCKS>(g, part, st);
   if (g.lda) return g.bf16 ? run<OpBf16, A_ROWS>(g, part, st) : run<OpF16, A_ROWS>(g, part, st);
   return g.bf16 ? run<OpBf16, A_BLOCKS>(g, part, st) : run<OpF16, A_BLOCKS>(g, part, st);
 }
