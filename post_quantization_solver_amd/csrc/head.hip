@@ -42,8 +42,9 @@ struct Carve {
   }
 };
 
-// What a piece's planes, and its logits, should take: half of the last-level cache.
-constexpr int64_t H_BYTES = (int64_t)128 << 20, H_ROWS = 1024;
+// What logits that are kept, or a piece's operands, should take: half of the last-level
+// cache; the planes of a head whose logits are kept, which both passes read: four times that.
+constexpr int64_t H_BYTES = (int64_t)128 << 20, H_PIECE = (int64_t)256 << 20, H_PLANES = (int64_t)512 << 20, H_ROWS = 1024;
 
 // ------------------------------------------------------------------ tokens
 
@@ -604,8 +605,8 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
   const int64_t lds = (V + 255) / 256 * 256;
   const bool kept = T * lds * 4 <= H_BYTES;
   // rows of a piece
-  int64_t rows = H_BYTES / (WP * Kp * 2);
-  if (!kept) rows = std::min(rows, H_BYTES / (T * 4));
+  int64_t rows = (kept ? H_PLANES : H_PIECE) / (WP * Kp * 2);
+  if (!kept) rows = std::min(rows, H_PIECE / (T * 4));
   rows = std::min(std::max(rows / 256 * 256, H_ROWS), lds);
   const int64_t pieces = (V + rows - 1) / rows, last = V - (pieces - 1) * rows;
   const HeadTile tile = head_tile(rows, T);
@@ -723,7 +724,7 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
   P.mid = few ? -1 : P.centre;
   QLayer Q;
   // The piece's rows, and its planes.
-  auto piece = [&](int64_t k, bool planes) -> hipError_t {
+  auto piece = [&](int64_t k, bool planes, int terms) -> hipError_t {
     const int64_t r0 = k * rows, nr = std::min(rows, V - r0), plane = up16(nr) * Kp;
     Q = layer_rows(L, r0, nr);
     P.m = nr;
@@ -751,7 +752,7 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
       H_LAUNCH(head_dense_kernel, ((unsigned)up16(nr)), 256, D);
     } else if (planes && !A.dense) {
       if (weights) H_TRY(launch_q_bounds(Q, refs + r0, st));
-      H_TRY(launch_q_unpack(Q, Kp, weights ? WP : 0, refs + r0, wp, plane, st));
+      H_TRY(launch_q_unpack(Q, Kp, weights ? terms : 0, refs + r0, wp, plane, st));
     }
     gz.A = wp; gz.planeA = plane;
     if (in_place) {
@@ -780,7 +781,7 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
     H_TRY(launch_q_skinny(F, K.planes, 0, K.plane, T, XP, false, O, st));
   }
   for (int64_t k = 0; k < pieces && !few; ++k) {
-    H_TRY(piece(k, true));
+    H_TRY(piece(k, true, WP));
     if (kept) {
       gz.O.y = S + P.row0; gz.O.ldy = lds;
       gz.O.rowmax = rowmax;
@@ -822,7 +823,7 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
   // (a single piece's planes are still there)
   const bool again = pieces > 1 || few;
   for (int64_t k = 0; k < pieces; ++k) {
-    H_TRY(piece(k, again && (!kept || A.need_dx)));
+    H_TRY(piece(k, again && (!kept || A.need_dx), kept ? WX : WP));   // (kept: for dx alone)
     const int64_t r0 = P.row0, nr = P.m, mp = P.mp;
     P.d = A.need_dx ? d : nullptr;
     P.rowpart = sums ? rowpart : nullptr;
