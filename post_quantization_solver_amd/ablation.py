@@ -2,7 +2,8 @@
 
     python -m post_quantization_solver_amd.ablation [--config c5] [--T 1 4 8 16] [--S 0 1 3]
                                                     [--group G] [--json FILE] [--markdown FILE]
-                                                    [--head-tokens N [--tune-steps S]]
+                                                    [--head-tokens N [--tune-steps S [--tune-on divergence|tokens]
+                                                                                    [--state-bits 32|8]]]
 
 Reproduces the shape of the ablation table of the papernotes.org MPQ summary
 (ablation section, Table 3: VAMP iterations x CD sweeps against a greedy
@@ -31,7 +32,9 @@ and the rest (distill).  --tune-steps S tunes each cell's scales and offsets, th
 codes fixed, by S steps of Adam on that divergence (distill's gradient through
 linear_backward) over other hidden states, and reports the divergence after, on
 the N states and on the tuning's own (a synthetic layer's errors are noise, so
-there the second falls and the first does not).
+there the second falls and the first does not).  --tune-on tokens tunes on the cross
+entropy of the drawn tokens instead (linear_cross_entropy: no logits are kept), by the
+library's own step (AdamW), whose moments --state-bits 8 keeps in a byte each.
 """
 from __future__ import annotations
 
@@ -126,8 +129,27 @@ def tune_affine(ref, layer, steps, lr=2e-4):
         p.grad = None
 
 
+def tune_affine_on_tokens(ref, layer, steps, lr=2e-4, state_bits=32, max_norm=None):
+    """Steps of AdamW on the layer's scales and offsets (in place, where there are any), the codes fixed: the mean
+    cross entropy of the drawn tokens, without a matrix of logits.  lr: in units of the mean scale.  Returns the
+    losses (steps float32 on the device)."""
+    import torch
+    import post_quantization_solver_amd as mpq
+    names = ["dscale"] + (["doffset"] if layer.offset is not None else [])
+    opt = mpq.AdamW([layer.scale, layer.offset][:len(names)], lr=lr * float(layer.scale.abs().mean()),
+                    state_bits=state_bits)
+    t = ref["x"].shape[0]
+    weights = torch.full((t,), 1.0 / max(t, 1), device=ref["x"].device)
+    losses = torch.empty(steps, device=ref["x"].device)
+    for k in range(steps):
+        out = mpq.linear_cross_entropy(ref["x"], layer, ref["targets"], weights=weights, need_dx=False)
+        losses[k] = out["loss"].sum()
+        opt.step([out[name] for name in names], max_norm=max_norm)
+    return losses
+
+
 def run_grid(W, s, V, E, a, o, T_list=(1, 4, 8, 16), S_list=(0, 1, 3), damping=0.5, group=0, log=print,
-             head_tokens=0, tune_steps=0):
+             head_tokens=0, tune_steps=0, tune_on="divergence", state_bits=32):
     """All cells of the grid on device tensors (W, s, V, a, o) and the host
     codebook E.  Returns a list of dicts (one per cell); with head_tokens also
     head_error, head_nll, head_ppl, head_kl and the original's
@@ -154,7 +176,10 @@ def run_grid(W, s, V, E, a, o, T_list=(1, 4, 8, 16), S_list=(0, 1, 3), damping=0
         layer = mpq.pack_layer(codes, cb, a.clone(), o.clone(), group=group or None)
         res = dict(head_stats(held, layer), head_ppl_original=float(np.exp(held["nll"])))
         if tune_steps:
-            tune_affine(seen, layer, tune_steps)
+            if tune_on == "tokens":
+                tune_affine_on_tokens(seen, layer, tune_steps, state_bits=state_bits)
+            else:
+                tune_affine(seen, layer, tune_steps)
             res["head_kl_tuned"] = head_stats(held, layer)["head_kl"]
             res["head_kl_tuning"] = head_stats(seen, layer)["head_kl"]
         return res
@@ -242,6 +267,8 @@ def main(argv=None):
     ap.add_argument("--group", type=int, default=0)
     ap.add_argument("--head-tokens", type=int, default=0)
     ap.add_argument("--tune-steps", type=int, default=0)
+    ap.add_argument("--tune-on", choices=("divergence", "tokens"), default="divergence")
+    ap.add_argument("--state-bits", type=int, choices=(8, 32), default=32)
     ap.add_argument("--json", default="")
     ap.add_argument("--markdown", default="")
     args = ap.parse_args(argv)
@@ -249,6 +276,8 @@ def main(argv=None):
         ap.error("--head-tokens and --tune-steps are not negative")
     if args.tune_steps and not args.head_tokens:
         ap.error("--tune-steps needs --head-tokens")
+    if args.state_bits != 32 and args.tune_on != "tokens":
+        ap.error("--state-bits needs --tune-on tokens")
     import torch
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     if root not in sys.path:
@@ -261,7 +290,8 @@ def main(argv=None):
     t = lambda x: torch.from_numpy(np.ascontiguousarray(x)).to(dev)  # noqa: E731
     print(f"[ablation] {L.name}: m={L.m} n={L.n} r={L.r} K={L.K} d={L.d} group={L.group}", flush=True)
     cells = run_grid(t(L.W), t(L.s), t(L.V), L.E, t(L.a), t(L.o), args.T, args.S, L.damping, L.group,
-                     log=lambda msg: print(msg, flush=True), head_tokens=args.head_tokens, tune_steps=args.tune_steps)
+                     log=lambda msg: print(msg, flush=True), head_tokens=args.head_tokens, tune_steps=args.tune_steps,
+                     tune_on=args.tune_on, state_bits=args.state_bits)
     title = (f"{L.name}: m={L.m} n={L.n} K={L.K} d={L.d}" + (f" g={L.group}" if L.group else "") +
              ", one MI355X, seconds per layer solve")
     if args.json:
