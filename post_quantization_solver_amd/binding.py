@@ -1176,7 +1176,7 @@ class AdamW:
     def _plan(self, torch):
         """The parameters' places for the kernels (again where one has moved)."""
         lib, count = load_library(), len(self.params)
-        self._where = array.array("Q", (p.data_ptr() for p in self.params))
+        self._where = [p.data_ptr() for p in self.params]
         tensors = (AdamWTensor * count)(*(
             AdamWTensor(p, n, at, lr, wd, _dtype_code(t, "params"), 0) for p, n, at, lr, wd, t in
             zip(self._where, self._counts, self.offsets, *self._rates, self.params)))
@@ -1196,7 +1196,7 @@ class AdamW:
         try:
             if (list(map(T.numel, tensors)) == self._counts and [t.dtype for t in tensors] == self._dtypes
                     and all(map(T.is_contiguous, tensors)) and set(map(T.get_device, tensors)) <= {self.device.index}):
-                return array.array("Q", map(T.data_ptr, tensors))
+                return array.array("Q", list(map(T.data_ptr, tensors)))
         except TypeError:
             pass
         if len(tensors) != len(self.params):
@@ -1224,7 +1224,7 @@ class AdamW:
         if max_norm is not None and not max_norm > 0.0:
             raise ValueError(f"max_norm must be positive, got {max_norm}")
         with _guard(dev):
-            if array.array("Q", map(torch.Tensor.data_ptr, self.params)) != self._where:
+            if list(map(torch.Tensor.data_ptr, self.params)) != self._where:
                 self._same(self.params, "params")
                 self._plan(torch)
             lr_scale = 1.0

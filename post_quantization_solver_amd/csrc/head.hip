@@ -171,46 +171,80 @@ struct DenseArgs {
   uint16_t* out; int64_t plane;   // m rows of Kp
 };
 
-// Rows' largest magnitudes and planes: a workgroup per row of the planes.
+// Rows' largest magnitudes and planes: a wave per row of the planes, which keeps a row of
+// up to 2048 columns in registers (longer ones are read again).
 __global__ __launch_bounds__(256) void head_dense_kernel(DenseArgs A) {
-  __shared__ uint32_t red[4];
-  const int64_t row = blockIdx.x;
+  constexpr int HOLD = 4;
+  const int lane = threadIdx.x & 63;
+  const int64_t row = (int64_t)blockIdx.x * 4 + wave_id();
+  if (row >= (A.m + 15) / 16 * 16) return;
   const bool live = row < A.m;
   auto load8 = [&](int64_t j, float* v) {
     const int have = live ? (int)max((int64_t)0, min((int64_t)8, A.n - j)) : 0;
-    load4(A.W, row * A.ldw + j, A.dtype, A.vec, min(have, 4), v);
-    load4(A.W, row * A.ldw + j + 4, A.dtype, A.vec, max(have - 4, 0), v + 4);
+    if (have == 8 && A.vec) {
+      load4(A.W, row * A.ldw + j, A.dtype, true, 4, v);
+      load4(A.W, row * A.ldw + j + 4, A.dtype, true, 4, v + 4);
+    } else {
+      load4(A.W, row * A.ldw + j, A.dtype, false, min(have, 4), v);
+      load4(A.W, row * A.ldw + j + 4, A.dtype, false, max(have - 4, 0), v + 4);
+    }
   };
+  float held[HOLD][8];
   uint32_t top = 0;
-  for (int64_t j = threadIdx.x * 8; j < A.n; j += 256 * 8) {
+#pragma unroll
+  for (int h = 0; h < HOLD; ++h) {
+    load8((h * 64 + lane) * 8, held[h]);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top = max(top, abs_bits(held[h][k]));
+  }
+  for (int64_t j = (HOLD * 64 + lane) * 8; j < A.n; j += 64 * 8) {
     float v[8];
     load8(j, v);
 #pragma unroll
     for (int k = 0; k < 8; ++k) top = max(top, abs_bits(v[k]));
   }
   for (int o = 32; o; o >>= 1) top = max(top, (uint32_t)shfl_xor_i((int)top, o));
-  if ((threadIdx.x & 63) == 0) red[wave_id()] = top;
-  __syncthreads();
-  top = max(max(red[0], red[1]), max(red[2], red[3]));
-  if (threadIdx.x == 0 && live) A.refs[row] = top;
+  if (lane == 0 && live) A.refs[row] = top;
   const float f = pow2(pow2_shift(top));
-  for (int64_t j = threadIdx.x * 8; j < A.Kp; j += 256 * 8) {
-    float v[8];
-    load8(j, v);
+  auto put = [&](int64_t j, float* v) {
+    if (j >= A.Kp) return;
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] *= f;
     put_terms(A.out + q_at(row, j, A.Kp), A.plane, A.terms, v);
     put_terms(A.out + q_at(row, j + 4, A.Kp), A.plane, A.terms, v + 4);
+  };
+#pragma unroll
+  for (int h = 0; h < HOLD; ++h) put((h * 64 + lane) * 8, held[h]);
+  for (int64_t j = (HOLD * 64 + lane) * 8; j < A.Kp; j += 64 * 8) {
+    float v[8];
+    load8(j, v);
+    put(j, v);
   }
 }
+
 // ------------------------------------------------------------------ a piece's logits
 
 struct Col4 {
   float a[4], o[4], b[4];
 };
+// (the vectors may begin at any float)
+typedef float v4fu __attribute__((ext_vector_type(4), aligned(4)));
 __device__ __forceinline__ Col4 col4(const PieceArgs& A, int64_t i) {
   Col4 C;
   const float mid = A.mid >= 0 ? A.levels[A.mid] : 0.f;
+  if (i + 4 <= A.m) {
+    v4fu a = {1.f, 1.f, 1.f, 1.f}, o = {0.f, 0.f, 0.f, 0.f}, b = o;
+    if (A.a) a = *reinterpret_cast<const v4fu*>(A.a + i);
+    if (A.o) o = *reinterpret_cast<const v4fu*>(A.o + i);
+    if (A.b) b = *reinterpret_cast<const v4fu*>(A.b + i);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      C.a[k] = a[k];
+      C.o[k] = A.a ? fmaf(a[k], mid, o[k]) : 0.f;
+      C.b[k] = b[k];
+    }
+    return C;
+  }
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     C.a[k] = 1.f;
@@ -497,7 +531,7 @@ __global__ __launch_bounds__(256) void head_colsum_kernel(const float* __restric
     out[c][i] = (float)s;
   }
 }
-// Rows' sums over the pieces so far; and the row of the largest magnitudes that dz^T's planes share.
+// Rows' sums over the pieces so far.
 __global__ __launch_bounds__(256) void head_rowsum_kernel(const float* __restrict__ part, int64_t tiles, int64_t T, bool first,
                                                           float* __restrict__ rowadd) {
   const int64_t t = (int64_t)blockIdx.x * 4 + wave_id();
@@ -608,13 +642,14 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
   int64_t rows = (kept ? H_PLANES : H_PIECE) / (WP * Kp * 2);
   if (!kept) rows = std::min(rows, H_PIECE / (T * 4));
   rows = std::min(std::max(rows / 256 * 256, H_ROWS), lds);
-  const int64_t pieces = (V + rows - 1) / rows, last = V - (pieces - 1) * rows;
+  const int64_t pieces = (V + rows - 1) / rows;
   const HeadTile tile = head_tile(rows, T);
   // Few tokens: straight from the packed codes.
   const bool few = kept && !A.dense && q_few_rows(L, A.dtype, T);
   const int64_t seg_rows = T <= 64 ? 1024 : 4096;   // (short segments: as many workgroups as there are CUs)
-  // (pieces begin at multiples of the tile's rows)
-  const bool short_rows = kept && V <= 16384;   // (one workgroup a token, start to end)
+  // One workgroup a token, start to end. (Longer rows in segments: a token of 32000 logits takes
+  // 15.6 us in one workgroup of sixteen waves, 8 in segments with their join.)
+  const bool short_rows = kept && V <= 16384;
   const int64_t seg = kept ? seg_rows : tile.rows, all_segs = (V + seg - 1) / seg;
   const int64_t row_tiles = kept ? rows / 64 : rows / tile.rows, token_tiles = kept ? ttiles : (T + 127) / 128;
   Carve W{base};
@@ -737,7 +772,7 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
     P.o = weights ? nullptr : Q.offset;
     P.b = A.bias ? A.bias + r0 : nullptr;
     P.refs = weights && !in_place ? refs + r0 : nullptr;
-    P.part = part + r0 / tile.rows * T;
+    P.part = part + r0 / tile.rows * T;   // (pieces begin at multiples of the tile's rows)
     if (planes && A.dense && !in_place) {
       DenseArgs D;
       memset(&D, 0, sizeof(D));
@@ -749,7 +784,7 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
       D.terms = WP;
       D.refs = refs + r0;
       D.out = wp; D.plane = plane;
-      H_LAUNCH(head_dense_kernel, ((unsigned)up16(nr)), 256, D);
+      H_LAUNCH(head_dense_kernel, ((unsigned)(up16(nr) / 4)), 256, D);
     } else if (planes && !A.dense) {
       if (weights) H_TRY(launch_q_bounds(Q, refs + r0, st));
       H_TRY(launch_q_unpack(Q, Kp, weights ? terms : 0, refs + r0, wp, plane, st));

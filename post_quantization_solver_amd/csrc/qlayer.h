@@ -395,12 +395,20 @@ __device__ __forceinline__ uint32_t q_code4(const QLayer& L, int64_t i, int64_t 
 }
 __device__ __forceinline__ void q_entries4(const QLayer& L, uint32_t code, int64_t j, float* e) {
   const int half = (int)(j >> 2) & 1;
-  if (L.fmt == QF_NIB) {
+  if (L.fmt == QF_NIB || L.fmt == QF_BYTE) {
+    uint32_t q[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) e[k] = L.levels[(code >> (8 * half + 4 * (k >> 1) + 16 * (k & 1))) & 15u];
-  } else if (L.fmt == QF_BYTE) {
+    for (int k = 0; k < 4; ++k)
+      q[k] = L.fmt == QF_NIB ? (code >> (8 * half + 4 * (k >> 1) + 16 * (k & 1))) & 15u
+                             : (code >> (8 * (k >> 1) + 16 * (k & 1))) & 63u;
+    if (L.uniform) {   // (exactly the same, and no look-up)
+      const float base = L.levels[0], step = L.levels[1] - base;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) e[k] = L.levels[(code >> (8 * (k >> 1) + 16 * (k & 1))) & 63u];
+      for (int k = 0; k < 4; ++k) e[k] = fmaf((float)q[k], step, base);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) e[k] = L.levels[q[k]];
+    }
   } else if (L.fmt == QF_E8) {
     const uint32_t v = q_e8_nibbles(L, L.lut, code);
 #pragma unroll
@@ -493,12 +501,10 @@ hipError_t launch_q_linear(const QLinearArgs& A, void* ws, hipStream_t st);
 size_t q_grad_workspace(const QLinearGrad& A);
 hipError_t launch_q_grad(const QLinearGrad& A, void* ws, hipStream_t st);
 // Parts of them, float16: a layer's planes in operand order (planes = 0: entries; else
-// terms of its weights times 2^pow2_shift(refs)), their transposes (rows of mp), the
-// bounds refs, and the affine's sums of a dW that is contracted (cpart) or in memory.
+// terms of its weights times 2^pow2_shift(refs)), the bounds refs, and the affine's sums
+// of a dW that is contracted (cpart) or in memory.
 hipError_t launch_q_unpack(const QLayer& L, int64_t Kp, int planes, const uint32_t* refs, uint16_t* out, int64_t plane,
                            hipStream_t st);
-hipError_t launch_q_unpack_t(const QLayer& L, int64_t mp, int planes, const uint32_t* refs, uint16_t* out, int64_t plane,
-                             hipStream_t st);
 hipError_t launch_q_bounds(const QLayer& L, uint32_t* refs, hipStream_t st);
 hipError_t launch_q_affine_sums(const QLayer& L, const float2* cpart, int splits, int64_t cblocks, const float* dW, int64_t ldw,
                                 float* dscale, float* doffset, hipStream_t st);

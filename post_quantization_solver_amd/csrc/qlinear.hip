@@ -535,37 +535,66 @@ __global__ __launch_bounds__(256) void q_grad_rowsum_kernel(DuArgs A, float* __r
   rowadd[t] = (float)s;
 }
 
-// The contraction's parts, added up in order in float64: sixteen lanes per (row, group).
+// The contraction's parts, added up in order in float64: sixteen lanes per (row, group), or
+// one where that has one or two blocks (the sum is the same; 50257 rows of 16 groups of two
+// 43 us with sixteen).
+template <int LANES>
 __global__ __launch_bounds__(256) void q_contract_finish_kernel(QLayer L, const float2* __restrict__ part, int splits,
                                                                 int64_t rows, int64_t blocks, int64_t row0,
                                                                 float* __restrict__ dscale,
                                                                 float* __restrict__ doffset, DuArgs A,
                                                                 float* __restrict__ dbias) {
-  const int64_t own = (rows * L.G + 15) / 16;
+  constexpr int PER = 256 / LANES;
+  const int64_t own = (rows * L.G + PER - 1) / PER;
   if (blockIdx.x >= own) {   // d bias
     add_bias(A, (blockIdx.x - own) * 256 + threadIdx.x, dbias);
     return;
   }
-  const int lane = threadIdx.x & 15;
-  const int64_t w = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+  const int lane = threadIdx.x % LANES;
+  const int64_t w = (int64_t)blockIdx.x * PER + threadIdx.x / LANES;
   if (w >= rows * L.G) return;
   const int64_t row = w / L.G, g = w - row * L.G;
   const int64_t b0 = g * (L.group / Q_CONTRACT), b1 = L.G == 1 ? blocks : min(blocks, b0 + L.group / Q_CONTRACT);
   double se = 0.0, s1 = 0.0;
-  for (int s = 0; s < splits; ++s)
-    for (int64_t b = b0 + lane; b < b1; b += 16) {
-      const float2 p = part[((size_t)s * rows + row) * blocks + b];
-      se += (double)p.x;
-      s1 += (double)p.y;
+  if constexpr (LANES == 1) {
+    for (int64_t b = b0; b < b1; ++b) {   // (each block's own sum, as a lane's)
+      double be = 0.0, b1s = 0.0;
+      for (int s = 0; s < splits; ++s) {
+        const float2 p = part[((size_t)s * rows + row) * blocks + b];
+        be += (double)p.x;
+        b1s += (double)p.y;
+      }
+      se += be;
+      s1 += b1s;
     }
-  for (int o = 8; o; o >>= 1) {
-    se += shfl_d(se, (int)(threadIdx.x & 63) ^ o);
-    s1 += shfl_d(s1, (int)(threadIdx.x & 63) ^ o);
+  } else {
+    for (int s = 0; s < splits; ++s)
+      for (int64_t b = b0 + lane; b < b1; b += 16) {
+        const float2 p = part[((size_t)s * rows + row) * blocks + b];
+        se += (double)p.x;
+        s1 += (double)p.y;
+      }
+    for (int o = 8; o; o >>= 1) {
+      se += shfl_d(se, (int)(threadIdx.x & 63) ^ o);
+      s1 += shfl_d(s1, (int)(threadIdx.x & 63) ^ o);
+    }
   }
   if (lane == 0) {
     dscale[(row0 + row) * L.G + g] = (float)se;
     doffset[(row0 + row) * L.G + g] = (float)s1;
   }
+}
+
+// Behind its workgroups `bias` more, for d bias.
+void launch_contract_finish(const QLayer& L, const float2* part, int splits, int64_t rows, int64_t blocks, int64_t row0,
+                            float* dscale, float* doffset, const DuArgs& A, unsigned bias, float* dbias, hipStream_t st) {
+  const int64_t pairs = rows * L.G;
+  if (L.G > 1 && L.group / Q_CONTRACT <= 2)
+    hipLaunchKernelGGL(q_contract_finish_kernel<1>, dim3((unsigned)((pairs + 255) / 256) + bias), dim3(256), 0, st, L, part,
+                       splits, rows, blocks, row0, dscale, doffset, A, dbias);
+  else
+    hipLaunchKernelGGL(q_contract_finish_kernel<16>, dim3((unsigned)((pairs + 15) / 16) + bias), dim3(256), 0, st, L, part,
+                       splits, rows, blocks, row0, dscale, doffset, A, dbias);
 }
 
 // Groups that are no multiple of 64 columns: the contraction of a dW in memory.
@@ -940,8 +969,7 @@ hipError_t backward(const QLinearGrad& A, char* base, size_t* bytes, hipStream_t
       // d bias rides behind the first block of rows
       const unsigned bias = r0 == 0 ? (unsigned)((L.m + 255) / 256) : 0;
       if (contract)
-        hipLaunchKernelGGL(q_contract_finish_kernel, dim3((unsigned)((nr * L.G + 15) / 16) + bias), dim3(256), 0, st, L,
-                           cpart, splits, nr, cblocks, r0, A.dscale, A.doffset, D, A.dbias);
+        launch_contract_finish(L, cpart, splits, nr, cblocks, r0, A.dscale, A.doffset, D, bias, A.dbias, st);
       else
         hipLaunchKernelGGL(q_affine_grad_kernel, dim3((unsigned)((nr * L.G + 3) / 4) + bias), dim3(256), 0, st, L, dW,
                            ldw, r0, nr, A.dscale, A.doffset, D, A.dbias);
@@ -999,10 +1027,6 @@ hipError_t launch_q_unpack(const QLayer& L, int64_t Kp, int planes, const uint32
                            hipStream_t st) {
   return unpack<OpF16>(L, 0, L.tiles, Kp, planes, refs, out, plane, st);
 }
-hipError_t launch_q_unpack_t(const QLayer& L, int64_t mp, int planes, const uint32_t* refs, uint16_t* out, int64_t plane,
-                             hipStream_t st) {
-  return unpack_t(L, mp, planes, refs, out, plane, st);
-}
 hipError_t launch_q_bounds(const QLayer& L, uint32_t* refs, hipStream_t st) {
   PrepArgs P;
   memset(&P, 0, sizeof(P));
@@ -1017,8 +1041,7 @@ hipError_t launch_q_affine_sums(const QLayer& L, const float2* cpart, int splits
   DuArgs D;   // (no d bias beside them)
   memset(&D, 0, sizeof(D));
   if (cpart)
-    hipLaunchKernelGGL(q_contract_finish_kernel, dim3((unsigned)((L.m * L.G + 15) / 16)), dim3(256), 0, st, L, cpart, splits,
-                       L.m, cblocks, 0, dscale, doffset, D, nullptr);
+    launch_contract_finish(L, cpart, splits, L.m, cblocks, 0, dscale, doffset, D, 0, nullptr, st);
   else
     hipLaunchKernelGGL(q_affine_grad_kernel, dim3((unsigned)((L.m * L.G + 3) / 4)), dim3(256), 0, st, L, dW, ldw, 0, L.m,
                        dscale, doffset, D, nullptr);
