@@ -44,6 +44,11 @@ struct Carve {
 
 // What logits that are kept, or a piece's operands, should take: half of the last-level
 // cache; the planes of a head whose logits are kept, which both passes read: four times that.
+// Tokens whose input gradient comes straight from the packed codes.  Measured, whole calls with
+// gradients, 4 tokens so | 5 through planes: E8 128256 x 4096 323 | 600 us, 32000 x 2048 72 | 97;
+// 4 bits 32000 x 4096 102 | 165, groups of 128 117 | 232; 6 bits 32000 x 2048 80 | 114.  (One
+// token: 186, 54, 65, 72, 62.)  Eight would read and decode the codes twice.
+constexpr int64_t H_FEW = 4;
 constexpr int64_t H_BYTES = (int64_t)128 << 20, H_PIECE = (int64_t)256 << 20, H_PLANES = (int64_t)512 << 20, H_ROWS = 1024;
 
 // ------------------------------------------------------------------ tokens
@@ -543,6 +548,8 @@ __global__ __launch_bounds__(256) void head_rowsum_kernel(const float* __restric
   if (lane == 0) rowadd[t] = (float)((first ? 0.0 : (double)rowadd[t]) + s);
 }
 
+// Steps of eight columns (a lane's) of a chunk: 64 sums for the tokens.
+constexpr int few_dx_steps(int fmt, int tokens) { return q_steps(fmt) < 8 / tokens ? q_steps(fmt) : 8 / tokens; }
 // dx from its sums over the pieces, and the targets' terms -w rest W[r] where dz's operand
 // leaves them out: the largest of a token's, they would carry their 16-bit rounding into
 // all of its row.
@@ -575,6 +582,7 @@ __global__ __launch_bounds__(256) void head_dx_kernel(const float* __restrict__ 
     const int64_t t = k / quads, j = (k - t * quads) * 4;
     const float add = rowadd ? rowadd[t] : 0.f;
     float v[4] = {add, add, add, add};
+#pragma unroll 8
     for (int s = 0; s < splits; ++s) {
       const float4 q = *reinterpret_cast<const float4*>(acc + ((int64_t)s * T + t) * lda + j);
       v[0] += q.x;
@@ -590,6 +598,124 @@ __global__ __launch_bounds__(256) void head_dx_kernel(const float* __restrict__ 
     }
     store4(dx, t * ld + j, dtype, vec, (int)min((int64_t)4, n - j), v);
   }
+}
+
+// dx of up to four tokens straight from the packed codes, with the sums that a packed head's
+// gradients are where one affine has a row: no planes (32 bytes written and read for eight
+// codes) and no tile of 128 tokens for one.  A lane decodes its row's part of a chunk of columns
+// (SP steps of eight; the more tokens, the fewer) and adds dz a times it to columns of its own;
+// sixteen rows, a workgroup's waves and the splits of the rows are joined after that alone.
+template <int FMT, int TN, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void head_few_dx_kernel(PieceArgs A, QLayer L, bool sums, int splits,
+                                                                 float* __restrict__ out, int64_t lda) {
+  extern __shared__ __attribute__((aligned(16))) uint32_t few_lds[];
+  constexpr int STEPS = q_steps(FMT), SP = few_dx_steps(FMT, TN), PARTS = STEPS / SP, COLS = SP * 32;
+  const int lane = threadIdx.x & 63, wave = wave_id(), kb = lane >> 4;
+  q_lut_fill<FMT, OpF16>(L, few_lds, 64 * WAVES);
+  if (FMT == QF_E8) q_lut_wait<0>();
+  __syncthreads();
+  const int split = (int)(blockIdx.x % splits), place = (int)(blockIdx.x / splits), c = place / PARTS, part = place % PARTS;
+  const int g = L.G > 1 ? (int)((int64_t)c * (STEPS * 32) / L.group) : 0;
+  const float mid = q_centre(L), zmid = A.mid >= 0 ? A.levels[A.mid] : 0.f;
+  float top[TN], scale[TN], own[TN], X[TN], rest[TN], acc[SP * 8][TN];
+  int target[TN];
+  bool read[TN];   // (a token that is not has no s)
+#pragma unroll
+  for (int t = 0; t < TN; ++t) {
+    const bool live = read[t] = t < A.t && A.weight[min((int64_t)t, A.t - 1)] != 0.f;
+    top[t] = live ? A.row_top[t] : 0.f;
+    scale[t] = live ? A.row_scale[t] : 0.f;
+    own[t] = live ? A.row_target[t] : 0.f;
+    X[t] = live ? A.sum[t] : 0.f;
+    target[t] = live ? A.targets[t] : -1;
+    rest[t] = 0.f;
+#pragma unroll
+    for (int k = 0; k < SP * 8; ++k) acc[k][t] = 0.f;
+  }
+  for (int tile = split * WAVES + wave; tile < L.tiles; tile += splits * WAVES) {
+    const uint4 code = L.packed[((size_t)tile * L.chunks + c) * 64 + lane];
+    const int64_t v = (int64_t)tile * 16 + (lane & 15), at = min(v, A.m - 1);
+    const bool live = v < A.m;
+    const float a = L.scale[at * L.G + g], o = fmaf(a, mid, L.offset ? L.offset[at * L.G + g] : 0.f);
+    const float za = A.a ? A.a[at] : 1.f, zo = A.a ? fmaf(za, zmid, A.o ? A.o[at] : 0.f) : 0.f, zb = A.b ? A.b[at] : 0.f;
+    float u[TN], part3[3][4] = {};
+#pragma unroll
+    for (int t = 0; t < TN; ++t) {
+      const float s = A.S[min((int64_t)t, A.t - 1) * A.lds + at], z = fmaf(za, s, fmaf(zo, X[t], zb));
+      float d = target[t] == v ? own[t] : scale[t] == 0.f ? 0.f : __builtin_amdgcn_exp2f((z - top[t]) * H_LOG2E) * scale[t];
+      if (!live) d = 0.f;
+      u[t] = d * a;
+      rest[t] = fmaf(d, o, rest[t]);
+      part3[0][t] = d;
+      part3[1][t] = read[t] ? fmaf(d, fmaf(zmid, X[t], s), 0.f) : 0.f;   // (rounded here: no product joins a sum)
+      part3[2][t] = fmaf(d, X[t], 0.f);
+    }
+    if (sums && place == 0 && kb == 0 && live) {   // (in head_grad_kernel's order)
+      float* const to[3] = {A.dbias, A.dscale, A.doffset};
+#pragma unroll
+      for (int k = 0; k < 3; ++k) to[k][v] = (part3[k][0] + part3[k][1]) + (part3[k][2] + part3[k][3]);
+    }
+    uint4 w = code;
+    if constexpr (PARTS == 2) w = part ? make_uint4(code.z, code.w, 0, 0) : make_uint4(code.x, code.y, 0, 0);
+    if constexpr (PARTS == 4) w = make_uint4(part == 0 ? code.x : part == 1 ? code.y : part == 2 ? code.z : code.w, 0, 0, 0);
+#pragma unroll
+    for (int s = 0; s < SP; ++s) {
+      const v4u e = q_decode<FMT, OpF16>(L, few_lds, w, s);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const float x = OpF16::val(q & 1 ? e[q >> 1] >> 16 : e[q >> 1]);
+#pragma unroll
+        for (int t = 0; t < TN; ++t) acc[s * 8 + q][t] = fmaf(x, u[t], acc[s * 8 + q][t]);
+      }
+    }
+  }
+  __syncthreads();   // (the table's place takes the sums)
+  float* red = reinterpret_cast<float*>(few_lds);   // [WAVES][TN][COLS]
+#pragma unroll
+  for (int t = 0; t < TN; ++t) {
+    const float r = sum16(rest[t]);
+#pragma unroll
+    for (int k = 0; k < SP * 8; ++k) {
+      const float s = sum16(acc[k][t]) + r;
+      if ((lane & 15) == (k & 15)) red[(wave * TN + t) * COLS + ((k >> 3) * 4 + kb) * 8 + (k & 7)] = s;
+    }
+  }
+  __syncthreads();
+  for (int k = threadIdx.x; k < TN * COLS; k += 64 * WAVES) {
+    const int t = k / COLS, q = k % COLS;
+    const int64_t j = ((int64_t)c * STEPS + part * SP) * 32 + q;
+    if (t >= A.t || j >= lda) continue;
+    float s = 0.f;
+    for (int w = 0; w < WAVES; ++w) s += red[(w * TN + t) * COLS + q];
+    out[((int64_t)split * A.t + t) * lda + j] = s;
+  }
+}
+struct FewDx {
+  int tokens, waves, splits;
+  unsigned grid;
+  size_t shared;
+};
+FewDx few_dx_plan(const QLayer& L, int64_t T) {
+  FewDx P;
+  P.tokens = T <= 1 ? 1 : T <= 2 ? 2 : 4;
+  // (E8's table fills a CU's LDS)
+  P.waves = L.fmt == QF_E8 ? 16 : 4;
+  const int steps = few_dx_steps(L.fmt, P.tokens);
+  const int64_t places = (int64_t)L.chunks * (q_steps(L.fmt) / steps), most = L.fmt == QF_E8 ? 256 : 1024;
+  P.splits = (int)std::max<int64_t>(1, std::min({most / places, (L.tiles + P.waves - 1) / (int64_t)P.waves, (int64_t)64}));
+  P.grid = (unsigned)(places * P.splits);
+  P.shared = std::max((size_t)q_lut_words(L.fmt, (L.lut_entries + 3) / 4 * 4) * 4, (size_t)P.waves * P.tokens * steps * 32 * 4);
+  return P;
+}
+template <int FMT, int WAVES>
+hipError_t launch_few_dx(const FewDx& P, const PieceArgs& A, const QLayer& L, bool sums, float* out, int64_t lda, hipStream_t st) {
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(P.grid), dim3(64 * WAVES), P.shared, st, A, L, sums, P.splits, out, lda);
+    return hipGetLastError();
+  };
+  return P.tokens == 1   ? go(head_few_dx_kernel<FMT, 1, WAVES>)
+         : P.tokens == 2 ? go(head_few_dx_kernel<FMT, 2, WAVES>)
+                         : go(head_few_dx_kernel<FMT, 4, WAVES>);
 }
 
 bool whole_quads(const void* p, int64_t ld, int dtype) {
@@ -646,6 +772,8 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
   const HeadTile tile = head_tile(rows, T);
   // Few tokens: straight from the packed codes.
   const bool few = kept && !A.dense && q_few_rows(L, A.dtype, T);
+  // ... and their input gradient (planes_dx: through planes).
+  const bool few_dx = few && A.need_dx && T <= H_FEW, planes_dx = A.need_dx && !few_dx;
   const int64_t seg_rows = T <= 64 ? 1024 : 4096;   // (short segments: as many workgroups as there are CUs)
   // One workgroup a token, start to end. (Longer rows in segments: a token of 32000 logits takes
   // 15.6 us in one workgroup of sixteen waves, 8 in segments with their join.)
@@ -692,8 +820,12 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
   const int64_t lda = (n + 3) / 4 * 4, cblocks = (n + Q_CONTRACT - 1) / Q_CONTRACT;
   int splits = 1, dx_splits = 1;
   // (workspaces are sized without the offset's pointer: room for its sums either way)
-  const bool sums = A.need_dx && !weights && L.has_offset();
-  if (A.need_dx) {
+  const bool sums = planes_dx && !weights && L.has_offset();
+  if (few_dx) {
+    dx_splits = few_dx_plan(L, T).splits;
+    acc = W.take<float>((size_t)dx_splits * T * lda * 4);
+  }
+  if (planes_dx) {
     d = W.take<uint16_t>((size_t)DX * up16(T) * rows * 2);
     dmax = W.take<uint32_t>((size_t)T * 4);
     rowpart = W.take<float>((size_t)T * row_tiles * 4);
@@ -735,7 +867,7 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
   const int64_t xplane = twice ? K.plane_again : K.plane;
   if (!twice) K.again = nullptr;
   K.ones = few && !weights ? ones : nullptr;
-  if (A.need_dx && !weights) {
+  if (planes_dx && !weights) {
     K.scale = L.scale;
     K.fpart = fpart;
   }
@@ -847,20 +979,35 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
   if (!short_rows) H_LAUNCH(head_join_kernel, ((unsigned)((T + 15) / 16)), 256, part, all_segs, T, K.target_z, O);
   if (!grads) return hipSuccess;
   P.raw_d = K.raw;
-  P.own_target = !f32 && (P.raw_d || A.dtype == DT_F16);
-  if (A.need_dx && weights && !in_place) {
+  P.own_target = planes_dx && !f32 && (P.raw_d || A.dtype == DT_F16);
+  if (planes_dx && weights && !in_place) {
     PieceArgs F = P;
     F.m = V;
     F.refs = refs;
     if (few) H_TRY(launch_q_bounds(L, refs, st));
     H_LAUNCH(head_factor_kernel, (64), 256, F, fpart);
   }
+  if (few_dx) {
+    PieceArgs F = P;
+    F.m = V;
+    F.S = S;
+    F.a = weights ? nullptr : L.scale;
+    F.o = weights ? nullptr : L.offset;
+    F.b = A.bias;
+    F.dbias = A.dbias; F.dscale = A.dscale; F.doffset = A.doffset;
+    const bool own_sums = A.need_dhead && !weights;
+    const FewDx D = few_dx_plan(L, T);
+    H_TRY(L.fmt == QF_E8     ? (launch_few_dx<QF_E8, 16>(D, F, L, own_sums, acc, lda, st))
+          : L.fmt == QF_NIB  ? (launch_few_dx<QF_NIB, 4>(D, F, L, own_sums, acc, lda, st))
+          : L.fmt == QF_BYTE ? (launch_few_dx<QF_BYTE, 4>(D, F, L, own_sums, acc, lda, st))
+                             : (launch_few_dx<QF_VEC, 4>(D, F, L, own_sums, acc, lda, st)));
+  }
   // (a single piece's planes are still there)
-  const bool again = pieces > 1 || few;
-  for (int64_t k = 0; k < pieces; ++k) {
-    H_TRY(piece(k, again && (!kept || A.need_dx), kept ? WX : WP));   // (kept: for dx alone)
+  const bool again = pieces > 1 || few, rest = planes_dx || product || (A.need_dhead && !few_dx);
+  for (int64_t k = 0; k < pieces && rest; ++k) {
+    H_TRY(piece(k, again && (!kept || planes_dx), kept ? WX : WP));   // (kept: for dx alone)
     const int64_t r0 = P.row0, nr = P.m, mp = P.mp;
-    P.d = A.need_dx ? d : nullptr;
+    P.d = planes_dx ? d : nullptr;
     P.rowpart = sums ? rowpart : nullptr;
     P.dt = product ? dt : nullptr;
     const bool straight = kept && ttiles == 1;   // no tiles of tokens to add up
@@ -881,7 +1028,7 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
                weights ? nullptr : A.dscale + r0, weights ? nullptr : A.doffset + r0);
     if (sums) H_LAUNCH(head_rowsum_kernel, ((unsigned)((T + 3) / 4)), 256, rowpart,
                        kept ? mp / 64 : (nr + own.rows - 1) / own.rows, T, k == 0, rowadd);
-    if (A.need_dx) {
+    if (planes_dx) {
       gx.A = gz.A; gx.lda = gz.lda; gx.planeA = gz.planeA;
       gx.bf16 = gz.bf16;
       gx.acols = Kp; gx.arows = nr;

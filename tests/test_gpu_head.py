@@ -220,6 +220,28 @@ def test_packed_groups(dtype, name, n, group, t):
     packed_case(name, 210, n, t, dtype, group=group, seed=n + t, padded=t > 1)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("name,n,group", [("s3", 256, 0), ("s16", 500, 0), ("s16", 1152, 128), ("s64", 333, 0), ("s64", 320, 64),
+                                          ("levels", 130, 0), ("vec", 264, 0), ("e8240", 520, 0), ("e865536", 1096, 0)])
+@pytest.mark.parametrize("t", [1, 2, 3, 4, 5])
+def test_few_tokens(dtype, name, n, group, t):
+    """The gradients of some tokens, straight from the codes or through planes; rows behind a last whole tile."""
+    packed_case(name, 1003, n, t, dtype, group=group, seed=n + t, padded=t == 4)
+
+
+@pytest.mark.parametrize("t", [1, 3])
+@pytest.mark.parametrize("name", ["s16", "e8240"])
+def test_few_tokens_wanted_outputs(name, t):
+    """The parts alone are the bits of the whole here too; a long vocabulary, many splits of its rows."""
+    import torch
+    import post_quantization_solver_amd as mpq
+    head, x, targets, b, w, full = packed_case(name, 20011, 64, t, "bf16", seed=t)
+    for need_dx, need_dhead in ((False, False), (True, False), (False, True)):
+        got = mpq.linear_cross_entropy(x, head, targets, bias=b, weights=w, need_dx=need_dx, need_dhead=need_dhead)
+        for k, v in got.items():
+            assert v is None or torch.equal(v, full[k]), k
+
+
 @pytest.mark.parametrize("need_dx,need_dhead", [(False, False), (True, False), (False, True)])
 def test_wanted_outputs(need_dx, need_dhead):
     """The parts alone are the bits of the whole."""
