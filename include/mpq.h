@@ -612,10 +612,13 @@ int mpq_distill(const void* logits, int dtype, int64_t t, int64_t V, int64_t ld,
  * (elements below 2^-28 of their row's largest lose bits, those below 2^-39 are gone),
  * two (22 bits) for float32; the weights of column groups as two terms.  For dx, dz
  * (under a power of two per token) and the weights of column groups enter as one term
- * (11 bits; float32: two); for the gradients of column groups dz as two.
- * 1 <= m, 0 <= t < 2^22, ceil(t / 64) ceil(n / 64) < 2^24.  The workspace holds some
- * 128 MB of operands and of logits each, or 1024 rows of the head's; t = 0: gradients
- * of zero. */
+ * (11 bits; float32: two; for a float16 x the target's term of dx is float32; up
+ * to four tokens' dx is float32 all in all, but for groups that end inside a chunk of the packed
+ * codes); for the gradients of column groups dz as two.
+ * 1 <= m, 0 <= t < 2^22, ceil(t / 64) ceil(n / 64) < 2^24.  The workspace holds the
+ * logits where they take up to 128 MB; of the head's operands up to 512 MB then, else
+ * 256 MB, or 1024 rows; and for those rows what the gradients take (dz: t x rows x 2 or
+ * 4 bytes).  t = 0: gradients of zero. */
 size_t mpq_linear_cross_entropy_workspace_bytes(int dtype, int64_t t, int64_t m, int64_t n, int64_t K, int64_t d,
                                                 int64_t group);
 int mpq_linear_cross_entropy(const void* x, int dtype, int64_t t, int64_t ldx, const void* packed, int64_t m, int64_t n,
@@ -664,8 +667,8 @@ int mpq_matrix_cross_entropy(const void* x, int dtype, int64_t t, int64_t ldx, c
  * (2^F + f) 2^(E - 1); the largest of 256 has the largest code.  Codes are rounded
  * up or down at random with the probability of where the value (of a root: its
  * square, so that m and v are what they would be on average) lies between them (a root
- * that is not zero, never to zero), and so are 16-bit parameters: the random bits are a hash of (seed, t, place in the moments), and the same call
- * gives the same bits.  State of 8 bits is computed in float64.  step: device
+ * that is not zero, never to zero), and so are 16-bit parameters: the random bits are a
+ * hash of (seed, t, place in the moments), and the same call gives the same bits.  State of 8 bits is computed in float64.  step: device
  * int32, the number of steps taken, counted by the call (0 at first).
  *
  * grads: HOST array of `count` device pointers, gradients in their parameters'
@@ -679,7 +682,8 @@ int mpq_matrix_cross_entropy(const void* x, int dtype, int64_t t, int64_t ldx, c
  * and writes device memory alone once it is enqueued, so that it may be captured and
  * replayed with gradients at the same addresses.
  * Errors: MPQ_ENULL, MPQ_ESHAPE (state.elements), MPQ_EPARAM (betas outside [0, 1),
- * eps <= 0, grad_scale, max_norm or lr_scale out of range, state.bits, a plan that mpq_adamw_plan did not fill). */
+ * eps <= 0, grad_scale, max_norm or lr_scale out of range, state.bits, a plan that
+ * mpq_adamw_plan did not fill). */
 typedef struct {
   void* param;
   int64_t count, at;

@@ -135,8 +135,7 @@ int matrix_shape(QLayer& L, int64_t m, int64_t n) {
   return MPQ_OK;
 }
 
-// Grids of 256 threads a workgroup (fewer than 2^32 in all): the transpose of x in
-// tiles of 64 x 64, 16 entries of a piece's affine a workgroup.
+// Grids of fewer than 2^32 threads: a workgroup per token, tiles of dx of 64 x 64 at least.
 bool head_fits(const HeadArgs& A) {
   return A.t >= 0 && A.t < HEAD_MAX_T && A.L.m >= 1 && (A.t + 63) / 64 * ((A.L.n + 63) / 64) < (int64_t)1 << 24;
 }

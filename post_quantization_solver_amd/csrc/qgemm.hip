@@ -48,6 +48,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void q_gemm_kernel(QGemm g, float*
   float* own = reg + qrow * PITCH + qcol;   // and every RPI rows from there
   const QCol C = q_col4(g.O, ii);
   auto slot = [&](int it) { return reinterpret_cast<v4f*>(own + it * RPI * PITCH); };
+  QLevels levels = {0.f, 0.f};
+  float shared = 1.f;
+  if (g.cpart) {
+    levels = q_levels(g.L);
+    if (g.O.one_rowmax) shared = pow2(-pow2_shift(g.O.rowmax[0]));
+  }
 #pragma unroll 1
   for (int j = 0; j < SN; ++j) {   // (one copy of the body; the accumulators by constant index)
 #pragma unroll
@@ -60,19 +66,21 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void q_gemm_kernel(QGemm g, float*
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
     const int64_t jj = j0 + (wn * SN + j) * 16 + qrow;   // and every RPI rows from there
-    if (g.cpart) {
+    if (g.cpart) {   // (rows past the last: of its sixteen, or of the last)
+      const uint16_t* codes = q_code4_at(g.L, (g.row0 + min(j0 + (wn * SN + j) * 16, (g.N - 1) & ~(int64_t)15)) >> 4,
+                                         min(ii, (g.M - 1) & ~(int64_t)3));
       uint32_t code[IT];
       float f[IT];
 #pragma unroll
       for (int it = 0; it < IT; ++it) {
         const int64_t row = min(jj + it * RPI, g.N - 1);
-        code[it] = q_code4(g.L, g.row0 + row, min(ii, (g.M - 1) & ~(int64_t)3));
-        f[it] = pow2(-pow2_shift(g.O.rowmax[g.O.one_rowmax ? 0 : row]));
+        code[it] = q_code4_of(g.L, codes, qrow + it * RPI);
+        f[it] = g.O.one_rowmax ? shared : pow2(-pow2_shift(g.O.rowmax[row]));
       }
 #pragma unroll
       for (int it = 0; it < IT; ++it) {
         float e[4], se = 0.f, s1 = 0.f;
-        q_entries4(g.L, code[it], ii, e);
+        q_entries4(g.L, levels, code[it], ii, e);
         const v4f x = *slot(it);
 #pragma unroll
         for (int k = 0; k < 4; ++k)

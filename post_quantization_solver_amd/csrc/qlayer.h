@@ -383,17 +383,35 @@ __device__ __forceinline__ void q_finish4(const QOut& O, int64_t j, int64_t i, f
 // The entries of row i's columns j .. j + 3 (j a multiple of 4, inside the packed
 // chunks): the code's bits first, then the entries, so that loads of several
 // quads can be on their way together.
-__device__ __forceinline__ uint32_t q_code4(const QLayer& L, int64_t i, int64_t j) {
+// (A row's code lies 16 bytes after the one before it, within their sixteen: q_code4_at for
+// the sixteen's first, q_code4_of for a row of them.)
+__device__ __forceinline__ const uint16_t* q_code4_at(const QLayer& L, int64_t block, int64_t j) {
   const int steps = q_steps(L.fmt);
-  const uint16_t* codes = reinterpret_cast<const uint16_t*>(L.packed);
   const int64_t blk = j >> 3, c = blk / (4 * steps);
   const int kb = (int)(blk & 3), s = (int)(blk - c * 4 * steps) >> 2, half = (int)(j >> 2) & 1;
-  const size_t at = (((size_t)(i >> 4) * L.chunks + c) * 64 + kb * 16 + (i & 15)) * 8;   // 16-bit words
-  if (L.fmt == QF_NIB) return *reinterpret_cast<const uint32_t*>(codes + at + s * 2);
-  if (L.fmt == QF_BYTE) return *reinterpret_cast<const uint32_t*>(codes + at + s * 4 + half * 2);
-  return codes[at + s];
+  const size_t at = (((size_t)block * L.chunks + c) * 64 + kb * 16) * 8;   // 16-bit words
+  return reinterpret_cast<const uint16_t*>(L.packed) + at + (L.fmt == QF_NIB ? s * 2 : L.fmt == QF_BYTE ? s * 4 + half * 2 : s);
 }
-__device__ __forceinline__ void q_entries4(const QLayer& L, uint32_t code, int64_t j, float* e) {
+__device__ __forceinline__ uint32_t q_code4_of(const QLayer& L, const uint16_t* first, int row) {
+  first += row * 8;
+  return L.fmt == QF_NIB || L.fmt == QF_BYTE ? *reinterpret_cast<const uint32_t*>(first) : *first;
+}
+__device__ __forceinline__ uint32_t q_code4(const QLayer& L, int64_t i, int64_t j) {
+  return q_code4_of(L, q_code4_at(L, i >> 4, j), (int)(i & 15));
+}
+// (base, step: of uniform levels)
+struct QLevels {
+  float base, step;
+};
+__device__ __forceinline__ QLevels q_levels(const QLayer& L) {
+  QLevels v = {0.f, 0.f};
+  if ((L.fmt == QF_NIB || L.fmt == QF_BYTE) && L.uniform) {
+    v.base = L.levels[0];
+    v.step = L.levels[1] - v.base;
+  }
+  return v;
+}
+__device__ __forceinline__ void q_entries4(const QLayer& L, const QLevels& v, uint32_t code, int64_t j, float* e) {
   const int half = (int)(j >> 2) & 1;
   if (L.fmt == QF_NIB || L.fmt == QF_BYTE) {
     uint32_t q[4];
@@ -402,22 +420,24 @@ __device__ __forceinline__ void q_entries4(const QLayer& L, uint32_t code, int64
       q[k] = L.fmt == QF_NIB ? (code >> (8 * half + 4 * (k >> 1) + 16 * (k & 1))) & 15u
                              : (code >> (8 * (k >> 1) + 16 * (k & 1))) & 63u;
     if (L.uniform) {   // (exactly the same, and no look-up)
-      const float base = L.levels[0], step = L.levels[1] - base;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) e[k] = fmaf((float)q[k], step, base);
+      for (int k = 0; k < 4; ++k) e[k] = fmaf((float)q[k], v.step, v.base);
     } else {
 #pragma unroll
       for (int k = 0; k < 4; ++k) e[k] = L.levels[q[k]];
     }
   } else if (L.fmt == QF_E8) {
-    const uint32_t v = q_e8_nibbles(L, L.lut, code);
+    const uint32_t w = q_e8_nibbles(L, L.lut, code);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      e[k] = 0.5f * (float)((int)((v >> (8 * half + 4 * (k >> 1) + 16 * (k & 1))) & 15u) - 8);
+      e[k] = 0.5f * (float)((int)((w >> (8 * half + 4 * (k >> 1) + 16 * (k & 1))) & 15u) - 8);
   } else {
     const float4 q = *reinterpret_cast<const float4*>(L.e32 + (size_t)code * 8 + half * 4);
     e[0] = q.x; e[1] = q.y; e[2] = q.z; e[3] = q.w;
   }
+}
+__device__ __forceinline__ void q_entries4(const QLayer& L, uint32_t code, int64_t j, float* e) {
+  q_entries4(L, q_levels(L), code, j, e);
 }
 #endif
 
