@@ -16,8 +16,14 @@
 // Order.  The vocabulary goes in pieces of some thousand rows: the piece's
 // operand planes, its logits, and of each token the largest and the sum of the
 // exponentials.  Once all pieces have gone by (R is known) they come again for the
-// gradients: logits once more, dz, its products.  A vocabulary that is one
-// piece is multiplied once.
+// gradients: logits once more, dz, its products.  Logits that fit are kept instead, and
+// multiplied once.
+//
+// Bound.  Many tokens: the products, see headgemm.hip (2048 x 128256 x 4096 E8: 1.64 ms for
+// the loss, 5.24 with the gradients of the layer's affine and of x, of which 0.22 and 0.46 lay
+// the planes out at 5.4 TB/s).  Logits that are kept (509 x 50257 x 2048, groups of 128: 0.93
+// ms): the products take 0.70, planes 0.13, dz 0.07.  A token (32000 x 4096 E8: 40 us): the
+// few-row product of the codes, 26.
 #include <string.h>
 #include <math.h>
 #include <algorithm>
@@ -42,8 +48,11 @@ struct Carve {
   }
 };
 
-// What logits that are kept, or a piece's operands, should take: half of the last-level
-// cache; the planes of a head whose logits are kept, which both passes read: four times that.
+// What logits that are kept should take (half of the last-level cache); a piece's planes, and
+// its dz; the planes of a head whose logits are kept, which both passes read.  (Measured, 2048 x
+// 128256 x 4096 E8 with gradients, pieces of 64, 128, 256, 512 MB: 5.84, 5.55, 5.35, 5.27 ms, the
+// last for twice the workspace; 509 x 50257 x 2048, groups of 128: planes in pieces, laid out
+// twice, 1.28 ms, in one piece of 412 MB 1.01.)
 // Tokens whose input gradient comes straight from the packed codes.  Measured, whole calls with
 // gradients, 4 tokens so | 5 through planes: E8 128256 x 4096 323 | 600 us, 32000 x 2048 72 | 97;
 // 4 bits 32000 x 4096 102 | 165, groups of 128 117 | 232; 6 bits 32000 x 2048 80 | 114.  (One
@@ -177,7 +186,8 @@ struct DenseArgs {
 };
 
 // Rows' largest magnitudes and planes: a wave per row of the planes, which keeps a row of
-// up to 2048 columns in registers (longer ones are read again).
+// up to 2048 columns in registers (longer ones are read again).  32000 x 1024 float32, two
+// terms: 66 us for 262 MB, 4 TB/s (a workgroup per row, which reads each twice: 75).
 __global__ __launch_bounds__(256) void head_dense_kernel(DenseArgs A) {
   constexpr int HOLD = 4;
   const int lane = threadIdx.x & 63;
@@ -431,7 +441,9 @@ __global__ __launch_bounds__(256) void head_factor_kernel(PieceArgs A, float* __
   if (threadIdx.x == 0) out[blockIdx.x] = bits_max(bits_max(red[0], red[1]), bits_max(red[2], red[3]));
 }
 
-// A 64 x 64 tile of dz: its planes, its transpose's, its rows' and columns' sums.
+// A 64 x 64 tile of dz: its planes, its transpose's (turned in LDS: a lane stores four
+// tokens of a row), its rows' and columns' sums.  509 x 50257, with the transpose in two
+// terms: 70 us for 258 MB, 3.7 TB/s; vector instructions 63 % of the clocks.
 __global__ __launch_bounds__(256) void head_grad_kernel(PieceArgs A) {
   __shared__ float tl[64][65];
   __shared__ float cs[3][4][64];
@@ -774,7 +786,9 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
   const bool few = kept && !A.dense && q_few_rows(L, A.dtype, T);
   // ... and their input gradient (planes_dx: through planes).
   const bool few_dx = few && A.need_dx && T <= H_FEW, planes_dx = A.need_dx && !few_dx;
-  const int64_t seg_rows = T <= 64 ? 1024 : 4096;   // (short segments: as many workgroups as there are CUs)
+  // (A token of 32000 logits: 32 segments of 1024, with their join 10 us; 8 of 4096 would leave
+  // most CUs without one.  Many tokens: 509 x 50257, 4096 rows a workgroup 32 us.)
+  const int64_t seg_rows = T <= 64 ? 1024 : 4096;
   // One workgroup a token, start to end. (Longer rows in segments: a token of 32000 logits takes
   // 15.6 us in one workgroup of sixteen waves, 8 in segments with their join.)
   const bool short_rows = kept && V <= 16384;

@@ -50,6 +50,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void q_gemm_kernel(QGemm g, float*
   auto slot = [&](int it) { return reinterpret_cast<v4f*>(own + it * RPI * PITCH); };
   QLevels levels = {0.f, 0.f};
   float shared = 1.f;
+  const bool nib = g.L.fmt == QF_NIB;
   if (g.cpart) {
     levels = q_levels(g.L);
     if (g.O.one_rowmax) shared = pow2(-pow2_shift(g.O.rowmax[0]));
@@ -77,26 +78,36 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void q_gemm_kernel(QGemm g, float*
         code[it] = q_code4_of(g.L, codes, qrow + it * RPI);
         f[it] = g.O.one_rowmax ? shared : pow2(-pow2_shift(g.O.rowmax[row]));
       }
+      auto contract = [&](auto entries) {
 #pragma unroll
-      for (int it = 0; it < IT; ++it) {
-        float e[4], se = 0.f, s1 = 0.f;
-        q_entries4(g.L, levels, code[it], ii, e);
-        const v4f x = *slot(it);
+        for (int it = 0; it < IT; ++it) {
+          float e[4], se = 0.f, s1 = 0.f;
+          entries(code[it], e);
+          const v4f x = *slot(it);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (k < C.live) {
-            const float v = x[k] * C.a[k] * f[it];
+          for (int k = 0; k < 4; ++k) {
+            const float v = k < C.live ? x[k] * C.a[k] * f[it] : 0.f;
             se = fmaf(e[k], v, se);
             s1 += v;
           }
-        // sixteen lanes hold one row's 64 columns
-        se += dpp_f<DPP_XOR1>(se); s1 += dpp_f<DPP_XOR1>(s1);
-        se += dpp_f<DPP_XOR2>(se); s1 += dpp_f<DPP_XOR2>(s1);
-        se += dpp_f<DPP_HALF_MIRROR>(se); s1 += dpp_f<DPP_HALF_MIRROR>(s1);
-        se += dpp_f<DPP_MIRROR>(se); s1 += dpp_f<DPP_MIRROR>(s1);
-        if ((lane & 15) == 0 && jj + it * RPI < g.N && C.live > 0)
-          g.cpart[((size_t)split * g.N + jj + it * RPI) * g.cblocks + ii / Q_CONTRACT] = make_float2(se, s1);
-      }
+          // sixteen lanes hold one row's 64 columns
+          se += dpp_f<DPP_XOR1>(se); s1 += dpp_f<DPP_XOR1>(s1);
+          se += dpp_f<DPP_XOR2>(se); s1 += dpp_f<DPP_XOR2>(s1);
+          se += dpp_f<DPP_HALF_MIRROR>(se); s1 += dpp_f<DPP_HALF_MIRROR>(s1);
+          se += dpp_f<DPP_MIRROR>(se); s1 += dpp_f<DPP_MIRROR>(s1);
+          if ((lane & 15) == 0 && jj + it * RPI < g.N && C.live > 0)
+            g.cpart[((size_t)split * g.N + jj + it * RPI) * g.cblocks + ii / Q_CONTRACT] = make_float2(se, s1);
+        }
+      };
+      if ((g.L.fmt == QF_NIB || g.L.fmt == QF_BYTE) && g.L.uniform)   // (no branch in the loop)
+        contract([&](uint32_t c, float* e) {
+          c >>= nib ? 8 * (qcol >> 2 & 1) : 0;
+          const uint32_t q[4] = {c, c >> 16, c >> (nib ? 4 : 8), c >> (nib ? 20 : 24)};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) e[k] = fmaf((float)(q[k] & (nib ? 15u : 63u)), levels.step, levels.base);
+        });
+      else
+        contract([&](uint32_t c, float* e) { q_entries4(g.L, levels, c, ii, e); });
     } else if (part) {
       // rows of part are padded to four columns
 #pragma unroll

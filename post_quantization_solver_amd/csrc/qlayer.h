@@ -336,21 +336,36 @@ struct QCol {
   float a[4], o[4], b[4];
   int live;   // columns there are (<= 0: none)
 };
+// (vectors of the columns may begin at any element)
+typedef float v4f_any __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t v4u_any __attribute__((ext_vector_type(4), aligned(4)));
 __device__ __forceinline__ QCol q_col4(const QOut& O, int64_t i) {
   QCol C;
   C.live = (int)min((int64_t)4, O.cols - i);
   const float mid = O.colscale && O.mid >= 0 ? O.levels[O.mid] : 0.f;
+  v4f_any b = {0.f, 0.f, 0.f, 0.f}, a = {1.f, 1.f, 1.f, 1.f}, o = b;
+  v4u_any top = {0u, 0u, 0u, 0u};   // (factor 1)
+  if (C.live == 4) {   // all of them on their way together
+    if (O.bias) b = *reinterpret_cast<const v4f_any*>(O.bias + i);
+    if (O.colscale) a = *reinterpret_cast<const v4f_any*>(O.colscale + i);
+    if (O.colscale && O.coloff) o = *reinterpret_cast<const v4f_any*>(O.coloff + i);
+    if (O.colmax) top = *reinterpret_cast<const v4u_any*>(O.colmax + i);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      if (k >= C.live) continue;
+      if (O.bias) b[k] = O.bias[i + k];
+      if (O.colscale) a[k] = O.colscale[i + k];
+      if (O.colscale && O.coloff) o[k] = O.coloff[i + k];
+      if (O.colmax) top[k] = O.colmax[i + k];
+    }
+  }
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    C.a[k] = C.o[k] = 1.f;
-    C.b[k] = 0.f;
-    if (k >= C.live) continue;
-    if (O.bias) C.b[k] = O.bias[i + k];
-    if (O.colscale) {
-      C.a[k] = O.colscale[i + k];
-      C.o[k] = fmaf(C.a[k], mid, O.coloff ? O.coloff[i + k] : 0.f);
-    }
-    if (O.colmax) C.a[k] *= pow2(-pow2_shift(O.colmax[i + k]));
+    C.b[k] = b[k];
+    C.a[k] = a[k];
+    C.o[k] = O.colscale ? fmaf(a[k], mid, o[k]) : 1.f;
+    C.a[k] *= pow2(-pow2_shift(top[k]));
   }
   return C;
 }
