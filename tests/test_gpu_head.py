@@ -242,6 +242,53 @@ def test_few_tokens_wanted_outputs(name, t):
             assert v is None or torch.equal(v, full[k]), k
 
 
+@pytest.mark.parametrize("name,group", [("s16", 0), ("s16", 128), ("s64", 0), ("e8240", 0), ("vec", 0)])
+def test_few_tokens_that_are_not_read(name, group):
+    """Of four tokens: one without a target and NaN in its row, one of weight 0 with infinities, one past the vocabulary;
+    a vocabulary with rows masked by -inf; a workspace that held something else."""
+    import torch
+    import post_quantization_solver_amd as mpq
+    head, x, targets, b, w, _ = packed_case(name, 700, 256, 4, "bf16", group=group, seed=8)
+    ws = torch.full((64 << 20,), 255, dtype=torch.uint8, device="cuda")
+    b[::3] = -float("inf")
+    targets.copy_(torch.tensor([4, 5, 7, 10], dtype=torch.int32))
+    alone = [mpq.linear_cross_entropy(x[k:k + 1], head, targets[k:k + 1], bias=b, weights=w[k:k + 1]) for k in range(4)]
+    targets[0], w[1] = -1, 0.0
+    x[0], x[1] = float("nan"), float("inf")
+    got = mpq.linear_cross_entropy(x, head, targets, bias=b, weights=w, workspace=ws)
+    assert not got["loss"][:2].any() and not got["dx"][:2].any()
+    for k in (2, 3):   # (sums of another split: dx is rounded to bfloat16, 2^-8 of a value near the row's largest at most)
+        assert torch.isfinite(got["loss"][k]) and (got["loss"][k] - alone[k]["loss"][0]).abs() <= 2.0 ** -18 * got["loss"][k].abs()
+        one = alone[k]["dx"][0].float()
+        assert ((got["dx"][k].float() - one).abs() <= 2.0 ** -7 * one.abs() + 2.0 ** -14 * one.abs().max()).all()
+    assert not got["dbias"][::3].any()
+    total = alone[2]["dbias"].double() + alone[3]["dbias"].double()
+    assert ((got["dbias"].double() - total).abs() <= 2.0 ** -17 * (alone[2]["dbias"].abs() + alone[3]["dbias"].abs())).all()
+    targets[2] = 700
+    got2 = mpq.linear_cross_entropy(x, head, targets, bias=b, weights=w, workspace=ws)
+    assert torch.isnan(got2["loss"][2]) and torch.isnan(got2["dx"][2]).all()
+    assert torch.equal(got2["loss"][3], got["loss"][3]) and torch.equal(got2["dx"][3], got["dx"][3])
+    assert not got2["dx"][:2].any()
+
+
+def test_addresses_past_32_bits():
+    """Activations and their gradient of more than 2^31 elements: the first and the last tokens."""
+    import torch
+    import post_quantization_solver_amd as mpq
+    t, n, m = 33000, 65536, 96
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.empty(t, n, dtype=torch.bfloat16, device="cuda")
+    for k in range(0, t, 3300):
+        x[k:k + 3300] = torch.randn(3300, n, generator=gen, device="cuda")
+    W = (torch.randn(m, n, generator=gen, device="cuda") * (3.0 / 256)).to(torch.bfloat16)
+    targets = torch.randint(m, (t,), generator=gen, device="cuda", dtype=torch.int32)
+    w = torch.ones(t, device="cuda")
+    got = mpq.linear_cross_entropy(x, W, targets, need_dhead=False)
+    for part in (slice(0, 40), slice(t - 40, t)):
+        ref = reference(x[part], dict(W=W), targets[part], None, w[part])
+        check(dict(loss=got["loss"][part], dx=got["dx"][part], dbias=None), ref, "bf16", n, True, "matrix", need_dhead=False)
+
+
 @pytest.mark.parametrize("need_dx,need_dhead", [(False, False), (True, False), (False, True)])
 def test_wanted_outputs(need_dx, need_dhead):
     """The parts alone are the bits of the whole."""
