@@ -195,18 +195,26 @@ __global__ __launch_bounds__(256) void q_prep_kernel(PrepArgs A) {
   }
 }
 
-// Eight weights of row i from their entries, times f.
+// Eight weights from their entries, times f; columns from j0 on, n in all.
+__device__ __forceinline__ void weights8_of(float a, float o, v4u e, int64_t j0, int64_t n, float f, float* v) {
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+    v[q] = j0 + q < n ? fmaf(a, OpF16::val(q & 1 ? e[q >> 1] >> 16 : e[q >> 1] & 0xffffu), o) * f : 0.f;
+}
+// A column's group (32 bits: a division of 64 costs more than all the rest).
+__device__ __forceinline__ uint32_t group_of(const QLayer& L, int64_t j) {
+  return (uint32_t)min(j, L.n - 1) / (uint32_t)L.group;
+}
+// The same of row i, whatever the groups.
 __device__ __forceinline__ void weights8(const QLayer& L, int64_t i, int64_t j0, v4u e, float mid, float f, float* v) {
   if (L.group % 8 == 0 || L.G == 1) {   // one group
-    const int64_t g = i * L.G + (L.G > 1 ? min(j0, L.n - 1) / L.group : 0);
+    const int64_t g = i * L.G + (L.G > 1 ? group_of(L, j0) : 0);
     const float a = L.scale[g], o = fmaf(a, mid, L.offset ? L.offset[g] : 0.f);
-#pragma unroll
-    for (int q = 0; q < 8; ++q)
-      v[q] = j0 + q < L.n ? fmaf(a, OpF16::val(q & 1 ? e[q >> 1] >> 16 : e[q >> 1] & 0xffffu), o) * f : 0.f;
+    weights8_of(a, o, e, j0, L.n, f, v);
   } else {
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      const int64_t g = i * L.G + min(j0 + q, L.n - 1) / L.group;
+      const int64_t g = i * L.G + group_of(L, j0 + q);
       const float a = L.scale[g], o = fmaf(a, mid, L.offset ? L.offset[g] : 0.f);
       v[q] = j0 + q < L.n ? fmaf(a, OpF16::val(q & 1 ? e[q >> 1] >> 16 : e[q >> 1] & 0xffffu), o) * f : 0.f;
     }
@@ -225,12 +233,19 @@ __global__ __launch_bounds__(64 * WAVES) void q_unpack_kernel(QLayer L, int tile
   if (FMT == QF_E8) q_lut_wait<0>();
   __syncthreads();
   const float mid = q_centre(L);
+  const bool whole = L.G == 1 || L.group % q_chunk(FMT) == 0;   // a chunk has one affine
   const int64_t total = (int64_t)tiles * L.chunks;
   for (int64_t w = (int64_t)blockIdx.x * WAVES + wave; w < total; w += (int64_t)gridDim.x * WAVES) {
     const int tl = (int)(w / L.chunks), c = (int)(w - (int64_t)tl * L.chunks);
     const uint4 code = L.packed[((size_t)(tile0 + tl) * L.chunks + c) * 64 + lane];
     const int64_t row = tl * 16 + (lane & 15), i = (int64_t)tile0 * 16 + row;
     const float f = planes ? pow2(pow2_shift(refs[min(i, L.m - 1)])) : 1.f;
+    float a = 1.f, o1 = 0.f;
+    if (planes && whole) {
+      const int64_t g = min(i, L.m - 1) * L.G + (L.G > 1 ? group_of(L, (int64_t)c * q_chunk(FMT)) : 0);
+      a = L.scale[g];
+      o1 = fmaf(a, mid, L.offset ? L.offset[g] : 0.f);
+    }
 #pragma unroll
     for (int s = 0; s < q_steps(FMT); ++s) {
       const int64_t j0 = (((int64_t)c * q_steps(FMT) + s) * 4 + (lane >> 4)) * 8;
@@ -248,7 +263,8 @@ __global__ __launch_bounds__(64 * WAVES) void q_unpack_kernel(QLayer L, int tile
       } else if constexpr (T::HALF) {
         float v[8];
         v4u o[2];
-        weights8(L, min(i, L.m - 1), j0, e, mid, f, v);
+        if (whole) weights8_of(a, o1, e, j0, L.n, f, v);
+        else weights8(L, min(i, L.m - 1), j0, e, mid, f, v);
         weight_terms(v, o);
         *reinterpret_cast<v4u*>(dst) = o[0];
         if (planes > 1) *reinterpret_cast<v4u*>(dst + plane) = o[1];
