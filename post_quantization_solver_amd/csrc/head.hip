@@ -21,8 +21,8 @@
 //
 // Bound.  Many tokens: the products, see headgemm.hip (2048 x 128256 x 4096 E8: 1.64 ms for
 // the loss, 5.24 with the gradients of the layer's affine and of x, of which 0.22 and 0.46 lay
-// the planes out at 5.4 TB/s).  Logits that are kept (509 x 50257 x 2048, groups of 128: 0.93
-// ms): the products take 0.70, planes 0.13, dz 0.07.  A token (32000 x 4096 E8: 40 us): the
+// the planes out at 5.4 TB/s).  Logits that are kept (509 x 50257 x 2048, groups of 128: 0.89
+// ms): the products take 0.66, planes 0.11, dz 0.07.  A token (32000 x 4096 E8: 40 us): the
 // few-row product of the codes, 26.
 #include <string.h>
 #include <math.h>
@@ -780,6 +780,9 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
   int64_t rows = (kept ? H_PLANES : H_PIECE) / (WP * Kp * 2);
   if (!kept) rows = std::min(rows, H_PIECE / (T * 4));
   rows = std::min(std::max(rows / 256 * 256, H_ROWS), lds);
+  // (a wave per group of a row sums up a dW in memory: fewer than 2^32 threads; whatever is wanted,
+  // as the workspace is sized)
+  if (!A.dense && !contract) rows = std::min(rows, (((int64_t)1 << 26) - 1) / L.G / 256 * 256);
   const int64_t pieces = (V + rows - 1) / rows;
   const HeadTile tile = head_tile(rows, T);
   // Few tokens: straight from the packed codes.

@@ -265,19 +265,20 @@ struct DxPlan {
   int64_t tiles;
   int splits;
 };
-// The tile and the splits of `steps` of the least time, by what a step of a round of
-// workgroups takes (0.82, 0.46 and 0.55 us, the last with two on each CU, as rounds of these
-// kernels measure), and what a split's sum does, read and written (4 TB/s).
+// The tile and the splits of `steps` of the least time, by what a round of workgroups takes
+// (24 us to begin and end, and a step 0.82, 0.55 and 0.62, the last with two on each CU: 512
+// steps of 256 x 256 420 us, 98 of them 108; 196 of 256 x 128 136, 143 98; 143 of 128 x 128
+// 112), and what a split's sum does, read and written (4 TB/s).
 DxPlan dx_plan(int64_t n, int64_t T, int64_t steps) {
   constexpr int bm[3] = {256, 256, 128}, bn[3] = {256, 128, 128}, slots[3] = {256, 256, 512};
-  constexpr double step_us[3] = {0.82, 0.46, 0.55};
+  constexpr double step_us[3] = {0.82, 0.55, 0.62};
   DxPlan best = {0, 0, 1};
   double least = 1e30;
   for (int tile = 0; tile < 3; ++tile) {
     const int64_t tiles = (n + bm[tile] - 1) / bm[tile] * ((T + bn[tile] - 1) / bn[tile]);
     for (int splits = 1; splits <= 32 && (splits == 1 || steps / splits >= 8); ++splits) {
       const double rounds = (double)((tiles * splits + slots[tile] - 1) / slots[tile]);
-      const double us = rounds * (double)((steps + splits - 1) / splits) * step_us[tile] + splits * (double)(T * n) * 8.0 / 4e6;
+      const double us = rounds * (24.0 + (double)((steps + splits - 1) / splits) * step_us[tile]) + splits * (double)(T * n) * 8.0 / 4e6;
       if (us < least) {
         least = us;
         best = {tile, tiles, splits};

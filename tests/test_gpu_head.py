@@ -271,6 +271,23 @@ def test_few_tokens_that_are_not_read(name, group):
     assert not got2["dx"][:2].any()
 
 
+def test_a_column_a_group():
+    """As many groups as columns: more than a grid can sum up in one piece."""
+    import torch
+    import post_quantization_solver_amd as mpq
+    m, n, t = 33000, 2048, 3
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    codes = torch.randint(16, (m, n), generator=gen, device="cuda", dtype=torch.int32)
+    E = np.arange(16, dtype=np.float64)[:, None] - 7.5
+    a = torch.rand(m, n, generator=gen, device="cuda") * 0.01 + 0.005
+    o = torch.randn(m, n, generator=gen, device="cuda") * 0.01
+    layer = mpq.pack_layer(codes, E, a, o, group=1)
+    x, targets, b, w = inputs(np.random.default_rng(7), m, n, t, "bf16", True, False, 0, 0)
+    got = mpq.linear_cross_entropy(x, layer, targets, bias=b, weights=w)
+    head = dict(e=codes.double() - 7.5, a=a.double(), o=o.double(), mid=0.5, col=torch.arange(n, device="cuda"))
+    check(got, reference(x, head, targets, b, w), "bf16", n, False, "groups", head)
+
+
 def test_addresses_past_32_bits():
     """Activations and their gradient of more than 2^31 elements: the first and the last tokens."""
     import torch
