@@ -632,7 +632,7 @@ int mpq_linear_cross_entropy(const void* x, int dtype, int64_t t, int64_t ldx, c
  * together, or both NULL.  W's rows enter as x does, or, in 16 bits with 16-byte aligned
  * rows of a multiple of 64 columns, as they are: then dz too enters dx in bfloat16 with
  * a bfloat16 matrix, but for the target's, whose term is float32.  For dW, dz enters as
- * one term (float32: two). */
+ * two terms (bfloat16: one). */
 size_t mpq_matrix_cross_entropy_workspace_bytes(int dtype, int64_t t, int64_t m, int64_t n);
 int mpq_matrix_cross_entropy(const void* x, int dtype, int64_t t, int64_t ldx, const void* W, int64_t ldw, int64_t m,
                              int64_t n, const float* bias, const int32_t* targets, const float* weights, float* loss,

@@ -769,7 +769,8 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
                         reinterpret_cast<uintptr_t>(A.W) % 16 == 0;
   const int DX = f32 ? 2 : 1;                   // dz for dx
   const int WX = f32 ? WP : 1;                  // the weights for dx: as many terms as dz
-  const int DT = A.dense && !f32 ? 1 : 2;       // dz^T for dW
+  // dz^T for dW: one term has eight times a bfloat16 result's precision, and no more than a float16 one's.
+  const int DT = A.dense && A.dtype == DT_BF16 ? 1 : 2;
   const bool contract = !A.dense && L.group % Q_CONTRACT == 0;
   // Logits that fit half of the last-level cache are kept for the gradients: written and
   // read there, they cost less than their product.  Others leave the product as

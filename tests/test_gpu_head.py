@@ -16,7 +16,7 @@ is the sum of (e' the entry less the middle level, o' the offset with it):
     elements below 2^-28 of the row's bound 2^-39 of it, float32 sums over the
     vocabulary (V / 16 + 32) 2^-22, one rounding of the result;
   - the head's gradients: dz's, s's own d_t, sums of 64 tokens (2^-19); of a matrix and
-    of groups: dz^T's terms (2^-11 for a 16-bit matrix, 2^-20), its elements below 2^-28
+    of groups: dz^T's terms (2^-11 for a bfloat16 matrix, 2^-20), its elements below 2^-28
     of the largest dz's bound, float32 sums over the tokens and a group's columns.
 """
 import numpy as np
@@ -106,7 +106,7 @@ def check(got, ref, dtype, n, exact_terms, kind, head=None, need_dx=True, need_d
     if kind == "matrix":
         M, E = adzT @ ref["ax"], ddzT @ ref["ax"]
         low = 2.0 ** -38 * bound.max() * (one @ ref["ax"])[None]
-        tol = E + ((2.0 ** -11 if half else 2.0 ** -19) + (t / 16 + 32) * 2.0 ** -22) * M + low
+        tol = E + ((2.0 ** -11 if dtype == "bf16" else 2.0 ** -19) + (t / 16 + 32) * 2.0 ** -22) * M + low
         want = dzT @ ref["x"]
         within("dweight", got["dweight"], want, tol + step * (want.abs() + tol) + tiny)
         return
@@ -269,6 +269,32 @@ def test_few_tokens_that_are_not_read(name, group):
     assert torch.isnan(got2["loss"][2]) and torch.isnan(got2["dx"][2]).all()
     assert torch.equal(got2["loss"][3], got["loss"][3]) and torch.equal(got2["dx"][3], got["dx"][3])
     assert not got2["dx"][:2].any()
+
+
+@pytest.mark.parametrize("n", [512, 500])
+@pytest.mark.parametrize("t", [1, 3, 70])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+def test_matrix_gradient_is_rounded_once(dtype, t, n):
+    """The gradient of a matrix is as near as its type allows: by their mean square relative to the gradient, errors are
+    those of rounding the formula's value (a second rounding of 11 bits before it would make float16's 1.41 of that; dz
+    in float32 is good to some 2^-18).  A bfloat16 matrix has dz in one term: each product dz x is off by 2^-11 of itself
+    at most, so an element by 2^-11 sum |dz| |x|, which is more than its own rounding where the tokens cancel."""
+    import torch
+    import post_quantization_solver_amd as mpq
+    g = np.random.default_rng(40 + t)
+    W = rows(g, 600, n, dtype, 0, 0, scale=1.0 / np.sqrt(n))
+    x, targets, b, w = inputs(g, 600, n, t, dtype, False, False, 0, 0)
+    got = mpq.linear_cross_entropy(x, W, targets, weights=w)["dweight"]
+    ref = reference(x, dict(W=W), targets, None, w)
+    want = ref["dz"].t().contiguous() @ ref["x"]
+    # (float16's subnormal steps say nothing of this)
+    keep = want.abs() > (2.0 ** -12 if dtype == "fp16" else 0.0)
+    assert keep.sum() > 500
+
+    def size(v):
+        return float((v[keep] / want.abs()[keep].clamp_min(1e-3 * float(want.abs().mean()))).square().mean().sqrt())
+    terms = 2.0 ** -11 * size(ref["dz"].abs().t().contiguous() @ ref["ax"]) if dtype == "bf16" else 0.0
+    assert size(got.double() - want) <= 1.2 * size(want.to(got.dtype).double() - want) + terms + (2.0 ** -16 if dtype == "fp32" else 0.0)
 
 
 def test_a_column_a_group():
