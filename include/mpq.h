@@ -614,11 +614,12 @@ int mpq_distill(const void* logits, int dtype, int64_t t, int64_t V, int64_t ld,
  * (under a power of two per token) and the weights of column groups enter as one term
  * (11 bits; float32: two; for a float16 x the target's term of dx is float32; up
  * to four tokens' dx is float32 all in all, but for groups that end inside a chunk of the packed
- * codes); for the gradients of column groups dz as two.
+ * codes); for the gradients of column groups dz as two, under a power of two per row of
+ * the head: a row that no token makes likely has as exact a gradient as any other.
  * 1 <= m, 0 <= t < 2^22, ceil(t / 64) ceil(n / 64) < 2^24.  The workspace holds the
  * logits where they take up to 128 MB; of the head's operands up to 512 MB then, else
  * 256 MB, or 1024 rows; and for those rows what the gradients take (dz: t x rows x 2 or
- * 4 bytes).  t = 0: gradients of zero. */
+ * 4 bytes; of column groups and matrices it again, and the logits).  t = 0: gradients of zero. */
 size_t mpq_linear_cross_entropy_workspace_bytes(int dtype, int64_t t, int64_t m, int64_t n, int64_t K, int64_t d,
                                                 int64_t group);
 int mpq_linear_cross_entropy(const void* x, int dtype, int64_t t, int64_t ldx, const void* packed, int64_t m, int64_t n,
@@ -632,7 +633,7 @@ int mpq_linear_cross_entropy(const void* x, int dtype, int64_t t, int64_t ldx, c
  * together, or both NULL.  W's rows enter as x does, or, in 16 bits with 16-byte aligned
  * rows of a multiple of 64 columns, as they are: then dz too enters dx in bfloat16 with
  * a bfloat16 matrix, but for the target's, whose term is float32.  For dW, dz enters as
- * two terms (bfloat16: one). */
+ * two terms (bfloat16: one), under a power of two per row of W. */
 size_t mpq_matrix_cross_entropy_workspace_bytes(int dtype, int64_t t, int64_t m, int64_t n);
 int mpq_matrix_cross_entropy(const void* x, int dtype, int64_t t, int64_t ldx, const void* W, int64_t ldw, int64_t m,
                              int64_t n, const float* bias, const int32_t* targets, const float* weights, float* loss,

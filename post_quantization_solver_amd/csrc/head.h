@@ -34,7 +34,7 @@ struct PieceArgs {
   float2* part;                    // per segment and token: the largest, the sum
   // gradients
   const float *row_top, *row_scale, *row_target;   // the largest, w / sum of exponentials, dz of the target
-  const uint32_t* gmax;
+  const uint32_t* tmax;            // the bounds that dz^T's rows are scaled by
   const float* fmax;               // the largest factor of dz, in 64 parts (nullptr: 1)
   const uint32_t* xmax;            // the tokens' factors in x's operand: dz^T carries the inverse
   const uint32_t* refs;            // the weights' planes' factors (nullptr: a is dz's factor)

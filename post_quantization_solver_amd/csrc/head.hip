@@ -71,7 +71,6 @@ struct TokenArgs {
   bool vec;                           // rows of x four elements at a time
   float *weight, *sum, *target_z;     // the weight (0: the row is not read), X, the target's logit
   uint32_t* rowmax;
-  uint32_t* gmax;                     // cleared
   uint16_t* planes; int64_t plane;    // float16 terms, operand order of Kp columns
   int terms; int64_t Kp;
   bool raw;                           // bfloat16 as it is, in place of terms
@@ -144,7 +143,6 @@ __global__ __launch_bounds__(256) void head_token_kernel(TokenArgs A) {
     A.rowmax[row] = top;
     A.target_z[row] = __uint_as_float(0x7fc00000u);   // a target past the vocabulary stays NaN
   }
-  if (row == 0 && threadIdx.x == 0) *A.gmax = 0;
   const float f = pow2(pow2_shift(top));
   for (int64_t j = threadIdx.x * 8; j < A.Kp; j += 256 * 8) {
     float v[8];
@@ -322,8 +320,6 @@ __global__ __launch_bounds__(256) void head_stats_kernel(PieceArgs A) {
 struct TokenOut {
   const float* weight;
   float *loss, *row_top, *row_scale, *row_target;
-  const uint32_t* xmax;   // dz^T's operand carries the inverse of the token's factor
-  uint32_t* gmax;
 };
 __device__ __forceinline__ void finish_token(const TokenOut& A, int64_t t, float top, double s, float zt) {
   const float w = A.weight[t];
@@ -334,7 +330,6 @@ __device__ __forceinline__ void finish_token(const TokenOut& A, int64_t t, float
   if (!(s == s) || !(zt == zt)) {
     A.row_top[t] = 0.f;
     A.loss[t] = A.row_scale[t] = A.row_target[t] = __uint_as_float(0x7fc00000u);
-    atomicMax(A.gmax, 0x7fc00000u);
     return;
   }
   // R - z of the target: log of the others' mass over its own
@@ -344,12 +339,10 @@ __device__ __forceinline__ void finish_token(const TokenOut& A, int64_t t, float
   const double l = none ? INFINITY : d > 0.0 ? d + log1p(exp(-d)) : log1p(exp(d));
   const float all = fmaxf(top, zt);
   const double total = s * exp((double)top - (double)all) + exp((double)zt - (double)all);
-  const float target = all == -INFINITY ? 0.f : (float)(-(double)w * rest);
   A.loss[t] = (float)((double)w * l);
   A.row_top[t] = all;
   A.row_scale[t] = all == -INFINITY ? 0.f : (float)((double)w / total);
-  A.row_target[t] = target;
-  atomicMax(A.gmax, abs_bits(target * pow2(-pow2_shift(A.xmax[t]))));
+  A.row_target[t] = all == -INFINITY ? 0.f : (float)(-(double)w * rest);
 }
 
 // The segments joined: sixteen tokens a workgroup, sixteen threads each.
@@ -441,6 +434,55 @@ __global__ __launch_bounds__(256) void head_factor_kernel(PieceArgs A, float* __
   if (threadIdx.x == 0) out[blockIdx.x] = bits_max(bits_max(red[0], red[1]), bits_max(red[2], red[3]));
 }
 
+// What a row's dz over all tokens, times the inverse of the tokens' factors, is at most: dz^T's
+// operand of each row of the head carries a power of two of its own, so that the gradient of a
+// row that no token makes likely is as exact as any other's (under one power of two for all
+// rows a row 20 nats below the likeliest kept 11 bits, one 27 nats below none).  By its
+// logarithm; a workgroup takes 256 rows and its share of the tokens, a wave every sixteenth of
+// those (several shares: `out` is zeroed before, and the largest stays).
+constexpr int BOUND_ROWS = 256, BOUND_WAVES = 16;
+__global__ __launch_bounds__(64 * BOUND_WAVES) void head_bound_kernel(PieceArgs A, uint32_t* __restrict__ out) {
+  __shared__ float red[BOUND_WAVES][BOUND_ROWS];
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  const int64_t i = (int64_t)blockIdx.x * BOUND_ROWS + lane * 4;
+  const Col4 C = col4(A, i);
+  float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 4
+  for (int64_t t = (int64_t)blockIdx.y * BOUND_WAVES + wave; t < A.t; t += (int64_t)gridDim.y * BOUND_WAVES) {
+    const float f = pow2(-pow2_shift(A.xmax[t]));
+    // (0: -inf, or NaN, which a maximum passes over)
+    const float others = __builtin_amdgcn_logf(fabsf(A.row_scale[t]) * f) - A.row_top[t] * H_LOG2E;
+    const float own = __builtin_amdgcn_logf(fabsf(A.row_target[t]) * f);
+    const int64_t target = (int64_t)A.targets[t] - A.row0;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (i < A.m) s = *reinterpret_cast<const float4*>(A.S + t * A.lds + i);
+    const float v[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) top[q] = fmaxf(top[q], i + q == target ? own : fmaf(v[q] + C.b[q], H_LOG2E, others));
+  }
+  *reinterpret_cast<float4*>(&red[wave][lane * 4]) = make_float4(top[0], top[1], top[2], top[3]);
+  __syncthreads();
+  if (threadIdx.x >= BOUND_ROWS) return;
+  const int64_t row = (int64_t)blockIdx.x * BOUND_ROWS + threadIdx.x;
+  float most = -126.f;   // (a factor of 2^126 at most)
+#pragma unroll
+  for (int w = 0; w < BOUND_WAVES; ++w) most = fmaxf(most, red[w][threadIdx.x]);
+  if (row >= A.m) return;
+  const uint32_t bits = __float_as_uint(__builtin_amdgcn_exp2f(most));
+  if (gridDim.y > 1) atomicMax(out + row, bits);
+  else out[row] = bits;
+}
+hipError_t launch_bound(const PieceArgs& A, uint32_t* out, hipStream_t st) {
+  const int64_t groups = (A.m + BOUND_ROWS - 1) / BOUND_ROWS;
+  const int64_t shares = std::max<int64_t>(1, std::min(256 / groups, (A.t + 127) / 128));
+  if (shares > 1) {
+    const hipError_t e = launch_fill_i32(reinterpret_cast<int32_t*>(out), A.m, 0, st);
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(head_bound_kernel, dim3((unsigned)groups, (unsigned)shares), dim3(64 * BOUND_WAVES), 0, st, A, out);
+  return hipGetLastError();
+}
+
 // A 64 x 64 tile of dz: its planes, its transpose's (turned in LDS: a lane stores four
 // tokens of a row), its rows' and columns' sums.  509 x 50257, with the transpose in two
 // terms: 70 us for 258 MB, 3.7 TB/s; vector instructions 63 % of the clocks.
@@ -521,11 +563,11 @@ __global__ __launch_bounds__(256) void head_grad_kernel(PieceArgs A) {
     }
   }
   if (!A.dt) return;
-  const float g = pow2(pow2_shift(*A.gmax));
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const int64_t r = i0 + ry + 16 * k;
     if (r >= A.m) continue;
+    const float g = pow2(pow2_shift(A.tmax[r]));
     float v[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) v[q] = tl[cx * 4 + q][ry + 16 * k] * g;
@@ -786,6 +828,9 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
   if (!A.dense && !contract) rows = std::min(rows, (((int64_t)1 << 26) - 1) / L.G / 256 * 256);
   const int64_t pieces = (V + rows - 1) / rows;
   const HeadTile tile = head_tile(rows, T);
+  // The gradients' pass takes logits in memory: those that are kept, or a piece's, formed again
+  // there where dz^T is wanted (a row's factor is known once all its tokens' dz are).
+  const bool stored = kept || product;
   // Few tokens: straight from the packed codes.
   const bool few = kept && !A.dense && q_few_rows(L, A.dtype, T);
   // ... and their input gradient (planes_dx: through planes).
@@ -797,7 +842,7 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
   // 15.6 us in one workgroup of sixteen waves, 8 in segments with their join.)
   const bool short_rows = kept && V <= 16384;
   const int64_t seg = kept ? seg_rows : tile.rows, all_segs = (V + seg - 1) / seg;
-  const int64_t row_tiles = kept ? rows / 64 : rows / tile.rows, token_tiles = kept ? ttiles : (T + 127) / 128;
+  const int64_t row_tiles = stored ? rows / 64 : rows / tile.rows, token_tiles = stored ? ttiles : (T + 127) / 128;
   Carve W{base};
   TokenArgs K;
   memset(&K, 0, sizeof(K));
@@ -805,7 +850,6 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
   K.sum = W.take<float>((size_t)T * 4);
   K.target_z = W.take<float>((size_t)T * 4);
   K.rowmax = W.take<uint32_t>((size_t)T * 4);
-  K.gmax = W.take<uint32_t>(8);
   float* fpart = W.take<float>(64 * 4);
   float* ones = W.take<float>(!A.dense && !weights ? (size_t)V * 4 : 0);
   float* row_top = W.take<float>((size_t)T * 4);
@@ -816,7 +860,8 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
   K.planes = W.take<uint16_t>((size_t)XP * K.plane * 2);
   uint32_t* refs = W.take<uint32_t>(weights ? (size_t)V * 4 : 0);
   uint16_t* wp = W.take<uint16_t>((size_t)WP * up16(rows) * Kp * 2);
-  float* S = W.take<float>(kept ? (size_t)T * lds * 4 : 0);
+  const int64_t lds_p = kept ? lds : rows;   // of the logits that the gradients' pass takes
+  float* S = W.take<float>(stored ? (size_t)T * lds_p * 4 : 0);
   float2* part = W.take<float2>((size_t)all_segs * T * sizeof(float2));
   QGemm gz, gx, gw;
   memset(&gz, 0, sizeof(gz));
@@ -830,9 +875,9 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
     f(std::min(rows, V));
     f(V - (pieces - 1) * rows);
   };
-  if (kept) both_sizes([&](int64_t nr) { ps = std::max(ps, q_gemm_workspace(nr, T, Kp, gz.npairs)); });
+  if (stored) both_sizes([&](int64_t nr) { ps = std::max(ps, q_gemm_workspace(nr, T, Kp, gz.npairs)); });
   uint16_t *d = nullptr, *dt = nullptr;
-  uint32_t* dmax = nullptr;
+  uint32_t *dmax = nullptr, *tmax = nullptr;
   float *rowpart = nullptr, *rowadd = nullptr, *acc = nullptr, *colpart = nullptr, *dW = nullptr;
   float2* cpart = nullptr;
   const int64_t lda = (n + 3) / 4 * 4, cblocks = (n + Q_CONTRACT - 1) / Q_CONTRACT;
@@ -857,6 +902,7 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
     K.Kp_again = Kp;
     K.again = W.take<uint16_t>((size_t)XP * K.plane_again * 2);
     dt = W.take<uint16_t>((size_t)DT * up16(rows) * tp * 2);
+    tmax = W.take<uint32_t>((size_t)rows * 4);
     if (contract) {
       both_sizes([&](int64_t nr) { splits = std::max(splits, q_gemm_splits(n, nr, tp, gw.npairs)); });
       cpart = W.take<float2>((size_t)splits * rows * cblocks * sizeof(float2));
@@ -893,13 +939,13 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
   H_LAUNCH(head_token_kernel, ((unsigned)(up16(T) + (K.fpart ? 64 : 0) + (K.ones ? (V + 255) / 256 : 0))), 256, K);
   PieceArgs P;
   memset(&P, 0, sizeof(P));
-  P.lds = lds;
+  P.lds = lds_p;
   P.t = T;
   P.weight = K.weight; P.sum = K.sum;
   P.targets = A.targets;
   P.target_z = K.target_z;
   P.row_top = row_top; P.row_scale = row_scale; P.row_target = row_target;
-  P.gmax = K.gmax; P.xmax = K.rowmax;
+  P.tmax = tmax; P.xmax = K.rowmax;
   P.fmax = in_place ? nullptr : fpart;
   P.dmax = dmax;
   P.terms_d = DX; P.terms_t = DT;
@@ -917,7 +963,7 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
     P.mp = up64(nr);
     P.plane_d = up16(T) * P.mp;
     P.plane_t = up16(nr) * tp;
-    P.S = S + r0;
+    P.S = kept ? S + r0 : S;
     P.a = weights ? nullptr : Q.scale;
     P.o = weights ? nullptr : Q.offset;
     P.b = A.bias ? A.bias + r0 : nullptr;
@@ -965,22 +1011,21 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
     O.rows = T; O.cols = V;
     H_TRY(launch_q_skinny(F, K.planes, 0, K.plane, T, XP, false, O, st));
   }
+  auto store = [&]() {   // the piece's logits, as P.S says
+    gz.O.y = const_cast<float*>(P.S); gz.O.ldy = lds_p;
+    gz.O.rowmax = rowmax;
+    gz.O.colmax = P.refs;
+    gz.O.mid = -1;
+    gz.O.dtype = DT_F32;
+    gz.O.vec = 1;
+    gz.O.rows = T; gz.O.cols = P.m;
+    return launch_q_gemm(gz, gpart, st);
+  };
   for (int64_t k = 0; k < pieces && !few; ++k) {
     H_TRY(piece(k, true, WP));
-    if (kept) {
-      gz.O.y = S + P.row0; gz.O.ldy = lds;
-      gz.O.rowmax = rowmax;
-      gz.O.colmax = P.refs;
-      gz.O.mid = -1;
-      gz.O.dtype = DT_F32;
-      gz.O.vec = 1;
-      gz.O.rows = T; gz.O.cols = P.m;
-      H_TRY(launch_q_gemm(gz, gpart, st));
-    } else {
-      H_TRY(launch_head_gemm(gz, P, rowmax, false, st));
-    }
+    H_TRY(kept ? store() : launch_head_gemm(gz, P, rowmax, false, st));
   }
-  const TokenOut O = {K.weight, A.loss, row_top, row_scale, row_target, K.rowmax, K.gmax};
+  const TokenOut O = {K.weight, A.loss, row_top, row_scale, row_target};
   if (kept) {
     PieceArgs F = P;   // all of it
     F.m = V;
@@ -1028,24 +1073,26 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
     P.d = planes_dx ? d : nullptr;
     P.rowpart = sums ? rowpart : nullptr;
     P.dt = product ? dt : nullptr;
-    const bool straight = kept && ttiles == 1;   // no tiles of tokens to add up
+    const bool straight = stored && ttiles == 1;   // no tiles of tokens to add up
     P.colpart = A.need_dhead && !straight ? colpart : nullptr;
     if (A.need_dhead && straight) {
       P.dbias = A.dbias + r0;
       P.dscale = weights ? nullptr : A.dscale + r0;
       P.doffset = weights ? nullptr : A.doffset + r0;
     }
-    if (kept)
+    if (!kept && product) H_TRY(store());
+    if (product) H_TRY(launch_bound(P, tmax, st));
+    if (stored)
       H_LAUNCH(head_grad_kernel, ((unsigned)(mp / 64 * ttiles)), 256, P);
     else
       H_TRY(launch_head_gemm(gz, P, rowmax, true, st));
     const HeadTile own = head_tile(nr, T);   // (of the last piece, smaller)
     if (P.colpart)
       H_LAUNCH(head_colsum_kernel, ((unsigned)((nr + 255) / 256)), 256, colpart,
-               kept ? ttiles : (T + own.tokens - 1) / own.tokens, nr, A.dbias + r0,
+               stored ? ttiles : (T + own.tokens - 1) / own.tokens, nr, A.dbias + r0,
                weights ? nullptr : A.dscale + r0, weights ? nullptr : A.doffset + r0);
     if (sums) H_LAUNCH(head_rowsum_kernel, ((unsigned)((T + 3) / 4)), 256, rowpart,
-                       kept ? mp / 64 : (nr + own.rows - 1) / own.rows, T, k == 0, rowadd);
+                       stored ? mp / 64 : (nr + own.rows - 1) / own.rows, T, k == 0, rowadd);
     if (planes_dx) {
       gx.A = gz.A; gx.lda = gz.lda; gx.planeA = gz.planeA;
       gx.bf16 = gz.bf16;
@@ -1059,8 +1106,7 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
       gw.acols = Kp; gw.arows = T;
       gw.B = dt; gw.planeB = P.plane_t;
       gw.M = n; gw.N = nr; gw.K = tp;
-      gw.O.rowmax = K.gmax;
-      gw.O.one_rowmax = true;
+      gw.O.rowmax = tmax;
       gw.O.mid = -1;
       gw.O.rows = nr; gw.O.cols = n;
       if (A.dense) {

@@ -23,23 +23,6 @@ namespace mpq {
 
 namespace {
 
-// v[k] of lane 4 a + b becomes v[b] of lane 4 a + k.
-__device__ __forceinline__ void transpose_quads(float* v, int lane) {
-  const bool odd = lane & 1, high = lane & 2;
-#pragma unroll
-  for (int p = 0; p < 4; p += 2) {
-    const float got = dpp_f<DPP_XOR1>(odd ? v[p] : v[p + 1]);
-    v[p] = odd ? got : v[p];
-    v[p + 1] = odd ? v[p + 1] : got;
-  }
-#pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    const float got = dpp_f<DPP_XOR2>(high ? v[p] : v[p + 2]);
-    v[p] = high ? got : v[p];
-    v[p + 2] = high ? v[p + 2] : got;
-  }
-}
-
 template <typename T, int BM, int BN, int WM, int WN, bool GRADS, int AMODE>
 __global__ __launch_bounds__(64 * WM * WN, 2) void head_gemm_kernel(QGemm g, PieceArgs A, const uint32_t* __restrict__ rowmax) {
   constexpr int SM = BM / WM / 16, SN = BN / WN / 16;
@@ -130,9 +113,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void head_gemm_kernel(QGemm g, Pie
       A.part[i0 / BM * A.t + j0 + k] = make_float2(top, sum);
     }
   } else {
-    float f[SN], X[SN], top[SN], scale[SN], own[SN], gd[SN], ft[SN], rows[SN];
+    float f[SN], X[SN], top[SN], scale[SN], own[SN], gd[SN], rows[SN];
     int target[SN];
-    const float fm = A.d ? largest_factor(A) : 0.f, gt = A.dt ? pow2(pow2_shift(*A.gmax)) : 1.f;
+    const float fm = A.d ? largest_factor(A) : 0.f;
 #pragma unroll
     for (int jj = 0; jj < SN; ++jj) {
       const int64_t t = j0 + (wn * SN + jj) * 16 + r, th = min(t, A.t - 1);
@@ -147,7 +130,6 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void head_gemm_kernel(QGemm g, Pie
       const uint32_t bound = abs_bits(own[jj] * fm);
       if (A.d && i0 == 0 && wm == 0 && kb == 0 && live) A.dmax[t] = bound;
       gd[jj] = pow2(pow2_shift(bound));
-      ft[jj] = A.dt ? pow2(-pow2_shift(A.xmax[th])) * gt : 0.f;
       rows[jj] = 0.f;
     }
     float* red = work;   // [WN][3][BM], and [WM][BN] after it
@@ -175,13 +157,6 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void head_gemm_kernel(QGemm g, Pie
         }
         if (A.rowpart) rows[jj] += fmaf(v[0], o[0], v[1] * o[1]) + fmaf(v[2], o[2], v[3] * o[3]);
         if (A.d && t < A.t && i < A.mp) put_dz(A, t, i, u);
-        if (A.dt) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) v[k] *= ft[jj];
-          transpose_quads(v, lane);
-          const int64_t row = i + (r & 3), tok = t & ~(int64_t)3;
-          if (row < A.m && tok < A.tp) put_terms(A.dt + q_at(row, tok, A.tp), A.plane_t, A.terms_t, v);
-        }
       }
       if (A.colpart)
 #pragma unroll

@@ -49,12 +49,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void q_gemm_kernel(QGemm g, float*
   const QCol C = q_col4(g.O, ii);
   auto slot = [&](int it) { return reinterpret_cast<v4f*>(own + it * RPI * PITCH); };
   QLevels levels = {0.f, 0.f};
-  float shared = 1.f;
   const bool nib = g.L.fmt == QF_NIB;
-  if (g.cpart) {
-    levels = q_levels(g.L);
-    if (g.O.one_rowmax) shared = pow2(-pow2_shift(g.O.rowmax[0]));
-  }
+  if (g.cpart) levels = q_levels(g.L);
 #pragma unroll 1
   for (int j = 0; j < SN; ++j) {   // (one copy of the body; the accumulators by constant index)
 #pragma unroll
@@ -76,7 +72,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void q_gemm_kernel(QGemm g, float*
       for (int it = 0; it < IT; ++it) {
         const int64_t row = min(jj + it * RPI, g.N - 1);
         code[it] = q_code4_of(g.L, codes, qrow + it * RPI);
-        f[it] = g.O.one_rowmax ? shared : pow2(-pow2_shift(g.O.rowmax[row]));
+        f[it] = pow2(-pow2_shift(g.O.rowmax[row]));
       }
       auto contract = [&](auto entries) {
 #pragma unroll

@@ -326,7 +326,6 @@ struct QOut {
   const float* levels; int mid;     // d = 1: levels[mid] (mid < 0: zero)
   int act, dtype;
   int vec;                          // 4-element alignment of y, pre, res
-  bool one_rowmax;                  // rowmax[0] is every row's
   int64_t rows, cols;
 };
 
@@ -371,7 +370,7 @@ __device__ __forceinline__ QCol q_col4(const QOut& O, int64_t i) {
 }
 // Row j's part of it.
 __device__ __forceinline__ void q_affine4(const QOut& O, const QCol& C, int64_t j, float* v) {
-  const float f = O.rowmax ? pow2(-pow2_shift(O.rowmax[O.one_rowmax ? 0 : j])) : 1.f;
+  const float f = O.rowmax ? pow2(-pow2_shift(O.rowmax[j])) : 1.f;
   const float add = O.rowadd ? O.rowadd[j] : 0.f;
 #pragma unroll
   for (int k = 0; k < 4; ++k) v[k] = fmaf(C.a[k], v[k] * f, (O.rowadd ? C.o[k] * add : 0.f) + C.b[k]);
