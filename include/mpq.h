@@ -683,7 +683,7 @@ int mpq_matrix_cross_entropy(const void* x, int dtype, int64_t t, int64_t ldx, c
  * and writes device memory alone once it is enqueued, so that it may be captured and
  * replayed with gradients at the same addresses.
  * Errors: MPQ_ENULL, MPQ_ESHAPE (state.elements), MPQ_EPARAM (betas outside [0, 1),
- * eps <= 0, grad_scale, max_norm or lr_scale out of range, state.bits, a plan that
+ * eps below float32's normal range, grad_scale, max_norm or lr_scale out of range, state.bits, a plan that
  * mpq_adamw_plan did not fill). */
 typedef struct {
   void* param;

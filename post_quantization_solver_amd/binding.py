@@ -1149,8 +1149,8 @@ class AdamW:
                 raise ValueError(f"{len(values)} values of {name} for {count} parameters")
             self._rates.append(values)
         self.betas, self.eps, self.state_bits, self.seed = tuple(map(float, betas)), float(eps), state_bits, int(seed)
-        if not (all(0.0 <= b < 1.0 for b in self.betas) and len(self.betas) == 2) or not self.eps > 0.0:
-            raise ValueError(f"betas must lie in [0, 1) and eps be positive, got {betas} and {eps}")
+        if not (all(0.0 <= b < 1.0 for b in self.betas) and len(self.betas) == 2) or not self.eps >= 2.0 ** -126:
+            raise ValueError(f"betas must lie in [0, 1) and eps be positive (2^-126 at least), got {betas} and {eps}")
         self._counts = [p.numel() for p in self.params]
         self._dtypes = [p.dtype for p in self.params]
         self.offsets, total = [], 0

@@ -1,6 +1,7 @@
 // The C ABI's operators of a tuning step (include/mpq.h): argument checks on
 // the host, then launches on the caller's stream.
 #include <hip/hip_runtime.h>
+#include <float.h>
 #include <math.h>
 #include <string.h>
 #include <algorithm>
@@ -260,9 +261,10 @@ int mpq_adamw(const mpq_adamw_plan_t* plan, const void* const* grads, const mpq_
   if (!plan || !options || !state) return MPQ_ENULL;
   if (plan->magic != PLAN_MAGIC) return MPQ_EPARAM;
   const mpq_adamw_options& o = *options;
-  if (!(o.beta1 >= 0.0 && o.beta1 < 1.0) || !(o.beta2 >= 0.0 && o.beta2 < 1.0) || !(o.eps > 0.0) || !isfinite((float)o.eps) ||
-      (float)o.eps == 0.f || !isfinite(o.grad_scale) || !(o.max_norm >= 0.0) ||
-      !(o.lr_scale >= 0.0) || !isfinite((float)o.lr_scale))
+  // (the reciprocal of an eps below float32's normal range is infinite: times a first moment of 0, NaN)
+  if (!(o.beta1 >= 0.0 && o.beta1 < 1.0) || !(o.beta2 >= 0.0 && o.beta2 < 1.0) || !((float)o.eps >= FLT_MIN) ||
+      !isfinite((float)o.eps) || !isfinite(o.grad_scale) || !(o.max_norm >= 0.0) || !(o.lr_scale >= 0.0) ||
+      !isfinite((float)o.lr_scale))
     return MPQ_EPARAM;
   const int rc = state_ok(*state, plan->elements);
   if (rc) return rc;
