@@ -1125,7 +1125,8 @@ class AdamW:
 
     The moments lie one tensor after another, each from a multiple of 256 on:
     `m`, `v` (32 bits), or the codes `m`, `r` (of sqrt(v)) with `m_scale`, `r_scale`;
-    `steps` counts the steps taken, on the device.
+    `steps` counts the steps taken, on the device.  A parameter that has moved (`p.data` set
+    to other memory) is found by the next step; captured steps follow it from then on.
     """
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0, state_bits=32, seed=0):
@@ -1158,6 +1159,7 @@ class AdamW:
             self.offsets.append(total)
             total += -(-n // 256) * 256
         self.elements = total
+        self._table, self._struct = None, AdamWPlan()
         with _guard(dev):
             self.steps = torch.zeros(1, dtype=torch.int32, device=dev)
             kind = torch.uint8 if state_bits == 8 else torch.float32
@@ -1174,19 +1176,23 @@ class AdamW:
                                  state_bits, self.seed & 0xffffffff)
 
     def _plan(self, torch):
-        """The parameters' places for the kernels (again where one has moved)."""
+        """The parameters' places for the kernels (again where one has moved: in the same memory, which captured steps
+        read)."""
         lib, count = load_library(), len(self.params)
-        self._where = [p.data_ptr() for p in self.params]
+        where = [p.data_ptr() for p in self.params]
         tensors = (AdamWTensor * count)(*(
             AdamWTensor(p, n, at, lr, wd, _dtype_code(t, "params"), 0) for p, n, at, lr, wd, t in
-            zip(self._where, self._counts, self.offsets, *self._rates, self.params)))
-        nb = int(lib.mpq_adamw_plan_bytes(tensors, count))
-        if nb == 0:
-            raise MPQError(-2, "mpq_adamw_plan_bytes")
-        self._table = torch.empty(nb, dtype=torch.uint8, device=self.device)
-        self._struct = AdamWPlan()
-        _check(lib.mpq_adamw_plan(tensors, count, _at(self._table), nb, _raw_stream(self.device),
+            zip(where, self._counts, self.offsets, *self._rates, self.params)))
+        if self._table is None:
+            nb = int(lib.mpq_adamw_plan_bytes(tensors, count))
+            if nb == 0:
+                raise MPQError(-2, "mpq_adamw_plan_bytes")
+            self._table = torch.empty(nb, dtype=torch.uint8, device=self.device)
+        elif torch.cuda.is_current_stream_capturing():
+            raise ValueError("a parameter has moved: a step before the capture has to find its place")
+        _check(lib.mpq_adamw_plan(tensors, count, _at(self._table), self._table.numel(), _raw_stream(self.device),
                                   ctypes.byref(self._struct)), "mpq_adamw_plan")
+        self._where = where
 
     def _same(self, tensors, name):
         """Raises unless the tensors are laid out as the parameters were; their addresses."""

@@ -23,3 +23,56 @@ def test_smallest_eps(bits):
     for eps in (1e-39, 2.0 ** -127, 0.0, float("nan")):
         with pytest.raises(ValueError):
             mpq.AdamW(params, eps=eps, state_bits=bits)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_captured_step_outlives_a_move(bits):
+    """A parameter moves after a step was captured: the eager step that finds it again leaves the graph's plan in place,
+    and replays step the parameter where it is now."""
+    import torch
+    import post_quantization_solver_amd as mpq
+    params, grads = problem(("fp32", "bf16"), [3000, 257, 70000], seed=21)
+    twin = [p.clone() for p in params]
+    a = mpq.AdamW(params, lr=1e-2, state_bits=bits, seed=4)
+    b = mpq.AdamW(twin, lr=1e-2, state_bits=bits, seed=4)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(graph, stream=side):
+            a.step(grads, max_norm=1.0)
+    torch.cuda.current_stream().wait_stream(side)
+    old = params[2]
+    params[2] = a.params[2] = old.clone()
+    a.step(grads, max_norm=1.0)
+    b.step(grads, max_norm=1.0)
+    # what a plan that had been let go of would be given to
+    others = [torch.full((int(a._table.numel()),), 255, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    left = old.clone()
+    for _ in range(3):
+        graph.replay()
+        b.step(grads, max_norm=1.0)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(params + list(a.state_dict().values()),
+                                                     twin + list(b.state_dict().values())))
+    assert torch.equal(old, left) and all(bool((o == 255).all()) for o in others)
+
+
+def test_a_move_is_not_found_while_capturing():
+    """The plan is written by the host: refused, with nothing enqueued and nothing changed."""
+    import torch
+    import post_quantization_solver_amd as mpq
+    params, grads = problem(("fp32",), [300], seed=22)
+    opt = mpq.AdamW(params, lr=1e-2)
+    opt.step(grads)
+    opt.params[0] = params[0].clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            with pytest.raises(ValueError, match="moved"):
+                opt.step(grads)
+            grads[0].mul_(1.0)   # (a graph of something)
+    torch.cuda.current_stream().wait_stream(side)
+    check_step(opt, grads)
