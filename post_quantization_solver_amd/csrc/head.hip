@@ -634,17 +634,18 @@ __global__ __launch_bounds__(256) void head_dx_kernel(const float* __restrict__ 
   const int64_t quads = (n + 3) / 4, step = (int64_t)gridDim.x * 256;
   for (int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x; k < T * quads; k += step) {
     const int64_t t = k / quads, j = (k - t * quads) * 4;
-    const float add = rowadd ? rowadd[t] : 0.f;
+    const bool read = R.weight[t] != 0.f;   // (else zeros, whatever the head holds: no 0 times NaN)
+    const float add = rowadd && read ? rowadd[t] : 0.f;
     float v[4] = {add, add, add, add};
 #pragma unroll 8
-    for (int s = 0; s < splits; ++s) {
+    for (int s = 0; s < splits && read; ++s) {
       const float4 q = *reinterpret_cast<const float4*>(acc + ((int64_t)s * T + t) * lda + j);
       v[0] += q.x;
       v[1] += q.y;
       v[2] += q.z;
       v[3] += q.w;
     }
-    if (R.wanted && R.weight[t] != 0.f && R.targets[t] < R.V) {
+    if (R.wanted && read && R.targets[t] < R.V) {
       float w[4];
       target_row4(R, R.targets[t], j, w);
 #pragma unroll
