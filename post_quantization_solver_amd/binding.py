@@ -889,12 +889,12 @@ def _activation(name):
     return ACTIVATIONS[name]
 
 
-def _no_graph(t, name):
+def _no_graph(t, name, what="linear", instead="take the gradients from linear_backward"):
     """Refuses a tensor that requires a gradient, where its graph would end here unnoticed."""
     import torch
     if torch.is_grad_enabled():
-        raise ValueError(f"{name} requires a gradient, which linear does not record: detach it, or call under "
-                         "torch.no_grad(), and take the gradients from linear_backward")
+        raise ValueError(f"{name} requires a gradient, which {what} does not record: detach it, or call under "
+                         f"torch.no_grad(), and {instead}")
 
 
 def linear(x, layer, bias=None, activation=None, residual=None, return_pre=False, out=None, workspace=None):
@@ -1065,10 +1065,13 @@ def linear_cross_entropy(x, head, targets, bias=None, weights=None, need_dx=True
     type, and of the head, float32 unless it is a matrix of 16 bits: dscale, doffset
     and dbias (in the shapes of the layer's affine and (m,)), or dweight and
     dbias.  What is not wanted is None.  The gradients are those of the losses' sum; no
-    autograd graph is recorded (x.backward(dx) takes it on).
+    autograd graph is recorded (x.backward(dx) takes it on: an x that requires a gradient is
+    refused where gradients are enabled and dx is not wanted).
     """
     import torch
     code = _dtype_code(x, "x")
+    if x.requires_grad and not need_dx:
+        _no_graph(x, "x", "linear_cross_entropy", "ask for dx, which x.backward(dx) takes on")
     ldx = _rows(x, "x")
     t, n = x.shape
     dev = x.device

@@ -49,3 +49,21 @@ def test_a_head_with_nan(kind, dtype, t):
     targets[::4] = -1
     again = mpq.linear_cross_entropy(x, head, targets, bias=b, weights=w)
     assert not again["dx"][none].any() and all(torch.isfinite(v).all() for v in list(again.values()) + list(before.values()))
+
+
+def test_an_autograd_graph_does_not_end_unnoticed():
+    """x with a graph: its gradient is handed on by dx, or refused where none is wanted."""
+    import torch
+    import post_quantization_solver_amd as mpq
+    head, x, targets, b, w, got = packed_case("s16", 100, 64, 5, "fp32", seed=3)
+    leaf = (x / 2).requires_grad_()
+    with pytest.raises(ValueError, match="requires a gradient"):
+        mpq.linear_cross_entropy(leaf * 2, head, targets, bias=b, weights=w, need_dx=False)
+    y = leaf * 2
+    y.backward(mpq.linear_cross_entropy(y, head, targets, bias=b, weights=w)["dx"])
+    assert torch.equal(leaf.grad, 2 * got["dx"])
+    with torch.no_grad():
+        alone = mpq.linear_cross_entropy(leaf * 2, head, targets, bias=b, weights=w, need_dx=False)
+    assert torch.equal(alone["loss"], got["loss"]) and torch.equal(alone["dscale"], got["dscale"])
+    alone = mpq.linear_cross_entropy((leaf * 2).detach(), head, targets, bias=b, weights=w, need_dx=False)
+    assert torch.equal(alone["loss"], got["loss"]) and alone["dx"] is None
