@@ -617,7 +617,8 @@ int mpq_distill(const void* logits, int dtype, int64_t t, int64_t V, int64_t ld,
  * codes); for the gradients of column groups dz as two, under a power of two per row of
  * the head: a row that no token makes likely has as exact a gradient as any other.
  * 1 <= m, 0 <= t < 2^22, ceil(t / 64) ceil(n / 64) < 2^24.  The workspace holds the
- * logits where they take up to 128 MB; of the head's operands up to 512 MB then, else
+ * logits where they take up to 128 MB; of the head's operands up to 512 MB then (none for
+ * up to four tokens of a packed head whose groups end with chunks of the packed codes), else
  * 256 MB, or 1024 rows; and for those rows what the gradients take (dz: t x rows x 2 or
  * 4 bytes; of column groups and matrices it again, and the logits).  t = 0: gradients of zero. */
 size_t mpq_linear_cross_entropy_workspace_bytes(int dtype, int64_t t, int64_t m, int64_t n, int64_t K, int64_t d,

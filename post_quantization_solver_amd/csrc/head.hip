@@ -860,7 +860,9 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
   K.plane = up16(T) * Kx;
   K.planes = W.take<uint16_t>((size_t)XP * K.plane * 2);
   uint32_t* refs = W.take<uint32_t>(weights ? (size_t)V * 4 : 0);
-  uint16_t* wp = W.take<uint16_t>((size_t)WP * up16(rows) * Kp * 2);
+  // (as many tokens as come straight from the codes both ways lay no plane out, whatever is wanted)
+  const bool planes = !few || T > H_FEW;
+  uint16_t* wp = W.take<uint16_t>(planes ? (size_t)WP * up16(rows) * Kp * 2 : 0);
   const int64_t lds_p = kept ? lds : rows;   // of the logits that the gradients' pass takes
   float* S = W.take<float>(stored ? (size_t)T * lds_p * 4 : 0);
   float2* part = W.take<float2>((size_t)all_segs * T * sizeof(float2));
@@ -876,7 +878,7 @@ hipError_t head(const HeadArgs& A, char* base, size_t* bytes, hipStream_t st) {
     f(std::min(rows, V));
     f(V - (pieces - 1) * rows);
   };
-  if (stored) both_sizes([&](int64_t nr) { ps = std::max(ps, q_gemm_workspace(nr, T, Kp, gz.npairs)); });
+  if (stored && !few) both_sizes([&](int64_t nr) { ps = std::max(ps, q_gemm_workspace(nr, T, Kp, gz.npairs)); });
   uint16_t *d = nullptr, *dt = nullptr;
   uint32_t *dmax = nullptr, *tmax = nullptr;
   float *rowpart = nullptr, *rowadd = nullptr, *acc = nullptr, *colpart = nullptr, *dW = nullptr;
