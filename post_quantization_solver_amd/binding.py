@@ -1267,17 +1267,21 @@ class AdamW:
         return {"step": self.steps, **{k: getattr(self, k) for k in names}}
 
     def state_dict(self):
-        """The step count and the moments (the live tensors)."""
-        return self._saved()
+        """The step count and the moments (the live tensors), and the seed of the random bits."""
+        import torch
+        return {**self._saved(), "seed": torch.tensor(self._state.seed)}
 
     def load_state_dict(self, state):
-        """Copies a state_dict of an AdamW of the same sizes and state_bits."""
+        """Copies a state_dict of an AdamW of the same sizes and state_bits; one without a seed leaves this one's."""
         own = self._saved()
-        if set(state) != set(own):
-            raise ValueError(f"the state has {sorted(state)}, expected {sorted(own)}")
+        if set(state) - {"seed"} != set(own):
+            raise ValueError(f"the state has {sorted(state)}, expected {sorted(own)} and seed")
         for k, t in own.items():
             if state[k].shape != t.shape or state[k].dtype != t.dtype:
                 raise ValueError(f"{k} has shape {tuple(state[k].shape)} and type {state[k].dtype}, expected "
                                  f"{tuple(t.shape)} and {t.dtype}")
         for k, t in own.items():
             t.copy_(state[k])
+        if "seed" in state:
+            self.seed = int(state["seed"])
+            self._state.seed = self.seed & 0xffffffff

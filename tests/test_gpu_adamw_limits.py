@@ -76,3 +76,28 @@ def test_a_move_is_not_found_while_capturing():
             grads[0].mul_(1.0)   # (a graph of something)
     torch.cuda.current_stream().wait_stream(side)
     check_step(opt, grads)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_resumed_run_rounds_as_the_first(bits, tmp_path):
+    """A state_dict carries the seed of the random bits: the steps after it are the same bits, whatever the new seed was."""
+    import torch
+    import post_quantization_solver_amd as mpq
+    params, grads = problem(("bf16", "fp16", "fp32"), [3000, 700, 513], seed=23)
+    a = mpq.AdamW(params, state_bits=bits, seed=2 ** 32 - 7)
+    a.step(grads)
+    twin = [p.clone() for p in params]
+    torch.save(a.state_dict(), tmp_path / "state")
+    b = mpq.AdamW(twin, state_bits=bits)
+    b.load_state_dict(torch.load(tmp_path / "state", weights_only=True))
+    assert b.seed == a.seed
+    for _ in range(3):
+        a.step(grads)
+        b.step(grads)
+    assert all(torch.equal(x, y) for x, y in zip(params, twin))
+    assert all(torch.equal(v, b.state_dict()[k]) for k, v in a.state_dict().items())
+    check_step(b, grads)
+    old = {k: v for k, v in a.state_dict().items() if k != "seed"}   # (one that was saved without)
+    c = mpq.AdamW(twin, state_bits=bits, seed=11)
+    c.load_state_dict(old)
+    assert c.seed == 11
