@@ -594,7 +594,8 @@ int mpq_distill(const void* logits, int dtype, int64_t t, int64_t V, int64_t ld,
 /* ------------------------------------------------------------------ a head's cross entropy */
 
 /* Softmax cross entropy of an output head, in pieces of its vocabulary (m rows)
- * and without keeping the logits: per token with target r = targets[t]
+ * and with logits in memory only where they are few (up to 128 MB of workspace, or a
+ * piece's): per token with target r = targets[t]
  *   z_v = sum_j x_j W[v][j] + bias_v,   loss = weight (log sum_v exp z_v - z_r),
  * the head as in mpq_linear, and, where asked for, the gradients of the sum of the
  * losses, the codes fixed:
@@ -606,8 +607,11 @@ int mpq_distill(const void* logits, int dtype, int64_t t, int64_t V, int64_t ld,
  * >= m: the row's loss and gradient NaN (and so the head's gradients).  loss: t
  * float32; small losses keep their relative accuracy.  A bias of -inf takes its token
  * out of the vocabulary: a target among those has loss +inf, and where no other token
- * is left either, gradient 0.
- * Sums are float32, joined in float64 beyond a workgroup.  Entries enter as they are;
+ * is left either, gradient 0.  (Its row of the head still enters sums, times 0: it has to be
+ * finite, as any that a token that is read meets.)
+ * Sums are float32.  Those of exponentials, of dz and of the head's gradients are joined in
+ * float64 beyond a workgroup; dx's go on in float32 over pieces of the vocabulary and over
+ * splits of a piece, in a fixed order.  Entries enter as they are;
  * x as float16 terms under a power of two per token: one, exact, for 16-bit types
  * (elements below 2^-28 of their row's largest lose bits, those below 2^-39 are gone),
  * two (22 bits) for float32; the weights of column groups as two terms.  For dx, dz
@@ -669,8 +673,9 @@ int mpq_matrix_cross_entropy(const void* x, int dtype, int64_t t, int64_t ldx, c
  * (2^F + f) 2^(E - 1); the largest of 256 has the largest code.  Codes are rounded
  * up or down at random with the probability of where the value (of a root: its
  * square, so that m and v are what they would be on average) lies between them (a root
- * that is not zero, never to zero), and so are 16-bit parameters: the random bits are a
- * hash of (seed, t, place in the moments), and the same call gives the same bits.  State of 8 bits is computed in float64.  step: device
+ * that is not zero, never to zero), and so are 16-bit parameters (float16 below its normal
+ * range: to the nearest): the random bits are a hash of (seed, t, place in the moments), and
+ * the same call gives the same bits.  State of 8 bits is computed in float64.  step: device
  * int32, the number of steps taken, counted by the call (0 at first).
  *
  * grads: HOST array of `count` device pointers, gradients in their parameters'
@@ -684,8 +689,8 @@ int mpq_matrix_cross_entropy(const void* x, int dtype, int64_t t, int64_t ldx, c
  * and writes device memory alone once it is enqueued, so that it may be captured and
  * replayed with gradients at the same addresses.
  * Errors: MPQ_ENULL, MPQ_ESHAPE (state.elements), MPQ_EPARAM (betas outside [0, 1),
- * eps below float32's normal range, grad_scale, max_norm or lr_scale out of range, state.bits, a plan that
- * mpq_adamw_plan did not fill). */
+ * eps below float32's normal range, grad_scale, max_norm or lr_scale out of range,
+ * state.bits, a plan that mpq_adamw_plan did not fill). */
 typedef struct {
   void* param;
   int64_t count, at;

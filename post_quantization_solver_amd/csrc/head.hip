@@ -1,5 +1,5 @@
 // Softmax cross entropy of an output head in pieces of the vocabulary, and its
-// gradients; the logits are never kept.
+// gradients; logits are kept only where they take up to 128 MB.
 //
 // Mathematics.  z_tv = a_v s_tv + o_v X_t + b_v with s = x e^T over the head's
 // entries and X_t = sum_j x_tj (a matrix or column groups: s = x W^T alone); r the
@@ -17,13 +17,14 @@
 // operand planes, its logits, and of each token the largest and the sum of the
 // exponentials.  Once all pieces have gone by (R is known) they come again for the
 // gradients: logits once more, dz, its products.  Logits that fit are kept instead, and
-// multiplied once.
+// multiplied once; for the gradient of a matrix or of column groups, where dz^T's rows have a
+// factor each that takes all tokens to know, a piece's are formed again in memory.
 //
 // Bound.  Many tokens: the products, see headgemm.hip (2048 x 128256 x 4096 E8: 1.64 ms for
-// the loss, 5.24 with the gradients of the layer's affine and of x, of which 0.22 and 0.46 lay
-// the planes out at 5.4 TB/s).  Logits that are kept (509 x 50257 x 2048, groups of 128: 0.89
-// ms): the products take 0.66, planes 0.11, dz 0.07.  A token (32000 x 4096 E8: 40 us): the
-// few-row product of the codes, 26.
+// the loss, 5.34 with the gradients of the layer's affine and of x, of which 0.22 and 0.46 lay
+// the planes out at 5.4 TB/s).  Logits that are kept (509 x 50257 x 2048, groups of 128: 0.91
+// to 0.94 ms): the products take 0.67, planes 0.11, dz 0.07, its bounds 0.02.  A token (32000 x
+// 4096 E8: 37 us): the few-row product of the codes, 26.
 #include <string.h>
 #include <math.h>
 #include <algorithm>
@@ -48,16 +49,21 @@ struct Carve {
   }
 };
 
-// What logits that are kept should take (half of the last-level cache); a piece's planes, and
-// its dz; the planes of a head whose logits are kept, which both passes read.  (Measured, 2048 x
-// 128256 x 4096 E8 with gradients, pieces of 64, 128, 256, 512 MB: 5.84, 5.55, 5.35, 5.27 ms, the
-// last for twice the workspace; 509 x 50257 x 2048, groups of 128: planes in pieces, laid out
-// twice, 1.28 ms, in one piece of 412 MB 1.01.)
 // Tokens whose input gradient comes straight from the packed codes.  Measured, whole calls with
 // gradients, 4 tokens so | 5 through planes: E8 128256 x 4096 323 | 600 us, 32000 x 2048 72 | 97;
 // 4 bits 32000 x 4096 102 | 165, groups of 128 117 | 232; 6 bits 32000 x 2048 80 | 114.  (One
 // token: 186, 54, 65, 72, 62.)  Eight would read and decode the codes twice.
 constexpr int64_t H_FEW = 4;
+// What logits that are kept should take (half of the last-level cache); a piece's planes, and
+// its dz; the planes of a head whose logits are kept, which both passes read; rows that a piece
+// has at least.  Measured: pieces of 64, 128, 256, 512 MB (2048 x 128256 x 4096 E8 with
+// gradients) 5.84, 5.55, 5.35, 5.27 ms, the last for twice the workspace.  Kept logits' planes
+// in pieces of 256 | 512 | 1024 MB, where those are more than one they are laid out twice: 412 MB
+// (509 x 50257 x 2048, groups of 128) 1100 | 934 | 934 us, 512 MB (300 x 32001 x 8000 bfloat16,
+// not in place) 626 | 508 | 508, 524 MB (333 x 64000 x 2048 float32) 1840 | 1535 | 1535, 823 MB
+// (512 x 50257 x 8192 E8) 1474 | 1340 | 1017, 1.6 GB (256 x 100000 x 4096, groups of 128)
+// 2970 | 2700 | 2580: 512 MB take in all of the heads that vocabularies of some 50000 and kept
+// logits mostly go with, and twice that is workspace which every such call would hold.
 constexpr int64_t H_BYTES = (int64_t)128 << 20, H_PIECE = (int64_t)256 << 20, H_PLANES = (int64_t)512 << 20, H_ROWS = 1024;
 
 // ------------------------------------------------------------------ tokens
@@ -437,8 +443,9 @@ __global__ __launch_bounds__(256) void head_factor_kernel(PieceArgs A, float* __
 // What a row's dz over all tokens, times the inverse of the tokens' factors, is at most: dz^T's
 // operand of each row of the head carries a power of two of its own, so that the gradient of a
 // row that no token makes likely is as exact as any other's (under one power of two for all
-// rows a row 20 nats below the likeliest kept 11 bits, one 27 nats below none).  By its
-// logarithm; a workgroup takes 256 rows and its share of the tokens, a wave every sixteenth of
+// rows a row 20 nats below the likeliest kept 11 bits, one 27 nats below none).  509 x 50257:
+// 24 us for 102 MB, 4.3 TB/s, the waves waiting 60 % of their time; with the factors that the
+// contraction reads per row, whole calls 876 -> 914 us, so.  By its logarithm; a workgroup takes 256 rows and its share of the tokens, a wave every sixteenth of
 // those (several shares: `out` is zeroed before, and the largest stays).
 constexpr int BOUND_ROWS = 256, BOUND_WAVES = 16;
 __global__ __launch_bounds__(64 * BOUND_WAVES) void head_bound_kernel(PieceArgs A, uint32_t* __restrict__ out) {
@@ -485,7 +492,7 @@ hipError_t launch_bound(const PieceArgs& A, uint32_t* out, hipStream_t st) {
 
 // A 64 x 64 tile of dz: its planes, its transpose's (turned in LDS: a lane stores four
 // tokens of a row), its rows' and columns' sums.  509 x 50257, with the transpose in two
-// terms: 70 us for 258 MB, 3.7 TB/s; vector instructions 63 % of the clocks.
+// terms: 72 us for 258 MB, 3.6 TB/s; vector instructions 65 % of the clocks.
 __global__ __launch_bounds__(256) void head_grad_kernel(PieceArgs A) {
   __shared__ float tl[64][65];
   __shared__ float cs[3][4][64];

@@ -9,9 +9,10 @@
 // (16 bits a logit and term) and as sums over the tile's tokens and rows.
 //
 // Bound.  As the product alone: 2048 tokens, 32768 rows of 4096 columns, statistics 380 us
-// (1.45 PFLOP/s; products alone reach 2.07), dz 445.  The matrix cores are busy 66 % of the
-// clocks (54 % with dz), which their power holds at 1.97 GHz; without any load or LDS read in
-// the loop the statistics would still take 330.  What is left is the step's barrier and the
+// (1.45 PFLOP/s; products alone reach 2.07), dz 445 (for a packed head with an affine per row,
+// or for dx alone).  The matrix cores are busy 66 % of the clocks (55 % with dz), which their
+// power holds at 1.97 GHz; without any load or LDS read in the loop the statistics would still
+// take 330.  What is left is the step's barrier and the
 // epilogue (some 12 vector instructions a logit for the statistics, 35 for dz) in the one
 // workgroup that fits a CU.  Tried: four waves of 128 x 128 each, statistics 440 us; two
 // workgroups of 256 x 128 on a CU 408, dz 468.

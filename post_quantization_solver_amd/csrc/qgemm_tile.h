@@ -184,8 +184,7 @@ __device__ __forceinline__ void interleave() {
 
 // Which tile this workgroup has, and its products summed up: D[j0 + (wn SN + b) 16 +
 // lane % 16][i0 + (wm SM + a) 16 + 4 (lane / 16) + k] = acc[a][b][k], with wave
-// wm WN + wn.  At the end every wave is done with the stages.  AROWS: A stays in rows of
-// g.lda elements (as B in rows of g.ldb).
+// wm WN + wn.  At the end every wave is done with the stages.  AMODE: how A lies.
 template <typename T, int BM, int BN, int WM, int WN, int AMODE>
 __device__ __forceinline__ void q_gemm_tile(const QGemm& g, int splits, uint16_t (&lds)[gemm_stages(BM, BN)][(BM + BN) * BK],
                                             v4f (&acc)[BM / WM / 16][BN / WN / 16], int& split, int64_t& i0, int64_t& j0) {
@@ -265,9 +264,9 @@ __device__ __forceinline__ void q_gemm_tile(const QGemm& g, int splits, uint16_t
     wait_stage<(STAGES - 2) * LOADS>();                                                                      \
     at.fetch(g, wave, off, lds[here]);                                                                       \
     here = here + 1 == STAGES ? 0 : here + 1;                                                                \
-    Q_READ(lds[here], nxt);                                                    \
+    Q_READ(lds[here], nxt);                                                                                  \
     multiply<T, SM, SN>(cur, acc);                                                                           \
-    interleave<SM * SN, (a_transposed(AMODE) ? 2 : 1) * SM + SN, a_transposed(AMODE) ? 0 : LOADS>();                                                                   \
+    interleave<SM * SN, (a_transposed(AMODE) ? 2 : 1) * SM + SN, a_transposed(AMODE) ? 0 : LOADS>();         \
     if (at.k == kts) at.seek(g, i0, j0, wave, off, at.pair + 1, 0);                                          \
   }
   for (; kt + STAGES + 1 < kt1; kt += 2) {
@@ -283,7 +282,7 @@ __device__ __forceinline__ void q_gemm_tile(const QGemm& g, int splits, uint16_t
       if (at.k == kts) at.seek(g, i0, j0, wave, off, at.pair + 1, 0);                                        \
     }                                                                                                        \
     here = here + 1 == STAGES ? 0 : here + 1;                                                                \
-    if ((kt) + 1 < kt1) Q_READ(lds[here], nxt);                                \
+    if ((kt) + 1 < kt1) Q_READ(lds[here], nxt);                                                              \
     multiply<T, SM, SN>(cur, acc);                                                                           \
   }
   for (; kt < kt1; kt += 2) {
