@@ -680,7 +680,7 @@ int mpq_matrix_cross_entropy(const void* x, int dtype, int64_t t, int64_t ldx, c
  *
  * grads: HOST array of `count` device pointers, gradients in their parameters'
  * types.  grad_scale: finite.  max_norm: 0 for none; else > 0, +inf for the norm
- * alone: a step whose norm is not finite is not taken (nothing changes but
+ * alone: a step whose norm is not finite in float32 is not taken (nothing changes but
  * *norm), and `norm` (device float, may be NULL) receives the norm of the gradients
  * times grad_scale, before clipping.  Without max_norm a gradient that is not finite
  * makes its element's moments (8 bits: the 256's) NaN.  Every learning rate is

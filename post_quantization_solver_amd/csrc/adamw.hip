@@ -273,7 +273,7 @@ __global__ __launch_bounds__(THREADS) void adamw_norm_kernel(AdamwTable T, int64
   __syncthreads();
   if (threadIdx.x == 0) {
     const double n = sqrt((part[0] + part[1]) + (part[2] + part[3])) * fabs(grad_scale);
-    const bool finite = n <= 1.7976931348623157e308;
+    const bool finite = (float)n <= 3.40282347e38f;   // (as the caller sees it)
     T.control[CTL_FACTOR] = __float_as_uint((float)(grad_scale * (n > max_norm ? max_norm / n : 1.0)));
     T.control[CTL_SKIP] = !finite;
     if (norm) *norm = (float)n;

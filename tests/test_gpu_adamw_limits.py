@@ -101,3 +101,25 @@ def test_a_resumed_run_rounds_as_the_first(bits, tmp_path):
     c = mpq.AdamW(twin, state_bits=bits, seed=11)
     c.load_state_dict(old)
     assert c.seed == 11
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_norm_beyond_float32(bits):
+    """The norm is handed back in float32: a step is taken where that is finite, and where it is infinite it is not, although
+    every gradient is finite and so is the sum in float64."""
+    import torch
+    import post_quantization_solver_amd as mpq
+    params, grads = problem(("fp32",), [500, 70], seed=24)
+    opt = mpq.AdamW(params, state_bits=bits)
+    opt.step(grads)
+    before = [t.clone() for t in params + list(opt.state_dict().values())]
+    large = [g.clone() for g in grads]
+    large[0][:4] = 3e38
+    for limit in (1.0, float("inf")):
+        assert torch.isposinf(opt.step(large, max_norm=limit))
+        assert torch.isposinf(opt.step(large, max_norm=limit, grad_scale=-1.0))
+        assert all(torch.equal(a, b) for a, b in zip(before, params + list(opt.state_dict().values())))
+    # (3e38 twice the square root of 4, halved and more)
+    norm = opt.step(large, max_norm=1.0, grad_scale=0.25)
+    assert torch.isfinite(norm) and abs(float(norm) / 1.5e38 - 1) < 2.0 ** -22 and int(opt.steps) == 2
+    assert all(torch.isfinite(p).all() for p in params)
